@@ -77,6 +77,26 @@ class gemm_problem_t(ctypes.Structure):
                 ("dtypes", gemm_dtypes_t)]
 
 
+class gemm_rmsnorm_t(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int64), ("H", ctypes.c_int64),
+                ("type", ctypes.c_int), ("w_type", ctypes.c_int), ("y_type", ctypes.c_int),
+                ("eps", ctypes.c_float),
+                ("x", ctypes.c_void_p), ("ldx", ctypes.c_int64),
+                ("r", ctypes.c_void_p), ("ldr", ctypes.c_int64), ("weight", ctypes.c_void_p),
+                ("h", ctypes.c_void_p), ("ldh", ctypes.c_int64),
+                ("y", ctypes.c_void_p), ("ldy", ctypes.c_int64),
+                ("scale", ctypes.c_void_p), ("rstd", ctypes.c_void_p)]
+
+
+class gemm_rmsnorm_bwd_t(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int64), ("H", ctypes.c_int64),
+                ("type", ctypes.c_int), ("w_type", ctypes.c_int), ("dw_type", ctypes.c_int),
+                ("dy", ctypes.c_void_p), ("lddy", ctypes.c_int64),
+                ("h", ctypes.c_void_p), ("ldh", ctypes.c_int64), ("weight", ctypes.c_void_p),
+                ("rstd", ctypes.c_void_p), ("dh", ctypes.c_void_p), ("lddh", ctypes.c_int64),
+                ("dx", ctypes.c_void_p), ("lddx", ctypes.c_int64), ("dweight", ctypes.c_void_p)]
+
+
 class GemmError(RuntimeError):
     def __init__(self, status: int, what: str = ""):
         self.status = status
@@ -130,10 +150,17 @@ def library():
             lib.gemm_last_config.argtypes = [vp, ctypes.POINTER(gemm_config_t)]
             lib.gemm_tmem_columns.argtypes = [i32, i32]
             lib.gemm_set_timeout_ns.argtypes = [vp, ctypes.c_uint64]
+            lib.gemm_rmsnorm.argtypes = [vp, ctypes.POINTER(gemm_rmsnorm_t), vp]
+            lib.gemm_rmsnorm_check.argtypes = [ctypes.POINTER(gemm_rmsnorm_t)]
+            lib.gemm_rmsnorm_bwd_check.argtypes = [ctypes.POINTER(gemm_rmsnorm_bwd_t)]
+            lib.gemm_rmsnorm_bwd_workspace.argtypes = [i64, i64]
+            lib.gemm_rmsnorm_bwd_workspace.restype = i64
+            lib.gemm_rmsnorm_bwd.argtypes = [vp, ctypes.POINTER(gemm_rmsnorm_bwd_t), vp, i64, vp]
             for name in ("gemm_create", "gemm_destroy", "gemm_run", "gemm_run_noalloc",
                          "gemm_sync_status",
                          "gemm_check", "gemm_plan", "gemm_set_config", "gemm_last_config",
-                         "gemm_tmem_columns", "gemm_set_timeout_ns"):
+                         "gemm_tmem_columns", "gemm_set_timeout_ns", "gemm_rmsnorm",
+                         "gemm_rmsnorm_check", "gemm_rmsnorm_bwd", "gemm_rmsnorm_bwd_check"):
                 getattr(lib, name).restype = i32
             _lib = lib
     return _lib
@@ -277,8 +304,90 @@ def make_problem(M, N, K, L, A=None, lda=0, layoutA=GEMM_K_MAJOR, B=None, ldb=0,
                           dtypes if dtypes is not None else make_dtypes("f16"))
 
 
+def gemm_rmsnorm(handle, problem: gemm_rmsnorm_t, stream=None, check=True) -> int:
+    st = library().gemm_rmsnorm(handle, ctypes.byref(problem), _stream(stream))
+    if check and st != GEMM_OK:
+        raise GemmError(st, "gemm_rmsnorm")
+    return st
+
+
+def gemm_rmsnorm_check(problem: gemm_rmsnorm_t) -> int:
+    return library().gemm_rmsnorm_check(ctypes.byref(problem))
+
+
+def gemm_rmsnorm_bwd_check(problem: gemm_rmsnorm_bwd_t) -> int:
+    return library().gemm_rmsnorm_bwd_check(ctypes.byref(problem))
+
+
+def gemm_rmsnorm_bwd_workspace(M, H) -> int:
+    """Bytes of workspace gemm_rmsnorm_bwd needs."""
+    return library().gemm_rmsnorm_bwd_workspace(M, H)
+
+
+def gemm_rmsnorm_bwd(handle, problem: gemm_rmsnorm_bwd_t, workspace=None, workspace_bytes=0,
+                     stream=None, check=True) -> int:
+    st = library().gemm_rmsnorm_bwd(handle, ctypes.byref(problem), _ptr(workspace),
+                                    workspace_bytes, _stream(stream))
+    if check and st != GEMM_OK:
+        raise GemmError(st, "gemm_rmsnorm_bwd")
+    return st
+
+
+# ------------------------------------------------------------------ tensors
+
+# Type codes by the name of a tensor's dtype.
+_TENSOR_CODES = {"torch.float32": GEMM_F32, "torch.float16": GEMM_F16,
+                 "torch.bfloat16": GEMM_BF16, "torch.float8_e4m3fn": GEMM_E4M3,
+                 "torch.float8_e5m2": GEMM_E5M2}
+_CODE_OF = {}           # the same by the dtype object, filled as they are met
+
+
+def _code(t, what):
+    code = _CODE_OF.get(t.dtype)
+    if code is None:
+        code = _TENSOR_CODES.get(str(t.dtype))
+        if code is None:
+            raise GemmError(GEMM_ERR_UNSUPPORTED_DTYPE, f"{what}: {t.dtype}")
+        _CODE_OF[t.dtype] = code
+    return code
+
+
+def _rows(t, M, N, what, code=None):
+    """(address, row stride) of an M x N tensor whose rows are contiguous, of type
+    `code` if given; (None, 0) for None."""
+    if t is None:
+        return None, 0
+    shape = t.shape
+    if len(shape) != 2 or shape[0] != M or shape[1] != N:
+        raise GemmError(GEMM_ERR_INVALID_ARG, f"{what}: shape {tuple(shape)}, not ({M}, {N})")
+    s0, s1 = t.stride()
+    if s1 != 1 and N > 1:
+        raise GemmError(GEMM_ERR_INVALID_ARG, f"{what}: rows are not contiguous")
+    if code is not None and _code(t, what) != code:
+        raise GemmError(GEMM_ERR_UNSUPPORTED_DTYPE, f"{what}: {t.dtype}")
+    # the stride of a single row says nothing: any sufficient aligned one will do
+    return t.data_ptr(), s0 if M > 1 else max(s0, (N + 15) // 16 * 16)
+
+
+def _vector(t, n, what, code=None):
+    """Address of a contiguous vector of n elements (of type `code` if given); None for None."""
+    if t is None:
+        return None
+    if len(t.shape) != 1 or t.shape[0] != n or (n > 1 and t.stride()[0] != 1):
+        raise GemmError(GEMM_ERR_INVALID_ARG, f"{what}: not a contiguous vector of {n}")
+    if code is not None and _code(t, what) != code:
+        raise GemmError(GEMM_ERR_UNSUPPORTED_DTYPE, f"{what}: {t.dtype}")
+    return t.data_ptr()
+
+
 class Gemm:
-    """Owns one library handle on `device`."""
+    """Owns one library handle on `device`.
+
+    run, run_host: the C entry points' arguments.  rmsnorm, rmsnorm_bwd: the operators
+    around the product on tensors (torch's or any with data_ptr, dtype, shape and
+    stride), whose types, sizes and row strides the calls read off and check; outputs
+    are the caller's tensors too.  Tensors are used on `stream` (None: the default
+    stream) and must be ready there."""
 
     def __init__(self, device: int = 0):
         self.handle = gemm_create(device)
@@ -327,3 +436,40 @@ class Gemm:
 
     def last_config(self):
         return gemm_last_config(self.handle)
+
+    def rmsnorm(self, x, weight, y, residual=None, h=None, scale=None, rstd=None, eps=1e-6,
+                stream=None):
+        """y = (x + residual) * rstd * weight; see gemm_rmsnorm in the C header.  An 8-bit
+        y (float8_e4m3fn, float8_e5m2) is quantised per row, with its scales in
+        `scale`; `h` receives x + residual, `rstd` the rows' factors."""
+        M, H = x.shape
+        t = _code(x, "x")
+        px, ldx = _rows(x, M, H, "x")
+        pr, ldr = _rows(residual, M, H, "residual", t)
+        ph, ldh = _rows(h, M, H, "h", t)
+        py, ldy = _rows(y, M, H, "y")
+        p = gemm_rmsnorm_t(M, H, t, _code(weight, "weight"), _code(y, "y"), eps, px, ldx, pr, ldr,
+                           _vector(weight, H, "weight"), ph, ldh, py, ldy,
+                           _vector(scale, M, "scale", GEMM_F32),
+                           _vector(rstd, M, "rstd", GEMM_F32))
+        gemm_rmsnorm(self.handle, p, stream)
+
+    def rmsnorm_bwd(self, dy, h, weight, rstd, dx, dweight, dh=None, workspace=None,
+                    stream=None):
+        """Gradients of x (= of the residual) and of weight; see gemm_rmsnorm_bwd in the C
+        header.  `workspace`: a contiguous tensor of at least
+        gemm_rmsnorm_bwd_workspace(M, H) bytes."""
+        M, H = dy.shape
+        t = _code(dy, "dy")
+        pdy, lddy = _rows(dy, M, H, "dy")
+        ph, ldh = _rows(h, M, H, "h", t)
+        pdh, lddh = _rows(dh, M, H, "dh", t)
+        pdx, lddx = _rows(dx, M, H, "dx", t)
+        p = gemm_rmsnorm_bwd_t(M, H, t, _code(weight, "weight"), _code(dweight, "dweight"),
+                               pdy, lddy, ph, ldh, _vector(weight, H, "weight"),
+                               _vector(rstd, M, "rstd", GEMM_F32), pdh, lddh, pdx, lddx,
+                               _vector(dweight, H, "dweight"))
+        ws, nbytes = None, 0
+        if workspace is not None:
+            ws, nbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        gemm_rmsnorm_bwd(self.handle, p, ws, nbytes, stream)

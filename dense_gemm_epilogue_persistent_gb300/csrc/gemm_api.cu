@@ -12,7 +12,6 @@
 // cudaDevAttrMaxSharedMemoryPerBlockOptin before launching.
 #include <cuda.h>
 #include <cuda_runtime.h>
-#include <nvtx3/nvToolsExt.h>
 
 #include <algorithm>
 #include <cstdint>
@@ -21,22 +20,13 @@
 
 #include "gemm_gb300.h"
 #include "gemm_kernel.cuh"
+#include "handle.h"
 #include "kernels.h"
-
-#define GEMM_API extern "C" __attribute__((visibility("default")))
 
 namespace {
 
-using gb300::KernelParams;
+using namespace gb300host;
 
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-constexpr uint64_t kDefaultTimeoutNs = 4000000000ull;
-constexpr int kMaxStages = 12;
-constexpr int kMaxEpiSlots = 6;
 // Default L2 priorities: evict-first for every TMA copy (A/B loads, C/X loads,
 // D/Y stores).  Interleaved sustained sweeps on GB300 found it best or tied
 // on all five benchmark shapes (fp8 3000x5000x4096: +11% over evict-normal);
@@ -53,110 +43,8 @@ constexpr int kDefaultEpiWaitNs = 0;
 // barriers
 constexpr int kSmemSlack = 1024 + 16 + 8 * gb300::kMaxEpiWarps * gb300::kMaxChunks + 16;
 
-struct VariantState {
-  bool smem_attr_set = false;  // max dynamic smem attribute raised to the opt-in limit
-  int occ_smem = 0;            // dynamic smem size of the last occupancy query
-  int max_clusters = 0;        // resident clusters at that size
-};
-
-// Everything a launch needs, prepared once per distinct call.  A call whose
-// arguments (every field of the problem, byte for byte) and forced
-// configuration equal a cached entry's launches from it without planning or
-// encoding tensor maps again.
-struct LaunchKey {
-  gemm_problem_t problem;
-  uint64_t config_gen;       // bumped by gemm_set_config
-};
-
-struct LaunchEntry {
-  bool valid = false;
-  LaunchKey key;
-  gemm_config_t cfg{};
-  const void* kern = nullptr;
-  int cluster_ctas = 0;
-  CUtensorMap maps[6];       // A, B, C, X, D, Y
-  KernelParams kp{};
-};
-
-constexpr int kLaunchCacheEntries = 4;
-
-// NVTX ranges in the "gemm_gb300" domain around every entry point that
-// enqueues work (and around planning and tensor-map encoding on a launch-cache
-// miss), so that a profiler's timeline and its range filters (ncu --nvtx
-// --nvtx-include "gemm_gb300@gemm_run/") can pick the library's calls out.
-// Without a tool attached each push and pop returns at once.
-nvtxDomainHandle_t nvtx_domain() {
-  static const nvtxDomainHandle_t d = nvtxDomainCreateA("gemm_gb300");
-  return d;
-}
-
-struct NvtxRange {
-  explicit NvtxRange(const char* name) {
-    nvtxEventAttributes_t a{};
-    a.version = NVTX_VERSION;
-    a.size = NVTX_EVENT_ATTRIB_STRUCT_SIZE;
-    a.messageType = NVTX_MESSAGE_TYPE_ASCII;
-    a.message.ascii = name;
-    nvtxDomainRangePushEx(nvtx_domain(), &a);
-  }
-  ~NvtxRange() { nvtxDomainRangePop(nvtx_domain()); }
-  NvtxRange(const NvtxRange&) = delete;
-  NvtxRange& operator=(const NvtxRange&) = delete;
-};
-
-}  // namespace
-
-struct gemm_handle {
-  int device = 0;
-  int sm_count = 0;
-  int smem_optin = 0;
-  EncodeTiledFn encode = nullptr;
-  uint32_t* d_status = nullptr;
-  bool forced = false;
-  gemm_config_t forced_cfg{};
-  gemm_config_t last{};
-  uint64_t timeout_ns = kDefaultTimeoutNs;
-  VariantState variants[3][2][2][2][2][2][2];   // [ab 16/8/32][cta_group][k atoms][mc][nc][epw][sk]
-  int clusters_by_size[9] = {0, 0, 0, 0, 0, 0, 0, 0, 0};   // resident clusters of 1, 2, 4, 8 CTAs
-  uint64_t config_gen = 0;
-  LaunchEntry cache[kLaunchCacheEntries];
-  int cache_next = 0;
-  std::mutex mu;
-  void* ws = nullptr;          // gemm_run_host's device copies of its host buffers
-  size_t ws_bytes = 0;
-  std::mutex ws_mu;
-  unsigned long long* d_stats = nullptr;   // ring statistics (statistics build only)
-  // Stream-K workspace: one 128 x 256 fp32 partial slot and one flag per SM
-  // (null: stream-K is never planned for this handle).
-  float* sk_partials = nullptr;
-  uint32_t* sk_flags = nullptr;
-};
-
-namespace {
-
-int dtype_bytes(int dt) {
-  switch (dt) {
-    case GEMM_F32: return 4;
-    case GEMM_F16: return 2;
-    case GEMM_BF16: return 2;
-    case GEMM_E4M3: return 1;
-    case GEMM_E5M2: return 1;
-    case GEMM_TF32: return 4;
-  }
-  return 0;
-}
-
-bool is_epi_type(int dt) { return dt == GEMM_F32 || dt == GEMM_F16 || dt == GEMM_BF16; }
-bool is_fp8(int dt) { return dt == GEMM_E4M3 || dt == GEMM_E5M2; }
-bool is_ab_type(int dt) {
-  return dt == GEMM_F16 || dt == GEMM_BF16 || is_fp8(dt) || dt == GEMM_TF32;
-}
 // B's type: the descriptor's b when set (0 = GEMM_F32 means "same as ab").
 int b_type(const gemm_dtypes_t& t) { return t.b == GEMM_F32 ? t.ab : t.b; }
-bool is_layout(int v) { return v == GEMM_K_MAJOR || v == GEMM_MN_MAJOR; }
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 bool reads_c(const gemm_problem_t& p) { return p.beta != 0.0f; }
 bool reads_x(const gemm_problem_t& p) { return p.X != nullptr && p.x_factor != 0.0f; }

@@ -1,0 +1,141 @@
+// Host state shared by the library's entry-point units: the handle, its launch
+// cache, NVTX ranges and the small helpers every argument check uses.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <nvtx3/nvToolsExt.h>
+
+#include <cstdint>
+#include <mutex>
+
+#include "gemm_gb300.h"
+#include "gemm_kernel.cuh"
+
+#define GEMM_API extern "C" __attribute__((visibility("default")))
+
+namespace gb300host {
+
+using gb300::KernelParams;
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+constexpr uint64_t kDefaultTimeoutNs = 4000000000ull;
+constexpr int kMaxStages = 12;
+constexpr int kMaxEpiSlots = 6;
+
+struct VariantState {
+  bool smem_attr_set = false;  // max dynamic smem attribute raised to the opt-in limit
+  int occ_smem = 0;            // dynamic smem size of the last occupancy query
+  int max_clusters = 0;        // resident clusters at that size
+};
+
+// Everything a launch needs, prepared once per distinct call.  A call whose
+// arguments (every field of the problem, byte for byte) and forced
+// configuration equal a cached entry's launches from it without planning or
+// encoding tensor maps again.
+struct LaunchKey {
+  gemm_problem_t problem;
+  uint64_t config_gen;       // bumped by gemm_set_config
+};
+
+struct LaunchEntry {
+  bool valid = false;
+  LaunchKey key;
+  gemm_config_t cfg{};
+  const void* kern = nullptr;
+  int cluster_ctas = 0;
+  CUtensorMap maps[6];       // A, B, C, X, D, Y
+  KernelParams kp{};
+};
+
+constexpr int kLaunchCacheEntries = 4;
+
+// NVTX ranges in the "gemm_gb300" domain around every entry point that
+// enqueues work (and around planning and tensor-map encoding on a launch-cache
+// miss), so that a profiler's timeline and its range filters (ncu --nvtx
+// --nvtx-include "gemm_gb300@gemm_run/") can pick the library's calls out.
+// Without a tool attached each push and pop returns at once.
+inline nvtxDomainHandle_t nvtx_domain() {
+  static const nvtxDomainHandle_t d = nvtxDomainCreateA("gemm_gb300");
+  return d;
+}
+
+struct NvtxRange {
+  explicit NvtxRange(const char* name) {
+    nvtxEventAttributes_t a{};
+    a.version = NVTX_VERSION;
+    a.size = NVTX_EVENT_ATTRIB_STRUCT_SIZE;
+    a.messageType = NVTX_MESSAGE_TYPE_ASCII;
+    a.message.ascii = name;
+    nvtxDomainRangePushEx(nvtx_domain(), &a);
+  }
+  ~NvtxRange() { nvtxDomainRangePop(nvtx_domain()); }
+  NvtxRange(const NvtxRange&) = delete;
+  NvtxRange& operator=(const NvtxRange&) = delete;
+};
+
+}  // namespace gb300host
+
+struct gemm_handle {
+  int device = 0;
+  int sm_count = 0;
+  int smem_optin = 0;
+  gb300host::EncodeTiledFn encode = nullptr;
+  uint32_t* d_status = nullptr;
+  bool forced = false;
+  gemm_config_t forced_cfg{};
+  gemm_config_t last{};
+  uint64_t timeout_ns = gb300host::kDefaultTimeoutNs;
+  gb300host::VariantState variants[3][2][2][2][2][2][2];   // [ab 16/8/32][cta_group][k atoms][mc][nc][epw][sk]
+  int clusters_by_size[9] = {0, 0, 0, 0, 0, 0, 0, 0, 0};   // resident clusters of 1, 2, 4, 8 CTAs
+  uint64_t config_gen = 0;
+  gb300host::LaunchEntry cache[gb300host::kLaunchCacheEntries];
+  int cache_next = 0;
+  std::mutex mu;
+  void* ws = nullptr;          // gemm_run_host's device copies of its host buffers
+  size_t ws_bytes = 0;
+  std::mutex ws_mu;
+  unsigned long long* d_stats = nullptr;   // ring statistics (statistics build only)
+  // Stream-K workspace: one 128 x 256 fp32 partial slot and one flag per SM
+  // (null: stream-K is never planned for this handle).
+  float* sk_partials = nullptr;
+  uint32_t* sk_flags = nullptr;
+};
+
+namespace gb300host {
+
+inline int dtype_bytes(int dt) {
+  switch (dt) {
+    case GEMM_F32: return 4;
+    case GEMM_F16: return 2;
+    case GEMM_BF16: return 2;
+    case GEMM_E4M3: return 1;
+    case GEMM_E5M2: return 1;
+    case GEMM_TF32: return 4;
+  }
+  return 0;
+}
+
+inline bool is_epi_type(int dt) { return dt == GEMM_F32 || dt == GEMM_F16 || dt == GEMM_BF16; }
+inline bool is_fp8(int dt) { return dt == GEMM_E4M3 || dt == GEMM_E5M2; }
+inline bool is_ab_type(int dt) {
+  return dt == GEMM_F16 || dt == GEMM_BF16 || is_fp8(dt) || dt == GEMM_TF32;
+}
+inline bool is_layout(int v) { return v == GEMM_K_MAJOR || v == GEMM_MN_MAJOR; }
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Whether the calling thread's current device is the handle's.
+inline bool on_device(const gemm_handle* h) {
+  int cur = -1;
+  if (cudaGetDevice(&cur) == cudaSuccess && cur == h->device) return true;
+  cudaGetLastError();
+  return false;
+}
+
+}  // namespace gb300host

@@ -377,6 +377,90 @@ gemm_status_t gemm_run_noalloc(int64_t M, int64_t N, int64_t K, int64_t L,
                                const gemm_dtypes_t* dtypes, struct CUstream_st* stream,
                                uint32_t* watchdog_out);
 
+/* ====================================================================
+ * Operators around the product: root-mean-square normalisation (which can
+ * write the 8-bit operand and row scales of an fp8 product) and its backward
+ * pass.
+ *
+ * All of them: tensors are device memory of the handle's device, owned by the
+ * caller; matrices are row-major with a leading dimension (row stride, in
+ * elements) of their own, which may exceed the row length; every matrix, weight
+ * and bias starts on a 16-byte boundary and every leading dimension times its element size is a multiple of 16
+ * bytes (GEMM_ERR_MISALIGNED otherwise), while the sizes themselves may be
+ * odd.  Calls validate on the host, enqueue on `stream` and return; they
+ * neither synchronise nor allocate, keep nothing between calls, and may be
+ * captured into a CUDA graph.  Sums and statistics are fp32 in a fixed order:
+ * the same call gives the same bits.  Any overlap between an output and
+ * another tensor that is not named as allowed is undefined. */
+
+/* y = norm(x + r):
+ *     h(m,c)  = x(m,c) + r(m,c)                       (fp32; r NULL: h = x)
+ *     rstd(m) = 1 / sqrt(mean_c h(m,c)^2 + eps)
+ *     y(m,c)  = h(m,c) * rstd(m) * weight(c)
+ * with h rounded only where it is written.  An 8-bit y (E4M3 or E5M2) is
+ * quantised per row:
+ *     scale(m) = max(max_c |y(m,c)|, 2^-100) / T,  T = 448 (E4M3), 57344 (E5M2)
+ *     q(m,c)   = round(y(m,c) / scale(m))          nearest even, |q| <= T
+ * so q and scale are the A and row_scale of an 8-bit product.  (y is multiplied
+ * by the reciprocal, which can move a value that lies within an fp32 rounding
+ * of the middle between two codes to the other one.)  A row that holds a NaN
+ * gets a NaN scale, rstd and row.
+ *   M rows of H elements; M or H = 0: nothing to do.
+ *   type: F32, F16 or BF16, the type of x, r and h.  w_type: any of the
+ *   three.  y_type: those, E4M3 or E5M2.
+ *   r, h, rstd: optional (NULL).  scale: required for an 8-bit y, else NULL.
+ * h may be x or r (same leading dimension), y may be x or r (same type and
+ * leading dimension). */
+typedef struct {
+  int64_t M, H;
+  gemm_dtype_t type, w_type, y_type;
+  float eps;
+  const void* x; int64_t ldx;
+  const void* r; int64_t ldr;
+  const void* weight;
+  void* h; int64_t ldh;
+  void* y; int64_t ldy;
+  float* scale;
+  float* rstd;
+} gemm_rmsnorm_t;
+
+gemm_status_t gemm_rmsnorm(gemm_handle_t h, const gemm_rmsnorm_t* p, struct CUstream_st* stream);
+
+/* Host-only validation of the call's arguments, exactly as the call performs
+ * it (as gemm_check is for gemm_run); likewise for the operators below. */
+gemm_status_t gemm_rmsnorm_check(const gemm_rmsnorm_t* p);
+
+/* Its backward pass, from h and rstd as gemm_rmsnorm wrote them and dy, the
+ * gradient of y (of the values an 8-bit y stands for):
+ *     n(m,c)     = h(m,c) * rstd(m)
+ *     g(m,c)     = dy(m,c) * weight(c)
+ *     dx(m,c)    = rstd(m) * (g(m,c) - n(m,c) * mean_c(g n)) + dh(m,c)
+ *     dweight(c) = sum_m dy(m,c) * n(m,c)
+ * dx is the gradient of x and of r alike.  dh (optional) is the gradient that
+ * reaches h by its other uses.
+ *   type: F32, F16 or BF16, the type of dy, h, dh and dx.  w_type, dw_type: any
+ *   of the three.  M = 0: dweight = 0.  H = 0: nothing to do.
+ * dx may be dh (same leading dimension).
+ * workspace: device memory of at least gemm_rmsnorm_bwd_workspace(M, H) bytes
+ * (16-byte aligned; NULL where that is 0), used until the call has run on
+ * `stream`: calls that may overlap need one each. */
+typedef struct {
+  int64_t M, H;
+  gemm_dtype_t type, w_type, dw_type;
+  const void* dy; int64_t lddy;
+  const void* h; int64_t ldh;
+  const void* weight;
+  const float* rstd;
+  const void* dh; int64_t lddh;
+  void* dx; int64_t lddx;
+  void* dweight;
+} gemm_rmsnorm_bwd_t;
+
+int64_t gemm_rmsnorm_bwd_workspace(int64_t M, int64_t H);
+gemm_status_t gemm_rmsnorm_bwd_check(const gemm_rmsnorm_bwd_t* p);
+gemm_status_t gemm_rmsnorm_bwd(gemm_handle_t h, const gemm_rmsnorm_bwd_t* p, void* workspace,
+                               int64_t workspace_bytes, struct CUstream_st* stream);
+
 #ifdef __cplusplus
 }
 #endif
