@@ -37,10 +37,16 @@ GEMM_ERR_DEVICE_CHECK = 8
 GEMM_F32, GEMM_F16, GEMM_BF16, GEMM_E4M3, GEMM_E5M2, GEMM_TF32 = 0, 1, 2, 3, 4, 5
 GEMM_K_MAJOR, GEMM_MN_MAJOR = 0, 1
 GEMM_EPI_LINEAR, GEMM_EPI_RELU = 0, 1
+GEMM_ACT_NONE, GEMM_ACT_RELU, GEMM_ACT_GELU, GEMM_ACT_GELU_TANH, GEMM_ACT_SILU = 0, 1, 2, 3, 4
 GEMM_RING_STAT_WORDS = 16
 
 DTYPE_CODES = {"f32": GEMM_F32, "f16": GEMM_F16, "bf16": GEMM_BF16, "e4m3": GEMM_E4M3,
                "e5m2": GEMM_E5M2, "tf32": GEMM_TF32}
+
+
+ACTIVATION_CODES = {None: GEMM_ACT_NONE, "none": GEMM_ACT_NONE, "relu": GEMM_ACT_RELU,
+                    "gelu": GEMM_ACT_GELU, "gelu_tanh": GEMM_ACT_GELU_TANH,
+                    "silu": GEMM_ACT_SILU}
 
 
 class gemm_dtypes_t(ctypes.Structure):
@@ -95,6 +101,34 @@ class gemm_rmsnorm_bwd_t(ctypes.Structure):
                 ("h", ctypes.c_void_p), ("ldh", ctypes.c_int64), ("weight", ctypes.c_void_p),
                 ("rstd", ctypes.c_void_p), ("dh", ctypes.c_void_p), ("lddh", ctypes.c_int64),
                 ("dx", ctypes.c_void_p), ("lddx", ctypes.c_int64), ("dweight", ctypes.c_void_p)]
+
+
+class gemm_linear_t(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64),
+                ("a_type", ctypes.c_int), ("b_type", ctypes.c_int), ("bias_type", ctypes.c_int),
+                ("r_type", ctypes.c_int), ("z_type", ctypes.c_int), ("d_type", ctypes.c_int),
+                ("layoutA", ctypes.c_int), ("layoutB", ctypes.c_int),
+                ("activation", ctypes.c_int), ("alpha", ctypes.c_float),
+                ("A", ctypes.c_void_p), ("lda", ctypes.c_int64),
+                ("B", ctypes.c_void_p), ("ldb", ctypes.c_int64),
+                ("row_scale", ctypes.c_void_p), ("col_scale", ctypes.c_void_p),
+                ("bias", ctypes.c_void_p), ("R", ctypes.c_void_p), ("ldr", ctypes.c_int64),
+                ("Z", ctypes.c_void_p), ("ldz", ctypes.c_int64),
+                ("D", ctypes.c_void_p), ("ldd", ctypes.c_int64)]
+
+
+class gemm_linear_bwd_t(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64),
+                ("type", ctypes.c_int), ("da_type", ctypes.c_int), ("db_type", ctypes.c_int),
+                ("dbias_type", ctypes.c_int), ("activation", ctypes.c_int),
+                ("accumulate", ctypes.c_int), ("alpha", ctypes.c_float),
+                ("dd", ctypes.c_void_p), ("lddd", ctypes.c_int64),
+                ("z", ctypes.c_void_p), ("ldz", ctypes.c_int64),
+                ("a", ctypes.c_void_p), ("lda", ctypes.c_int64),
+                ("b", ctypes.c_void_p), ("ldb", ctypes.c_int64),
+                ("dz", ctypes.c_void_p), ("lddz", ctypes.c_int64),
+                ("da", ctypes.c_void_p), ("ldda", ctypes.c_int64),
+                ("db", ctypes.c_void_p), ("lddb", ctypes.c_int64), ("dbias", ctypes.c_void_p)]
 
 
 class GemmError(RuntimeError):
@@ -156,11 +190,17 @@ def library():
             lib.gemm_rmsnorm_bwd_workspace.argtypes = [i64, i64]
             lib.gemm_rmsnorm_bwd_workspace.restype = i64
             lib.gemm_rmsnorm_bwd.argtypes = [vp, ctypes.POINTER(gemm_rmsnorm_bwd_t), vp, i64, vp]
+            lib.gemm_linear_check.argtypes = [ctypes.POINTER(gemm_linear_t)]
+            lib.gemm_linear.argtypes = [vp, ctypes.POINTER(gemm_linear_t), vp]
+            lib.gemm_linear_bwd_check.argtypes = [ctypes.POINTER(gemm_linear_bwd_t)]
+            lib.gemm_linear_bwd.argtypes = [vp, ctypes.POINTER(gemm_linear_bwd_t), vp]
             for name in ("gemm_create", "gemm_destroy", "gemm_run", "gemm_run_noalloc",
                          "gemm_sync_status",
                          "gemm_check", "gemm_plan", "gemm_set_config", "gemm_last_config",
                          "gemm_tmem_columns", "gemm_set_timeout_ns", "gemm_rmsnorm",
-                         "gemm_rmsnorm_check", "gemm_rmsnorm_bwd", "gemm_rmsnorm_bwd_check"):
+                         "gemm_rmsnorm_check", "gemm_rmsnorm_bwd", "gemm_rmsnorm_bwd_check",
+                         "gemm_linear", "gemm_linear_check", "gemm_linear_bwd",
+                         "gemm_linear_bwd_check"):
                 getattr(lib, name).restype = i32
             _lib = lib
     return _lib
@@ -333,6 +373,28 @@ def gemm_rmsnorm_bwd(handle, problem: gemm_rmsnorm_bwd_t, workspace=None, worksp
     return st
 
 
+def gemm_linear_check(problem: gemm_linear_t) -> int:
+    return library().gemm_linear_check(ctypes.byref(problem))
+
+
+def gemm_linear(handle, problem: gemm_linear_t, stream=None, check=True) -> int:
+    st = library().gemm_linear(handle, ctypes.byref(problem), _stream(stream))
+    if check and st != GEMM_OK:
+        raise GemmError(st, "gemm_linear")
+    return st
+
+
+def gemm_linear_bwd_check(problem: gemm_linear_bwd_t) -> int:
+    return library().gemm_linear_bwd_check(ctypes.byref(problem))
+
+
+def gemm_linear_bwd(handle, problem: gemm_linear_bwd_t, stream=None, check=True) -> int:
+    st = library().gemm_linear_bwd(handle, ctypes.byref(problem), _stream(stream))
+    if check and st != GEMM_OK:
+        raise GemmError(st, "gemm_linear_bwd")
+    return st
+
+
 # ------------------------------------------------------------------ tensors
 
 # Type codes by the name of a tensor's dtype.
@@ -369,6 +431,26 @@ def _rows(t, M, N, what, code=None):
     return t.data_ptr(), s0 if M > 1 else max(s0, (N + 15) // 16 * 16)
 
 
+def _operand(t, R, K, what):
+    """(address, stride, layout) of an R x K product operand, either dimension contiguous."""
+    shape = t.shape
+    if len(shape) != 2 or shape[0] != R or shape[1] != K:
+        raise GemmError(GEMM_ERR_INVALID_ARG, f"{what}: shape {tuple(shape)}, not ({R}, {K})")
+    s0, s1 = t.stride()
+    if s1 == 1 and not (s0 == 1 and R > 1):
+        return t.data_ptr(), s0 if R > 1 else max(s0, (K + 15) // 16 * 16), GEMM_K_MAJOR
+    if s0 == 1 or R == 1:
+        return t.data_ptr(), s1 if K > 1 else max(s1, (R + 15) // 16 * 16), GEMM_MN_MAJOR
+    raise GemmError(GEMM_ERR_INVALID_ARG, f"{what}: neither dimension is contiguous")
+
+
+def _activation(name):
+    try:
+        return ACTIVATION_CODES[name]
+    except KeyError:
+        raise GemmError(GEMM_ERR_INVALID_ARG, f"activation {name!r}") from None
+
+
 def _vector(t, n, what, code=None):
     """Address of a contiguous vector of n elements (of type `code` if given); None for None."""
     if t is None:
@@ -383,8 +465,8 @@ def _vector(t, n, what, code=None):
 class Gemm:
     """Owns one library handle on `device`.
 
-    run, run_host: the C entry points' arguments.  rmsnorm, rmsnorm_bwd: the operators
-    around the product on tensors (torch's or any with data_ptr, dtype, shape and
+    run, run_host: the C entry points' arguments.  rmsnorm, rmsnorm_bwd, linear,
+    linear_bwd: the operators around the product on tensors (torch's or any with data_ptr, dtype, shape and
     stride), whose types, sizes and row strides the calls read off and check; outputs
     are the caller's tensors too.  Tensors are used on `stream` (None: the default
     stream) and must be ready there."""
@@ -473,3 +555,49 @@ class Gemm:
         if workspace is not None:
             ws, nbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
         gemm_rmsnorm_bwd(self.handle, p, ws, nbytes, stream)
+
+    def linear(self, a, b, d, bias=None, activation=None, residual=None, z=None, row_scale=None,
+               col_scale=None, alpha=1.0, stream=None):
+        """d = act(alpha * (a b^T) * row_scale * col_scale + bias) + residual; see gemm_linear
+        in the C header.  a [M, K] and b [N, K], either dimension contiguous (fp32 ones
+        are read at tf32 precision); activation: None, "relu", "gelu", "gelu_tanh" or "silu";
+        z receives what the activation is applied to."""
+        M, K = a.shape
+        N = b.shape[0]
+        ta, tb = _code(a, "a"), _code(b, "b")
+        pa, lda, la = _operand(a, M, K, "a")
+        pb, ldb, lb = _operand(b, N, K, "b")
+        pr, ldr = _rows(residual, M, N, "residual")
+        pz, ldz = _rows(z, M, N, "z")
+        pd, ldd = _rows(d, M, N, "d")
+        p = gemm_linear_t(M, N, K, ta or GEMM_TF32, tb or GEMM_TF32,
+                          0 if bias is None else _code(bias, "bias"),
+                          0 if residual is None else _code(residual, "residual"),
+                          0 if z is None else _code(z, "z"), _code(d, "d"), la, lb,
+                          _activation(activation), alpha, pa, lda, pb, ldb,
+                          _vector(row_scale, M, "row_scale", GEMM_F32),
+                          _vector(col_scale, N, "col_scale", GEMM_F32),
+                          _vector(bias, N, "bias"), pr, ldr, pz, ldz, pd, ldd)
+        gemm_linear(self.handle, p, stream)
+
+    def linear_bwd(self, dd, a, b, z=None, activation=None, dz=None, da=None, db=None, dbias=None,
+                   accumulate=False, alpha=1.0, stream=None):
+        """Gradients of linear from dd, the gradient of d: dz, da, db (added to with
+        `accumulate`) and dbias, each where given; see gemm_linear_bwd in the C header."""
+        M, N = dd.shape
+        K = a.shape[1]
+        t = _code(dd, "dd")
+        pdd, lddd = _rows(dd, M, N, "dd")
+        pz, ldz = _rows(z, M, N, "z", t)
+        pa, lda = _rows(a, M, K, "a", t)
+        pb, ldb = _rows(b, N, K, "b", t)
+        pdz, lddz = _rows(dz, M, N, "dz", t)
+        pda, ldda = _rows(da, M, K, "da")
+        pdb, lddb = _rows(db, N, K, "db")
+        p = gemm_linear_bwd_t(M, N, K, t, 0 if da is None else _code(da, "da"),
+                              0 if db is None else _code(db, "db"),
+                              0 if dbias is None else _code(dbias, "dbias"),
+                              _activation(activation), int(accumulate), alpha, pdd, lddd, pz, ldz,
+                              pa, lda, pb, ldb, pdz, lddz, pda, ldda, pdb, lddb,
+                              _vector(dbias, N, "dbias"))
+        gemm_linear_bwd(self.handle, p, stream)

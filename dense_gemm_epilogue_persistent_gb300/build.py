@@ -63,12 +63,15 @@ PLAIN_UNITS = [(f"kern_plain_ab{ab}_e{epw}_s{sk}", "kern_plain.cu",
 SHARED_UNITS = [(f"kern_shared_ab{ab}_m{mc}_n{nc}", "kern_shared.cu",
                  [f"-DGB300_AB={ab}", f"-DGB300_MC={mc}", f"-DGB300_NC={nc}"])
                 for ab in (2, 1, 4) for mc, nc in ((2, 1), (1, 2), (2, 2))]
-# The operators around the product: normalisation.
-ROW_UNITS = [("norm", "norm.cu", [])]
+# The operators around the product: normalisation, the linear layer and its kernels.
+ROW_UNITS = [("norm", "norm.cu", []), ("linear", "linear.cu", [])]
+LINEAR_UNITS = [(f"kern_linear_ab{ab}_e{epw}", "kern_linear.cu",
+                 [f"-DGB300_AB={ab}", f"-DGB300_EPW={epw}"]) for ab in (2, 1, 4) for epw in (1, 2)]
 # Files the multi-GPU library is built from (its translation units and every
 # header they include): none of them names a multicast TMA load.
-NOMC_FILES = ["gemm_api.cu", "norm.cu", "kern_plain.cu", "gemm_kernel.cuh", "rows.cuh", "ptx.cuh",
-              "kernels.h", "handle.h"]
+NOMC_FILES = ["gemm_api.cu", "norm.cu", "linear.cu", "kern_plain.cu", "kern_linear.cu",
+              "gemm_kernel.cuh", "activations.cuh", "rows.cuh", "ptx.cuh", "kernels.h", "handle.h",
+              "rows_host.h"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler",
@@ -78,9 +81,10 @@ FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler",
 def units(kind: str):
     """Translation units of one library: (object name, source, -D flags)."""
     if kind == "nomc":
-        return [("gemm_api_nomc", "gemm_api.cu", ["-DGB300_MULTICAST=0"])] + ROW_UNITS + PLAIN_UNITS
-    return ([("gemm_api", "gemm_api.cu", ["-DGB300_MULTICAST=1"])] + ROW_UNITS + PLAIN_UNITS +
-            SHARED_UNITS)
+        return ([("gemm_api_nomc", "gemm_api.cu", ["-DGB300_MULTICAST=0"])] + ROW_UNITS +
+                LINEAR_UNITS + PLAIN_UNITS)
+    return ([("gemm_api", "gemm_api.cu", ["-DGB300_MULTICAST=1"])] + ROW_UNITS + LINEAR_UNITS +
+            PLAIN_UNITS + SHARED_UNITS)
 
 
 def _nvcc() -> str:

@@ -43,12 +43,6 @@ constexpr int kDefaultEpiWaitNs = 0;
 // barriers
 constexpr int kSmemSlack = 1024 + 16 + 8 * gb300::kMaxEpiWarps * gb300::kMaxChunks + 16;
 
-// B's type: the descriptor's b when set (0 = GEMM_F32 means "same as ab").
-int b_type(const gemm_dtypes_t& t) { return t.b == GEMM_F32 ? t.ab : t.b; }
-
-bool reads_c(const gemm_problem_t& p) { return p.beta != 0.0f; }
-bool reads_x(const gemm_problem_t& p) { return p.X != nullptr && p.x_factor != 0.0f; }
-
 gemm_status_t validate(const gemm_problem_t* pp) {
   if (!pp) return GEMM_ERR_INVALID_ARG;
   const gemm_problem_t& p = *pp;
@@ -136,8 +130,10 @@ int epi_slot_bytes(const gemm_problem_t& p) {
 // (full/empty per stage, full/empty per accumulator stage, one per epilogue
 // warp and slot), tensor-memory address and abort flag, plus 1 KiB of
 // alignment slack.
-int total_smem(int cg, int bn, int ka, int stages, int slots, int slot_bytes) {
-  return ring_bytes(cg, bn, ka, stages) + slots * slot_bytes + 8 * 4 * slots + 4 + kSmemSlack;
+// `extra`: what an epilogue keeps there besides.
+int total_smem(int cg, int bn, int ka, int stages, int slots, int slot_bytes, int extra) {
+  return ring_bytes(cg, bn, ka, stages) + slots * slot_bytes + 8 * 4 * slots + 4 + kSmemSlack +
+         extra;
 }
 
 // Tile widths: multiples of 32 from 64 to 256 (the custom-epilogue example's
@@ -201,7 +197,7 @@ struct TileCost {
 };
 
 TileCost tile_cost(int64_t tiles, int64_t k_blocks, int cg, int ka, int bn, int64_t clusters,
-                   double epi_kb, bool can_split) {
+                   double epi_kb, bool can_split, double epi_extra) {
   clusters = std::max<int64_t>(1, clusters);
   const int64_t full = tiles / clusters, rem = tiles % clusters;
   TileCost t;
@@ -218,7 +214,7 @@ TileCost tile_cost(int64_t tiles, int64_t k_blocks, int cg, int ka, int bn, int6
     t.fixed = 11.0 - 0.4 * (bn - 128) / 128.0;
   }
   t.main_loop = (double)k_blocks * per_kb;
-  t.epilogue = (double)(bn / gb300::kEpiChunk) * (2.5 + 0.08 * epi_kb);
+  t.epilogue = (double)(bn / gb300::kEpiChunk) * (2.5 + 0.08 * epi_kb + epi_extra);
   return t;
 }
 
@@ -275,13 +271,12 @@ int64_t resident_clusters(int sm_count, const int* clusters_by_size, int csize) 
   return std::max(1, sm_count / csize);
 }
 
-gemm_status_t plan(const gemm_problem_t* pp, int sm_count, int smem_optin,
-                   const gemm_config_t* forced, gemm_config_t* out,
-                   const int* clusters_by_size = nullptr, bool stream_k_ok = true) {
-  gemm_status_t st = validate(pp);
-  if (st != GEMM_OK) return st;
-  if (!out || sm_count <= 0 || smem_optin <= 0) return GEMM_ERR_INVALID_ARG;
-  const gemm_problem_t& p = *pp;
+}  // namespace
+
+gemm_status_t gb300host::plan_valid(const gemm_problem_t& p, int sm_count, int smem_optin,
+                                    const gemm_config_t* forced, gemm_config_t* out,
+                                    const int* clusters_by_size, bool stream_k_ok,
+                                    const EpilogueExtra& extra) {
   const int ab_bytes = dtype_bytes(p.dtypes.ab);
 
   const int fcg = forced ? forced->cta_group : 0;
@@ -322,7 +317,8 @@ gemm_status_t plan(const gemm_problem_t* pp, int sm_count, int smem_optin,
           const int64_t units = resident_clusters(sm_count, clusters_by_size, a * m * n);
           const TileCost tc = tile_cost(tiles, cdiv(p.K, 128 / ab_bytes), a, ka, b, units, epi_kb,
                                         can_split_tail(p, a, b, m, n) &&
-                                            !(forced && forced->tail_split == 1));
+                                            !(forced && forced->tail_split == 1),
+                                        extra.chunk_cost);
           // Epilogue warps per lane quarter: forced, or 1 and (where it pays,
           // for clusters of one CTA group) 2.
           for (int e : {1, 2}) {
@@ -343,7 +339,7 @@ gemm_status_t plan(const gemm_problem_t* pp, int sm_count, int smem_optin,
   const int slot = epi_slot_bytes(p);
   auto max_stages_for = [&](int slots) {
     int n = 0;
-    while (n < kMaxStages && total_smem(cg, bn, ka, n + 1, slots, slot) <= smem_optin) ++n;
+    while (n < kMaxStages && total_smem(cg, bn, ka, n + 1, slots, slot, extra.smem) <= smem_optin) ++n;
     return n;
   };
   // The deepest A/B ring that still leaves two epilogue slots, then every
@@ -359,12 +355,12 @@ gemm_status_t plan(const gemm_problem_t* pp, int sm_count, int smem_optin,
   const int64_t units = resident_clusters(sm_count, clusters_by_size, csize);
   if (stages < 2 || stages > max_stages) return GEMM_ERR_UNSUPPORTED_CONFIG;
   int slots = 2;
-  while (slots < kMaxEpiSlots && total_smem(cg, bn, ka, stages, slots + 1, slot) <= smem_optin)
+  while (slots < kMaxEpiSlots && total_smem(cg, bn, ka, stages, slots + 1, slot, extra.smem) <= smem_optin)
     ++slots;
   if (forced && forced->epi_slots) {
     slots = forced->epi_slots;
     if (slots < 2 || slots > kMaxEpiSlots ||
-        total_smem(cg, bn, ka, stages, slots, slot) > smem_optin)
+        total_smem(cg, bn, ka, stages, slots, slot, extra.smem) > smem_optin)
       return GEMM_ERR_UNSUPPORTED_CONFIG;
   }
 
@@ -399,7 +395,7 @@ gemm_status_t plan(const gemm_problem_t* pp, int sm_count, int smem_optin,
   c.epi_slot_bytes = slot;
   // At least half the opt-in limit: one CTA per SM, so no two CTAs ever
   // contend for the 512 tensor-memory columns each allocates.
-  c.smem_bytes = std::max(total_smem(cg, bn, ka, stages, slots, slot), smem_optin / 2 + 1024);
+  c.smem_bytes = std::max(total_smem(cg, bn, ka, stages, slots, slot, extra.smem), smem_optin / 2 + 1024);
   c.tiles = tiles;
   // Stream-K: when the tiles fill less than one wave of clusters, every
   // resident cluster takes an equal contiguous share of all the tiles'
@@ -424,6 +420,18 @@ gemm_status_t plan(const gemm_problem_t* pp, int sm_count, int smem_optin,
   return GEMM_OK;
 }
 
+namespace {
+
+gemm_status_t plan(const gemm_problem_t* pp, int sm_count, int smem_optin,
+                   const gemm_config_t* forced, gemm_config_t* out,
+                   const int* clusters_by_size = nullptr, bool stream_k_ok = true) {
+  gemm_status_t st = validate(pp);
+  if (st != GEMM_OK) return st;
+  if (!out || sm_count <= 0 || smem_optin <= 0) return GEMM_ERR_INVALID_ARG;
+  return plan_valid(*pp, sm_count, smem_optin, forced, out, clusters_by_size, stream_k_ok,
+                    EpilogueExtra{});
+}
+
 CUtensorMapDataType tma_type(int dt) {
   switch (dt) {
     case GEMM_F16: return CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
@@ -433,10 +441,12 @@ CUtensorMapDataType tma_type(int dt) {
   }
 }
 
+}  // namespace
+
 // Operand tensor map.  K-major: dims {K, rows, L}, box {one 128-byte atom of
 // K, box_rows}.  MN-major: dims {rows, K, L}, box {128 bytes of rows, tile_k}.
 // Out-of-range elements of a box are filled with zeros.
-bool encode_operand(EncodeTiledFn enc, CUtensorMap* map, const void* ptr, int dt, int64_t rows,
+bool gb300host::encode_operand(EncodeTiledFn enc, CUtensorMap* map, const void* ptr, int dt, int64_t rows,
                     int64_t K, int64_t L, int64_t ld, bool mn_major, int box_rows, int tile_k) {
   const int64_t es = dtype_bytes(dt);
   cuuint64_t dims[3], strides[2];
@@ -458,12 +468,13 @@ bool encode_operand(EncodeTiledFn enc, CUtensorMap* map, const void* ptr, int dt
   return r == CUDA_SUCCESS;
 }
 
-// Epilogue tensor map over a packed M x N x L tensor, box = 32 rows x 32
+// Epilogue tensor map over an M x N x L tensor whose rows (row-major) or columns
+// (column-major) are `ld` elements apart, batches packed, box = 32 rows x 32
 // columns (one epilogue warp's rows of one chunk).  Row-major: dims {N, M, L},
 // 128-byte (fp32) or 64-byte (16-bit) rows swizzled to match the epilogue's
 // shared-memory reads.  Column-major: dims {M, N, L}, unswizzled.
-bool encode_epi(EncodeTiledFn enc, CUtensorMap* map, const void* ptr, int dt, int64_t M,
-                int64_t N, int64_t L, bool m_major) {
+bool gb300host::encode_epi(EncodeTiledFn enc, CUtensorMap* map, const void* ptr, int dt, int64_t M,
+                           int64_t N, int64_t L, bool m_major, int64_t ld) {
   const int64_t es = dtype_bytes(dt);
   cuuint64_t dims[3], strides[2];
   cuuint32_t box[3], estr[3] = {1, 1, 1};
@@ -471,14 +482,14 @@ bool encode_epi(EncodeTiledFn enc, CUtensorMap* map, const void* ptr, int dt, in
   CUtensorMapDataType ty = dt == GEMM_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : tma_type(dt);
   if (!m_major) {
     dims[0] = (cuuint64_t)N; dims[1] = (cuuint64_t)M; dims[2] = (cuuint64_t)L;
-    strides[0] = (cuuint64_t)(N * es);
-    strides[1] = (cuuint64_t)(N * es * M);
+    strides[0] = (cuuint64_t)(ld * es);
+    strides[1] = (cuuint64_t)(ld * es * M);
     box[0] = gb300::kEpiChunk; box[1] = gb300::kSubRows; box[2] = 1;
     sw = es == 4 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
   } else {
     dims[0] = (cuuint64_t)M; dims[1] = (cuuint64_t)N; dims[2] = (cuuint64_t)L;
-    strides[0] = (cuuint64_t)(M * es);
-    strides[1] = (cuuint64_t)(M * es * N);
+    strides[0] = (cuuint64_t)(ld * es);
+    strides[1] = (cuuint64_t)(ld * es * N);
     box[0] = gb300::kSubRows; box[1] = gb300::kEpiChunk; box[2] = 1;
     sw = CU_TENSOR_MAP_SWIZZLE_NONE;
   }
@@ -488,7 +499,7 @@ bool encode_epi(EncodeTiledFn enc, CUtensorMap* map, const void* ptr, int dt, in
   return r == CUDA_SUCCESS;
 }
 
-uint32_t make_idesc(int a_type, int b_type_, bool acc_f16, int cg, int bn, bool a_mn, bool b_mn) {
+uint32_t gb300host::make_idesc(int a_type, int b_type_, bool acc_f16, int cg, int bn, bool a_mn, bool b_mn) {
   // kind::f16 / kind::tf32: format 0 = fp16, 1 = bf16, 2 = tf32.
   // kind::f8f6f4: 0 = e4m3, 1 = e5m2.
   auto fmt = [](int t) {
@@ -504,6 +515,47 @@ uint32_t make_idesc(int a_type, int b_type_, bool acc_f16, int cg, int bn, bool 
   d |= (uint32_t)((128 * cg) >> 4) << 24;         // M >> 4
   return d;
 }
+
+// Resident clusters of kernel `kern` (its state in `vs`) at the shared memory
+// and cluster size of `cfg`; also raises its shared-memory attribute, once, to
+// the device's opt-in limit, so that every prepared launch of it (cached ones
+// included) may use any size.
+gemm_status_t gb300host::resident_kernel_clusters(const gemm_handle* h, VariantState& vs,
+                                                  const void* kern, const gemm_config_t& cfg,
+                                                  int csize, int* clusters) {
+  cudaLaunchConfig_t lc{};
+  cudaLaunchAttribute attr[1];
+  lc.blockDim = dim3(gb300::threads_for(cfg.epi_warps));
+  lc.dynamicSmemBytes = (size_t)cfg.smem_bytes;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)csize;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  lc.attrs = attr;
+  lc.numAttrs = 1;
+  if (!vs.smem_attr_set) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             h->smem_optin) != cudaSuccess) {
+      cudaGetLastError();
+      return GEMM_ERR_CUDA;
+    }
+    vs.smem_attr_set = true;
+  }
+  if (vs.occ_smem != cfg.smem_bytes) {
+    int nclusters = 0;
+    lc.gridDim = dim3((unsigned)(csize * h->sm_count));
+    if (cudaOccupancyMaxActiveClusters(&nclusters, kern, &lc) != cudaSuccess || nclusters <= 0) {
+      cudaGetLastError();
+      return GEMM_ERR_CUDA;
+    }
+    vs.occ_smem = cfg.smem_bytes;
+    vs.max_clusters = nclusters;
+  }
+  *clusters = vs.max_clusters;
+  return GEMM_OK;
+}
+
+namespace {
 
 // Plan the launch of problem `p` on handle `h` (which the caller holds
 // locked) and fill `ent`: configuration, kernel, grid, tensor maps and kernel
@@ -532,45 +584,17 @@ gemm_status_t prepare_launch(gemm_handle* h, const gemm_problem_t& p, LaunchEntr
                                 [ka - 1][cfg.cluster_m - 1][cfg.cluster_n - 1]
                                 [cfg.epi_warps - 1][sk];
 
-  cudaLaunchConfig_t lc{};
-  cudaLaunchAttribute attr[1];
-  lc.blockDim = dim3(gb300::threads_for(cfg.epi_warps));
-  lc.dynamicSmemBytes = (size_t)cfg.smem_bytes;
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)csize;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  lc.attrs = attr;
-  lc.numAttrs = 1;
-
-  // The attribute is raised once to the device's opt-in limit, so that every
-  // prepared launch of this kernel (cached ones included) may use any size.
-  if (!vs.smem_attr_set) {
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             h->smem_optin) != cudaSuccess) {
-      cudaGetLastError();
-      return GEMM_ERR_CUDA;
-    }
-    vs.smem_attr_set = true;
-  }
-  if (vs.occ_smem != cfg.smem_bytes) {
-    int nclusters = 0;
-    lc.gridDim = dim3((unsigned)(csize * h->sm_count));
-    if (cudaOccupancyMaxActiveClusters(&nclusters, kern, &lc) != cudaSuccess || nclusters <= 0) {
-      cudaGetLastError();
-      return GEMM_ERR_CUDA;
-    }
-    vs.occ_smem = cfg.smem_bytes;
-    vs.max_clusters = nclusters;
-  }
-  int64_t clusters = std::min<int64_t>(cfg.tiles + cfg.tail_split, vs.max_clusters);
+  int max_clusters = 0;
+  const gemm_status_t occ = resident_kernel_clusters(h, vs, kern, cfg, csize, &max_clusters);
+  if (occ != GEMM_OK) return occ;
+  int64_t clusters = std::min<int64_t>(cfg.tiles + cfg.tail_split, max_clusters);
   if (cfg.stream_k > 0) {
     // Stream-K runs one item pair on every cluster the kernel can keep
     // resident; the k-block ranges are cut for exactly that many clusters.
     const int64_t k_blocks = cdiv(K, (int64_t)cfg.tile_k);
-    clusters = std::min<int64_t>(cfg.stream_k, vs.max_clusters);
+    clusters = std::min<int64_t>(cfg.stream_k, max_clusters);
     if (clusters <= cfg.tiles || cfg.tiles * k_blocks < clusters) {
-      clusters = std::min<int64_t>(cfg.tiles, vs.max_clusters);   // not worth it here: off
+      clusters = std::min<int64_t>(cfg.tiles, max_clusters);   // not worth it here: off
       cfg.stream_k = 0;
     } else {
       cfg.stream_k = (int)clusters;
@@ -598,10 +622,11 @@ gemm_status_t prepare_launch(gemm_handle* h, const gemm_problem_t& p, LaunchEntr
   std::memset(&tmC, 0, sizeof(tmC));
   std::memset(&tmX, 0, sizeof(tmX));
   std::memset(&tmY, 0, sizeof(tmY));
-  if (!encode_epi(h->encode, &tmD, D, dtypes->d, M, N, L, cd_m) ||
-      (reads_c(p) && !encode_epi(h->encode, &tmC, C, dtypes->c, M, N, L, cd_m)) ||
-      (reads_x(p) && !encode_epi(h->encode, &tmX, X, dtypes->x, M, N, L, cd_m)) ||
-      (Y && !encode_epi(h->encode, &tmY, Y, dtypes->y, M, N, L, cd_m)))
+  const int64_t ld = cd_m ? M : N;            // packed
+  if (!encode_epi(h->encode, &tmD, D, dtypes->d, M, N, L, cd_m, ld) ||
+      (reads_c(p) && !encode_epi(h->encode, &tmC, C, dtypes->c, M, N, L, cd_m, ld)) ||
+      (reads_x(p) && !encode_epi(h->encode, &tmX, X, dtypes->x, M, N, L, cd_m, ld)) ||
+      (Y && !encode_epi(h->encode, &tmY, Y, dtypes->y, M, N, L, cd_m, ld)))
     return GEMM_ERR_CUDA;
 
   KernelParams kp{};

@@ -4,6 +4,10 @@
 //   (fp32 accumulation, or fp16 for fp16/fp8 inputs; fp32 epilogue; optional relu
 //   of alpha*(A*B) + beta*C before X is added)
 //
+// or, with EPI = 1, the linear layer's epilogue in the same pipeline:
+//
+//   Z = alpha*row_scale*col_scale*(A*B) + bias,   D = act(Z) + residual
+//
 // What the kernel computes and its warp roles follow "custom_epilogue_dense_gemm.py"
 // (CuTeDSL Blackwell example), module docstring "This GEMM works as follows" (DMA
 // warp; MMA warp; EPILOGUE warps that tcgen05.ld the accumulator, TMA-load C and X
@@ -68,6 +72,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include "activations.cuh"
 #include "kernels.h"
 #include "ptx.cuh"
 
@@ -85,6 +90,19 @@ struct EpiParams {
   int slots;                 // epilogue shared-memory slots (>= 2)
   uint32_t cd_bytes;         // bytes of a slot's C/D region
   uint32_t xy_bytes;         // bytes of a slot's X/Y region (0: neither X nor Y)
+  // The linear epilogue (EPI = 1; C holds the residual, Y the pre-activation):
+  // z = alpha * row_scale[m] * col_scale[n] * acc + bias[n],  D = act(z) + C
+  const float* row_scale;    // null: 1
+  const float* col_scale;    // null: 1
+  const void* bias;          // null: 0
+  int bias_dt;
+  int act;
+  // A TMA store clips at whole 16-byte pieces, so where a row of D or Z ends
+  // inside one, the chunk with the row's end is stored element by element.
+  int d_ragged, y_ragged;
+  void* d_ptr;
+  void* y_ptr;
+  long long ldd, ldy;
 };
 
 struct KernelParams {
@@ -491,6 +509,31 @@ __device__ __forceinline__ void smem_write_row(uint8_t* sub, int dt, int m_major
   }
 }
 
+// The linear epilogue's per-warp column vectors: 32 scales and 32 bias values
+// of the current chunk, in shared memory after the barriers.
+constexpr uint32_t kColumnVecBytes = 2 * kEpiChunk * 4;
+constexpr uint32_t kLinearSmem = kMaxEpiWarps * kColumnVecBytes + 16;
+
+// Element i of a vector of type dt as fp32.
+__device__ __forceinline__ float vector_elem(const void* p, int i, int dt) {
+  if (dt == DT_F32) return __ldg(static_cast<const float*>(p) + i);
+  const uint16_t b = __ldg(static_cast<const uint16_t*>(p) + i);
+  return dt == DT_F16 ? __half2float(__ushort_as_half(b)) : __uint_as_float((uint32_t)b << 16);
+}
+
+// Stores v[0, n) at p, one element at a time (a row's ragged end).
+__device__ __forceinline__ void store_row_end(void* p, int dt, int n,
+                                              const float (&v)[kEpiChunk]) {
+#pragma unroll
+  for (int i = 0; i < kEpiChunk; ++i) {
+    if (i >= n) continue;
+    if (dt == DT_F32) static_cast<float*>(p)[i] = v[i];
+    else
+      static_cast<uint16_t*>(p)[i] = dt == DT_F16 ? __half_as_ushort(__float2half_rn(v[i]))
+                                                  : __bfloat16_as_ushort(__float2bfloat16_rn(v[i]));
+  }
+}
+
 // Bytes of one warp's sub-tile of a tensor of type dt.
 __device__ __forceinline__ uint32_t sub_bytes(int dt) {
   return (uint32_t)(kSubRows * kEpiChunk) * (dt == DT_F32 ? 4u : 2u);
@@ -498,7 +541,8 @@ __device__ __forceinline__ uint32_t sub_bytes(int dt) {
 
 // ------------------------------------------------------------------ the kernel
 
-template <int CG, int AB_BYTES, int KA, int MC, int NC, int EPW, int SK>
+// EPI = 0: the GEMM's epilogue; 1: the linear layer's (EpiParams).
+template <int CG, int AB_BYTES, int KA, int MC, int NC, int EPW, int SK, int EPI = 0>
 __global__ void __launch_bounds__(threads_for(EPW), 1)
 persistent_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
                        const __grid_constant__ CUtensorMap tmB,
@@ -580,6 +624,8 @@ persistent_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
   // the partials it adds (pread)
   const uint32_t pdone = rfull0 + 8u * (uint32_t)(kMaxEpiWarps * kMaxChunks);
   const uint32_t pread = pdone + 8u;
+  // linear epilogue: the epilogue warps' column vectors
+  const uint32_t cvec0 = (pread + 8u + 15u) & ~15u;
   const uint32_t ring_bytes = (uint32_t)S * ((uint32_t)G::A_STAGE + (uint32_t)T.b_stage);
 
   if (threadIdx.x == 0) {
@@ -910,6 +956,23 @@ persistent_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
       tile_coords(wk.tile, p, tm, tn, tl);
       const int nchunks = half < 0 ? T.chunks : T.chunks / 2;
       const int ncol0 = tn * (BN * NC) + (int)gn * BN + (half > 0 ? BN / 2 : 0);
+      // Linear epilogue: this lane's row factor, and one column's scale and
+      // bias of the warp's first chunk, on their way while the accumulator is
+      // waited for (each chunk then fetches the next one's).
+      float row_factor = 1.f, col_s = 1.f, col_b = 0.f;
+      auto fetch_column = [&](int j) {
+        const int col = ncol0 + j * kEpiChunk + lane;
+        if (col < p.N) {
+          if (e.col_scale) col_s = __ldg(e.col_scale + col);
+          if (e.bias) col_b = vector_elem(e.bias, col, e.bias_dt);
+        }
+      };
+      if constexpr (EPI == 1) {
+        const int row = tm * G::CM + (int)gm * (G::BM * CG) + (int)rank * G::BM + q * kSubRows + lane;
+        row_factor = e.alpha;
+        if (e.row_scale && row < p.M) row_factor *= __ldg(e.row_scale + row);
+        if (strm < nchunks) fetch_column(strm);
+      }
       const long long t_t = stat_clock();
       const bool ready = wait_phase(tfull0 + 8u * acc, aph, w, kWaitEpilogue, p.epi_wait_ns);
       if constexpr (kRingStats) st_tfull += clock64() - t_t;
@@ -1049,7 +1112,7 @@ persistent_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
         long long t_r = 0;
         if constexpr (kRingStats) { t_r = clock64(); st_cfull += t_r - t_c; }
         got = __all_sync(0xFFFFFFFFu, got);
-        if constexpr (EPW == 1) {
+        if constexpr (EPW == 1 && EPI == 0) {
           // One warp per lane quarter: the C/X rows are read while the
           // accumulator load is in flight.
           if (got && e.read_c) {
@@ -1102,8 +1165,50 @@ persistent_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
         // D from the accumulator, C (zero when not read) and X; the branches
         // are uniform and outside the element loops.
         float dv[kEpiChunk];
+        bool d_edge = false, y_edge = false;
         const float al = e.alpha, be = e.beta, xf = e.x_factor;
-        if constexpr (EPW == 2) {
+        if constexpr (EPI == 1) {
+          // The chunk's column vectors go through shared memory, one column
+          // per lane in, all 32 broadcast out; the next chunk's are fetched
+          // meanwhile.
+          float* const cvec = reinterpret_cast<float*>(gbase + (cvec0 - base)) +
+                              ew * (kColumnVecBytes / 4);
+          cvec[lane] = col_s;
+          cvec[kEpiChunk + lane] = col_b;
+          __syncwarp();
+          if (j + EPW < nchunks) fetch_column(j + EPW);
+#pragma unroll
+          for (int k = 0; k < kEpiChunk / 4; ++k) {
+            const float4 s4 = reinterpret_cast<const float4*>(cvec)[k];
+            const float4 b4 = reinterpret_cast<const float4*>(cvec + kEpiChunk)[k];
+            dv[4 * k] = fmaf(__uint_as_float(raw_acc[4 * k]) * row_factor, s4.x, b4.x);
+            dv[4 * k + 1] = fmaf(__uint_as_float(raw_acc[4 * k + 1]) * row_factor, s4.y, b4.y);
+            dv[4 * k + 2] = fmaf(__uint_as_float(raw_acc[4 * k + 2]) * row_factor, s4.z, b4.z);
+            dv[4 * k + 3] = fmaf(__uint_as_float(raw_acc[4 * k + 3]) * row_factor, s4.w, b4.w);
+          }
+          const int col0 = ncol0 + j * kEpiChunk;
+          const bool row_end = col0 + kEpiChunk > p.N;
+          d_edge = row_end && e.d_ragged;
+          y_edge = row_end && e.y_ragged;
+          auto store_end = [&](void* t, long long ld, int dt) {
+            const long long row = row0 + lane;
+            if (row < p.M)
+              store_row_end(static_cast<uint8_t*>(t) + (row * ld + col0) * (dt == DT_F32 ? 4 : 2),
+                            dt, p.N - col0, dv);
+          };
+          if (e.write_y) {
+            if (y_edge) store_end(e.y_ptr, e.ldy, e.y_dt);
+            else smem_write_row(slot + cd_sub, e.y_dt, 0, lane, dv);
+          }
+          with_activation(e.act, [&](auto a) {
+#pragma unroll
+            for (int i = 0; i < kEpiChunk; ++i) dv[i] = activate<decltype(a)::value>(dv[i]);
+          });
+          if (e.read_c)
+            smem_row_each(slot, e.c_dt, 0, lane, [&](int i, float c) { dv[i] += c; });
+          __syncwarp();                     // every lane has read its residual row
+          if (d_edge) store_end(e.d_ptr, e.ldd, e.d_dt);
+        } else if constexpr (EPW == 2) {
           // Two warps per lane quarter (a 168-register budget): C and X are
           // folded into D as their pieces are read, after the accumulator
           // load, so no whole C or X row is held; the same operations in the
@@ -1165,8 +1270,8 @@ persistent_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
               dv[i] = fmaf(al, __uint_as_float(raw_acc[i]), be * cv[i]);
           }
         }
-        smem_write_row(slot, e.d_dt, e.cd_m_major, lane, dv);
-        if (e.write_y) {
+        if (!d_edge) smem_write_row(slot, e.d_dt, e.cd_m_major, lane, dv);
+        if (EPI == 0 && e.write_y) {
           float yv[kEpiChunk];
 #pragma unroll
           for (int i = 0; i < kEpiChunk; ++i) yv[i] = __uint_as_float(raw_acc[i]);
@@ -1184,8 +1289,8 @@ persistent_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
           if (dbg_check(x0 >= 0 && x1 >= 0 && inner_ok(x0, e.d_dt) &&
                             (!e.write_y || inner_ok(x0, e.y_dt)),
                         kChkEpiStore, w)) {
-            tma_store_3d(&tmD, s_addr, x0, x1, tl, pol_out);
-            if (e.write_y) tma_store_3d(&tmY, s_addr + cd_sub, x0, x1, tl, pol_out);
+            if (!d_edge) tma_store_3d(&tmD, s_addr, x0, x1, tl, pol_out);
+            if (e.write_y && !y_edge) tma_store_3d(&tmY, s_addr + cd_sub, x0, x1, tl, pol_out);
           }
           bulk_commit_group();
           if (loads) {

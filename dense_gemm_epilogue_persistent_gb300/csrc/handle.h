@@ -91,6 +91,7 @@ struct gemm_handle {
   gemm_config_t last{};
   uint64_t timeout_ns = gb300host::kDefaultTimeoutNs;
   gb300host::VariantState variants[3][2][2][2][2][2][2];   // [ab 16/8/32][cta_group][k atoms][mc][nc][epw][sk]
+  gb300host::VariantState linear_variants[3][2][2][2];   // [ab][cta_group][k atoms][epw]
   int clusters_by_size[9] = {0, 0, 0, 0, 0, 0, 0, 0, 0};   // resident clusters of 1, 2, 4, 8 CTAs
   uint64_t config_gen = 0;
   gb300host::LaunchEntry cache[gb300host::kLaunchCacheEntries];
@@ -129,6 +130,33 @@ inline bool is_layout(int v) { return v == GEMM_K_MAJOR || v == GEMM_MN_MAJOR; }
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// B's type: the descriptor's b when set (0 = GEMM_F32 means "same as ab").
+inline int b_type(const gemm_dtypes_t& t) { return t.b == GEMM_F32 ? t.ab : t.b; }
+
+inline bool reads_c(const gemm_problem_t& p) { return p.beta != 0.0f; }
+inline bool reads_x(const gemm_problem_t& p) { return p.X != nullptr && p.x_factor != 0.0f; }
+
+// What an epilogue other than the GEMM's own adds to a plan: shared memory per
+// CTA, and time per 32-column chunk in the cost model's units.
+struct EpilogueExtra {
+  int smem = 0;
+  double chunk_cost = 0.0;
+};
+
+// gemm_api.cu: the planner on a problem whose arguments have been checked, and
+// what a launch is prepared with (described at their definitions).
+gemm_status_t plan_valid(const gemm_problem_t& p, int sm_count, int smem_optin,
+                         const gemm_config_t* forced, gemm_config_t* out,
+                         const int* clusters_by_size, bool stream_k_ok,
+                         const EpilogueExtra& extra);
+bool encode_operand(EncodeTiledFn enc, CUtensorMap* map, const void* ptr, int dt, int64_t rows,
+                    int64_t K, int64_t L, int64_t ld, bool mn_major, int box_rows, int tile_k);
+bool encode_epi(EncodeTiledFn enc, CUtensorMap* map, const void* ptr, int dt, int64_t M,
+                int64_t N, int64_t L, bool m_major, int64_t ld);
+uint32_t make_idesc(int a_type, int b_type_, bool acc_f16, int cg, int bn, bool a_mn, bool b_mn);
+gemm_status_t resident_kernel_clusters(const gemm_handle* h, VariantState& vs, const void* kern,
+                                       const gemm_config_t& cfg, int csize, int* clusters);
 
 // Whether the calling thread's current device is the handle's.
 inline bool on_device(const gemm_handle* h) {

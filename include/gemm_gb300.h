@@ -379,15 +379,16 @@ gemm_status_t gemm_run_noalloc(int64_t M, int64_t N, int64_t K, int64_t L,
 
 /* ====================================================================
  * Operators around the product: root-mean-square normalisation (which can
- * write the 8-bit operand and row scales of an fp8 product) and its backward
- * pass.
+ * write the 8-bit operand and row scales of an fp8 product), the linear layer
+ * (the product with scales, bias, activation and residual), and the backward
+ * pass of each.
  *
  * All of them: tensors are device memory of the handle's device, owned by the
  * caller; matrices are row-major with a leading dimension (row stride, in
- * elements) of their own, which may exceed the row length; every matrix, weight
- * and bias starts on a 16-byte boundary and every leading dimension times its element size is a multiple of 16
+ * elements) of their own, which may exceed the row length; every matrix and
+ * weight vector starts on a 16-byte boundary and every leading dimension times its element size is a multiple of 16
  * bytes (GEMM_ERR_MISALIGNED otherwise), while the sizes themselves may be
- * odd.  Calls validate on the host, enqueue on `stream` and return; they
+ * odd; bias and scale vectors need their elements' alignment only.  Calls validate on the host, enqueue on `stream` and return; they
  * neither synchronise nor allocate, keep nothing between calls, and may be
  * captured into a CUDA graph.  Sums and statistics are fp32 in a fixed order:
  * the same call gives the same bits.  Any overlap between an output and
@@ -460,6 +461,81 @@ int64_t gemm_rmsnorm_bwd_workspace(int64_t M, int64_t H);
 gemm_status_t gemm_rmsnorm_bwd_check(const gemm_rmsnorm_bwd_t* p);
 gemm_status_t gemm_rmsnorm_bwd(gemm_handle_t h, const gemm_rmsnorm_bwd_t* p, void* workspace,
                                int64_t workspace_bytes, struct CUstream_st* stream);
+
+/* Activations: max(z, 0); z Phi(z) with the normal distribution function;
+ * z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2; z / (1 + exp(-z)). */
+typedef enum {
+  GEMM_ACT_NONE = 0, GEMM_ACT_RELU = 1, GEMM_ACT_GELU = 2, GEMM_ACT_GELU_TANH = 3,
+  GEMM_ACT_SILU = 4
+} gemm_activation_t;
+
+/* The linear layer:
+ *     z(m,n) = alpha * row_scale(m) * col_scale(n) * sum_k A(m,k) B(n,k) + bias(n)
+ *     D(m,n) = act(z(m,n)) + R(m,n),        Z(m,n) = z(m,n)
+ * fp32 accumulation and epilogue; Z and D are each rounded once, D from the
+ * unrounded z.
+ *   A, B: layouts, leading dimensions and types as for gemm_run with L = 1
+ *   (F16, BF16, E4M3, E5M2 or TF32; the types equal, or any pair of 8-bit ones;
+ *   TF32 K-major only); required when K > 0.  K = 0: the sum is 0.
+ *   row_scale [M], col_scale [N]: fp32, optional (NULL: 1).  bias [N]: F32, F16
+ *   or BF16, optional.  R (residual) and Z (the pre-activation the backward
+ *   pass needs): optional.  R, Z and D: F32, F16 or BF16 each.
+ *   M or N = 0: nothing to do.
+ * D may be R (same type and leading dimension).  A configuration forced with
+ * gemm_set_config applies (clusters of one CTA group only), and a launch is
+ * under the watchdog of gemm_sync_status. */
+typedef struct {
+  int64_t M, N, K;
+  gemm_dtype_t a_type, b_type, bias_type, r_type, z_type, d_type;
+  gemm_layout_t layoutA, layoutB;
+  gemm_activation_t activation;
+  float alpha;
+  const void* A; int64_t lda;
+  const void* B; int64_t ldb;
+  const float* row_scale;
+  const float* col_scale;
+  const void* bias;
+  const void* R; int64_t ldr;
+  void* Z; int64_t ldz;
+  void* D; int64_t ldd;
+} gemm_linear_t;
+
+gemm_status_t gemm_linear_check(const gemm_linear_t* p);
+gemm_status_t gemm_linear(gemm_handle_t h, const gemm_linear_t* p, struct CUstream_st* stream);
+
+/* Its backward pass for 16-bit operands without scale vectors (K-major a [M,K]
+ * and b [N,K], z as the forward pass wrote it, dd the gradient of D):
+ *     dz = dd * act'(z)               rounded to `type` where it is written
+ *     dbias(n) = sum_m dz(m,n)        of the unrounded values
+ *     da = alpha * dz b               of the rounded ones, as are
+ *     db = alpha * dz^T a  (+ db)     where accumulate is non-zero
+ * The gradient of the residual is dd itself.
+ *   type: F16 or BF16, the type of dd, z, a, b and dz.  da_type, db_type,
+ *   dbias_type: F32, F16 or BF16.
+ *   z: required unless activation is NONE.  da, db, dbias: each optional
+ *   (NULL: not computed; a is read for db only, b for da only).  dz: required
+ *   for da or db with an activation; without one it is optional (where given
+ *   it receives dd).  M = 0: dbias and db are 0 (db unchanged where accumulated).
+ * dz may be dd or z (same leading dimension). */
+typedef struct {
+  int64_t M, N, K;
+  gemm_dtype_t type, da_type, db_type, dbias_type;
+  gemm_activation_t activation;
+  int accumulate;
+  float alpha;
+  const void* dd; int64_t lddd;
+  const void* z; int64_t ldz;
+  const void* a; int64_t lda;
+  const void* b; int64_t ldb;
+  void* dz; int64_t lddz;
+  void* da; int64_t ldda;
+  void* db; int64_t lddb;
+  void* dbias;
+} gemm_linear_bwd_t;
+
+gemm_status_t gemm_linear_bwd_check(const gemm_linear_bwd_t* p);
+gemm_status_t gemm_linear_bwd(gemm_handle_t h, const gemm_linear_bwd_t* p,
+                              struct CUstream_st* stream);
 
 #ifdef __cplusplus
 }
