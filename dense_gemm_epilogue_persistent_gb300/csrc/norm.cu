@@ -105,6 +105,100 @@ rmsnorm_any_kernel(const __grid_constant__ NormParams p) {
   }
 }
 
+// A row held in registers: read once, written once.  T threads (a block, or a
+// warp where WARP: then a block holds 4 rows) keep VPT vectors of the row each,
+// vector i of thread t being elements 8 (i T + t).  The outputs follow two
+// reductions over the row (sum of squares; largest output magnitude where the
+// output is 8-bit).  DRAM-bound: 4 es + eo bytes an element with a residual.
+template <int DT, int VPT, bool WARP>
+__global__ void __launch_bounds__(WARP ? 128 : 1024)
+rmsnorm_row_kernel(const __grid_constant__ NormParams p) {
+  __shared__ float sums[32];
+  __shared__ uint32_t maxs[32];
+  grid_launch_dependents();
+  grid_dependency_wait();
+  const int t = WARP ? threadIdx.x & 31 : threadIdx.x;
+  const int T = WARP ? 32 : blockDim.x;
+  const long long row = WARP ? (long long)blockIdx.x * 4 + (threadIdx.x >> 5) : blockIdx.x;
+  if (WARP && row >= p.M) return;
+  constexpr int es = elem_bytes(DT);
+  const uint8_t* const x = static_cast<const uint8_t*>(p.x) + row * p.ldx * es;
+  RawVec<DT> xv[VPT], rv[VPT];
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int c = (i * T + t) * kVec;
+    if (c < p.H) xv[i] = load_raw<DT>(x, c, p.H);
+    else xv[i] = RawVec<DT>{};
+  }
+  if (p.r) {
+    const uint8_t* const r = static_cast<const uint8_t*>(p.r) + row * p.ldr * es;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int c = (i * T + t) * kVec;
+      if (c < p.H) rv[i] = load_raw<DT>(r, c, p.H);
+      else rv[i] = RawVec<DT>{};
+    }
+  }
+  float v[VPT][kVec];
+  float ss = 0.f;
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    unpack<DT>(xv[i], v[i]);
+    if (p.r) {
+      float u[kVec];
+      unpack<DT>(rv[i], u);
+#pragma unroll
+      for (int k = 0; k < kVec; ++k) v[i][k] += u[k];
+    }
+#pragma unroll
+    for (int k = 0; k < kVec; ++k) ss = fmaf(v[i][k], v[i][k], ss);
+  }
+  const float total = WARP ? warp_sum(ss) : block_sum(ss, sums);
+  const float rstd = 1.f / sqrtf(total * p.inv_h + p.eps);
+  if (t == 0 && p.rstd) p.rstd[row] = rstd;
+  if (p.h) {
+    uint8_t* const h = static_cast<uint8_t*>(p.h) + row * p.ldh * es;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int c = (i * T + t) * kVec;
+      if (c < p.H) store_vec(h, DT, c, p.H, v[i]);
+    }
+  }
+  const bool fp8 = p.y_dt >= DT_E4M3;
+  uint32_t big = 0;
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int c = (i * T + t) * kVec;
+    if (c >= p.H) continue;
+    float w[kVec];
+    load_vec_dt(p.w, p.w_dt, c, p.H, w);
+#pragma unroll
+    for (int k = 0; k < kVec; ++k) {
+      v[i][k] = v[i][k] * rstd * w[k];
+      big = max(big, abs_bits(v[i][k]));
+    }
+  }
+  float inv = 1.f;
+  if (fp8) {
+    big = WARP ? __reduce_max_sync(0xFFFFFFFFu, big) : block_max(big, maxs);
+    big = max(big, __float_as_uint(kAmaxFloor));
+    const float amax = __uint_as_float(big), top = largest_fp8(p.y_dt);
+    inv = top / amax;
+    if (t == 0) p.scale[row] = amax / top;
+  }
+  uint8_t* const y = static_cast<uint8_t*>(p.y) + row * p.ldy * elem_bytes(p.y_dt);
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int c = (i * T + t) * kVec;
+    if (c >= p.H) continue;
+    if (fp8) {
+#pragma unroll
+      for (int k = 0; k < kVec; ++k) v[i][k] *= inv;
+    }
+    store_vec(y, p.y_dt, c, p.H, v[i]);
+  }
+}
+
 // ------------------------------------------------------------------ backward
 
 struct NormBwdParams {
@@ -119,7 +213,21 @@ struct NormBwdParams {
   int M, H;
   int w_dt, dw_dt;
   float inv_h;
+  float* partials;                  // rows of H partial weight gradients
 };
+
+struct SumParams {
+  const float* partials;
+  void* out;
+  int rows, H, out_dt;
+};
+
+// Partial sums [c, c + 8) of a row of H floats (rows of any alignment).
+__device__ __forceinline__ void store_partial(float* row, int c, int n, const float (&v)[kVec]) {
+#pragma unroll
+  for (int k = 0; k < kVec; ++k)
+    if (c + k < n) row[c + k] = v[k];
+}
 
 // dx of a row of any length: one block, two passes (mean of dy w n, outputs);
 // dx may be dh.
@@ -162,6 +270,141 @@ rmsnorm_bwd_any_kernel(const __grid_constant__ NormBwdParams p) {
       for (int i = 0; i < kVec; ++i) o[i] += u[i];
     }
     store_vec(dx, DT, c, p.H, o);
+  }
+}
+
+// Both gradients in one reading of dy, h and dh.  Blocks walk the rows
+// blockIdx.x, + gridDim.x, ...; each thread keeps the same VPT vectors of
+// columns throughout (a block's T threads span a row; with WARP a warp does and
+// the block's 8 warps take different rows), so the weight gradient of the rows
+// it has seen stays in its registers.  The next row's vectors are requested
+// before the current row's reduction.  At the end every block writes its H
+// sums to the workspace; sum_partials_kernel adds them in block order.
+template <int DT, int VPT, bool WARP>
+__global__ void __launch_bounds__(WARP ? 256 : 512)
+rmsnorm_bwd_row_kernel(const __grid_constant__ NormBwdParams p) {
+  __shared__ float sums[2][32];
+  extern __shared__ float warp_dw[];     // WARP: 8 rows of H sums
+  grid_launch_dependents();
+  grid_dependency_wait();
+  const int t = WARP ? threadIdx.x & 31 : threadIdx.x;
+  const int T = WARP ? 32 : blockDim.x;
+  const int walkers = WARP ? gridDim.x * 8 : gridDim.x;
+  constexpr int es = elem_bytes(DT);
+  RawVec<DT> g_raw[VPT], h_raw[VPT], d_raw[VPT];
+  auto fetch = [&](long long row) {
+    const uint8_t* const dy = static_cast<const uint8_t*>(p.dy) + row * p.lddy * es;
+    const uint8_t* const h = static_cast<const uint8_t*>(p.h) + row * p.ldh * es;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int c = (i * T + t) * kVec;
+      if (c >= p.H) continue;
+      g_raw[i] = load_raw<DT>(dy, c, p.H);
+      h_raw[i] = load_raw<DT>(h, c, p.H);
+      if (p.dh)
+        d_raw[i] = load_raw<DT>(static_cast<const uint8_t*>(p.dh) + row * p.lddh * es, c, p.H);
+    }
+  };
+  float dw[VPT][kVec];
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    g_raw[i] = h_raw[i] = d_raw[i] = RawVec<DT>{};
+#pragma unroll
+    for (int k = 0; k < kVec; ++k) dw[i][k] = 0.f;
+  }
+  const int first = WARP ? (int)blockIdx.x * 8 + (threadIdx.x >> 5) : blockIdx.x;
+  if (first < p.M) fetch(first);
+  int buf = 0;
+  for (long long row = first; row < p.M; row += walkers, buf ^= 1) {
+    float n[VPT][kVec], g[VPT][kVec], u[VPT][kVec];
+    const float rstd = p.rstd[row];
+    float dot = 0.f;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      unpack<DT>(g_raw[i], g[i]);
+      unpack<DT>(h_raw[i], n[i]);
+      unpack<DT>(d_raw[i], u[i]);
+    }
+    if (row + walkers < p.M) fetch(row + walkers);
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int c = (i * T + t) * kVec;
+      float w[kVec];
+      if (c < p.H) {
+        load_vec_dt(p.w, p.w_dt, c, p.H, w);
+      } else {
+#pragma unroll
+        for (int k = 0; k < kVec; ++k) w[k] = 0.f;
+      }
+#pragma unroll
+      for (int k = 0; k < kVec; ++k) {
+        n[i][k] *= rstd;
+        dw[i][k] = fmaf(g[i][k], n[i][k], dw[i][k]);
+        g[i][k] *= w[k];
+        dot = fmaf(g[i][k], n[i][k], dot);
+      }
+    }
+    const float mean = (WARP ? warp_sum(dot) : block_sum(dot, sums[buf])) * p.inv_h;
+    uint8_t* const dx = static_cast<uint8_t*>(p.dx) + row * p.lddx * es;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int c = (i * T + t) * kVec;
+      if (c >= p.H) continue;
+#pragma unroll
+      for (int k = 0; k < kVec; ++k) {
+        g[i][k] = rstd * (g[i][k] - n[i][k] * mean);
+        if (p.dh) g[i][k] += u[i][k];
+      }
+      store_vec(dx, DT, c, p.H, g[i]);
+    }
+  }
+  float* const out = p.partials + (long long)blockIdx.x * p.H;
+  if constexpr (!WARP) {
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int c = (i * T + t) * kVec;
+      if (c < p.H) store_partial(out, c, p.H, dw[i]);
+    }
+  } else {
+    float* const mine = warp_dw + (threadIdx.x >> 5) * p.H;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int c = (i * T + t) * kVec;
+#pragma unroll
+      for (int k = 0; k < kVec; ++k)
+        if (c + k < p.H) mine[c + k] = dw[i][k];
+    }
+    __syncthreads();
+    for (int c = threadIdx.x; c < p.H; c += 256) {
+      float s = 0.f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) s += warp_dw[k * p.H + c];
+      out[c] = s;
+    }
+  }
+}
+
+// Column sums of `rows` rows of H partial sums: 32 columns a block, 32 row
+// groups, added in order.
+__global__ void __launch_bounds__(1024)
+sum_partials_kernel(const __grid_constant__ SumParams p) {
+  __shared__ float part[32][33];
+  grid_launch_dependents();
+  grid_dependency_wait();
+  const int lane = threadIdx.x & 31, group = threadIdx.x >> 5;
+  const int c = blockIdx.x * 32 + lane;
+  float s = 0.f;
+  if (c < p.H) {
+#pragma unroll 4
+    for (int r = group; r < p.rows; r += 32) s += p.partials[(long long)r * p.H + c];
+  }
+  part[group][lane] = s;
+  __syncthreads();
+  if (group == 0 && c < p.H) {
+    s = 0.f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) s += part[i][lane];
+    store_elem(p.out, c, p.out_dt, s);
   }
 }
 
@@ -211,6 +454,74 @@ using namespace gb300host;
 // warps, at most 1024.
 int row_threads(int64_t H) {
   return (int)std::min<int64_t>(1024, cdiv(cdiv(H, gb300::kVec), 32) * 32);
+}
+
+// Rows up to kRowMax elements are held in registers: vectors per thread and
+// threads per row (a warp's 32 where warp).
+constexpr int kRowMax = 32768, kBwdRowMax = 16384;
+struct RowShape {
+  int vpt, threads;
+  bool warp;
+};
+
+RowShape forward_shape(int64_t M, int64_t H) {
+  const int vecs = (int)cdiv(H, gb300::kVec);
+  (void)M;
+  RowShape s{};
+  if (vecs <= 128) {
+    s.warp = true;
+    s.vpt = vecs <= 32 ? 1 : vecs <= 64 ? 2 : 4;
+    s.threads = 128;
+    return s;
+  }
+  s.vpt = vecs <= 256 ? 1 : vecs <= 2048 ? 2 : 4;
+  s.threads = (int)cdiv(cdiv(vecs, s.vpt), 32) * 32;
+  return s;
+}
+
+RowShape backward_shape(int64_t H) {
+  const int vecs = (int)cdiv(H, gb300::kVec);
+  RowShape s{};
+  if (vecs <= 128) {
+    s.warp = true;
+    s.vpt = vecs <= 32 ? 1 : vecs <= 64 ? 2 : 4;
+    s.threads = 256;
+    return s;
+  }
+  s.vpt = vecs <= 256 ? 1 : vecs <= 1024 ? 2 : 4;
+  s.threads = (int)cdiv(cdiv(vecs, s.vpt), 32) * 32;
+  return s;
+}
+
+// Blocks of the backward row kernel (one row of partial sums each).
+constexpr int kBwdBlocks = 304;
+int backward_blocks(int64_t M, int64_t H) {
+  const RowShape s = backward_shape(H);
+  return (int)std::min<int64_t>(s.warp ? cdiv(M, 8) : M, kBwdBlocks);
+}
+
+typedef void (*NormKern)(gb300::NormParams);
+template <int DT, bool WARP>
+NormKern forward_kernel(int vpt) {
+  return vpt == 1   ? gb300::rmsnorm_row_kernel<DT, 1, WARP>
+         : vpt == 2 ? gb300::rmsnorm_row_kernel<DT, 2, WARP>
+                    : gb300::rmsnorm_row_kernel<DT, 4, WARP>;
+}
+template <int DT>
+NormKern forward_kernel(const RowShape& s) {
+  return s.warp ? forward_kernel<DT, true>(s.vpt) : forward_kernel<DT, false>(s.vpt);
+}
+
+typedef void (*NormBwdKern)(gb300::NormBwdParams);
+template <int DT, bool WARP>
+NormBwdKern backward_kernel(int vpt) {
+  return vpt == 1   ? gb300::rmsnorm_bwd_row_kernel<DT, 1, WARP>
+         : vpt == 2 ? gb300::rmsnorm_bwd_row_kernel<DT, 2, WARP>
+                    : gb300::rmsnorm_bwd_row_kernel<DT, 4, WARP>;
+}
+template <int DT>
+NormBwdKern backward_kernel(const RowShape& s) {
+  return s.warp ? backward_kernel<DT, true>(s.vpt) : backward_kernel<DT, false>(s.vpt);
 }
 
 gemm_status_t check_extents(int64_t M, int64_t H) {
@@ -291,15 +602,22 @@ GEMM_API gemm_status_t gemm_rmsnorm(gemm_handle_t h, const gemm_rmsnorm_t* pp,
   k.M = (int)p.M; k.H = (int)p.H;
   k.eps = p.eps;
   k.inv_h = (float)(1.0 / (double)p.H);
-  void (*kern)(gb300::NormParams) = p.type == GEMM_F32   ? gb300::rmsnorm_any_kernel<gb300::DT_F32>
+  if (p.H <= kRowMax) {
+    const RowShape s = forward_shape(p.M, p.H);
+    return launch(p.type == GEMM_F32   ? forward_kernel<gb300::DT_F32>(s)
+                  : p.type == GEMM_F16 ? forward_kernel<gb300::DT_F16>(s)
+                                       : forward_kernel<gb300::DT_BF16>(s),
+                  k, s.warp ? cdiv(p.M, 4) : p.M, s.threads, 0, stream);
+  }
+  NormKern kern = p.type == GEMM_F32   ? gb300::rmsnorm_any_kernel<gb300::DT_F32>
                                     : p.type == GEMM_F16 ? gb300::rmsnorm_any_kernel<gb300::DT_F16>
                                                          : gb300::rmsnorm_any_kernel<gb300::DT_BF16>;
   return launch(kern, k, p.M, row_threads(p.H), 0, stream);
 }
 
 GEMM_API int64_t gemm_rmsnorm_bwd_workspace(int64_t M, int64_t H) {
-  (void)M; (void)H;
-  return 0;
+  if (M <= 0 || H <= 0 || H > kBwdRowMax) return 0;
+  return backward_blocks(M, H) * H * (int64_t)sizeof(float);
 }
 
 GEMM_API gemm_status_t gemm_rmsnorm_bwd(gemm_handle_t h, const gemm_rmsnorm_bwd_t* pp,
@@ -324,11 +642,21 @@ GEMM_API gemm_status_t gemm_rmsnorm_bwd(gemm_handle_t h, const gemm_rmsnorm_bwd_
   k.dw = p.dweight; k.dw_dt = device_dt(p.dw_type);
   k.M = (int)p.M; k.H = (int)p.H;
   k.inv_h = (float)(1.0 / (double)p.H);
-  typedef void (*Kern)(gb300::NormBwdParams);
-  Kern dx = p.type == GEMM_F32   ? gb300::rmsnorm_bwd_any_kernel<gb300::DT_F32>
+  if (need > 0) {
+    const RowShape s = backward_shape(p.H);
+    const int blocks = backward_blocks(p.M, p.H);
+    k.partials = static_cast<float*>(workspace);
+    GB300_CHECK(launch(p.type == GEMM_F32   ? backward_kernel<gb300::DT_F32>(s)
+                       : p.type == GEMM_F16 ? backward_kernel<gb300::DT_F16>(s)
+                                            : backward_kernel<gb300::DT_BF16>(s),
+                       k, blocks, s.threads, s.warp ? 8 * (size_t)p.H * sizeof(float) : 0, stream));
+    gb300::SumParams q{k.partials, p.dweight, blocks, (int)p.H, k.dw_dt};
+    return launch(gb300::sum_partials_kernel, q, cdiv(p.H, 32), 1024, 0, stream);
+  }
+  NormBwdKern dx = p.type == GEMM_F32   ? gb300::rmsnorm_bwd_any_kernel<gb300::DT_F32>
             : p.type == GEMM_F16 ? gb300::rmsnorm_bwd_any_kernel<gb300::DT_F16>
                                  : gb300::rmsnorm_bwd_any_kernel<gb300::DT_BF16>;
-  Kern dw = p.type == GEMM_F32   ? gb300::rmsnorm_dw_kernel<gb300::DT_F32>
+  NormBwdKern dw = p.type == GEMM_F32   ? gb300::rmsnorm_dw_kernel<gb300::DT_F32>
             : p.type == GEMM_F16 ? gb300::rmsnorm_dw_kernel<gb300::DT_F16>
                                  : gb300::rmsnorm_dw_kernel<gb300::DT_BF16>;
   if (p.M > 0) GB300_CHECK(launch(dx, k, p.M, row_threads(p.H), 0, stream));

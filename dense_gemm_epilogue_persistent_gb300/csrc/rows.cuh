@@ -152,12 +152,17 @@ __device__ __forceinline__ void store_vec(void* row, int dt, int c, int n,
 
 // ------------------------------------------------------------------ reductions
 
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  return v;
+}
+
 // Sum over the block, the same value in every thread and in every run: lanes
 // by a butterfly, warps in warp order.  `scratch` holds 32 floats; two calls
 // in a row need different scratch (or a barrier between them).
 __device__ __forceinline__ float block_sum(float v, float* scratch) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  v = warp_sum(v);
   const int warps = (int)blockDim.x >> 5;
   if (warps == 1) return v;
   if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
