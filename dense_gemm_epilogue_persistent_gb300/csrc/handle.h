@@ -101,6 +101,10 @@ struct gemm_handle {
   size_t ws_bytes = 0;
   std::mutex ws_mu;
   unsigned long long* d_stats = nullptr;   // ring statistics (statistics build only)
+  // Kernels whose dynamic shared-memory limit this handle has raised.
+  static constexpr int kMaxRaised = 64;
+  const void* raised[kMaxRaised] = {};
+  int raised_count = 0;
   // Stream-K workspace: one 128 x 256 fp32 partial slot and one flag per SM
   // (null: stream-K is never planned for this handle).
   float* sk_partials = nullptr;

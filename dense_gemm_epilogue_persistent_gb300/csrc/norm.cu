@@ -214,6 +214,7 @@ struct NormBwdParams {
   int w_dt, dw_dt;
   float inv_h;
   float* partials;                  // rows of H partial weight gradients
+  int depth;                        // rows a thread requests ahead
 };
 
 struct SumParams {
@@ -228,6 +229,61 @@ __device__ __forceinline__ void store_partial(float* row, int c, int n, const fl
   for (int k = 0; k < kVec; ++k)
     if (c + k < n) row[c + k] = v[k];
 }
+
+// The backward kernel's blocks stay and walk rows first, first + walkers, ...;
+// every thread copies its own vectors of the next rows into its own slots of
+// shared memory with cp.async, `depth` rows ahead, so no thread waits on
+// another for data and the loads in flight do not depend on registers or on the
+// reductions.  cp.async's byte count clips the row's end exactly (the rest of
+// the 16 bytes reads as zero).
+
+__device__ __forceinline__ void copy16_async(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+               :: "r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copy_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+// Wait until at most `n` of this thread's latest groups are in flight (n < 4).
+__device__ __forceinline__ void copy_wait(int n) {
+  if (n == 0) asm volatile("cp.async.wait_group 0;" ::: "memory");
+  else if (n == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
+  else if (n == 2) asm volatile("cp.async.wait_group 2;" ::: "memory");
+  else asm volatile("cp.async.wait_group 3;" ::: "memory");
+}
+
+// A thread's slots for one vector of each of its rows: 16-byte pieces of one
+// tensor lie blockDim.x pieces apart, so a warp's pieces are contiguous.
+template <int DT, int VPT>
+struct RowPipe {
+  static constexpr int kPieces = DT == DT_F32 ? 2 : 1;      // 16-byte pieces of a vector
+  static constexpr int kPer = VPT * kPieces;                // ... of a thread's row of one tensor
+  // Request this thread's part of a row into slot `s` (tensor slots).
+  __device__ static __forceinline__ void request(uint8_t* smem, int s, const uint8_t* row, int t,
+                                                 int T, int H) {
+    constexpr int es = elem_bytes(DT);
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+#pragma unroll
+      for (int k = 0; k < kPieces; ++k) {
+        const int c = (i * T + t) * kVec + k * (16 / es);
+        const int bytes = min(16, max(0, (H - c) * es));
+        const uint8_t* const src = bytes > 0 ? row + (size_t)c * es : row;
+        copy16_async(smem_u32(smem + ((size_t)(s * kPer + i * kPieces + k) * blockDim.x +
+                                      threadIdx.x) * 16),
+                     src, bytes);
+      }
+    }
+  }
+  __device__ static __forceinline__ void read(const uint8_t* smem, int s, int i, float (&v)[kVec]) {
+    RawVec<DT> raw;
+#pragma unroll
+    for (int k = 0; k < kPieces; ++k)
+      raw.q[k] = *reinterpret_cast<const uint4*>(
+          smem + ((size_t)(s * kPer + i * kPieces + k) * blockDim.x + threadIdx.x) * 16);
+    unpack<DT>(raw, v);
+  }
+};
 
 // dx of a row of any length: one block, two passes (mean of dy w n, outputs);
 // dx may be dh.
@@ -273,74 +329,63 @@ rmsnorm_bwd_any_kernel(const __grid_constant__ NormBwdParams p) {
   }
 }
 
-// Both gradients in one reading of dy, h and dh.  Blocks walk the rows
-// blockIdx.x, + gridDim.x, ...; each thread keeps the same VPT vectors of
-// columns throughout (a block's T threads span a row; with WARP a warp does and
-// the block's 8 warps take different rows), so the weight gradient of the rows
-// it has seen stays in its registers.  The next row's vectors are requested
-// before the current row's reduction.  At the end every block writes its H
-// sums to the workspace; sum_partials_kernel adds them in block order.
+// Both gradients in one reading of dy, h and dh, pipelined like the many-row
+// forward kernel.  Each thread keeps the same VPT vectors of columns throughout
+// (a block's threads span a row; with WARP a warp does and the block's 8 warps
+// take different rows), so the weight gradient of the rows it has seen stays in
+// its registers.  At the end every block writes its H sums to the workspace;
+// sum_partials_kernel adds them in block order.
 template <int DT, int VPT, bool WARP>
 __global__ void __launch_bounds__(WARP ? 256 : 512)
-rmsnorm_bwd_row_kernel(const __grid_constant__ NormBwdParams p) {
+rmsnorm_bwd_rows_kernel(const __grid_constant__ NormBwdParams p) {
   __shared__ float sums[2][32];
-  extern __shared__ float warp_dw[];     // WARP: 8 rows of H sums
+  extern __shared__ __align__(16) uint8_t slots[];     // afterwards, WARP: 8 rows of H sums
+  using Pipe = RowPipe<DT, VPT>;
   grid_launch_dependents();
-  grid_dependency_wait();
   const int t = WARP ? threadIdx.x & 31 : threadIdx.x;
   const int T = WARP ? 32 : blockDim.x;
   const int walkers = WARP ? gridDim.x * 8 : gridDim.x;
+  const int first = WARP ? (int)blockIdx.x * 8 + (threadIdx.x >> 5) : blockIdx.x;
   constexpr int es = elem_bytes(DT);
-  RawVec<DT> g_raw[VPT], h_raw[VPT], d_raw[VPT];
-  auto fetch = [&](long long row) {
-    const uint8_t* const dy = static_cast<const uint8_t*>(p.dy) + row * p.lddy * es;
-    const uint8_t* const h = static_cast<const uint8_t*>(p.h) + row * p.ldh * es;
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int c = (i * T + t) * kVec;
-      if (c >= p.H) continue;
-      g_raw[i] = load_raw<DT>(dy, c, p.H);
-      h_raw[i] = load_raw<DT>(h, c, p.H);
+  const int D = p.depth, tensors = p.dh ? 3 : 2;
+  grid_dependency_wait();
+  auto request = [&](long long row, int s) {
+    if (row < p.M) {
+      const int q = s * tensors;
+      Pipe::request(slots, q, static_cast<const uint8_t*>(p.dy) + row * p.lddy * es, t, T, p.H);
+      Pipe::request(slots, q + 1, static_cast<const uint8_t*>(p.h) + row * p.ldh * es, t, T, p.H);
       if (p.dh)
-        d_raw[i] = load_raw<DT>(static_cast<const uint8_t*>(p.dh) + row * p.lddh * es, c, p.H);
+        Pipe::request(slots, q + 2, static_cast<const uint8_t*>(p.dh) + row * p.lddh * es, t, T,
+                      p.H);
     }
+    copy_commit();
   };
-  float dw[VPT][kVec];
+  for (int s = 0; s < D; ++s) request(first + (long long)s * walkers, s);
+  float dw[VPT][kVec], w[VPT][kVec];
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
-    g_raw[i] = h_raw[i] = d_raw[i] = RawVec<DT>{};
+    const int c = (i * T + t) * kVec;
 #pragma unroll
-    for (int k = 0; k < kVec; ++k) dw[i][k] = 0.f;
+    for (int k = 0; k < kVec; ++k) dw[i][k] = w[i][k] = 0.f;
+    if (c < p.H) load_vec_dt(p.w, p.w_dt, c, p.H, w[i]);
   }
-  const int first = WARP ? (int)blockIdx.x * 8 + (threadIdx.x >> 5) : blockIdx.x;
-  if (first < p.M) fetch(first);
-  int buf = 0;
+  float next_rstd = first < p.M ? p.rstd[first] : 0.f;
+  int s = 0, buf = 0;
   for (long long row = first; row < p.M; row += walkers, buf ^= 1) {
-    float n[VPT][kVec], g[VPT][kVec], u[VPT][kVec];
-    const float rstd = p.rstd[row];
+    const float rstd = next_rstd;
+    if (row + walkers < p.M) next_rstd = p.rstd[row + walkers];
+    copy_wait(D - 1);
+    float n[VPT][kVec], g[VPT][kVec];
     float dot = 0.f;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      unpack<DT>(g_raw[i], g[i]);
-      unpack<DT>(h_raw[i], n[i]);
-      unpack<DT>(d_raw[i], u[i]);
-    }
-    if (row + walkers < p.M) fetch(row + walkers);
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int c = (i * T + t) * kVec;
-      float w[kVec];
-      if (c < p.H) {
-        load_vec_dt(p.w, p.w_dt, c, p.H, w);
-      } else {
-#pragma unroll
-        for (int k = 0; k < kVec; ++k) w[k] = 0.f;
-      }
+      Pipe::read(slots, s * tensors, i, g[i]);
+      Pipe::read(slots, s * tensors + 1, i, n[i]);
 #pragma unroll
       for (int k = 0; k < kVec; ++k) {
         n[i][k] *= rstd;
         dw[i][k] = fmaf(g[i][k], n[i][k], dw[i][k]);
-        g[i][k] *= w[k];
+        g[i][k] *= w[i][k];
         dot = fmaf(g[i][k], n[i][k], dot);
       }
     }
@@ -349,15 +394,20 @@ rmsnorm_bwd_row_kernel(const __grid_constant__ NormBwdParams p) {
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int c = (i * T + t) * kVec;
-      if (c >= p.H) continue;
 #pragma unroll
-      for (int k = 0; k < kVec; ++k) {
-        g[i][k] = rstd * (g[i][k] - n[i][k] * mean);
-        if (p.dh) g[i][k] += u[i][k];
+      for (int k = 0; k < kVec; ++k) g[i][k] = rstd * (g[i][k] - n[i][k] * mean);
+      if (p.dh) {
+        float u[kVec];
+        Pipe::read(slots, s * tensors + 2, i, u);
+#pragma unroll
+        for (int k = 0; k < kVec; ++k) g[i][k] += u[k];
       }
-      store_vec(dx, DT, c, p.H, g[i]);
+      if (c < p.H) store_vec(dx, DT, c, p.H, g[i]);
     }
+    request(row + (long long)D * walkers, s);
+    if (++s == D) s = 0;
   }
+  copy_wait(0);
   float* const out = p.partials + (long long)blockIdx.x * p.H;
   if constexpr (!WARP) {
 #pragma unroll
@@ -366,7 +416,9 @@ rmsnorm_bwd_row_kernel(const __grid_constant__ NormBwdParams p) {
       if (c < p.H) store_partial(out, c, p.H, dw[i]);
     }
   } else {
+    float* const warp_dw = reinterpret_cast<float*>(slots);
     float* const mine = warp_dw + (threadIdx.x >> 5) * p.H;
+    __syncthreads();                     // the slots are free
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int c = (i * T + t) * kVec;
@@ -395,7 +447,7 @@ sum_partials_kernel(const __grid_constant__ SumParams p) {
   const int c = blockIdx.x * 32 + lane;
   float s = 0.f;
   if (c < p.H) {
-#pragma unroll 4
+#pragma unroll 10
     for (int r = group; r < p.rows; r += 32) s += p.partials[(long long)r * p.H + c];
   }
   part[group][lane] = s;
@@ -456,48 +508,82 @@ int row_threads(int64_t H) {
   return (int)std::min<int64_t>(1024, cdiv(cdiv(H, gb300::kVec), 32) * 32);
 }
 
-// Rows up to kRowMax elements are held in registers: vectors per thread and
-// threads per row (a warp's 32 where warp).
+// Forward rows up to kRowMax elements are held in registers, a warp's up to
+// 1024 elements and a block's above: vectors per thread and threads.
 constexpr int kRowMax = 32768, kBwdRowMax = 16384;
 struct RowShape {
   int vpt, threads;
   bool warp;
 };
 
+// Four vectors a thread once there are rows enough to fill the GPU with such
+// blocks: fewer threads a row leave more rows in flight, and DRAM busier
+// (8192 x 8192 bf16 -> E4M3 with residual: 73.9 us at 4, 94.1 at 2, 118 at 1;
+// 32768 x 2048: 71.6, 77.1, 94.0; 608 x 8192: 9.0, 10.5, 11.7).  Below that the
+// row's own latency counts, which more threads shorten (304 x 4096: 3.9 us at 4, 3.3
+// at 1; 1 x 8192: 3.7 at 4, 3.1 at 2, 3.3 at 1).
 RowShape forward_shape(int64_t M, int64_t H) {
   const int vecs = (int)cdiv(H, gb300::kVec);
-  (void)M;
   RowShape s{};
-  if (vecs <= 128) {
-    s.warp = true;
+  s.warp = vecs <= 128;
+  if (s.warp) {
     s.vpt = vecs <= 32 ? 1 : vecs <= 64 ? 2 : 4;
     s.threads = 128;
     return s;
   }
-  s.vpt = vecs <= 256 ? 1 : vecs <= 2048 ? 2 : 4;
+  s.vpt = M >= 500 || vecs > 2048 ? 4 : vecs > 512 ? 2 : 1;
   s.threads = (int)cdiv(cdiv(vecs, s.vpt), 32) * 32;
   return s;
 }
 
-RowShape backward_shape(int64_t H) {
+// The backward row kernel: two vectors a thread and about 512 threads an SM
+// (their registers fill it), two rows ahead: 8192 x 8192 bf16 with dh 87.4 us
+// at 2 vectors x 512 threads x 2 rows against 105 with 4 x 256 x 1 and 122 with
+// 1 block of each; 32768 x 2048: 84.8 us with 4 blocks of 128 threads, 89.7 with
+// 8, 100.8 with 1 vector.  Longer rows (over 8192) take 4 vectors, one row ahead
+// (4096 x 16384: 112 us, 121 with two).
+struct BwdShape {
+  int vpt, threads, blocks_per_sm, depth;
+  bool warp;
+};
+
+BwdShape backward_shape(int64_t H) {
   const int vecs = (int)cdiv(H, gb300::kVec);
-  RowShape s{};
-  if (vecs <= 128) {
-    s.warp = true;
+  BwdShape s{};
+  s.warp = vecs <= 128;
+  if (s.warp) {
     s.vpt = vecs <= 32 ? 1 : vecs <= 64 ? 2 : 4;
     s.threads = 256;
-    return s;
+    s.blocks_per_sm = s.vpt == 4 ? 1 : 2;
+  } else {
+    s.vpt = vecs <= 1024 ? 2 : 4;
+    s.threads = (int)cdiv(cdiv(vecs, s.vpt), 32) * 32;
+    s.blocks_per_sm = std::max(1, 512 / s.threads);
   }
-  s.vpt = vecs <= 256 ? 1 : vecs <= 1024 ? 2 : 4;
-  s.threads = (int)cdiv(cdiv(vecs, s.vpt), 32) * 32;
+  // (4-byte rows of four vectors a thread: two do not fit in shared memory)
+  s.depth = s.vpt == 4 && !s.warp ? 1 : 2;
   return s;
 }
 
-// Blocks of the backward row kernel (one row of partial sums each).
-constexpr int kBwdBlocks = 304;
+// Most blocks the backward row kernel runs on (one row of partial sums each):
+// its blocks per SM on 152 SMs.
 int backward_blocks(int64_t M, int64_t H) {
-  const RowShape s = backward_shape(H);
-  return (int)std::min<int64_t>(s.warp ? cdiv(M, 8) : M, kBwdBlocks);
+  const BwdShape s = backward_shape(H);
+  return (int)std::min<int64_t>(s.warp ? cdiv(M, 8) : M, 152 * s.blocks_per_sm);
+}
+
+// Raises `kern`'s dynamic shared-memory limit, once per handle.
+gemm_status_t raise_smem(gemm_handle* h, const void* kern) {
+  std::lock_guard<std::mutex> g(h->mu);
+  for (int i = 0; i < h->raised_count; ++i)
+    if (h->raised[i] == kern) return GEMM_OK;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           h->smem_optin - 1024) != cudaSuccess) {
+    cudaGetLastError();
+    return GEMM_ERR_CUDA;
+  }
+  if (h->raised_count < gemm_handle::kMaxRaised) h->raised[h->raised_count++] = kern;
+  return GEMM_OK;
 }
 
 typedef void (*NormKern)(gb300::NormParams);
@@ -515,12 +601,12 @@ NormKern forward_kernel(const RowShape& s) {
 typedef void (*NormBwdKern)(gb300::NormBwdParams);
 template <int DT, bool WARP>
 NormBwdKern backward_kernel(int vpt) {
-  return vpt == 1   ? gb300::rmsnorm_bwd_row_kernel<DT, 1, WARP>
-         : vpt == 2 ? gb300::rmsnorm_bwd_row_kernel<DT, 2, WARP>
-                    : gb300::rmsnorm_bwd_row_kernel<DT, 4, WARP>;
+  return vpt == 1   ? gb300::rmsnorm_bwd_rows_kernel<DT, 1, WARP>
+         : vpt == 2 ? gb300::rmsnorm_bwd_rows_kernel<DT, 2, WARP>
+                    : gb300::rmsnorm_bwd_rows_kernel<DT, 4, WARP>;
 }
 template <int DT>
-NormBwdKern backward_kernel(const RowShape& s) {
+NormBwdKern backward_kernel(const BwdShape& s) {
   return s.warp ? backward_kernel<DT, true>(s.vpt) : backward_kernel<DT, false>(s.vpt);
 }
 
@@ -643,13 +729,19 @@ GEMM_API gemm_status_t gemm_rmsnorm_bwd(gemm_handle_t h, const gemm_rmsnorm_bwd_
   k.M = (int)p.M; k.H = (int)p.H;
   k.inv_h = (float)(1.0 / (double)p.H);
   if (need > 0) {
-    const RowShape s = backward_shape(p.H);
-    const int blocks = backward_blocks(p.M, p.H);
+    const BwdShape s = backward_shape(p.H);
+    const int blocks = (int)std::min<int64_t>(backward_blocks(p.M, p.H),
+                                              (int64_t)h->sm_count * s.blocks_per_sm);
     k.partials = static_cast<float*>(workspace);
-    GB300_CHECK(launch(p.type == GEMM_F32   ? backward_kernel<gb300::DT_F32>(s)
+    k.depth = s.depth;
+    NormBwdKern kern = p.type == GEMM_F32   ? backward_kernel<gb300::DT_F32>(s)
                        : p.type == GEMM_F16 ? backward_kernel<gb300::DT_F16>(s)
-                                            : backward_kernel<gb300::DT_BF16>(s),
-                       k, blocks, s.threads, s.warp ? 8 * (size_t)p.H * sizeof(float) : 0, stream));
+                                            : backward_kernel<gb300::DT_BF16>(s);
+    GB300_CHECK(raise_smem(h, reinterpret_cast<const void*>(kern)));
+    const size_t slots = (size_t)s.depth * (p.dh ? 3 : 2) * s.threads * s.vpt * gb300::kVec *
+                         dtype_bytes(p.type);
+    const size_t sums = s.warp ? 8 * (size_t)p.H * sizeof(float) : 0;
+    GB300_CHECK(launch(kern, k, blocks, s.threads, std::max(slots, sums), stream));
     gb300::SumParams q{k.partials, p.dweight, blocks, (int)p.H, k.dw_dt};
     return launch(gb300::sum_partials_kernel, q, cdiv(p.H, 32), 1024, 0, stream);
   }
