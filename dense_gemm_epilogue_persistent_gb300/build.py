@@ -64,14 +64,15 @@ SHARED_UNITS = [(f"kern_shared_ab{ab}_m{mc}_n{nc}", "kern_shared.cu",
                  [f"-DGB300_AB={ab}", f"-DGB300_MC={mc}", f"-DGB300_NC={nc}"])
                 for ab in (2, 1, 4) for mc, nc in ((2, 1), (1, 2), (2, 2))]
 # The operators around the product: normalisation, the linear layer and its kernels.
-ROW_UNITS = [("norm", "norm.cu", []), ("linear", "linear.cu", [])]
+ROW_UNITS = [("norm", "norm.cu", []), ("linear", "linear.cu", []),
+             ("kern_split", "kern_split.cu", [])]
 LINEAR_UNITS = [(f"kern_linear_ab{ab}_e{epw}", "kern_linear.cu",
                  [f"-DGB300_AB={ab}", f"-DGB300_EPW={epw}"]) for ab in (2, 1, 4) for epw in (1, 2)]
 # Files the multi-GPU library is built from (its translation units and every
 # header they include): none of them names a multicast TMA load.
 NOMC_FILES = ["gemm_api.cu", "norm.cu", "linear.cu", "kern_plain.cu", "kern_linear.cu",
-              "gemm_kernel.cuh", "activations.cuh", "rows.cuh", "ptx.cuh", "kernels.h", "handle.h",
-              "rows_host.h"]
+              "kern_split.cu", "gemm_kernel.cuh", "split_kernel.cuh", "activations.cuh", "rows.cuh",
+              "ptx.cuh", "kernels.h", "handle.h", "rows_host.h"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler",

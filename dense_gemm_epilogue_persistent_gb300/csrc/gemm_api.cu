@@ -875,7 +875,9 @@ GEMM_API gemm_status_t gemm_set_config(gemm_handle_t h, const gemm_config_t* cfg
     return GEMM_OK;
   }
   if ((cfg->cta_group && cfg->cta_group != 1 && cfg->cta_group != 2) ||
-      (cfg->tile_n && !valid_tile_n(cfg->tile_n)) || cfg->stages < 0 ||
+      (cfg->split_k > 0 ? cfg->tile_n < 0 || cfg->tile_n > 128 || cfg->tile_n % 16 != 0
+                        : cfg->tile_n && !valid_tile_n(cfg->tile_n)) ||
+      cfg->split_k > 8 || cfg->stages < 0 ||
       (cfg->cluster_m && cfg->cluster_m != 1 && cfg->cluster_m != 2) ||
       (cfg->cluster_n && cfg->cluster_n != 1 && cfg->cluster_n != 2) ||
       cfg->epi_slots < 0 || cfg->epi_slots > kMaxEpiSlots || cfg->epi_wait_ns < 0 ||

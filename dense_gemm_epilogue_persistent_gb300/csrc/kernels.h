@@ -87,4 +87,7 @@ inline const void* linear_kernel_for(int ab_bytes, int cta_group, int ka, int ep
   return nullptr;
 }
 
+// kern_split.cu: the linear layer's split-K kernel, by input width.
+const void* split_kernel_for(int ab_bytes);
+
 }  // namespace gb300

@@ -12,6 +12,7 @@
 #include "kernels.h"
 #include "rows.cuh"
 #include "rows_host.h"
+#include "split_kernel.cuh"
 
 namespace gb300 {
 
@@ -23,51 +24,86 @@ struct ActGradParams {
   void* dbias;                      // or null
   int M, N;
   int act, dbias_dt;
+  int row_split;                    // blocks of a cluster, sharing the rows
 };
 
 // dz = dd act'(z) and dbias = its column sums (of the values before dz is
-// rounded).  A block owns 64 columns (8 lanes of one vector each) and walks all
-// rows, 32 at a time; the 32 row groups' sums are added in order through shared
-// memory.
+// rounded), DRAM-bound at 6 bytes an element.  A block owns 64 columns (8 lanes of one
+// vector each) and 1/R of the rows, R the cluster size: thread group g of 32
+// walks rows first + g, + 32, ..., four at a time so that their loads are in
+// flight together.  A column's sum is added in a fixed order: a thread's rows,
+// the 32 groups through shared memory, the cluster's blocks by its first one.
 template <int DT>
 __global__ void __launch_bounds__(256)
 act_grad_kernel(const __grid_constant__ ActGradParams p) {
   __shared__ float part[32][64];
-  grid_dependency_wait();
-  grid_launch_dependents();
+  __shared__ float block_part[64];
+  constexpr int kUnroll = 4;
   constexpr int es = elem_bytes(DT);
+  grid_launch_dependents();
   const int lane = threadIdx.x & 7, group = threadIdx.x >> 3;
-  const int c = blockIdx.x * 64 + lane * kVec;
+  const int R = p.row_split, rank = blockIdx.x % R, strip = blockIdx.x / R;
+  const int c = strip * 64 + lane * kVec;
+  const int share = (p.M + R - 1) / R;
+  const long long first = (long long)rank * share;
+  const long long last = min((long long)p.M, first + share);
   float acc[kVec];
 #pragma unroll
   for (int i = 0; i < kVec; ++i) acc[i] = 0.f;
+  grid_dependency_wait();
   if (c < p.N) {
+    const uint8_t* const dd = static_cast<const uint8_t*>(p.dd);
+    const uint8_t* const zz = static_cast<const uint8_t*>(p.z);
     with_activation(p.act, [&](auto a) {
-      for (long long row = group; row < p.M; row += 32) {
-        float g[kVec];
-        load_vec<DT>(static_cast<const uint8_t*>(p.dd) + row * p.lddd * es, c, p.N, g);
-        if constexpr (decltype(a)::value != ACT_NONE) {
-          float z[kVec];
-          load_vec<DT>(static_cast<const uint8_t*>(p.z) + row * p.ldz * es, c, p.N, z);
+      constexpr int ACT = decltype(a)::value;
+      for (long long row0 = first + group; row0 < last; row0 += 32 * kUnroll) {
+        RawVec<DT> g_raw[kUnroll], z_raw[kUnroll];
 #pragma unroll
-          for (int i = 0; i < kVec; ++i) g[i] *= activate_grad<decltype(a)::value>(z[i]);
+        for (int u = 0; u < kUnroll; ++u) {
+          const long long row = row0 + 32 * u;
+          g_raw[u] = z_raw[u] = RawVec<DT>{};
+          if (row < last) {
+            g_raw[u] = load_raw<DT>(dd + row * p.lddd * es, c, p.N);
+            if constexpr (ACT != ACT_NONE) z_raw[u] = load_raw<DT>(zz + row * p.ldz * es, c, p.N);
+          }
         }
-        if (p.dz) store_vec(static_cast<uint8_t*>(p.dz) + row * p.lddz * es, DT, c, p.N, g);
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) acc[i] += g[i];
+        for (int u = 0; u < kUnroll; ++u) {
+          const long long row = row0 + 32 * u;
+          if (row >= last) break;
+          float g[kVec];
+          unpack<DT>(g_raw[u], g);
+          if constexpr (ACT != ACT_NONE) {
+            float z[kVec];
+            unpack<DT>(z_raw[u], z);
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) g[i] *= activate_grad<ACT>(z[i]);
+          }
+          if (p.dz) store_vec(static_cast<uint8_t*>(p.dz) + row * p.lddz * es, DT, c, p.N, g);
+#pragma unroll
+          for (int i = 0; i < kVec; ++i) acc[i] += g[i];
+        }
       }
     });
   }
-  if (!p.dbias) return;
+  if (!p.dbias) return;                  // (the whole grid)
 #pragma unroll
   for (int i = 0; i < kVec; ++i) part[group][lane * kVec + i] = acc[i];
   __syncthreads();
-  const int col = blockIdx.x * 64 + (int)threadIdx.x;
-  if (threadIdx.x < 64 && col < p.N) {
+  if (threadIdx.x < 64) {
     float s = 0.f;
     for (int i = 0; i < 32; ++i) s += part[i][threadIdx.x];
+    block_part[threadIdx.x] = s;
+  }
+  if (R > 1) cluster_sync_all(); else __syncthreads();
+  const int col = strip * 64 + (int)threadIdx.x;
+  if (rank == 0 && threadIdx.x < 64 && col < p.N) {
+    float s = block_part[threadIdx.x];
+    for (int r = 1; r < R; ++r)
+      s += load_cluster_f32(map_to_rank(smem_u32(&block_part[threadIdx.x]), (uint32_t)r));
     store_elem(p.dbias, col, p.dbias_dt, s);
   }
+  if (R > 1) cluster_sync_all();         // the first block has read the others' sums
 }
 
 }  // namespace gb300
@@ -259,9 +295,157 @@ gemm_status_t run_persistent(gemm_handle* h, const gemm_linear_t& p, struct CUst
   return GEMM_OK;
 }
 
+// The split-K kernel's plan: tokens per tile, CTAs per cluster, ring depth.
+struct SplitPlan {
+  int bn, feats, split, ka, stages, smem;
+  int64_t tiles_m, tiles_n;
+};
+
+// The ring, its barriers and the alignment; the last stage's matrix operand,
+// 128 rows whatever `feats`, has to lie inside.
+int split_smem(int bn, int feats, int ka, int stages) {
+  const int tail = std::max(0, (128 - feats) * 128 - stages * ka * bn * 128);
+  return stages * ka * (feats + bn) * 128 + tail + (int)gb300::kSplitBarBytes + 1024;
+}
+
+// Dynamic shared memory of its CTAs: 113 KB, half of an SM's 228 KB less the
+// 1 KB the system takes for each.
+constexpr int kSplitSmem = 113 * 1024;
+
+// Whether the kernel can run `p` with such tiles, and the plan.  K is split
+// into at most one k-block per CTA; MN-major tokens are staged in whole atoms.
+bool plan_split(const gemm_linear_t& p, int bn, int feats, int split, SplitPlan* out) {
+  const int es = dtype_bytes(p.a_type);
+  const int64_t k_blocks = cdiv(p.K, 128 / es);
+  if (p.K == 0 || bn < 16 || bn > 128 || bn % 16 != 0 || split < 1 || split > 8 ||
+      feats < 8 || feats > 128 || feats % 8 != 0 || split > k_blocks)
+    return false;
+  if (p.layoutB == GEMM_MN_MAJOR && feats != 128) return false;
+  if (p.layoutA == GEMM_MN_MAJOR && bn % (128 / es) != 0) return false;
+  out->bn = bn;
+  out->feats = feats;
+  out->split = split;
+  out->tiles_m = cdiv(p.M, bn);
+  out->tiles_n = cdiv(p.N, feats);
+  // Two CTAs fit an SM, so that the next launch's set-up overlaps the end of
+  // this one; three do not, and neither does one beside a CTA of the
+  // persistent kernel (half an SM's shared memory and 1 KB at least): whatever
+  // shares an SM then has its tensor memory (128 columns at most each) at once,
+  // and no cluster waits for one that waits for it.
+  out->smem = kSplitSmem;
+  out->ka = split_smem(bn, feats, 2, 3) <= out->smem ? 2 : 1;
+  out->stages = 0;
+  while (out->stages < gb300::kSplitMaxStages &&
+         split_smem(bn, feats, out->ka, out->stages + 1) <= out->smem)
+    ++out->stages;
+  // The exchange takes place in the ring.
+  const int own = (int)cdiv(cdiv(bn, split), 4) * 4;
+  if (out->stages < 2 || (split > 1 && split * own * 512 > out->stages * out->ka * (feats + bn) * 128))
+    return false;
+  return out->tiles_m * out->tiles_n * split <= INT32_MAX;
+}
+
+gemm_status_t run_split(gemm_handle* h, const gemm_linear_t& p, const SplitPlan& s,
+                        struct CUstream_st* stream) {
+  const int es = dtype_bytes(p.a_type);
+  const void* kern = gb300::split_kernel_for(es);
+  GB300_CHECK(raise_smem(h, kern));
+  const bool a_mn = p.layoutA == GEMM_MN_MAJOR, b_mn = p.layoutB == GEMM_MN_MAJOR;
+  CUtensorMap feat, tok;
+  if (!encode_operand(h->encode, &feat, p.B, p.b_type, p.N, p.K, 1, p.ldb, b_mn, s.feats,
+                      128 / es) ||
+      !encode_operand(h->encode, &tok, p.A, p.a_type, p.M, p.K, 1, p.lda, a_mn, s.bn, 128 / es))
+    return GEMM_ERR_CUDA;
+  gb300::SplitParams k{};
+  k.M = (int)p.M; k.N = (int)p.N;
+  k.bn = s.bn;
+  k.feats = s.feats;
+  k.ka = s.ka;
+  k.tiles_m = (int)s.tiles_m;
+  k.split = s.split;
+  k.own = (int)cdiv(cdiv(s.bn, s.split), 4) * 4;
+  k.k_blocks = (int)cdiv(p.K, 128 / es);
+  k.stages = s.stages;
+  k.feat_mn = b_mn;
+  k.tok_mn = a_mn;
+  k.idesc = make_idesc(p.b_type, p.a_type, false, 1, s.bn, b_mn, a_mn);
+  k.tmem_cols = 32;
+  while ((int)k.tmem_cols < s.bn) k.tmem_cols *= 2;
+  k.status = h->d_status;
+  k.timeout_ns = h->timeout_ns;
+  k.alpha = p.alpha;
+  k.row_scale = p.row_scale;
+  k.col_scale = p.col_scale;
+  k.bias = p.bias; k.bias_dt = p.bias_type;
+  k.r = p.R; k.ldr = p.ldr; k.r_dt = p.r_type;
+  k.z = p.Z; k.ldz = p.ldz; k.z_dt = p.z_type;
+  k.d = p.D; k.ldd = p.ldd; k.d_dt = p.d_type;
+  k.act = p.activation;
+  {
+    std::lock_guard<std::mutex> guard(h->mu);
+    k.inject_stall = h->forced && h->forced_cfg.inject_stall;
+    gemm_config_t c{};
+    c.cta_group = 1;
+    c.tile_m = s.feats;
+    c.tile_n = s.bn;
+    c.tile_k = 128 / es * s.ka;
+    c.stages = s.stages;
+    c.acc_stages = 1;
+    c.ring_bytes = s.stages * s.ka * (s.feats + s.bn) * 128;
+    c.smem_bytes = s.smem;
+    c.tiles = s.tiles_m * s.tiles_n;
+    c.grid_ctas = (int)(c.tiles * s.split);
+    c.epi_warps = 1;
+    c.split_k = s.split;
+    h->last = c;
+  }
+  cudaLaunchConfig_t lc{};
+  cudaLaunchAttribute attr[2];
+  lc.gridDim = dim3((unsigned)(s.tiles_m * s.tiles_n * s.split));
+  lc.blockDim = dim3((unsigned)gb300::kSplitThreads);
+  lc.dynamicSmemBytes = (size_t)s.smem;
+  lc.stream = reinterpret_cast<cudaStream_t>(stream);
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)s.split;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  lc.attrs = attr;
+  lc.numAttrs = s.split > 1 ? 2 : 1;
+  void* args[3] = {&feat, &tok, &k};
+  if (cudaLaunchKernelExC(&lc, kern, args) != cudaSuccess) {
+    cudaGetLastError();
+    return GEMM_ERR_CUDA;
+  }
+  return GEMM_OK;
+}
+
+// The kernel for a call: forced, or by the number of tokens.
 gemm_status_t run_linear(gemm_handle* h, const gemm_linear_t& p, struct CUstream_st* stream) {
   if (p.M == 0 || p.N == 0) return GEMM_OK;
+  gemm_config_t forced{};
+  {
+    std::lock_guard<std::mutex> guard(h->mu);
+    if (h->forced) forced = h->forced_cfg;
+    else forced.split_k = -2;            // none
+  }
+  SplitPlan s{};
+  if (forced.split_k > 0) {
+    if (!plan_split(p, forced.tile_n ? forced.tile_n : 64,
+                    forced.tile_m ? forced.tile_m : 128, forced.split_k, &s))
+      return GEMM_ERR_UNSUPPORTED_CONFIG;
+    return run_split(h, p, s, stream);
+  }
   return run_persistent(h, p, stream);
+}
+
+// Blocks per cluster of the activation gradient: enough for eight blocks an SM
+// (all that its registers hold), at least 128 rows a block.
+int act_grad_split(int64_t M, int64_t N, int sm_count) {
+  int r = 1;
+  while (r < 8 && cdiv(N, 64) * r < 8 * (int64_t)sm_count && M >= 256 * r) r *= 2;
+  return r;
 }
 
 // The backward pass's two products as linear calls.  da[M,K] = alpha dz[M,N] b[N,K]
@@ -367,9 +551,10 @@ GEMM_API gemm_status_t gemm_linear_bwd(gemm_handle_t h, const gemm_linear_bwd_t*
     k.dbias = p.dbias; k.dbias_dt = device_dt(p.dbias_type);
     k.M = (int)p.M; k.N = (int)p.N;
     k.act = p.activation;
+    k.row_split = act_grad_split(p.M, p.N, h->sm_count);
     GB300_CHECK(launch(p.type == GEMM_F16 ? gb300::act_grad_kernel<gb300::DT_F16>
                                           : gb300::act_grad_kernel<gb300::DT_BF16>,
-                       k, cdiv(p.N, 64), 256, 0, stream));
+                       k, cdiv(p.N, 64) * k.row_split, 256, 0, stream, k.row_split));
   }
   int64_t lddz = 0;
   const void* dz = dz_of(p, lddz);

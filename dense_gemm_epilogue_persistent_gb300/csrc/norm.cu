@@ -572,20 +572,6 @@ int backward_blocks(int64_t M, int64_t H) {
   return (int)std::min<int64_t>(s.warp ? cdiv(M, 8) : M, 152 * s.blocks_per_sm);
 }
 
-// Raises `kern`'s dynamic shared-memory limit, once per handle.
-gemm_status_t raise_smem(gemm_handle* h, const void* kern) {
-  std::lock_guard<std::mutex> g(h->mu);
-  for (int i = 0; i < h->raised_count; ++i)
-    if (h->raised[i] == kern) return GEMM_OK;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           h->smem_optin - 1024) != cudaSuccess) {
-    cudaGetLastError();
-    return GEMM_ERR_CUDA;
-  }
-  if (h->raised_count < gemm_handle::kMaxRaised) h->raised[h->raised_count++] = kern;
-  return GEMM_OK;
-}
-
 typedef void (*NormKern)(gb300::NormParams);
 template <int DT, bool WARP>
 NormKern forward_kernel(int vpt) {

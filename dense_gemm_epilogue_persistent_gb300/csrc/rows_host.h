@@ -32,21 +32,40 @@ inline gemm_status_t check_matrix(const void* p, int64_t ld, int64_t cols, int d
     if (check_status != GEMM_OK) return check_status;         \
   } while (0)
 
+// Raises `kern`'s dynamic shared-memory limit, once per handle.
+inline gemm_status_t raise_smem(gemm_handle* h, const void* kern) {
+  std::lock_guard<std::mutex> g(h->mu);
+  for (int i = 0; i < h->raised_count; ++i)
+    if (h->raised[i] == kern) return GEMM_OK;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           h->smem_optin - 1024) != cudaSuccess) {
+    cudaGetLastError();
+    return GEMM_ERR_CUDA;
+  }
+  if (h->raised_count < gemm_handle::kMaxRaised) h->raised[h->raised_count++] = kern;
+  return GEMM_OK;
+}
+
 // Launch on `stream`, allowed to be scheduled while the stream's previous
-// kernel finishes (every kernel here waits for it before touching memory).
+// kernel finishes (every kernel here waits for it before touching memory), in
+// clusters of `cluster` blocks.
 template <typename P>
 gemm_status_t launch(void (*kern)(P), const P& params, int64_t grid, int threads, size_t smem,
-                     struct CUstream_st* stream) {
+                     struct CUstream_st* stream, int cluster = 1) {
   cudaLaunchConfig_t lc{};
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   lc.gridDim = dim3((unsigned)grid);
   lc.blockDim = dim3((unsigned)threads);
   lc.dynamicSmemBytes = smem;
   lc.stream = reinterpret_cast<cudaStream_t>(stream);
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   lc.attrs = attr;
-  lc.numAttrs = 1;
+  lc.numAttrs = cluster > 1 ? 2 : 1;
   void* args[1] = {const_cast<P*>(&params)};
   if (cudaLaunchKernelExC(&lc, reinterpret_cast<const void*>(kern), args) != cudaSuccess) {
     cudaGetLastError();

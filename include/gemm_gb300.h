@@ -143,6 +143,14 @@ typedef struct {
  *               creation (gemm_run_noalloc never uses it).  As an input:
  *               0 = automatic, 1 = never, 2 = wherever allowed.  As an output:
  *               the number of clusters sharing the k-blocks (0 = off).
+ *   split_k     (last field; gemm_linear and gemm_linear_bwd only, gemm_run
+ *               ignores it) CTAs of a cluster that share a tile's K in the
+ *               split-K kernel, whose tiles are tile_m features (a multiple of
+ *               8 up to 128; 128 where B is MN-major) x tile_n tokens (a multiple
+ *               of 16 up to 128).  As an input, with a configuration forced: 0
+ *               or less = the persistent kernel, 1..8 = the split-K kernel
+ *               (tile_m 0 = 128, tile_n 0 = 64; of the other fields only
+ *               inject_stall applies).  Without one the call chooses.
  *   Fields marked "diagnostic" are for tuning and testing the kernel, not
  *   part of the GEMM contract; leave them 0.
  *   l2_hints    (diagnostic; also an input) L2 eviction priority of the TMA
@@ -194,6 +202,7 @@ typedef struct {
   int cluster_n;
   int epi_warps;
   int stream_k;
+  int split_k;
 } gemm_config_t;
 
 /* Every argument of one gemm_run call, for the host-only planning calls. */

@@ -316,6 +316,84 @@ def test_forward_forced_configurations(gemm, cfg, ab):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("bn,split", [(16, 1), (16, 2), (16, 8), (32, 3), (48, 5), (64, 4), (64, 7),
+                                      (80, 2), (96, 8), (112, 3), (128, 1), (128, 6), (128, 8)])
+@pytest.mark.parametrize("ab", ["bf16", "e4m3", "tf32"])
+def test_forward_split_over_a_cluster(gemm, bn, split, ab):
+    """The split-K kernel at every tile width class and cluster size, ragged, one tile and
+    several, K from one k-block per CTA up."""
+    gemm.set_config(split_k=split, tile_n=bn)
+    try:
+        for M, N, K in ((1, 1, 1030), (37, 203, 1033), (bn + 3, 264, 1500)):
+            _check_forward(gemm, M, N, K, ab, d_t="f16", act="gelu", r_t="bf16", z_t="f32",
+                           scales=True)
+            c = gemm.last_config()
+            assert (c.split_k, c.tile_n) == (split, bn)
+        if split > 1:                            # more CTAs than k-blocks
+            with pytest.raises(G.GemmError) as e:
+                _check_forward(gemm, 4, 8, 16 if ab == "tf32" else 32, ab)
+            assert e.value.status == G.GEMM_ERR_UNSUPPORTED_CONFIG
+    finally:
+        gemm.set_config(None)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("feats", [8, 24, 56, 96, 120])
+@pytest.mark.parametrize("bn,split", [(16, 1), (16, 3), (64, 4), (96, 2), (128, 1)])
+def test_forward_split_narrow_feature_tiles(gemm, feats, bn, split):
+    gemm.set_config(split_k=split, tile_n=bn, tile_m=feats)
+    try:
+        for ab, N in (("f16", 203), ("e4m3", 88)):
+            _check_forward(gemm, bn - 3, N, 1100, ab, act="silu", r_t="f32", z_t="bf16",
+                           scales=ab == "e4m3")
+            assert gemm.last_config().tile_m == feats
+    finally:
+        gemm.set_config(None)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("a_mn,b_mn", [(True, False), (False, True), (True, True)])
+@pytest.mark.parametrize("bn,split", [(64, 2), (128, 3), (128, 8), (128, 1)])
+def test_forward_split_layouts(gemm, bn, split, a_mn, b_mn):
+    gemm.set_config(split_k=split, tile_n=bn)
+    try:
+        for ab in ("f16", "e5m2"):
+            if ab == "e5m2" and a_mn and bn % 128:
+                continue
+            _check_forward(gemm, 150, 203, 1100, ab, a_mn=a_mn, b_mn=b_mn, scales=ab == "e5m2",
+                           act="silu", r_t="f32", bias_t="bf16")
+        if a_mn:
+            gemm.set_config(split_k=split, tile_n=48)
+            with pytest.raises(G.GemmError):
+                _check_forward(gemm, 150, 203, 1100, "f16", a_mn=True)
+    finally:
+        gemm.set_config(None)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("split", [0, 1, 4])
+def test_watchdog_ends_a_stalled_layer(gemm, split):
+    """The matrix-unit warp waits on a barrier nothing arrives at (an injected stall with a
+    100 ms limit): the launch ends by itself, the status names the wait, and the next call
+    computes."""
+    g = G.Gemm(0)
+    try:
+        G.gemm_set_timeout_ns(g.handle, 100_000_000)
+        g.set_config(inject_stall=1, split_k=split)
+        e = lambda *s: torch.ones(*s, dtype=torch.float16, device="cuda")
+        d = e(40, 264)
+        g.linear(e(40, 512), e(264, 512), d)
+        st, detail = g.sync_status()
+        assert st == G.GEMM_ERR_DEVICE_TIMEOUT and (detail >> 24) == 0xE0, hex(detail)
+        G.gemm_set_timeout_ns(g.handle, 0)
+        g.set_config(None)
+        g.linear(e(40, 512), e(264, 512), d)
+        assert g.sync_status()[0] == G.GEMM_OK and (d == 512).all()
+    finally:
+        g.close()
+
+
+@pytest.mark.gpu
 def test_forward_refuses_multicast_clusters(gemm):
     gemm.set_config(cluster_m=2)
     try:
