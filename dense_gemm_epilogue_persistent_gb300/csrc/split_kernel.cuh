@@ -63,16 +63,39 @@ constexpr int kSplitMaxStages = 12;
 // the watchdog test's, tensor-memory address and abort flag.
 constexpr uint32_t kSplitBarBytes = 8 * (2 * kSplitMaxStages + 2) + 8;
 
-__device__ __forceinline__ float epi_load(const void* p, long long i, int dt) {
-  if (dt == DT_F32) return static_cast<const float*>(p)[i];
-  const uint16_t b = static_cast<const uint16_t*>(p)[i];
+__device__ __forceinline__ int epi_bytes(int dt) { return dt == DT_F32 ? 4 : 2; }
+
+__device__ __forceinline__ float epi_load(const void* p, int dt) {
+  if (dt == DT_F32) return *static_cast<const float*>(p);
+  const uint16_t b = *static_cast<const uint16_t*>(p);
   return dt == DT_F16 ? __half2float(__ushort_as_half(b)) : __uint_as_float((uint32_t)b << 16);
 }
 
-__device__ __forceinline__ void epi_store(void* p, long long i, int dt, float v) {
-  if (dt == DT_F32) static_cast<float*>(p)[i] = v;
-  else if (dt == DT_F16) static_cast<uint16_t*>(p)[i] = __half_as_ushort(__float2half_rn(v));
-  else static_cast<uint16_t*>(p)[i] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+// Elements of `count` (up to 4) rows `step` bytes apart.
+__device__ __forceinline__ void epi_store4(uint8_t* p, long long step, int dt, int count,
+                                           const float4& v) {
+  const float e[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (i >= count) break;
+    uint8_t* const at = p + i * step;
+    if (dt == DT_F32) *reinterpret_cast<float*>(at) = e[i];
+    else
+      *reinterpret_cast<uint16_t*>(at) = dt == DT_F16
+                                             ? __half_as_ushort(__float2half_rn(e[i]))
+                                             : __bfloat16_as_ushort(__float2bfloat16_rn(e[i]));
+  }
+}
+
+// One copy of the activations' code, called: the epilogue runs each line of
+// its own code once or a few times, so that fetching it costs more than a call.
+template <int AB_BYTES>
+__device__ __noinline__ float4 activate4(float4 v, int act) {
+  with_activation(act, [&](auto a) {
+    constexpr int ACT = decltype(a)::value;
+    v = make_float4(activate<ACT>(v.x), activate<ACT>(v.y), activate<ACT>(v.z), activate<ACT>(v.w));
+  });
+  return v;
 }
 
 template <int AB_BYTES>
@@ -144,6 +167,31 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tmF, const __grid_consta
   const bool mine = n < p.N && q * 32 + lane < p.feats;
   float scale = p.alpha, bias = 0.f;
   bool ready = true;
+  // The columns this CTA finishes: [c_lo, c_lo + n_cols) of the tile, those of
+  // its share that hold tokens, four at a time.  Residuals are fetched 16
+  // columns ahead (the first ones while the main loop runs); a lane holds one
+  // column's row factor of 32.
+  const int with_tokens = min(p.bn, p.M - m0);
+  const int c_lo = S > 1 ? (int)rank * p.own : 0;
+  const int n_cols = max(0, min(S > 1 ? p.own : p.bn, with_tokens - c_lo));
+  const long long m_lo = m0 + c_lo;
+  const long long d_step = p.ldd * epi_bytes(p.d_dt), r_step = p.ldr * epi_bytes(p.r_dt);
+  const long long z_step = p.ldz * epi_bytes(p.z_dt);
+  uint8_t* d_at = static_cast<uint8_t*>(p.d) + m_lo * d_step + (long long)n * epi_bytes(p.d_dt);
+  uint8_t* z_at = static_cast<uint8_t*>(p.z) + m_lo * z_step + (long long)n * epi_bytes(p.z_dt);
+  const uint8_t* r_at =
+      static_cast<const uint8_t*>(p.r) + m_lo * r_step + (long long)n * epi_bytes(p.r_dt);
+  float r[16];
+  auto fetch = [&](int g, int c) {               // r[4 g ..] for columns c ..
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      r[4 * g + i] =
+          p.r && mine && c + i < n_cols ? epi_load(r_at + (c + i) * r_step, p.r_dt) : 0.f;
+  };
+  auto row_factor = [&](int c) {                 // this lane's of columns c .. c + 31
+    return p.row_scale && c + lane < n_cols ? __ldg(p.row_scale + m_lo + c + lane) : 1.f;
+  };
+  float factor = 1.f, next_factor = 1.f;
 
   // The producer and the MMA warp run their loops whole, with only the
   // asynchronous instructions under the elected lane: addresses, coordinates and
@@ -228,113 +276,82 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tmF, const __grid_consta
       if (p.col_scale) scale *= __ldg(p.col_scale + n);
       if (p.bias) bias = vector_elem(p.bias, n, p.bias_dt);
     }
+#pragma unroll
+    for (int g = 0; g < 4; ++g)
+      if (4 * g < n_cols) fetch(g, 4 * g);
+    next_factor = row_factor(0);
     ready = __all_sync(0xFFFFFFFFu, wait_phase<true>(done, 0u, w, kWaitEpilogue));
     tc_fence_after_sync();
   }
 
-  // `cols` (up to W, the length of v) columns of the tile: tokens m0 + col .., this thread's feature.  Loads
-  // are issued for all of them before the first is used.
-  auto finish = [&](int col, auto& v, int cols) {
-    constexpr int W = sizeof(v) / sizeof(v[0]);
-    const int m = m0 + col, count = mine ? min(cols, p.M - m) : 0;
-    if (p.row_scale) {
-      float f[W];
-#pragma unroll
-      for (int i = 0; i < W; ++i) f[i] = i < count ? __ldg(p.row_scale + m + i) : 0.f;
-#pragma unroll
-      for (int i = 0; i < W; ++i) v[i] = fmaf(v[i], scale * f[i], bias);
-    } else {
-#pragma unroll
-      for (int i = 0; i < W; ++i) v[i] = fmaf(v[i], scale, bias);
-    }
-    float r[W];
-#pragma unroll
-    for (int i = 0; i < W; ++i)
-      r[i] = p.r && i < count ? epi_load(p.r, (m + i) * p.ldr + n, p.r_dt) : 0.f;
-    if (p.z) {
-#pragma unroll
-      for (int i = 0; i < W; ++i)
-        if (i < count) epi_store(p.z, (m + i) * p.ldz + n, p.z_dt, v[i]);
-    }
-    with_activation(p.act, [&](auto a) {
-#pragma unroll
-      for (int i = 0; i < W; ++i) v[i] = activate<decltype(a)::value>(v[i]);
-    });
-#pragma unroll
-    for (int i = 0; i < W; ++i)
-      if (i < count) epi_store(p.d, (m + i) * p.ldd + n, p.d_dt, p.r ? v[i] + r[i] : v[i]);
-  };
-  // Columns c .. c + 15 of this warp's lanes.
-  const uint32_t tbase = tmem + ((uint32_t)(q * 32) << 16);
-  auto read_acc = [&](int c, float (&v)[16]) {
-    uint32_t acc[16];
-    __syncwarp();                                // (.aligned, after per-lane work)
-    tmem_load_16cols(tbase + c, acc);
-    tmem_wait_ld16(acc);
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(acc[i]);
-  };
   const bool active = warp >= 2 && ready && q * 32 < p.feats;
-  if (S == 1) {
-    if (active) {
-      for (int c = 0; c < p.bn && m0 + c < p.M; c += 16) {
-        float v[16];
-        read_acc(c, v);
-        if (p.M - m0 - c > 4) {
-          finish(c, v, 16);
-        } else {
-          float u[4] = {v[0], v[1], v[2], v[3]};
-          finish(c, u, 4);
-        }
-      }
-    }
-  } else {
-    // Exchange: the piece of 4 columns c goes to CTA c / own, at
-    // [source][piece][feature] of its drained ring.
-    const int pieces = p.own / 4;                // of one owner
+  const uint32_t tbase = tmem + ((uint32_t)(q * 32) << 16);
+  // Partial sums by pieces of 4 columns: [source][piece of its owner][feature].
+  const int pieces = p.own / 4;
+  const uint32_t my_piece = (uint32_t)(q * 32 + lane) * 16u;
+  if (S > 1) {
     cluster_sync_all();                          // every CTA's products are complete
     if (active) {
-      for (int c = 0; c < p.bn; c += 16) {
-        float v[16];
-        read_acc(c, v);
+      int owner = 0, piece = 0;
+      for (int c = 0; c < with_tokens; c += 16) {
+        uint32_t acc[16];
+        __syncwarp();
+        tmem_load_16cols(tbase + c, acc);
+        tmem_wait_ld16(acc);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int owner = (c + 4 * i) / p.own, piece = (c + 4 * i - owner * p.own) / 4;
-          const uint32_t at = base + (uint32_t)((((int)rank * pieces + piece) * 128 + q * 32 + lane) * 16);
-          store_cluster_v4(map_to_rank(at, (uint32_t)owner), __float_as_uint(v[4 * i]),
-                           __float_as_uint(v[4 * i + 1]), __float_as_uint(v[4 * i + 2]),
-                           __float_as_uint(v[4 * i + 3]));
+          if (c + 4 * i < with_tokens)
+            store_cluster_v4(map_to_rank(base + (rank * pieces + piece) * 2048u + my_piece,
+                                         (uint32_t)owner),
+                             acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
+          if (++piece == pieces) { piece = 0; ++owner; }
         }
       }
     }
     cluster_sync_all();                          // every partial sum has arrived
-    // W columns from piece `piece` on: the sources' sums in rank order.
-    auto gather = [&](int piece, auto& v) {
-      constexpr int W = sizeof(v) / sizeof(v[0]);
-      const int col = (int)rank * p.own + piece * 4;
+  }
+  if (active) {
+#pragma unroll 1
+    for (int c0 = 0; c0 < n_cols; c0 += 16) {
+      if ((c0 & 31) == 0) {
+        factor = next_factor;
+        next_factor = row_factor(c0 + 32);
+      }
 #pragma unroll
-      for (int i = 0; i < W; ++i) v[i] = 0.f;
-      for (int src = 0; src < S; ++src) {
-#pragma unroll
-        for (int i = 0; i < W / 4; ++i) {
-          if (piece + i >= pieces) break;
-          const float4 u = *reinterpret_cast<const float4*>(
-              gbase + (size_t)(((src * pieces + piece + i) * 128 + q * 32 + lane) * 16));
-          v[4 * i] += u.x; v[4 * i + 1] += u.y; v[4 * i + 2] += u.z; v[4 * i + 3] += u.w;
+      for (int g = 0; g < 4; ++g) {
+        const int c = c0 + 4 * g;
+        if (c >= n_cols) break;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (S == 1) {
+          uint32_t acc[4];
+          __syncwarp();                          // (.aligned, after per-lane work)
+          tmem_load_4cols(tbase + c, acc);
+          tmem_wait_ld4(acc);
+          v = make_float4(__uint_as_float(acc[0]), __uint_as_float(acc[1]),
+                          __uint_as_float(acc[2]), __uint_as_float(acc[3]));
+        } else {
+          const uint8_t* at = gbase + c * 512 + my_piece;
+          for (int src = 0; src < S; ++src, at += pieces * 2048) {
+            const float4 u = *reinterpret_cast<const float4*>(at);
+            v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
+          }
         }
-      }
-      finish(col, v, min(W, min(p.own - piece * 4, p.bn - col)));
-    };
-    if (active) {
-      const int cols = min(p.own, min(p.bn, p.M - m0) - (int)rank * p.own);   // with tokens
-      int c = 0;
-      for (; c + 4 < cols; c += 16) {
-        float v[16];
-        gather(c / 4, v);
-      }
-      if (c < cols) {
-        float v[4];
-        gather(c / 4, v);
+        v.x = fmaf(v.x, scale * __shfl_sync(0xFFFFFFFFu, factor, c & 31), bias);
+        v.y = fmaf(v.y, scale * __shfl_sync(0xFFFFFFFFu, factor, (c + 1) & 31), bias);
+        v.z = fmaf(v.z, scale * __shfl_sync(0xFFFFFFFFu, factor, (c + 2) & 31), bias);
+        v.w = fmaf(v.w, scale * __shfl_sync(0xFFFFFFFFu, factor, (c + 3) & 31), bias);
+        const int count = mine ? n_cols - c : 0;
+        if (p.z) {
+          epi_store4(z_at, z_step, p.z_dt, count, v);
+          z_at += 4 * z_step;
+        }
+        v = activate4<AB_BYTES>(v, p.act);
+        if (p.r) {
+          v.x += r[4 * g]; v.y += r[4 * g + 1]; v.z += r[4 * g + 2]; v.w += r[4 * g + 3];
+          if (c + 16 < n_cols) fetch(g, c + 16);
+        }
+        epi_store4(d_at, d_step, p.d_dt, count, v);
+        d_at += 4 * d_step;
       }
     }
   }
