@@ -15,6 +15,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -185,16 +186,16 @@ def library():
             lib.gemm_last_config.argtypes = [vp, ctypes.POINTER(gemm_config_t)]
             lib.gemm_tmem_columns.argtypes = [i32, i32]
             lib.gemm_set_timeout_ns.argtypes = [vp, ctypes.c_uint64]
-            lib.gemm_rmsnorm.argtypes = [vp, ctypes.POINTER(gemm_rmsnorm_t), vp]
+            lib.gemm_rmsnorm.argtypes = [vp, vp, vp]
             lib.gemm_rmsnorm_check.argtypes = [ctypes.POINTER(gemm_rmsnorm_t)]
             lib.gemm_rmsnorm_bwd_check.argtypes = [ctypes.POINTER(gemm_rmsnorm_bwd_t)]
             lib.gemm_rmsnorm_bwd_workspace.argtypes = [i64, i64]
             lib.gemm_rmsnorm_bwd_workspace.restype = i64
-            lib.gemm_rmsnorm_bwd.argtypes = [vp, ctypes.POINTER(gemm_rmsnorm_bwd_t), vp, i64, vp]
+            lib.gemm_rmsnorm_bwd.argtypes = [vp, vp, vp, i64, vp]
             lib.gemm_linear_check.argtypes = [ctypes.POINTER(gemm_linear_t)]
-            lib.gemm_linear.argtypes = [vp, ctypes.POINTER(gemm_linear_t), vp]
+            lib.gemm_linear.argtypes = [vp, vp, vp]
             lib.gemm_linear_bwd_check.argtypes = [ctypes.POINTER(gemm_linear_bwd_t)]
-            lib.gemm_linear_bwd.argtypes = [vp, ctypes.POINTER(gemm_linear_bwd_t), vp]
+            lib.gemm_linear_bwd.argtypes = [vp, vp, vp]
             for name in ("gemm_create", "gemm_destroy", "gemm_run", "gemm_run_noalloc",
                          "gemm_sync_status",
                          "gemm_check", "gemm_plan", "gemm_set_config", "gemm_last_config",
@@ -397,6 +398,15 @@ def gemm_linear_bwd(handle, problem: gemm_linear_bwd_t, stream=None, check=True)
 
 
 # ------------------------------------------------------------------ tensors
+#
+# The calls on tensors fill the C structures by struct.pack (the fields of the
+# ctypes structures above, in order): a call then costs about half of what building
+# a ctypes structure and keyword checks would.
+
+_RMSNORM = struct.Struct("<2q3if11Q")
+_RMSNORM_BWD = struct.Struct("<2q3i4x11Q")
+_LINEAR = struct.Struct("<3q9if13Q")
+_LINEAR_BWD = struct.Struct("<3q6if4x15Q")
 
 # Type codes by the name of a tensor's dtype.
 _TENSOR_CODES = {"torch.float32": GEMM_F32, "torch.float16": GEMM_F16,
@@ -406,57 +416,67 @@ _CODE_OF = {}           # the same by the dtype object, filled as they are met
 
 
 def _code(t, what):
-    code = _CODE_OF.get(t.dtype)
+    dtype = t.dtype
+    if dtype in _CODE_OF:
+        return _CODE_OF[dtype]
+    code = _TENSOR_CODES.get(str(dtype))
     if code is None:
-        code = _TENSOR_CODES.get(str(t.dtype))
-        if code is None:
-            raise GemmError(GEMM_ERR_UNSUPPORTED_DTYPE, f"{what}: {t.dtype}")
-        _CODE_OF[t.dtype] = code
+        raise GemmError(GEMM_ERR_UNSUPPORTED_DTYPE, f"{what}: {dtype}")
+    _CODE_OF[dtype] = code
     return code
 
 
-def _rows(t, M, N, what, code=None):
-    """(address, row stride) of an M x N tensor whose rows are contiguous, of type
-    `code` if given; (None, 0) for None."""
-    if t is None:
-        return None, 0
+def _shape(t, what):
     shape = t.shape
-    if len(shape) != 2 or shape[0] != M or shape[1] != N:
-        raise GemmError(GEMM_ERR_INVALID_ARG, f"{what}: shape {tuple(shape)}, not ({M}, {N})")
-    s0, s1 = t.stride()
-    if s1 != 1 and N > 1:
-        raise GemmError(GEMM_ERR_INVALID_ARG, f"{what}: rows are not contiguous")
+    if len(shape) != 2:
+        raise GemmError(GEMM_ERR_INVALID_ARG, f"{what}: shape {tuple(shape)}, not a matrix")
+    return shape
+
+
+def _rows(t, shape, what, code=None):
+    """(address, row stride) of a matrix of that shape whose rows are contiguous, of type
+    `code` if given; (0, 0) for None."""
+    if t is None:
+        return 0, 0
+    if t.shape != shape:
+        raise GemmError(GEMM_ERR_INVALID_ARG, f"{what}: shape {tuple(t.shape)}, not {tuple(shape)}")
     if code is not None and _code(t, what) != code:
         raise GemmError(GEMM_ERR_UNSUPPORTED_DTYPE, f"{what}: {t.dtype}")
-    # the stride of a single row says nothing: any sufficient aligned one will do
-    return t.data_ptr(), s0 if M > 1 else max(s0, (N + 15) // 16 * 16)
-
-
-def _operand(t, R, K, what):
-    """(address, stride, layout) of an R x K product operand, either dimension contiguous."""
-    shape = t.shape
-    if len(shape) != 2 or shape[0] != R or shape[1] != K:
-        raise GemmError(GEMM_ERR_INVALID_ARG, f"{what}: shape {tuple(shape)}, not ({R}, {K})")
     s0, s1 = t.stride()
+    if s1 != 1 and shape[1] > 1:
+        raise GemmError(GEMM_ERR_INVALID_ARG, f"{what}: rows are not contiguous")
+    if shape[0] == 1:
+        # the stride of a single row says nothing: any sufficient aligned one will do
+        s0 = max(s0, (shape[1] + 15) // 16 * 16)
+        s0 = (s0 + 15) // 16 * 16
+    return t.data_ptr(), s0
+
+
+def _operand(t, shape, what):
+    """(address, stride, layout) of an R x K product operand, either dimension contiguous."""
+    if t.shape != shape:
+        raise GemmError(GEMM_ERR_INVALID_ARG, f"{what}: shape {tuple(t.shape)}, not {tuple(shape)}")
+    s0, s1 = t.stride()
+    R, K = shape
     if s1 == 1 and not (s0 == 1 and R > 1):
-        return t.data_ptr(), s0 if R > 1 else max(s0, (K + 15) // 16 * 16), GEMM_K_MAJOR
+        return t.data_ptr(), s0 if R > 1 else (max(s0, K) + 15) // 16 * 16, GEMM_K_MAJOR
     if s0 == 1 or R == 1:
-        return t.data_ptr(), s1 if K > 1 else max(s1, (R + 15) // 16 * 16), GEMM_MN_MAJOR
+        return t.data_ptr(), s1 if K > 1 else (max(s1, R) + 15) // 16 * 16, GEMM_MN_MAJOR
     raise GemmError(GEMM_ERR_INVALID_ARG, f"{what}: neither dimension is contiguous")
 
 
 def _activation(name):
     try:
         return ACTIVATION_CODES[name]
-    except KeyError:
+    except (KeyError, TypeError):
         raise GemmError(GEMM_ERR_INVALID_ARG, f"activation {name!r}") from None
 
 
 def _vector(t, n, what, code=None):
-    """Address of a contiguous vector of n elements (of type `code` if given); None for None."""
+    """Address of a contiguous vector of n elements (of type `code` if given); 0 for None."""
     if t is None:
-        return None
-    if len(t.shape) != 1 or t.shape[0] != n or (n > 1 and t.stride()[0] != 1):
+        return 0
+    if t.shape != (n,) or (n > 1 and t.stride()[0] != 1):
         raise GemmError(GEMM_ERR_INVALID_ARG, f"{what}: not a contiguous vector of {n}")
     if code is not None and _code(t, what) != code:
         raise GemmError(GEMM_ERR_UNSUPPORTED_DTYPE, f"{what}: {t.dtype}")
@@ -474,6 +494,7 @@ class Gemm:
 
     def __init__(self, device: int = 0):
         self.handle = gemm_create(device)
+        self._lib = library()
 
     def close(self):
         if self.handle:
@@ -525,37 +546,36 @@ class Gemm:
         """y = (x + residual) * rstd * weight; see gemm_rmsnorm in the C header.  An 8-bit
         y (float8_e4m3fn, float8_e5m2) is quantised per row, with its scales in
         `scale`; `h` receives x + residual, `rstd` the rows' factors."""
-        M, H = x.shape
+        shape = _shape(x, "x")
+        M, H = shape
         t = _code(x, "x")
-        px, ldx = _rows(x, M, H, "x")
-        pr, ldr = _rows(residual, M, H, "residual", t)
-        ph, ldh = _rows(h, M, H, "h", t)
-        py, ldy = _rows(y, M, H, "y")
-        p = gemm_rmsnorm_t(M, H, t, _code(weight, "weight"), _code(y, "y"), eps, px, ldx, pr, ldr,
-                           _vector(weight, H, "weight"), ph, ldh, py, ldy,
-                           _vector(scale, M, "scale", GEMM_F32),
-                           _vector(rstd, M, "rstd", GEMM_F32))
-        gemm_rmsnorm(self.handle, p, stream)
+        st = self._lib.gemm_rmsnorm(self.handle, _RMSNORM.pack(
+            M, H, t, _code(weight, "weight"), _code(y, "y"), eps, *_rows(x, shape, "x"),
+            *_rows(residual, shape, "residual", t), _vector(weight, H, "weight"),
+            *_rows(h, shape, "h", t), *_rows(y, shape, "y"), _vector(scale, M, "scale", GEMM_F32),
+            _vector(rstd, M, "rstd", GEMM_F32)), stream and _stream(stream))
+        if st:
+            raise GemmError(st, "gemm_rmsnorm")
 
     def rmsnorm_bwd(self, dy, h, weight, rstd, dx, dweight, dh=None, workspace=None,
                     stream=None):
         """Gradients of x (= of the residual) and of weight; see gemm_rmsnorm_bwd in the C
         header.  `workspace`: a contiguous tensor of at least
         gemm_rmsnorm_bwd_workspace(M, H) bytes."""
-        M, H = dy.shape
+        shape = _shape(dy, "dy")
+        M, H = shape
         t = _code(dy, "dy")
-        pdy, lddy = _rows(dy, M, H, "dy")
-        ph, ldh = _rows(h, M, H, "h", t)
-        pdh, lddh = _rows(dh, M, H, "dh", t)
-        pdx, lddx = _rows(dx, M, H, "dx", t)
-        p = gemm_rmsnorm_bwd_t(M, H, t, _code(weight, "weight"), _code(dweight, "dweight"),
-                               pdy, lddy, ph, ldh, _vector(weight, H, "weight"),
-                               _vector(rstd, M, "rstd", GEMM_F32), pdh, lddh, pdx, lddx,
-                               _vector(dweight, H, "dweight"))
         ws, nbytes = None, 0
         if workspace is not None:
             ws, nbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-        gemm_rmsnorm_bwd(self.handle, p, ws, nbytes, stream)
+        st = self._lib.gemm_rmsnorm_bwd(self.handle, _RMSNORM_BWD.pack(
+            M, H, t, _code(weight, "weight"), _code(dweight, "dweight"), *_rows(dy, shape, "dy"),
+            *_rows(h, shape, "h", t), _vector(weight, H, "weight"),
+            _vector(rstd, M, "rstd", GEMM_F32), *_rows(dh, shape, "dh", t),
+            *_rows(dx, shape, "dx", t), _vector(dweight, H, "dweight")), ws, nbytes,
+            stream and _stream(stream))
+        if st:
+            raise GemmError(st, "gemm_rmsnorm_bwd")
 
     def linear(self, a, b, d, bias=None, activation=None, residual=None, z=None, row_scale=None,
                col_scale=None, alpha=1.0, stream=None):
@@ -563,42 +583,39 @@ class Gemm:
         in the C header.  a [M, K] and b [N, K], either dimension contiguous (fp32 ones
         are read at tf32 precision); activation: None, "relu", "gelu", "gelu_tanh" or "silu";
         z receives what the activation is applied to."""
-        M, K = a.shape
-        N = b.shape[0]
-        ta, tb = _code(a, "a"), _code(b, "b")
-        pa, lda, la = _operand(a, M, K, "a")
-        pb, ldb, lb = _operand(b, N, K, "b")
-        pr, ldr = _rows(residual, M, N, "residual")
-        pz, ldz = _rows(z, M, N, "z")
-        pd, ldd = _rows(d, M, N, "d")
-        p = gemm_linear_t(M, N, K, ta or GEMM_TF32, tb or GEMM_TF32,
-                          0 if bias is None else _code(bias, "bias"),
-                          0 if residual is None else _code(residual, "residual"),
-                          0 if z is None else _code(z, "z"), _code(d, "d"), la, lb,
-                          _activation(activation), alpha, pa, lda, pb, ldb,
-                          _vector(row_scale, M, "row_scale", GEMM_F32),
-                          _vector(col_scale, N, "col_scale", GEMM_F32),
-                          _vector(bias, N, "bias"), pr, ldr, pz, ldz, pd, ldd)
-        gemm_linear(self.handle, p, stream)
+        shape = _shape(a, "a")
+        M, K = shape
+        N = _shape(b, "b")[0]
+        pa, lda, la = _operand(a, shape, "a")
+        pb, ldb, lb = _operand(b, (N, K), "b")
+        out = (M, N)
+        st = self._lib.gemm_linear(self.handle, _LINEAR.pack(
+            M, N, K, _code(a, "a") or GEMM_TF32, _code(b, "b") or GEMM_TF32,
+            0 if bias is None else _code(bias, "bias"),
+            0 if residual is None else _code(residual, "residual"),
+            0 if z is None else _code(z, "z"), _code(d, "d"), la, lb, _activation(activation), alpha,
+            pa, lda, pb, ldb, _vector(row_scale, M, "row_scale", GEMM_F32),
+            _vector(col_scale, N, "col_scale", GEMM_F32), _vector(bias, N, "bias"),
+            *_rows(residual, out, "residual"), *_rows(z, out, "z"), *_rows(d, out, "d")),
+            stream and _stream(stream))
+        if st:
+            raise GemmError(st, "gemm_linear")
 
     def linear_bwd(self, dd, a, b, z=None, activation=None, dz=None, da=None, db=None, dbias=None,
                    accumulate=False, alpha=1.0, stream=None):
         """Gradients of linear from dd, the gradient of d: dz, da, db (added to with
         `accumulate`) and dbias, each where given; see gemm_linear_bwd in the C header."""
-        M, N = dd.shape
-        K = a.shape[1]
+        out = _shape(dd, "dd")
+        M, N = out
+        K = _shape(a, "a")[1]
         t = _code(dd, "dd")
-        pdd, lddd = _rows(dd, M, N, "dd")
-        pz, ldz = _rows(z, M, N, "z", t)
-        pa, lda = _rows(a, M, K, "a", t)
-        pb, ldb = _rows(b, N, K, "b", t)
-        pdz, lddz = _rows(dz, M, N, "dz", t)
-        pda, ldda = _rows(da, M, K, "da")
-        pdb, lddb = _rows(db, N, K, "db")
-        p = gemm_linear_bwd_t(M, N, K, t, 0 if da is None else _code(da, "da"),
-                              0 if db is None else _code(db, "db"),
-                              0 if dbias is None else _code(dbias, "dbias"),
-                              _activation(activation), int(accumulate), alpha, pdd, lddd, pz, ldz,
-                              pa, lda, pb, ldb, pdz, lddz, pda, ldda, pdb, lddb,
-                              _vector(dbias, N, "dbias"))
-        gemm_linear_bwd(self.handle, p, stream)
+        rows_a, rows_b = (M, K), (N, K)
+        st = self._lib.gemm_linear_bwd(self.handle, _LINEAR_BWD.pack(
+            M, N, K, t, 0 if da is None else _code(da, "da"), 0 if db is None else _code(db, "db"),
+            0 if dbias is None else _code(dbias, "dbias"), _activation(activation),
+            int(accumulate), alpha, *_rows(dd, out, "dd"), *_rows(z, out, "z", t),
+            *_rows(a, rows_a, "a", t), *_rows(b, rows_b, "b", t), *_rows(dz, out, "dz", t),
+            *_rows(da, rows_a, "da"), *_rows(db, rows_b, "db"), _vector(dbias, N, "dbias")),
+            stream and _stream(stream))
+        if st:
+            raise GemmError(st, "gemm_linear_bwd")

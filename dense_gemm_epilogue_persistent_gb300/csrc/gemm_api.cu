@@ -197,7 +197,7 @@ struct TileCost {
 };
 
 TileCost tile_cost(int64_t tiles, int64_t k_blocks, int cg, int ka, int bn, int64_t clusters,
-                   double epi_kb, bool can_split, double epi_extra) {
+                   double epi_kb, bool can_split, const EpilogueExtra& extra) {
   clusters = std::max<int64_t>(1, clusters);
   const int64_t full = tiles / clusters, rem = tiles % clusters;
   TileCost t;
@@ -206,6 +206,18 @@ TileCost tile_cost(int64_t tiles, int64_t k_blocks, int cg, int ka, int bn, int6
   t.cta_group = cg;
   const double w = bn / 256.0;
   double per_kb;
+  if (extra.linear) {
+    // The linear layer's kernels (issue by whole warps, a heavier epilogue),
+    // fitted the same way on GB300 to 31 problems (256^3 to 8192^3; bf16 with
+    // and without gelu and a kept pre-activation, E4M3 with scales, silu and a
+    // residual, MN-major operands) x 28 variants: the pick is within 1 % of the
+    // measured fastest on average and 5 % at worst.
+    per_kb = cg == 2 ? w : ka == 1 ? 1.14 * w : w + 0.24 * (256 - bn) / 128.0;
+    t.fixed = cg == 2 ? 12.3 - 2.0 * (bn - 128) / 128.0 : 9.2 - 0.3 * (bn - 128) / 128.0;
+    t.main_loop = (double)k_blocks * per_kb;
+    t.epilogue = (double)(bn / gb300::kEpiChunk) * (4.6 + 0.3 * epi_kb + 1.25 * extra.chunk_cost);
+    return t;
+  }
   if (cg == 2) {
     per_kb = w + 0.22 * (256 - bn) / 128.0;
     t.fixed = 15.0 - 1.9 * (bn - 128) / 128.0;
@@ -214,7 +226,7 @@ TileCost tile_cost(int64_t tiles, int64_t k_blocks, int cg, int ka, int bn, int6
     t.fixed = 11.0 - 0.4 * (bn - 128) / 128.0;
   }
   t.main_loop = (double)k_blocks * per_kb;
-  t.epilogue = (double)(bn / gb300::kEpiChunk) * (2.5 + 0.08 * epi_kb + epi_extra);
+  t.epilogue = (double)(bn / gb300::kEpiChunk) * (2.5 + 0.08 * epi_kb);
   return t;
 }
 
@@ -226,7 +238,15 @@ bool two_epilogue_warps_pay(const TileCost& t) {
   return t.single_wave || t.epilogue >= t.main_loop;
 }
 
-double plan_cost(const TileCost& t, int epw) {
+double plan_cost(const TileCost& t, int epw, bool linear) {
+  if (linear) {
+    const double main_loop = epw == 2 ? 1.08 * t.main_loop : t.main_loop;
+    const double epilogue = epw == 2 ? 0.2 * t.epilogue : t.epilogue;
+    const double fixed = epw == 2 ? 0.8 * t.fixed : t.fixed;
+    if (t.single_wave)
+      return main_loop + 0.03 * epilogue + fixed + (t.cta_group == 2 ? 4.5 : 0.0);
+    return t.waves * (std::max(main_loop, epilogue) + fixed);
+  }
   const double main_loop = epw == 2 ? 1.015 * t.main_loop : t.main_loop;
   const double epilogue = epw == 2 ? 0.55 * t.epilogue : t.epilogue;
   const double fixed = epw == 2 ? 0.9 * t.fixed : t.fixed;
@@ -276,7 +296,7 @@ int64_t resident_clusters(int sm_count, const int* clusters_by_size, int csize) 
 gemm_status_t gb300host::plan_valid(const gemm_problem_t& p, int sm_count, int smem_optin,
                                     const gemm_config_t* forced, gemm_config_t* out,
                                     const int* clusters_by_size, bool stream_k_ok,
-                                    const EpilogueExtra& extra) {
+                                    const EpilogueExtra& extra, double* cost) {
   const int ab_bytes = dtype_bytes(p.dtypes.ab);
 
   const int fcg = forced ? forced->cta_group : 0;
@@ -292,14 +312,14 @@ gemm_status_t gb300host::plan_valid(const gemm_problem_t& p, int sm_count, int s
       ((reads_c(p) ? dtype_bytes(p.dtypes.c) : 0) + (reads_x(p) ? dtype_bytes(p.dtypes.x) : 0) +
        dtype_bytes(p.dtypes.d) + (p.Y ? dtype_bytes(p.dtypes.y) : 0)) / 1024.0;
   // Widest tiles first: among equal costs the wider (fewer-tile) one wins.
-  // The automatic choice takes widths of 128 and more (the range the cost
-  // model's constants were measured on); 64 and 96 run when forced.
+  // The GEMM's automatic choice takes widths of 128 and more (the range its
+  // cost model's constants were measured on); 64 and 96 run when forced.
   for (int a : {2, 1})
     for (int b = 256; b >= 64; b -= 32)
       for (int m : {1, 2})
         for (int n : {1, 2}) {
           if ((fcg && a != fcg) || (fbn && b != fbn)) continue;
-          if (!fbn && b < 128) continue;
+          if (!fbn && b < 128 && !extra.linear) continue;
           // The library for multi-GPU processes has no multicast kernels.
           if (!GB300_MULTICAST && (m > 1 || n > 1)) continue;
           // Automatic choice: no operand-sharing clusters (see plan_cost); a
@@ -318,18 +338,19 @@ gemm_status_t gb300host::plan_valid(const gemm_problem_t& p, int sm_count, int s
           const TileCost tc = tile_cost(tiles, cdiv(p.K, 128 / ab_bytes), a, ka, b, units, epi_kb,
                                         can_split_tail(p, a, b, m, n) &&
                                             !(forced && forced->tail_split == 1),
-                                        extra.chunk_cost);
+                                        extra);
           // Epilogue warps per lane quarter: forced, or 1 and (where it pays,
           // for clusters of one CTA group) 2.
           for (int e : {1, 2}) {
             if (fepw ? e != fepw
-                     : e == 2 && (m != 1 || n != 1 || !two_epilogue_warps_pay(tc)))
+                     : e == 2 && (m != 1 || n != 1 || !(extra.linear || two_epilogue_warps_pay(tc))))
               continue;
-            const double c = plan_cost(tc, e);
+            const double c = plan_cost(tc, e, extra.linear);
             if (c < best - 1e-9) { best = c; cg = a; bn = b; mc = m; nc = n; epw = e; }
           }
         }
   if (!cg) return GEMM_ERR_UNSUPPORTED_CONFIG;
+  if (cost) *cost = best;
   if (gemm_tmem_columns(128, bn) > (int)gb300::kAccStride) return GEMM_ERR_UNSUPPORTED_CONFIG;
   const int ka = gb300::k_atoms(cg, bn);
   const int csize = cg * mc * nc;
@@ -347,14 +368,19 @@ gemm_status_t gb300host::plan_valid(const gemm_problem_t& p, int sm_count, int s
   // keeps the epilogue ahead of fast main loops (8-bit inputs, short K).  (A
   // CTA's last tile takes the C/X its lookahead has not reached from the
   // drained ring, so single-wave problems need no extra slots.)
-  const int max_stages = max_stages_for(2);
+  // (The linear layer's epilogue gives up its second slot for a third stage:
+  // with two the main loop stalls.  Each of a lane quarter's warps needs a
+  // sub-slot of its own, so only with one warp a quarter.)
+  const int min_slots =
+      extra.linear && epw == 1 && max_stages_for(2) < 3 && max_stages_for(1) >= 3 ? 1 : 2;
+  const int max_stages = max_stages_for(min_slots);
   const int stages = forced && forced->stages ? forced->stages : max_stages;
   const int64_t tiles_m = cdiv(std::max<int64_t>(p.M, 1), 128 * cg * mc);
   const int64_t tiles_n = cdiv(std::max<int64_t>(p.N, 1), (int64_t)bn * nc);
   const int64_t tiles = tiles_m * tiles_n * std::max<int64_t>(p.L, 1);
   const int64_t units = resident_clusters(sm_count, clusters_by_size, csize);
   if (stages < 2 || stages > max_stages) return GEMM_ERR_UNSUPPORTED_CONFIG;
-  int slots = 2;
+  int slots = min_slots;
   while (slots < kMaxEpiSlots && total_smem(cg, bn, ka, stages, slots + 1, slot, extra.smem) <= smem_optin)
     ++slots;
   if (forced && forced->epi_slots) {

@@ -566,6 +566,8 @@ persistent_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
   // Stream-K items (a separate instantiation, so that the other kernels carry
   // none of its code).
   constexpr bool kSK = SK != 0;
+  // The linear layer's kernels issue by whole warps (see the producer).
+  constexpr bool kWarpIssue = EPI == 1;
 
   // The next GEMM of the stream may start its prologue on SMs this grid leaves
   // idle; it touches global memory only after its own dependency wait below.
@@ -673,7 +675,10 @@ persistent_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
 
   if (warp == 0) {
     // ---------------------------------------------------------- TMA producer
-    if (lane == 0) {
+    // kWarpIssue: the whole warp runs the loop and only the asynchronous
+    // instructions sit under the elected lane, so that their operands stay in
+    // uniform registers; else one lane runs all of it.
+    if (kWarpIssue || lane == 0) {
       const uint64_t pol = make_l2_policy(p.l2_hints & 3u);
       const uint32_t tx_bytes = (uint32_t)(CG * (G::A_STAGE + T.b_stage));
       int s = 0;
@@ -702,9 +707,12 @@ persistent_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
         const bool k_down = p.k_alternate && ((it / num_clusters) & 1);
         for (int kb = wk.kb0; kb < wk.kb1; ++kb) {
           const long long t_w = stat_clock();
-          if (!wait_phase(empty0 + 8u * s, ph ^ 1u, w, kWaitProducer)) { ok = false; break; }
+          bool drained = wait_phase(empty0 + 8u * s, ph ^ 1u, w, kWaitProducer);
+          if constexpr (kWarpIssue) drained = __all_sync(0xFFFFFFFFu, drained);
+          if (!drained) { ok = false; break; }
           if constexpr (kRingStats) st_empty += clock64() - t_w;
           const uint32_t fb = full0 + 8u * s;
+          if (!kWarpIssue || elect_one()) {
           if (rank == 0) mbar_arrive_expect_tx(fb, tx_bytes);
           const uint32_t fb_target = (CG == 2) ? map_to_rank(fb, pair_leader) : fb;
           const int k0 = (k_down ? p.k_blocks - 1 - kb : kb) * G::BK;
@@ -751,11 +759,16 @@ persistent_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
               issue_b(sb + ((int)gm * atoms + j) * G::ATOM_BYTES, n0 + j * G::ATOM_MN, k0,
                       G::ATOM_BYTES);
           }
+          }                                  // (elected)
+          if constexpr (kWarpIssue) {
+            __syncwarp();
+            if (kDebug) ok = __all_sync(0xFFFFFFFFu, ok);
+          }
           if (kDebug && !ok) break;
           if (++s == S) { s = 0; ph ^= 1u; }
         }
       }
-      if constexpr (kRingStats) if (p.stats) {
+      if constexpr (kRingStats) if (p.stats && lane == 0) {
         unsigned long long* const o = p.stats + (size_t)blockIdx.x * kStatWords;
         o[kStatProdEmpty] = st_empty;
         o[kStatProdLoop] = clock64() - st_t0;
@@ -764,7 +777,59 @@ persistent_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
     __syncwarp();
   } else if (warp == 1) {
     // ---------------------------------------------------------- MMA issuer
-    if (rank == 0 && lane == 0) {
+    if constexpr (kWarpIssue) {
+      // The same loop for the whole warp, the MMAs and commits under the elected
+      // lane.  The descriptors' constant parts are built once (their address
+      // field counts 16-byte units); a stage and a K step only add to them.
+      if (rank == 0) {
+        const uint64_t a0 = p.a_mn_major ? smem_desc_sw128(a_ring, G::ATOM_BYTES, 1024)
+                                         : smem_desc_sw128(a_ring, 16, 1024);
+        const uint64_t b0 = p.b_mn_major ? smem_desc_sw128(b_ring, G::ATOM_BYTES, 1024)
+                                         : smem_desc_sw128(b_ring, 16, 1024);
+        // 16-byte units from one K step to the next, and from one K-major atom
+        // of 4 steps to the next
+        const uint32_t a_step = (p.a_mn_major ? G::UMMA_K * 128 : 32) / 16;
+        const uint32_t b_step = (p.b_mn_major ? G::UMMA_K * 128 : 32) / 16;
+        const uint32_t a_atom =
+            p.a_mn_major ? G::STEPS_PER_ATOM * a_step : (uint32_t)G::A_ATOM / 16;
+        const uint32_t b_atom = p.b_mn_major ? G::STEPS_PER_ATOM * b_step : (uint32_t)T.b_atom / 16;
+        int s = 0, acc = 0;
+        uint32_t ph = 0, aph = 0;
+        bool ok = !p.inject_stall ||
+                  __all_sync(0xFFFFFFFFu, wait_phase(never_bar, 0u, w, kWaitInjected));
+        for (int it = cluster_id; ok && it < p.num_items; it += num_clusters) {
+          const Work wk = work_item<kSK>(it, p, num_clusters);
+          if (!__all_sync(0xFFFFFFFFu, wait_phase(tempty0 + 8u * acc, aph ^ 1u, w, kWaitMmaAcc)))
+            break;
+          tc_fence_after_sync();
+          const uint32_t d_tmem = tmem_base + (uint32_t)acc * kAccStride;
+          const uint32_t idesc = wk.half < 0 ? p.idesc : p.idesc_half;
+          for (int kb = wk.kb0; kb < wk.kb1; ++kb) {
+            ok = __all_sync(0xFFFFFFFFu, wait_phase(full0 + 8u * s, ph, w, kWaitMmaFull));
+            if (!ok) break;
+            tc_fence_after_sync();
+            const uint64_t ad = a0 + (uint32_t)(s * G::A_STAGE) / 16;
+            const uint64_t bd = b0 + (uint32_t)(s * T.b_stage) / 16;
+            if (elect_one()) {
+#pragma unroll
+              for (int k = 0; k < G::K_STEPS; ++k) {
+                const int at = k / G::STEPS_PER_ATOM, in = k % G::STEPS_PER_ATOM;
+                umma<CG, KIND>(d_tmem, ad + (at * a_atom + in * a_step),
+                               bd + (at * b_atom + in * b_step), idesc,
+                               (kb != wk.kb0 || k != 0) ? 1u : 0u);
+              }
+              umma_commit<CG, MULTI>(empty0 + 8u * s, all_mask);
+            }
+            __syncwarp();
+            if (++s == S) { s = 0; ph ^= 1u; }
+          }
+          if (!ok) break;
+          if (elect_one()) umma_commit<CG, (CG == 2)>(tfull0 + 8u * acc, pair_mask);
+          __syncwarp();
+          if (++acc == kAccStages) { acc = 0; aph ^= 1u; }
+        }
+      }
+    } else if (rank == 0 && lane == 0) {
       int s = 0, acc = 0;
       uint32_t ph = 0, aph = 0;
       long long st_full = 0, st_acc = 0, st_stages = 0;

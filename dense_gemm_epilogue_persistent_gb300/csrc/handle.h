@@ -54,6 +54,27 @@ struct LaunchEntry {
 
 constexpr int kLaunchCacheEntries = 4;
 
+// Plans of the linear layer's latest shapes.  A plan depends on sizes, layouts,
+// types, activation and which tensors are there, never on an address.
+struct SplitPlan {           // split-K kernel: tokens, features and CTAs of a tile, ring
+  int bn, feats, split, ka, stages, smem;
+  int64_t tiles_m, tiles_n;
+};
+struct LinearKey {
+  int64_t M, N, K;
+  uint64_t config_gen;
+  int a_type, b_type, r_type, z_type, d_type, layoutA, layoutB, activation, has_r, has_z;
+};
+struct LinearPlan {
+  bool valid = false;
+  LinearKey key;
+  bool split = false;        // the split-K kernel, else the persistent one
+  SplitPlan s{};
+  gemm_config_t cfg{};
+  const void* kern = nullptr;
+};
+constexpr int kLinearPlans = 16;
+
 // NVTX ranges in the "gemm_gb300" domain around every entry point that
 // enqueues work (and around planning and tensor-map encoding on a launch-cache
 // miss), so that a profiler's timeline and its range filters (ncu --nvtx
@@ -96,6 +117,9 @@ struct gemm_handle {
   uint64_t config_gen = 0;
   gb300host::LaunchEntry cache[gb300host::kLaunchCacheEntries];
   int cache_next = 0;
+  gb300host::LinearPlan linear_plans[gb300host::kLinearPlans];
+  int linear_next = 0;
+  int split_clusters[9] = {0, 0, 0, 0, 0, 0, 0, 0, 0};   // resident, by cluster size (0: not asked)
   std::mutex mu;
   void* ws = nullptr;          // gemm_run_host's device copies of its host buffers
   size_t ws_bytes = 0;
@@ -141,9 +165,10 @@ inline int b_type(const gemm_dtypes_t& t) { return t.b == GEMM_F32 ? t.ab : t.b;
 inline bool reads_c(const gemm_problem_t& p) { return p.beta != 0.0f; }
 inline bool reads_x(const gemm_problem_t& p) { return p.X != nullptr && p.x_factor != 0.0f; }
 
-// What an epilogue other than the GEMM's own adds to a plan: shared memory per
-// CTA, and time per 32-column chunk in the cost model's units.
+// What the linear layer's epilogue adds to a plan: its own cost model, shared
+// memory per CTA, and the activation's time per 32-column chunk.
 struct EpilogueExtra {
+  bool linear = false;
   int smem = 0;
   double chunk_cost = 0.0;
 };
@@ -153,7 +178,7 @@ struct EpilogueExtra {
 gemm_status_t plan_valid(const gemm_problem_t& p, int sm_count, int smem_optin,
                          const gemm_config_t* forced, gemm_config_t* out,
                          const int* clusters_by_size, bool stream_k_ok,
-                         const EpilogueExtra& extra);
+                         const EpilogueExtra& extra, double* cost = nullptr);
 bool encode_operand(EncodeTiledFn enc, CUtensorMap* map, const void* ptr, int dt, int64_t rows,
                     int64_t K, int64_t L, int64_t ld, bool mn_major, int box_rows, int tile_k);
 bool encode_epi(EncodeTiledFn enc, CUtensorMap* map, const void* ptr, int dt, int64_t M,

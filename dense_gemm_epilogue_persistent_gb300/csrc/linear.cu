@@ -34,7 +34,7 @@ struct ActGradParams {
 // flight together.  A column's sum is added in a fixed order: a thread's rows,
 // the 32 groups through shared memory, the cluster's blocks by its first one.
 template <int DT>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, 4)
 act_grad_kernel(const __grid_constant__ ActGradParams p) {
   __shared__ float part[32][64];
   __shared__ float block_part[64];
@@ -194,25 +194,33 @@ double activation_cost(int act) {
   }
 }
 
-// Enqueue a checked call on the persistent kernel.
-gemm_status_t run_persistent(gemm_handle* h, const gemm_linear_t& p, struct CUstream_st* stream) {
+// Plan a checked call on the persistent kernel (h->mu held); *cost receives the
+// cost model's figure.
+gemm_status_t plan_persistent(gemm_handle* h, const gemm_linear_t& p, LinearPlan& out,
+                              double* cost) {
   const gemm_problem_t g = as_problem(p);
-  std::lock_guard<std::mutex> guard(h->mu);
-  gemm_config_t cfg{};
+  gemm_config_t& cfg = out.cfg;
   GB300_CHECK(plan_valid(g, h->sm_count, h->smem_optin, h->forced ? &h->forced_cfg : nullptr, &cfg,
                          h->clusters_by_size, false,
-                         EpilogueExtra{(int)gb300::kLinearSmem, activation_cost(p.activation)}));
+                         EpilogueExtra{true, (int)gb300::kLinearSmem, activation_cost(p.activation)},
+                         cost));
   if (cfg.cluster_m != 1 || cfg.cluster_n != 1) return GEMM_ERR_UNSUPPORTED_CONFIG;
   const int es = dtype_bytes(p.a_type);
   const int ka = gb300::k_atoms(cfg.cta_group, cfg.tile_n);
-  const void* kern = gb300::linear_kernel_for(es, cfg.cta_group, ka, cfg.epi_warps);
-  if (!kern) return GEMM_ERR_UNSUPPORTED_CONFIG;
+  out.kern = gb300::linear_kernel_for(es, cfg.cta_group, ka, cfg.epi_warps);
+  if (!out.kern) return GEMM_ERR_UNSUPPORTED_CONFIG;
   VariantState& vs = h->linear_variants[es == 2 ? 0 : es == 1 ? 1 : 2][cfg.cta_group - 1][ka - 1]
                                        [cfg.epi_warps - 1];
   int resident = 0;
-  GB300_CHECK(resident_kernel_clusters(h, vs, kern, cfg, cfg.cta_group, &resident));
+  GB300_CHECK(resident_kernel_clusters(h, vs, out.kern, cfg, cfg.cta_group, &resident));
   cfg.grid_ctas = (int)std::min<int64_t>(cfg.tiles + cfg.tail_split, resident) * cfg.cta_group;
+  return GEMM_OK;
+}
 
+// Enqueue a call on the persistent kernel by its plan.
+gemm_status_t run_persistent(gemm_handle* h, const gemm_linear_t& p, const LinearPlan& plan,
+                             struct CUstream_st* stream) {
+  const gemm_config_t& cfg = plan.cfg;
   CUtensorMap maps[6];                 // A, B, C, X, D, Y
   std::memset(maps, 0, sizeof(maps));
   const bool a_mn = p.layoutA == GEMM_MN_MAJOR, b_mn = p.layoutB == GEMM_MN_MAJOR;
@@ -287,19 +295,12 @@ gemm_status_t run_persistent(gemm_handle* h, const gemm_linear_t& p, struct CUst
   lc.attrs = attr;
   lc.numAttrs = 2;
   void* args[7] = {&maps[0], &maps[1], &maps[2], &maps[3], &maps[4], &maps[5], &kp};
-  if (cudaLaunchKernelExC(&lc, kern, args) != cudaSuccess) {
+  if (cudaLaunchKernelExC(&lc, plan.kern, args) != cudaSuccess) {
     cudaGetLastError();
     return GEMM_ERR_CUDA;
   }
-  h->last = cfg;
   return GEMM_OK;
 }
-
-// The split-K kernel's plan: tokens per tile, CTAs per cluster, ring depth.
-struct SplitPlan {
-  int bn, feats, split, ka, stages, smem;
-  int64_t tiles_m, tiles_n;
-};
 
 // The ring, its barriers and the alignment; the last stage's matrix operand,
 // 128 rows whatever `feats`, has to lie inside.
@@ -345,11 +346,28 @@ bool plan_split(const gemm_linear_t& p, int bn, int feats, int split, SplitPlan*
   return out->tiles_m * out->tiles_n * split <= INT32_MAX;
 }
 
-gemm_status_t run_split(gemm_handle* h, const gemm_linear_t& p, const SplitPlan& s,
+// What gemm_last_config reports of a split-K launch.
+gemm_config_t config_of(const SplitPlan& s, int es) {
+  gemm_config_t c{};
+  c.cta_group = 1;
+  c.tile_m = s.feats;
+  c.tile_n = s.bn;
+  c.tile_k = 128 / es * s.ka;
+  c.stages = s.stages;
+  c.acc_stages = 1;
+  c.ring_bytes = s.stages * s.ka * (s.feats + s.bn) * 128;
+  c.smem_bytes = s.smem;
+  c.tiles = s.tiles_m * s.tiles_n;
+  c.grid_ctas = (int)(c.tiles * s.split);
+  c.epi_warps = 1;
+  c.split_k = s.split;
+  return c;
+}
+
+gemm_status_t run_split(gemm_handle* h, const gemm_linear_t& p, const LinearPlan& plan,
                         struct CUstream_st* stream) {
+  const SplitPlan& s = plan.s;
   const int es = dtype_bytes(p.a_type);
-  const void* kern = gb300::split_kernel_for(es);
-  GB300_CHECK(raise_smem(h, kern));
   const bool a_mn = p.layoutA == GEMM_MN_MAJOR, b_mn = p.layoutB == GEMM_MN_MAJOR;
   CUtensorMap feat, tok;
   if (!encode_operand(h->encode, &feat, p.B, p.b_type, p.N, p.K, 1, p.ldb, b_mn, s.feats,
@@ -381,24 +399,7 @@ gemm_status_t run_split(gemm_handle* h, const gemm_linear_t& p, const SplitPlan&
   k.z = p.Z; k.ldz = p.ldz; k.z_dt = p.z_type;
   k.d = p.D; k.ldd = p.ldd; k.d_dt = p.d_type;
   k.act = p.activation;
-  {
-    std::lock_guard<std::mutex> guard(h->mu);
-    k.inject_stall = h->forced && h->forced_cfg.inject_stall;
-    gemm_config_t c{};
-    c.cta_group = 1;
-    c.tile_m = s.feats;
-    c.tile_n = s.bn;
-    c.tile_k = 128 / es * s.ka;
-    c.stages = s.stages;
-    c.acc_stages = 1;
-    c.ring_bytes = s.stages * s.ka * (s.feats + s.bn) * 128;
-    c.smem_bytes = s.smem;
-    c.tiles = s.tiles_m * s.tiles_n;
-    c.grid_ctas = (int)(c.tiles * s.split);
-    c.epi_warps = 1;
-    c.split_k = s.split;
-    h->last = c;
-  }
+  k.inject_stall = plan.cfg.inject_stall;
   cudaLaunchConfig_t lc{};
   cudaLaunchAttribute attr[2];
   lc.gridDim = dim3((unsigned)(s.tiles_m * s.tiles_n * s.split));
@@ -414,30 +415,122 @@ gemm_status_t run_split(gemm_handle* h, const gemm_linear_t& p, const SplitPlan&
   lc.attrs = attr;
   lc.numAttrs = s.split > 1 ? 2 : 1;
   void* args[3] = {&feat, &tok, &k};
-  if (cudaLaunchKernelExC(&lc, kern, args) != cudaSuccess) {
+  if (cudaLaunchKernelExC(&lc, plan.kern, args) != cudaSuccess) {
     cudaGetLastError();
     return GEMM_ERR_CUDA;
   }
   return GEMM_OK;
 }
 
-// The kernel for a call: forced, or by the number of tokens.
+// Clusters of `split` CTAs of the split-K kernel the device holds at once (two
+// CTAs an SM, less what the cluster size leaves over in each GPC), asked for
+// once per size.
+int split_clusters(gemm_handle* h, int split) {
+  int& n = h->split_clusters[split];
+  if (n > 0) return n;
+  const void* kern = gb300::split_kernel_for(2);
+  cudaLaunchConfig_t lc{};
+  cudaLaunchAttribute attr[1];
+  lc.gridDim = dim3((unsigned)(split * 2 * h->sm_count));
+  lc.blockDim = dim3((unsigned)gb300::kSplitThreads);
+  lc.dynamicSmemBytes = (size_t)kSplitSmem;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)split;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  lc.attrs = attr;
+  lc.numAttrs = 1;
+  if (raise_smem(h, kern) != GEMM_OK ||
+      cudaOccupancyMaxActiveClusters(&n, kern, &lc) != cudaSuccess || n <= 0) {
+    cudaGetLastError();
+    n = std::max(1, h->sm_count / split);
+  }
+  return n;
+}
+
+// The split-K kernel's tiles where the call chooses: all features of an MMA,
+// the tokens cut evenly into tiles of at most 128 (whole atoms where they are
+// MN-major), and as many CTAs a tile, with two k-blocks each, as leave every
+// tile's cluster resident (48 x 5000 x 4096 E4M3, 40 tiles: 8.8 us with 6, 9.7 with
+// 5; with 7 some clusters wait for others to end, 13.6).
+bool choose_split(gemm_handle* h, const gemm_linear_t& p, SplitPlan* out) {
+  const int es = dtype_bytes(p.a_type);
+  const int64_t per_tile = cdiv(p.M, cdiv(p.M, 128));
+  int bn = (int)cdiv(per_tile, 16) * 16;
+  if (p.layoutA == GEMM_MN_MAJOR) bn = (int)cdiv(bn, 128 / es) * (128 / es);
+  if (bn > 128 || p.K == 0) return false;
+  const int64_t tiles = cdiv(p.M, bn) * cdiv(p.N, 128);
+  if (tiles > 2 * (int64_t)h->sm_count) return false;
+  int split = (int)std::max<int64_t>(1, std::min<int64_t>(8, cdiv(p.K, 128 / es) / 2));
+  while (split > 1 && tiles > split_clusters(h, split)) --split;
+  return plan_split(p, bn, 128, split, out);
+}
+
+// Which kernel: estimated microseconds of both, linear fits to 200 problems on
+// GB300 (1 to 1024 tokens, 512 to 8192 features and inner sizes, bf16 and E4M3, every
+// layout).  Choosing by them costs 0.3 % over the faster kernel on average, 4 %
+// or more on 5 of them (19 % at worst).  For instance (split-K, persistent):
+// 1 x 4096 x 4096 bf16 9.4, 32.6 us; 64 x 4096 x 4096 12.1, 15.7; 128 x 4096 x 4096
+// 18.2, 15.8; 256 x 1024 x 8192 17.9, 22.5; 512 x 512 x 512 11.9, 5.9.
+bool split_is_faster(const gemm_linear_t& p, const SplitPlan& s, double persistent_cost) {
+  const int es = dtype_bytes(p.a_type);
+  const double weights = (double)p.N * (double)p.K * es / 6.3e6;       // us at 6.3 TB/s
+  const double tokens = (double)p.M * (double)p.K * es * (double)s.tiles_n / 6.3e6;
+  const double k_blocks = (double)cdiv(p.K, 128 / es) / s.split;
+  const double own = (double)cdiv(cdiv(s.bn, s.split), 4) * 4;
+  const double split_us = 2.8 + 0.139 * k_blocks + 0.145 * own +
+                          (s.split > 1 ? 0.041 * s.bn : 0.0) + 0.61 * weights + 0.49 * tokens;
+  const double persistent_us = 1.73 + 0.331 * persistent_cost + 0.514 * weights;
+  return split_us < persistent_us;
+}
+
+// Plan a checked call (h->mu held): as forced, or the faster kernel.
+gemm_status_t plan_linear(gemm_handle* h, const gemm_linear_t& p, LinearPlan& out) {
+  const int es = dtype_bytes(p.a_type);
+  const gemm_config_t& f = h->forced_cfg;
+  double cost = 0.0;
+  if (h->forced && f.split_k > 0) {
+    if (!plan_split(p, f.tile_n ? f.tile_n : 64, f.tile_m ? f.tile_m : 128, f.split_k, &out.s))
+      return GEMM_ERR_UNSUPPORTED_CONFIG;
+    out.split = true;
+  } else {
+    GB300_CHECK(plan_persistent(h, p, out, &cost));
+    out.split = !h->forced && choose_split(h, p, &out.s) && split_is_faster(p, out.s, cost);
+  }
+  if (out.split) {
+    out.kern = gb300::split_kernel_for(es);
+    GB300_CHECK(raise_smem(h, out.kern));
+    out.cfg = config_of(out.s, es);
+    out.cfg.inject_stall = h->forced && f.inject_stall ? 1 : 0;
+  }
+  return GEMM_OK;
+}
+
 gemm_status_t run_linear(gemm_handle* h, const gemm_linear_t& p, struct CUstream_st* stream) {
   if (p.M == 0 || p.N == 0) return GEMM_OK;
-  gemm_config_t forced{};
-  {
-    std::lock_guard<std::mutex> guard(h->mu);
-    if (h->forced) forced = h->forced_cfg;
-    else forced.split_k = -2;            // none
+  LinearKey key;
+  std::memset(&key, 0, sizeof(key));           // padding included: keys compare bytewise
+  key.M = p.M; key.N = p.N; key.K = p.K;
+  key.a_type = p.a_type; key.b_type = p.b_type; key.d_type = p.d_type;
+  key.r_type = p.R ? p.r_type : 0; key.z_type = p.Z ? p.z_type : 0;
+  key.layoutA = p.layoutA; key.layoutB = p.layoutB;
+  key.activation = p.activation;
+  key.has_r = p.R != nullptr; key.has_z = p.Z != nullptr;
+  std::lock_guard<std::mutex> guard(h->mu);
+  key.config_gen = h->config_gen;
+  LinearPlan* plan = nullptr;
+  for (LinearPlan& c : h->linear_plans)
+    if (c.valid && std::memcmp(&c.key, &key, sizeof(key)) == 0) { plan = &c; break; }
+  if (!plan) {
+    plan = &h->linear_plans[h->linear_next];
+    plan->valid = false;
+    GB300_CHECK(plan_linear(h, p, *plan));
+    plan->key = key;
+    plan->valid = true;
+    h->linear_next = (h->linear_next + 1) % kLinearPlans;
   }
-  SplitPlan s{};
-  if (forced.split_k > 0) {
-    if (!plan_split(p, forced.tile_n ? forced.tile_n : 64,
-                    forced.tile_m ? forced.tile_m : 128, forced.split_k, &s))
-      return GEMM_ERR_UNSUPPORTED_CONFIG;
-    return run_split(h, p, s, stream);
-  }
-  return run_persistent(h, p, stream);
+  h->last = plan->cfg;
+  return plan->split ? run_split(h, p, *plan, stream) : run_persistent(h, p, *plan, stream);
 }
 
 // Blocks per cluster of the activation gradient: enough for eight blocks an SM

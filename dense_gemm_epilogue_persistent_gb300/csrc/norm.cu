@@ -723,7 +723,10 @@ GEMM_API gemm_status_t gemm_rmsnorm_bwd(gemm_handle_t h, const gemm_rmsnorm_bwd_
     NormBwdKern kern = p.type == GEMM_F32   ? backward_kernel<gb300::DT_F32>(s)
                        : p.type == GEMM_F16 ? backward_kernel<gb300::DT_F16>(s)
                                             : backward_kernel<gb300::DT_BF16>(s);
-    GB300_CHECK(raise_smem(h, reinterpret_cast<const void*>(kern)));
+    {
+      std::lock_guard<std::mutex> guard(h->mu);
+      GB300_CHECK(raise_smem(h, reinterpret_cast<const void*>(kern)));
+    }
     const size_t slots = (size_t)s.depth * (p.dh ? 3 : 2) * s.threads * s.vpt * gb300::kVec *
                          dtype_bytes(p.type);
     const size_t sums = s.warp ? 8 * (size_t)p.H * sizeof(float) : 0;

@@ -32,9 +32,8 @@ inline gemm_status_t check_matrix(const void* p, int64_t ld, int64_t cols, int d
     if (check_status != GEMM_OK) return check_status;         \
   } while (0)
 
-// Raises `kern`'s dynamic shared-memory limit, once per handle.
+// Raises `kern`'s dynamic shared-memory limit, once per handle (h->mu held).
 inline gemm_status_t raise_smem(gemm_handle* h, const void* kern) {
-  std::lock_guard<std::mutex> g(h->mu);
   for (int i = 0; i < h->raised_count; ++i)
     if (h->raised[i] == kern) return GEMM_OK;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,

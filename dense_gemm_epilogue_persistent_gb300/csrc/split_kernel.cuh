@@ -65,12 +65,6 @@ constexpr uint32_t kSplitBarBytes = 8 * (2 * kSplitMaxStages + 2) + 8;
 
 __device__ __forceinline__ int epi_bytes(int dt) { return dt == DT_F32 ? 4 : 2; }
 
-__device__ __forceinline__ float epi_load(const void* p, int dt) {
-  if (dt == DT_F32) return *static_cast<const float*>(p);
-  const uint16_t b = *static_cast<const uint16_t*>(p);
-  return dt == DT_F16 ? __half2float(__ushort_as_half(b)) : __uint_as_float((uint32_t)b << 16);
-}
-
 // Elements of `count` (up to 4) rows `step` bytes apart.
 __device__ __forceinline__ void epi_store4(uint8_t* p, long long step, int dt, int count,
                                            const float4& v) {
@@ -181,12 +175,27 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tmF, const __grid_consta
   uint8_t* z_at = static_cast<uint8_t*>(p.z) + m_lo * z_step + (long long)n * epi_bytes(p.z_dt);
   const uint8_t* r_at =
       static_cast<const uint8_t*>(p.r) + m_lo * r_step + (long long)n * epi_bytes(p.r_dt);
-  float r[16];
+  // (as they lie in memory: converted where they are used, so that a fetch
+  // waits for nothing)
+  uint32_t r[16];
   auto fetch = [&](int g, int c) {               // r[4 g ..] for columns c ..
+    const uint8_t* const at = r_at + c * r_step;
+    if (p.r_dt == DT_F32) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      r[4 * g + i] =
-          p.r && mine && c + i < n_cols ? epi_load(r_at + (c + i) * r_step, p.r_dt) : 0.f;
+      for (int i = 0; i < 4; ++i)
+        r[4 * g + i] = mine && c + i < n_cols
+                           ? *reinterpret_cast<const uint32_t*>(at + i * r_step) : 0u;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        r[4 * g + i] = mine && c + i < n_cols
+                           ? *reinterpret_cast<const uint16_t*>(at + i * r_step) : 0u;
+    }
+  };
+  auto residual = [&](uint32_t bits) {
+    return p.r_dt == DT_F32   ? __uint_as_float(bits)
+           : p.r_dt == DT_F16 ? __half2float(__ushort_as_half((uint16_t)bits))
+                              : __uint_as_float(bits << 16);
   };
   auto row_factor = [&](int c) {                 // this lane's of columns c .. c + 31
     return p.row_scale && c + lane < n_cols ? __ldg(p.row_scale + m_lo + c + lane) : 1.f;
@@ -278,7 +287,7 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tmF, const __grid_consta
     }
 #pragma unroll
     for (int g = 0; g < 4; ++g)
-      if (4 * g < n_cols) fetch(g, 4 * g);
+      if (p.r && 4 * g < n_cols) fetch(g, 4 * g);
     next_factor = row_factor(0);
     ready = __all_sync(0xFFFFFFFFu, wait_phase<true>(done, 0u, w, kWaitEpilogue));
     tc_fence_after_sync();
@@ -347,7 +356,10 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tmF, const __grid_consta
         }
         v = activate4<AB_BYTES>(v, p.act);
         if (p.r) {
-          v.x += r[4 * g]; v.y += r[4 * g + 1]; v.z += r[4 * g + 2]; v.w += r[4 * g + 3];
+          v.x += residual(r[4 * g]);
+          v.y += residual(r[4 * g + 1]);
+          v.z += residual(r[4 * g + 2]);
+          v.w += residual(r[4 * g + 3]);
           if (c + 16 < n_cols) fetch(g, c + 16);
         }
         epi_store4(d_at, d_step, p.d_dt, count, v);

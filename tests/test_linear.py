@@ -8,6 +8,7 @@ activation of slope at most 1.13 carries an error of z on at 1.13 times its size
 and its own evaluation is off by at most 2^-21 of max(1, |z|): the exponential's
 2^-22 and the published 1.5e-7 of the distribution function.  Results are rounded
 once."""
+import ctypes
 import itertools
 
 import pytest
@@ -106,6 +107,16 @@ def _bwd(**kw):
 ])
 def test_check_linear_bwd(lib, kw, code):
     assert G.gemm_linear_bwd_check(_bwd(**kw)) == code
+
+
+def test_packed_calls_match_the_structures():
+    """The tensor calls pack the C structures by format: same size, every field in its place."""
+    for fmt, cls in ((G._LINEAR, G.gemm_linear_t), (G._LINEAR_BWD, G.gemm_linear_bwd_t),
+                     (G._RMSNORM, G.gemm_rmsnorm_t), (G._RMSNORM_BWD, G.gemm_rmsnorm_bwd_t)):
+        values = [float(i + 1) if t is ctypes.c_float else i + 1
+                  for i, (_, t) in enumerate(cls._fields_)]
+        assert fmt.size == ctypes.sizeof(cls)
+        assert fmt.pack(*values) == bytes(cls(*values)), cls
 
 
 def test_null_arguments(lib):
