@@ -101,6 +101,78 @@ __device__ __forceinline__ float activate_grad(float v) {
   return 1.f;
 }
 
+// Two elements at once: the packed fp32 operations of sm_100 and later (one issue
+// slot for two lanes' worth) carry the polynomial of the normal distribution and
+// the products; roundings are those of the single forms.
+struct Pair {
+  unsigned long long v;
+};
+__device__ __forceinline__ Pair pair(float lo, float hi) {
+  Pair r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpair(Pair p, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(p.v));
+}
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+  Pair r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
+  Pair r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ Pair add2(Pair a, Pair b) {
+  Pair r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ Pair both(float x) { return pair(x, x); }
+
+// normal_cdf_exp of two elements; a0, a1 as a.
+__device__ __forceinline__ void normal_cdf_exp2(float v0, float v1, Pair a, Pair& cdf, Pair& e) {
+  float x0, x1;
+  unpair(fma2(a, both(0.231641888f), both(1.f)), x0, x1);
+  const Pair t = pair(rcp_fast(x0), rcp_fast(x1));
+  unpair(mul2(mul2(a, a), both(-0.5f * kLog2e)), x0, x1);
+  const float e0 = exp2_fast(x0), e1 = exp2_fast(x1);
+  e = pair(e0, e1);
+  Pair p = fma2(both(0.5307027145f), t, both(-0.7265760135f));
+  p = fma2(p, t, both(0.7107068705f));
+  p = fma2(p, t, both(-0.142248368f));
+  p = fma2(p, t, both(0.127414796f));
+  unpair(fma2(mul2(p, t), pair(-e0, -e1), both(0.5f)), x0, x1);
+  cdf = add2(both(0.5f), pair(copysignf(x0, v0), copysignf(x1, v1)));
+}
+
+template <int ACT>
+__device__ __forceinline__ void activate2(float& v0, float& v1) {
+  if constexpr (ACT == ACT_GELU) {
+    Pair cdf, e;
+    normal_cdf_exp2(v0, v1, pair(min_abs(v0, 20.f), min_abs(v1, 20.f)), cdf, e);
+    unpair(mul2(pair(v0, v1), cdf), v0, v1);
+  } else {
+    v0 = activate<ACT>(v0);
+    v1 = activate<ACT>(v1);
+  }
+}
+
+// Derivatives at v0, v1.
+template <int ACT>
+__device__ __forceinline__ Pair activate_grad2(float v0, float v1) {
+  if constexpr (ACT == ACT_GELU) {
+    const float a0 = min_abs(v0, 20.f), a1 = min_abs(v1, 20.f);
+    Pair cdf, e;
+    normal_cdf_exp2(v0, v1, pair(a0, a1), cdf, e);
+    return fma2(mul2(pair(copysignf(a0, v0), copysignf(a1, v1)), both(0.3989422804f)), e, cdf);
+  } else {
+    return pair(activate_grad<ACT>(v0), activate_grad<ACT>(v1));
+  }
+}
+
 // f(integral constant) for the activation `act`, outside the element loops.
 template <int V>
 struct IntC { static constexpr int value = V; };

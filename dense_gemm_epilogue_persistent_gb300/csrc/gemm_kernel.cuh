@@ -1267,7 +1267,8 @@ persistent_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
           }
           with_activation(e.act, [&](auto a) {
 #pragma unroll
-            for (int i = 0; i < kEpiChunk; ++i) dv[i] = activate<decltype(a)::value>(dv[i]);
+            for (int i = 0; i < kEpiChunk; i += 2)
+              activate2<decltype(a)::value>(dv[i], dv[i + 1]);
           });
           if (e.read_c)
             smem_row_each(slot, e.c_dt, 0, lane, [&](int i, float c) { dv[i] += c; });

@@ -28,17 +28,18 @@ struct ActGradParams {
 };
 
 // dz = dd act'(z) and dbias = its column sums (of the values before dz is
-// rounded), DRAM-bound at 6 bytes an element.  A block owns 64 columns (8 lanes of one
-// vector each) and 1/R of the rows, R the cluster size: thread group g of 32
-// walks rows first + g, + 32, ..., four at a time so that their loads are in
-// flight together.  A column's sum is added in a fixed order: a thread's rows,
-// the 32 groups through shared memory, the cluster's blocks by its first one.
-template <int DT>
-__global__ void __launch_bounds__(256, 4)
+// rounded), 6 bytes and about 25 instructions an element.  A block owns 64
+// columns (8 lanes of one vector each) and 1/R of the rows, R the cluster size:
+// thread group g of G = THREADS / 8 walks rows first + g, + G, ..., a few at a
+// time so that their loads are in flight together.  A column's sum is added in
+// a fixed order: a thread's rows, the groups through shared memory, the
+// cluster's blocks by its first one.
+template <int DT, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS)
 act_grad_kernel(const __grid_constant__ ActGradParams p) {
-  __shared__ float part[32][64];
+  constexpr int G = THREADS / 8;
+  __shared__ float part[G][64];
   __shared__ float block_part[64];
-  constexpr int kUnroll = 4;
   constexpr int es = elem_bytes(DT);
   grid_launch_dependents();
   const int lane = threadIdx.x & 7, group = threadIdx.x >> 3;
@@ -56,11 +57,12 @@ act_grad_kernel(const __grid_constant__ ActGradParams p) {
     const uint8_t* const zz = static_cast<const uint8_t*>(p.z);
     with_activation(p.act, [&](auto a) {
       constexpr int ACT = decltype(a)::value;
-      for (long long row0 = first + group; row0 < last; row0 += 32 * kUnroll) {
+      constexpr int kUnroll = ACT == ACT_NONE ? 4 : 2;
+      for (long long row0 = first + group; row0 < last; row0 += G * kUnroll) {
         RawVec<DT> g_raw[kUnroll], z_raw[kUnroll];
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
-          const long long row = row0 + 32 * u;
+          const long long row = row0 + G * u;
           g_raw[u] = z_raw[u] = RawVec<DT>{};
           if (row < last) {
             g_raw[u] = load_raw<DT>(dd + row * p.lddd * es, c, p.N);
@@ -69,7 +71,7 @@ act_grad_kernel(const __grid_constant__ ActGradParams p) {
         }
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
-          const long long row = row0 + 32 * u;
+          const long long row = row0 + G * u;
           if (row >= last) break;
           float g[kVec];
           unpack<DT>(g_raw[u], g);
@@ -77,7 +79,9 @@ act_grad_kernel(const __grid_constant__ ActGradParams p) {
             float z[kVec];
             unpack<DT>(z_raw[u], z);
 #pragma unroll
-            for (int i = 0; i < kVec; ++i) g[i] *= activate_grad<ACT>(z[i]);
+            for (int i = 0; i < kVec; i += 2)
+              unpair(mul2(pair(g[i], g[i + 1]), activate_grad2<ACT>(z[i], z[i + 1])), g[i],
+                     g[i + 1]);
           }
           if (p.dz) store_vec(static_cast<uint8_t*>(p.dz) + row * p.lddz * es, DT, c, p.N, g);
 #pragma unroll
@@ -90,10 +94,15 @@ act_grad_kernel(const __grid_constant__ ActGradParams p) {
 #pragma unroll
   for (int i = 0; i < kVec; ++i) part[group][lane * kVec + i] = acc[i];
   __syncthreads();
-  if (threadIdx.x < 64) {
+  // 4 threads a column take a quarter of the groups each, added in lane order.
+  if (threadIdx.x < 256) {
+    const int col = threadIdx.x >> 2, quarter = threadIdx.x & 3;
     float s = 0.f;
-    for (int i = 0; i < 32; ++i) s += part[i][threadIdx.x];
-    block_part[threadIdx.x] = s;
+#pragma unroll 8
+    for (int i = quarter * (G / 4); i < (quarter + 1) * (G / 4); ++i) s += part[i][col];
+    s += __shfl_down_sync(0xFFFFFFFFu, s, 1);
+    s += __shfl_down_sync(0xFFFFFFFFu, s, 2);
+    if (quarter == 0) block_part[col] = s;
   }
   if (R > 1) cluster_sync_all(); else __syncthreads();
   const int col = strip * 64 + (int)threadIdx.x;
@@ -533,12 +542,28 @@ gemm_status_t run_linear(gemm_handle* h, const gemm_linear_t& p, struct CUstream
   return plan->split ? run_split(h, p, *plan, stream) : run_persistent(h, p, *plan, stream);
 }
 
-// Blocks per cluster of the activation gradient: enough for eight blocks an SM
-// (all that its registers hold), at least 128 rows a block.
-int act_grad_split(int64_t M, int64_t N, int sm_count) {
-  int r = 1;
-  while (r < 8 && cdiv(N, 64) * r < 8 * (int64_t)sm_count && M >= 256 * r) r *= 2;
-  return r;
+// Launch shape of the activation gradient: blocks per cluster for four blocks an
+// SM (all that its registers hold) where the rows allow, with 64 rows a block
+// at least.  Where even clusters of 8 leave SMs without a block (N up to 1216),
+// blocks of 1024 threads (8192 x 1024 gelu: 28 us with 256).
+struct ActGradShape {
+  int split, threads;
+};
+
+ActGradShape act_grad_shape(int64_t M, int64_t N, int sm_count) {
+  ActGradShape s{1, 256};
+  const int64_t strips = cdiv(N, 64);
+  while (s.split < 8 && strips * s.split < 8 * (int64_t)sm_count && M >= 128 * s.split) s.split *= 2;
+  if (strips * 8 <= sm_count && M >= 256 * s.split) s.threads = 1024;
+  return s;
+}
+
+template <int DT>
+gemm_status_t launch_act_grad(gemm_handle* h, gb300::ActGradParams& k, struct CUstream_st* stream) {
+  const ActGradShape s = act_grad_shape(k.M, k.N, h->sm_count);
+  k.row_split = s.split;
+  return launch(s.threads == 256 ? gb300::act_grad_kernel<DT, 256> : gb300::act_grad_kernel<DT, 1024>,
+                k, cdiv(k.N, 64) * s.split, s.threads, 0, stream, s.split);
 }
 
 // The backward pass's two products as linear calls.  da[M,K] = alpha dz[M,N] b[N,K]
@@ -644,10 +669,8 @@ GEMM_API gemm_status_t gemm_linear_bwd(gemm_handle_t h, const gemm_linear_bwd_t*
     k.dbias = p.dbias; k.dbias_dt = device_dt(p.dbias_type);
     k.M = (int)p.M; k.N = (int)p.N;
     k.act = p.activation;
-    k.row_split = act_grad_split(p.M, p.N, h->sm_count);
-    GB300_CHECK(launch(p.type == GEMM_F16 ? gb300::act_grad_kernel<gb300::DT_F16>
-                                          : gb300::act_grad_kernel<gb300::DT_BF16>,
-                       k, cdiv(p.N, 64) * k.row_split, 256, 0, stream, k.row_split));
+    GB300_CHECK(p.type == GEMM_F16 ? launch_act_grad<gb300::DT_F16>(h, k, stream)
+                                   : launch_act_grad<gb300::DT_BF16>(h, k, stream));
   }
   int64_t lddz = 0;
   const void* dz = dz_of(p, lddz);

@@ -87,7 +87,8 @@ template <int AB_BYTES>
 __device__ __noinline__ float4 activate4(float4 v, int act) {
   with_activation(act, [&](auto a) {
     constexpr int ACT = decltype(a)::value;
-    v = make_float4(activate<ACT>(v.x), activate<ACT>(v.y), activate<ACT>(v.z), activate<ACT>(v.w));
+    activate2<ACT>(v.x, v.y);
+    activate2<ACT>(v.z, v.w);
   });
   return v;
 }
