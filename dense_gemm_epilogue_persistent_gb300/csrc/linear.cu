@@ -431,9 +431,10 @@ gemm_status_t run_split(gemm_handle* h, const gemm_linear_t& p, const LinearPlan
   return GEMM_OK;
 }
 
-// Clusters of `split` CTAs of the split-K kernel the device holds at once (two
-// CTAs an SM, less what the cluster size leaves over in each GPC), asked for
-// once per size.
+// Clusters of `split` CTAs the device holds at one CTA an SM (what the cluster
+// size leaves over in each GPC taken off), asked for once per size.  (The
+// occupancy calculator counts one CTA an SM for this kernel; two are resident, as
+// start and end times of consecutive launches' blocks show.)
 int split_clusters(gemm_handle* h, int split) {
   int& n = h->split_clusters[split];
   if (n > 0) return n;
@@ -460,8 +461,10 @@ int split_clusters(gemm_handle* h, int split) {
 // The split-K kernel's tiles where the call chooses: all features of an MMA,
 // the tokens cut evenly into tiles of at most 128 (whole atoms where they are
 // MN-major), and as many CTAs a tile, with two k-blocks each, as leave every
-// tile's cluster resident (48 x 5000 x 4096 E4M3, 40 tiles: 8.8 us with 6, 9.7 with
-// 5; with 7 some clusters wait for others to end, 13.6).
+// tile's cluster resident, at 2.2 times the calculator's clusters (48 x 5000 x 4096
+// E4M3, 40 tiles: 8.8 us with 6, 9.8 with 5; with 7 some clusters wait for others to
+// end, 13.8; 1 x 8192 x 8192 bf16, 64 tiles: 21.1 with 4, 23.7 with 3; 1 x 4096 x 4096,
+// 32 tiles: 9.3 with 8, 9.8 with 6).
 bool choose_split(gemm_handle* h, const gemm_linear_t& p, SplitPlan* out) {
   const int es = dtype_bytes(p.a_type);
   const int64_t per_tile = cdiv(p.M, cdiv(p.M, 128));
@@ -471,7 +474,7 @@ bool choose_split(gemm_handle* h, const gemm_linear_t& p, SplitPlan* out) {
   const int64_t tiles = cdiv(p.M, bn) * cdiv(p.N, 128);
   if (tiles > 2 * (int64_t)h->sm_count) return false;
   int split = (int)std::max<int64_t>(1, std::min<int64_t>(8, cdiv(p.K, 128 / es) / 2));
-  while (split > 1 && tiles > split_clusters(h, split)) --split;
+  while (split > 1 && 10 * tiles > 22 * (int64_t)split_clusters(h, split)) --split;
   return plan_split(p, bn, 128, split, out);
 }
 
