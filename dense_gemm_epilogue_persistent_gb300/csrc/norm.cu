@@ -220,15 +220,12 @@ struct NormBwdParams {
 struct SumParams {
   const float* partials;
   void* out;
-  int rows, H, out_dt;
+  int rows, H, ld, out_dt;
 };
 
-// Partial sums [c, c + 8) of a row of H floats (rows of any alignment).
-__device__ __forceinline__ void store_partial(float* row, int c, int n, const float (&v)[kVec]) {
-#pragma unroll
-  for (int k = 0; k < kVec; ++k)
-    if (c + k < n) row[c + k] = v[k];
-}
+// Floats from one row of partial sums to the next: whole 16-byte pieces.
+__host__ __device__ constexpr int partial_ld(int H) { return (H + 3) & ~3; }
+
 
 // The backward kernel's blocks stay and walk rows first, first + walkers, ...;
 // every thread copies its own vectors of the next rows into its own slots of
@@ -408,12 +405,12 @@ rmsnorm_bwd_rows_kernel(const __grid_constant__ NormBwdParams p) {
     if (++s == D) s = 0;
   }
   copy_wait(0);
-  float* const out = p.partials + (long long)blockIdx.x * p.H;
+  float* const out = p.partials + (long long)blockIdx.x * partial_ld(p.H);
   if constexpr (!WARP) {
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int c = (i * T + t) * kVec;
-      if (c < p.H) store_partial(out, c, p.H, dw[i]);
+      if (c < p.H) store_vec(out, DT_F32, c, p.H, dw[i]);
     }
   } else {
     float* const warp_dw = reinterpret_cast<float*>(slots);
@@ -436,27 +433,32 @@ rmsnorm_bwd_rows_kernel(const __grid_constant__ NormBwdParams p) {
   }
 }
 
-// Column sums of `rows` rows of H partial sums: 32 columns a block, 32 row
-// groups, added in order.
+// Column sums of `rows` rows of partial sums, `ld` floats apart: a warp's lanes
+// take 4 columns each, a block's 32 warps rows w, w + 32, ..., added in that
+// order and then in warp order.
 __global__ void __launch_bounds__(1024)
 sum_partials_kernel(const __grid_constant__ SumParams p) {
-  __shared__ float part[32][33];
+  __shared__ float4 part[32][32];
   grid_launch_dependents();
   grid_dependency_wait();
   const int lane = threadIdx.x & 31, group = threadIdx.x >> 5;
-  const int c = blockIdx.x * 32 + lane;
-  float s = 0.f;
+  const int c = (blockIdx.x * 32 + lane) * 4;
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
   if (c < p.H) {
 #pragma unroll 10
-    for (int r = group; r < p.rows; r += 32) s += p.partials[(long long)r * p.H + c];
+    for (int r = group; r < p.rows; r += 32) {
+      const float4 v = *reinterpret_cast<const float4*>(p.partials + (long long)r * p.ld + c);
+      s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+    }
   }
   part[group][lane] = s;
   __syncthreads();
-  if (group == 0 && c < p.H) {
-    s = 0.f;
+  if (threadIdx.x < 128) {
+    const int col = blockIdx.x * 128 + (int)threadIdx.x;
+    float t = 0.f;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) s += part[i][lane];
-    store_elem(p.out, c, p.out_dt, s);
+    for (int i = 0; i < 32; ++i) t += reinterpret_cast<const float*>(part[i])[threadIdx.x];
+    if (col < p.H) store_elem(p.out, col, p.out_dt, t);
   }
 }
 
@@ -689,7 +691,7 @@ GEMM_API gemm_status_t gemm_rmsnorm(gemm_handle_t h, const gemm_rmsnorm_t* pp,
 
 GEMM_API int64_t gemm_rmsnorm_bwd_workspace(int64_t M, int64_t H) {
   if (M <= 0 || H <= 0 || H > kBwdRowMax) return 0;
-  return backward_blocks(M, H) * H * (int64_t)sizeof(float);
+  return backward_blocks(M, H) * (int64_t)gb300::partial_ld((int)H) * (int64_t)sizeof(float);
 }
 
 GEMM_API gemm_status_t gemm_rmsnorm_bwd(gemm_handle_t h, const gemm_rmsnorm_bwd_t* pp,
@@ -731,8 +733,8 @@ GEMM_API gemm_status_t gemm_rmsnorm_bwd(gemm_handle_t h, const gemm_rmsnorm_bwd_
                          dtype_bytes(p.type);
     const size_t sums = s.warp ? 8 * (size_t)p.H * sizeof(float) : 0;
     GB300_CHECK(launch(kern, k, blocks, s.threads, std::max(slots, sums), stream));
-    gb300::SumParams q{k.partials, p.dweight, blocks, (int)p.H, k.dw_dt};
-    return launch(gb300::sum_partials_kernel, q, cdiv(p.H, 32), 1024, 0, stream);
+    gb300::SumParams q{k.partials, p.dweight, blocks, k.H, gb300::partial_ld(k.H), k.dw_dt};
+    return launch(gb300::sum_partials_kernel, q, cdiv(p.H, 128), 1024, 0, stream);
   }
   NormBwdKern dx = p.type == GEMM_F32   ? gb300::rmsnorm_bwd_any_kernel<gb300::DT_F32>
             : p.type == GEMM_F16 ? gb300::rmsnorm_bwd_any_kernel<gb300::DT_F16>
