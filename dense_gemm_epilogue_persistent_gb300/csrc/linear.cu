@@ -368,7 +368,7 @@ gemm_config_t config_of(const SplitPlan& s, int es) {
   c.smem_bytes = s.smem;
   c.tiles = s.tiles_m * s.tiles_n;
   c.grid_ctas = (int)(c.tiles * s.split);
-  c.epi_warps = 1;
+  c.epi_warps = s.bn <= 16 ? 1 : 2;
   c.split_k = s.split;
   return c;
 }
@@ -412,7 +412,7 @@ gemm_status_t run_split(gemm_handle* h, const gemm_linear_t& p, const LinearPlan
   cudaLaunchConfig_t lc{};
   cudaLaunchAttribute attr[2];
   lc.gridDim = dim3((unsigned)(s.tiles_m * s.tiles_n * s.split));
-  lc.blockDim = dim3((unsigned)gb300::kSplitThreads);
+  lc.blockDim = dim3((unsigned)gb300::threads_for(plan.cfg.epi_warps));
   lc.dynamicSmemBytes = (size_t)s.smem;
   lc.stream = reinterpret_cast<cudaStream_t>(stream);
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -480,19 +480,19 @@ bool choose_split(gemm_handle* h, const gemm_linear_t& p, SplitPlan* out) {
 
 // Which kernel: estimated microseconds of both, linear fits to 200 problems on
 // GB300 (1 to 1024 tokens, 512 to 8192 features and inner sizes, bf16 and E4M3, every
-// layout).  Choosing by them costs 0.3 % over the faster kernel on average, 4 %
-// or more on 5 of them (19 % at worst).  For instance (split-K, persistent):
-// 1 x 4096 x 4096 bf16 9.4, 32.6 us; 64 x 4096 x 4096 12.1, 15.7; 128 x 4096 x 4096
-// 18.2, 15.8; 256 x 1024 x 8192 17.9, 22.5; 512 x 512 x 512 11.9, 5.9.
+// layout).  Choosing by them costs 0.1 % over the faster kernel on average and 5 %
+// at worst.  For instance (split-K, persistent): 1 x 4096 x 4096 bf16 9.4, 32.6 us;
+// 64 x 4096 x 4096 11.4, 15.6; 128 x 4096 x 4096 16.7, 15.7; 256 x 1024 x 8192 16.4,
+// 22.3; 512 x 512 x 512 8.1, 5.7.
 bool split_is_faster(const gemm_linear_t& p, const SplitPlan& s, double persistent_cost) {
   const int es = dtype_bytes(p.a_type);
   const double weights = (double)p.N * (double)p.K * es / 6.3e6;       // us at 6.3 TB/s
   const double tokens = (double)p.M * (double)p.K * es * (double)s.tiles_n / 6.3e6;
   const double k_blocks = (double)cdiv(p.K, 128 / es) / s.split;
   const double own = (double)cdiv(cdiv(s.bn, s.split), 4) * 4;
-  const double split_us = 2.8 + 0.139 * k_blocks + 0.145 * own +
-                          (s.split > 1 ? 0.041 * s.bn : 0.0) + 0.61 * weights + 0.49 * tokens;
-  const double persistent_us = 1.73 + 0.331 * persistent_cost + 0.514 * weights;
+  const double split_us = 3.41 + 0.141 * k_blocks + 0.0525 * own +
+                          (s.split > 1 ? 0.032 * s.bn : 0.0) + 0.592 * weights + 0.582 * tokens;
+  const double persistent_us = 1.59 + 0.333 * persistent_cost + 0.498 * weights;
   return split_us < persistent_us;
 }
 

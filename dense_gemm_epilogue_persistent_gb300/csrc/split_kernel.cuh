@@ -17,8 +17,10 @@
 // which adds them in rank order and runs the epilogue: one launch, no
 // workspace, the same bits every time.
 //
-// Block = 6 warps: TMA producer, tensor-memory allocator + MMA issuer, four
-// epilogue warps.  Every barrier wait is bounded as in gemm_kernel.cuh; the
+// Block = 6 or 10 warps: TMA producer, tensor-memory allocator + MMA issuer, and
+// one or two epilogue warps per lane quarter, which take its groups of columns in
+// turn (128 x 512 x 512 E4M3 7.9 us with two, 8.9 with one; 1 x 4096 x 4096 bf16 9.4
+// and 9.1: two from 17 tokens on).  Every barrier wait is bounded as in gemm_kernel.cuh; the
 // cluster barriers are reached by every thread on every path.
 #pragma once
 
@@ -56,7 +58,7 @@ struct SplitParams {
   int act;
 };
 
-constexpr int kSplitThreads = 192;
+constexpr int kSplitThreads = 320;           // at most: 192 with four epilogue warps
 constexpr int kSplitMaxStages = 12;
 
 // Shared memory behind the ring: full and empty barriers, the accumulator's,
@@ -68,16 +70,18 @@ __device__ __forceinline__ int epi_bytes(int dt) { return dt == DT_F32 ? 4 : 2; 
 // Elements of `count` (up to 4) rows `step` bytes apart.
 __device__ __forceinline__ void epi_store4(uint8_t* p, long long step, int dt, int count,
                                            const float4& v) {
-  const float e[4] = {v.x, v.y, v.z, v.w};
+  if (dt == DT_F32) {
+    const float e[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (i >= count) break;
-    uint8_t* const at = p + i * step;
-    if (dt == DT_F32) *reinterpret_cast<float*>(at) = e[i];
-    else
-      *reinterpret_cast<uint16_t*>(at) = dt == DT_F16
-                                             ? __half_as_ushort(__float2half_rn(e[i]))
-                                             : __bfloat16_as_ushort(__float2bfloat16_rn(e[i]));
+    for (int i = 0; i < 4; ++i)
+      if (i < count) *reinterpret_cast<float*>(p + i * step) = e[i];
+  } else {
+    const uint32_t w[2] = {dt == DT_F16 ? pack_f16x2(v.x, v.y) : pack_bf16x2(v.x, v.y),
+                           dt == DT_F16 ? pack_f16x2(v.z, v.w) : pack_bf16x2(v.z, v.w)};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < count)
+        *reinterpret_cast<uint16_t*>(p + i * step) = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
   }
 }
 
@@ -94,7 +98,7 @@ __device__ __noinline__ float4 activate4(float4 v, int act) {
 }
 
 template <int AB_BYTES>
-__global__ void __launch_bounds__(kSplitThreads, 1)
+__global__ void __launch_bounds__(kSplitThreads, 2)
 linear_split_kernel(const __grid_constant__ CUtensorMap tmF, const __grid_constant__ CUtensorMap tmT,
                     const __grid_constant__ SplitParams p) {
   constexpr int KIND = (AB_BYTES == 1) ? 1 : (AB_BYTES == 4 ? 2 : 0);
@@ -157,15 +161,15 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tmF, const __grid_consta
   const Watch w{abort_ptr, p.status, p.timeout_ns};
 
   // The epilogue warps' state: feature n of this thread, its scale and bias.
-  const int q = warp & 3;
+  const int q = warp & 3, turn = (warp - 2) >> 2, turns = ((int)blockDim.x - 64) >> 7;
   const int n = n0 + q * 32 + lane;
   const bool mine = n < p.N && q * 32 + lane < p.feats;
   float scale = p.alpha, bias = 0.f;
   bool ready = true;
   // The columns this CTA finishes: [c_lo, c_lo + n_cols) of the tile, those of
-  // its share that hold tokens, four at a time.  Residuals are fetched 16
-  // columns ahead (the first ones while the main loop runs); a lane holds one
-  // column's row factor of 32.
+  // its share that hold tokens, four at a time, every `turns`-th four this warp's.
+  // Residuals of its first four groups are fetched while the main loop runs,
+  // then four groups ahead; a lane holds one column's row factor of 32.
   const int with_tokens = min(p.bn, p.M - m0);
   const int c_lo = S > 1 ? (int)rank * p.own : 0;
   const int n_cols = max(0, min(S > 1 ? p.own : p.bn, with_tokens - c_lo));
@@ -288,7 +292,7 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tmF, const __grid_consta
     }
 #pragma unroll
     for (int g = 0; g < 4; ++g)
-      if (p.r && 4 * g < n_cols) fetch(g, 4 * g);
+      if (p.r && 4 * (g * turns + turn) < n_cols) fetch(g, 4 * (g * turns + turn));
     next_factor = row_factor(0);
     ready = __all_sync(0xFFFFFFFFu, wait_phase<true>(done, 0u, w, kWaitEpilogue));
     tc_fence_after_sync();
@@ -303,7 +307,12 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tmF, const __grid_consta
     cluster_sync_all();                          // every CTA's products are complete
     if (active) {
       int owner = 0, piece = 0;
-      for (int c = 0; c < with_tokens; c += 16) {
+      auto advance = [&](int n_pieces) {
+        piece += n_pieces;
+        while (piece >= pieces) { piece -= pieces; ++owner; }
+      };
+      advance(4 * turn);
+      for (int c = 16 * turn; c < with_tokens; c += 16 * turns) {
         uint32_t acc[16];
         __syncwarp();
         tmem_load_16cols(tbase + c, acc);
@@ -314,58 +323,61 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tmF, const __grid_consta
             store_cluster_v4(map_to_rank(base + (rank * pieces + piece) * 2048u + my_piece,
                                          (uint32_t)owner),
                              acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
-          if (++piece == pieces) { piece = 0; ++owner; }
+          advance(1);
         }
+        advance(4 * (turns - 1));
       }
     }
     cluster_sync_all();                          // every partial sum has arrived
   }
   if (active) {
+    // (not unrolled: the body runs once or a few times, from instruction lines
+    // nothing has fetched yet)
+    z_at += 4 * turn * z_step;
+    d_at += 4 * turn * d_step;
 #pragma unroll 1
-    for (int c0 = 0; c0 < n_cols; c0 += 16) {
-      if ((c0 & 31) == 0) {
+    for (int c = 4 * turn; c < n_cols; c += 4 * turns) {
+      if ((c & 31) < 4 * turns) {                        // (the warp's first group of 32)
         factor = next_factor;
-        next_factor = row_factor(c0 + 32);
+        next_factor = row_factor((c & ~31) + 32);
       }
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (S == 1) {
+        uint32_t acc[4];
+        __syncwarp();                            // (.aligned, after per-lane work)
+        tmem_load_4cols(tbase + c, acc);
+        tmem_wait_ld4(acc);
+        v = make_float4(__uint_as_float(acc[0]), __uint_as_float(acc[1]), __uint_as_float(acc[2]),
+                        __uint_as_float(acc[3]));
+      } else {
+        const uint8_t* at = gbase + c * 512 + my_piece;
+#pragma unroll 2
+        for (int src = 0; src < S; ++src, at += pieces * 2048) {
+          const float4 u = *reinterpret_cast<const float4*>(at);
+          v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
+        }
+      }
+      v.x = fmaf(v.x, scale * __shfl_sync(0xFFFFFFFFu, factor, c & 31), bias);
+      v.y = fmaf(v.y, scale * __shfl_sync(0xFFFFFFFFu, factor, (c + 1) & 31), bias);
+      v.z = fmaf(v.z, scale * __shfl_sync(0xFFFFFFFFu, factor, (c + 2) & 31), bias);
+      v.w = fmaf(v.w, scale * __shfl_sync(0xFFFFFFFFu, factor, (c + 3) & 31), bias);
+      const int count = mine ? n_cols - c : 0;
+      if (p.z) {
+        epi_store4(z_at, z_step, p.z_dt, count, v);
+        z_at += 4 * turns * z_step;
+      }
+      if (p.act != ACT_NONE) v = activate4<AB_BYTES>(v, p.act);
+      if (p.r) {
+        v.x += residual(r[0]);
+        v.y += residual(r[1]);
+        v.z += residual(r[2]);
+        v.w += residual(r[3]);
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const int c = c0 + 4 * g;
-        if (c >= n_cols) break;
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (S == 1) {
-          uint32_t acc[4];
-          __syncwarp();                          // (.aligned, after per-lane work)
-          tmem_load_4cols(tbase + c, acc);
-          tmem_wait_ld4(acc);
-          v = make_float4(__uint_as_float(acc[0]), __uint_as_float(acc[1]),
-                          __uint_as_float(acc[2]), __uint_as_float(acc[3]));
-        } else {
-          const uint8_t* at = gbase + c * 512 + my_piece;
-          for (int src = 0; src < S; ++src, at += pieces * 2048) {
-            const float4 u = *reinterpret_cast<const float4*>(at);
-            v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
-          }
-        }
-        v.x = fmaf(v.x, scale * __shfl_sync(0xFFFFFFFFu, factor, c & 31), bias);
-        v.y = fmaf(v.y, scale * __shfl_sync(0xFFFFFFFFu, factor, (c + 1) & 31), bias);
-        v.z = fmaf(v.z, scale * __shfl_sync(0xFFFFFFFFu, factor, (c + 2) & 31), bias);
-        v.w = fmaf(v.w, scale * __shfl_sync(0xFFFFFFFFu, factor, (c + 3) & 31), bias);
-        const int count = mine ? n_cols - c : 0;
-        if (p.z) {
-          epi_store4(z_at, z_step, p.z_dt, count, v);
-          z_at += 4 * z_step;
-        }
-        v = activate4<AB_BYTES>(v, p.act);
-        if (p.r) {
-          v.x += residual(r[4 * g]);
-          v.y += residual(r[4 * g + 1]);
-          v.z += residual(r[4 * g + 2]);
-          v.w += residual(r[4 * g + 3]);
-          if (c + 16 < n_cols) fetch(g, c + 16);
-        }
-        epi_store4(d_at, d_step, p.d_dt, count, v);
-        d_at += 4 * d_step;
+        for (int i = 0; i < 12; ++i) r[i] = r[i + 4];
+        if (c + 16 * turns < n_cols) fetch(3, c + 16 * turns);
       }
+      epi_store4(d_at, d_step, p.d_dt, count, v);
+      d_at += 4 * turns * d_step;
     }
   }
 
