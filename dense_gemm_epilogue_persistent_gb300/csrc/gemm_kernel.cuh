@@ -100,6 +100,12 @@ struct EpiParams {
   // A TMA store clips at whole 16-byte pieces, so where a row of D or Z ends
   // inside one, the chunk with the row's end is stored element by element.
   int d_ragged, y_ragged;
+  // Two launches that do not depend on each other, both after one that they do
+  // depend on: the first lets the second be scheduled only once its own
+  // dependency wait has returned (trigger_late), so the second need not wait
+  // before it touches memory; it waits at its end instead (wait_late), so that
+  // whatever follows it in the stream follows both.
+  int trigger_late, wait_late;
   void* d_ptr;
   void* y_ptr;
   long long ldd, ldy;
@@ -571,7 +577,8 @@ persistent_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
 
   // The next GEMM of the stream may start its prologue on SMs this grid leaves
   // idle; it touches global memory only after its own dependency wait below.
-  grid_launch_dependents();
+  const bool trigger_late = EPI == 1 && p.epi.trigger_late, wait_late = EPI == 1 && p.epi.wait_late;
+  if (!trigger_late) grid_launch_dependents();
 
   extern __shared__ uint8_t smem_raw[];
   // 1024-byte alignment for the swizzle atoms (identical in both CTAs of a pair:
@@ -669,7 +676,8 @@ persistent_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
   // Everything above touched only this CTA's shared and tensor memory and the
   // kernel parameters.  From here on global memory is read and written: wait
   // for the previous grid of the stream (programmatic dependent launch).
-  grid_dependency_wait();
+  if (!wait_late) grid_dependency_wait();
+  if (trigger_late) grid_launch_dependents();
 
   const Watch w{abort_ptr, p.status, p.timeout_ns};
 
@@ -1424,6 +1432,7 @@ persistent_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
     tc_fence_after_sync();
     tmem_dealloc<CG>(tmem_base, kTmemCols);
   }
+  if (wait_late) grid_dependency_wait();
 }
 
 }  // namespace gb300

@@ -226,9 +226,12 @@ gemm_status_t plan_persistent(gemm_handle* h, const gemm_linear_t& p, LinearPlan
   return GEMM_OK;
 }
 
+// A launch's place beside another that it does not depend on (EpiParams).
+enum Place { kAlone, kFirstOfTwo, kSecondOfTwo };
+
 // Enqueue a call on the persistent kernel by its plan.
 gemm_status_t run_persistent(gemm_handle* h, const gemm_linear_t& p, const LinearPlan& plan,
-                             struct CUstream_st* stream) {
+                             Place place, struct CUstream_st* stream) {
   const gemm_config_t& cfg = plan.cfg;
   CUtensorMap maps[6];                 // A, B, C, X, D, Y
   std::memset(maps, 0, sizeof(maps));
@@ -282,6 +285,8 @@ gemm_status_t run_persistent(gemm_handle* h, const gemm_linear_t& p, const Linea
   kp.epi.bias = p.bias;
   kp.epi.bias_dt = p.bias_type;
   kp.epi.act = p.activation;
+  kp.epi.trigger_late = place == kFirstOfTwo;
+  kp.epi.wait_late = place == kSecondOfTwo;
   kp.epi.d_ptr = p.D; kp.epi.ldd = p.ldd;
   kp.epi.d_ragged = (p.N * dtype_bytes(p.d_type)) % 16 != 0;
   if (p.Z) {
@@ -374,7 +379,7 @@ gemm_config_t config_of(const SplitPlan& s, int es) {
 }
 
 gemm_status_t run_split(gemm_handle* h, const gemm_linear_t& p, const LinearPlan& plan,
-                        struct CUstream_st* stream) {
+                        Place place, struct CUstream_st* stream) {
   const SplitPlan& s = plan.s;
   const int es = dtype_bytes(p.a_type);
   const bool a_mn = p.layoutA == GEMM_MN_MAJOR, b_mn = p.layoutB == GEMM_MN_MAJOR;
@@ -409,6 +414,8 @@ gemm_status_t run_split(gemm_handle* h, const gemm_linear_t& p, const LinearPlan
   k.d = p.D; k.ldd = p.ldd; k.d_dt = p.d_type;
   k.act = p.activation;
   k.inject_stall = plan.cfg.inject_stall;
+  k.trigger_late = place == kFirstOfTwo;
+  k.wait_late = place == kSecondOfTwo;
   cudaLaunchConfig_t lc{};
   cudaLaunchAttribute attr[2];
   lc.gridDim = dim3((unsigned)(s.tiles_m * s.tiles_n * s.split));
@@ -518,7 +525,8 @@ gemm_status_t plan_linear(gemm_handle* h, const gemm_linear_t& p, LinearPlan& ou
   return GEMM_OK;
 }
 
-gemm_status_t run_linear(gemm_handle* h, const gemm_linear_t& p, struct CUstream_st* stream) {
+gemm_status_t run_linear(gemm_handle* h, const gemm_linear_t& p, struct CUstream_st* stream,
+                         Place place = kAlone) {
   if (p.M == 0 || p.N == 0) return GEMM_OK;
   LinearKey key;
   std::memset(&key, 0, sizeof(key));           // padding included: keys compare bytewise
@@ -542,13 +550,16 @@ gemm_status_t run_linear(gemm_handle* h, const gemm_linear_t& p, struct CUstream
     h->linear_next = (h->linear_next + 1) % kLinearPlans;
   }
   h->last = plan->cfg;
-  return plan->split ? run_split(h, p, *plan, stream) : run_persistent(h, p, *plan, stream);
+  return plan->split ? run_split(h, p, *plan, place, stream)
+                     : run_persistent(h, p, *plan, place, stream);
 }
 
 // Launch shape of the activation gradient: blocks per cluster for four blocks an
 // SM (all that its registers hold) where the rows allow, with 64 rows a block
 // at least.  Where even clusters of 8 leave SMs without a block (N up to 1216),
-// blocks of 1024 threads (8192 x 1024 gelu: 28 us with 256).
+// larger blocks: 512 threads, or 1024 while every cluster of those is resident
+// (the device holds 15 of 8 such blocks; 16 of them, 8192 x 1024, run as two waves:
+// gelu 28 us with 256 threads, 30.6 with 1024).
 struct ActGradShape {
   int split, threads;
 };
@@ -557,7 +568,7 @@ ActGradShape act_grad_shape(int64_t M, int64_t N, int sm_count) {
   ActGradShape s{1, 256};
   const int64_t strips = cdiv(N, 64);
   while (s.split < 8 && strips * s.split < 8 * (int64_t)sm_count && M >= 128 * s.split) s.split *= 2;
-  if (strips * 8 <= sm_count && M >= 256 * s.split) s.threads = 1024;
+  if (strips * 8 <= sm_count && M >= 256 * s.split) s.threads = strips <= 12 ? 1024 : 512;
   return s;
 }
 
@@ -565,7 +576,9 @@ template <int DT>
 gemm_status_t launch_act_grad(gemm_handle* h, gb300::ActGradParams& k, struct CUstream_st* stream) {
   const ActGradShape s = act_grad_shape(k.M, k.N, h->sm_count);
   k.row_split = s.split;
-  return launch(s.threads == 256 ? gb300::act_grad_kernel<DT, 256> : gb300::act_grad_kernel<DT, 1024>,
+  return launch(s.threads == 256   ? gb300::act_grad_kernel<DT, 256>
+                : s.threads == 512 ? gb300::act_grad_kernel<DT, 512>
+                                   : gb300::act_grad_kernel<DT, 1024>,
                 k, cdiv(k.N, 64) * s.split, s.threads, 0, stream, s.split);
 }
 
@@ -677,7 +690,12 @@ GEMM_API gemm_status_t gemm_linear_bwd(gemm_handle_t h, const gemm_linear_bwd_t*
   }
   int64_t lddz = 0;
   const void* dz = dz_of(p, lddz);
-  if (p.da) GB300_CHECK(run_linear(h, product_da(p, dz, lddz), stream));
-  if (p.db) GB300_CHECK(run_linear(h, product_db(p, dz, lddz), stream));
+  // (both empty or both launched where both are asked for: an empty product
+  // launches nothing)
+  const bool two = p.da && p.db && p.M > 0 && p.N > 0 && p.K > 0;
+  if (p.da)
+    GB300_CHECK(run_linear(h, product_da(p, dz, lddz), stream, two ? kFirstOfTwo : kAlone));
+  if (p.db)
+    GB300_CHECK(run_linear(h, product_db(p, dz, lddz), stream, two ? kSecondOfTwo : kAlone));
   return GEMM_OK;
 }

@@ -44,6 +44,7 @@ struct SplitParams {
   uint32_t idesc;
   uint32_t tmem_cols;        // power of two >= bn
   int inject_stall;          // test only, as in KernelParams
+  int trigger_late, wait_late;   // as in EpiParams
   uint32_t* status;
   unsigned long long timeout_ns;
   float alpha;
@@ -107,7 +108,7 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tmF, const __grid_consta
   constexpr int ATOM_MN = 128 / AB_BYTES;        // rows of one MN-major atom
   constexpr uint32_t ATOM_BYTES = BK * 128;      // bytes of one MN-major atom column
 
-  grid_launch_dependents();
+  if (!p.trigger_late) grid_launch_dependents();
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;  // the same in every CTA of the cluster
@@ -157,7 +158,8 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tmF, const __grid_consta
     for (int a = 0; a < n_pre; ++a) tma_prefetch_3d(&tmF, (kb0 + a) * BK, n0, 0);
   }
   __syncwarp();
-  grid_dependency_wait();
+  if (!p.wait_late) grid_dependency_wait();
+  if (p.trigger_late) grid_launch_dependents();
   const Watch w{abort_ptr, p.status, p.timeout_ns};
 
   // The epilogue warps' state: feature n of this thread, its scale and bias.
@@ -394,6 +396,7 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tmF, const __grid_consta
     tc_fence_after_sync();
     tmem_dealloc<1>(tmem, p.tmem_cols);
   }
+  if (p.wait_late) grid_dependency_wait();
 }
 
 }  // namespace gb300

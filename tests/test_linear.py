@@ -476,6 +476,13 @@ def test_backward_sizes(gemm, M, N, K, t):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("M,N", [(2100, 1003), (2100, 700), (2300, 200), (4000, 1216), (600, 1217)])
+def test_backward_narrow_layers(gemm, M, N):
+    """Few columns and many rows: the activation gradient's larger blocks, alone."""
+    _check_backward(gemm, M, N, 8, "bf16", "gelu", give=("dz", "dbias"))
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("act", ACTS)
 def test_backward_activations(gemm, act):
     _check_backward(gemm, 200, 264, 136, "f16", act, da_t="f32", db_t="f32", alpha=0.5)
