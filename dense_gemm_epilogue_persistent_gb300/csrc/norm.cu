@@ -518,13 +518,16 @@ struct RowShape {
   bool warp;
 };
 
-// Four vectors a thread once there are rows enough to fill the GPU with such
-// blocks: fewer threads a row leave more rows in flight, and DRAM busier
-// (8192 x 8192 bf16 -> E4M3 with residual: 73.9 us at 4, 94.1 at 2, 118 at 1;
-// 32768 x 2048: 71.6, 77.1, 94.0; 608 x 8192: 9.0, 10.5, 11.7).  Below that the
-// row's own latency counts, which more threads shorten (304 x 4096: 3.9 us at 4, 3.3
-// at 1; 1 x 8192: 3.7 at 4, 3.1 at 2, 3.3 at 1).
-RowShape forward_shape(int64_t M, int64_t H) {
+// One, two or four vectors a thread, by an estimate of each: up to two waves of
+// blocks, waves x (1.5 us + the bytes of a full wave's rows), beyond that all bytes at
+// the rate each reaches (90, 80, 60 % of 6.8 TB/s).  Fewer threads a row leave more
+// rows in flight, and DRAM busier (8192 x 8192 bf16 -> E4M3 with residual: 73.9 us at
+// 4 vectors, 94.1 at 2, 118 at 1); more threads a row shorten it where its latency or
+// a last wave counts (1000 x 5003: 11.2 us at 2, 13.0 at 4; 600 x 2048: 3.4 at 1, 4.7 at
+// 4), up to 768 of them, where their joining costs more again (1 x 8192: 3.09 us at 2,
+// 3.33 at 1, 3.73 at 4).  Over 178 sizes (1 to 7000 rows of 1536 to 12000) the choice is
+// 1.1 % over the fastest on average, 12 % at worst.
+RowShape forward_shape(int64_t M, int64_t H, int64_t row_bytes, int sm_count) {
   const int vecs = (int)cdiv(H, gb300::kVec);
   RowShape s{};
   s.warp = vecs <= 128;
@@ -533,8 +536,24 @@ RowShape forward_shape(int64_t M, int64_t H) {
     s.threads = 128;
     return s;
   }
-  s.vpt = M >= 500 || vecs > 2048 ? 4 : vecs > 512 ? 2 : 1;
-  s.threads = (int)cdiv(cdiv(vecs, s.vpt), 32) * 32;
+  double best = 0.0;
+  for (int v : {1, 2, 4}) {
+    const int threads = (int)cdiv(cdiv(vecs, v), 32) * 32;
+    if (threads > 768 && v < 4) continue;
+    const int regs = v == 4 ? 64 : v == 2 ? 48 : 32;     // as compiled, in allocation steps
+    const int64_t slots =
+        (int64_t)sm_count * std::max(1, std::min(2048 / threads, 65536 / (regs * threads)));
+    const int64_t waves = cdiv(M, slots);
+    const double rate = v == 4 ? 0.9 : v == 2 ? 0.8 : 0.6;
+    const double us =
+        waves <= 2 ? (double)waves * (1.5 + (double)(std::min(M, slots) * row_bytes) / 6.8e6)
+                   : 1.5 + (double)M * (double)row_bytes / (6.8e6 * rate);
+    if (s.vpt == 0 || us < best) {
+      best = us;
+      s.vpt = v;
+      s.threads = threads;
+    }
+  }
   return s;
 }
 
@@ -677,7 +696,9 @@ GEMM_API gemm_status_t gemm_rmsnorm(gemm_handle_t h, const gemm_rmsnorm_t* pp,
   k.eps = p.eps;
   k.inv_h = (float)(1.0 / (double)p.H);
   if (p.H <= kRowMax) {
-    const RowShape s = forward_shape(p.M, p.H);
+    const int64_t row_bytes = p.H * (dtype_bytes(p.type) * (1 + (p.r != nullptr) + (p.h != nullptr)) +
+                                     dtype_bytes(p.y_type));
+    const RowShape s = forward_shape(p.M, p.H, row_bytes, h->sm_count);
     return launch(p.type == GEMM_F32   ? forward_kernel<gb300::DT_F32>(s)
                   : p.type == GEMM_F16 ? forward_kernel<gb300::DT_F16>(s)
                                        : forward_kernel<gb300::DT_BF16>(s),
