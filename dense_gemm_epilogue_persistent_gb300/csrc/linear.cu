@@ -242,9 +242,16 @@ gemm_status_t run_persistent(gemm_handle* h, const gemm_linear_t& p, const Linea
        !encode_operand(h->encode, &maps[1], p.B, p.b_type, p.N, p.K, 1, p.ldb, b_mn,
                        cfg.tile_n / cfg.cta_group, cfg.tile_k)))
     return GEMM_ERR_CUDA;
+  // D and Z as far as their rows' whole 16-byte pieces (a row without one is
+  // not stored through its map).
+  const auto stored = [&](gemm_dtype_t t) {
+    const int64_t piece = 16 / dtype_bytes(t);
+    return p.N < piece ? p.N : p.N - p.N % piece;
+  };
   if ((p.R && !encode_epi(h->encode, &maps[2], p.R, p.r_type, p.M, p.N, 1, false, p.ldr)) ||
-      !encode_epi(h->encode, &maps[4], p.D, p.d_type, p.M, p.N, 1, false, p.ldd) ||
-      (p.Z && !encode_epi(h->encode, &maps[5], p.Z, p.z_type, p.M, p.N, 1, false, p.ldz)))
+      !encode_epi(h->encode, &maps[4], p.D, p.d_type, p.M, stored(p.d_type), 1, false, p.ldd) ||
+      (p.Z &&
+       !encode_epi(h->encode, &maps[5], p.Z, p.z_type, p.M, stored(p.z_type), 1, false, p.ldz)))
     return GEMM_ERR_CUDA;
 
   KernelParams kp{};
