@@ -66,8 +66,9 @@ SHARED_UNITS = [(f"kern_shared_ab{ab}_m{mc}_n{nc}", "kern_shared.cu",
 # The operators around the product: normalisation, the linear layer and its kernels.
 ROW_UNITS = [("norm", "norm.cu", []), ("linear", "linear.cu", []),
              ("kern_split", "kern_split.cu", [])]
-LINEAR_UNITS = [(f"kern_linear_ab{ab}_e{epw}", "kern_linear.cu",
-                 [f"-DGB300_AB={ab}", f"-DGB300_EPW={epw}"]) for ab in (2, 1, 4) for epw in (1, 2)]
+LINEAR_UNITS = [(f"kern_linear_ab{ab}_e{epw}_p{epi}", "kern_linear.cu",
+                 [f"-DGB300_AB={ab}", f"-DGB300_EPW={epw}", f"-DGB300_EPI={epi}"])
+                for ab, epi in ((2, 1), (1, 1), (4, 1), (2, 2)) for epw in (1, 2)]
 # Files the multi-GPU library is built from (its translation units and every
 # header they include): none of them names a multicast TMA load.
 NOMC_FILES = ["gemm_api.cu", "norm.cu", "linear.cu", "kern_plain.cu", "kern_linear.cu",

@@ -146,6 +146,20 @@ struct KernelParams {
   EpiParams epi;
 };
 
+// Two products in one launch (EPI = 2; no column vectors, activation or
+// pre-activation): items below first_items are the first's, whose parameters
+// these are, the rest the second's.  num_items counts both; the tile, the ring
+// and the slots are common.  The first's items are dealt to the clusters in
+// turn; of the second's, lead_items go to the clusters from lead_from on, which
+// got one of the first's less, and the rest again to all in turn.
+struct PairParams : KernelParams {
+  KernelParams second;
+  int first_items, lead_items, lead_from;
+  CUtensorMap a2, b2, c2, d2;
+};
+template <int EPI> struct ParamsOf { using type = KernelParams; };
+template <> struct ParamsOf<2> { using type = PairParams; };
+
 // Ring statistics: a separate build of the library (GB300_RING_STATS=1) in
 // which each CTA's producer, MMA issuer and epilogue store thread count the
 // clock cycles they spend waiting on each barrier and in their loops, so the
@@ -578,7 +592,8 @@ __device__ __forceinline__ uint32_t sub_bytes(int dt) {
 
 // ------------------------------------------------------------------ the kernel
 
-// EPI = 0: the GEMM's epilogue; 1: the linear layer's (EpiParams).
+// EPI = 0: the GEMM's epilogue; 1: the linear layer's (EpiParams); 2: the same
+// for two products (PairParams).
 template <int CG, int AB_BYTES, int KA, int MC, int NC, int EPW, int SK, int EPI = 0>
 __global__ void __launch_bounds__(threads_for(EPW), 1)
 persistent_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
@@ -587,7 +602,7 @@ persistent_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
                        const __grid_constant__ CUtensorMap tmX,
                        const __grid_constant__ CUtensorMap tmD,
                        const __grid_constant__ CUtensorMap tmY,
-                       const __grid_constant__ KernelParams p) {
+                       const __grid_constant__ typename ParamsOf<EPI>::type p) {
   using G = Geometry<CG, AB_BYTES, KA, MC, NC>;
   constexpr int KIND = (AB_BYTES == 1) ? 1 : (AB_BYTES == 4 ? 2 : 0);
   constexpr bool MULTI = G::CLUSTER > 1;
@@ -603,12 +618,28 @@ persistent_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
   // Stream-K items (a separate instantiation, so that the other kernels carry
   // none of its code).
   constexpr bool kSK = SK != 0;
+  constexpr bool kLinear = EPI != 0, kPair = EPI == 2;
   // The linear layer's kernels issue by whole warps (see the producer).
-  constexpr bool kWarpIssue = EPI == 1;
+  constexpr bool kWarpIssue = kLinear;
+  // The product that item `it` is of, and its number there.
+  const auto is_second = [&](int it) {
+    if constexpr (kPair) return it >= p.first_items;
+    else return false;
+  };
+  const auto product = [&](int it) -> const KernelParams& {
+    if constexpr (kPair) {
+      if (it >= p.first_items) return p.second;
+    }
+    return p;
+  };
+  const auto number = [&](int it) {
+    if constexpr (kPair) return it >= p.first_items ? it - p.first_items : it;
+    else return it;
+  };
 
   // The next GEMM of the stream may start its prologue on SMs this grid leaves
   // idle; it touches global memory only after its own dependency wait below.
-  const bool trigger_late = EPI == 1 && p.epi.trigger_late, wait_late = EPI == 1 && p.epi.wait_late;
+  const bool trigger_late = kLinear && p.epi.trigger_late, wait_late = kLinear && p.epi.wait_late;
   if (!trigger_late) grid_launch_dependents();
 
   extern __shared__ uint8_t smem_raw[];
@@ -628,6 +659,32 @@ persistent_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
   const uint32_t pair_leader = grp * CG;          // cluster rank of the pair's leader
   const int cluster_id = blockIdx.x / G::CLUSTER;
   const int num_clusters = gridDim.x / G::CLUSTER;
+  // The cluster's sequence of items.
+  const auto second_item = [&]() {
+    if constexpr (kPair) {
+      const int lead = p.first_items + p.lead_items;
+      return p.lead_items > 0 && cluster_id >= p.lead_from
+                 ? p.first_items + cluster_id - p.lead_from : lead + cluster_id;
+    } else {
+      return 0;
+    }
+  };
+  const auto next_item = [&](int it) {
+    if constexpr (kPair) {
+      const int lead = p.first_items + p.lead_items;
+      if (it < p.first_items)
+        return it + num_clusters < p.first_items ? it + num_clusters : second_item();
+      if (it < lead) {
+        const int next = it + num_clusters - p.lead_from;
+        return next < lead ? next : lead + cluster_id;
+      }
+    }
+    return it + num_clusters;
+  };
+  int first_item = cluster_id;
+  if constexpr (kPair) {
+    if (cluster_id >= p.first_items) first_item = second_item();
+  }
   // CTAs receiving this CTA's B part: the same peer position in every group of
   // its cluster column; its A part: the same position in every group of its row.
   uint16_t b_mask = 0, a_mask = 0;
@@ -694,6 +751,11 @@ persistent_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
     if (p.epi.write_y) prefetch_tensormap(&tmY);
     if (p.epi.read_c) prefetch_tensormap(&tmC);
     if (p.epi.read_x) prefetch_tensormap(&tmX);
+    if constexpr (kPair) {
+      prefetch_tensormap(&p.a2);
+      prefetch_tensormap(&p.b2);
+      prefetch_tensormap(&p.d2);
+    }
   }
   if (warp == 1) {
     tmem_alloc<CG>(holder, kTmemCols);
@@ -725,12 +787,18 @@ persistent_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
       bool ok = true;
       long long st_empty = 0;
       const long long st_t0 = stat_clock();
-      for (int it = cluster_id; ok && it < p.num_items; it += num_clusters) {
-        const Work wk = work_item<kSK>(it, p, num_clusters);
+      for (int it = first_item; ok && it < p.num_items; it = next_item(it)) {
+        const KernelParams& P = product(it);
+        const CUtensorMap* map_a = &tmA;
+        const CUtensorMap* map_b = &tmB;
+        if constexpr (kPair) {
+          if (is_second(it)) { map_a = &p.a2; map_b = &p.b2; }
+        }
+        const Work wk = work_item<kSK>(number(it), P, num_clusters);
         if (wk.empty) continue;
         const int half = wk.half;
         int tm, tn, tl;
-        tile_coords(wk.tile, p, tm, tn, tl);
+        tile_coords(wk.tile, P, tm, tn, tl);
         // A half-width item covers columns [half * BN/2, +BN/2) of its tile: its
         // CTAs load full B boxes from that origin and the MMA reads their first
         // half.  m0: this CTA's 128 A rows; n0: the first of its B rows, plus
@@ -754,7 +822,7 @@ persistent_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
           if (!kWarpIssue || elect_one()) {
           if (rank == 0) mbar_arrive_expect_tx(fb, tx_bytes);
           const uint32_t fb_target = (CG == 2) ? map_to_rank(fb, pair_leader) : fb;
-          const int k0 = (k_down ? p.k_blocks - 1 - kb : kb) * G::BK;
+          const int k0 = (k_down ? P.k_blocks - 1 - kb : kb) * G::BK;
           const uint32_t sa = a_ring + s * G::A_STAGE;
           const uint32_t sb = b_ring + s * T.b_stage;
           // (debug build: the box's bytes inside this stage, the inner
@@ -763,15 +831,15 @@ persistent_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
             if (!dbg_check(in_range(dst, bytes, sa, sa + G::A_STAGE) &&
                                ((long long)c0 * AB_BYTES) % 16 == 0 && c1 >= 0,
                            kChkLoadA, w)) { ok = false; return; }
-            OperandLoad<CG, (NC > 1)>::load(dst, &tmA, fb_target, c0, c1, tl, a_mask, pol);
+            OperandLoad<CG, (NC > 1)>::load(dst, map_a, fb_target, c0, c1, tl, a_mask, pol);
           };
           auto issue_b = [&](uint32_t dst, int c0, int c1, uint32_t bytes) {
             if (!dbg_check(in_range(dst, bytes, sb, sb + (uint32_t)T.b_stage) &&
                                ((long long)c0 * AB_BYTES) % 16 == 0 && c1 >= 0,
                            kChkLoadB, w)) { ok = false; return; }
-            OperandLoad<CG, (MC > 1)>::load(dst, &tmB, fb_target, c0, c1, tl, b_mask, pol);
+            OperandLoad<CG, (MC > 1)>::load(dst, map_b, fb_target, c0, c1, tl, b_mask, pol);
           };
-          if (!p.a_mn_major) {
+          if (!P.a_mn_major) {
             // boxes {ATOM_K, A_PART}: this CTA's part of its cluster row's A rows
 #pragma unroll
             for (int a = 0; a < KA; ++a)
@@ -786,7 +854,7 @@ persistent_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
               issue_a(sa + aj * G::ATOM_BYTES, m0 + aj * G::ATOM_MN, k0, G::ATOM_BYTES);
             }
           }
-          if (!p.b_mn_major) {
+          if (!P.b_mn_major) {
             // boxes {ATOM_K, bn_part}
 #pragma unroll
             for (int a = 0; a < KA; ++a)
@@ -821,28 +889,29 @@ persistent_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
       // lane.  The descriptors' constant parts are built once (their address
       // field counts 16-byte units); a stage and a K step only add to them.
       if (rank == 0) {
-        const uint64_t a0 = p.a_mn_major ? smem_desc_sw128(a_ring, G::ATOM_BYTES, 1024)
-                                         : smem_desc_sw128(a_ring, 16, 1024);
-        const uint64_t b0 = p.b_mn_major ? smem_desc_sw128(b_ring, G::ATOM_BYTES, 1024)
-                                         : smem_desc_sw128(b_ring, 16, 1024);
-        // 16-byte units from one K step to the next, and from one K-major atom
-        // of 4 steps to the next
-        const uint32_t a_step = (p.a_mn_major ? G::UMMA_K * 128 : 32) / 16;
-        const uint32_t b_step = (p.b_mn_major ? G::UMMA_K * 128 : 32) / 16;
-        const uint32_t a_atom =
-            p.a_mn_major ? G::STEPS_PER_ATOM * a_step : (uint32_t)G::A_ATOM / 16;
-        const uint32_t b_atom = p.b_mn_major ? G::STEPS_PER_ATOM * b_step : (uint32_t)T.b_atom / 16;
         int s = 0, acc = 0;
         uint32_t ph = 0, aph = 0;
         bool ok = !p.inject_stall ||
                   __all_sync(0xFFFFFFFFu, wait_phase(never_bar, 0u, w, kWaitInjected));
-        for (int it = cluster_id; ok && it < p.num_items; it += num_clusters) {
-          const Work wk = work_item<kSK>(it, p, num_clusters);
+        for (int it = first_item; ok && it < p.num_items; it = next_item(it)) {
+          const KernelParams& P = product(it);
+          const Work wk = work_item<kSK>(number(it), P, num_clusters);
+          const uint64_t a0 = P.a_mn_major ? smem_desc_sw128(a_ring, G::ATOM_BYTES, 1024)
+                                           : smem_desc_sw128(a_ring, 16, 1024);
+          const uint64_t b0 = P.b_mn_major ? smem_desc_sw128(b_ring, G::ATOM_BYTES, 1024)
+                                           : smem_desc_sw128(b_ring, 16, 1024);
+          // 16-byte units from one K step to the next, and from one K-major atom
+          // of 4 steps to the next
+          const uint32_t a_step = (P.a_mn_major ? G::UMMA_K * 128 : 32) / 16;
+          const uint32_t b_step = (P.b_mn_major ? G::UMMA_K * 128 : 32) / 16;
+          const uint32_t a_atom =
+              P.a_mn_major ? G::STEPS_PER_ATOM * a_step : (uint32_t)G::A_ATOM / 16;
+          const uint32_t b_atom = P.b_mn_major ? G::STEPS_PER_ATOM * b_step : (uint32_t)T.b_atom / 16;
           if (!__all_sync(0xFFFFFFFFu, wait_phase(tempty0 + 8u * acc, aph ^ 1u, w, kWaitMmaAcc)))
             break;
           tc_fence_after_sync();
           const uint32_t d_tmem = tmem_base + (uint32_t)acc * kAccStride;
-          const uint32_t idesc = wk.half < 0 ? p.idesc : p.idesc_half;
+          const uint32_t idesc = wk.half < 0 ? P.idesc : P.idesc_half;
           for (int kb = wk.kb0; kb < wk.kb1; ++kb) {
             ok = __all_sync(0xFFFFFFFFu, wait_phase(full0 + 8u * s, ph, w, kWaitMmaFull));
             if (!ok) break;
@@ -874,7 +943,7 @@ persistent_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
       long long st_full = 0, st_acc = 0, st_stages = 0;
       const long long st_t0 = stat_clock();
       bool ok = !p.inject_stall || wait_phase(never_bar, 0u, w, kWaitInjected);
-      for (int it = cluster_id; ok && it < p.num_items; it += num_clusters) {
+      for (int it = first_item; ok && it < p.num_items; it = next_item(it)) {
         const Work wk = work_item<kSK>(it, p, num_clusters);
         if (wk.empty) continue;
         const long long t_a = stat_clock();
@@ -961,8 +1030,12 @@ persistent_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
     const int ew = warp - 2;                // epilogue warp index, 0 .. 4 * EPW - 1
     const int strm = ew >> 2;               // which of the quarter's EPW chunk streams
     const bool lead = lane == 0;
-    const bool loads = e.read_c || e.read_x;
-    const uint32_t load_tx = (e.read_c ? sub_bytes(e.c_dt) : 0u) + (e.read_x ? sub_bytes(e.x_dt) : 0u);
+    bool loads = e.read_c || e.read_x;
+    if constexpr (kPair) loads = loads || p.second.epi.read_c;
+    const auto load_bytes = [](const EpiParams& t) {
+      return (t.read_c ? sub_bytes(t.c_dt) : 0u) + (t.read_x ? sub_bytes(t.x_dt) : 0u);
+    };
+    const uint32_t load_tx = load_bytes(e);
     const uint32_t sub = slot_bytes / 4;               // one warp's share of a slot
     const uint32_t cd_sub = e.cd_bytes / 4;            // ... of which C/D
     // sub-slots of this warp: all E with one warp per quarter, else E / 2
@@ -981,14 +1054,15 @@ persistent_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
     // column-major ones.
     struct Cursor { int it, j, nch, row0, col0, tl; };
     auto cursor_enter = [&](Cursor& cc) {
-      for (; cc.it < p.num_items; cc.it += num_clusters) {
-        const Work wk = work_item<kSK>(cc.it, p, num_clusters);
+      for (; cc.it < p.num_items; cc.it = next_item(cc.it)) {
+        const KernelParams& P = product(cc.it);
+        const Work wk = work_item<kSK>(number(cc.it), P, num_clusters);
         if (wk.empty || !wk.owner) continue;   // no C/X: nothing, or a stream-K partial
         const int half = wk.half;
         cc.nch = half < 0 ? T.chunks : T.chunks / 2;
         if (strm >= cc.nch) continue;       // no chunk of this item in this stream
         int tm, tn;
-        tile_coords(wk.tile, p, tm, tn, cc.tl);
+        tile_coords(wk.tile, P, tm, tn, cc.tl);
         cc.j = strm;
         cc.row0 = tm * G::CM + (int)gm * (G::BM * CG) + (int)rank * G::BM + q * kSubRows;
         cc.col0 = tn * (BN * NC) + (int)gn * BN + (half > 0 ? BN / 2 : 0);
@@ -997,7 +1071,7 @@ persistent_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
     };
     auto cursor_next = [&](Cursor& cc) {
       if (cc.it < p.num_items && (cc.j += EPW) >= cc.nch) {
-        cc.it += num_clusters;
+        cc.it = next_item(cc.it);
         cursor_enter(cc);
       }
     };
@@ -1017,19 +1091,28 @@ persistent_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
       return (in_slots || in_ring) && (!e.read_c || inner_ok(x0, e.c_dt)) &&
              (!e.read_x || inner_ok(x0, e.x_dt));
     };
-    Cursor ld{cluster_id, 0, 0, 0, 0, 0};
+    Cursor ld{first_item, 0, 0, 0, 0, 0};
     int ld_slot = 0;
+    // (a product without C: its chunks' barriers complete at once)
+    auto load_chunk = [&](uint32_t dst, uint32_t bar, int x0, int x1) {
+      if constexpr (kPair) {
+        const EpiParams& le = product(ld.it).epi;
+        mbar_arrive_expect_tx(bar, load_bytes(le));
+        if (le.read_c)
+          tma_load_3d(dst, is_second(ld.it) ? &p.c2 : &tmC, bar, x0, x1, ld.tl, pol_in);
+      } else {
+        mbar_arrive_expect_tx(bar, load_tx);
+        if (e.read_c) tma_load_3d(dst, &tmC, bar, x0, x1, ld.tl, pol_in);
+        if (e.read_x) tma_load_3d(dst + cd_sub, &tmX, bar, x0, x1, ld.tl, pol_in);
+      }
+    };
     auto issue_loads = [&]() {              // lane 0 only
       if (ld.it < p.num_items) {
         int x0, x1;
         cursor_xy(ld, x0, x1);
         const uint32_t slot = ring0 + (uint32_t)ld_slot * sub;
         const uint32_t bar = bar0 + 8u * (uint32_t)ld_slot;
-        if (dbg_check(load_ok(slot, x0), kChkEpiLoad, w)) {
-          mbar_arrive_expect_tx(bar, load_tx);
-          if (e.read_c) tma_load_3d(slot, &tmC, bar, x0, x1, ld.tl, pol_in);
-          if (e.read_x) tma_load_3d(slot + cd_sub, &tmX, bar, x0, x1, ld.tl, pol_in);
-        }
+        if (dbg_check(load_ok(slot, x0), kChkEpiLoad, w)) load_chunk(slot, bar, x0, x1);
       }
       if (++ld_slot == Ew) ld_slot = 0;
       cursor_next(ld);
@@ -1052,12 +1135,18 @@ persistent_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
     long long st_tfull = 0, st_cfull = 0, st_read = 0, st_math = 0, st_issue = 0;
     long long st_chunks = 0;
     const long long st_t0 = stat_clock();
-    for (int it = cluster_id; ok && it < p.num_items; it += num_clusters) {
-      const Work wk = work_item<kSK>(it, p, num_clusters);
+    for (int it = first_item; ok && it < p.num_items; it = next_item(it)) {
+      const KernelParams& P = product(it);
+      const EpiParams& e = P.epi;
+      const CUtensorMap* map_d = &tmD;
+      if constexpr (kPair) {
+        if (is_second(it)) map_d = &p.d2;
+      }
+      const Work wk = work_item<kSK>(number(it), P, num_clusters);
       if (wk.empty) continue;
       const int half = wk.half;
       int tm, tn, tl;
-      tile_coords(wk.tile, p, tm, tn, tl);
+      tile_coords(wk.tile, P, tm, tn, tl);
       const int nchunks = half < 0 ? T.chunks : T.chunks / 2;
       const int ncol0 = tn * (BN * NC) + (int)gn * BN + (half > 0 ? BN / 2 : 0);
       // Linear epilogue: this lane's row factor, and one column's scale and
@@ -1066,15 +1155,15 @@ persistent_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
       float row_factor = 1.f, col_s = 1.f, col_b = 0.f;
       auto fetch_column = [&](int j) {
         const int col = ncol0 + j * kEpiChunk + lane;
-        if (col < p.N) {
+        if (col < P.N) {
           if (e.col_scale) col_s = __ldg(e.col_scale + col);
           if (e.bias) col_b = vector_elem(e.bias, col, e.bias_dt);
         }
       };
-      if constexpr (EPI == 1) {
+      if constexpr (kLinear) {
         const int row = tm * G::CM + (int)gm * (G::BM * CG) + (int)rank * G::BM + q * kSubRows + lane;
         row_factor = e.alpha;
-        if (e.row_scale && row < p.M) row_factor *= __ldg(e.row_scale + row);
+        if (e.row_scale && row < P.M) row_factor *= __ldg(e.row_scale + row);
         if (strm < nchunks) fetch_column(strm);
       }
       const long long t_t = stat_clock();
@@ -1143,7 +1232,7 @@ persistent_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
       // none).
       // Only lane 0 keeps the cursor; it decides and tells the warp.
       int batch0 = nchunks;
-      if (loads && (it + num_clusters >= p.num_items || (kSK && p.sk_units))) {   // (stream-K: owned items come last)
+      if (loads && (next_item(it) >= p.num_items || (kSK && p.sk_units))) {   // (stream-K: owned items come last)
         const int nb = ld.it == it ? (nchunks - ld.j + EPW - 1) / EPW : 0;   // this warp's
         if (lead && nb > 0 && (uint32_t)nb * (4u * EPW) * sub <= ring_bytes) {
           batch0 = ld.j;
@@ -1153,9 +1242,7 @@ persistent_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
             const uint32_t dst = b_ring + (uint32_t)(c * 4 * EPW + ew) * sub;
             const uint32_t rb = rfull0 + 8u * (uint32_t)(ew * kMaxChunks + c);
             if (!dbg_check(load_ok(dst, x0), kChkEpiLoad, w)) break;
-            mbar_arrive_expect_tx(rb, load_tx);
-            if (e.read_c) tma_load_3d(dst, &tmC, rb, x0, x1, ld.tl, pol_in);
-            if (e.read_x) tma_load_3d(dst + cd_sub, &tmX, rb, x0, x1, ld.tl, pol_in);
+            load_chunk(dst, rb, x0, x1);
             cursor_next(ld);
           }
           ld.it = p.num_items;               // the cursor has nothing left to load
@@ -1271,7 +1358,7 @@ persistent_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
         float dv[kEpiChunk];
         bool d_end_only = false, y_end_only = false;
         const float al = e.alpha, be = e.beta, xf = e.x_factor;
-        if constexpr (EPI == 1) {
+        if constexpr (kLinear) {
           // The chunk's column vectors go through shared memory, one column
           // per lane in, all 32 broadcast out; the next chunk's are fetched
           // meanwhile.
@@ -1295,14 +1382,14 @@ persistent_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
           // piece; a chunk without a whole piece has no other store.
           auto store_end = [&](void* t, long long ld, int dt) {
             const int piece = dt == DT_F32 ? 4 : 8;
-            const int left = p.N - col0, lo = left & ~(piece - 1);
+            const int left = P.N - col0, lo = left & ~(piece - 1);
             const long long row = row0 + lane;
-            if (row < p.M)
+            if (row < P.M)
               store_row_end(static_cast<uint8_t*>(t) + (row * ld + col0) * (dt == DT_F32 ? 4 : 2),
                             dt, lo, left - lo, dv);
             return lo == 0;
           };
-          const bool row_end = col0 + kEpiChunk > p.N;
+          const bool row_end = col0 + kEpiChunk > P.N;
           if (e.write_y) {
             smem_write_row(slot + cd_sub, e.y_dt, 0, lane, dv);
             if (row_end && e.y_ragged) y_end_only = store_end(e.y_ptr, e.ldy, e.y_dt);
@@ -1397,7 +1484,7 @@ persistent_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
           if (dbg_check(x0 >= 0 && x1 >= 0 && inner_ok(x0, e.d_dt) &&
                             (!e.write_y || inner_ok(x0, e.y_dt)),
                         kChkEpiStore, w)) {
-            if (!d_end_only) tma_store_3d(&tmD, s_addr, x0, x1, tl, pol_out);
+            if (!d_end_only) tma_store_3d(map_d, s_addr, x0, x1, tl, pol_out);
             if (e.write_y && !y_end_only) tma_store_3d(&tmY, s_addr + cd_sub, x0, x1, tl, pol_out);
           }
           bulk_commit_group();

@@ -75,6 +75,25 @@ struct LinearPlan {
 };
 constexpr int kLinearPlans = 16;
 
+// Plans of the latest two products run in one launch (the linear layer's
+// gradients).
+struct PairKey {
+  int64_t M, N, K;
+  uint64_t config_gen;
+  int type, da_type, db_type, accumulate;
+};
+struct PairPlan {
+  bool valid = false;
+  PairKey key;
+  bool one = false;          // one launch for both; else each by its own plan
+  bool db_first = false;     // the items of db come first
+  int lead_items = 0, lead_from = 0;   // as in PairParams
+  gemm_config_t cfg{};       // tile, ring and grid
+  gemm_config_t each[2]{};   // the same with each product's tiles (da, db)
+  const void* kern = nullptr;
+};
+constexpr int kPairPlans = 8;
+
 // NVTX ranges in the "gemm_gb300" domain around every entry point that
 // enqueues work (and around planning and tensor-map encoding on a launch-cache
 // miss), so that a profiler's timeline and its range filters (ncu --nvtx
@@ -113,12 +132,15 @@ struct gemm_handle {
   uint64_t timeout_ns = gb300host::kDefaultTimeoutNs;
   gb300host::VariantState variants[3][2][2][2][2][2][2];   // [ab 16/8/32][cta_group][k atoms][mc][nc][epw][sk]
   gb300host::VariantState linear_variants[3][2][2][2];   // [ab][cta_group][k atoms][epw]
+  gb300host::VariantState pair_variants[2][2][2];        // [cta_group][k atoms][epw]
   int clusters_by_size[9] = {0, 0, 0, 0, 0, 0, 0, 0, 0};   // resident clusters of 1, 2, 4, 8 CTAs
   uint64_t config_gen = 0;
   gb300host::LaunchEntry cache[gb300host::kLaunchCacheEntries];
   int cache_next = 0;
   gb300host::LinearPlan linear_plans[gb300host::kLinearPlans];
   int linear_next = 0;
+  gb300host::PairPlan pair_plans[gb300host::kPairPlans];
+  int pair_next = 0;
   int split_clusters[9] = {0, 0, 0, 0, 0, 0, 0, 0, 0};   // resident, by cluster size (0: not asked)
   std::mutex mu;
   void* ws = nullptr;          // gemm_run_host's device copies of its host buffers

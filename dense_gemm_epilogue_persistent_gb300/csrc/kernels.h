@@ -19,8 +19,10 @@ namespace gb300 {
   X(2, 1, 0) X(1, 1, 0) X(4, 1, 0) X(2, 2, 0) X(1, 2, 0) X(4, 2, 0) X(2, 1, 1) X(1, 1, 1) \
   X(4, 1, 1) X(2, 2, 1) X(1, 2, 1) X(4, 2, 1)
 // kern_linear.cu, compiled once per input width and epw, holds the clusters of
-// one CTA group with the linear layer's epilogue.
-#define GB300_LINEAR_ENTRIES(X) X(2, 1) X(1, 1) X(4, 1) X(2, 2) X(1, 2) X(4, 2)
+// one CTA group with the linear layer's epilogue (epi = 1) and, at 16 bits, those
+// that run two products (epi = 2).
+#define GB300_LINEAR_ENTRIES(X) \
+  X(2, 1, 1) X(1, 1, 1) X(4, 1, 1) X(2, 2, 1) X(1, 2, 1) X(4, 2, 1) X(2, 1, 2) X(2, 2, 2)
 #define GB300_SHARED_ENTRIES(X) \
   X(2, 2, 1) X(2, 1, 2) X(2, 2, 2) X(1, 2, 1) X(1, 1, 2) X(1, 2, 2) X(4, 2, 1) X(4, 1, 2) X(4, 2, 2)
 
@@ -30,11 +32,11 @@ namespace gb300 {
 #define GB300_SHARED_NAME_(ab, mc, nc) kernel_shared_ab##ab##_m##mc##_n##nc
 #define GB300_SHARED_NAME(ab, mc, nc) GB300_SHARED_NAME_(ab, mc, nc)
 
-#define GB300_LINEAR_NAME_(ab, epw) kernel_linear_ab##ab##_e##epw
-#define GB300_LINEAR_NAME(ab, epw) GB300_LINEAR_NAME_(ab, epw)
+#define GB300_LINEAR_NAME_(ab, epw, epi) kernel_linear_ab##ab##_e##epw##_p##epi
+#define GB300_LINEAR_NAME(ab, epw, epi) GB300_LINEAR_NAME_(ab, epw, epi)
 
-#define GB300_DECLARE_LINEAR(ab, epw) \
-  const void* GB300_LINEAR_NAME(ab, epw)(int cta_group, int ka);
+#define GB300_DECLARE_LINEAR(ab, epw, epi) \
+  const void* GB300_LINEAR_NAME(ab, epw, epi)(int cta_group, int ka);
 #define GB300_DECLARE_PLAIN(ab, epw, sk) \
   const void* GB300_PLAIN_NAME(ab, epw, sk)(int cta_group, int ka);
 #define GB300_DECLARE_SHARED(ab, mc, nc) \
@@ -78,10 +80,10 @@ inline const void* kernel_for(int ab_bytes, int cta_group, int ka, int mc, int n
   return nullptr;
 }
 
-// The same for the linear layer's epilogue.
-inline const void* linear_kernel_for(int ab_bytes, int cta_group, int ka, int epw) {
-#define GB300_PICK_LINEAR(ab, e) \
-  if (ab_bytes == ab && epw == e) return GB300_LINEAR_NAME(ab, e)(cta_group, ka);
+// The same for the linear layer's epilogue (epi = 1) and for two products (2).
+inline const void* linear_kernel_for(int ab_bytes, int cta_group, int ka, int epw, int epi = 1) {
+#define GB300_PICK_LINEAR(ab, e, k) \
+  if (ab_bytes == ab && epw == e && epi == k) return GB300_LINEAR_NAME(ab, e, k)(cta_group, ka);
   GB300_LINEAR_ENTRIES(GB300_PICK_LINEAR)
 #undef GB300_PICK_LINEAR
   return nullptr;

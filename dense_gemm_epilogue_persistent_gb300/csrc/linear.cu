@@ -229,11 +229,9 @@ gemm_status_t plan_persistent(gemm_handle* h, const gemm_linear_t& p, LinearPlan
 // A launch's place beside another that it does not depend on (EpiParams).
 enum Place { kAlone, kFirstOfTwo, kSecondOfTwo };
 
-// Enqueue a call on the persistent kernel by its plan.
-gemm_status_t run_persistent(gemm_handle* h, const gemm_linear_t& p, const LinearPlan& plan,
-                             Place place, struct CUstream_st* stream) {
-  const gemm_config_t& cfg = plan.cfg;
-  CUtensorMap maps[6];                 // A, B, C, X, D, Y
+// A call's tensor maps (A, B, C, X, D, Y) and parameters for the persistent kernel.
+gemm_status_t prepare_persistent(gemm_handle* h, const gemm_linear_t& p, const gemm_config_t& cfg,
+                                 CUtensorMap (&maps)[6], KernelParams& kp) {
   std::memset(maps, 0, sizeof(maps));
   const bool a_mn = p.layoutA == GEMM_MN_MAJOR, b_mn = p.layoutB == GEMM_MN_MAJOR;
   if (p.K > 0 &&
@@ -254,7 +252,6 @@ gemm_status_t run_persistent(gemm_handle* h, const gemm_linear_t& p, const Linea
        !encode_epi(h->encode, &maps[5], p.Z, p.z_type, p.M, stored(p.z_type), 1, false, p.ldz)))
     return GEMM_ERR_CUDA;
 
-  KernelParams kp{};
   kp.M = (int)p.M; kp.N = (int)p.N; kp.K = (int)p.K; kp.L = 1;
   kp.bn = cfg.tile_n;
   kp.tiles_m = (int)cdiv(p.M, cfg.tile_m);
@@ -292,15 +289,17 @@ gemm_status_t run_persistent(gemm_handle* h, const gemm_linear_t& p, const Linea
   kp.epi.bias = p.bias;
   kp.epi.bias_dt = p.bias_type;
   kp.epi.act = p.activation;
-  kp.epi.trigger_late = place == kFirstOfTwo;
-  kp.epi.wait_late = place == kSecondOfTwo;
   kp.epi.d_ptr = p.D; kp.epi.ldd = p.ldd;
   kp.epi.d_ragged = (p.N * dtype_bytes(p.d_type)) % 16 != 0;
   if (p.Z) {
     kp.epi.y_ptr = p.Z; kp.epi.ldy = p.ldz;
     kp.epi.y_ragged = (p.N * dtype_bytes(p.z_type)) % 16 != 0;
   }
+  return GEMM_OK;
+}
 
+gemm_status_t launch_persistent(const gemm_config_t& cfg, const void* kern, void** args,
+                                struct CUstream_st* stream) {
   cudaLaunchConfig_t lc{};
   cudaLaunchAttribute attr[2];
   lc.gridDim = dim3((unsigned)cfg.grid_ctas);
@@ -315,12 +314,23 @@ gemm_status_t run_persistent(gemm_handle* h, const gemm_linear_t& p, const Linea
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   lc.attrs = attr;
   lc.numAttrs = 2;
-  void* args[7] = {&maps[0], &maps[1], &maps[2], &maps[3], &maps[4], &maps[5], &kp};
-  if (cudaLaunchKernelExC(&lc, plan.kern, args) != cudaSuccess) {
+  if (cudaLaunchKernelExC(&lc, kern, args) != cudaSuccess) {
     cudaGetLastError();
     return GEMM_ERR_CUDA;
   }
   return GEMM_OK;
+}
+
+// Enqueue a call on the persistent kernel by its plan.
+gemm_status_t run_persistent(gemm_handle* h, const gemm_linear_t& p, const LinearPlan& plan,
+                             Place place, struct CUstream_st* stream) {
+  CUtensorMap maps[6];
+  KernelParams kp{};
+  GB300_CHECK(prepare_persistent(h, p, plan.cfg, maps, kp));
+  kp.epi.trigger_late = place == kFirstOfTwo;
+  kp.epi.wait_late = place == kSecondOfTwo;
+  void* args[7] = {&maps[0], &maps[1], &maps[2], &maps[3], &maps[4], &maps[5], &kp};
+  return launch_persistent(plan.cfg, plan.kern, args, stream);
 }
 
 // The ring, its barriers and the alignment; the last stage's matrix operand,
@@ -561,6 +571,186 @@ gemm_status_t run_linear(gemm_handle* h, const gemm_linear_t& p, struct CUstream
                      : run_persistent(h, p, *plan, place, stream);
 }
 
+// Microseconds of one item of one of two products in one launch, beside the
+// launch's own: fitted on GB300 to 57 problems (256 to 8192 tokens, 364 to 8192 features
+// and inner sizes; db in bf16, or in fp32 and added to) x 28 variants, of which the
+// estimate's choice is 0.4 % over the fastest on average and 9 % at worst.
+// `bytes`: of C and D an element.
+double pair_item(const gemm_config_t& c, int64_t k_blocks, int bytes) {
+  const double w = c.tile_n / 256.0;
+  double per_kb = c.cta_group == 1 ? 0.279 * w + 0.086 : 0.323 * w + 0.009;
+  per_kb *= 1.0 + 0.147 * std::max(0.0, 180.0 - c.ring_bytes / 1024.0) / 64.0;
+  const double fixed = c.cta_group == 1 ? 0.167 + 1.393 * w : 1.593 + 0.347 * w;
+  return (double)k_blocks * per_kb + fixed + (c.epi_warps == 1 ? 1.545 * w : 0.0) +
+         0.452 * w * std::max(0, bytes - 2);
+}
+
+// The longest cluster's time, when `first` items of one product, then `second` of the
+// other (the last `halves` of them half-width) are dealt to `clusters` clusters,
+// `lead` of the second's ahead to those from lead_from on (PairParams).
+double pair_time(int64_t first, int64_t second, int64_t halves, int64_t lead, int64_t lead_from,
+                 int64_t clusters, double first_us, double second_us) {
+  double longest = 0.0;
+  for (int64_t c = 0; c < clusters; ++c) {
+    const int64_t n1 = c < first ? cdiv(first - c, clusters) : 0;
+    const int64_t rest = second - lead;
+    const int64_t n2 = c < rest ? cdiv(rest - c, clusters) : 0;
+    const int64_t ahead = c >= lead_from ? lead / (clusters - lead_from) : 0;
+    double t = (double)n1 * first_us + (double)(n2 + ahead) * second_us;
+    if (n2 > 0 && c + (n2 - 1) * clusters >= rest - halves) t -= 0.3 * second_us;
+    longest = std::max(longest, t);
+  }
+  return longest;
+}
+
+// Plan the two gradients as one launch (h->mu held): both on the persistent
+// kernel with a common tile, the one with more k-blocks a tile first, the last
+// partial wave in half-width items where that fits.  One launch where neither
+// is the split-K kernel's, against one each (1001 x 2003 x 1501 fp16 18.4 us, 26.1;
+// 600 x 600 x 600 7.5, 13.4; 3000 x 5000 x 4096 bf16 148, 174, with db fp32 and added to
+// 161, 204): a tile's start and end, and the last wave's idle SMs, are paid once.
+gemm_status_t plan_pair(gemm_handle* h, const gemm_linear_t& da, const gemm_linear_t& db,
+                        PairPlan& out) {
+  out.one = false;
+  const gemm_config_t* const forced = h->forced ? &h->forced_cfg : nullptr;
+  if (forced && forced->split_k > 0) return GEMM_OK;
+  for (const gemm_linear_t* p : {&da, &db}) {
+    LinearPlan plan;
+    GB300_CHECK(plan_linear(h, *p, plan));
+    if (plan.split) return GEMM_OK;
+  }
+  out.db_first = db.K > da.K;
+  const gemm_linear_t& first = out.db_first ? db : da;
+  const gemm_linear_t& second = out.db_first ? da : db;
+  // The common ring and slots: db's operands ask for more than da's (both
+  // MN-major); the wider output type, and db itself where it is added to.
+  gemm_linear_t both = db;
+  if (dtype_bytes(da.d_type) > dtype_bytes(db.d_type)) both.d_type = da.d_type;
+  const EpilogueExtra extra{true, (int)gb300::kLinearSmem, activation_cost(GEMM_ACT_NONE)};
+  double best = 0.0;
+  for (int cg : {2, 1})
+    for (int bn = 256; bn >= 64; bn -= 32)
+      for (int epw : {2, 1}) {
+        gemm_config_t f = forced ? *forced : gemm_config_t{};
+        if ((f.cta_group && f.cta_group != cg) || (f.tile_n && f.tile_n != bn) ||
+            (f.epi_warps && f.epi_warps != epw))
+          continue;
+        const bool may_split = f.tail_split != 1 && (bn / 2) % gb300::kEpiChunk == 0 &&
+                               (bn / cg / 2) % 64 == 0;
+        f.cta_group = cg;
+        f.tile_n = bn;
+        f.epi_warps = epw;
+        f.tail_split = 1;
+        gemm_config_t c, each[2];
+        const auto plan = [&](const gemm_linear_t& p, gemm_config_t* o) {
+          return plan_valid(as_problem(p), h->sm_count, h->smem_optin, &f, o, h->clusters_by_size,
+                            false, extra) == GEMM_OK;
+        };
+        if (!plan(both, &c) || !plan(first, &each[0]) || !plan(second, &each[1]) ||
+            c.cluster_m != 1 || c.cluster_n != 1)
+          continue;
+        const int ka = gb300::k_atoms(cg, bn);
+        const void* kern = gb300::linear_kernel_for(2, cg, ka, epw, 2);
+        int resident = 0;
+        GB300_CHECK(resident_kernel_clusters(h, h->pair_variants[cg - 1][ka - 1][epw - 1], kern, c,
+                                             cg, &resident));
+        double us[2];
+        for (int i = 0; i < 2; ++i) {
+          const gemm_linear_t& p = i ? second : first;
+          us[i] = pair_item(c, cdiv(p.K, 64),
+                            dtype_bytes(p.d_type) + (p.R ? dtype_bytes(p.r_type) : 0));
+        }
+        const int64_t n1 = each[0].tiles, n2 = each[1].tiles;
+        const int64_t clusters = std::min<int64_t>(n1 + n2, resident);
+        // Rounds of the second's items for the clusters with one of the first's
+        // less; the last round of the rest in half-width items or not.
+        const int64_t from = n1 % clusters;
+        const int64_t most =
+            from ? std::min<int64_t>(n2 / (clusters - from), (int64_t)(us[0] / us[1]) + 1) : 0;
+        for (int64_t rounds = 0; rounds <= most; ++rounds) {
+          const int64_t lead = rounds * (clusters - from), rem = (n2 - lead) % clusters;
+          for (const int64_t split : {(int64_t)0, may_split && 2 * rem <= clusters ? rem : 0}) {
+            const double t =
+                pair_time(n1, n2 + split, 2 * split, lead, from, clusters, us[0], us[1]);
+            if (out.one && t >= best) continue;
+            best = t;
+            out.one = true;
+            out.kern = kern;
+            out.lead_items = (int)lead;
+            out.lead_from = (int)from;
+            out.cfg = c;
+            out.cfg.tiles = n1 + n2;
+            out.cfg.tail_split = (int)split;
+            out.cfg.grid_ctas = (int)clusters * cg;
+            for (int i = 0; i < 2; ++i) {
+              gemm_config_t& o = out.each[out.db_first ? 1 - i : i];
+              o = out.cfg;
+              o.tiles = each[i].tiles;
+              o.group_m = each[i].group_m;
+              o.tail_split = i ? (int)split : 0;
+            }
+          }
+        }
+      }
+  return GEMM_OK;
+}
+
+gemm_status_t run_pair(gemm_handle* h, const gemm_linear_t& da, const gemm_linear_t& db,
+                       const PairPlan& plan, struct CUstream_st* stream) {
+  CUtensorMap maps[6], second[6];
+  gb300::PairParams kp{};
+  GB300_CHECK(plan.db_first ? prepare_persistent(h, db, plan.each[1], maps, kp)
+                            : prepare_persistent(h, da, plan.each[0], maps, kp));
+  GB300_CHECK(plan.db_first ? prepare_persistent(h, da, plan.each[0], second, kp.second)
+                            : prepare_persistent(h, db, plan.each[1], second, kp.second));
+  // one layout of the slots for both
+  for (gb300::EpiParams* e : {&kp.epi, &kp.second.epi}) {
+    e->cd_bytes = (uint32_t)plan.cfg.epi_slot_bytes;
+    e->xy_bytes = 0;
+  }
+  kp.first_items = kp.num_items;
+  kp.num_items += kp.second.num_items;
+  kp.lead_items = plan.lead_items;
+  kp.lead_from = plan.lead_from;
+  kp.a2 = second[0];
+  kp.b2 = second[1];
+  kp.c2 = second[2];
+  kp.d2 = second[4];
+  void* args[7] = {&maps[0], &maps[1], &maps[2], &maps[3], &maps[4], &maps[5], &kp};
+  return launch_persistent(plan.cfg, plan.kern, args, stream);
+}
+
+// Both gradients of a layer from dz, neither empty.
+gemm_status_t run_products(gemm_handle* h, const gemm_linear_bwd_t& p, const gemm_linear_t& da,
+                           const gemm_linear_t& db, struct CUstream_st* stream) {
+  PairKey key;
+  std::memset(&key, 0, sizeof(key));           // padding included: keys compare bytewise
+  key.M = p.M; key.N = p.N; key.K = p.K;
+  key.type = p.type; key.da_type = p.da_type; key.db_type = p.db_type;
+  key.accumulate = p.accumulate != 0;
+  {
+    std::lock_guard<std::mutex> guard(h->mu);
+    key.config_gen = h->config_gen;
+    PairPlan* plan = nullptr;
+    for (PairPlan& c : h->pair_plans)
+      if (c.valid && std::memcmp(&c.key, &key, sizeof(key)) == 0) { plan = &c; break; }
+    if (!plan) {
+      plan = &h->pair_plans[h->pair_next];
+      plan->valid = false;
+      GB300_CHECK(plan_pair(h, da, db, *plan));
+      plan->key = key;
+      plan->valid = true;
+      h->pair_next = (h->pair_next + 1) % kPairPlans;
+    }
+    if (plan->one) {
+      h->last = plan->cfg;
+      return run_pair(h, da, db, *plan, stream);
+    }
+  }
+  GB300_CHECK(run_linear(h, da, stream, kFirstOfTwo));
+  return run_linear(h, db, stream, kSecondOfTwo);
+}
+
 // Launch shape of the activation gradient: blocks per cluster for four blocks an
 // SM (all that its registers hold) where the rows allow, with 64 rows a block
 // at least.  Where even clusters of 8 leave SMs without a block (N up to 1216),
@@ -697,12 +887,9 @@ GEMM_API gemm_status_t gemm_linear_bwd(gemm_handle_t h, const gemm_linear_bwd_t*
   }
   int64_t lddz = 0;
   const void* dz = dz_of(p, lddz);
-  // (both empty or both launched where both are asked for: an empty product
-  // launches nothing)
-  const bool two = p.da && p.db && p.M > 0 && p.N > 0 && p.K > 0;
-  if (p.da)
-    GB300_CHECK(run_linear(h, product_da(p, dz, lddz), stream, two ? kFirstOfTwo : kAlone));
-  if (p.db)
-    GB300_CHECK(run_linear(h, product_db(p, dz, lddz), stream, two ? kSecondOfTwo : kAlone));
+  if (p.da && p.db && p.M > 0 && p.N > 0 && p.K > 0)
+    return run_products(h, p, product_da(p, dz, lddz), product_db(p, dz, lddz), stream);
+  if (p.da) GB300_CHECK(run_linear(h, product_da(p, dz, lddz), stream));
+  if (p.db) GB300_CHECK(run_linear(h, product_db(p, dz, lddz), stream));
   return GEMM_OK;
 }
