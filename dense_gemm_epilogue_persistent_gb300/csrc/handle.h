@@ -69,6 +69,7 @@ struct LinearPlan {
   bool valid = false;
   LinearKey key;
   bool split = false;        // the split-K kernel, else the persistent one
+  double us = 0.0;           // the estimate that it was chosen by
   SplitPlan s{};
   gemm_config_t cfg{};
   const void* kern = nullptr;

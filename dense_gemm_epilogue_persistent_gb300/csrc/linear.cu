@@ -508,16 +508,19 @@ bool choose_split(gemm_handle* h, const gemm_linear_t& p, SplitPlan* out) {
 // at worst.  For instance (split-K, persistent): 1 x 4096 x 4096 bf16 9.4, 32.6 us;
 // 64 x 4096 x 4096 11.4, 15.6; 128 x 4096 x 4096 16.7, 15.7; 256 x 1024 x 8192 16.4,
 // 22.3; 512 x 512 x 512 8.1, 5.7.
-bool split_is_faster(const gemm_linear_t& p, const SplitPlan& s, double persistent_cost) {
+double split_us(const gemm_linear_t& p, const SplitPlan& s) {
   const int es = dtype_bytes(p.a_type);
   const double weights = (double)p.N * (double)p.K * es / 6.3e6;       // us at 6.3 TB/s
   const double tokens = (double)p.M * (double)p.K * es * (double)s.tiles_n / 6.3e6;
   const double k_blocks = (double)cdiv(p.K, 128 / es) / s.split;
   const double own = (double)cdiv(cdiv(s.bn, s.split), 4) * 4;
-  const double split_us = 3.41 + 0.141 * k_blocks + 0.0525 * own +
-                          (s.split > 1 ? 0.032 * s.bn : 0.0) + 0.592 * weights + 0.582 * tokens;
-  const double persistent_us = 1.59 + 0.333 * persistent_cost + 0.498 * weights;
-  return split_us < persistent_us;
+  return 3.41 + 0.141 * k_blocks + 0.0525 * own + (s.split > 1 ? 0.032 * s.bn : 0.0) +
+         0.592 * weights + 0.582 * tokens;
+}
+
+double persistent_us(const gemm_linear_t& p, double cost) {
+  const double weights = (double)p.N * (double)p.K * dtype_bytes(p.a_type) / 6.3e6;
+  return 1.59 + 0.333 * cost + 0.498 * weights;
 }
 
 // Plan a checked call (h->mu held): as forced, or the faster kernel.
@@ -531,7 +534,13 @@ gemm_status_t plan_linear(gemm_handle* h, const gemm_linear_t& p, LinearPlan& ou
     out.split = true;
   } else {
     GB300_CHECK(plan_persistent(h, p, out, &cost));
-    out.split = !h->forced && choose_split(h, p, &out.s) && split_is_faster(p, out.s, cost);
+    out.us = persistent_us(p, cost);
+    out.split = false;
+    if (!h->forced && choose_split(h, p, &out.s)) {
+      const double us = split_us(p, out.s);
+      out.split = us < out.us;
+      out.us = std::min(us, out.us);
+    }
   }
   if (out.split) {
     out.kern = gb300::split_kernel_for(es);
@@ -572,17 +581,17 @@ gemm_status_t run_linear(gemm_handle* h, const gemm_linear_t& p, struct CUstream
 }
 
 // Microseconds of one item of one of two products in one launch, beside the
-// launch's own: fitted on GB300 to 57 problems (256 to 8192 tokens, 364 to 8192 features
-// and inner sizes; db in bf16, or in fp32 and added to) x 28 variants, of which the
-// estimate's choice is 0.4 % over the fastest on average and 9 % at worst.
-// `bytes`: of C and D an element.
+// launch's own.  `bytes`: of C and D an element.  The constants here and in
+// plan_pair are fitted on GB300 to 61 problems (256 to 8192 tokens, 364 to 8192
+// features and inner sizes; db in bf16, or in fp32 and added to) x 28 variants: the
+// choice is 0.5 % over the fastest on average and 9 % at worst.
 double pair_item(const gemm_config_t& c, int64_t k_blocks, int bytes) {
   const double w = c.tile_n / 256.0;
-  double per_kb = c.cta_group == 1 ? 0.279 * w + 0.086 : 0.323 * w + 0.009;
-  per_kb *= 1.0 + 0.147 * std::max(0.0, 180.0 - c.ring_bytes / 1024.0) / 64.0;
-  const double fixed = c.cta_group == 1 ? 0.167 + 1.393 * w : 1.593 + 0.347 * w;
-  return (double)k_blocks * per_kb + fixed + (c.epi_warps == 1 ? 1.545 * w : 0.0) +
-         0.452 * w * std::max(0, bytes - 2);
+  double per_kb = c.cta_group == 1 ? 0.250 * w + 0.082 : 0.280 * w + 0.020;
+  per_kb *= 1.0 + 0.281 * std::max(0.0, 180.0 - c.ring_bytes / 1024.0) / 64.0;
+  const double fixed = c.cta_group == 1 ? 0.185 + 1.390 * w : 1.671 + 0.293 * w;
+  return (double)k_blocks * per_kb + fixed + (c.epi_warps == 1 ? 2.177 * w : 0.0) +
+         0.388 * w * std::max(0, bytes - 2);
 }
 
 // The longest cluster's time, when `first` items of one product, then `second` of the
@@ -605,19 +614,26 @@ double pair_time(int64_t first, int64_t second, int64_t halves, int64_t lead, in
 
 // Plan the two gradients as one launch (h->mu held): both on the persistent
 // kernel with a common tile, the one with more k-blocks a tile first, the last
-// partial wave in half-width items where that fits.  One launch where neither
-// is the split-K kernel's, against one each (1001 x 2003 x 1501 fp16 18.4 us, 26.1;
-// 600 x 600 x 600 7.5, 13.4; 3000 x 5000 x 4096 bf16 148, 174, with db fp32 and added to
-// 161, 204): a tile's start and end, and the last wave's idle SMs, are paid once.
+// round in half-width items where that fits.  One launch wherever each would
+// take the persistent kernel anyway (1001 x 2003 x 1501 fp16 18.3 us, 26.4 as two;
+// 600 x 600 x 600 7.5, 13.4; 3000 x 5000 x 4096 bf16 147, 176, with db in fp32 and added to
+// 158, 201): a launch's start and end, and the last wave's idle SMs, are paid once.
+// Where one would take split-K, by the estimates (128 x 1024 x 4096 bf16 11.7 us in one,
+// 16.9; 300 x 4096 x 1024 22 planned as two, 17.5).  Fewer than 128 tokens stay two
+// launches: db's items are then one or two k-blocks long, which the estimate does
+// not hold for (64 x 4096 x 4096: 36 as it would choose, 31; 1 x 8192 x 2048: 43, 30).
 gemm_status_t plan_pair(gemm_handle* h, const gemm_linear_t& da, const gemm_linear_t& db,
                         PairPlan& out) {
   out.one = false;
   const gemm_config_t* const forced = h->forced ? &h->forced_cfg : nullptr;
-  if (forced && forced->split_k > 0) return GEMM_OK;
+  if (da.M < 128 || (forced && forced->split_k > 0)) return GEMM_OK;
+  bool any_split = false;
+  double alone = 0.0;
   for (const gemm_linear_t* p : {&da, &db}) {
     LinearPlan plan;
     GB300_CHECK(plan_linear(h, *p, plan));
-    if (plan.split) return GEMM_OK;
+    any_split = any_split || plan.split;
+    alone += plan.us;
   }
   out.db_first = db.K > da.K;
   const gemm_linear_t& first = out.db_first ? db : da;
@@ -661,6 +677,9 @@ gemm_status_t plan_pair(gemm_handle* h, const gemm_linear_t& da, const gemm_line
                             dtype_bytes(p.d_type) + (p.R ? dtype_bytes(p.r_type) : 0));
         }
         const int64_t n1 = each[0].tiles, n2 = each[1].tiles;
+        // All SMs' operand loads at the 16.3 TB/s that they come to together.
+        const double l2_us = (double)(n1 * cdiv(first.K, 64) + n2 * cdiv(second.K, 64)) *
+                             (double)(cg * 128 + bn) * 128.0 / 16.3e6;
         const int64_t clusters = std::min<int64_t>(n1 + n2, resident);
         // Rounds of the second's items for the clusters with one of the first's
         // less; the last round of the rest in half-width items or not.
@@ -670,8 +689,9 @@ gemm_status_t plan_pair(gemm_handle* h, const gemm_linear_t& da, const gemm_line
         for (int64_t rounds = 0; rounds <= most; ++rounds) {
           const int64_t lead = rounds * (clusters - from), rem = (n2 - lead) % clusters;
           for (const int64_t split : {(int64_t)0, may_split && 2 * rem <= clusters ? rem : 0}) {
-            const double t =
+            const double longest =
                 pair_time(n1, n2 + split, 2 * split, lead, from, clusters, us[0], us[1]);
+            const double t = std::max(longest, l2_us) + 0.01 * longest;
             if (out.one && t >= best) continue;
             best = t;
             out.one = true;
@@ -692,6 +712,12 @@ gemm_status_t plan_pair(gemm_handle* h, const gemm_linear_t& da, const gemm_line
           }
         }
       }
+  if (out.one && any_split) {
+    const double bytes = 2.0 * ((double)da.M * (double)da.K * 2.0 + (double)da.M * (double)da.N * 3.0 +
+                                (double)db.M * (double)db.N * 2.0) +
+                         (db.R ? 6.0 * (double)db.M * (double)db.N : 0.0);
+    out.one = 6.48 + best + 0.174 * bytes / 6.3e6 < alone;
+  }
   return GEMM_OK;
 }
 
