@@ -3,6 +3,7 @@
 // the persistent kernel with the linear epilogue, and the activation-gradient
 // kernel.
 #include <algorithm>
+#include <cmath>
 #include <cstdint>
 #include <cstring>
 
@@ -30,15 +31,23 @@ struct ActGradParams {
 // dz = dd act'(z) and dbias = its column sums (of the values before dz is
 // rounded), 6 bytes and about 25 instructions an element.  A block owns 64
 // columns (8 lanes of one vector each) and 1/R of the rows, R the cluster size:
-// thread group g of G = THREADS / 8 walks rows first + g, + G, ..., a few at a
-// time so that their loads are in flight together.  A column's sum is added in
-// a fixed order: a thread's rows, the groups through shared memory, the
-// cluster's blocks by its first one.
+// thread group g of G = THREADS / 8 walks rows first + g, + G, ..., each thread
+// copying its own pieces of the next kActDepth rows into its own slots of shared
+// memory (16 bytes and the row's end as they lie in memory; loads into registers, two
+// rows at a time, took 43.6 us for 4096 x 8192 gelu, 39.0 so, and 20.3, 13.1 for 8192 x
+// 700, whose rows end inside a piece).  A column's sum is added in a fixed order: a
+// thread's rows, the groups through shared memory, the cluster's blocks by its
+// first one.
+// (4096 x 8192 gelu: 39.0 us with three rows, 40.5 with two, 38.9 with four; 16384 x
+// 4096: 70.1, 69.9, 73.7)
+constexpr int kActDepth = 3;
+
 template <int DT, int THREADS>
 __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
 act_grad_kernel(const __grid_constant__ ActGradParams p) {
   constexpr int G = THREADS / 8;
-  __shared__ float part[G][64];
+  extern __shared__ uint4 act_ring[];    // [kActDepth][dd, z][thread], then
+  float(*const part)[64] = reinterpret_cast<float(*)[64]>(act_ring + kActDepth * 2 * THREADS);
   __shared__ float block_part[64];
   constexpr int es = elem_bytes(DT);
   grid_launch_dependents();
@@ -57,36 +66,37 @@ act_grad_kernel(const __grid_constant__ ActGradParams p) {
     const uint8_t* const zz = static_cast<const uint8_t*>(p.z);
     with_activation(p.act, [&](auto a) {
       constexpr int ACT = decltype(a)::value;
-      constexpr int kUnroll = ACT == ACT_NONE ? 4 : 2;
-      for (long long row0 = first + group; row0 < last; row0 += G * kUnroll) {
-        RawVec<DT> g_raw[kUnroll], z_raw[kUnroll];
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-          const long long row = row0 + G * u;
-          g_raw[u] = z_raw[u] = RawVec<DT>{};
-          if (row < last) {
-            g_raw[u] = load_raw<DT>(dd + row * p.lddd * es, c, p.N);
-            if constexpr (ACT != ACT_NONE) z_raw[u] = load_raw<DT>(zz + row * p.ldz * es, c, p.N);
-          }
+      const int bytes = min(kVec, p.N - c) * es;
+      const uint32_t ring = smem_u32(act_ring) + threadIdx.x * 16;
+      auto request = [&](long long row, int slot) {
+        if (row < last) {
+          const uint32_t at = ring + slot * (2 * THREADS * 16);
+          copy16_async(at, dd + (row * p.lddd + c) * es, bytes);
+          if constexpr (ACT != ACT_NONE)
+            copy16_async(at + THREADS * 16, zz + (row * p.ldz + c) * es, bytes);
         }
+        copy_commit();
+      };
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-          const long long row = row0 + G * u;
-          if (row >= last) break;
-          float g[kVec];
-          unpack<DT>(g_raw[u], g);
-          if constexpr (ACT != ACT_NONE) {
-            float z[kVec];
-            unpack<DT>(z_raw[u], z);
+      for (int s = 0; s < kActDepth; ++s) request(first + group + s * G, s);
+      int slot = 0;
+      for (long long row = first + group; row < last; row += G) {
+        copy_wait(kActDepth - 1);
+        const uint4* const at = act_ring + slot * (2 * THREADS) + threadIdx.x;
+        float g[kVec];
+        unpack<DT>(RawVec<DT>{{at[0]}}, g);
+        if constexpr (ACT != ACT_NONE) {
+          float z[kVec];
+          unpack<DT>(RawVec<DT>{{at[THREADS]}}, z);
 #pragma unroll
-            for (int i = 0; i < kVec; i += 2)
-              unpair(mul2(pair(g[i], g[i + 1]), activate_grad2<ACT>(z[i], z[i + 1])), g[i],
-                     g[i + 1]);
-          }
-          if (p.dz) store_vec(static_cast<uint8_t*>(p.dz) + row * p.lddz * es, DT, c, p.N, g);
-#pragma unroll
-          for (int i = 0; i < kVec; ++i) acc[i] += g[i];
+          for (int i = 0; i < kVec; i += 2)
+            unpair(mul2(pair(g[i], g[i + 1]), activate_grad2<ACT>(z[i], z[i + 1])), g[i], g[i + 1]);
         }
+        if (p.dz) store_vec(static_cast<uint8_t*>(p.dz) + row * p.lddz * es, DT, c, p.N, g);
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) acc[i] += g[i];
+        request(row + kActDepth * G, slot);       // (into the slot just read)
+        if (++slot == kActDepth) slot = 0;
       }
     });
   }
@@ -777,36 +787,73 @@ gemm_status_t run_products(gemm_handle* h, const gemm_linear_bwd_t& p, const gem
   return run_linear(h, db, stream, kSecondOfTwo);
 }
 
-// Launch shape of the activation gradient: blocks per cluster for four blocks an
-// SM (all that its registers hold) where the rows allow, with 64 rows a block
-// at least.  Where even clusters of 8 leave SMs without a block (N up to 1216),
-// larger blocks: 512 threads, or 1024 while every cluster of those is resident
-// (the device holds 15 of 8 such blocks; 16 of them, 8192 x 1024, run as two waves:
-// gelu 28 us with 256 threads, 30.6 with 1024).
-struct ActGradShape {
-  int split, threads;
-};
-
-ActGradShape act_grad_shape(int64_t M, int64_t N, int sm_count) {
-  ActGradShape s{1, 256};
-  const int64_t strips = cdiv(N, 64);
-  while (s.split < 8 && strips * s.split < 8 * (int64_t)sm_count && M >= 128 * s.split) s.split *= 2;
-  if (strips * 8 <= sm_count && M >= 256 * s.split) s.threads = strips <= 12 ? 1024 : 512;
-  return s;
+// Clusters of `split` blocks of kern that the device holds at once, asked for once.
+template <class Kern>
+int act_clusters(gemm_handle* h, Kern kern, int size, int threads, size_t smem, int split) {
+  int& n = h->act_clusters[size][split];
+  if (n > 0) return n;
+  cudaLaunchConfig_t lc{};
+  cudaLaunchAttribute attr[1];
+  lc.gridDim = dim3((unsigned)(split * 4 * h->sm_count));
+  lc.blockDim = dim3((unsigned)threads);
+  lc.dynamicSmemBytes = smem;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)split;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  lc.attrs = attr;
+  lc.numAttrs = 1;
+  if (cudaOccupancyMaxActiveClusters(&n, kern, &lc) != cudaSuccess || n <= 0) {
+    cudaGetLastError();
+    n = std::max(1, h->sm_count * (1024 / threads) / split);
+  }
+  return n;
 }
 
+// Enqueue the activation gradient, with the block size and the blocks a cluster
+// (which share a strip's rows) of the shortest estimate: waves x (rows a thread
+// walks x a row's time, which grows with the SMs' load, + a block's start).
+// Fitted on GB300 to 21 sizes (16 to 20000 rows of 64 to 28672) x 24 shapes: 3 % over
+// the fastest on average, 15 % at worst.  For instance, gelu: 4096 x 8192 33.5 us with
+// 128 blocks of 1024, 36.4 with 512 of 256 in clusters of 4, 38.9 with 1024 in clusters
+// of 8; 8192 x 1024 14.3 with 16 clusters of 6 blocks of 1024, 22.8 with clusters of 8,
+// of which the device holds 15; 3000 x 5000 18.4 with clusters of 7 of 256, 21.4 with 8.
 template <int DT>
 gemm_status_t launch_act_grad(gemm_handle* h, gb300::ActGradParams& k, struct CUstream_st* stream) {
-  const ActGradShape s = act_grad_shape(k.M, k.N, h->sm_count);
-  k.row_split = s.split;
-  return launch(s.threads == 256   ? gb300::act_grad_kernel<DT, 256>
-                : s.threads == 512 ? gb300::act_grad_kernel<DT, 512>
-                                   : gb300::act_grad_kernel<DT, 1024>,
-                k, cdiv(k.N, 64) * s.split, s.threads, 0, stream, s.split);
+  typedef void (*Kern)(gb300::ActGradParams);
+  const Kern kerns[3] = {gb300::act_grad_kernel<DT, 1024>, gb300::act_grad_kernel<DT, 512>,
+                         gb300::act_grad_kernel<DT, 256>};
+  const int64_t strips = cdiv(k.N, 64);
+  Kern kern = nullptr;
+  int threads = 0;
+  double best = 0.0;
+  const auto smem = [](int t) { return (size_t)(gb300::kActDepth * 2 * 16 + 32) * t; };
+  {
+    std::lock_guard<std::mutex> guard(h->mu);
+    for (int size = 0; size < 3; ++size) {
+      const int t = 1024 >> size;
+      GB300_CHECK(raise_smem(h, reinterpret_cast<const void*>(kerns[size])));
+      for (int split = 1; split <= 8; ++split) {
+        const int held = act_clusters(h, kerns[size], size, t, smem(t), split);
+        const double full = (double)strips / held;
+        const double waves = full <= 1.0 ? 1.0 : full + 0.156 * (std::ceil(full) - full);
+        const double rows = (double)cdiv(k.M, (int64_t)split * (t / 8));
+        const double load = std::min(1.0, (double)(std::min<int64_t>(strips, held) * split * t) /
+                                              (1024.0 * h->sm_count));
+        const double us = waves * (rows * (0.359 + 1.004 * load) + 1.166) + 0.078 * split +
+                          0.133 * t / 1024.0;
+        if (!kern || us < best) {
+          best = us;
+          kern = kerns[size];
+          threads = t;
+          k.row_split = split;
+        }
+      }
+    }
+  }
+  return launch(kern, k, strips * k.row_split, threads, smem(threads), stream, k.row_split);
 }
 
-// The backward pass's two products as linear calls.  da[M,K] = alpha dz[M,N] b[N,K]
-// (b read N-major) and db[N,K] (+)= alpha dz^T a (both operands M-major).
 gemm_linear_t product_da(const gemm_linear_bwd_t& p, const void* dz, int64_t lddz) {
   gemm_linear_t q{};
   q.M = p.M; q.N = p.K; q.K = p.N;

@@ -234,21 +234,6 @@ __host__ __device__ constexpr int partial_ld(int H) { return (H + 3) & ~3; }
 // reductions.  cp.async's byte count clips the row's end exactly (the rest of
 // the 16 bytes reads as zero).
 
-__device__ __forceinline__ void copy16_async(uint32_t dst, const void* src, int bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
-               :: "r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void copy_commit() {
-  asm volatile("cp.async.commit_group;" ::: "memory");
-}
-// Wait until at most `n` of this thread's latest groups are in flight (n < 4).
-__device__ __forceinline__ void copy_wait(int n) {
-  if (n == 0) asm volatile("cp.async.wait_group 0;" ::: "memory");
-  else if (n == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
-  else if (n == 2) asm volatile("cp.async.wait_group 2;" ::: "memory");
-  else asm volatile("cp.async.wait_group 3;" ::: "memory");
-}
-
 // A thread's slots for one vector of each of its rows: 16-byte pieces of one
 // tensor lie blockDim.x pieces apart, so a warp's pieces are contiguous.
 template <int DT, int VPT>

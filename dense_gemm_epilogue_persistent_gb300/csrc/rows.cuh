@@ -42,6 +42,23 @@ struct RawVec {
   uint4 q[DT == DT_F32 ? 2 : 1];
 };
 
+// Asynchronous copies of 16 bytes to shared memory, `bytes` of them read and the
+// rest zero; a thread waits for its own, all but its latest n groups.
+__device__ __forceinline__ void copy16_async(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+               :: "r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copy_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+// Wait until at most `n` of this thread's latest groups are in flight (n < 4).
+__device__ __forceinline__ void copy_wait(int n) {
+  if (n == 0) asm volatile("cp.async.wait_group 0;" ::: "memory");
+  else if (n == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
+  else if (n == 2) asm volatile("cp.async.wait_group 2;" ::: "memory");
+  else asm volatile("cp.async.wait_group 3;" ::: "memory");
+}
+
 // Elements [c, c + 8) of a row (p 16-byte aligned at c), those at or past `n`
 // read as zero and not touched in memory.
 template <int DT>
