@@ -417,12 +417,12 @@ _CODE_OF = {}           # the same by the dtype object, filled as they are met
 
 def _code(t, what):
     dtype = t.dtype
-    if dtype in _CODE_OF:
-        return _CODE_OF[dtype]
-    code = _TENSOR_CODES.get(str(dtype))
+    code = _CODE_OF.get(dtype)
     if code is None:
-        raise GemmError(GEMM_ERR_UNSUPPORTED_DTYPE, f"{what}: {dtype}")
-    _CODE_OF[dtype] = code
+        code = _TENSOR_CODES.get(str(dtype))
+        if code is None:
+            raise GemmError(GEMM_ERR_UNSUPPORTED_DTYPE, f"{what}: {dtype}")
+        _CODE_OF[dtype] = code
     return code
 
 
@@ -440,24 +440,21 @@ def _rows(t, shape, what, code=None):
         return 0, 0
     if t.shape != shape:
         raise GemmError(GEMM_ERR_INVALID_ARG, f"{what}: shape {tuple(t.shape)}, not {tuple(shape)}")
-    if code is not None and _code(t, what) != code:
+    if code is not None and _CODE_OF.get(t.dtype) != code and _code(t, what) != code:
         raise GemmError(GEMM_ERR_UNSUPPORTED_DTYPE, f"{what}: {t.dtype}")
     s0, s1 = t.stride()
-    if s1 != 1 and shape[1] > 1:
+    M, N = shape
+    if s1 != 1 and N > 1:
         raise GemmError(GEMM_ERR_INVALID_ARG, f"{what}: rows are not contiguous")
-    if shape[0] == 1:
+    if M == 1 and (s0 & 15 or s0 < N):
         # the stride of a single row says nothing: any sufficient aligned one will do
-        s0 = max(s0, (shape[1] + 15) // 16 * 16)
-        s0 = (s0 + 15) // 16 * 16
+        s0 = (max(s0, N) + 15) // 16 * 16
     return t.data_ptr(), s0
 
 
-def _operand(t, shape, what):
+def _operand(t, R, K, what):
     """(address, stride, layout) of an R x K product operand, either dimension contiguous."""
-    if t.shape != shape:
-        raise GemmError(GEMM_ERR_INVALID_ARG, f"{what}: shape {tuple(t.shape)}, not {tuple(shape)}")
     s0, s1 = t.stride()
-    R, K = shape
     if s1 == 1 and not (s0 == 1 and R > 1):
         return t.data_ptr(), s0 if R > 1 else (max(s0, K) + 15) // 16 * 16, GEMM_K_MAJOR
     if s0 == 1 or R == 1:
@@ -476,9 +473,9 @@ def _vector(t, n, what, code=None):
     """Address of a contiguous vector of n elements (of type `code` if given); 0 for None."""
     if t is None:
         return 0
-    if t.shape != (n,) or (n > 1 and t.stride()[0] != 1):
+    if t.shape != (n,) or (t.stride() != (1,) and n > 1):
         raise GemmError(GEMM_ERR_INVALID_ARG, f"{what}: not a contiguous vector of {n}")
-    if code is not None and _code(t, what) != code:
+    if code is not None and _CODE_OF.get(t.dtype) != code and _code(t, what) != code:
         raise GemmError(GEMM_ERR_UNSUPPORTED_DTYPE, f"{what}: {t.dtype}")
     return t.data_ptr()
 
@@ -583,11 +580,12 @@ class Gemm:
         in the C header.  a [M, K] and b [N, K], either dimension contiguous (fp32 ones
         are read at tf32 precision); activation: None, "relu", "gelu", "gelu_tanh" or "silu";
         z receives what the activation is applied to."""
-        shape = _shape(a, "a")
-        M, K = shape
-        N = _shape(b, "b")[0]
-        pa, lda, la = _operand(a, shape, "a")
-        pb, ldb, lb = _operand(b, (N, K), "b")
+        M, K = _shape(a, "a")
+        N, inner = _shape(b, "b")
+        if inner != K:
+            raise GemmError(GEMM_ERR_INVALID_ARG, f"b: shape {(N, inner)}, not {(N, K)}")
+        pa, lda, la = _operand(a, M, K, "a")
+        pb, ldb, lb = _operand(b, N, K, "b")
         out = (M, N)
         st = self._lib.gemm_linear(self.handle, _LINEAR.pack(
             M, N, K, _code(a, "a") or GEMM_TF32, _code(b, "b") or GEMM_TF32,
