@@ -626,11 +626,12 @@ persistent_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
     if constexpr (kPair) return it >= p.first_items;
     else return false;
   };
+  const KernelParams& first_product = p;
   const auto product = [&](int it) -> const KernelParams& {
     if constexpr (kPair) {
       if (it >= p.first_items) return p.second;
     }
-    return p;
+    return first_product;
   };
   const auto number = [&](int it) {
     if constexpr (kPair) return it >= p.first_items ? it - p.first_items : it;
@@ -1160,7 +1161,7 @@ persistent_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
           if (e.bias) col_b = vector_elem(e.bias, col, e.bias_dt);
         }
       };
-      if constexpr (kLinear) {
+      if constexpr (kLinear && !kPair) {
         const int row = tm * G::CM + (int)gm * (G::BM * CG) + (int)rank * G::BM + q * kSubRows + lane;
         row_factor = e.alpha;
         if (e.row_scale && row < P.M) row_factor *= __ldg(e.row_scale + row);
@@ -1359,23 +1360,28 @@ persistent_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
         bool d_end_only = false, y_end_only = false;
         const float al = e.alpha, be = e.beta, xf = e.x_factor;
         if constexpr (kLinear) {
-          // The chunk's column vectors go through shared memory, one column
-          // per lane in, all 32 broadcast out; the next chunk's are fetched
-          // meanwhile.
-          float* const cvec = reinterpret_cast<float*>(gbase + (cvec0 - base)) +
-                              ew * (kColumnVecBytes / 4);
-          cvec[lane] = col_s;
-          cvec[kEpiChunk + lane] = col_b;
-          __syncwarp();
-          if (j + EPW < nchunks) fetch_column(j + EPW);
+          if constexpr (kPair) {
 #pragma unroll
-          for (int k = 0; k < kEpiChunk / 4; ++k) {
-            const float4 s4 = reinterpret_cast<const float4*>(cvec)[k];
-            const float4 b4 = reinterpret_cast<const float4*>(cvec + kEpiChunk)[k];
-            dv[4 * k] = fmaf(__uint_as_float(raw_acc[4 * k]) * row_factor, s4.x, b4.x);
-            dv[4 * k + 1] = fmaf(__uint_as_float(raw_acc[4 * k + 1]) * row_factor, s4.y, b4.y);
-            dv[4 * k + 2] = fmaf(__uint_as_float(raw_acc[4 * k + 2]) * row_factor, s4.z, b4.z);
-            dv[4 * k + 3] = fmaf(__uint_as_float(raw_acc[4 * k + 3]) * row_factor, s4.w, b4.w);
+            for (int i = 0; i < kEpiChunk; ++i) dv[i] = __uint_as_float(raw_acc[i]) * e.alpha;
+          } else {
+            // The chunk's column vectors go through shared memory, one column
+            // per lane in, all 32 broadcast out; the next chunk's are fetched
+            // meanwhile.
+            float* const cvec = reinterpret_cast<float*>(gbase + (cvec0 - base)) +
+                                ew * (kColumnVecBytes / 4);
+            cvec[lane] = col_s;
+            cvec[kEpiChunk + lane] = col_b;
+            __syncwarp();
+            if (j + EPW < nchunks) fetch_column(j + EPW);
+#pragma unroll
+            for (int k = 0; k < kEpiChunk / 4; ++k) {
+              const float4 s4 = reinterpret_cast<const float4*>(cvec)[k];
+              const float4 b4 = reinterpret_cast<const float4*>(cvec + kEpiChunk)[k];
+              dv[4 * k] = fmaf(__uint_as_float(raw_acc[4 * k]) * row_factor, s4.x, b4.x);
+              dv[4 * k + 1] = fmaf(__uint_as_float(raw_acc[4 * k + 1]) * row_factor, s4.y, b4.y);
+              dv[4 * k + 2] = fmaf(__uint_as_float(raw_acc[4 * k + 2]) * row_factor, s4.z, b4.z);
+              dv[4 * k + 3] = fmaf(__uint_as_float(raw_acc[4 * k + 3]) * row_factor, s4.w, b4.w);
+            }
           }
           const int col0 = ncol0 + j * kEpiChunk;
           // The row's last elements, where its end is in this chunk and inside a
@@ -1390,15 +1396,17 @@ persistent_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
             return lo == 0;
           };
           const bool row_end = col0 + kEpiChunk > P.N;
-          if (e.write_y) {
+          if (!kPair && e.write_y) {
             smem_write_row(slot + cd_sub, e.y_dt, 0, lane, dv);
             if (row_end && e.y_ragged) y_end_only = store_end(e.y_ptr, e.ldy, e.y_dt);
           }
-          with_activation(e.act, [&](auto a) {
+          if constexpr (!kPair) {
+            with_activation(e.act, [&](auto a) {
 #pragma unroll
-            for (int i = 0; i < kEpiChunk; i += 2)
-              activate2<decltype(a)::value>(dv[i], dv[i + 1]);
-          });
+              for (int i = 0; i < kEpiChunk; i += 2)
+                activate2<decltype(a)::value>(dv[i], dv[i + 1]);
+            });
+          }
           if (e.read_c)
             smem_row_each(slot, e.c_dt, 0, lane, [&](int i, float c) { dv[i] += c; });
           __syncwarp();                     // every lane has read its residual row

@@ -625,13 +625,13 @@ double pair_time(int64_t first, int64_t second, int64_t halves, int64_t lead, in
 // Plan the two gradients as one launch (h->mu held): both on the persistent
 // kernel with a common tile, the one with more k-blocks a tile first, the last
 // round in half-width items where that fits.  One launch wherever each would
-// take the persistent kernel anyway (1001 x 2003 x 1501 fp16 18.3 us, 26.4 as two;
-// 600 x 600 x 600 7.5, 13.4; 3000 x 5000 x 4096 bf16 147, 176, with db in fp32 and added to
-// 158, 201): a launch's start and end, and the last wave's idle SMs, are paid once.
-// Where one would take split-K, by the estimates (128 x 1024 x 4096 bf16 11.7 us in one,
-// 16.9; 300 x 4096 x 1024 22 planned as two, 17.5).  Fewer than 128 tokens stay two
-// launches: db's items are then one or two k-blocks long, which the estimate does
-// not hold for (64 x 4096 x 4096: 36 as it would choose, 31; 1 x 8192 x 2048: 43, 30).
+// take the persistent kernel anyway (1001 x 2003 x 1501 fp16 17.4 us, 26.4 as two;
+// 600 x 600 x 600 7.2, 13.4; 3000 x 5000 x 4096 bf16 142, 164, with db in fp32 and added to
+// 154, 205): a launch's start and end, and the last wave's idle SMs, are paid once.
+// Where one would take split-K, by the estimates (5000 x 768 x 768 bf16 19.9 us in one,
+// 28.4; 128 x 8192 x 512 27.3, 20.4).  Fewer than 128 tokens stay two launches: db's
+// items are then one or two k-blocks long, which the estimate does not hold for
+// (64 x 4096 x 4096: 36 as it would choose, 31; 1 x 8192 x 2048: 43, 30).
 gemm_status_t plan_pair(gemm_handle* h, const gemm_linear_t& da, const gemm_linear_t& db,
                         PairPlan& out) {
   out.one = false;
@@ -726,7 +726,9 @@ gemm_status_t plan_pair(gemm_handle* h, const gemm_linear_t& da, const gemm_line
     const double bytes = 2.0 * ((double)da.M * (double)da.K * 2.0 + (double)da.M * (double)da.N * 3.0 +
                                 (double)db.M * (double)db.N * 2.0) +
                          (db.R ? 6.0 * (double)db.M * (double)db.N : 0.0);
-    out.one = 6.48 + best + 0.174 * bytes / 6.3e6 < alone;
+    // (two launches take 1.17 times their estimates; of 30 problems, among them 128 x 8192 x
+    // 512 and 20000 x 512 x 512 where two are faster, none is then decided wrongly)
+    out.one = 6.48 + best + 0.174 * bytes / 6.3e6 < 1.17 * alone;
   }
   return GEMM_OK;
 }
