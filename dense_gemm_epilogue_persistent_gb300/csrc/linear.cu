@@ -687,6 +687,7 @@ gemm_status_t plan_pair(gemm_handle* h, const gemm_linear_t& da, const gemm_line
                             dtype_bytes(p.d_type) + (p.R ? dtype_bytes(p.r_type) : 0));
         }
         const int64_t n1 = each[0].tiles, n2 = each[1].tiles;
+        if (n1 + n2 > INT32_MAX / 2) continue;
         // All SMs' operand loads at the 16.3 TB/s that they come to together.
         const double l2_us = (double)(n1 * cdiv(first.K, 64) + n2 * cdiv(second.K, 64)) *
                              (double)(cg * 128 + bn) * 128.0 / 16.3e6;
@@ -696,7 +697,7 @@ gemm_status_t plan_pair(gemm_handle* h, const gemm_linear_t& da, const gemm_line
         const int64_t from = n1 % clusters;
         const int64_t most =
             from ? std::min<int64_t>(n2 / (clusters - from), (int64_t)(us[0] / us[1]) + 1) : 0;
-        for (int64_t rounds = 0; rounds <= most; ++rounds) {
+        for (int64_t rounds = 0; rounds <= most; rounds += 1 + most / 32) {
           const int64_t lead = rounds * (clusters - from), rem = (n2 - lead) % clusters;
           for (const int64_t split : {(int64_t)0, may_split && 2 * rem <= clusters ? rem : 0}) {
             const double longest =
