@@ -151,7 +151,8 @@ struct KernelParams {
 // these are, the rest the second's.  num_items counts both; the tile, the ring
 // and the slots are common.  The first's items are dealt to the clusters in
 // turn; of the second's, lead_items go to the clusters from lead_from on, which
-// got one of the first's less, and the rest again to all in turn.
+// got one of the first's less, and the rest again to all in turn.  (With no
+// second product: a single one without column vectors, activation and z.)
 struct PairParams : KernelParams {
   KernelParams second;
   int first_items, lead_items, lead_from;
@@ -753,9 +754,11 @@ persistent_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
     if (p.epi.read_c) prefetch_tensormap(&tmC);
     if (p.epi.read_x) prefetch_tensormap(&tmX);
     if constexpr (kPair) {
-      prefetch_tensormap(&p.a2);
-      prefetch_tensormap(&p.b2);
-      prefetch_tensormap(&p.d2);
+      if (p.first_items < p.num_items) {
+        prefetch_tensormap(&p.a2);
+        prefetch_tensormap(&p.b2);
+        prefetch_tensormap(&p.d2);
+      }
     }
   }
   if (warp == 1) {

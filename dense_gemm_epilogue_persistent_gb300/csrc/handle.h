@@ -63,12 +63,13 @@ struct SplitPlan {           // split-K kernel: tokens, features and CTAs of a t
 struct LinearKey {
   int64_t M, N, K;
   uint64_t config_gen;
-  int a_type, b_type, r_type, z_type, d_type, layoutA, layoutB, activation, has_r, has_z;
+  int a_type, b_type, r_type, z_type, d_type, layoutA, layoutB, activation, has_r, has_z, plain;
 };
 struct LinearPlan {
   bool valid = false;
   LinearKey key;
   bool split = false;        // the split-K kernel, else the persistent one
+  bool plain = false;        // ... the latter as the first of two products (is_plain)
   double us = 0.0;           // the estimate that it was chosen by
   SplitPlan s{};
   gemm_config_t cfg{};

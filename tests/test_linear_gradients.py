@@ -1,5 +1,5 @@
-"""The linear layer's two gradients in one launch, against 64 bits (tolerances as in
-test_linear): either product first, several rounds of tiles, extra rounds for the
+"""The linear layer's two gradients in one launch, and its products with nothing behind
+them, which run on the same kernel, against 64 bits (tolerances as in test_linear): either product first, several rounds of tiles, extra rounds for the
 clusters with one tile less, half-width last rounds, every tile shape, and rows
 that end inside a 16-byte piece."""
 import pytest
@@ -105,5 +105,29 @@ def test_rows_ending_inside_a_piece(gemm, N, d_t, z_t):
     gemm.set_config(cta_group=1, tile_n=64)
     try:
         _check_forward(gemm, 150, N, 40, "f16", d_t=d_t, z_t=z_t, act="gelu", r_t="f16")
+    finally:
+        gemm.set_config(None)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M,N,K", [(300, 1003, 520), (1200, 1100, 64), (2100, 700, 301), (150, 7, 8),
+                                   (129, 4000, 1)])
+@pytest.mark.parametrize("ab,d_t,r_t", [("bf16", "bf16", None), ("f16", "f32", None),
+                                        ("bf16", "f16", "f32"), ("f16", "f32", "bf16")])
+def test_products_with_nothing_behind(gemm, M, N, K, ab, d_t, r_t):
+    _check_forward(gemm, M, N, K, ab, d_t=d_t, bias_t=None, r_t=r_t, alpha=0.75)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("cfg", [dict(cta_group=1, tile_n=64), dict(cta_group=1, tile_n=256),
+                                 dict(cta_group=2, tile_n=96), dict(cta_group=2, tile_n=256),
+                                 dict(cta_group=2, tile_n=128, epi_warps=1)])
+def test_products_with_nothing_behind_forced(gemm, cfg):
+    """One shape through both kernels in turn: each by its own plan."""
+    gemm.set_config(**cfg)
+    try:
+        for bias_t, r_t in ((None, None), ("f32", None), (None, "bf16"), ("bf16", "bf16")):
+            _check_forward(gemm, 1000, 1500, 136, "bf16", bias_t=bias_t, r_t=r_t,
+                           in_place=r_t is not None)
     finally:
         gemm.set_config(None)
