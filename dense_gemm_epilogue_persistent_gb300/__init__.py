@@ -426,6 +426,15 @@ def _code(t, what):
     return code
 
 
+def _elsewhere(t, what, device):
+    """The error for a tensor that is not in the memory of GPU `device`: a kernel would follow
+    its address all the same.  (A tensor that does not say where it is, without get_device,
+    is taken to be there.)"""
+    index = t.get_device()
+    where = "the host" if index < 0 else f"GPU {index}"
+    return GemmError(GEMM_ERR_INVALID_ARG, f"{what}: on {where}, not on GPU {device}")
+
+
 def _shape(t, what):
     shape = t.shape
     if len(shape) != 2:
@@ -433,11 +442,16 @@ def _shape(t, what):
     return shape
 
 
-def _rows(t, shape, what, code=None):
-    """(address, row stride) of a matrix of that shape whose rows are contiguous, of type
-    `code` if given; (0, 0) for None."""
+def _rows(t, shape, what, device, code=None):
+    """(address, row stride) of a matrix of that shape whose rows are contiguous, on GPU
+    `device` and of type `code` if given; (0, 0) for None."""
     if t is None:
         return 0, 0
+    try:
+        if t.get_device() != device:
+            raise _elsewhere(t, what, device)
+    except AttributeError:
+        pass
     if t.shape != shape:
         raise GemmError(GEMM_ERR_INVALID_ARG, f"{what}: shape {tuple(t.shape)}, not {tuple(shape)}")
     if code is not None and _CODE_OF.get(t.dtype) != code and _code(t, what) != code:
@@ -452,8 +466,14 @@ def _rows(t, shape, what, code=None):
     return t.data_ptr(), s0
 
 
-def _operand(t, R, K, what):
-    """(address, stride, layout) of an R x K product operand, either dimension contiguous."""
+def _operand(t, R, K, what, device):
+    """(address, stride, layout) of an R x K product operand on GPU `device`, either
+    dimension contiguous."""
+    try:
+        if t.get_device() != device:
+            raise _elsewhere(t, what, device)
+    except AttributeError:
+        pass
     s0, s1 = t.stride()
     if s1 == 1 and not (s0 == 1 and R > 1):
         return t.data_ptr(), s0 if R > 1 else (max(s0, K) + 15) // 16 * 16, GEMM_K_MAJOR
@@ -469,10 +489,16 @@ def _activation(name):
         raise GemmError(GEMM_ERR_INVALID_ARG, f"activation {name!r}") from None
 
 
-def _vector(t, n, what, code=None):
-    """Address of a contiguous vector of n elements (of type `code` if given); 0 for None."""
+def _vector(t, n, what, device, code=None):
+    """Address of a contiguous vector of n elements on GPU `device` (of type `code` if given);
+    0 for None."""
     if t is None:
         return 0
+    try:
+        if t.get_device() != device:
+            raise _elsewhere(t, what, device)
+    except AttributeError:
+        pass
     if t.shape != (n,) or (t.stride() != (1,) and n > 1):
         raise GemmError(GEMM_ERR_INVALID_ARG, f"{what}: not a contiguous vector of {n}")
     if code is not None and _CODE_OF.get(t.dtype) != code and _code(t, what) != code:
@@ -484,13 +510,14 @@ class Gemm:
     """Owns one library handle on `device`.
 
     run, run_host: the C entry points' arguments.  rmsnorm, rmsnorm_bwd, linear,
-    linear_bwd: the operators around the product on tensors (torch's or any with data_ptr, dtype, shape and
-    stride), whose types, sizes and row strides the calls read off and check; outputs
-    are the caller's tensors too.  Tensors are used on `stream` (None: the default
-    stream) and must be ready there."""
+    linear_bwd: the operators around the product on tensors (torch's or any with
+    data_ptr, dtype, shape and stride), whose device, types, sizes and row strides the
+    calls read off and check; outputs are the caller's tensors too.
+    Tensors are used on `stream` (None: the default stream) and must be ready there."""
 
     def __init__(self, device: int = 0):
         self.handle = gemm_create(device)
+        self.device = int(device)
         self._lib = library()
 
     def close(self):
@@ -545,12 +572,13 @@ class Gemm:
         `scale`; `h` receives x + residual, `rstd` the rows' factors."""
         shape = _shape(x, "x")
         M, H = shape
-        t = _code(x, "x")
+        t, dev = _code(x, "x"), self.device
         st = self._lib.gemm_rmsnorm(self.handle, _RMSNORM.pack(
-            M, H, t, _code(weight, "weight"), _code(y, "y"), eps, *_rows(x, shape, "x"),
-            *_rows(residual, shape, "residual", t), _vector(weight, H, "weight"),
-            *_rows(h, shape, "h", t), *_rows(y, shape, "y"), _vector(scale, M, "scale", GEMM_F32),
-            _vector(rstd, M, "rstd", GEMM_F32)), stream and _stream(stream))
+            M, H, t, _code(weight, "weight"), _code(y, "y"), eps, *_rows(x, shape, "x", dev),
+            *_rows(residual, shape, "residual", dev, t), _vector(weight, H, "weight", dev),
+            *_rows(h, shape, "h", dev, t), *_rows(y, shape, "y", dev),
+            _vector(scale, M, "scale", dev, GEMM_F32), _vector(rstd, M, "rstd", dev, GEMM_F32)),
+            stream and _stream(stream))
         if st:
             raise GemmError(st, "gemm_rmsnorm")
 
@@ -561,15 +589,21 @@ class Gemm:
         gemm_rmsnorm_bwd_workspace(M, H) bytes."""
         shape = _shape(dy, "dy")
         M, H = shape
-        t = _code(dy, "dy")
+        t, dev = _code(dy, "dy"), self.device
         ws, nbytes = None, 0
         if workspace is not None:
+            try:
+                if workspace.get_device() != dev:
+                    raise _elsewhere(workspace, "workspace", dev)
+            except AttributeError:
+                pass
             ws, nbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
         st = self._lib.gemm_rmsnorm_bwd(self.handle, _RMSNORM_BWD.pack(
-            M, H, t, _code(weight, "weight"), _code(dweight, "dweight"), *_rows(dy, shape, "dy"),
-            *_rows(h, shape, "h", t), _vector(weight, H, "weight"),
-            _vector(rstd, M, "rstd", GEMM_F32), *_rows(dh, shape, "dh", t),
-            *_rows(dx, shape, "dx", t), _vector(dweight, H, "dweight")), ws, nbytes,
+            M, H, t, _code(weight, "weight"), _code(dweight, "dweight"),
+            *_rows(dy, shape, "dy", dev), *_rows(h, shape, "h", dev, t),
+            _vector(weight, H, "weight", dev), _vector(rstd, M, "rstd", dev, GEMM_F32),
+            *_rows(dh, shape, "dh", dev, t), *_rows(dx, shape, "dx", dev, t),
+            _vector(dweight, H, "dweight", dev)), ws, nbytes,
             stream and _stream(stream))
         if st:
             raise GemmError(st, "gemm_rmsnorm_bwd")
@@ -584,17 +618,19 @@ class Gemm:
         N, inner = _shape(b, "b")
         if inner != K:
             raise GemmError(GEMM_ERR_INVALID_ARG, f"b: shape {(N, inner)}, not {(N, K)}")
-        pa, lda, la = _operand(a, M, K, "a")
-        pb, ldb, lb = _operand(b, N, K, "b")
+        dev = self.device
+        pa, lda, la = _operand(a, M, K, "a", dev)
+        pb, ldb, lb = _operand(b, N, K, "b", dev)
         out = (M, N)
         st = self._lib.gemm_linear(self.handle, _LINEAR.pack(
             M, N, K, _code(a, "a") or GEMM_TF32, _code(b, "b") or GEMM_TF32,
             0 if bias is None else _code(bias, "bias"),
             0 if residual is None else _code(residual, "residual"),
             0 if z is None else _code(z, "z"), _code(d, "d"), la, lb, _activation(activation), alpha,
-            pa, lda, pb, ldb, _vector(row_scale, M, "row_scale", GEMM_F32),
-            _vector(col_scale, N, "col_scale", GEMM_F32), _vector(bias, N, "bias"),
-            *_rows(residual, out, "residual"), *_rows(z, out, "z"), *_rows(d, out, "d")),
+            pa, lda, pb, ldb, _vector(row_scale, M, "row_scale", dev, GEMM_F32),
+            _vector(col_scale, N, "col_scale", dev, GEMM_F32), _vector(bias, N, "bias", dev),
+            *_rows(residual, out, "residual", dev), *_rows(z, out, "z", dev),
+            *_rows(d, out, "d", dev)),
             stream and _stream(stream))
         if st:
             raise GemmError(st, "gemm_linear")
@@ -606,14 +642,15 @@ class Gemm:
         out = _shape(dd, "dd")
         M, N = out
         K = _shape(a, "a")[1]
-        t = _code(dd, "dd")
+        t, dev = _code(dd, "dd"), self.device
         rows_a, rows_b = (M, K), (N, K)
         st = self._lib.gemm_linear_bwd(self.handle, _LINEAR_BWD.pack(
             M, N, K, t, 0 if da is None else _code(da, "da"), 0 if db is None else _code(db, "db"),
             0 if dbias is None else _code(dbias, "dbias"), _activation(activation),
-            int(accumulate), alpha, *_rows(dd, out, "dd"), *_rows(z, out, "z", t),
-            *_rows(a, rows_a, "a", t), *_rows(b, rows_b, "b", t), *_rows(dz, out, "dz", t),
-            *_rows(da, rows_a, "da"), *_rows(db, rows_b, "db"), _vector(dbias, N, "dbias")),
+            int(accumulate), alpha, *_rows(dd, out, "dd", dev), *_rows(z, out, "z", dev, t),
+            *_rows(a, rows_a, "a", dev, t), *_rows(b, rows_b, "b", dev, t),
+            *_rows(dz, out, "dz", dev, t), *_rows(da, rows_a, "da", dev),
+            *_rows(db, rows_b, "db", dev), _vector(dbias, N, "dbias", dev)),
             stream and _stream(stream))
         if st:
             raise GemmError(st, "gemm_linear_bwd")

@@ -1,0 +1,112 @@
+"""Arguments of the layer operators that no kernel may be given: each is refused on the host
+before anything is enqueued.  Those that are somewhere else are tested with a library that
+counts its calls."""
+import inspect
+
+import pytest
+import torch
+
+import dense_gemm_epilogue_persistent_gb300 as G
+
+
+class Placed:
+    """A CPU tensor that says it is on GPU `index`."""
+
+    def __init__(self, t, index):
+        self._t, self._index = t, index
+
+    def get_device(self):
+        return self._index
+
+    def __getattr__(self, name):
+        return getattr(self._t, name)
+
+
+class Library:
+    """A library whose calls succeed and are counted."""
+    calls = 0
+
+    def __getattr__(self, name):
+        def call(*args):
+            self.calls += 1
+            return G.GEMM_OK
+        return call
+
+
+def _handle(lib, device=0):
+    g = object.__new__(G.Gemm)
+    g.handle, g.device, g._lib = None, device, lib
+    return g
+
+
+def _calls():
+    """(method, its tensors by name), every optional one given."""
+    e = lambda *s, dt=torch.float16: torch.zeros(*s, dtype=dt)
+    f = lambda n: torch.zeros(n)
+    m, n = e(4, 64), e(4, 32)
+    return [
+        ("rmsnorm", dict(x=m, weight=e(64), y=e(4, 64, dt=torch.float8_e4m3fn), residual=m, h=m,
+                         scale=f(4), rstd=f(4))),
+        ("rmsnorm_bwd", dict(dy=m, h=m, weight=e(64), rstd=f(4), dx=m, dweight=f(64), dh=m,
+                             workspace=e(4096))),
+        ("linear", dict(a=m, b=e(32, 64), d=n, bias=f(32), residual=n, z=n, row_scale=f(4),
+                        col_scale=f(32))),
+        ("linear_bwd", dict(dd=n, a=m, b=e(32, 64), z=n, dz=n, da=m, db=e(32, 64), dbias=f(32))),
+    ]
+
+
+TENSORS = [(name, k) for name, kw in _calls() for k in kw]
+
+
+@pytest.mark.parametrize("name,wrong", TENSORS)
+@pytest.mark.parametrize("where", [-1, 1])
+def test_a_tensor_elsewhere_is_refused(name, wrong, where):
+    """On the host, or on another GPU than the handle's."""
+    kw = {k: Placed(t, where if k == wrong else 0) for k, t in dict(_calls())[name].items()}
+    lib = Library()
+    with pytest.raises(G.GemmError) as e:
+        getattr(_handle(lib), name)(**kw)
+    assert e.value.status == G.GEMM_ERR_INVALID_ARG and wrong in str(e.value)
+    assert lib.calls == 0
+
+
+@pytest.mark.parametrize("name", [name for name, _ in _calls()])
+@pytest.mark.parametrize("device", [0, 3])
+def test_tensors_on_the_handle_s_gpu_are_taken(name, device):
+    """... and those that do not say where they are."""
+    lib = Library()
+    tensors = dict(_calls())[name]
+    getattr(_handle(lib, device), name)(**{k: Placed(t, device) for k, t in tensors.items()})
+
+    class Silent:
+        def __init__(self, t):
+            for attr in ("data_ptr", "dtype", "shape", "stride", "numel", "element_size"):
+                setattr(self, attr, getattr(t, attr))
+
+    getattr(_handle(lib, device), name)(**{k: Silent(t) for k, t in tensors.items()})
+    assert lib.calls == 2
+
+
+def test_every_tensor_argument_is_covered():
+    for name, kw in _calls():
+        other = {"self", "eps", "stream", "activation", "alpha", "accumulate"}
+        assert set(kw) == set(inspect.signature(getattr(G.Gemm, name)).parameters) - other
+
+
+@pytest.mark.gpu
+def test_host_tensors_are_refused_by_a_real_handle():
+    """Each tensor in turn left on the host, pinned or not."""
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    g = G.Gemm(0)
+    try:
+        for name, kw in _calls():
+            for wrong in kw:
+                for host in (kw[wrong], kw[wrong].pin_memory()):
+                    with pytest.raises(G.GemmError) as e:
+                        getattr(g, name)(**{k: host if k == wrong else t.cuda()
+                                            for k, t in kw.items()})
+                    assert e.value.status == G.GEMM_ERR_INVALID_ARG and wrong in str(e.value)
+        assert g.sync_status()[0] == G.GEMM_OK
+    finally:
+        g.close()
