@@ -137,8 +137,11 @@ bool aligned_to(const void* p, int bytes) {
   return (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(bytes - 1)) == 0;
 }
 
-// Sizes the kernels index with 32 bits, and tensor-map strides below 2^40 bytes.
-bool extent_ok(int64_t v) { return v >= 0 && v <= INT32_MAX; }
+// Sizes the kernels index with 32 bits: what they add to an index on the way to its
+// bound (the rest of the last tile, whose width need not divide 2^31; a vector's
+// end; a cluster's shares of the rows) stays below 2^31.
+bool is_extent(int64_t v) { return v >= 0 && v <= INT32_MAX - 8192; }
+// Tensor-map strides below 2^40 bytes.
 bool map_ok(int64_t ld, int64_t rows, int dt) {
   return (double)ld * dtype_bytes(dt) * (double)rows < 1099511627776.0;
 }
@@ -150,7 +153,7 @@ gemm_status_t check_operand(const void* p, int64_t ld, int64_t inner, int64_t ro
 }
 
 gemm_status_t check_linear(const gemm_linear_t& p) {
-  if (!extent_ok(p.M) || !extent_ok(p.N) || !extent_ok(p.K)) return GEMM_ERR_INVALID_ARG;
+  if (!is_extent(p.M) || !is_extent(p.N) || !is_extent(p.K)) return GEMM_ERR_INVALID_ARG;
   if (!is_layout(p.layoutA) || !is_layout(p.layoutB) || !is_activation(p.activation))
     return GEMM_ERR_INVALID_ARG;
   if (!is_ab_type(p.a_type) || !is_ab_type(p.b_type) ||
@@ -902,7 +905,7 @@ const void* dz_of(const gemm_linear_bwd_t& p, int64_t& ld) {
 }
 
 gemm_status_t check_linear_bwd(const gemm_linear_bwd_t& p) {
-  if (!extent_ok(p.M) || !extent_ok(p.N) || !extent_ok(p.K) || !is_activation(p.activation))
+  if (!is_extent(p.M) || !is_extent(p.N) || !is_extent(p.K) || !is_activation(p.activation))
     return GEMM_ERR_INVALID_ARG;
   if (p.type != GEMM_F16 && p.type != GEMM_BF16) return GEMM_ERR_UNSUPPORTED_DTYPE;
   if ((p.da && !is_epi_type(p.da_type)) || (p.db && !is_epi_type(p.db_type)) ||

@@ -395,11 +395,13 @@ gemm_status_t gemm_run_noalloc(int64_t M, int64_t N, int64_t K, int64_t L,
  * All of them: tensors are device memory of the handle's device, owned by the
  * caller; matrices are row-major with a leading dimension (row stride, in
  * elements) of their own, which may exceed the row length; every matrix and
- * weight vector starts on a 16-byte boundary and every leading dimension times its element size is a multiple of 16
- * bytes (GEMM_ERR_MISALIGNED otherwise), while the sizes themselves may be
- * odd; bias and scale vectors need their elements' alignment only.  Calls validate on the host, enqueue on `stream` and return; they
- * neither synchronise nor allocate, keep nothing between calls, and may be
- * captured into a CUDA graph.  Sums and statistics are fp32 in a fixed order:
+ * weight vector starts on a 16-byte boundary and every leading dimension times
+ * its element size is a multiple of 16 bytes (GEMM_ERR_MISALIGNED otherwise),
+ * while the sizes themselves may be odd; bias and scale vectors need their
+ * elements' alignment only.  Sizes are at most 2^31 - 8193, a normalisation's
+ * rows 2^31 - 1 (GEMM_ERR_INVALID_ARG above).  Calls validate on the host,
+ * enqueue on `stream` and return; they neither synchronise nor allocate, keep
+ * nothing between calls, and may be captured into a CUDA graph.  Sums and statistics are fp32 in a fixed order:
  * the same call gives the same bits.  Any overlap between an output and
  * another tensor that is not named as allowed is undefined. */
 

@@ -110,3 +110,42 @@ def test_host_tensors_are_refused_by_a_real_handle():
         assert g.sync_status()[0] == G.GEMM_OK
     finally:
         g.close()
+
+
+# ------------------------------------------------------------------ the C entry points' checks
+
+@pytest.fixture(scope="module")
+def lib():
+    from dense_gemm_epilogue_persistent_gb300 import build as B
+    B.build()
+    return G.library()
+
+
+P = [(i + 1) << 20 for i in range(10)]     # fake, aligned device addresses
+LARGEST = (1 << 31) - 8193
+
+
+def _linear(**kw):
+    base = dict(M=4, N=64, K=64, a_type=G.GEMM_F16, b_type=G.GEMM_F16, d_type=G.GEMM_F16,
+                activation=G.GEMM_ACT_GELU, alpha=1.0, A=P[0], B=P[1], bias=P[2], D=P[3])
+    base.update(kw)
+    up = lambda n: (n + 15) // 16 * 16
+    return G.gemm_linear_t(lda=up(base["K"]), ldb=up(base["K"]), ldd=up(base["N"]), **base)
+
+
+def _linear_bwd(**kw):
+    base = dict(M=4, N=64, K=64, type=G.GEMM_F16, activation=G.GEMM_ACT_GELU, alpha=1.0,
+                dd=P[0], z=P[1], a=P[2], b=P[3], dz=P[4], da=P[5], db=P[6], dbias=P[7])
+    base.update(kw)
+    up = lambda n: (n + 15) // 16 * 16
+    n, k = up(base["N"]), up(base["K"])
+    return G.gemm_linear_bwd_t(lddd=n, ldz=n, lda=k, ldb=k, lddz=n, ldda=k, lddb=k, **base)
+
+
+@pytest.mark.parametrize("size", "MNK")
+def test_sizes_end_before_a_32_bit_index_could_wrap(lib, size):
+    """Kernels go on to the end of the last tile, whose width need not divide 2^31."""
+    for make, check in ((_linear, G.gemm_linear_check), (_linear_bwd, G.gemm_linear_bwd_check)):
+        for n, code in ((LARGEST, G.GEMM_OK), (LARGEST + 1, G.GEMM_ERR_INVALID_ARG),
+                        ((1 << 31) - 1, G.GEMM_ERR_INVALID_ARG)):
+            assert check(make(**{size: n})) == code, (check, n)
