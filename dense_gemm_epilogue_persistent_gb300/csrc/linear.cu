@@ -133,10 +133,6 @@ using namespace gb300host;
 
 bool is_activation(int a) { return a >= GEMM_ACT_NONE && a <= GEMM_ACT_SILU; }
 
-bool aligned_to(const void* p, int bytes) {
-  return (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(bytes - 1)) == 0;
-}
-
 // Sizes the kernels index with 32 bits: what they add to an index on the way to its
 // bound (the rest of the last tile, whose width need not divide 2^31; a vector's
 // end; a cluster's shares of the rows) stays below 2^31.

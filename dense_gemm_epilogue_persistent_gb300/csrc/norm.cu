@@ -624,6 +624,7 @@ gemm_status_t check_rmsnorm(const gemm_rmsnorm_t& p) {
   if (!aligned16(p.weight)) return GEMM_ERR_MISALIGNED;
   // an 8-bit output has a scale per row, and only it
   if (is_fp8(p.y_type) != (p.scale != nullptr)) return GEMM_ERR_INVALID_ARG;
+  if (!aligned_to(p.scale, 4) || !aligned_to(p.rstd, 4)) return GEMM_ERR_MISALIGNED;
   // in place: element for element only
   if (p.h && ((p.h == p.x && p.ldh != p.ldx) || (p.h == p.r && p.ldh != p.ldr)))
     return GEMM_ERR_INVALID_ARG;
@@ -645,7 +646,7 @@ gemm_status_t check_rmsnorm_bwd(const gemm_rmsnorm_bwd_t& p) {
     GB300_CHECK(check_matrix(p.dx, p.lddx, p.H, p.type));
     if (p.dh) GB300_CHECK(check_matrix(p.dh, p.lddh, p.H, p.type));
     if (!p.weight || !p.rstd) return GEMM_ERR_INVALID_ARG;
-    if (!aligned16(p.weight)) return GEMM_ERR_MISALIGNED;
+    if (!aligned16(p.weight) || !aligned_to(p.rstd, 4)) return GEMM_ERR_MISALIGNED;
     if (p.dx == p.h || p.dx == p.dy || (p.dh && p.dx == p.dh && p.lddx != p.lddh))
       return GEMM_ERR_INVALID_ARG;
   }

@@ -1,6 +1,8 @@
 // Host helpers of the row and column operators: argument checks and launches.
 #pragma once
 
+#include <cstdint>
+
 #include "gemm_gb300.h"
 #include "handle.h"
 #include "rows.cuh"
@@ -16,6 +18,10 @@ inline int device_dt(int t) {
     case GEMM_E4M3: return gb300::DT_E4M3;
     default: return gb300::DT_E5M2;
   }
+}
+
+inline bool aligned_to(const void* p, int bytes) {
+  return (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(bytes - 1)) == 0;
 }
 
 // One matrix argument: present where required, at least `cols` wide, its base

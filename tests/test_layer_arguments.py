@@ -149,3 +149,19 @@ def test_sizes_end_before_a_32_bit_index_could_wrap(lib, size):
         for n, code in ((LARGEST, G.GEMM_OK), (LARGEST + 1, G.GEMM_ERR_INVALID_ARG),
                         ((1 << 31) - 1, G.GEMM_ERR_INVALID_ARG)):
             assert check(make(**{size: n})) == code, (check, n)
+
+
+@pytest.mark.parametrize("at", [1, 2, 3])
+def test_row_factors_off_their_elements_are_refused(lib, at):
+    """rstd and scale are read and written as 4-byte elements."""
+    fwd = dict(M=4, H=64, type=G.GEMM_BF16, w_type=G.GEMM_BF16, y_type=G.GEMM_E4M3, eps=1e-6, x=P[0],
+               ldx=64, weight=P[1], y=P[2], ldy=64, scale=P[3], rstd=P[4])
+    bwd = dict(M=4, H=64, type=G.GEMM_BF16, w_type=G.GEMM_BF16, dw_type=G.GEMM_F32, dy=P[0], lddy=64,
+               h=P[1], ldh=64, weight=P[2], rstd=P[3], dx=P[4], lddx=64, dweight=P[5])
+    for make, check, base, names in (
+            (G.gemm_rmsnorm_t, G.gemm_rmsnorm_check, fwd, ("scale", "rstd")),
+            (G.gemm_rmsnorm_bwd_t, G.gemm_rmsnorm_bwd_check, bwd, ("rstd",))):
+        assert check(make(**base)) == G.GEMM_OK
+        for name in names:
+            assert check(make(**{**base, name: base[name] + 4})) == G.GEMM_OK
+            assert check(make(**{**base, name: base[name] + at})) == G.GEMM_ERR_MISALIGNED
