@@ -25,6 +25,12 @@ __device__ __forceinline__ float min_abs(float x, float m) {
   asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(fabsf(x)), "f"(m));
   return y;
 }
+// max(x, 0), NaN where x is (fmaxf would drop it).
+__device__ __forceinline__ float max_zero(float x) {
+  float y;
+  asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(y) : "f"(x));
+  return y;
+}
 
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -64,7 +70,7 @@ __device__ __forceinline__ float gelu_tanh_arg(float v) {
 
 template <int ACT>
 __device__ __forceinline__ float activate(float v) {
-  if constexpr (ACT == ACT_RELU) return fmaxf(v, 0.f);
+  if constexpr (ACT == ACT_RELU) return max_zero(v);
   if constexpr (ACT == ACT_GELU) {
     float cdf, e;
     normal_cdf_exp(v, min_abs(v, 20.f), cdf, e);
@@ -79,7 +85,7 @@ __device__ __forceinline__ float activate(float v) {
 // the last bit of fp32; the factors of v are held there.
 template <int ACT>
 __device__ __forceinline__ float activate_grad(float v) {
-  if constexpr (ACT == ACT_RELU) return v > 0.f ? 1.f : 0.f;
+  if constexpr (ACT == ACT_RELU) return v > 0.f ? 1.f : v <= 0.f ? 0.f : v;
   if constexpr (ACT == ACT_GELU) {
     const float a = min_abs(v, 20.f);
     float cdf, e;

@@ -474,7 +474,8 @@ gemm_status_t gemm_rmsnorm_bwd(gemm_handle_t h, const gemm_rmsnorm_bwd_t* p, voi
                                int64_t workspace_bytes, struct CUstream_st* stream);
 
 /* Activations: max(z, 0); z Phi(z) with the normal distribution function;
- * z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2; z / (1 + exp(-z)). */
+ * z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2; z / (1 + exp(-z)).  A NaN stays
+ * a NaN in each and in its derivative. */
 typedef enum {
   GEMM_ACT_NONE = 0, GEMM_ACT_RELU = 1, GEMM_ACT_GELU = 2, GEMM_ACT_GELU_TANH = 3,
   GEMM_ACT_SILU = 4

@@ -1,0 +1,70 @@
+"""The layer operators on values where arithmetic goes wrong first.
+
+A pre-activation reaches the activation exactly as a test gives it: as the bias of a
+product of zeros (forward), and as z (backward)."""
+import pytest
+import torch
+
+import dense_gemm_epilogue_persistent_gb300 as G
+import layer_oracle as O
+
+pytestmark = pytest.mark.gpu
+ACTS = ["none", "relu", "gelu", "gelu_tanh", "silu"]
+NAMES = {torch.float32: "f32", torch.float16: "f16", torch.bfloat16: "bf16"}
+ROWS = [1, 40, 300]          # the split-K kernel with one and with several CTAs, the persistent one
+
+
+@pytest.fixture(scope="module")
+def gemm():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    h = G.Gemm(0)
+    yield h
+    h.close()
+
+
+def _forward(gemm, z, act, rows, dtype=torch.float32, K=64):
+    """(act(z), z) as the layer computes them, on the last of `rows` rows."""
+    a = torch.zeros(rows, K, dtype=torch.float16, device="cuda")
+    b = torch.zeros(len(z), K, dtype=torch.float16, device="cuda")
+    d, kept = (O.strided(torch.zeros(rows, len(z)), t)[0] for t in (NAMES[dtype], "f32"))
+    gemm.linear(a, b, d, bias=z.cuda(), activation=act, z=kept)
+    assert gemm.sync_status()[0] == G.GEMM_OK
+    return d[rows - 1].cpu(), kept[rows - 1].cpu()
+
+
+def _slope(gemm, z, act, rows=3):
+    """act'(z) as the backward pass computes it, in z's type, on the last of `rows` rows."""
+    t = NAMES[z.dtype]
+    zs, dz, one = (O.strided(v.expand(rows, len(z)), t)[0] for v in (z, 0 * z, torch.ones_like(z)))
+    a = torch.zeros(rows, 64, dtype=z.dtype, device="cuda")
+    b = torch.zeros(len(z), 64, dtype=z.dtype, device="cuda")
+    gemm.linear_bwd(one, a, b, z=zs, activation=act, dz=dz)
+    assert gemm.sync_status()[0] == G.GEMM_OK
+    return dz[rows - 1].cpu()
+
+
+@pytest.mark.parametrize("rows", ROWS)
+@pytest.mark.parametrize("act", ACTS)
+def test_nan_passes_every_activation(gemm, act, rows):
+    """A NaN comes out where it went in and nowhere else; infinities keep their limits."""
+    z = torch.linspace(-3, 3, 77)
+    z[[0, 31, 40, 76]] = float("nan")
+    z[50] = float("inf")
+    d, kept = _forward(gemm, z, act, rows)
+    assert torch.equal(torch.isnan(d), torch.isnan(z)) and torch.equal(torch.isnan(kept), torch.isnan(z))
+    assert d[50] == float("inf")
+    if act == "relu":
+        low = torch.tensor([-float("inf"), -1.0, -0.0, 0.0, 2.0])
+        assert _forward(gemm, low, act, rows)[0].tolist() == [0.0, 0.0, 0.0, 0.0, 2.0]
+
+
+@pytest.mark.parametrize("act", ACTS[1:])
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_nan_passes_every_derivative(gemm, act, dtype):
+    z = torch.linspace(-3, 3, 77).to(dtype)
+    z[[0, 31, 40, 76]] = float("nan")
+    z[50], z[51] = float("inf"), -float("inf")
+    dz = _slope(gemm, z, act)
+    assert torch.equal(torch.isnan(dz), torch.isnan(z))
+    assert dz[50] == 1 and dz[51] == 0
