@@ -68,3 +68,49 @@ def test_nan_passes_every_derivative(gemm, act, dtype):
     dz = _slope(gemm, z, act)
     assert torch.equal(torch.isnan(dz), torch.isnan(z))
     assert dz[50] == 1 and dz[51] == 0
+
+
+# The tails.  Beside the result's own rounding: the fitted distribution function's 2.2e-6, and
+# twice that for fp32's rounding of the exponent (at most 128 before 2^x, two roundings of
+# 2^-24, times log 2: 1.1e-5) and a few roundings more, together below 2^-15 of the result.
+TAIL = 2.0 ** -15
+ENDS = {"gelu": 13.0, "gelu_tanh": 10.0, "silu": 80.0}     # results stay normal fp32 numbers
+
+
+@pytest.mark.parametrize("rows", ROWS)
+@pytest.mark.parametrize("act", sorted(ENDS))
+def test_small_results_keep_their_digits(gemm, act, rows):
+    """Left of the minimum the result falls off to 1e-35: each is right to its own size."""
+    z = -torch.linspace(1.0, ENDS[act], 501)
+    d, _ = _forward(gemm, z, act, rows)
+    want = O.act(z.double(), act)
+    O.within(d, want, want.abs() * TAIL, "d")
+
+
+@pytest.mark.parametrize("rows", ROWS)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_small_16_bit_results_are_the_nearest(gemm, dtype, rows):
+    z = -torch.linspace(1.0, 13.0 if dtype == torch.bfloat16 else 5.2, 501)
+    d, _ = _forward(gemm, z, "gelu", rows, dtype)
+    want = O.act(z.double(), "gelu")
+    O.within(d, want, O.rounding(want, NAMES[dtype]) + want.abs() * TAIL, "d")
+
+
+@pytest.mark.parametrize("act", sorted(ENDS))
+def test_small_derivatives_keep_their_digits(gemm, act):
+    """act' = p + z p' with p the sigmoid or distribution function: right to the size of its
+    two terms."""
+    z = -torch.linspace(1.0, ENDS[act] - 1, 501).bfloat16()
+    dz = _slope(gemm, z, act)
+    v = z.double()
+    want = O.act_grad(v, act)
+    size = want.abs() + 2 * O.act(v, act).abs() / v.abs()
+    O.within(dz, want, O.rounding(want, "bf16") * (1 + 2 * TAIL) + size * TAIL, "dz")
+
+
+@pytest.mark.parametrize("rows", ROWS)
+def test_gelu_near_zero(gemm, rows):
+    """In the middle gelu is right to 2^-21 of z: the distribution function to 2^-22."""
+    z = torch.linspace(-4, 4, 1001)
+    d, _ = _forward(gemm, z, "gelu", rows)
+    O.within(d, O.act(z.double(), "gelu"), z.double().abs() * 2.0 ** -21 + 1e-30, "d")
