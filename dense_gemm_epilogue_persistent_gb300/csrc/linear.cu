@@ -573,20 +573,19 @@ gemm_status_t plan_linear(gemm_handle* h, const gemm_linear_t& p, LinearPlan& ou
   return GEMM_OK;
 }
 
-gemm_status_t run_linear(gemm_handle* h, const gemm_linear_t& p, struct CUstream_st* stream,
-                         Place place = kAlone) {
-  if (p.M == 0 || p.N == 0) return GEMM_OK;
+// The plan of a checked call that is not empty (h->mu held): one of the latest, or made
+// now.
+gemm_status_t find_plan(gemm_handle* h, const gemm_linear_t& p, LinearPlan& out) {
   LinearKey key;
   std::memset(&key, 0, sizeof(key));           // padding included: keys compare bytewise
   key.M = p.M; key.N = p.N; key.K = p.K;
+  key.config_gen = h->config_gen;
   key.a_type = p.a_type; key.b_type = p.b_type; key.d_type = p.d_type;
   key.r_type = p.R ? p.r_type : 0; key.z_type = p.Z ? p.z_type : 0;
   key.layoutA = p.layoutA; key.layoutB = p.layoutB;
   key.activation = p.activation;
   key.has_r = p.R != nullptr; key.has_z = p.Z != nullptr;
   key.plain = is_plain(p);
-  std::lock_guard<std::mutex> guard(h->mu);
-  key.config_gen = h->config_gen;
   LinearPlan* plan = nullptr;
   for (LinearPlan& c : h->linear_plans)
     if (c.valid && std::memcmp(&c.key, &key, sizeof(key)) == 0) { plan = &c; break; }
@@ -598,9 +597,16 @@ gemm_status_t run_linear(gemm_handle* h, const gemm_linear_t& p, struct CUstream
     plan->valid = true;
     h->linear_next = (h->linear_next + 1) % kLinearPlans;
   }
-  h->last = plan->cfg;
-  return plan->split ? run_split(h, p, *plan, place, stream)
-                     : run_persistent(h, p, *plan, place, stream);
+  out = *plan;
+  return GEMM_OK;
+}
+
+// Enqueue a call by its plan (h->mu held).
+gemm_status_t run_planned(gemm_handle* h, const gemm_linear_t& p, const LinearPlan& plan,
+                          Place place, struct CUstream_st* stream) {
+  h->last = plan.cfg;
+  return plan.split ? run_split(h, p, plan, place, stream)
+                    : run_persistent(h, p, plan, place, stream);
 }
 
 // Microseconds of one item of one of two products in one launch, beside the
@@ -772,35 +778,54 @@ gemm_status_t run_pair(gemm_handle* h, const gemm_linear_t& da, const gemm_linea
   return launch_persistent(plan.cfg, plan.kern, args, stream);
 }
 
-// Both gradients of a layer from dz, neither empty.
-gemm_status_t run_products(gemm_handle* h, const gemm_linear_bwd_t& p, const gemm_linear_t& da,
-                           const gemm_linear_t& db, struct CUstream_st* stream) {
-  PairKey key;
-  std::memset(&key, 0, sizeof(key));           // padding included: keys compare bytewise
-  key.M = p.M; key.N = p.N; key.K = p.K;
-  key.type = p.type; key.da_type = p.da_type; key.db_type = p.db_type;
-  key.accumulate = p.accumulate != 0;
-  {
-    std::lock_guard<std::mutex> guard(h->mu);
+// How a layer's gradients run: both in one launch, or each by its own plan.
+struct ProductPlans {
+  PairPlan pair;
+  LinearPlan da, db;
+};
+
+// Plan them (null: not wanted, or empty), all of it before anything is enqueued: a
+// configuration that one of them cannot take leaves every tensor as it was.
+gemm_status_t plan_products(gemm_handle* h, const gemm_linear_bwd_t& p, const gemm_linear_t* da,
+                            const gemm_linear_t* db, ProductPlans& out) {
+  std::lock_guard<std::mutex> guard(h->mu);
+  if (da && db && da->K > 0 && db->K > 0) {
+    PairKey key;
+    std::memset(&key, 0, sizeof(key));         // padding included: keys compare bytewise
+    key.M = p.M; key.N = p.N; key.K = p.K;
     key.config_gen = h->config_gen;
+    key.type = p.type; key.da_type = p.da_type; key.db_type = p.db_type;
+    key.accumulate = p.accumulate != 0;
     PairPlan* plan = nullptr;
     for (PairPlan& c : h->pair_plans)
       if (c.valid && std::memcmp(&c.key, &key, sizeof(key)) == 0) { plan = &c; break; }
     if (!plan) {
       plan = &h->pair_plans[h->pair_next];
       plan->valid = false;
-      GB300_CHECK(plan_pair(h, da, db, *plan));
+      GB300_CHECK(plan_pair(h, *da, *db, *plan));
       plan->key = key;
       plan->valid = true;
       h->pair_next = (h->pair_next + 1) % kPairPlans;
     }
-    if (plan->one) {
-      h->last = plan->cfg;
-      return run_pair(h, da, db, *plan, stream);
-    }
+    out.pair = *plan;
+    if (plan->one) return GEMM_OK;
   }
-  GB300_CHECK(run_linear(h, da, stream, kFirstOfTwo));
-  return run_linear(h, db, stream, kSecondOfTwo);
+  if (da) GB300_CHECK(find_plan(h, *da, out.da));
+  if (db) GB300_CHECK(find_plan(h, *db, out.db));
+  return GEMM_OK;
+}
+
+gemm_status_t run_products(gemm_handle* h, const gemm_linear_t* da, const gemm_linear_t* db,
+                           const ProductPlans& plans, struct CUstream_st* stream) {
+  std::lock_guard<std::mutex> guard(h->mu);
+  if (plans.pair.one) {
+    h->last = plans.pair.cfg;
+    return run_pair(h, *da, *db, plans.pair, stream);
+  }
+  const bool two = da && db;
+  if (da) GB300_CHECK(run_planned(h, *da, plans.da, two ? kFirstOfTwo : kAlone, stream));
+  if (db) GB300_CHECK(run_planned(h, *db, plans.db, two ? kSecondOfTwo : kAlone, stream));
+  return GEMM_OK;
 }
 
 // Clusters of `split` blocks of kern that the device holds at once, asked for once.
@@ -949,7 +974,11 @@ GEMM_API gemm_status_t gemm_linear(gemm_handle_t h, const gemm_linear_t* p,
   if (!h || !p) return GEMM_ERR_INVALID_ARG;
   GB300_CHECK(check_linear(*p));
   if (!on_device(h)) return GEMM_ERR_INVALID_ARG;
-  return run_linear(h, *p, stream);
+  if (p->M == 0 || p->N == 0) return GEMM_OK;
+  std::lock_guard<std::mutex> guard(h->mu);
+  LinearPlan plan;
+  GB300_CHECK(find_plan(h, *p, plan));
+  return run_planned(h, *p, plan, kAlone, stream);
 }
 
 GEMM_API gemm_status_t gemm_linear_bwd_check(const gemm_linear_bwd_t* p) {
@@ -963,6 +992,13 @@ GEMM_API gemm_status_t gemm_linear_bwd(gemm_handle_t h, const gemm_linear_bwd_t*
   const gemm_linear_bwd_t& p = *pp;
   GB300_CHECK(check_linear_bwd(p));
   if (!on_device(h)) return GEMM_ERR_INVALID_ARG;
+  int64_t lddz = 0;
+  const void* dz = dz_of(p, lddz);
+  const gemm_linear_t q_da = product_da(p, dz, lddz), q_db = product_db(p, dz, lddz);
+  const gemm_linear_t* const da = p.da && p.M > 0 && p.K > 0 ? &q_da : nullptr;
+  const gemm_linear_t* const db = p.db && p.N > 0 && p.K > 0 ? &q_db : nullptr;
+  ProductPlans plans;
+  GB300_CHECK(plan_products(h, p, da, db, plans));
   if (p.N > 0 && (p.dz || p.dbias)) {
     gb300::ActGradParams k{};
     k.dd = p.dd; k.lddd = p.lddd;
@@ -974,11 +1010,5 @@ GEMM_API gemm_status_t gemm_linear_bwd(gemm_handle_t h, const gemm_linear_bwd_t*
     GB300_CHECK(p.type == GEMM_F16 ? launch_act_grad<gb300::DT_F16>(h, k, stream)
                                    : launch_act_grad<gb300::DT_BF16>(h, k, stream));
   }
-  int64_t lddz = 0;
-  const void* dz = dz_of(p, lddz);
-  if (p.da && p.db && p.M > 0 && p.N > 0 && p.K > 0)
-    return run_products(h, p, product_da(p, dz, lddz), product_db(p, dz, lddz), stream);
-  if (p.da) GB300_CHECK(run_linear(h, product_da(p, dz, lddz), stream));
-  if (p.db) GB300_CHECK(run_linear(h, product_db(p, dz, lddz), stream));
-  return GEMM_OK;
+  return run_products(h, da, db, plans, stream);
 }

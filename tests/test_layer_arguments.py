@@ -165,3 +165,39 @@ def test_row_factors_off_their_elements_are_refused(lib, at):
         for name in names:
             assert check(make(**{**base, name: base[name] + 4})) == G.GEMM_OK
             assert check(make(**{**base, name: base[name] + at})) == G.GEMM_ERR_MISALIGNED
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("cfg,give", [
+    (cfg, give) for give in (("da", "db"), ("da",), ("db",))
+    for cfg in (dict(split_k=1, tile_n=48),      # db's MN-major tokens: whole atoms (da takes it)
+                dict(split_k=8),                 # more CTAs than k-blocks
+                dict(split_k=2, tile_m=64),      # MN-major features: 128
+                dict(cluster_m=2), dict(cta_group=1, tile_n=128, stages=12))
+    if give != ("da",) or cfg != dict(split_k=1, tile_n=48)])
+@pytest.mark.parametrize("over", [None, "dd", "z"])
+def test_a_configuration_the_products_cannot_take_changes_nothing(cfg, give, over):
+    """The gradients are planned before any of them is enqueued."""
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    g = G.Gemm(0)
+    try:
+        one = lambda *s: torch.ones(*s, dtype=torch.float16, device="cuda")
+        t = dict(dd=one(200, 128), z=one(200, 128), a=one(200, 64), b=one(128, 64))
+        out = dict(da=one(200, 64), db=one(128, 64), dz=one(200, 128),
+                   dbias=torch.ones(128, device="cuda"))
+        out["dz"] = t.get(over, out["dz"])
+        call = lambda: g.linear_bwd(**t, activation="gelu", dz=out["dz"], dbias=out["dbias"],
+                                    **{k: out[k] for k in give})
+        g.set_config(**cfg)
+        with pytest.raises(G.GemmError) as e:
+            call()
+        assert e.value.status == G.GEMM_ERR_UNSUPPORTED_CONFIG
+        torch.cuda.synchronize()
+        assert all((v == 1).all() for v in (*t.values(), *out.values()))
+        g.set_config(None)
+        call()
+        assert g.sync_status()[0] == G.GEMM_OK
+        assert all((out[k] != 1).any() for k in ("dz", *give))
+    finally:
+        g.close()
