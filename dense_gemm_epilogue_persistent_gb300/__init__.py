@@ -638,10 +638,12 @@ class Gemm:
     def linear_bwd(self, dd, a, b, z=None, activation=None, dz=None, da=None, db=None, dbias=None,
                    accumulate=False, alpha=1.0, stream=None):
         """Gradients of linear from dd, the gradient of d: dz, da, db (added to with
-        `accumulate`) and dbias, each where given; see gemm_linear_bwd in the C header."""
+        `accumulate`) and dbias, each where given; see gemm_linear_bwd in the C header.  a is
+        read for db only and b for da only: else either may be None."""
         out = _shape(dd, "dd")
         M, N = out
-        K = _shape(a, "a")[1]
+        inner = a if a is not None else b if b is not None else da if da is not None else db
+        K = 0 if inner is None else _shape(inner, "a or b")[1]
         t, dev = _code(dd, "dd"), self.device
         rows_a, rows_b = (M, K), (N, K)
         st = self._lib.gemm_linear_bwd(self.handle, _LINEAR_BWD.pack(

@@ -1,6 +1,7 @@
 """Arguments of the layer operators that no kernel may be given: each is refused on the host
 before anything is enqueued.  Those that are somewhere else are tested with a library that
 counts its calls."""
+import ctypes
 import inspect
 
 import pytest
@@ -165,6 +166,60 @@ def test_row_factors_off_their_elements_are_refused(lib, at):
         for name in names:
             assert check(make(**{**base, name: base[name] + 4})) == G.GEMM_OK
             assert check(make(**{**base, name: base[name] + at})) == G.GEMM_ERR_MISALIGNED
+
+
+class Checked:
+    """The library's host-only check in place of its call."""
+
+    def __init__(self, lib):
+        self.lib = lib
+
+    def gemm_linear_bwd(self, handle, packed, stream):
+        p = G.gemm_linear_bwd_t.from_buffer_copy(packed)
+        return self.lib.gemm_linear_bwd_check(ctypes.byref(p))
+
+
+@pytest.mark.parametrize("without,give,ok", [
+    ("a", ("da",), True), ("b", ("db",), True), ("ab", (), True), ("a", (), True), ("b", (), True),
+    ("a", ("db",), False), ("b", ("da",), False), ("a", ("da", "db"), False), ("ab", ("da",), False),
+    ("ab", ("db",), False)])
+def test_an_operand_no_gradient_reads_may_be_left_out(lib, without, give, ok):
+    """a is read for db and b for da."""
+    kw = {k: Placed(t, 0) for k, t in dict(_calls())["linear_bwd"].items()
+          if k not in ("da", "db") or k in give}
+    for k in without:
+        kw[k] = None
+    g = _handle(Checked(lib))
+    if ok:
+        g.linear_bwd(**kw, activation="gelu")
+    else:
+        with pytest.raises(G.GemmError) as e:
+            g.linear_bwd(**kw, activation="gelu")
+        assert e.value.status == G.GEMM_ERR_INVALID_ARG
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M,N,K", [(3, 40, 72), (300, 264, 136)])
+def test_gradients_without_the_operand_they_do_not_read(M, N, K):
+    """The same bits with it and without."""
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    g = G.Gemm(0)
+    try:
+        gen = torch.Generator().manual_seed(M)
+        dd, z, a, b = (torch.randn(*s, generator=gen).to("cuda", torch.bfloat16)
+                       for s in ((M, N), (M, N), (M, K), (N, K)))
+        new = lambda *s: torch.zeros(*s, dtype=torch.bfloat16, device="cuda")
+        want, got = ({k: new(*s) for k, s in (("dz", (M, N)), ("da", (M, K)), ("db", (N, K)))}
+                     for _ in range(2))
+        for k, without in (("da", "a"), ("db", "b")):
+            for outs, ab in ((want, dict(a=a, b=b)), (got, {**dict(a=a, b=b), without: None})):
+                g.linear_bwd(dd, **ab, z=z, activation="silu", dz=outs["dz"], **{k: outs[k]})
+        assert g.sync_status()[0] == G.GEMM_OK
+        for k in want:
+            assert torch.equal(want[k], got[k]) and (got[k] != 0).any(), k
+    finally:
+        g.close()
 
 
 @pytest.mark.gpu
