@@ -254,7 +254,8 @@ struct Watch {
 // Debug build (GB300_DEBUG=1, a separate library): before use, every TMA
 // copy's shared-memory range and inner coordinate (16-byte aligned, stores not
 // below zero), every tensor-memory column range the MMA writes or the
-// epilogue reads, and every MMA operand address are checked.  A failed check
+// epilogue reads, every MMA operand address, and what epilogues store from
+// registers and exchange between CTAs are checked.  A failed check
 // records 0xD0CCBBBB (CC the check, BBBB the low 16 bits of the block) in the
 // status word, raises the abort flag and skips the access, so the launch ends
 // through the watchdog's drain path; nothing traps.  The product build
@@ -284,6 +285,13 @@ __device__ __forceinline__ bool dbg_check(bool cond, uint32_t check, const Watch
 __device__ __forceinline__ bool in_range(uint32_t lo, uint32_t bytes, uint32_t begin,
                                          uint32_t end) {
   return lo >= begin && lo + bytes <= end;
+}
+
+// 32 bytes from where an operand descriptor starts lie inside [begin, begin + bytes).  (A
+// descriptor holds an address's lowest 18 bits; above them a cluster's CTAs count.)
+__device__ __forceinline__ bool desc_in_range(uint64_t desc, uint32_t begin, uint32_t bytes) {
+  return in_range((uint32_t)(desc & 0x3FFFu) << 4, 32, begin & 0x3FFFFu,
+                  (begin & 0x3FFFFu) + bytes);
 }
 
 // Bounded wait for the phase with parity `parity`.  A non-zero `hint_ns` lets
@@ -916,12 +924,28 @@ persistent_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
           tc_fence_after_sync();
           const uint32_t d_tmem = tmem_base + (uint32_t)acc * kAccStride;
           const uint32_t idesc = wk.half < 0 ? P.idesc : P.idesc_half;
+          // (debug build: as below, by every lane alike)
+          if (!dbg_check((uint32_t)(wk.half < 0 ? BN : BN / 2) <= kAccStride &&
+                             (uint32_t)acc * kAccStride + kAccStride <= kTmemCols,
+                         kChkMmaTmem, w))
+            break;
           for (int kb = wk.kb0; kb < wk.kb1; ++kb) {
             ok = __all_sync(0xFFFFFFFFu, wait_phase(full0 + 8u * s, ph, w, kWaitMmaFull));
             if (!ok) break;
             tc_fence_after_sync();
             const uint64_t ad = a0 + (uint32_t)(s * G::A_STAGE) / 16;
             const uint64_t bd = b0 + (uint32_t)(s * T.b_stage) / 16;
+            if constexpr (kDebug) {
+              const uint32_t sa = a_ring + s * G::A_STAGE, sb = b_ring + s * T.b_stage;
+              for (int k = 0; k < G::K_STEPS; ++k) {
+                const int at = k / G::STEPS_PER_ATOM, in = k % G::STEPS_PER_ATOM;
+                ok = ok && dbg_check(desc_in_range(ad + (at * a_atom + in * a_step), sa, G::A_STAGE) &&
+                                         desc_in_range(bd + (at * b_atom + in * b_step), sb,
+                                                       (uint32_t)T.b_stage),
+                                     kChkMmaSmem, w);
+              }
+              if (!ok) break;
+            }
             if (elect_one()) {
 #pragma unroll
               for (int k = 0; k < G::K_STEPS; ++k) {
@@ -1159,7 +1183,7 @@ persistent_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
       float row_factor = 1.f, col_s = 1.f, col_b = 0.f;
       auto fetch_column = [&](int j) {
         const int col = ncol0 + j * kEpiChunk + lane;
-        if (col < P.N) {
+        if (col < P.N && dbg_check(col >= 0, kChkEpiLoad, w)) {
           if (e.col_scale) col_s = __ldg(e.col_scale + col);
           if (e.bias) col_b = vector_elem(e.bias, col, e.bias_dt);
         }
@@ -1393,7 +1417,9 @@ persistent_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
             const int piece = dt == DT_F32 ? 4 : 8;
             const int left = P.N - col0, lo = left & ~(piece - 1);
             const long long row = row0 + lane;
-            if (row < P.M)
+            // (debug build: the piece is the row's last, inside the row)
+            if (row < P.M && dbg_check(row0 >= 0 && col0 >= 0 && left <= kEpiChunk && P.N <= ld,
+                                       kChkEpiStore, w))
               store_row_end(static_cast<uint8_t*>(t) + (row * ld + col0) * (dt == DT_F32 ? 4 : 2),
                             dt, lo, left - lo, dv);
             return lo == 0;

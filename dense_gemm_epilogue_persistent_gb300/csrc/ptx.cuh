@@ -35,6 +35,13 @@ __device__ __forceinline__ uint32_t map_to_rank(uint32_t addr, uint32_t rank) {
   return out;
 }
 
+// Bytes of dynamic shared memory the block was launched with.
+__device__ __forceinline__ uint32_t dynamic_smem_bytes() {
+  uint32_t n;
+  asm("mov.u32 %0, %%dynamic_smem_size;" : "=r"(n));
+  return n;
+}
+
 // A float in the shared memory of another CTA of the cluster.
 __device__ __forceinline__ float load_cluster_f32(uint32_t cluster_addr) {
   float v;

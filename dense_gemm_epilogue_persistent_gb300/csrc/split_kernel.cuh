@@ -227,6 +227,14 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tmF, const __grid_consta
         break;
       const uint32_t fb = full0 + 8u * s;
       const int n_atoms = min(ka, kb1 - kb);
+      // (debug build, by every lane alike: the boxes inside this stage, their inner
+      // coordinates whole 16 bytes, all from 0 on)
+      if (!dbg_check(in_range(f_ring + s * f_stage, n_atoms * f_atom, f_ring, t_ring) &&
+                         in_range(t_ring + s * t_stage, n_atoms * t_atom, t_ring, bars) &&
+                         n0 >= 0 && m0 >= 0 && (!feat_mn || n0 * AB_BYTES % 16 == 0) &&
+                         (!tok_mn || m0 * AB_BYTES % 16 == 0),
+                     kChkLoadA, w))
+        break;
       if (elect_one()) {
         mbar_arrive_expect_tx(fb, n_atoms * (f_atom + t_atom));
         for (int a = 0; a < n_atoms; ++a) {
@@ -269,6 +277,21 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tmF, const __grid_consta
       if (!ok) break;
       tc_fence_after_sync();
       const int n_atoms = min(ka, kb1 - kb);
+      // (debug build: the accumulator's columns allocated, the operands' start addresses
+      // inside the stage, and 128 rows of features inside the block's memory)
+      if constexpr (kDebug) {
+        ok = dbg_check((uint32_t)bn <= p.tmem_cols && p.tmem_cols <= kTmemCols, kChkMmaTmem, w);
+        for (int a = 0; a < n_atoms; ++a) {
+          const uint32_t fa = f_ring + s * f_stage + a * f_atom, ta = t_ring + s * t_stage + a * t_atom;
+          for (int k = 0; k < BK / UMMA_K; ++k)
+            ok = ok && dbg_check(desc_in_range(f_desc + a * (f_atom / 16) + k * f_step, fa, f_atom) &&
+                                     desc_in_range(t_desc + a * (t_atom / 16) + k * t_step, ta,
+                                                   t_atom) &&
+                                     fa + 128u * 128u <= raw + dynamic_smem_bytes(),
+                                 kChkMmaSmem, w);
+        }
+        if (!ok) break;
+      }
       if (elect_one()) {
         uint64_t fd = f_desc, td = t_desc;
         for (int a = 0; a < n_atoms; ++a) {
@@ -316,12 +339,17 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tmF, const __grid_consta
       advance(4 * turn);
       for (int c = 16 * turn; c < with_tokens; c += 16 * turns) {
         uint32_t acc[16];
+        // (debug build: the columns allocated, each piece inside its owner's ring)
+        if (!dbg_check((uint32_t)c + 16u <= p.tmem_cols, kChkEpiTmem, w)) break;
         __syncwarp();
         tmem_load_16cols(tbase + c, acc);
         tmem_wait_ld16(acc);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          if (c + 4 * i < with_tokens)
+          if (c + 4 * i < with_tokens &&
+              dbg_check(owner < S && in_range(base + (rank * pieces + piece) * 2048u + my_piece, 16,
+                                              base, bars),
+                        kChkEpiSmem, w))
             store_cluster_v4(map_to_rank(base + (rank * pieces + piece) * 2048u + my_piece,
                                          (uint32_t)owner),
                              acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
@@ -344,6 +372,14 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tmF, const __grid_consta
         next_factor = row_factor((c & ~31) + 32);
       }
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      // (debug build: accumulator columns allocated or pieces inside the ring; the stores
+      // below inside D)
+      if (!dbg_check(S == 1 ? (uint32_t)c + 4u <= p.tmem_cols
+                            : in_range(base + c * 512 + ((S - 1) * pieces) * 2048u + q * 512u, 512u,
+                                       base, bars),
+                     kChkEpiSmem, w) ||
+          !dbg_check(n0 >= 0 && m_lo >= 0 && m_lo + n_cols <= p.M, kChkEpiStore, w))
+        break;
       if (S == 1) {
         uint32_t acc[4];
         __syncwarp();                            // (.aligned, after per-lane work)

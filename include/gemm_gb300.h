@@ -305,7 +305,8 @@ gemm_status_t gemm_ring_stats(gemm_handle_t h, struct CUstream_st* stream, uint6
  * built with GB300_DEBUG=1) a device-side bounds check failed -- a TMA box
  * outside its shared-memory slot, a TMA coordinate that is not 16-byte
  * aligned or a store starting below zero, a tensor-memory column range past
- * its accumulator stage; the access was skipped and the status word holds
+ * its accumulator stage, an MMA operand, exchanged piece or register store out
+ * of its range; the access was skipped and the status word holds
  * 0xD0CCBBBB, CC the check -- GEMM_ERR_CUDA if the stream reported an error,
  * else GEMM_OK.
  * *detail (optional; may be NULL) receives the raw status word (0 when
