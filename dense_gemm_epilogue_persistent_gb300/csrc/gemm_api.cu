@@ -1095,7 +1095,9 @@ GEMM_API gemm_status_t gemm_ring_stats(gemm_handle_t h, struct CUstream_st* stre
   *n_ctas = 0;
   if (!gb300::kRingStats || !h->d_stats) return GEMM_ERR_UNSUPPORTED_CONFIG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const int n = std::min(h->last.grid_ctas, std::min(max_ctas, h->sm_count));
+  // (the split-K kernel keeps no counters: what is there is an earlier launch's)
+  const int n =
+      h->last.split_k > 0 ? 0 : std::min(h->last.grid_ctas, std::min(max_ctas, h->sm_count));
   if (cudaStreamSynchronize(s) != cudaSuccess ||
       (n > 0 && cudaMemcpy(out, h->d_stats, (size_t)n * gb300::kStatWords * sizeof(uint64_t),
                            cudaMemcpyDeviceToHost) != cudaSuccess)) {

@@ -903,6 +903,8 @@ persistent_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
       if (rank == 0) {
         int s = 0, acc = 0;
         uint32_t ph = 0, aph = 0;
+        long long st_full = 0, st_acc = 0, st_stages = 0;
+        const long long st_t0 = stat_clock();
         bool ok = !p.inject_stall ||
                   __all_sync(0xFFFFFFFFu, wait_phase(never_bar, 0u, w, kWaitInjected));
         for (int it = first_item; ok && it < p.num_items; it = next_item(it)) {
@@ -919,8 +921,10 @@ persistent_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
           const uint32_t a_atom =
               P.a_mn_major ? G::STEPS_PER_ATOM * a_step : (uint32_t)G::A_ATOM / 16;
           const uint32_t b_atom = P.b_mn_major ? G::STEPS_PER_ATOM * b_step : (uint32_t)T.b_atom / 16;
+          const long long t_a = stat_clock();
           if (!__all_sync(0xFFFFFFFFu, wait_phase(tempty0 + 8u * acc, aph ^ 1u, w, kWaitMmaAcc)))
             break;
+          if constexpr (kRingStats) st_acc += clock64() - t_a;
           tc_fence_after_sync();
           const uint32_t d_tmem = tmem_base + (uint32_t)acc * kAccStride;
           const uint32_t idesc = wk.half < 0 ? P.idesc : P.idesc_half;
@@ -930,8 +934,10 @@ persistent_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
                          kChkMmaTmem, w))
             break;
           for (int kb = wk.kb0; kb < wk.kb1; ++kb) {
+            const long long t_f = stat_clock();
             ok = __all_sync(0xFFFFFFFFu, wait_phase(full0 + 8u * s, ph, w, kWaitMmaFull));
             if (!ok) break;
+            if constexpr (kRingStats) { st_full += clock64() - t_f; ++st_stages; }
             tc_fence_after_sync();
             const uint64_t ad = a0 + (uint32_t)(s * G::A_STAGE) / 16;
             const uint64_t bd = b0 + (uint32_t)(s * T.b_stage) / 16;
@@ -963,6 +969,13 @@ persistent_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
           if (elect_one()) umma_commit<CG, (CG == 2)>(tfull0 + 8u * acc, pair_mask);
           __syncwarp();
           if (++acc == kAccStages) { acc = 0; aph ^= 1u; }
+        }
+        if constexpr (kRingStats) if (p.stats && lane == 0) {
+          unsigned long long* const o = p.stats + (size_t)blockIdx.x * kStatWords;
+          o[kStatMmaFull] = st_full;
+          o[kStatMmaAcc] = st_acc;
+          o[kStatMmaLoop] = clock64() - st_t0;
+          o[kStatMmaStages] = st_stages;
         }
       }
     } else if (rank == 0 && lane == 0) {

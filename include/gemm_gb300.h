@@ -294,7 +294,7 @@ gemm_status_t gemm_run_host(gemm_handle_t h, int64_t M, int64_t N, int64_t K, in
  * into shared memory, issuing the stores and next loads (with their wait);
  * the chunks the store thread's warp processed (the CTA's chunks with one
  * epilogue warp per lane quarter, about half of them with two); two spare
- * words. */
+ * words.  After a split-K launch *n_ctas is 0: that kernel keeps no counters. */
 #define GEMM_RING_STAT_WORDS 16
 gemm_status_t gemm_ring_stats(gemm_handle_t h, struct CUstream_st* stream, uint64_t* out,
                               int max_ctas, int* n_ctas);

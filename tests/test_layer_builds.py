@@ -1,7 +1,8 @@
 """The layer operators in the library's other builds, each in a subprocess so that the test
 process keeps the product library: against 64 bits, as in test_linear and test_norm, in
 the debug build (whose checks of shared-memory ranges, tensor-memory columns, coordinates,
-exchanged pieces and register stores all hold) and in the one without multicast."""
+exchanged pieces and register stores all hold) and in the one without multicast; and the ring
+statistics of the layer's launches."""
 import os
 import subprocess
 import sys
@@ -71,3 +72,56 @@ def test_layer_operators_in_another_build(kind):
     r = subprocess.run([sys.executable, "-c", CHILD, kind], cwd=ROOT, capture_output=True,
                        text=True, timeout=1200)
     assert r.returncode == 0 and "BUILD_OK" in r.stdout, r.stdout[-3000:] + r.stderr[-3000:]
+
+
+STATS = r'''
+import sys
+sys.path.insert(0, "tests")
+import torch
+import dense_gemm_epilogue_persistent_gb300 as G
+from dense_gemm_epilogue_persistent_gb300 import build as B
+G.select_library(B.build(kind="stats"))
+g = G.Gemm(0)
+one = lambda *s: torch.ones(*s, dtype=torch.float16, device="cuda")
+cdiv = lambda a, b: -(-a // b)
+
+def stages():
+    """Ring stages the last launch issued, and every wait within its loop."""
+    rows = g.ring_stats()
+    for r in rows:
+        assert r[0] + r[1] <= r[2], r
+    return sum(r[3] for r in rows), len(rows)
+
+for M, N, K, cfg in ((700, 1000, 300, None), (300, 520, 1000, dict(cta_group=1, tile_n=128, tail_split=1)),
+                     (1000, 1500, 136, dict(cta_group=2, tile_n=256, tail_split=1)), (300, 520, 0, None)):
+    for act in (None, "gelu"):                 # (no bias, no activation: the kernel of two products)
+        g.set_config(**cfg) if cfg else g.set_config(None)
+        pad = max(8, cdiv(K, 8) * 8)
+        g.linear(one(M, pad)[:, :K], one(N, pad)[:, :K], one(M, cdiv(N, 8) * 8)[:, :N], activation=act)
+        c = g.last_config()
+        items = c.tiles + c.tail_split
+        got, n = stages()
+        assert n == c.grid_ctas and got == items * cdiv(K, c.tile_k), (got, items, c.as_dict())
+g.set_config(cta_group=2, tile_n=256, tail_split=1)
+M, N, K = 1000, 1500, 136
+g.linear_bwd(one(M, N + 4)[:, :N], one(M, K), one(N, K), da=one(M, K), db=one(N, K))
+c = g.last_config()
+want = cdiv(M, 256) * cdiv(K, 256) * cdiv(N, c.tile_k) + cdiv(N, 256) * cdiv(K, 256) * cdiv(M, c.tile_k)
+assert stages() == (want, c.grid_ctas), (stages(), want)
+g.set_config(split_k=2)
+g.linear(one(4, 512), one(256, 512), one(4, 256))
+assert g.ring_stats() == [] and g.sync_status()[0] == G.GEMM_OK
+g.set_config(None)
+g.close()
+print("STATS_OK")
+'''
+
+
+def test_ring_statistics_count_the_layer_s_stages():
+    """Each launch's own counters: as many stages as its items have k-blocks; none of a split-K
+    launch."""
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    r = subprocess.run([sys.executable, "-c", STATS], cwd=ROOT, capture_output=True, text=True,
+                       timeout=1200)
+    assert r.returncode == 0 and "STATS_OK" in r.stdout, r.stdout[-3000:] + r.stderr[-3000:]
