@@ -595,6 +595,8 @@ class Gemm:
             try:
                 if workspace.get_device() != dev:
                     raise _elsewhere(workspace, "workspace", dev)
+                if not workspace.is_contiguous():    # (its bytes are not where they are counted)
+                    raise GemmError(GEMM_ERR_INVALID_ARG, "workspace: not contiguous")
             except AttributeError:
                 pass
             ws, nbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()

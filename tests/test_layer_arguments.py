@@ -88,6 +88,18 @@ def test_tensors_on_the_handle_s_gpu_are_taken(name, device):
     assert lib.calls == 2
 
 
+@pytest.mark.parametrize("workspace", [torch.zeros(1).expand(4096), torch.zeros(8192)[::2],
+                                       torch.zeros(64, 64).t()])
+def test_a_workspace_whose_bytes_lie_elsewhere_is_refused(workspace):
+    """Its size is counted from its elements, which a stride can place on one another or among
+    others'."""
+    lib = Library()
+    kw = {k: Placed(t, 0) for k, t in dict(_calls())["rmsnorm_bwd"].items()}
+    with pytest.raises(G.GemmError) as e:
+        _handle(lib).rmsnorm_bwd(**{**kw, "workspace": Placed(workspace, 0)})
+    assert e.value.status == G.GEMM_ERR_INVALID_ARG and lib.calls == 0
+
+
 def test_every_tensor_argument_is_covered():
     for name, kw in _calls():
         other = {"self", "eps", "stream", "activation", "alpha", "accumulate"}
