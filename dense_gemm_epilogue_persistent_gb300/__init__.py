@@ -613,9 +613,11 @@ class Gemm:
     def linear(self, a, b, d, bias=None, activation=None, residual=None, z=None, row_scale=None,
                col_scale=None, alpha=1.0, stream=None):
         """d = act(alpha * (a b^T) * row_scale * col_scale + bias) + residual; see gemm_linear
-        in the C header.  a [M, K] and b [N, K], either dimension contiguous (fp32 ones
-        are read at tf32 precision); activation: None, "relu", "gelu", "gelu_tanh" or "silu";
-        z receives what the activation is applied to."""
+        in the C header.  a [M, K] and b [N, K], either dimension contiguous; activation:
+        None, "relu", "gelu", "gelu_tanh" or "silu"; z receives what the activation is applied
+        to.  There is no product of full fp32 precision: fp32 a and b are GEMM_TF32's, of whose
+        fractions the matrix units read ten bits and drop the rest, up to 2^-10 of each operand
+        and always towards zero."""
         M, K = _shape(a, "a")
         N, inner = _shape(b, "b")
         if inner != K:

@@ -489,7 +489,9 @@ typedef enum {
  * unrounded z.
  *   A, B: layouts, leading dimensions and types as for gemm_run with L = 1
  *   (F16, BF16, E4M3, E5M2 or TF32; the types equal, or any pair of 8-bit ones;
- *   TF32 K-major only); required when K > 0.  K = 0: the sum is 0.
+ *   TF32 K-major only); required when K > 0.  K = 0: the sum is 0.  fp32
+ *   operands are TF32's: of fractions longer than ten bits the rest is dropped,
+ *   up to 2^-10 of each operand, towards zero.
  *   row_scale [M], col_scale [N]: fp32, optional (NULL: 1).  bias [N]: F32, F16
  *   or BF16, optional.  R (residual) and Z (the pre-activation the backward
  *   pass needs): optional.  R, Z and D: F32, F16 or BF16 each.

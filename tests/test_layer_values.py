@@ -114,3 +114,19 @@ def test_gelu_near_zero(gemm, rows):
     z = torch.linspace(-4, 4, 1001)
     d, _ = _forward(gemm, z, "gelu", rows)
     O.within(d, O.act(z.double(), "gelu"), z.double().abs() * 2.0 ** -21 + 1e-30, "d")
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 136, 260), (40, 200, 1031), (300, 520, 264)])
+def test_ordinary_fp32_operands(gemm, M, N, K):
+    """fp32 operands that are no tf32 values lose less than 2^-10 each to the dropped bits: 2^-9 +
+    2^-20 of the terms' magnitudes in the product, beside its accumulation's 2^-10.  Their dropping
+    alone, in 64 bits, is what the kernels do: then only the accumulation's error is left."""
+    gen = torch.Generator().manual_seed(K)
+    a, b = torch.randn(M, K, generator=gen), torch.randn(N, K, generator=gen)
+    d = O.strided(torch.zeros(M, N), "f32")[0]
+    gemm.linear(O.strided(a, "f32")[0], O.strided(b, "f32")[0], d)
+    assert gemm.sync_status()[0] == G.GEMM_OK
+    S = a.double().abs() @ b.double().abs().T
+    O.within(d, a.double() @ b.double().T, S * (2.0 ** -9 + 2.0 ** -20 + 2.0 ** -10), "d")
+    ten = lambda t: (t.view(torch.int32) & ~0x1FFF).view(torch.float32).double()
+    O.within(d, ten(a) @ ten(b).T, S * 2.0 ** -10, "d of ten fraction bits")
