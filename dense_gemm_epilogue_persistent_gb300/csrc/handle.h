@@ -144,7 +144,7 @@ struct gemm_handle {
   gb300host::PairPlan pair_plans[gb300host::kPairPlans];
   int pair_next = 0;
   int split_clusters[9] = {0, 0, 0, 0, 0, 0, 0, 0, 0};   // resident, by cluster size (0: not asked)
-  int act_clusters[3][9] = {};                 // activation gradient's, by block size and cluster
+  int act_clusters[2][3][9] = {};   // activation gradient's, by type, block size and cluster
   std::mutex mu;
   void* ws = nullptr;          // gemm_run_host's device copies of its host buffers
   size_t ws_bytes = 0;

@@ -828,10 +828,9 @@ gemm_status_t run_products(gemm_handle* h, const gemm_linear_t* da, const gemm_l
   return GEMM_OK;
 }
 
-// Clusters of `split` blocks of kern that the device holds at once, asked for once.
+// Clusters of `split` blocks of kern that the device holds at once, asked for once and kept in n.
 template <class Kern>
-int act_clusters(gemm_handle* h, Kern kern, int size, int threads, size_t smem, int split) {
-  int& n = h->act_clusters[size][split];
+int act_clusters(int& n, const gemm_handle* h, Kern kern, int threads, size_t smem, int split) {
   if (n > 0) return n;
   cudaLaunchConfig_t lc{};
   cudaLaunchAttribute attr[1];
@@ -875,7 +874,8 @@ gemm_status_t launch_act_grad(gemm_handle* h, gb300::ActGradParams& k, struct CU
       const int t = 1024 >> size;
       GB300_CHECK(raise_smem(h, reinterpret_cast<const void*>(kerns[size])));
       for (int split = 1; split <= 8; ++split) {
-        const int held = act_clusters(h, kerns[size], size, t, smem(t), split);
+        const int held = act_clusters(h->act_clusters[DT == gb300::DT_F16][size][split], h, kerns[size],
+                                      t, smem(t), split);
         const double full = (double)strips / held;
         const double waves = full <= 1.0 ? 1.0 : full + 0.156 * (std::ceil(full) - full);
         const double rows = (double)cdiv(k.M, (int64_t)split * (t / 8));
