@@ -109,7 +109,8 @@ rmsnorm_any_kernel(const __grid_constant__ NormParams p) {
 // warp where WARP: then a block holds 4 rows) keep VPT vectors of the row each,
 // vector i of thread t being elements 8 (i T + t).  The outputs follow two
 // reductions over the row (sum of squares; largest output magnitude where the
-// output is 8-bit).  DRAM-bound: 4 es + eo bytes an element with a residual.
+// output is 8-bit).  DRAM-bound: 3 es + eo bytes an element with a residual and h (es, eo the
+// types' sizes), es + eo without.
 template <int DT, int VPT, bool WARP>
 __global__ void __launch_bounds__(WARP ? 128 : 1024)
 rmsnorm_row_kernel(const __grid_constant__ NormParams p) {
@@ -226,7 +227,6 @@ struct SumParams {
 // Floats from one row of partial sums to the next: whole 16-byte pieces.
 __host__ __device__ constexpr int partial_ld(int H) { return (H + 3) & ~3; }
 
-
 // The backward kernel's blocks stay and walk rows first, first + walkers, ...;
 // every thread copies its own vectors of the next rows into its own slots of
 // shared memory with cp.async, `depth` rows ahead, so no thread waits on
@@ -311,12 +311,12 @@ rmsnorm_bwd_any_kernel(const __grid_constant__ NormBwdParams p) {
   }
 }
 
-// Both gradients in one reading of dy, h and dh, pipelined like the many-row
-// forward kernel.  Each thread keeps the same VPT vectors of columns throughout
-// (a block's threads span a row; with WARP a warp does and the block's 8 warps
-// take different rows), so the weight gradient of the rows it has seen stays in
-// its registers.  At the end every block writes its H sums to the workspace;
-// sum_partials_kernel adds them in block order.
+// Both gradients in one reading of dy, h and dh, requested ahead through RowPipe.
+// Each thread keeps the same VPT vectors of columns throughout (a block's threads
+// span a row; with WARP a warp does and the block's 8 warps take different rows), so
+// the weight gradient of the rows it has seen stays in its registers.  At the end
+// every block writes its H sums to the workspace; sum_partials_kernel adds them in a
+// fixed order.
 template <int DT, int VPT, bool WARP>
 __global__ void __launch_bounds__(WARP ? 256 : 512)
 rmsnorm_bwd_rows_kernel(const __grid_constant__ NormBwdParams p) {

@@ -23,12 +23,6 @@ __host__ __device__ constexpr int elem_bytes(int dt) {
   return dt == DT_F32 ? 4 : (dt == DT_F16 || dt == DT_BF16) ? 2 : 1;
 }
 
-__device__ __forceinline__ float load_elem(const void* p, long long i, int dt) {
-  if (dt == DT_F32) return static_cast<const float*>(p)[i];
-  const uint16_t b = static_cast<const uint16_t*>(p)[i];
-  return dt == DT_F16 ? __half2float(__ushort_as_half(b)) : __uint_as_float((uint32_t)b << 16);
-}
-
 __device__ __forceinline__ void store_elem(void* p, long long i, int dt, float v) {
   if (dt == DT_F32) static_cast<float*>(p)[i] = v;
   else if (dt == DT_F16) static_cast<uint16_t*>(p)[i] = __half_as_ushort(__float2half_rn(v));
