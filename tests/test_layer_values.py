@@ -130,3 +130,46 @@ def test_ordinary_fp32_operands(gemm, M, N, K):
     O.within(d, a.double() @ b.double().T, S * (2.0 ** -9 + 2.0 ** -20 + 2.0 ** -10), "d")
     ten = lambda t: (t.view(torch.int32) & ~0x1FFF).view(torch.float32).double()
     O.within(d, ten(a) @ ten(b).T, S * 2.0 ** -10, "d of ten fraction bits")
+
+
+def test_two_handles_at_once():
+    """Two handles on two streams, their calls interleaved without ordering between them: each
+    result as from one handle alone."""
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    handles, streams = [G.Gemm(0) for _ in range(2)], [torch.cuda.Stream() for _ in range(2)]
+    try:
+        gen = torch.Generator().manual_seed(2)
+        rnd = lambda *s: torch.randn(*s, generator=gen).to("cuda", torch.bfloat16)
+        sets = [(rnd(m, 1024), rnd(776, 1024), rnd(m, 776)) for m in (1, 24, 90, 300)]
+        w = rnd(1024)
+
+        def outputs():
+            e = lambda *s: torch.zeros(*s, dtype=torch.bfloat16, device="cuda")
+            return [dict(n=e(*a.shape), d=e(*dd.shape), z=e(*dd.shape), dz=e(*dd.shape),
+                         da=e(*a.shape), db=e(*b.shape)) for a, b, dd in sets]
+
+        def layer(g, i, o, stream):
+            a, b, dd = sets[i]
+            g.rmsnorm(a, w, o["n"], stream=stream)
+            g.linear(o["n"], b, o["d"], activation="gelu", z=o["z"], stream=stream)
+            g.linear_bwd(dd, o["n"], b, z=o["z"], activation="gelu", dz=o["dz"], da=o["da"],
+                         db=o["db"], stream=stream)
+
+        want, got = outputs(), [outputs() for _ in handles]
+        for i in range(len(sets)):
+            layer(handles[0], i, want[i], None)
+        torch.cuda.synchronize()
+        for _ in range(20):
+            for i in range(len(sets)):
+                for g, stream, outs in zip(handles, streams, got):
+                    layer(g, i, outs[i], stream)
+        torch.cuda.synchronize()
+        for g, outs in zip(handles, got):
+            assert g.sync_status()[0] == G.GEMM_OK
+            for o, ref in zip(outs, want):
+                for k in ref:
+                    assert torch.equal(o[k], ref[k]), k
+    finally:
+        for g in handles:
+            g.close()
