@@ -511,7 +511,8 @@ struct RowShape {
 // a last wave counts (1000 x 5003: 11.2 us at 2, 13.0 at 4; 600 x 2048: 3.4 at 1, 4.7 at
 // 4), up to 768 of them, where their joining costs more again (1 x 8192: 3.09 us at 2,
 // 3.33 at 1, 3.73 at 4).  Over 178 sizes (1 to 7000 rows of 1536 to 12000) the choice is
-// 1.1 % over the fastest on average, 12 % at worst.
+// 1.1 % over the fastest on average, 12 % at worst.  (Fitted on 16-bit rows; 32-bit ones
+// take the same rates, and their four-vector block kernel spills 104 bytes a thread.)
 RowShape forward_shape(int64_t M, int64_t H, int64_t row_bytes, int sm_count) {
   const int vecs = (int)cdiv(H, gb300::kVec);
   RowShape s{};
@@ -547,7 +548,7 @@ RowShape forward_shape(int64_t M, int64_t H, int64_t row_bytes, int sm_count) {
 // at 2 vectors x 512 threads x 2 rows against 105 with 4 x 256 x 1 and 122 with
 // 1 block of each; 32768 x 2048: 84.8 us with 4 blocks of 128 threads, 89.7 with
 // 8, 100.8 with 1 vector.  Longer rows (over 8192) take 4 vectors, one row ahead
-// (4096 x 16384: 112 us, 121 with two).
+// (4096 x 16384: 112 us, 121 with two), and spill 68 bytes a thread, 104 in 32 bits.
 struct BwdShape {
   int vpt, threads, blocks_per_sm, depth;
   bool warp;
@@ -596,9 +597,10 @@ NormKern forward_kernel(const RowShape& s) {
 typedef void (*NormBwdKern)(gb300::NormBwdParams);
 template <int DT, bool WARP>
 NormBwdKern backward_kernel(int vpt) {
-  return vpt == 1   ? gb300::rmsnorm_bwd_rows_kernel<DT, 1, WARP>
-         : vpt == 2 ? gb300::rmsnorm_bwd_rows_kernel<DT, 2, WARP>
-                    : gb300::rmsnorm_bwd_rows_kernel<DT, 4, WARP>;
+  if constexpr (WARP)                            // (a block's threads take two or four)
+    if (vpt == 1) return gb300::rmsnorm_bwd_rows_kernel<DT, 1, WARP>;
+  return vpt == 2 ? gb300::rmsnorm_bwd_rows_kernel<DT, 2, WARP>
+                  : gb300::rmsnorm_bwd_rows_kernel<DT, 4, WARP>;
 }
 template <int DT>
 NormBwdKern backward_kernel(const BwdShape& s) {
