@@ -33,13 +33,13 @@ struct ActGradParams {
 // columns (8 lanes of one vector each) and 1/R of the rows, R the cluster size:
 // thread group g of G = THREADS / 8 walks rows first + g, + G, ..., each thread
 // copying its own pieces of the next kActDepth rows into its own slots of shared
-// memory (16 bytes and the row's end as they lie in memory; loads into registers, two
-// rows at a time, took 43.6 us for 4096 x 8192 gelu, 39.0 so, and 20.3, 13.1 for 8192 x
-// 700, whose rows end inside a piece).  A column's sum is added in a fixed order: a
-// thread's rows, the groups through shared memory, the cluster's blocks by its
-// first one.
-// (4096 x 8192 gelu: 39.0 us with three rows, 40.5 with two, 38.9 with four; 16384 x
-// 4096: 70.1, 69.9, 73.7)
+// memory (16 bytes and the row's end as they lie in memory; before the launch shapes
+// were chosen as below, 4096 x 8192 gelu took 39.0 us so and 43.6 with loads into
+// registers, two rows at a time, 8192 x 700, whose rows end inside a piece, 13.1 and
+// 20.3).  A column's sum is added in a fixed order: a thread's rows, the groups
+// through shared memory, the cluster's blocks by its first one.
+// (4096 x 8192 gelu: 34.1 us with three rows, 35.1 with two, 34.2 with four; 16384 x
+// 4096: 65.5, 67.4, 65.1; 8192 x 700: 13.4, 12.9, 13.4)
 constexpr int kActDepth = 3;
 
 template <int DT, int THREADS>
@@ -854,10 +854,10 @@ int act_clusters(int& n, const gemm_handle* h, Kern kern, int threads, size_t sm
 // (which share a strip's rows) of the shortest estimate: waves x (rows a thread
 // walks x a row's time, which grows with the SMs' load, + a block's start).
 // Fitted on GB300 to 21 sizes (16 to 20000 rows of 64 to 28672) x 24 shapes: 3 % over
-// the fastest on average, 15 % at worst.  For instance, gelu: 4096 x 8192 33.5 us with
-// 128 blocks of 1024, 36.4 with 512 of 256 in clusters of 4, 38.9 with 1024 in clusters
-// of 8; 8192 x 1024 14.3 with 16 clusters of 6 blocks of 1024, 22.8 with clusters of 8,
-// of which the device holds 15; 3000 x 5000 18.4 with clusters of 7 of 256, 21.4 with 8.
+// the fastest on average, 15 % at worst.  For instance, gelu: 4096 x 8192 34.1 us with
+// 128 blocks of 1024, 37.4 with 512 of 256 in clusters of 4; 8192 x 1024 13.9 with 16
+// clusters of 6 blocks of 1024, 22.2 with clusters of 8, of which the device holds 15;
+// 3000 x 5000 17.8 with clusters of 7 of 256, 19.4 with 8.
 template <int DT>
 gemm_status_t launch_act_grad(gemm_handle* h, gb300::ActGradParams& k, struct CUstream_st* stream) {
   typedef void (*Kern)(gb300::ActGradParams);

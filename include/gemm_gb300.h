@@ -417,7 +417,8 @@ gemm_status_t gemm_run_noalloc(int64_t M, int64_t N, int64_t K, int64_t L,
  * so q and scale are the A and row_scale of an 8-bit product.  (y is multiplied
  * by the reciprocal, which can move a value that lies within an fp32 rounding
  * of the middle between two codes to the other one.)  A row that holds a NaN
- * gets a NaN scale, rstd and row.
+ * gets a NaN scale, rstd and row; one whose sum of squares exceeds fp32's range
+ * gets rstd 0.
  *   M rows of H elements; M or H = 0: nothing to do.
  *   type: F32, F16 or BF16, the type of x, r and h.  w_type: any of the
  *   three.  y_type: those, E4M3 or E5M2.
@@ -476,7 +477,8 @@ gemm_status_t gemm_rmsnorm_bwd(gemm_handle_t h, const gemm_rmsnorm_bwd_t* p, voi
 
 /* Activations: max(z, 0); z Phi(z) with the normal distribution function;
  * z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2; z / (1 + exp(-z)).  A NaN stays
- * a NaN in each and in its derivative. */
+ * a NaN in each and in its derivative.  At minus infinity GELU_TANH and SILU, there
+ * an infinity times 0, are NaN as well; every derivative has its limit. */
 typedef enum {
   GEMM_ACT_NONE = 0, GEMM_ACT_RELU = 1, GEMM_ACT_GELU = 2, GEMM_ACT_GELU_TANH = 3,
   GEMM_ACT_SILU = 4

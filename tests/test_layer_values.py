@@ -173,3 +173,14 @@ def test_two_handles_at_once():
     finally:
         for g in handles:
             g.close()
+
+
+@pytest.mark.parametrize("rows", ROWS)
+def test_minus_infinity(gemm, rows):
+    """0 times an infinity, NaN, for the tanh form and silu; the limit 0 for relu and gelu."""
+    z = torch.tensor([-float("inf"), -1.0, 1.0])
+    for act, want in (("none", -float("inf")), ("relu", 0.0), ("gelu", 0.0)):
+        assert _forward(gemm, z, act, rows)[0][0] == want, act
+    for act in ("gelu_tanh", "silu"):
+        d = _forward(gemm, z, act, rows)[0]
+        assert torch.isnan(d).tolist() == [True, False, False], act
