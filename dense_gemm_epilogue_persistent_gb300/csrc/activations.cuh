@@ -88,8 +88,7 @@ __device__ __forceinline__ float activate_grad(float v) {
 }
 
 // Two elements at once: the packed fp32 operations of sm_100 and later (one issue
-// slot for two lanes' worth) carry the polynomial of the normal distribution and
-// the products; roundings are those of the single forms.
+// slot for two lanes' worth) carry gelu's polynomial and the products.
 struct Pair {
   unsigned long long v;
 };
