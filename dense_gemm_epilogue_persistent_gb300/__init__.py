@@ -133,12 +133,92 @@ class gemm_linear_bwd_t(ctypes.Structure):
                 ("db", ctypes.c_void_p), ("lddb", ctypes.c_int64), ("dbias", ctypes.c_void_p)]
 
 
+class gemm_route_t(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("k", ctypes.c_int64), ("E", ctypes.c_int64),
+                ("index_bytes", ctypes.c_int), ("index", ctypes.c_void_p),
+                ("ldi", ctypes.c_int64), ("offsets", ctypes.c_void_p),
+                ("slot", ctypes.c_void_p), ("source", ctypes.c_void_p)]
+
+
+class gemm_dispatch_t(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("k", ctypes.c_int64), ("H", ctypes.c_int64),
+                ("R", ctypes.c_int64), ("type", ctypes.c_int), ("x", ctypes.c_void_p),
+                ("ldx", ctypes.c_int64), ("slot", ctypes.c_void_p), ("scale", ctypes.c_void_p),
+                ("y", ctypes.c_void_p), ("ldy", ctypes.c_int64), ("y_scale", ctypes.c_void_p)]
+
+
+class gemm_combine_t(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("k", ctypes.c_int64), ("H", ctypes.c_int64),
+                ("R", ctypes.c_int64), ("type", ctypes.c_int), ("r_type", ctypes.c_int),
+                ("y_type", ctypes.c_int), ("ys", ctypes.c_void_p), ("ldys", ctypes.c_int64),
+                ("slot", ctypes.c_void_p), ("weight", ctypes.c_void_p), ("r", ctypes.c_void_p),
+                ("ldr", ctypes.c_int64), ("y", ctypes.c_void_p), ("ldy", ctypes.c_int64)]
+
+
+class gemm_combine_bwd_t(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("k", ctypes.c_int64), ("H", ctypes.c_int64),
+                ("R", ctypes.c_int64), ("type", ctypes.c_int), ("dy", ctypes.c_void_p),
+                ("lddy", ctypes.c_int64), ("slot", ctypes.c_void_p),
+                ("weight", ctypes.c_void_p), ("ys", ctypes.c_void_p), ("ldys", ctypes.c_int64),
+                ("dys", ctypes.c_void_p), ("lddys", ctypes.c_int64),
+                ("dweight", ctypes.c_void_p)]
+
+
+class gemm_grouped_linear_t(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64),
+                ("groups", ctypes.c_int64), ("sets", ctypes.c_int64), ("a_type", ctypes.c_int),
+                ("b_type", ctypes.c_int), ("bias_type", ctypes.c_int),
+                ("r_type", ctypes.c_int), ("z_type", ctypes.c_int), ("d_type", ctypes.c_int),
+                ("layoutB", ctypes.c_int), ("activation", ctypes.c_int),
+                ("alpha", ctypes.c_float), ("offsets", ctypes.c_void_p),
+                ("index", ctypes.c_void_p), ("A", ctypes.c_void_p), ("lda", ctypes.c_int64),
+                ("B", ctypes.c_void_p), ("ldb", ctypes.c_int64), ("strideB", ctypes.c_int64),
+                ("row_scale", ctypes.c_void_p), ("col_scale", ctypes.c_void_p),
+                ("bias", ctypes.c_void_p), ("R", ctypes.c_void_p), ("ldr", ctypes.c_int64),
+                ("Z", ctypes.c_void_p), ("ldz", ctypes.c_int64), ("D", ctypes.c_void_p),
+                ("ldd", ctypes.c_int64)]
+
+
+class gemm_grouped_linear_bwd_t(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64),
+                ("groups", ctypes.c_int64), ("type", ctypes.c_int), ("da_type", ctypes.c_int),
+                ("db_type", ctypes.c_int), ("dbias_type", ctypes.c_int),
+                ("activation", ctypes.c_int), ("accumulate", ctypes.c_int),
+                ("alpha", ctypes.c_float), ("offsets", ctypes.c_void_p),
+                ("dd", ctypes.c_void_p), ("lddd", ctypes.c_int64), ("z", ctypes.c_void_p),
+                ("ldz", ctypes.c_int64), ("a", ctypes.c_void_p), ("lda", ctypes.c_int64),
+                ("b", ctypes.c_void_p), ("ldb", ctypes.c_int64), ("strideb", ctypes.c_int64),
+                ("dz", ctypes.c_void_p), ("lddz", ctypes.c_int64), ("da", ctypes.c_void_p),
+                ("ldda", ctypes.c_int64), ("db", ctypes.c_void_p), ("lddb", ctypes.c_int64),
+                ("stridedb", ctypes.c_int64), ("dbias", ctypes.c_void_p)]
+
+
+class gemm_adapters_t(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64),
+                ("rank", ctypes.c_int64), ("requests", ctypes.c_int64),
+                ("adapters", ctypes.c_int64), ("type", ctypes.c_int), ("r_type", ctypes.c_int),
+                ("d_type", ctypes.c_int), ("offsets", ctypes.c_void_p),
+                ("index", ctypes.c_void_p), ("x", ctypes.c_void_p), ("ldx", ctypes.c_int64),
+                ("A", ctypes.c_void_p), ("lda", ctypes.c_int64), ("strideA", ctypes.c_int64),
+                ("B", ctypes.c_void_p), ("ldb", ctypes.c_int64), ("strideB", ctypes.c_int64),
+                ("scale", ctypes.c_void_p), ("u", ctypes.c_void_p), ("ldu", ctypes.c_int64),
+                ("r", ctypes.c_void_p), ("ldr", ctypes.c_int64), ("d", ctypes.c_void_p),
+                ("ldd", ctypes.c_int64)]
+
+
 class GemmError(RuntimeError):
     def __init__(self, status: int, what: str = ""):
         self.status = status
         super().__init__(f"{what}: {gemm_status_string(status)}" if what else
                          gemm_status_string(status))
 
+
+# The operators whose weights change from row to row, by the structure they take.
+_PROBLEMS = {"gemm_route": gemm_route_t, "gemm_dispatch": gemm_dispatch_t,
+             "gemm_combine": gemm_combine_t, "gemm_combine_bwd": gemm_combine_bwd_t,
+             "gemm_grouped_linear": gemm_grouped_linear_t,
+             "gemm_grouped_linear_bwd": gemm_grouped_linear_bwd_t,
+             "gemm_adapters": gemm_adapters_t}
 
 _lock = threading.Lock()
 _lib = None
@@ -196,6 +276,10 @@ def library():
             lib.gemm_linear.argtypes = [vp, vp, vp]
             lib.gemm_linear_bwd_check.argtypes = [ctypes.POINTER(gemm_linear_bwd_t)]
             lib.gemm_linear_bwd.argtypes = [vp, vp, vp]
+            for name in _PROBLEMS:
+                call, check = getattr(lib, name), getattr(lib, name + "_check")
+                call.argtypes, check.argtypes = [vp, vp, vp], [ctypes.POINTER(_PROBLEMS[name])]
+                call.restype = check.restype = i32
             for name in ("gemm_create", "gemm_destroy", "gemm_run", "gemm_run_noalloc",
                          "gemm_sync_status",
                          "gemm_check", "gemm_plan", "gemm_set_config", "gemm_last_config",
@@ -397,6 +481,83 @@ def gemm_linear_bwd(handle, problem: gemm_linear_bwd_t, stream=None, check=True)
     return st
 
 
+def gemm_route_check(problem: gemm_route_t) -> int:
+    return library().gemm_route_check(ctypes.byref(problem))
+
+
+def gemm_route(handle, problem: gemm_route_t, stream=None, check=True) -> int:
+    st = library().gemm_route(handle, ctypes.byref(problem), _stream(stream))
+    if check and st != GEMM_OK:
+        raise GemmError(st, "gemm_route")
+    return st
+
+
+def gemm_dispatch_check(problem: gemm_dispatch_t) -> int:
+    return library().gemm_dispatch_check(ctypes.byref(problem))
+
+
+def gemm_dispatch(handle, problem: gemm_dispatch_t, stream=None, check=True) -> int:
+    st = library().gemm_dispatch(handle, ctypes.byref(problem), _stream(stream))
+    if check and st != GEMM_OK:
+        raise GemmError(st, "gemm_dispatch")
+    return st
+
+
+def gemm_combine_check(problem: gemm_combine_t) -> int:
+    return library().gemm_combine_check(ctypes.byref(problem))
+
+
+def gemm_combine(handle, problem: gemm_combine_t, stream=None, check=True) -> int:
+    st = library().gemm_combine(handle, ctypes.byref(problem), _stream(stream))
+    if check and st != GEMM_OK:
+        raise GemmError(st, "gemm_combine")
+    return st
+
+
+def gemm_combine_bwd_check(problem: gemm_combine_bwd_t) -> int:
+    return library().gemm_combine_bwd_check(ctypes.byref(problem))
+
+
+def gemm_combine_bwd(handle, problem: gemm_combine_bwd_t, stream=None, check=True) -> int:
+    st = library().gemm_combine_bwd(handle, ctypes.byref(problem), _stream(stream))
+    if check and st != GEMM_OK:
+        raise GemmError(st, "gemm_combine_bwd")
+    return st
+
+
+def gemm_grouped_linear_check(problem: gemm_grouped_linear_t) -> int:
+    return library().gemm_grouped_linear_check(ctypes.byref(problem))
+
+
+def gemm_grouped_linear(handle, problem: gemm_grouped_linear_t, stream=None, check=True) -> int:
+    st = library().gemm_grouped_linear(handle, ctypes.byref(problem), _stream(stream))
+    if check and st != GEMM_OK:
+        raise GemmError(st, "gemm_grouped_linear")
+    return st
+
+
+def gemm_grouped_linear_bwd_check(problem: gemm_grouped_linear_bwd_t) -> int:
+    return library().gemm_grouped_linear_bwd_check(ctypes.byref(problem))
+
+
+def gemm_grouped_linear_bwd(handle, problem: gemm_grouped_linear_bwd_t, stream=None, check=True) -> int:
+    st = library().gemm_grouped_linear_bwd(handle, ctypes.byref(problem), _stream(stream))
+    if check and st != GEMM_OK:
+        raise GemmError(st, "gemm_grouped_linear_bwd")
+    return st
+
+
+def gemm_adapters_check(problem: gemm_adapters_t) -> int:
+    return library().gemm_adapters_check(ctypes.byref(problem))
+
+
+def gemm_adapters(handle, problem: gemm_adapters_t, stream=None, check=True) -> int:
+    st = library().gemm_adapters(handle, ctypes.byref(problem), _stream(stream))
+    if check and st != GEMM_OK:
+        raise GemmError(st, "gemm_adapters")
+    return st
+
+
 # ------------------------------------------------------------------ tensors
 #
 # The calls on tensors fill the C structures by struct.pack (the fields of the
@@ -407,6 +568,13 @@ _RMSNORM = struct.Struct("<2q3if11Q")
 _RMSNORM_BWD = struct.Struct("<2q3i4x11Q")
 _LINEAR = struct.Struct("<3q9if13Q")
 _LINEAR_BWD = struct.Struct("<3q6if4x15Q")
+_ROUTE = struct.Struct("<3qi4x5Q")
+_DISPATCH = struct.Struct("<4qi4x7Q")
+_COMBINE = struct.Struct("<4q3i4x8Q")
+_COMBINE_BWD = struct.Struct("<4qi4x9Q")
+_GROUPED = struct.Struct("<5q8if4x16Q")
+_GROUPED_BWD = struct.Struct("<4q6if4x18Q")
+_ADAPTERS = struct.Struct("<6q3i4x17Q")
 
 # Type codes by the name of a tensor's dtype.
 _TENSOR_CODES = {"torch.float32": GEMM_F32, "torch.float16": GEMM_F16,
@@ -506,11 +674,105 @@ def _vector(t, n, what, device, code=None):
     return t.data_ptr()
 
 
+def _integers(t, shape, what, device):
+    """Address of a contiguous tensor of int32 of that shape on GPU `device`; 0 for None."""
+    if t is None:
+        return 0
+    try:
+        if t.get_device() != device:
+            raise _elsewhere(t, what, device)
+    except AttributeError:
+        pass
+    if str(t.dtype) != "torch.int32":
+        raise GemmError(GEMM_ERR_UNSUPPORTED_DTYPE, f"{what}: {t.dtype}")
+    _packed(t, shape, what)
+    return t.data_ptr()
+
+
+def _packed(t, shape, what):
+    """Refuses a tensor that is not contiguous of that shape."""
+    if t.shape != shape:
+        raise GemmError(GEMM_ERR_INVALID_ARG, f"{what}: shape {tuple(t.shape)}, not {tuple(shape)}")
+    want = 1
+    for n, stride in zip(reversed(shape), reversed(t.stride())):
+        if n > 1 and stride != want and 0 not in shape:
+            raise GemmError(GEMM_ERR_INVALID_ARG, f"{what}: not contiguous")
+        want *= n
+
+
+def _table(t, shape, what, device, code=None):
+    """Address of a contiguous matrix of that shape on GPU `device` (of type `code` if given);
+    0 for None."""
+    if t is None:
+        return 0
+    try:
+        if t.get_device() != device:
+            raise _elsewhere(t, what, device)
+    except AttributeError:
+        pass
+    _packed(t, shape, what)
+    if code is not None and _code(t, what) != code:
+        raise GemmError(GEMM_ERR_UNSUPPORTED_DTYPE, f"{what}: {t.dtype}")
+    return t.data_ptr()
+
+
+def _choices(slot, T, what="slot"):
+    """k of a [T, k] tensor of places."""
+    shape = _shape(slot, what)
+    if shape[0] != T:
+        raise GemmError(GEMM_ERR_INVALID_ARG, f"{what}: {shape[0]} tokens, not {T}")
+    return shape[1]
+
+
+def _groups(offsets, what="offsets"):
+    """Groups of a vector of their bounds."""
+    if len(offsets.shape) != 1 or offsets.shape[0] < 1:
+        raise GemmError(GEMM_ERR_INVALID_ARG, f"{what}: shape {tuple(offsets.shape)}")
+    return offsets.shape[0] - 1
+
+
+def _stack(t, shape, what, device, code=None, k_major=False):
+    """(address, row stride, layout, stride of the matrices) of a stack of that shape, either of
+    the last two dimensions contiguous (`k_major`: the last), on GPU `device`, of type
+    `code` if given; zeros for None."""
+    if t is None:
+        return 0, 0, GEMM_K_MAJOR, 0
+    if t.shape != shape:
+        raise GemmError(GEMM_ERR_INVALID_ARG, f"{what}: shape {tuple(t.shape)}, not {tuple(shape)}")
+    if code is not None and _code(t, what) != code:
+        raise GemmError(GEMM_ERR_UNSUPPORTED_DTYPE, f"{what}: {t.dtype}")
+    sets, R, K = shape
+    s0, s1, s2 = t.stride()
+    if not sets * R * K:                 # (no element: the strides say nothing)
+        layout, ld, s0 = GEMM_K_MAJOR, (K + 15) // 16 * 16, 0
+    elif s2 == 1 and not (s1 == 1 and R > 1) or (K == 1 and (R == 1 or k_major)):
+        layout, ld = GEMM_K_MAJOR, s1 if R > 1 else (max(s1, K) + 15) // 16 * 16
+    elif (s1 == 1 or R == 1) and not k_major:
+        layout, ld = GEMM_MN_MAJOR, s2 if K > 1 else (max(s2, R) + 15) // 16 * 16
+    else:
+        raise GemmError(GEMM_ERR_INVALID_ARG, f"{what}: " + (
+            "rows are not contiguous" if k_major else "neither dimension is contiguous"))
+    try:
+        if t.get_device() != device:
+            raise _elsewhere(t, what, device)
+    except AttributeError:
+        pass
+    return t.data_ptr(), ld, layout, s0 if sets > 1 else 0
+
+
+def _stack_shape(t, what):
+    shape = t.shape
+    if len(shape) != 3:
+        raise GemmError(GEMM_ERR_INVALID_ARG, f"{what}: shape {tuple(shape)}, not a stack of matrices")
+    return shape
+
+
 class Gemm:
     """Owns one library handle on `device`.
 
     run, run_host: the C entry points' arguments.  rmsnorm, rmsnorm_bwd, linear,
-    linear_bwd: the operators around the product on tensors (torch's or any with
+    linear_bwd, route, dispatch, combine, combine_bwd, grouped_linear,
+    grouped_linear_bwd, adapters: the operators around the product on tensors (torch's or any with
     data_ptr, dtype, shape and stride), whose device, types, sizes and row strides the
     calls read off and check; outputs are the caller's tensors too.
     Tensors are used on `stream` (None: the default stream) and must be ready there."""
@@ -660,3 +922,145 @@ class Gemm:
             stream and _stream(stream))
         if st:
             raise GemmError(st, "gemm_linear_bwd")
+
+    def route(self, index, offsets, slot, source=None, stream=None):
+        """Sorts the choices index [T, k] (int32 or int64, rows contiguous) by expert:
+        offsets [E + 1], each choice's place in slot [T, k] (-1: not an expert), the choice of
+        each place in source [T k], all int32; see gemm_route in the C header."""
+        shape = _shape(index, "index")
+        T, k = shape
+        dev = self.device
+        width = {"torch.int32": 4, "torch.int64": 8}.get(str(index.dtype))
+        if width is None:
+            raise GemmError(GEMM_ERR_UNSUPPORTED_DTYPE, f"index: {index.dtype}")
+        p_index, ldi = _rows(index, shape, "index", dev)
+        E = _groups(offsets)
+        st = self._lib.gemm_route(self.handle, _ROUTE.pack(
+            T, k, E, width, p_index, ldi, _integers(offsets, (E + 1,), "offsets", dev),
+            _integers(slot, shape, "slot", dev), _integers(source, (T * k,), "source", dev)),
+            stream and _stream(stream))
+        if st:
+            raise GemmError(st, "gemm_route")
+
+    def dispatch(self, x, slot, y, scale=None, y_scale=None, stream=None):
+        """Each row of x [T, H] to the rows slot [T, k] of y [R, H], its scale along; see
+        gemm_dispatch in the C header."""
+        shape = _shape(x, "x")
+        T, H = shape
+        k, R = _choices(slot, T), _shape(y, "y")[0]
+        t, dev = _code(x, "x"), self.device
+        st = self._lib.gemm_dispatch(self.handle, _DISPATCH.pack(
+            T, k, H, R, t, *_rows(x, shape, "x", dev), _integers(slot, (T, k), "slot", dev),
+            _vector(scale, T, "scale", dev, GEMM_F32), *_rows(y, (R, H), "y", dev, t),
+            _vector(y_scale, R, "y_scale", dev, GEMM_F32)), stream and _stream(stream))
+        if st:
+            raise GemmError(st, "gemm_dispatch")
+
+    def combine(self, ys, slot, y, weight=None, residual=None, stream=None):
+        """y [T, H] = residual + the sum of each token's rows slot [T, k] of ys [R, H], times
+        weight [T, k]; see gemm_combine in the C header."""
+        shape = _shape(y, "y")
+        T, H = shape
+        k, R = _choices(slot, T), _shape(ys, "ys")[0]
+        dev = self.device
+        st = self._lib.gemm_combine(self.handle, _COMBINE.pack(
+            T, k, H, R, _code(ys, "ys"), 0 if residual is None else _code(residual, "residual"),
+            _code(y, "y"), *_rows(ys, (R, H), "ys", dev), _integers(slot, (T, k), "slot", dev),
+            _table(weight, (T, k), "weight", dev, GEMM_F32),
+            *_rows(residual, shape, "residual", dev), *_rows(y, shape, "y", dev)),
+            stream and _stream(stream))
+        if st:
+            raise GemmError(st, "gemm_combine")
+
+    def combine_bwd(self, dy, slot, dys=None, weight=None, ys=None, dweight=None, stream=None):
+        """Gradients of combine from dy, the gradient of y: dys (rows slot [T, k]) and dweight
+        [T, k] (which reads ys), each where given; see gemm_combine_bwd in the C header."""
+        shape = _shape(dy, "dy")
+        T, H = shape
+        rows = dys if dys is not None else ys
+        k, R = _choices(slot, T), 0 if rows is None else _shape(rows, "dys or ys")[0]
+        t, dev = _code(dy, "dy"), self.device
+        st = self._lib.gemm_combine_bwd(self.handle, _COMBINE_BWD.pack(
+            T, k, H, R, t, *_rows(dy, shape, "dy", dev), _integers(slot, (T, k), "slot", dev),
+            _table(weight, (T, k), "weight", dev, GEMM_F32), *_rows(ys, (R, H), "ys", dev, t),
+            *_rows(dys, (R, H), "dys", dev, t),
+            _table(dweight, (T, k), "dweight", dev, GEMM_F32)), stream and _stream(stream))
+        if st:
+            raise GemmError(st, "gemm_combine_bwd")
+
+    def grouped_linear(self, a, b, offsets, d, index=None, bias=None, activation=None,
+                       residual=None, z=None, row_scale=None, col_scale=None, alpha=1.0,
+                       stream=None):
+        """linear with weights b[e] [N, K] of its own for each group of rows: group g has the
+        rows offsets[g] .. offsets[g + 1] - 1 of a [M, K] and the weights e = g, or
+        index[g] (int32; none outside b); bias and col_scale [sets, N]; see
+        gemm_grouped_linear in the C header.  fp32 a and b are GEMM_TF32's, as in linear."""
+        M, K = _shape(a, "a")
+        sets, N, inner = _stack_shape(b, "b")
+        if inner != K:
+            raise GemmError(GEMM_ERR_INVALID_ARG, f"b: shape {(sets, N, inner)}, not {(sets, N, K)}")
+        dev, groups = self.device, _groups(offsets)
+        pb, ldb, lb, stride = _stack(b, (sets, N, K), "b", dev)
+        out, cols = (M, N), (sets, N)
+        st = self._lib.gemm_grouped_linear(self.handle, _GROUPED.pack(
+            M, N, K, groups, sets, _code(a, "a") or GEMM_TF32, _code(b, "b") or GEMM_TF32,
+            0 if bias is None else _code(bias, "bias"),
+            0 if residual is None else _code(residual, "residual"),
+            0 if z is None else _code(z, "z"), _code(d, "d"), lb, _activation(activation), alpha,
+            _integers(offsets, (groups + 1,), "offsets", dev),
+            _integers(index, (groups,), "index", dev), *_rows(a, (M, K), "a", dev), pb, ldb, stride,
+            _vector(row_scale, M, "row_scale", dev, GEMM_F32),
+            _table(col_scale, cols, "col_scale", dev, GEMM_F32), _table(bias, cols, "bias", dev),
+            *_rows(residual, out, "residual", dev), *_rows(z, out, "z", dev),
+            *_rows(d, out, "d", dev)), stream and _stream(stream))
+        if st:
+            raise GemmError(st, "gemm_grouped_linear")
+
+    def grouped_linear_bwd(self, dd, a, b, offsets, z=None, activation=None, dz=None, da=None,
+                           db=None, dbias=None, accumulate=False, alpha=1.0, stream=None):
+        """Gradients of grouped_linear (without scales and index) from dd, the gradient of d:
+        dz, da, db [groups, N, K] (added to with `accumulate`) and dbias [groups, N], each
+        where given; see gemm_grouped_linear_bwd in the C header.  a is read for db only and b
+        for da only: else either may be None."""
+        out = _shape(dd, "dd")
+        M, N = out
+        inner = a if a is not None else da if da is not None else b if b is not None else db
+        K = 0 if inner is None else inner.shape[-1]
+        t, dev, groups = _code(dd, "dd"), self.device, _groups(offsets)
+        rows_a, stack_b = (M, K), (groups, N, K)
+        pb, ldb, _, strideb = _stack(b, stack_b, "b", dev, t, k_major=True)
+        pdb, lddb, _, stridedb = _stack(db, stack_b, "db", dev, k_major=True)
+        st = self._lib.gemm_grouped_linear_bwd(self.handle, _GROUPED_BWD.pack(
+            M, N, K, groups, t, 0 if da is None else _code(da, "da"),
+            0 if db is None else _code(db, "db"), 0 if dbias is None else _code(dbias, "dbias"),
+            _activation(activation), int(accumulate), alpha,
+            _integers(offsets, (groups + 1,), "offsets", dev), *_rows(dd, out, "dd", dev),
+            *_rows(z, out, "z", dev, t), *_rows(a, rows_a, "a", dev, t), pb, ldb, strideb,
+            *_rows(dz, out, "dz", dev, t), *_rows(da, rows_a, "da", dev), pdb, lddb, stridedb,
+            _table(dbias, (groups, N), "dbias", dev)), stream and _stream(stream))
+        if st:
+            raise GemmError(st, "gemm_grouped_linear_bwd")
+
+    def adapters(self, x, a, b, offsets, index, u, d, residual=None, scale=None, stream=None):
+        """d = residual + scale[e] * (x a[e]^T) b[e]^T, request s having the rows
+        offsets[s] .. offsets[s + 1] - 1 and the adapter e = index[s] (none outside a); a
+        [adapters, rank, K], b [adapters, N, rank]; u [M, rank] is a workspace; see
+        gemm_adapters in the C header."""
+        M, K = _shape(x, "x")
+        n, rank, inner = _stack_shape(a, "a")
+        if inner != K:
+            raise GemmError(GEMM_ERR_INVALID_ARG, f"a: shape {(n, rank, inner)}, not {(n, rank, K)}")
+        out = _shape(d, "d")
+        N = out[1]
+        t, dev, requests = _code(x, "x"), self.device, _groups(offsets)
+        pa, lda, _, stride_a = _stack(a, (n, rank, K), "a", dev, t, k_major=True)
+        pb, ldb, _, stride_b = _stack(b, (n, N, rank), "b", dev, t, k_major=True)
+        st = self._lib.gemm_adapters(self.handle, _ADAPTERS.pack(
+            M, N, K, rank, requests, n, t, 0 if residual is None else _code(residual, "residual"),
+            _code(d, "d"), _integers(offsets, (requests + 1,), "offsets", dev),
+            _integers(index, (requests,), "index", dev), *_rows(x, (M, K), "x", dev),
+            pa, lda, stride_a, pb, ldb, stride_b, _vector(scale, n, "scale", dev, GEMM_F32),
+            *_rows(u, (M, rank), "u", dev, t), *_rows(residual, (M, N), "residual", dev),
+            *_rows(d, (M, N), "d", dev)), stream and _stream(stream))
+        if st:
+            raise GemmError(st, "gemm_adapters")

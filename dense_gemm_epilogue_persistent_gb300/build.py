@@ -63,16 +63,21 @@ PLAIN_UNITS = [(f"kern_plain_ab{ab}_e{epw}_s{sk}", "kern_plain.cu",
 SHARED_UNITS = [(f"kern_shared_ab{ab}_m{mc}_n{nc}", "kern_shared.cu",
                  [f"-DGB300_AB={ab}", f"-DGB300_MC={mc}", f"-DGB300_NC={nc}"])
                 for ab in (2, 1, 4) for mc, nc in ((2, 1), (1, 2), (2, 2))]
-# The operators around the product: normalisation, the linear layer and its kernels.
+# The operators around the product: normalisation, the linear layer and its kernels; sorting
+# by expert, the linear layer over groups of rows and its kernel.
 ROW_UNITS = [("norm", "norm.cu", []), ("linear", "linear.cu", []),
-             ("kern_split", "kern_split.cu", [])]
+             ("kern_split", "kern_split.cu", []), ("routing", "routing.cu", []),
+             ("grouped", "grouped.cu", [])]
+GROUPED_UNITS = [(f"kern_grouped_ab{ab}", "kern_grouped.cu", [f"-DGB300_AB={ab}"])
+                 for ab in (2, 1, 4)]
 LINEAR_UNITS = [(f"kern_linear_ab{ab}_e{epw}_p{epi}", "kern_linear.cu",
                  [f"-DGB300_AB={ab}", f"-DGB300_EPW={epw}", f"-DGB300_EPI={epi}"])
                 for ab, epi in ((2, 1), (1, 1), (4, 1), (2, 2)) for epw in (1, 2)]
 # Files the multi-GPU library is built from (its translation units and every
 # header they include): none of them names a multicast TMA load.
 NOMC_FILES = ["gemm_api.cu", "norm.cu", "linear.cu", "kern_plain.cu", "kern_linear.cu",
-              "kern_split.cu", "gemm_kernel.cuh", "split_kernel.cuh", "activations.cuh", "rows.cuh",
+              "kern_split.cu", "routing.cu", "grouped.cu", "kern_grouped.cu", "gemm_kernel.cuh",
+              "split_kernel.cuh", "grouped_kernel.cuh", "activations.cuh", "rows.cuh",
               "ptx.cuh", "kernels.h", "handle.h", "rows_host.h"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -84,9 +89,9 @@ def units(kind: str):
     """Translation units of one library: (object name, source, -D flags)."""
     if kind == "nomc":
         return ([("gemm_api_nomc", "gemm_api.cu", ["-DGB300_MULTICAST=0"])] + ROW_UNITS +
-                LINEAR_UNITS + PLAIN_UNITS)
+                LINEAR_UNITS + GROUPED_UNITS + PLAIN_UNITS)
     return ([("gemm_api", "gemm_api.cu", ["-DGB300_MULTICAST=1"])] + ROW_UNITS + LINEAR_UNITS +
-            PLAIN_UNITS + SHARED_UNITS)
+            GROUPED_UNITS + PLAIN_UNITS + SHARED_UNITS)
 
 
 def _nvcc() -> str:

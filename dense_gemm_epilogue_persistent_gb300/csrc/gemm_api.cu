@@ -494,6 +494,23 @@ bool gb300host::encode_operand(EncodeTiledFn enc, CUtensorMap* map, const void* 
   return r == CUDA_SUCCESS;
 }
 
+// The same map over `sets` matrices of `rows` rows of `inner` contiguous elements, `stride`
+// elements apart: box {128 bytes, box_rows}.
+bool gb300host::encode_stack(EncodeTiledFn enc, CUtensorMap* map, const void* ptr, int dt,
+                             int64_t inner, int64_t rows, int64_t sets, int64_t ld, int64_t stride,
+                             int box_rows) {
+  const int64_t es = dtype_bytes(dt);
+  const cuuint64_t dims[3] = {(cuuint64_t)inner, (cuuint64_t)rows, (cuuint64_t)sets};
+  const cuuint64_t strides[2] = {(cuuint64_t)(ld * es),
+                                 (cuuint64_t)((sets > 1 ? stride : ld * rows) * es)};
+  const cuuint32_t box[3] = {(cuuint32_t)(128 / es), (cuuint32_t)box_rows, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return enc(map, tma_type(dt), 3, const_cast<void*>(ptr), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Epilogue tensor map over an M x N x L tensor whose rows (row-major) or columns
 // (column-major) are `ld` elements apart, batches packed, box = 32 rows x 32
 // columns (one epilogue warp's rows of one chunk).  Row-major: dims {N, M, L},
@@ -1005,6 +1022,7 @@ GEMM_API gemm_status_t gemm_run(gemm_handle_t h, int64_t M, int64_t N, int64_t K
     return GEMM_ERR_CUDA;
   }
   h->last = ent->cfg;
+  h->counted = true;
   return GEMM_OK;
 }
 
@@ -1095,9 +1113,9 @@ GEMM_API gemm_status_t gemm_ring_stats(gemm_handle_t h, struct CUstream_st* stre
   *n_ctas = 0;
   if (!gb300::kRingStats || !h->d_stats) return GEMM_ERR_UNSUPPORTED_CONFIG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  // (the split-K kernel keeps no counters: what is there is an earlier launch's)
-  const int n =
-      h->last.split_k > 0 ? 0 : std::min(h->last.grid_ctas, std::min(max_ctas, h->sm_count));
+  // (the split-K and grouped kernels keep no counters: what is there is an earlier launch's)
+  const int n = h->last.split_k > 0 || !h->counted
+                    ? 0 : std::min(h->last.grid_ctas, std::min(max_ctas, h->sm_count));
   if (cudaStreamSynchronize(s) != cudaSuccess ||
       (n > 0 && cudaMemcpy(out, h->d_stats, (size_t)n * gb300::kStatWords * sizeof(uint64_t),
                            cudaMemcpyDeviceToHost) != cudaSuccess)) {

@@ -1,0 +1,450 @@
+// The linear layer over groups of rows with weights of their own, its backward pass, and
+// low-rank adapters (include/gemm_gb300.h): argument checks, planning and launches of
+// the kernel in grouped_kernel.cuh.
+#include <algorithm>
+#include <cstdint>
+#include <cstring>
+
+#include "gemm_gb300.h"
+#include "grouped_kernel.cuh"
+#include "handle.h"
+#include "kernels.h"
+#include "rows_host.h"
+
+namespace {
+
+using namespace gb300host;
+
+// One launch of the kernel.  Rows form: F the weights [sets][feats, k] (f_mn: [k, feats]),
+// T the tokens [rows, k].  Weights form: F the tokens' inputs [rows, feats], T the
+// gradients of their outputs [rows, cols].
+struct Product {
+  bool weights = false;
+  int64_t rows = 0, feats = 0, cols = 0, k = 0, groups = 0, sets = 0;
+  gemm_dtype_t f_type{}, t_type{};
+  bool f_mn = false;
+  const void* f = nullptr; int64_t ldf = 0, stride_f = 0;
+  const void* t = nullptr; int64_t ldt = 0;
+  gb300::GroupedParams k_params{};     // the epilogue's part, offsets and index
+};
+
+struct GroupedPlan {
+  gemm_config_t cfg{};
+  const void* kern = nullptr;
+};
+
+// Widths of the token operand's boxes: a tile's width is a multiple of this x cta_group.
+int box_unit(bool weights, int cta_group, int bn) {
+  return weights ? 64 : cta_group == 2 ? 32 : bn % 32 == 0 && bn > 64 ? 32 : 16;
+}
+
+// The launch's tile, ring and grid (h->mu held).
+gemm_status_t plan_grouped(gemm_handle* h, const Product& p, GroupedPlan& out) {
+  const gemm_config_t f = h->forced ? h->forced_cfg : gemm_config_t{};
+  if (f.cluster_m > 1 || f.cluster_n > 1 || f.split_k > 0 || f.stream_k > 1)
+    return GEMM_ERR_UNSUPPORTED_CONFIG;
+  const int es = dtype_bytes(p.f_type);
+  const int64_t mean = cdiv(p.rows, std::max<int64_t>(1, std::min(p.groups, p.rows)));
+  gemm_config_t& c = out.cfg;
+  if (p.weights)
+    c.cta_group = p.groups * cdiv(p.feats, 256) * cdiv(p.cols, 256) * 2 > h->sm_count / 2 ? 2 : 1;
+  else
+    c.cta_group = p.feats > 128 && mean > 64 ? 2 : 1;
+  if (f.cta_group) c.cta_group = f.cta_group;
+  if (c.cta_group != 1 && c.cta_group != 2) return GEMM_ERR_UNSUPPORTED_CONFIG;
+  c.tile_n = c.cta_group == 2 ? 256 : p.weights ? 128 : 64;
+  if (f.tile_n) c.tile_n = f.tile_n;
+  if (c.tile_n < 16 || c.tile_n > 256) return GEMM_ERR_UNSUPPORTED_CONFIG;
+  const int unit = box_unit(p.weights, c.cta_group, c.tile_n);
+  if (c.tile_n % (unit * c.cta_group) != 0) return GEMM_ERR_UNSUPPORTED_CONFIG;
+  const int table = (int)p.groups;
+  const auto smem = [&](int stages) {
+    return gb300::grouped_smem(c.cta_group, c.tile_n, stages, table);
+  };
+  while (c.stages < gb300::kGroupedMaxStages && smem(c.stages + 1) <= h->smem_optin) ++c.stages;
+  if (f.stages) {
+    if (f.stages < 0 || f.stages > c.stages) return GEMM_ERR_UNSUPPORTED_CONFIG;
+    c.stages = f.stages;
+  }
+  if (c.stages < 1) return GEMM_ERR_UNSUPPORTED_CONFIG;
+  // (more than half an SM's shared memory: one CTA an SM, which owns its tensor memory)
+  c.smem_bytes = std::max(smem(c.stages), h->smem_optin / 2 + 1024);
+  c.tile_m = 128 * c.cta_group;
+  c.tile_k = 128 / es * gb300::kGroupedKA;
+  c.acc_stages = gb300::kAccStages;
+  c.ring_bytes = c.stages * gb300::grouped_stage_bytes(c.cta_group, c.tile_n);
+  c.cluster_m = c.cluster_n = 1;
+  c.epi_warps = 2;
+  c.inject_stall = f.inject_stall;
+  // At most this many items: the device finds out how many there are.
+  const int64_t tiles_f = cdiv(p.feats, c.tile_m);
+  c.tiles = p.weights ? p.groups * tiles_f * cdiv(p.cols, c.tile_n)
+                      : (p.rows / c.tile_n + std::min(p.groups, p.rows)) * tiles_f;
+  if (c.tiles > INT32_MAX / 2) return GEMM_ERR_INVALID_ARG;
+  out.kern = gb300::grouped_kernel_for(es, c.cta_group, p.weights);
+  if (!out.kern) return GEMM_ERR_UNSUPPORTED_CONFIG;
+  int resident = 0;
+  GB300_CHECK(resident_kernel_clusters(
+      h, h->grouped_variants[es == 2 ? 0 : es == 1 ? 1 : 2][c.cta_group - 1][p.weights], out.kern, c,
+      c.cta_group, &resident));
+  c.grid_ctas = (int)std::max<int64_t>(1, std::min<int64_t>(c.tiles, resident)) * c.cta_group;
+  return GEMM_OK;
+}
+
+// Enqueue a planned launch (h->mu held).
+gemm_status_t run_grouped(gemm_handle* h, const Product& p, const GroupedPlan& plan,
+                          struct CUstream_st* stream) {
+  const gemm_config_t& c = plan.cfg;
+  const int es = dtype_bytes(p.f_type);
+  const int unit = box_unit(p.weights, c.cta_group, c.tile_n), bk = c.tile_k;
+  CUtensorMap f, t;
+  std::memset(&f, 0, sizeof(f));
+  std::memset(&t, 0, sizeof(t));
+  gb300::GroupedParams k = p.k_params;
+  k.has_operands = p.weights ? p.rows > 0 : p.k > 0;
+  if (k.has_operands) {
+    const bool ok =
+        p.weights
+            ? encode_stack(h->encode, &f, p.f, p.f_type, p.feats, p.rows, 1, p.ldf, 0, bk) &&
+                  encode_stack(h->encode, &t, p.t, p.t_type, p.cols, p.rows, 1, p.ldt, 0, bk)
+            : (p.f_mn ? encode_stack(h->encode, &f, p.f, p.f_type, p.feats, p.k, p.sets, p.ldf,
+                                     p.stride_f, bk)
+                      : encode_stack(h->encode, &f, p.f, p.f_type, p.k, p.feats, p.sets, p.ldf,
+                                     p.stride_f, 128)) &&
+                  encode_stack(h->encode, &t, p.t, p.t_type, p.k, p.rows, 1, p.ldt, 0, unit);
+    if (!ok) return GEMM_ERR_CUDA;
+  }
+  k.rows = (int)p.rows; k.feats = (int)p.feats; k.cols = (int)p.cols; k.k = (int)p.k;
+  k.groups = (int)p.groups; k.sets = (int)p.sets;
+  k.bn = c.tile_n;
+  k.unit = unit;
+  k.tiles_f = (int)cdiv(p.feats, c.tile_m);
+  k.tiles_c = p.weights ? (int)cdiv(p.cols, c.tile_n) : 1;
+  k.stages = c.stages;
+  k.f_mn = p.f_mn;
+  k.idesc = make_idesc(p.f_type, p.t_type, false, c.cta_group, 0, p.weights || p.f_mn, p.weights);
+  k.status = h->d_status;
+  k.timeout_ns = h->timeout_ns;
+  k.inject_stall = c.inject_stall;
+  (void)es;
+  cudaLaunchConfig_t lc{};
+  cudaLaunchAttribute attr[2];
+  lc.gridDim = dim3((unsigned)c.grid_ctas);
+  lc.blockDim = dim3((unsigned)gb300::grouped_threads(p.weights));
+  lc.dynamicSmemBytes = (size_t)c.smem_bytes;
+  lc.stream = reinterpret_cast<cudaStream_t>(stream);
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)c.cta_group;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  lc.attrs = attr;
+  lc.numAttrs = c.cta_group > 1 ? 2 : 1;
+  h->last = c;
+  h->counted = false;
+  void* args[3] = {&f, &t, &k};
+  if (cudaLaunchKernelExC(&lc, plan.kern, args) != cudaSuccess) {
+    cudaGetLastError();
+    return GEMM_ERR_CUDA;
+  }
+  return GEMM_OK;
+}
+
+bool is_count(int64_t v) { return v >= 0 && v <= gb300::kGroupedMaxGroups; }
+
+// Offsets, and an index where there is one.
+gemm_status_t check_groups(const int32_t* offsets, const int32_t* index) {
+  if (!offsets) return GEMM_ERR_INVALID_ARG;
+  return aligned_to(offsets, 4) && aligned_to(index, 4) ? GEMM_OK : GEMM_ERR_MISALIGNED;
+}
+
+// `sets` matrices of `rows` rows of `inner` contiguous elements, `stride` apart.
+gemm_status_t check_stack(const void* p, int64_t ld, int64_t inner, int64_t rows, int64_t sets,
+                          int64_t stride, int dt) {
+  GB300_CHECK(check_operand(p, ld, inner, rows, dt));
+  if (sets <= 1) return GEMM_OK;
+  if (stride < 0 || (stride * dtype_bytes(dt)) % 16 != 0) return GEMM_ERR_MISALIGNED;
+  return map_ok(stride, 1, dt) ? GEMM_OK : GEMM_ERR_INVALID_ARG;
+}
+
+// Matrices that are written may not lie on one another.
+bool apart(int64_t stride, int64_t ld, int64_t rows, int64_t cols, int64_t sets) {
+  return sets <= 1 || rows == 0 || stride >= (rows - 1) * ld + cols;
+}
+
+// Feature tiles x token tiles of any grouping fit the items' numbers.
+bool items_ok(int64_t rows, int64_t groups, int64_t feats) {
+  return (cdiv(rows, 16) + groups) * cdiv(feats, 128) <= INT32_MAX / 2;
+}
+
+gemm_status_t check_grouped(const gemm_grouped_linear_t& p) {
+  if (!is_extent(p.M) || !is_extent(p.N) || !is_extent(p.K) || !is_count(p.groups) ||
+      !is_count(p.sets) || (!p.index && p.sets < p.groups))
+    return GEMM_ERR_INVALID_ARG;
+  if (!is_layout(p.layoutB) || !is_activation(p.activation)) return GEMM_ERR_INVALID_ARG;
+  if (!is_ab_type(p.a_type) || !is_ab_type(p.b_type) ||
+      (p.a_type != p.b_type && !(is_fp8(p.a_type) && is_fp8(p.b_type))))
+    return GEMM_ERR_UNSUPPORTED_DTYPE;
+  if (p.a_type == GEMM_TF32 && p.layoutB != GEMM_K_MAJOR) return GEMM_ERR_UNSUPPORTED_DTYPE;
+  if (!is_epi_type(p.d_type) || (p.bias && !is_epi_type(p.bias_type)) ||
+      (p.R && !is_epi_type(p.r_type)) || (p.Z && !is_epi_type(p.z_type)))
+    return GEMM_ERR_UNSUPPORTED_DTYPE;
+  if (p.M == 0 || p.N == 0 || p.groups == 0) return GEMM_OK;
+  GB300_CHECK(check_groups(p.offsets, p.index));
+  if (!items_ok(p.M, p.groups, p.N)) return GEMM_ERR_INVALID_ARG;
+  GB300_CHECK(check_operand(p.D, p.ldd, p.N, p.M, p.d_type));
+  if (p.R) GB300_CHECK(check_operand(p.R, p.ldr, p.N, p.M, p.r_type));
+  if (p.Z) GB300_CHECK(check_operand(p.Z, p.ldz, p.N, p.M, p.z_type));
+  if (p.K > 0 && p.sets > 0) {
+    const bool bn = p.layoutB == GEMM_MN_MAJOR;
+    GB300_CHECK(check_operand(p.A, p.lda, p.K, p.M, p.a_type));
+    GB300_CHECK(check_stack(p.B, p.ldb, bn ? p.N : p.K, bn ? p.K : p.N, p.sets, p.strideB, p.b_type));
+  }
+  if (!aligned_to(p.row_scale, 4) || !aligned_to(p.col_scale, 4) ||
+      (p.bias && !aligned_to(p.bias, dtype_bytes(p.bias_type))))
+    return GEMM_ERR_MISALIGNED;
+  // in place: element for element only; nothing else may share an output
+  if (p.R == p.D && (p.r_type != p.d_type || p.ldr != p.ldd)) return GEMM_ERR_INVALID_ARG;
+  if (p.Z && (p.Z == p.D || p.Z == p.R)) return GEMM_ERR_INVALID_ARG;
+  if (p.K > 0 && (p.D == p.A || p.D == p.B || (p.Z && (p.Z == p.A || p.Z == p.B))))
+    return GEMM_ERR_INVALID_ARG;
+  return GEMM_OK;
+}
+
+Product product_of(const gemm_grouped_linear_t& p) {
+  Product q;
+  q.rows = p.M; q.feats = p.N; q.groups = p.groups; q.sets = p.sets;
+  q.k = p.sets > 0 ? p.K : 0;          // (no group has weights)
+  q.f_type = p.b_type; q.t_type = p.a_type;
+  q.f_mn = p.layoutB == GEMM_MN_MAJOR;
+  q.f = p.B; q.ldf = p.ldb; q.stride_f = p.strideB;
+  q.t = p.A; q.ldt = p.lda;
+  gb300::GroupedParams& k = q.k_params;
+  k.offsets = p.offsets; k.index = p.index;
+  k.alpha = p.alpha;
+  k.row_scale = p.row_scale; k.col_scale = p.col_scale;
+  k.bias = p.bias; k.bias_dt = p.bias_type;
+  k.r = p.R; k.ldr = p.ldr; k.r_dt = p.r_type;
+  k.z = p.Z; k.ldz = p.ldz; k.z_dt = p.z_type;
+  k.d = p.D; k.ldd = p.ldd; k.d_dt = p.d_type;
+  k.act = p.activation;
+  k.skip_none = p.R == p.D && !p.Z;
+  return q;
+}
+
+// dz as the products read it: the caller's buffer, or dd itself where there is no
+// activation and no buffer.
+const void* dz_of(const gemm_grouped_linear_bwd_t& p, int64_t& ld) {
+  ld = p.dz ? p.lddz : p.lddd;
+  return p.dz ? p.dz : p.dd;
+}
+
+Product product_da(const gemm_grouped_linear_bwd_t& p, const void* dz, int64_t lddz) {
+  Product q;
+  q.rows = p.M; q.feats = p.K; q.k = p.N; q.groups = q.sets = p.groups;
+  q.f_type = q.t_type = p.type;
+  q.f_mn = true;
+  q.f = p.b; q.ldf = p.ldb; q.stride_f = p.strideb;
+  q.t = dz; q.ldt = lddz;
+  gb300::GroupedParams& k = q.k_params;
+  k.offsets = p.offsets;
+  k.alpha = p.alpha;
+  k.d = p.da; k.ldd = p.ldda; k.d_dt = p.da_type;
+  return q;
+}
+
+Product product_db(const gemm_grouped_linear_bwd_t& p, const void* dz, int64_t lddz) {
+  Product q;
+  q.weights = true;
+  q.rows = p.M; q.feats = p.K; q.cols = p.N; q.groups = q.sets = p.groups;
+  q.f_type = q.t_type = p.type;
+  q.f = p.a; q.ldf = p.lda;
+  q.t = dz; q.ldt = lddz;
+  gb300::GroupedParams& k = q.k_params;
+  k.offsets = p.offsets;
+  k.alpha = p.alpha;
+  k.d = p.db; k.ldd = p.lddb; k.sd = p.stridedb; k.d_dt = p.db_type;
+  if (p.accumulate) { k.r = p.db; k.ldr = p.lddb; k.r_dt = p.db_type; }
+  return q;
+}
+
+gemm_status_t check_grouped_bwd(const gemm_grouped_linear_bwd_t& p) {
+  if (!is_extent(p.M) || !is_extent(p.N) || !is_extent(p.K) || !is_count(p.groups) ||
+      !is_activation(p.activation))
+    return GEMM_ERR_INVALID_ARG;
+  if (p.type != GEMM_F16 && p.type != GEMM_BF16) return GEMM_ERR_UNSUPPORTED_DTYPE;
+  if ((p.da && !is_epi_type(p.da_type)) || (p.db && !is_epi_type(p.db_type)) ||
+      (p.dbias && !is_epi_type(p.dbias_type)))
+    return GEMM_ERR_UNSUPPORTED_DTYPE;
+  if (p.N == 0 || p.groups == 0) return GEMM_OK;
+  GB300_CHECK(check_groups(p.offsets, nullptr));
+  if (cdiv(p.N, 64) * p.groups > INT32_MAX / 8 || !items_ok(p.M, p.groups, p.K) ||
+      p.groups * cdiv(p.K, 128) * cdiv(p.N, 64) > INT32_MAX / 2)
+    return GEMM_ERR_INVALID_ARG;
+  if (p.M > 0) {
+    GB300_CHECK(check_operand(p.dd, p.lddd, p.N, p.M, p.type));
+    if (p.activation != GEMM_ACT_NONE) {
+      GB300_CHECK(check_operand(p.z, p.ldz, p.N, p.M, p.type));
+      // the products read dz; without them it may be left out
+      if (!p.dz && (p.da || p.db)) return GEMM_ERR_INVALID_ARG;
+    }
+    if (p.dz) {
+      GB300_CHECK(check_operand(p.dz, p.lddz, p.N, p.M, p.type));
+      if ((p.dz == p.dd && p.lddz != p.lddd) || (p.dz == p.z && p.lddz != p.ldz))
+        return GEMM_ERR_INVALID_ARG;
+    }
+  }
+  if (p.dbias && !aligned_to(p.dbias, dtype_bytes(p.dbias_type))) return GEMM_ERR_MISALIGNED;
+  if (p.K == 0) return GEMM_OK;
+  int64_t lddz = 0;
+  const void* dz = dz_of(p, lddz);
+  if (p.da && p.M > 0) {
+    GB300_CHECK(check_operand(p.da, p.ldda, p.K, p.M, p.da_type));
+    GB300_CHECK(check_stack(p.b, p.ldb, p.K, p.N, p.groups, p.strideb, p.type));
+    if (p.da == p.dd || p.da == dz || p.da == p.z || p.da == p.a || p.da == p.b || p.da == p.db)
+      return GEMM_ERR_INVALID_ARG;
+  }
+  if (p.db) {
+    GB300_CHECK(check_stack(p.db, p.lddb, p.K, p.N, p.groups, p.stridedb, p.db_type));
+    if (!apart(p.stridedb, p.lddb, p.N, p.K, p.groups)) return GEMM_ERR_INVALID_ARG;
+    if (p.M > 0) GB300_CHECK(check_operand(p.a, p.lda, p.K, p.M, p.type));
+    if (p.db == p.dd || (dz && p.db == dz) || (p.z && p.db == p.z) || (p.a && p.db == p.a) ||
+        (p.b && p.db == p.b))
+      return GEMM_ERR_INVALID_ARG;
+  }
+  return GEMM_OK;
+}
+
+gemm_status_t check_adapters(const gemm_adapters_t& p) {
+  if (!is_extent(p.M) || !is_extent(p.N) || !is_extent(p.K) || !is_extent(p.rank) ||
+      !is_count(p.requests) || !is_count(p.adapters))
+    return GEMM_ERR_INVALID_ARG;
+  if ((p.type != GEMM_F16 && p.type != GEMM_BF16) || !is_epi_type(p.d_type) ||
+      (p.r && !is_epi_type(p.r_type)))
+    return GEMM_ERR_UNSUPPORTED_DTYPE;
+  if (p.M == 0 || p.N == 0 || p.requests == 0) return GEMM_OK;
+  if (!p.index) return GEMM_ERR_INVALID_ARG;
+  GB300_CHECK(check_groups(p.offsets, p.index));
+  if (!items_ok(p.M, p.requests, p.N) || !items_ok(p.M, p.requests, p.rank))
+    return GEMM_ERR_INVALID_ARG;
+  GB300_CHECK(check_operand(p.d, p.ldd, p.N, p.M, p.d_type));
+  if (p.r) GB300_CHECK(check_operand(p.r, p.ldr, p.N, p.M, p.r_type));
+  if (p.rank > 0 && p.adapters > 0) {
+    GB300_CHECK(check_operand(p.u, p.ldu, p.rank, p.M, p.type));
+    if (p.K > 0) {
+      GB300_CHECK(check_operand(p.x, p.ldx, p.K, p.M, p.type));
+      GB300_CHECK(check_stack(p.A, p.lda, p.K, p.rank, p.adapters, p.strideA, p.type));
+    }
+    GB300_CHECK(check_stack(p.B, p.ldb, p.rank, p.N, p.adapters, p.strideB, p.type));
+    if (p.u == p.x || p.u == p.A || p.u == p.B || p.u == p.r || p.u == p.d || p.d == p.x ||
+        p.d == p.A || p.d == p.B)
+      return GEMM_ERR_INVALID_ARG;
+  }
+  if (!aligned_to(p.scale, 4)) return GEMM_ERR_MISALIGNED;
+  if (p.r == p.d && (p.r_type != p.d_type || p.ldr != p.ldd)) return GEMM_ERR_INVALID_ARG;
+  return GEMM_OK;
+}
+
+}  // namespace
+
+GEMM_API gemm_status_t gemm_grouped_linear_check(const gemm_grouped_linear_t* p) {
+  return p ? check_grouped(*p) : GEMM_ERR_INVALID_ARG;
+}
+
+GEMM_API gemm_status_t gemm_grouped_linear(gemm_handle_t h, const gemm_grouped_linear_t* p,
+                                           struct CUstream_st* stream) {
+  NvtxRange range("gemm_grouped_linear");
+  if (!h || !p) return GEMM_ERR_INVALID_ARG;
+  GB300_CHECK(check_grouped(*p));
+  if (!on_device(h)) return GEMM_ERR_INVALID_ARG;
+  if (p->M == 0 || p->N == 0 || p->groups == 0) return GEMM_OK;
+  const Product q = product_of(*p);
+  std::lock_guard<std::mutex> guard(h->mu);
+  GroupedPlan plan;
+  GB300_CHECK(plan_grouped(h, q, plan));
+  return run_grouped(h, q, plan, stream);
+}
+
+GEMM_API gemm_status_t gemm_grouped_linear_bwd_check(const gemm_grouped_linear_bwd_t* p) {
+  return p ? check_grouped_bwd(*p) : GEMM_ERR_INVALID_ARG;
+}
+
+GEMM_API gemm_status_t gemm_grouped_linear_bwd(gemm_handle_t h, const gemm_grouped_linear_bwd_t* pp,
+                                               struct CUstream_st* stream) {
+  NvtxRange range("gemm_grouped_linear_bwd");
+  if (!h || !pp) return GEMM_ERR_INVALID_ARG;
+  const gemm_grouped_linear_bwd_t& p = *pp;
+  GB300_CHECK(check_grouped_bwd(p));
+  if (!on_device(h)) return GEMM_ERR_INVALID_ARG;
+  if (p.N == 0 || p.groups == 0) return GEMM_OK;
+  int64_t lddz = 0;
+  const void* dz = dz_of(p, lddz);
+  const bool da = p.da && p.M > 0 && p.K > 0, db = p.db && p.K > 0;
+  const Product q_da = product_da(p, dz, lddz), q_db = product_db(p, dz, lddz);
+  // both planned before anything is enqueued: a refused configuration changes no tensor
+  GroupedPlan plan_da, plan_db;
+  {
+    std::lock_guard<std::mutex> guard(h->mu);
+    if (da) GB300_CHECK(plan_grouped(h, q_da, plan_da));
+    if (db) GB300_CHECK(plan_grouped(h, q_db, plan_db));
+  }
+  if ((p.dz && p.M > 0) || p.dbias) {
+    GroupedActGrad g{};
+    g.M = p.M; g.N = p.N; g.groups = p.groups;
+    g.type = p.type; g.dbias_type = p.dbias_type;
+    g.activation = p.activation;
+    g.offsets = p.offsets;
+    g.dd = p.dd; g.lddd = p.lddd;
+    g.z = p.z; g.ldz = p.ldz;
+    g.dz = p.dz; g.lddz = p.lddz;
+    g.dbias = p.dbias;
+    GB300_CHECK(grouped_act_grad(h, g, stream));
+  }
+  std::lock_guard<std::mutex> guard(h->mu);
+  if (da) GB300_CHECK(run_grouped(h, q_da, plan_da, stream));
+  if (db) GB300_CHECK(run_grouped(h, q_db, plan_db, stream));
+  return GEMM_OK;
+}
+
+GEMM_API gemm_status_t gemm_adapters_check(const gemm_adapters_t* p) {
+  return p ? check_adapters(*p) : GEMM_ERR_INVALID_ARG;
+}
+
+GEMM_API gemm_status_t gemm_adapters(gemm_handle_t h, const gemm_adapters_t* pp,
+                                     struct CUstream_st* stream) {
+  NvtxRange range("gemm_adapters");
+  if (!h || !pp) return GEMM_ERR_INVALID_ARG;
+  const gemm_adapters_t& p = *pp;
+  GB300_CHECK(check_adapters(p));
+  if (!on_device(h)) return GEMM_ERR_INVALID_ARG;
+  if (p.M == 0 || p.N == 0 || p.requests == 0) return GEMM_OK;
+  const bool any = p.rank > 0 && p.adapters > 0;
+  Product down, up;
+  down.rows = p.M; down.feats = p.rank; down.k = p.K; down.groups = p.requests;
+  down.sets = p.adapters;
+  down.f_type = down.t_type = p.type;
+  down.f = p.A; down.ldf = p.lda; down.stride_f = p.strideA;
+  down.t = p.x; down.ldt = p.ldx;
+  down.k_params.offsets = p.offsets; down.k_params.index = p.index;
+  down.k_params.alpha = 1.f;
+  down.k_params.d = p.u; down.k_params.ldd = p.ldu; down.k_params.d_dt = p.type;
+  down.k_params.skip_none = 1;             // (their u is not read)
+  up.rows = p.M; up.feats = p.N; up.k = any ? p.rank : 0; up.groups = p.requests;
+  up.sets = p.adapters;
+  up.f_type = up.t_type = p.type;
+  up.f = p.B; up.ldf = p.ldb; up.stride_f = p.strideB;
+  up.t = p.u; up.ldt = p.ldu;
+  up.k_params.offsets = p.offsets; up.k_params.index = p.index;
+  up.k_params.alpha = 1.f;
+  up.k_params.set_scale = p.scale;
+  up.k_params.r = p.r; up.k_params.ldr = p.ldr; up.k_params.r_dt = p.r_type;
+  up.k_params.d = p.d; up.k_params.ldd = p.ldd; up.k_params.d_dt = p.d_type;
+  up.k_params.skip_none = p.r == p.d;
+  std::lock_guard<std::mutex> guard(h->mu);
+  GroupedPlan plan_down, plan_up;
+  if (any) GB300_CHECK(plan_grouped(h, down, plan_down));
+  GB300_CHECK(plan_grouped(h, up, plan_up));
+  if (any) GB300_CHECK(run_grouped(h, down, plan_down, stream));
+  return run_grouped(h, up, plan_up, stream);
+}

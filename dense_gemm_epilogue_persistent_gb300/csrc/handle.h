@@ -131,6 +131,7 @@ struct gemm_handle {
   bool forced = false;
   gemm_config_t forced_cfg{};
   gemm_config_t last{};
+  bool counted = true;         // the latest launch is of a kernel with ring counters
   uint64_t timeout_ns = gb300host::kDefaultTimeoutNs;
   gb300host::VariantState variants[3][2][2][2][2][2][2];   // [ab 16/8/32][cta_group][k atoms][mc][nc][epw][sk]
   gb300host::VariantState linear_variants[3][2][2][2];   // [ab][cta_group][k atoms][epw]
@@ -143,8 +144,9 @@ struct gemm_handle {
   int linear_next = 0;
   gb300host::PairPlan pair_plans[gb300host::kPairPlans];
   int pair_next = 0;
+  gb300host::VariantState grouped_variants[3][2][2];     // [ab][cta_group][weights]
   int split_clusters[9] = {0, 0, 0, 0, 0, 0, 0, 0, 0};   // resident, by cluster size (0: not asked)
-  int act_clusters[2][3][9] = {};   // activation gradient's, by type, block size and cluster
+  int act_clusters[2][2][3][9] = {};   // activation gradient's, by form, type, block size and cluster
   std::mutex mu;
   void* ws = nullptr;          // gemm_run_host's device copies of its host buffers
   size_t ws_bytes = 0;
@@ -206,6 +208,8 @@ gemm_status_t plan_valid(const gemm_problem_t& p, int sm_count, int smem_optin,
                          const EpilogueExtra& extra, double* cost = nullptr);
 bool encode_operand(EncodeTiledFn enc, CUtensorMap* map, const void* ptr, int dt, int64_t rows,
                     int64_t K, int64_t L, int64_t ld, bool mn_major, int box_rows, int tile_k);
+bool encode_stack(EncodeTiledFn enc, CUtensorMap* map, const void* ptr, int dt, int64_t inner,
+                  int64_t rows, int64_t sets, int64_t ld, int64_t stride, int box_rows);
 bool encode_epi(EncodeTiledFn enc, CUtensorMap* map, const void* ptr, int dt, int64_t M,
                 int64_t N, int64_t L, bool m_major, int64_t ld);
 uint32_t make_idesc(int a_type, int b_type_, bool acc_f16, int cg, int bn, bool a_mn, bool b_mn);

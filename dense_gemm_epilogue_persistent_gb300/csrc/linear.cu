@@ -26,11 +26,16 @@ struct ActGradParams {
   int M, N;
   int act, dbias_dt;
   int row_split;                    // blocks of a cluster, sharing the rows
+  // Groups of rows (else null): group g's are those between offsets[g * span] and
+  // offsets[(g + 1) * span], clamped to 0..M, and it has its own dbias.
+  const int* offsets;
+  int span;
 };
 
 // dz = dd act'(z) and dbias = its column sums (of the values before dz is
 // rounded), 6 bytes and about 25 instructions an element.  A block owns 64
-// columns (8 lanes of one vector each) and 1/R of the rows, R the cluster size:
+// columns (8 lanes of one vector each) and 1/R of the rows (GROUPED: of one group's, a
+// cluster for each strip and group), R the cluster size:
 // thread group g of G = THREADS / 8 walks rows first + g, + G, ..., each thread
 // copying its own pieces of the next kActDepth rows into its own slots of shared
 // memory (16 bytes and the row's end as they lie in memory; before the launch shapes
@@ -42,7 +47,7 @@ struct ActGradParams {
 // 4096: 65.5, 67.4, 65.1; 8192 x 700: 13.4, 12.9, 13.4)
 constexpr int kActDepth = 3;
 
-template <int DT, int THREADS>
+template <int DT, int THREADS, bool GROUPED = false>
 __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
 act_grad_kernel(const __grid_constant__ ActGradParams p) {
   constexpr int G = THREADS / 8;
@@ -52,15 +57,25 @@ act_grad_kernel(const __grid_constant__ ActGradParams p) {
   constexpr int es = elem_bytes(DT);
   grid_launch_dependents();
   const int lane = threadIdx.x & 7, group = threadIdx.x >> 3;
-  const int R = p.row_split, rank = blockIdx.x % R, strip = blockIdx.x / R;
+  const int R = p.row_split, rank = blockIdx.x % R;
+  const int strips = (p.N + 63) / 64;
+  const int strip = GROUPED ? (int)(blockIdx.x / R) % strips : blockIdx.x / R;
+  const int grp = GROUPED ? (int)(blockIdx.x / R) / strips : 0;
   const int c = strip * 64 + lane * kVec;
   const int share = (p.M + R - 1) / R;
-  const long long first = (long long)rank * share;
-  const long long last = min((long long)p.M, first + share);
+  long long first = (long long)rank * share;
+  long long last = min((long long)p.M, first + share);
   float acc[kVec];
 #pragma unroll
   for (int i = 0; i < kVec; ++i) acc[i] = 0.f;
   grid_dependency_wait();
+  if constexpr (GROUPED) {
+    const int lo = min(max(__ldg(p.offsets + (long long)grp * p.span), 0), p.M);
+    const int hi = min(max(__ldg(p.offsets + (long long)(grp + 1) * p.span), lo), p.M);
+    const int part = (hi - lo + R - 1) / R;
+    first = min((long long)hi, lo + (long long)rank * part);
+    last = min((long long)hi, first + part);
+  }
   if (c < p.N) {
     const uint8_t* const dd = static_cast<const uint8_t*>(p.dd);
     const uint8_t* const zz = static_cast<const uint8_t*>(p.z);
@@ -120,7 +135,7 @@ act_grad_kernel(const __grid_constant__ ActGradParams p) {
     float s = block_part[threadIdx.x];
     for (int r = 1; r < R; ++r)
       s += load_cluster_f32(map_to_rank(smem_u32(&block_part[threadIdx.x]), (uint32_t)r));
-    store_elem(p.dbias, col, p.dbias_dt, s);
+    store_elem(p.dbias, (long long)grp * p.N + col, p.dbias_dt, s);
   }
   if (R > 1) cluster_sync_all();         // the first block has read the others' sums
 }
@@ -130,23 +145,6 @@ act_grad_kernel(const __grid_constant__ ActGradParams p) {
 namespace {
 
 using namespace gb300host;
-
-bool is_activation(int a) { return a >= GEMM_ACT_NONE && a <= GEMM_ACT_SILU; }
-
-// Sizes the kernels index with 32 bits: what they add to an index on the way to its
-// bound (the rest of the last tile, whose width need not divide 2^31; a vector's
-// end; a cluster's shares of the rows) stays below 2^31.
-bool is_extent(int64_t v) { return v >= 0 && v <= INT32_MAX - 8192; }
-// Tensor-map strides below 2^40 bytes.
-bool map_ok(int64_t ld, int64_t rows, int dt) {
-  return (double)ld * dtype_bytes(dt) * (double)rows < 1099511627776.0;
-}
-
-// One A or B operand: `inner` contiguous elements a row, `rows` rows.
-gemm_status_t check_operand(const void* p, int64_t ld, int64_t inner, int64_t rows, int dt) {
-  GB300_CHECK(check_matrix(p, ld, inner, dt));
-  return map_ok(ld, rows, dt) ? GEMM_OK : GEMM_ERR_INVALID_ARG;
-}
 
 gemm_status_t check_linear(const gemm_linear_t& p) {
   if (!is_extent(p.M) || !is_extent(p.N) || !is_extent(p.K)) return GEMM_ERR_INVALID_ARG;
@@ -605,6 +603,7 @@ gemm_status_t find_plan(gemm_handle* h, const gemm_linear_t& p, LinearPlan& out)
 gemm_status_t run_planned(gemm_handle* h, const gemm_linear_t& p, const LinearPlan& plan,
                           Place place, struct CUstream_st* stream) {
   h->last = plan.cfg;
+  h->counted = true;
   return plan.split ? run_split(h, p, plan, place, stream)
                     : run_persistent(h, p, plan, place, stream);
 }
@@ -820,6 +819,7 @@ gemm_status_t run_products(gemm_handle* h, const gemm_linear_t* da, const gemm_l
   std::lock_guard<std::mutex> guard(h->mu);
   if (plans.pair.one) {
     h->last = plans.pair.cfg;
+    h->counted = true;
     return run_pair(h, *da, *db, plans.pair, stream);
   }
   const bool two = da && db;
@@ -858,12 +858,16 @@ int act_clusters(int& n, const gemm_handle* h, Kern kern, int threads, size_t sm
 // 128 blocks of 1024, 37.4 with 512 of 256 in clusters of 4; 8192 x 1024 13.9 with 16
 // clusters of 6 blocks of 1024, 22.2 with clusters of 8, of which the device holds 15;
 // 3000 x 5000 17.8 with clusters of 7 of 256, 19.4 with 8.
-template <int DT>
-gemm_status_t launch_act_grad(gemm_handle* h, gb300::ActGradParams& k, struct CUstream_st* stream) {
+// With groups the same estimate for their mean number of rows.
+template <int DT, bool GROUPED = false>
+gemm_status_t launch_act_grad(gemm_handle* h, gb300::ActGradParams& k, struct CUstream_st* stream,
+                              int64_t groups = 1) {
   typedef void (*Kern)(gb300::ActGradParams);
-  const Kern kerns[3] = {gb300::act_grad_kernel<DT, 1024>, gb300::act_grad_kernel<DT, 512>,
-                         gb300::act_grad_kernel<DT, 256>};
-  const int64_t strips = cdiv(k.N, 64);
+  const Kern kerns[3] = {gb300::act_grad_kernel<DT, 1024, GROUPED>,
+                         gb300::act_grad_kernel<DT, 512, GROUPED>,
+                         gb300::act_grad_kernel<DT, 256, GROUPED>};
+  const int64_t strips = cdiv(k.N, 64) * groups;
+  const int64_t rows = cdiv(k.M, groups);
   Kern kern = nullptr;
   int threads = 0;
   double best = 0.0;
@@ -874,14 +878,14 @@ gemm_status_t launch_act_grad(gemm_handle* h, gb300::ActGradParams& k, struct CU
       const int t = 1024 >> size;
       GB300_CHECK(raise_smem(h, reinterpret_cast<const void*>(kerns[size])));
       for (int split = 1; split <= 8; ++split) {
-        const int held = act_clusters(h->act_clusters[DT == gb300::DT_F16][size][split], h, kerns[size],
+        const int held = act_clusters(h->act_clusters[GROUPED][DT == gb300::DT_F16][size][split], h, kerns[size],
                                       t, smem(t), split);
         const double full = (double)strips / held;
         const double waves = full <= 1.0 ? 1.0 : full + 0.156 * (std::ceil(full) - full);
-        const double rows = (double)cdiv(k.M, (int64_t)split * (t / 8));
+        const double walked = (double)cdiv(rows, (int64_t)split * (t / 8));
         const double load = std::min(1.0, (double)(std::min<int64_t>(strips, held) * split * t) /
                                               (1024.0 * h->sm_count));
-        const double us = waves * (rows * (0.359 + 1.004 * load) + 1.166) + 0.078 * split +
+        const double us = waves * (walked * (0.359 + 1.004 * load) + 1.166) + 0.078 * split +
                           0.133 * t / 1024.0;
         if (!kern || us < best) {
           best = us;
@@ -894,6 +898,28 @@ gemm_status_t launch_act_grad(gemm_handle* h, gb300::ActGradParams& k, struct CU
   }
   return launch(kern, k, strips * k.row_split, threads, smem(threads), stream, k.row_split);
 }
+
+}  // namespace
+
+gemm_status_t gb300host::grouped_act_grad(gemm_handle* h, const GroupedActGrad& g,
+                                          struct CUstream_st* stream) {
+  gb300::ActGradParams k{};
+  k.dd = g.dd; k.lddd = g.lddd;
+  k.z = g.z; k.ldz = g.ldz;
+  k.dz = g.dz; k.lddz = g.lddz;
+  k.dbias = g.dbias; k.dbias_dt = device_dt(g.dbias_type);
+  k.M = (int)g.M; k.N = (int)g.N;
+  k.act = g.activation;
+  k.offsets = g.offsets;
+  // (without a bias's gradient all groups' rows are one run of rows)
+  const int64_t groups = g.dbias ? g.groups : 1;
+  k.span = g.dbias ? 1 : (int)g.groups;
+  if (cdiv(g.N, 64) * groups > INT32_MAX / 8) return GEMM_ERR_INVALID_ARG;
+  return g.type == GEMM_F16 ? launch_act_grad<gb300::DT_F16, true>(h, k, stream, groups)
+                            : launch_act_grad<gb300::DT_BF16, true>(h, k, stream, groups);
+}
+
+namespace {
 
 gemm_linear_t product_da(const gemm_linear_bwd_t& p, const void* dz, int64_t lddz) {
   gemm_linear_t q{};

@@ -49,6 +49,13 @@ __device__ __forceinline__ float load_cluster_f32(uint32_t cluster_addr) {
   return v;
 }
 
+// A word there.
+__device__ __forceinline__ uint32_t load_cluster_u32(uint32_t cluster_addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(cluster_addr) : "memory");
+  return v;
+}
+
 // Four words into the shared memory of a CTA of the cluster (16-byte aligned).
 __device__ __forceinline__ void store_cluster_v4(uint32_t cluster_addr, uint32_t a, uint32_t b,
                                                  uint32_t c, uint32_t d) {
@@ -263,6 +270,11 @@ __device__ __forceinline__ void bulk_wait_group_all() {
 // async-proxy (TMA) reads of them.
 __device__ __forceinline__ void fence_proxy_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// The same for writes that the async proxy of the pair's other CTA may read.
+__device__ __forceinline__ void fence_proxy_async_all() {
+  asm volatile("fence.proxy.async;" ::: "memory");
 }
 
 // ------------------------------------------------------------------ global flags

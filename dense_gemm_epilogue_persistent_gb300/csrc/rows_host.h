@@ -38,6 +38,23 @@ inline gemm_status_t check_matrix(const void* p, int64_t ld, int64_t cols, int d
     if (check_status != GEMM_OK) return check_status;         \
   } while (0)
 
+inline bool is_activation(int a) { return a >= GEMM_ACT_NONE && a <= GEMM_ACT_SILU; }
+
+// Sizes the kernels index with 32 bits: what they add to an index on the way to its
+// bound (the rest of the last tile, whose width need not divide 2^31; a vector's
+// end; a cluster's shares of the rows) stays below 2^31.
+inline bool is_extent(int64_t v) { return v >= 0 && v <= INT32_MAX - 8192; }
+// Tensor-map strides below 2^40 bytes.
+inline bool map_ok(int64_t ld, int64_t rows, int dt) {
+  return (double)ld * dtype_bytes(dt) * (double)rows < 1099511627776.0;
+}
+
+// One A or B operand: `inner` contiguous elements a row, `rows` rows.
+inline gemm_status_t check_operand(const void* p, int64_t ld, int64_t inner, int64_t rows, int dt) {
+  GB300_CHECK(check_matrix(p, ld, inner, dt));
+  return map_ok(ld, rows, dt) ? GEMM_OK : GEMM_ERR_INVALID_ARG;
+}
+
 // Raises `kern`'s dynamic shared-memory limit, once per handle (h->mu held).
 inline gemm_status_t raise_smem(gemm_handle* h, const void* kern) {
   for (int i = 0; i < h->raised_count; ++i)
@@ -78,5 +95,19 @@ gemm_status_t launch(void (*kern)(P), const P& params, int64_t grid, int threads
   }
   return GEMM_OK;
 }
+
+// linear.cu: dz = dd act'(z) over the rows of groups, and each group's bias gradient
+// (either output may be null); the arguments have been checked.
+struct GroupedActGrad {
+  int64_t M, N, groups;
+  gemm_dtype_t type, dbias_type;
+  gemm_activation_t activation;
+  const int32_t* offsets;
+  const void* dd; int64_t lddd;
+  const void* z; int64_t ldz;
+  void* dz; int64_t lddz;
+  void* dbias;
+};
+gemm_status_t grouped_act_grad(gemm_handle* h, const GroupedActGrad& g, struct CUstream_st* stream);
 
 }  // namespace gb300host

@@ -554,6 +554,213 @@ gemm_status_t gemm_linear_bwd_check(const gemm_linear_bwd_t* p);
 gemm_status_t gemm_linear_bwd(gemm_handle_t h, const gemm_linear_bwd_t* p,
                               struct CUstream_st* stream);
 
+/* ====================================================================
+ * Layers whose weights change from row to row: tokens sorted by expert and
+ * back, the linear layer over groups of rows, low-rank adapters.  The rules
+ * of the operators above hold here too.  What says which rows are whose (expert
+ * numbers, places, offsets) lies in device memory and is never read by the host:
+ * one captured graph serves whatever a router decides.  Such numbers out of
+ * range never make a call read or write outside the tensors given: each
+ * operator says below what it makes of them. */
+
+/* Sorting by expert.  The T tokens' k choices, numbered i = t k + j, in order
+ * of (expert, i):
+ *     offsets(e) = number of choices of experts below e,  e = 0..E
+ *     slot(i)    = place of choice i;  source(slot(i)) = i
+ * A choice outside 0..E-1 has no place: its slot is -1, and source is written
+ * up to offsets(E) only.
+ *   index [T, k]: 4- or 8-byte signed integers (index_bytes), rows ldi apart, each
+ *   aligned to its size.  k at most 128, T k at most 2^31 - 8193, E at most 4096.
+ *   offsets [E + 1], slot [T k], source [T k] (optional): int32.
+ * T = 0: offsets are 0. */
+typedef struct {
+  int64_t T, k, E;
+  int index_bytes;
+  const void* index; int64_t ldi;
+  int32_t* offsets;
+  int32_t* slot;
+  int32_t* source;
+} gemm_route_t;
+
+gemm_status_t gemm_route_check(const gemm_route_t* p);
+gemm_status_t gemm_route(gemm_handle_t h, const gemm_route_t* p, struct CUstream_st* stream);
+
+/* Each token's row to the places of its choices:
+ *     y(slot(t k + j), c) = x(t, c),   y_scale(slot(t k + j)) = scale(t)
+ * A choice whose slot is outside 0..R-1 is left out; rows of y that no choice
+ * has stay as they were.  (Two choices of one slot: either's row.)
+ *   x [T, H], y [R, H] of one type (any but TF32); slot [T k]: int32; scale [T],
+ *   y_scale [R]: fp32, both or neither (the row scales of an 8-bit x).
+ * The gradient of x is gemm_combine's y of y's gradient, without weights. */
+typedef struct {
+  int64_t T, k, H, R;
+  gemm_dtype_t type;
+  const void* x; int64_t ldx;
+  const int32_t* slot;
+  const float* scale;
+  void* y; int64_t ldy;
+  float* y_scale;
+} gemm_dispatch_t;
+
+gemm_status_t gemm_dispatch_check(const gemm_dispatch_t* p);
+gemm_status_t gemm_dispatch(gemm_handle_t h, const gemm_dispatch_t* p, struct CUstream_st* stream);
+
+/* And back:
+ *     y(t, c) = r(t, c) + sum_j weight(t, j) ys(slot(t k + j), c)
+ * in fp32, in order of j, rounded once.  A choice whose slot is outside 0..R-1
+ * adds nothing, whatever its weight.
+ *   ys [R, H], r [T, H] (optional: 0), y [T, H]: F32, F16 or BF16 each.  weight
+ *   [T k]: fp32, optional (1).  y may be r (same type and leading dimension). */
+typedef struct {
+  int64_t T, k, H, R;
+  gemm_dtype_t type, r_type, y_type;
+  const void* ys; int64_t ldys;
+  const int32_t* slot;
+  const float* weight;
+  const void* r; int64_t ldr;
+  void* y; int64_t ldy;
+} gemm_combine_t;
+
+gemm_status_t gemm_combine_check(const gemm_combine_t* p);
+gemm_status_t gemm_combine(gemm_handle_t h, const gemm_combine_t* p, struct CUstream_st* stream);
+
+/* Its backward pass, from dy, the gradient of y (which is that of r too):
+ *     dys(slot(t k + j), c) = weight(t, j) dy(t, c)
+ *     dweight(t, j)         = sum_c dy(t, c) ys(slot(t k + j), c)
+ * A choice whose slot is outside 0..R-1 has dweight 0 and writes no row; rows
+ * of dys that no choice has stay as they were.
+ *   dy [T, H], ys [R, H], dys [R, H]: one type, F32, F16 or BF16.  weight [T k]:
+ *   fp32, optional (1).  dys, dweight [T k] fp32: each optional; ys is read
+ *   for dweight only.  dys may be ys (same leading dimension). */
+typedef struct {
+  int64_t T, k, H, R;
+  gemm_dtype_t type;
+  const void* dy; int64_t lddy;
+  const int32_t* slot;
+  const float* weight;
+  const void* ys; int64_t ldys;
+  void* dys; int64_t lddys;
+  float* dweight;
+} gemm_combine_bwd_t;
+
+gemm_status_t gemm_combine_bwd_check(const gemm_combine_bwd_t* p);
+gemm_status_t gemm_combine_bwd(gemm_handle_t h, const gemm_combine_bwd_t* p,
+                               struct CUstream_st* stream);
+
+/* The linear layer with weights of its own for each group of rows: for the rows
+ * offsets(g) <= m < offsets(g + 1) of group g, with e = index(g) (e = g without
+ * an index):
+ *     z(m,n) = alpha * row_scale(m) * col_scale(e,n) * sum_k A(m,k) B(e,n,k) + bias(e,n)
+ *     D(m,n) = act(z(m,n)) + R(m,n),        Z(m,n) = z(m,n)
+ * fp32 accumulation and epilogue; Z and D are each rounded once, D from the
+ * unrounded z.  A group whose index is outside 0..sets-1 has no weights: z = 0,
+ * D = R there.  Rows of no group (before offsets(0), behind offsets(groups), of
+ * groups of no or negative size) stay as they were in Z and D; offsets are clamped to
+ * 0..M.  (Groups that overlap: the rows that they share hold either's values.)
+ *   A [M, K]: K contiguous.  B: `sets` matrices [N, K], strideB elements
+ *   apart (a multiple of 16 bytes), each K-major or (8 and 16 bits) with N
+ *   contiguous (layoutB, ldb).  Types as for gemm_linear.  K = 0: the sum is 0.
+ *   offsets [groups + 1], index [groups] (optional): int32.  groups and sets at
+ *   most 4096; without an index sets >= groups.
+ *   row_scale [M], col_scale [sets, N]: fp32, optional (1).  bias [sets, N]: F32,
+ *   F16 or BF16, optional.  R, Z: optional.  R, Z and D: F32, F16 or BF16 each.
+ * D may be R (same type and leading dimension).  Of a configuration forced with
+ * gemm_set_config cta_group, tile_n (the widest tile, in tokens; a multiple of 64 in
+ * pairs), stages and inject_stall apply; multicast clusters, split_k and stream_k are
+ * refused.  A launch is under the watchdog of gemm_sync_status. */
+typedef struct {
+  int64_t M, N, K, groups, sets;
+  gemm_dtype_t a_type, b_type, bias_type, r_type, z_type, d_type;
+  gemm_layout_t layoutB;
+  gemm_activation_t activation;
+  float alpha;
+  const int32_t* offsets;
+  const int32_t* index;
+  const void* A; int64_t lda;
+  const void* B; int64_t ldb; int64_t strideB;
+  const float* row_scale;
+  const float* col_scale;
+  const void* bias;
+  const void* R; int64_t ldr;
+  void* Z; int64_t ldz;
+  void* D; int64_t ldd;
+} gemm_grouped_linear_t;
+
+gemm_status_t gemm_grouped_linear_check(const gemm_grouped_linear_t* p);
+gemm_status_t gemm_grouped_linear(gemm_handle_t h, const gemm_grouped_linear_t* p,
+                                  struct CUstream_st* stream);
+
+/* Its backward pass for 16-bit operands without scale vectors and index (group
+ * g has weights b(g)), dd the gradient of D:
+ *     dz = dd * act'(z)                   rounded to `type` where it is written
+ *     dbias(g,n) = sum_m dz(m,n)          over the group's rows, unrounded values
+ *     da = alpha * dz b(g)                of the rounded ones, as are
+ *     db(g) = alpha * dz^T a  (+ db(g))   over the group's rows; added to where
+ *                                         accumulate is non-zero
+ * The gradient of the residual is dd itself.  Rows of no group stay as they were in
+ * dz and da; an empty group's dbias and db are 0 (db unchanged where accumulated).
+ * What dd, z and a hold in rows of no group reaches nothing, infinities and NaN
+ * included.
+ *   dd, z, dz [M, N], a, da [M, K]; b, db: `groups` K-major matrices [N, K],
+ *   strideb and stridedb elements apart; dbias [groups, N].
+ *   type: F16 or BF16, the type of dd, z, a, b and dz.  da_type, db_type,
+ *   dbias_type: F32, F16 or BF16.
+ *   z: required unless activation is NONE.  da, db, dbias: each optional; a is
+ *   read for db only, b for da only.  dz: required for da or db with an activation;
+ *   without one it is optional (where given it receives dd).
+ * dz may be dd or z (same leading dimension). */
+typedef struct {
+  int64_t M, N, K, groups;
+  gemm_dtype_t type, da_type, db_type, dbias_type;
+  gemm_activation_t activation;
+  int accumulate;
+  float alpha;
+  const int32_t* offsets;
+  const void* dd; int64_t lddd;
+  const void* z; int64_t ldz;
+  const void* a; int64_t lda;
+  const void* b; int64_t ldb; int64_t strideb;
+  void* dz; int64_t lddz;
+  void* da; int64_t ldda;
+  void* db; int64_t lddb; int64_t stridedb;
+  void* dbias;
+} gemm_grouped_linear_bwd_t;
+
+gemm_status_t gemm_grouped_linear_bwd_check(const gemm_grouped_linear_bwd_t* p);
+gemm_status_t gemm_grouped_linear_bwd(gemm_handle_t h, const gemm_grouped_linear_bwd_t* p,
+                                      struct CUstream_st* stream);
+
+/* Low-rank adapters of many requests beside a shared layer: request s has the
+ * rows offsets(s) .. offsets(s + 1) - 1 and the adapter e = index(s):
+ *     u = x A(e)^T                          rounded to `type`
+ *     d = r + scale(e) * (u B(e)^T)
+ * A request whose index is outside 0..adapters-1 has none: d = r there.  Rows of
+ * no request stay as they were in d.
+ *   x [M, K]; A: `adapters` matrices [rank, K], B: as many [N, rank], strideA
+ *   and strideB elements apart (multiples of 16 bytes); u [M, rank]: a workspace that
+ *   the call overwrites (calls that may overlap need one each); all of one type,
+ *   F16 or BF16.  r [M, N] (optional: 0; typically the shared layer's output),
+ *   d [M, N]: F32, F16 or BF16 each.  scale [adapters]: fp32, optional (1).
+ *   offsets [requests + 1], index [requests]: int32.  requests and adapters at
+ *   most 4096.
+ * d may be r (same type and leading dimension). */
+typedef struct {
+  int64_t M, N, K, rank, requests, adapters;
+  gemm_dtype_t type, r_type, d_type;
+  const int32_t* offsets;
+  const int32_t* index;
+  const void* x; int64_t ldx;
+  const void* A; int64_t lda; int64_t strideA;
+  const void* B; int64_t ldb; int64_t strideB;
+  const float* scale;
+  void* u; int64_t ldu;
+  const void* r; int64_t ldr;
+  void* d; int64_t ldd;
+} gemm_adapters_t;
+
+gemm_status_t gemm_adapters_check(const gemm_adapters_t* p);
+gemm_status_t gemm_adapters(gemm_handle_t h, const gemm_adapters_t* p, struct CUstream_st* stream);
+
 #ifdef __cplusplus
 }
 #endif
