@@ -76,6 +76,9 @@ gemm_status_t plan_grouped(gemm_handle* h, const Product& p, GroupedPlan& out) {
   c.cluster_m = c.cluster_n = 1;
   c.epi_warps = 2;
   c.inject_stall = f.inject_stall;
+  c.group_m = f.group_m ? f.group_m : 8;
+  c.epi_wait_ns = f.epi_wait_ns;
+  c.l2_hints = f.l2_hints & 256 ? f.l2_hints & 255 : 6;
   // At most this many items: the device finds out how many there are.
   const int64_t tiles_f = cdiv(p.feats, c.tile_m);
   c.tiles = p.weights ? p.groups * tiles_f * cdiv(p.cols, c.tile_n)
@@ -121,6 +124,12 @@ gemm_status_t run_grouped(gemm_handle* h, const Product& p, const GroupedPlan& p
   k.tiles_f = (int)cdiv(p.feats, c.tile_m);
   k.tiles_c = p.weights ? (int)cdiv(p.cols, c.tile_n) : 1;
   k.stages = c.stages;
+  k.strip = std::min(c.group_m, gb300::kGroupedMaxStrip);
+  k.by_bn = gb300::fast_div(k.bn);
+  k.by_strip = gb300::fast_div(k.strip * k.tiles_f);
+  k.by_group = gb300::fast_div(k.tiles_f * k.tiles_c);
+  k.alternate = c.epi_wait_ns != 7;
+  k.l2_hints = (uint32_t)c.l2_hints;
   k.f_mn = p.f_mn;
   k.idesc = make_idesc(p.f_type, p.t_type, false, c.cta_group, 0, p.weights || p.f_mn, p.weights);
   k.status = h->d_status;

@@ -22,8 +22,9 @@
 // a warp of its own zeroes those rows of both operands in shared memory
 // before the MMA (a product with zeros in one operand only would keep another
 // group's infinities).  The two CTAs of a pair do so each for its own half: such a
-// stage's copies report to a barrier of the CTA, and the zeroing warps' arrivals
-// complete the stage.
+// stage's copies report to a barrier of the CTA, the other CTA's zeroing warp to the
+// leader's, which then completes the stage.  (A remote arrival for every stage instead, to
+// have the stages count both CTAs, cost a quarter: 8192^3 bf16 880 us, XXX so.)
 //
 // Block: warp 0 TMA producer, warp 1 tensor memory and MMA issue, warps 2-9
 // epilogue (two per lane quarter, taking 16-column chunks alternately), warp 10 (weights
@@ -37,6 +38,21 @@
 
 namespace gb300 {
 
+// n / d for 0 <= n < 2^31 by a multiplication: with 2^s >= d > 2^(s-1) and m = ceil(2^(31+s) / d),
+// floor(n m / 2^(31+s)) is exact, since m d - 2^(31+s) < d <= 2^s.
+struct FastDiv {
+  uint32_t mul, shift;
+  int d;
+};
+inline FastDiv fast_div(int d) {
+  uint32_t s = 0;
+  while ((1ull << s) < (unsigned long long)d) ++s;
+  return {(uint32_t)(((1ull << (31 + s)) + (unsigned long long)d - 1) / (unsigned long long)d), 31 + s, d};
+}
+__device__ __forceinline__ int fast_quot(int n, const FastDiv& f) {
+  return (int)(((unsigned long long)(uint32_t)n * f.mul) >> f.shift);
+}
+
 struct GroupedParams {
   int rows;                  // of the token matrix: groups are clamped to them
   int feats;                 // output features (MMA rows)
@@ -46,7 +62,11 @@ struct GroupedParams {
   int bn;                    // widest tile
   int unit;                  // columns of one box of the token operand
   int tiles_f, tiles_c;      // feature tiles; weights form: column tiles
+  FastDiv by_bn, by_strip, by_group;   // by bn, a whole strip's items, a group's (weights form)
   int stages;
+  int alternate;             // odd waves of items walk the k-blocks from the last one down
+  int strip;                 // token (or column) tiles walked together
+  uint32_t l2_hints;         // L2 eviction priority (0 normal, 1 last, 2 first): bits 0-1 features, 2-3 tokens
   int f_mn;                  // rows form: weights with contiguous features
   int has_operands;          // the tensor maps are encoded
   int skip_none;             // groups without weights are left out: their d is r already
@@ -72,42 +92,136 @@ struct GroupedParams {
 
 constexpr int kGroupedKA = 2;                  // 128-byte K atoms a ring stage
 constexpr int kGroupedEpiWarps = 8;
-constexpr int kGroupedChunk = 16;              // columns of an epilogue chunk
-constexpr int kGroupedStrip = 8;               // token tiles walked together for L2
+constexpr int kGroupedChunk = 32;              // columns of an epilogue chunk
+constexpr int kGroupedMaxStrip = 16;
 constexpr int kGroupedMaxGroups = 4096;        // what the tables in shared memory hold
 constexpr int kGroupedMaxStages = 8;
 
 constexpr int grouped_threads(bool weights) { return 64 + 32 * kGroupedEpiWarps + (weights ? 32 : 0); }
 
-// Bytes of a ring stage and of what follows the ring: barriers (full, empty, tail; two
+// Bytes of a ring stage and of what follows the ring: barriers (full, empty, tail, peer; two
 // accumulators' full and empty; one that nothing arrives at), tensor-memory
-// address and abort flag, warps' sums, the two tables.
+// address and abort flag, warps' sums, reciprocals, the two tables.
 constexpr int grouped_stage_bytes(int cta_group, int bn) {
   return kGroupedKA * (128 + bn / cta_group) * 128;
 }
-constexpr int grouped_bar_bytes() { return 8 * (3 * kGroupedMaxStages + 5) + 16 + 64; }
+constexpr int grouped_bar_bytes() { return 8 * (4 * kGroupedMaxStages + 5) + 16 + 64 + 80; }
 constexpr int grouped_smem(int cta_group, int bn, int stages, int groups) {
   return 1024 + stages * grouped_stage_bytes(cta_group, bn) + grouped_bar_bytes() + 8 * (groups + 1);
 }
 
-__device__ __forceinline__ uint32_t grouped_elem(const uint8_t* p, int dt) {
-  return dt == DT_F32 ? *reinterpret_cast<const uint32_t*>(p)
-                      : (uint32_t)*reinterpret_cast<const uint16_t*>(p);
+// Where a lane's values of the columns (tokens) of a matrix lie.  With 16 bits two neighbouring
+// lanes exchange halves of two columns x, x + 1, so that each moves two neighbouring
+// features, 4 bytes, of one of them: even lanes of x, odd lanes of x + 1.  (A quarter fewer
+// instructions than 2 bytes of each.)  That is the way of whole chunks (`pairs`); where columns or
+// the last of an odd number of features are missing every lane moves its own elements.
+struct EpiMatrix {
+  uint8_t* own;              // this lane's element of column 0
+  uint8_t* pair;             // the two elements that it moves of columns 0, 1
+  long long step;            // bytes from one column to the next
+  int dt;
+};
+__device__ __forceinline__ uint32_t swap_halves(uint32_t w, uint32_t odd) {
+  return __byte_perm(w, __shfl_xor_sync(0xFFFFFFFFu, w, 1), odd ? 0x3276 : 0x5410);
 }
 
-// 16 values, `count` of them, `step` bytes apart.
-__device__ __forceinline__ void grouped_store(uint8_t* p, long long step, int dt, int count,
-                                              const float (&v)[kGroupedChunk]) {
-  if (dt == DT_F32) {
+// 16 columns from c on, of which `left` are the item's, for lanes that have a feature (mine).
+template <int DT>
+__device__ __forceinline__ void epi_store_as(const EpiMatrix& m, int c, int left, bool pairs,
+                                             bool mine, uint32_t odd, const float (&v)[16]) {
+  if constexpr (DT == DT_F32) {
+    uint8_t* p = m.own + c * m.step;
+    if (left >= 16) {
+      if (mine) {
 #pragma unroll
-    for (int i = 0; i < kGroupedChunk; ++i)
-      if (i < count) *reinterpret_cast<float*>(p + i * step) = v[i];
+        for (int x = 0; x < 16; ++x, p += m.step) *reinterpret_cast<float*>(p) = v[x];
+      }
+    } else {
+#pragma unroll
+      for (int x = 0; x < 16; ++x, p += m.step)
+        if (mine && x < left) *reinterpret_cast<float*>(p) = v[x];
+    }
+  } else {
+    uint32_t w[8];
+#pragma unroll
+    for (int x = 0; x < 8; ++x)
+      w[x] = DT == DT_F16 ? pack_f16x2(v[2 * x], v[2 * x + 1]) : pack_bf16x2(v[2 * x], v[2 * x + 1]);
+    if (pairs && left >= 16) {
+#pragma unroll
+      for (int x = 0; x < 8; ++x) w[x] = swap_halves(w[x], odd);
+      if (mine) {
+        uint8_t* p = m.pair + c * m.step;
+#pragma unroll
+        for (int x = 0; x < 8; ++x, p += 2 * m.step) *reinterpret_cast<uint32_t*>(p) = w[x];
+      }
+    } else {
+      uint8_t* p = m.own + c * m.step;
+#pragma unroll
+      for (int x = 0; x < 16; ++x, p += m.step)
+        if (mine && x < left) *reinterpret_cast<uint16_t*>(p) = (uint16_t)(w[x / 2] >> (16 * (x & 1)));
+    }
+  }
+}
+__device__ __forceinline__ void epi_store(const EpiMatrix& m, int c, int left, bool pairs, bool mine,
+                                          uint32_t odd, const float (&v)[16]) {
+  if (m.dt == DT_BF16) epi_store_as<DT_BF16>(m, c, left, pairs, mine, odd, v);
+  else if (m.dt == DT_F16) epi_store_as<DT_F16>(m, c, left, pairs, mine, odd, v);
+  else epi_store_as<DT_F32>(m, c, left, pairs, mine, odd, v);
+}
+
+// The words of such 16 columns, as they lie in memory: 16 of 32 bits, or 8 of two columns of 16.
+template <int FROM>
+__device__ __forceinline__ void epi_load(const EpiMatrix& m, int c, int left, bool pairs, bool mine,
+                                         uint32_t (&r)[32]) {
+  if (m.dt == DT_F32) {
+    const uint8_t* p = m.own + c * m.step;
+#pragma unroll
+    for (int x = 0; x < 16; ++x, p += m.step)
+      r[(FROM + x) & 31] = mine && x < left ? *reinterpret_cast<const uint32_t*>(p) : 0u;
+  } else if (pairs && left >= 16) {
+    const uint8_t* p = m.pair + c * m.step;
+#pragma unroll
+    for (int x = 0; x < 8; ++x, p += 2 * m.step)
+      r[(FROM + x) & 31] = mine ? *reinterpret_cast<const uint32_t*>(p) : 0u;
+  } else {
+    const uint8_t* p = m.own + c * m.step;
+#pragma unroll
+    for (int x = 0; x < 8; ++x, p += 2 * m.step) {
+      const uint32_t lo = mine && 2 * x < left ? *reinterpret_cast<const uint16_t*>(p) : 0u;
+      const uint32_t hi =
+          mine && 2 * x + 1 < left ? *reinterpret_cast<const uint16_t*>(p + m.step) : 0u;
+      r[(FROM + x) & 31] = lo | hi << 16;
+    }
+  }
+}
+template <int FROM>
+__device__ __forceinline__ void epi_add(const EpiMatrix& m, int left, bool pairs, uint32_t odd,
+                                        const uint32_t (&r)[32], float (&v)[16]) {
+  if (m.dt == DT_F32) {
+#pragma unroll
+    for (int x = 0; x < 16; ++x) v[x] += __uint_as_float(r[(FROM + x) & 31]);
+    return;
+  }
+  uint32_t w[8];
+#pragma unroll
+  for (int x = 0; x < 8; ++x) w[x] = r[(FROM + x) & 31];
+  if (pairs && left >= 16) {
+#pragma unroll
+    for (int x = 0; x < 8; ++x) w[x] = swap_halves(w[x], odd);
+  }
+  if (m.dt == DT_F16) {
+#pragma unroll
+    for (int x = 0; x < 8; ++x) {
+      const float2 f = unpack_f16x2(w[x]);
+      v[2 * x] += f.x;
+      v[2 * x + 1] += f.y;
+    }
   } else {
 #pragma unroll
-    for (int i = 0; i < kGroupedChunk; i += 2) {
-      const uint32_t w = dt == DT_F16 ? pack_f16x2(v[i], v[i + 1]) : pack_bf16x2(v[i], v[i + 1]);
-      if (i < count) *reinterpret_cast<uint16_t*>(p + i * step) = (uint16_t)w;
-      if (i + 1 < count) *reinterpret_cast<uint16_t*>(p + (i + 1) * step) = (uint16_t)(w >> 16);
+    for (int x = 0; x < 8; ++x) {
+      const float2 f = unpack_bf16x2(w[x]);
+      v[2 * x] += f.x;
+      v[2 * x + 1] += f.y;
     }
   }
 }
@@ -144,19 +258,22 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmF, const __grid_constant__ 
   const uint32_t f_ring = base, t_ring = f_ring + S * F_STAGE;
   const uint32_t bars = t_ring + S * t_stage;
   const uint32_t full0 = bars, empty0 = full0 + 8u * S, tail0 = empty0 + 8u * S;
-  const uint32_t tfull0 = bars + 24u * kGroupedMaxStages, tempty0 = tfull0 + 16u;
+  const uint32_t peer0 = tail0 + 8u * S;         // the other CTA's half of a last block is zeroed
+  const uint32_t tfull0 = bars + 32u * kGroupedMaxStages, tempty0 = tfull0 + 16u;
   const uint32_t never_bar = tempty0 + 16u, holder = never_bar + 8u;
   volatile uint32_t* const holder_ptr = reinterpret_cast<volatile uint32_t*>(gbase + (holder - base));
   volatile uint32_t* const abort_ptr = holder_ptr + 1;
   int* const sums = reinterpret_cast<int*>(gbase + (holder + 16u - base));    // one per warp
-  int* const offs = sums + 16;                   // clamped offsets, [groups + 1]
+  uint32_t* const magic = reinterpret_cast<uint32_t*>(sums + 16);     // ceil(2^32 / n), [17]
+  int* const offs = sums + 16 + 20;              // clamped offsets, [groups + 1]
   int* const starts = offs + p.groups + 1;       // a group's first item, [groups + 1] (rows form)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
-      mbar_init(full0 + 8u * s, kWeights ? CG : 1);
+      mbar_init(full0 + 8u * s, 1);
       mbar_init(empty0 + 8u * s, 1);
       mbar_init(tail0 + 8u * s, 1);
+      mbar_init(peer0 + 8u * s, 1);
     }
     for (int a = 0; a < kAccStages; ++a) {
       mbar_init(tfull0 + 8u * a, 1);
@@ -188,8 +305,11 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmF, const __grid_constant__ 
       const int e = __ldg(p.index + g);
       if (e < 0 || e >= p.sets) return 0;
     }
-    return (rows + bn - 1) / bn;
+    return fast_quot(rows + bn - 1, p.by_bn);
   };
+  // (rr / high by __umulhi(rr, magic[high]): exact below 2^28, which holds 16 x the feature tiles)
+  if (threadIdx.x >= 2 && threadIdx.x <= kGroupedMaxStrip)
+    magic[threadIdx.x] = 0xFFFFFFFFu / threadIdx.x + 1u;
   for (int g = threadIdx.x; g <= p.groups; g += blockDim.x)
     offs[g] = min(max(__ldg(p.offsets + g), 0), p.rows);
   __syncthreads();
@@ -223,9 +343,10 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmF, const __grid_constant__ 
 
   const Watch w{abort_ptr, p.status, p.timeout_ns};
 
-  // An item: a feature tile of 128 CG features, and of its group either a tile of
-  // tokens (the group's rows cut evenly, in whole units, into the fewest tiles of at
-  // most bn) or a tile of output rows.
+  // An item: a feature tile of 128 CG features, and of its group either a tile of up to bn
+  // tokens (all but a group's last one bn wide) or a tile of output rows.  Items of a group
+  // go through its strips of `strip` token (or column) tiles, tile by tile, then feature by
+  // feature, so that CTAs at work together share operands in L2.
   struct Item {
     int g, e;                // group; set of weights, -1 for none
     int f0;                  // first feature
@@ -233,25 +354,19 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmF, const __grid_constant__ 
     int width, valid;        // MMA columns, and how many of them are the item's
     int m0, mn;              // weights form: the group's first row and number of rows
     int blocks;              // k-blocks
+    bool down;               // walked from the last one
   };
-  const int min_width = p.unit * CG;
-  int cursor = 0;                                // the last item's group
+  const int min_width = p.unit * CG;             // (a power of two)
+  const int k_blocks = (p.k + BK - 1) / BK;
+  int cursor = 0, wave = 0;                      // the last item's group; items so far
   const auto item_at = [&](int it) {
     Item i;
+    i.down = p.alternate && (wave++ & 1);
+    int r, tiles;
     if constexpr (kWeights) {
-      const int per = p.tiles_f * p.tiles_c;
-      i.g = it / per;
-      i.e = i.g;
-      const int r = it - i.g * per;
-      const int strip = r / (kGroupedStrip * p.tiles_f), rr = r - strip * kGroupedStrip * p.tiles_f;
-      const int high = min(kGroupedStrip, p.tiles_c - strip * kGroupedStrip);
-      i.f0 = rr / high * (128 * CG);
-      i.t0 = (strip * kGroupedStrip + rr % high) * bn;
-      i.valid = min(bn, p.cols - i.t0);
-      i.width = (i.valid + min_width - 1) / min_width * min_width;
-      i.m0 = offs[i.g];
-      i.mn = max(0, offs[i.g + 1] - i.m0);
-      i.blocks = (i.mn + BK - 1) / BK;
+      i.g = fast_quot(it, p.by_group);
+      r = it - i.g * p.by_group.d;
+      tiles = p.tiles_c;
     } else {
       // starts[lo] <= it < starts[hi]; items come in increasing order
       int lo = cursor, hi = p.groups;
@@ -262,27 +377,36 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmF, const __grid_constant__ 
       }
       cursor = lo;
       i.g = lo;
-      i.e = p.index ? __ldg(p.index + lo) : lo;
-      if (i.e < 0 || i.e >= p.sets) i.e = -1;
-      const int rows = offs[lo + 1] - offs[lo];
-      const int r = it - starts[lo], tiles = (rows + bn - 1) / bn;
-      const int strip = r / (kGroupedStrip * p.tiles_f), rr = r - strip * kGroupedStrip * p.tiles_f;
-      const int high = min(kGroupedStrip, tiles - strip * kGroupedStrip);
-      const int tile = strip * kGroupedStrip + rr % high;
-      i.f0 = rr / high * (128 * CG);
-      const int each = ((rows + tiles - 1) / tiles + min_width - 1) / min_width * min_width;
-      i.valid = max(0, min(each, rows - tile * each));
-      i.width = max(min_width, (i.valid + min_width - 1) / min_width * min_width);
-      i.t0 = offs[lo] + tile * each;
-      i.m0 = i.mn = 0;
-      i.blocks = i.e < 0 ? 0 : (p.k + BK - 1) / BK;
+      r = it - starts[lo];
+      tiles = fast_quot(offs[lo + 1] - offs[lo] + bn - 1, p.by_bn);
     }
+    const int strip = fast_quot(r, p.by_strip), rr = r - strip * p.by_strip.d;
+    const int high = min(p.strip, tiles - strip * p.strip);
+    const int ft = high == 1 ? rr : (int)__umulhi((uint32_t)rr, magic[high]);
+    const int tile = strip * p.strip + rr - ft * high;
+    i.f0 = ft * (128 * CG);
+    if constexpr (kWeights) {
+      i.e = i.g;
+      i.t0 = tile * bn;
+      i.valid = min(bn, p.cols - i.t0);
+      i.m0 = offs[i.g];
+      i.mn = max(0, offs[i.g + 1] - i.m0);
+      i.blocks = (i.mn + BK - 1) / BK;
+    } else {
+      i.e = p.index ? __ldg(p.index + i.g) : i.g;
+      if (i.e < 0 || i.e >= p.sets) i.e = -1;
+      i.t0 = offs[i.g] + tile * bn;
+      i.valid = min(bn, offs[i.g + 1] - i.t0);
+      i.m0 = i.mn = 0;
+      i.blocks = i.e < 0 ? 0 : k_blocks;
+    }
+    i.width = (i.valid + min_width - 1) & -min_width;
     return i;
   };
 
   if (warp == 0) {
     // ---------------------------------------------------------- TMA producer
-    const uint64_t pol = make_l2_policy(0);
+    const uint64_t pol_f = make_l2_policy(p.l2_hints & 3u), pol_t = make_l2_policy(p.l2_hints >> 2 & 3u);
     int s = 0;
     uint32_t ph = 0;
     bool ok = true;
@@ -291,7 +415,8 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmF, const __grid_constant__ 
       const int f0 = i.f0 + (int)rank * 128;
       const int width = i.width / CG;                    // this CTA's columns
       const int t0 = i.t0 + (int)rank * width;
-      for (int kb = 0; kb < i.blocks; ++kb) {
+      for (int n = 0; n < i.blocks; ++n) {
+        const int kb = i.down ? i.blocks - 1 - n : n;
         if (!__all_sync(0xFFFFFFFFu, wait_phase(empty0 + 8u * s, ph ^ 1u, w, kWaitProducer))) {
           ok = false;
           break;
@@ -317,18 +442,17 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmF, const __grid_constant__ 
               const uint32_t bar = tail0 + 8u * s;
               mbar_arrive_expect_tx(bar, bytes);
               for (int j = 0; j < F_BOXES; ++j)
-                tma_load_3d(sf + j * MN_ATOM, &tmF, bar, f0 + j * ATOM_K, m, 0, pol);
+                tma_load_3d(sf + j * MN_ATOM, &tmF, bar, f0 + j * ATOM_K, m, 0, pol_f);
               for (int j = 0; j < width / ATOM_K; ++j)
-                tma_load_3d(st + j * MN_ATOM, &tmT, bar, t0 + j * ATOM_K, m, 0, pol);
+                tma_load_3d(st + j * MN_ATOM, &tmT, bar, t0 + j * ATOM_K, m, 0, pol_t);
             } else {
               const uint32_t fb = full0 + 8u * s;
               const uint32_t bar = PAIR ? map_to_rank(fb, 0) : fb;
               if (rank == 0) mbar_arrive_expect_tx(fb, CG * bytes);
-              else mbar_arrive_cluster(bar);
               for (int j = 0; j < F_BOXES; ++j)
-                OperandLoad<CG, false>::load(sf + j * MN_ATOM, &tmF, bar, f0 + j * ATOM_K, m, 0, 0, pol);
+                OperandLoad<CG, false>::load(sf + j * MN_ATOM, &tmF, bar, f0 + j * ATOM_K, m, 0, 0, pol_f);
               for (int j = 0; j < width / ATOM_K; ++j)
-                OperandLoad<CG, false>::load(st + j * MN_ATOM, &tmT, bar, t0 + j * ATOM_K, m, 0, 0, pol);
+                OperandLoad<CG, false>::load(st + j * MN_ATOM, &tmT, bar, t0 + j * ATOM_K, m, 0, 0, pol_t);
             }
           } else {
             const int k0 = kb * BK;
@@ -340,15 +464,15 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmF, const __grid_constant__ 
                                               (uint32_t)(atoms * width) * 128u));
             if (p.f_mn) {
               for (int j = 0; j < F_BOXES; ++j)
-                OperandLoad<CG, false>::load(sf + j * MN_ATOM, &tmF, bar, f0 + j * ATOM_K, k0, i.e, 0, pol);
+                OperandLoad<CG, false>::load(sf + j * MN_ATOM, &tmF, bar, f0 + j * ATOM_K, k0, i.e, 0, pol_f);
             } else {
               for (int a = 0; a < atoms; ++a)
-                OperandLoad<CG, false>::load(sf + a * F_ATOM, &tmF, bar, k0 + a * ATOM_K, f0, i.e, 0, pol);
+                OperandLoad<CG, false>::load(sf + a * F_ATOM, &tmF, bar, k0 + a * ATOM_K, f0, i.e, 0, pol_f);
             }
             for (int a = 0; a < atoms; ++a)
               for (int u = 0; u < width; u += p.unit)
                 OperandLoad<CG, false>::load(st + a * t_atom + u * 128, &tmT, bar, k0 + a * ATOM_K,
-                                             t0 + u, 0, 0, pol);
+                                             t0 + u, 0, 0, pol_t);
           }
         }
         __syncwarp();
@@ -380,7 +504,8 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmF, const __grid_constant__ 
         const uint32_t d_tmem = tmem_base + (uint32_t)acc * kAccStride;
         const uint32_t idesc = p.idesc | (uint32_t)(i.width >> 3) << 17;
         if (!dbg_check((uint32_t)i.width <= kAccStride, kChkMmaTmem, w)) break;
-        for (int kb = 0; kb < i.blocks; ++kb) {
+        for (int n = 0; n < i.blocks; ++n) {
+          const int kb = i.down ? i.blocks - 1 - n : n;
           ok = __all_sync(0xFFFFFFFFu, wait_phase(full0 + 8u * s, ph, w, kWaitMmaFull));
           if (!ok) break;
           tc_fence_after_sync();
@@ -406,12 +531,12 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmF, const __grid_constant__ 
               for (int k = 0; k < K_STEPS; ++k)
                 umma<CG, KIND>(d_tmem, fd + (k / STEPS_PER_ATOM * f_next + k % STEPS_PER_ATOM * f_step),
                                td + (k / STEPS_PER_ATOM * t_next + k % STEPS_PER_ATOM * t_step),
-                               idesc, (kb | k) != 0 ? 1u : 0u);
+                               idesc, (n | k) != 0 ? 1u : 0u);
             } else {
               for (int k = 0; k < steps; ++k)
                 umma<CG, KIND>(d_tmem, fd + (k / STEPS_PER_ATOM * f_next + k % STEPS_PER_ATOM * f_step),
                                td + (k / STEPS_PER_ATOM * t_next + k % STEPS_PER_ATOM * t_step),
-                               idesc, (kb | k) != 0 ? 1u : 0u);
+                               idesc, (n | k) != 0 ? 1u : 0u);
             }
             umma_commit<CG, PAIR>(empty0 + 8u * s, 3);
           }
@@ -428,114 +553,142 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmF, const __grid_constant__ 
     // ---------------------------------------------------------- epilogue
     const int q = warp & 3;                      // TMEM lane quarter of this warp
     const int strm = (warp - 2) >> 2;
+    const uint32_t odd = lane & 1;
     int acc = 0, turn = 0;
     uint32_t aph = 0;
-    const int r_es = p.r_dt == DT_F32 ? 4 : 2, z_es = p.z_dt == DT_F32 ? 4 : 2,
-              d_es = p.d_dt == DT_F32 ? 4 : 2;
-    const long long r_step = p.ldr * r_es, z_step = p.ldz * z_es, d_step = p.ldd * d_es;
+    const auto bytes = [](int dt) { return dt == DT_F32 ? 4 : 2; };
+    const bool r16 = p.r_dt != DT_F32;
     for (int it = cluster_id; it < num_items; it += num_clusters, turn ^= 1) {
       const Item i = item_at(it);
       const int f = i.f0 + (int)rank * 128 + q * 32 + lane;
       const bool mine = f < p.feats;
+      const bool pairs = !(p.feats & 1) || !__any_sync(0xFFFFFFFFu, f + 1 == p.feats);
       // (debug build: what is stored lies inside d)
       if (!dbg_check(i.f0 >= 0 && i.t0 >= 0 && i.valid <= i.width &&
                          i.t0 + i.valid <= (kWeights ? p.cols : p.rows),
                      kChkEpiStore, w))
         break;
-      const long long first = kWeights ? (long long)i.g * p.sd + (long long)i.t0 * p.ldd + f : 0;
-      const long long row = i.t0;
-      const uint8_t* const r_at = static_cast<const uint8_t*>(p.r) +
-                                  (kWeights ? first * r_es : row * r_step + (long long)f * r_es);
-      uint8_t* const z_at = static_cast<uint8_t*>(p.z) + (row * z_step + (long long)f * z_es);
-      uint8_t* const d_at = static_cast<uint8_t*>(p.d) +
-                            (kWeights ? first * d_es : row * d_step + (long long)f * d_es);
-      const int count = mine ? i.valid : 0;
-      float scale = p.alpha, bias = 0.f;
+      const auto place = [&](const void* base, long long ld, int dt) {
+        uint8_t* const row = static_cast<uint8_t*>(const_cast<void*>(base)) +
+                             ((kWeights ? (long long)i.g * p.sd : 0ll) + (long long)i.t0 * ld) * bytes(dt);
+        return EpiMatrix{row + (long long)f * bytes(dt),
+                         row + (long long)(f & ~1) * bytes(dt) + (odd ? ld * bytes(dt) : 0ll),
+                         ld * bytes(dt), dt};
+      };
+      const EpiMatrix rm = place(p.r, p.ldr, p.r_dt), zm = place(p.z, p.ldz, p.z_dt),
+                      dm = place(p.d, p.ldd, p.d_dt);
+      float scale = i.blocks ? p.alpha : 0.f, bias = 0.f;
       if constexpr (!kWeights) {
         if (mine && i.e >= 0) {
           const long long at = (long long)i.e * p.feats + f;
-          if (p.set_scale) scale *= __ldg(p.set_scale + i.e);
-          if (p.col_scale) scale *= __ldg(p.col_scale + at);
+          if (p.set_scale && i.blocks) scale *= __ldg(p.set_scale + i.e);
+          if (p.col_scale && i.blocks) scale *= __ldg(p.col_scale + at);
           if (p.bias) bias = p.bias_dt == DT_F32 ? __ldg(static_cast<const float*>(p.bias) + at)
                              : p.bias_dt == DT_F16
                                  ? __half2float(__ushort_as_half(__ldg(static_cast<const uint16_t*>(p.bias) + at)))
                                  : __uint_as_float((uint32_t)__ldg(static_cast<const uint16_t*>(p.bias) + at) << 16);
         }
       }
-      // Chunks of 16 columns, every other one this warp's; which warp of the two starts
-      // alternates, so that items of one chunk are shared out.  A chunk's residual
-      // and row factors (one a lane) are on their way before the accumulator is
-      // waited for.
-      uint32_t res[kGroupedChunk];
+      // Chunks of 32 columns, every other one this warp's; which warp of the two starts
+      // alternates, so that items of one chunk are shared out.  The residual of the first
+      // two chunks (the first, of 32 bits) and the first's row factors (one a lane) are on their
+      // way before the accumulator is waited for, the others two chunks (one) ahead.
+      constexpr int kNext = 2 * kGroupedChunk;
+      uint32_t res[32];
       float factor = 1.f;
-      const auto fetch = [&](int c) {
-        if (p.r) {
-#pragma unroll
-          for (int x = 0; x < kGroupedChunk; ++x)
-            res[x] = c + x < count ? grouped_elem(r_at + (c + x) * r_step, p.r_dt) : 0u;
-        }
+      const auto fetch_32 = [&](int c) {
+        epi_load<0>(rm, c, i.valid - c, pairs, mine, res);
+        if (c + 16 < i.valid) epi_load<16>(rm, c + 16, i.valid - c - 16, pairs, mine, res);
+      };
+      const auto fetch_16 = [&](auto from, int c) {
+        constexpr int FROM = decltype(from)::value;
+        epi_load<FROM>(rm, c, i.valid - c, pairs, mine, res);
+        if (c + 16 < i.valid) epi_load<FROM + 8>(rm, c + 16, i.valid - c - 16, pairs, mine, res);
+      };
+      const auto fetch_factor = [&](int c) {
         if constexpr (!kWeights) {
           if (p.row_scale && i.blocks > 0)
-            factor = lane < kGroupedChunk && c + lane < i.valid
-                         ? __ldg(p.row_scale + row + c + lane) : 1.f;
+            factor = c + lane < i.valid ? __ldg(p.row_scale + i.t0 + c + lane) : 1.f;
         }
       };
       const int c_first = (strm ^ turn) * kGroupedChunk;
-      if (c_first < i.valid) fetch(c_first);
+      if (c_first < i.valid) {
+        if (p.r) {
+          if (r16) {
+            fetch_16(IntC<0>{}, c_first);
+            if (c_first + kNext < i.valid) fetch_16(IntC<16>{}, c_first + kNext);
+          } else {
+            fetch_32(c_first);
+          }
+        }
+        fetch_factor(c_first);
+      }
       if (!__all_sync(0xFFFFFFFFu, wait_phase(tfull0 + 8u * acc, aph, w, kWaitEpilogue))) break;
       tc_fence_after_sync();
+      // (What the arrival hands over is the accumulator, whose loads have completed; the
+      // pair's leader may be the other CTA.)
       const auto release = [&]() {
         tc_fence_before_sync();
         __syncwarp();
         if (lane == 0) {
           if constexpr (CG == 1) mbar_arrive(tempty0 + 8u * acc);
-          else mbar_arrive_cluster(map_to_rank(tempty0 + 8u * acc, 0));
+          else mbar_arrive_cluster_relaxed(map_to_rank(tempty0 + 8u * acc, 0));
         }
       };
       if (c_first >= i.valid) release();
       const uint32_t tbase = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)acc * kAccStride;
 #pragma unroll 1
-      for (int c = c_first; c < i.valid; c += 2 * kGroupedChunk) {
+      for (int c = c_first; c < i.valid; c += kNext) {
         uint32_t a[kGroupedChunk];
         __syncwarp();
-        tmem_load_16cols(tbase + c, a);
-        tmem_wait_ld16(a);
-        const bool last = c + 2 * kGroupedChunk >= i.valid;
-        if (last) release();
-        float v[kGroupedChunk];
+        tmem_load_32cols(tbase + c, a);
+        tmem_wait_ld(a);
+        if (c + kNext >= i.valid) release();
+        if (i.blocks == 0) {                     // (nothing was accumulated)
 #pragma unroll
-        for (int x = 0; x < kGroupedChunk; ++x) v[x] = i.blocks ? __uint_as_float(a[x]) * scale : 0.f;
-        if constexpr (!kWeights) {
-          if (p.row_scale) {
-#pragma unroll
-            for (int x = 0; x < kGroupedChunk; ++x) v[x] *= __shfl_sync(0xFFFFFFFFu, factor, x);
-          }
-          if (p.bias) {
-#pragma unroll
-            for (int x = 0; x < kGroupedChunk; ++x) v[x] += bias;
-          }
-          if (p.z) grouped_store(z_at + c * z_step, z_step, p.z_dt, count - c, v);
-          with_activation(p.act, [&](auto act) {
-#pragma unroll
-            for (int x = 0; x < kGroupedChunk; x += 2)
-              activate2<decltype(act)::value>(v[x], v[x + 1]);
-          });
+          for (int x = 0; x < kGroupedChunk; ++x) a[x] = 0u;
         }
-        if (p.r) {
-          if (p.r_dt == DT_F32) {
+        const auto half = [&](auto from) {
+          constexpr int FROM = decltype(from)::value;      // 0, 16
+          const int left = i.valid - c - FROM;
+          float v[16];
 #pragma unroll
-            for (int x = 0; x < kGroupedChunk; ++x) v[x] += __uint_as_float(res[x]);
-          } else if (p.r_dt == DT_F16) {
+          for (int x = 0; x < 16; ++x) v[x] = __uint_as_float(a[FROM + x]) * scale;
+          if constexpr (!kWeights) {
+            if (p.row_scale) {
 #pragma unroll
-            for (int x = 0; x < kGroupedChunk; ++x)
-              v[x] += __half2float(__ushort_as_half((uint16_t)res[x]));
-          } else {
+              for (int x = 0; x < 16; ++x) v[x] *= __shfl_sync(0xFFFFFFFFu, factor, FROM + x);
+            }
+            if (p.bias) {
 #pragma unroll
-            for (int x = 0; x < kGroupedChunk; ++x) v[x] += __uint_as_float(res[x] << 16);
+              for (int x = 0; x < 16; ++x) v[x] += bias;
+            }
+            if (p.z) epi_store(zm, c + FROM, left, pairs, mine, odd, v);
+            with_activation(p.act, [&](auto act) {
+#pragma unroll
+              for (int x = 0; x < 16; x += 2) activate2<decltype(act)::value>(v[x], v[x + 1]);
+            });
           }
+          if (p.r) {
+            if (r16) epi_add<FROM / 2>(rm, left, pairs, odd, res, v);
+            else epi_add<FROM>(rm, left, pairs, odd, res, v);
+          }
+          epi_store(dm, c + FROM, left, pairs, mine, odd, v);
+        };
+        half(IntC<0>{});
+        if (c + 16 < i.valid) half(IntC<16>{});
+        if (c + kNext < i.valid) {
+          if (p.r) {
+            if (r16) {
+#pragma unroll
+              for (int x = 0; x < 16; ++x) res[x] = res[16 + x];
+              if (c + 2 * kNext < i.valid) fetch_16(IntC<16>{}, c + 2 * kNext);
+            } else {
+              fetch_32(c + kNext);
+            }
+          }
+          fetch_factor(c + kNext);
         }
-        if (!last) fetch(c + 2 * kGroupedChunk);
-        grouped_store(d_at + c * d_step, d_step, p.d_dt, count - c, v);
       }
       if (++acc == kAccStages) { acc = 0; aph ^= 1u; }
     }
@@ -546,11 +699,10 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmF, const __grid_constant__ 
     for (int it = cluster_id; it < num_items; it += num_clusters) {
       const Item i = item_at(it);
       if (i.blocks > 0 && i.mn % UMMA_K != 0) {
-        const int at = (s + i.blocks - 1) % S;
+        const int at = i.down ? s : (s + i.blocks - 1) % S;
         if (!__all_sync(0xFFFFFFFFu, wait_phase<true>(tail0 + 8u * at, phases >> at & 1u, w,
                                                       kWaitProducer)))
           break;
-        phases ^= 1u << at;
         // rows [from, to) of every 128-byte wide atom column
         const int from = i.mn - (i.blocks - 1) * BK, to = (from + UMMA_K - 1) / UMMA_K * UMMA_K;
         uint8_t* const sf = gbase + (f_ring + at * F_STAGE - base);
@@ -563,10 +715,15 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmF, const __grid_constant__ 
         }
         fence_proxy_async_all();
         __syncwarp();
-        if (lane == 0) {
-          if constexpr (CG == 1) mbar_arrive(full0 + 8u * at);
-          else mbar_arrive_cluster(map_to_rank(full0 + 8u * at, 0));
+        if (rank != 0) {
+          if (lane == 0) mbar_arrive_cluster(map_to_rank(peer0 + 8u * at, 0));
+        } else {
+          if (PAIR && !__all_sync(0xFFFFFFFFu, wait_phase(peer0 + 8u * at, phases >> at & 1u, w,
+                                                          kWaitProducer)))
+            break;
+          if (lane == 0) mbar_arrive(full0 + 8u * at);
         }
+        phases ^= 1u << at;
       }
       s = (s + i.blocks) % S;
     }

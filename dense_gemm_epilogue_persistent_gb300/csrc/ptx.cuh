@@ -123,6 +123,14 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_bar) {
                :: "r"(cluster_bar) : "memory");
 }
 
+// The same without ordering this thread's earlier memory accesses (a release at cluster scope waits
+// for every global store before it): for arrivals that hand over nothing but what the
+// caller has finished reading.
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_bar) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];"
+               :: "r"(cluster_bar) : "memory");
+}
+
 // One non-blocking probe for completion of the phase with parity `parity`.
 // Acquire at cluster scope: arrivals may come from the peer CTA.
 __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
