@@ -28,6 +28,15 @@ struct Product {
   gb300::GroupedParams k_params{};     // the epilogue's part, offsets and index
 };
 
+// The kernel's form.
+int form_of(const Product& p) {
+  const gb300::GroupedParams& k = p.k_params;
+  if (p.weights) return gb300::kGroupedWeights;
+  const bool plain = dtype_bytes(p.f_type) == 2 && !k.row_scale && !k.col_scale && !k.bias && !k.z &&
+                     k.act == gb300::ACT_NONE;
+  return plain ? gb300::kGroupedPlainRows : gb300::kGroupedRows;
+}
+
 struct GroupedPlan {
   gemm_config_t cfg{};
   const void* kern = nullptr;
@@ -84,11 +93,12 @@ gemm_status_t plan_grouped(gemm_handle* h, const Product& p, GroupedPlan& out) {
   c.tiles = p.weights ? p.groups * tiles_f * cdiv(p.cols, c.tile_n)
                       : (p.rows / c.tile_n + std::min(p.groups, p.rows)) * tiles_f;
   if (c.tiles > INT32_MAX / 2) return GEMM_ERR_INVALID_ARG;
-  out.kern = gb300::grouped_kernel_for(es, c.cta_group, p.weights);
+  const int form = form_of(p);
+  out.kern = gb300::grouped_kernel_for(es, c.cta_group, form);
   if (!out.kern) return GEMM_ERR_UNSUPPORTED_CONFIG;
   int resident = 0;
   GB300_CHECK(resident_kernel_clusters(
-      h, h->grouped_variants[es == 2 ? 0 : es == 1 ? 1 : 2][c.cta_group - 1][p.weights], out.kern, c,
+      h, h->grouped_variants[es == 2 ? 0 : es == 1 ? 1 : 2][c.cta_group - 1][form], out.kern, c,
       c.cta_group, &resident));
   c.grid_ctas = (int)std::max<int64_t>(1, std::min<int64_t>(c.tiles, resident)) * c.cta_group;
   return GEMM_OK;

@@ -90,6 +90,7 @@ struct GroupedParams {
   int bias_dt, r_dt, z_dt, d_dt, act;
 };
 
+enum : int { kGroupedRows = 0, kGroupedPlainRows = 1, kGroupedWeights = 2 };
 constexpr int kGroupedKA = 2;                  // 128-byte K atoms a ring stage
 constexpr int kGroupedEpiWarps = 8;
 constexpr int kGroupedChunk = 32;              // columns of an epilogue chunk
@@ -126,63 +127,56 @@ __device__ __forceinline__ uint32_t swap_halves(uint32_t w, uint32_t odd) {
 }
 
 // 16 columns from c on, of which `left` are the item's, for lanes that have a feature (mine).
-template <int DT>
-__device__ __forceinline__ void epi_store_as(const EpiMatrix& m, int c, int left, bool pairs,
-                                             bool mine, uint32_t odd, const float (&v)[16]) {
-  if constexpr (DT == DT_F32) {
-    uint8_t* p = m.own + c * m.step;
-    if (left >= 16) {
-      if (mine) {
-#pragma unroll
-        for (int x = 0; x < 16; ++x, p += m.step) *reinterpret_cast<float*>(p) = v[x];
-      }
-    } else {
-#pragma unroll
-      for (int x = 0; x < 16; ++x, p += m.step)
-        if (mine && x < left) *reinterpret_cast<float*>(p) = v[x];
-    }
-  } else {
-    uint32_t w[8];
-#pragma unroll
-    for (int x = 0; x < 8; ++x)
-      w[x] = DT == DT_F16 ? pack_f16x2(v[2 * x], v[2 * x + 1]) : pack_bf16x2(v[2 * x], v[2 * x + 1]);
-    if (pairs && left >= 16) {
-#pragma unroll
-      for (int x = 0; x < 8; ++x) w[x] = swap_halves(w[x], odd);
-      if (mine) {
-        uint8_t* p = m.pair + c * m.step;
-#pragma unroll
-        for (int x = 0; x < 8; ++x, p += 2 * m.step) *reinterpret_cast<uint32_t*>(p) = w[x];
-      }
-    } else {
-      uint8_t* p = m.own + c * m.step;
-#pragma unroll
-      for (int x = 0; x < 16; ++x, p += m.step)
-        if (mine && x < left) *reinterpret_cast<uint16_t*>(p) = (uint16_t)(w[x / 2] >> (16 * (x & 1)));
-    }
-  }
-}
+// (One way through each of the two forms, its stores predicated by column: code that is run
+// once a chunk is fetched from memory as often as it is run.)
 __device__ __forceinline__ void epi_store(const EpiMatrix& m, int c, int left, bool pairs, bool mine,
                                           uint32_t odd, const float (&v)[16]) {
-  if (m.dt == DT_BF16) epi_store_as<DT_BF16>(m, c, left, pairs, mine, odd, v);
-  else if (m.dt == DT_F16) epi_store_as<DT_F16>(m, c, left, pairs, mine, odd, v);
-  else epi_store_as<DT_F32>(m, c, left, pairs, mine, odd, v);
+  if (m.dt == DT_F32) {
+    uint8_t* p = m.own + c * m.step;
+#pragma unroll
+    for (int x = 0; x < 16; ++x, p += m.step)
+      if (mine && x < left) *reinterpret_cast<float*>(p) = v[x];
+    return;
+  }
+  uint32_t w[8];
+  if (m.dt == DT_F16) {
+#pragma unroll
+    for (int x = 0; x < 8; ++x) w[x] = pack_f16x2(v[2 * x], v[2 * x + 1]);
+  } else {
+#pragma unroll
+    for (int x = 0; x < 8; ++x) w[x] = pack_bf16x2(v[2 * x], v[2 * x + 1]);
+  }
+  if (pairs) {
+#pragma unroll
+    for (int x = 0; x < 8; ++x) w[x] = swap_halves(w[x], odd);
+    const int mine_left = mine ? left - (int)odd : 0;
+    uint8_t* p = m.pair + c * m.step;
+#pragma unroll
+    for (int x = 0; x < 8; ++x, p += 2 * m.step)
+      if (2 * x < mine_left) *reinterpret_cast<uint32_t*>(p) = w[x];
+  } else {
+    uint8_t* p = m.own + c * m.step;
+#pragma unroll
+    for (int x = 0; x < 16; ++x, p += m.step)
+      if (mine && x < left) *reinterpret_cast<uint16_t*>(p) = (uint16_t)(w[x / 2] >> (16 * (x & 1)));
+  }
 }
 
 // The words of such 16 columns, as they lie in memory: 16 of 32 bits, or 8 of two columns of 16.
 template <int FROM>
 __device__ __forceinline__ void epi_load(const EpiMatrix& m, int c, int left, bool pairs, bool mine,
-                                         uint32_t (&r)[32]) {
+                                         uint32_t odd, uint32_t (&r)[32]) {
   if (m.dt == DT_F32) {
     const uint8_t* p = m.own + c * m.step;
 #pragma unroll
     for (int x = 0; x < 16; ++x, p += m.step)
       r[(FROM + x) & 31] = mine && x < left ? *reinterpret_cast<const uint32_t*>(p) : 0u;
-  } else if (pairs && left >= 16) {
+  } else if (pairs) {
+    const int mine_left = mine ? left - (int)odd : 0;
     const uint8_t* p = m.pair + c * m.step;
 #pragma unroll
     for (int x = 0; x < 8; ++x, p += 2 * m.step)
-      r[(FROM + x) & 31] = mine ? *reinterpret_cast<const uint32_t*>(p) : 0u;
+      r[(FROM + x) & 31] = 2 * x < mine_left ? *reinterpret_cast<const uint32_t*>(p) : 0u;
   } else {
     const uint8_t* p = m.own + c * m.step;
 #pragma unroll
@@ -195,7 +189,7 @@ __device__ __forceinline__ void epi_load(const EpiMatrix& m, int c, int left, bo
   }
 }
 template <int FROM>
-__device__ __forceinline__ void epi_add(const EpiMatrix& m, int left, bool pairs, uint32_t odd,
+__device__ __forceinline__ void epi_add(const EpiMatrix& m, bool pairs, uint32_t odd,
                                         const uint32_t (&r)[32], float (&v)[16]) {
   if (m.dt == DT_F32) {
 #pragma unroll
@@ -205,7 +199,7 @@ __device__ __forceinline__ void epi_add(const EpiMatrix& m, int left, bool pairs
   uint32_t w[8];
 #pragma unroll
   for (int x = 0; x < 8; ++x) w[x] = r[(FROM + x) & 31];
-  if (pairs && left >= 16) {
+  if (pairs) {
 #pragma unroll
     for (int x = 0; x < 8; ++x) w[x] = swap_halves(w[x], odd);
   }
@@ -226,10 +220,13 @@ __device__ __forceinline__ void epi_add(const EpiMatrix& m, int left, bool pairs
   }
 }
 
-template <int CG, int AB_BYTES, bool kWeights>
-__global__ void __launch_bounds__(grouped_threads(kWeights), 1)
+// FORM 0: rows; 1: rows with nothing but alpha, a set's scale and a residual behind the product;
+// 2: weights.
+template <int CG, int AB_BYTES, int FORM>
+__global__ void __launch_bounds__(grouped_threads(FORM == kGroupedWeights), 1)
 grouped_kernel(const __grid_constant__ CUtensorMap tmF, const __grid_constant__ CUtensorMap tmT,
                const __grid_constant__ GroupedParams p) {
+  constexpr bool kWeights = FORM == kGroupedWeights, kFull = FORM == kGroupedRows;
   constexpr int KIND = (AB_BYTES == 1) ? 1 : (AB_BYTES == 4 ? 2 : 0);
   constexpr int KA = kGroupedKA;
   constexpr int ATOM_K = 128 / AB_BYTES;         // K of a 128-byte atom; features of an MN-major one
@@ -359,9 +356,9 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmF, const __grid_constant__ 
   const int min_width = p.unit * CG;             // (a power of two)
   const int k_blocks = (p.k + BK - 1) / BK;
   int cursor = 0, wave = 0;                      // the last item's group; items so far
-  const auto item_at = [&](int it) {
+  const auto peek = [&](int it) {
     Item i;
-    i.down = p.alternate && (wave++ & 1);
+    i.down = p.alternate && (wave & 1);
     int r, tiles;
     if constexpr (kWeights) {
       i.g = fast_quot(it, p.by_group);
@@ -401,6 +398,11 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmF, const __grid_constant__ 
       i.blocks = i.e < 0 ? 0 : k_blocks;
     }
     i.width = (i.valid + min_width - 1) & -min_width;
+    return i;
+  };
+  const auto item_at = [&](int it) {
+    const Item i = peek(it);
+    ++wave;
     return i;
   };
 
@@ -579,9 +581,11 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmF, const __grid_constant__ 
                       dm = place(p.d, p.ldd, p.d_dt);
       float scale = i.blocks ? p.alpha : 0.f, bias = 0.f;
       if constexpr (!kWeights) {
+        if (p.set_scale && i.blocks) scale *= __ldg(p.set_scale + i.e);
+      }
+      if constexpr (kFull) {
         if (mine && i.e >= 0) {
           const long long at = (long long)i.e * p.feats + f;
-          if (p.set_scale && i.blocks) scale *= __ldg(p.set_scale + i.e);
           if (p.col_scale && i.blocks) scale *= __ldg(p.col_scale + at);
           if (p.bias) bias = p.bias_dt == DT_F32 ? __ldg(static_cast<const float*>(p.bias) + at)
                              : p.bias_dt == DT_F16
@@ -597,20 +601,32 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmF, const __grid_constant__ 
       uint32_t res[32];
       float factor = 1.f;
       const auto fetch_32 = [&](int c) {
-        epi_load<0>(rm, c, i.valid - c, pairs, mine, res);
-        if (c + 16 < i.valid) epi_load<16>(rm, c + 16, i.valid - c - 16, pairs, mine, res);
+        epi_load<0>(rm, c, i.valid - c, pairs, mine, odd, res);
+        if (c + 16 < i.valid) epi_load<16>(rm, c + 16, i.valid - c - 16, pairs, mine, odd, res);
       };
       const auto fetch_16 = [&](auto from, int c) {
         constexpr int FROM = decltype(from)::value;
-        epi_load<FROM>(rm, c, i.valid - c, pairs, mine, res);
-        if (c + 16 < i.valid) epi_load<FROM + 8>(rm, c + 16, i.valid - c - 16, pairs, mine, res);
+        epi_load<FROM>(rm, c, i.valid - c, pairs, mine, odd, res);
+        if (c + 16 < i.valid) epi_load<FROM + 8>(rm, c + 16, i.valid - c - 16, pairs, mine, odd, res);
       };
       const auto fetch_factor = [&](int c) {
-        if constexpr (!kWeights) {
+        if constexpr (kFull) {
           if (p.row_scale && i.blocks > 0)
             factor = c + lane < i.valid ? __ldg(p.row_scale + i.t0 + c + lane) : 1.f;
         }
       };
+      // The next item's residual into L2, a token a lane (a warp's 32 features of one are 64 or
+      // 128 bytes): 8191 x 8192 of inner size 64 XXX us, XXX without.
+      if (p.r && it + num_clusters < num_items) {
+        const Item next = peek(it + num_clusters);
+        const long long f_next = next.f0 + (int)rank * 128 + q * 32;
+        if (f_next < p.feats) {
+          const uint8_t* const at = static_cast<const uint8_t*>(p.r) +
+              ((kWeights ? (long long)next.g * p.sd : 0ll) + f_next) * bytes(p.r_dt);
+          for (int c = strm * 32 + lane; c < next.valid; c += 64)
+            prefetch_l2(at + (next.t0 + c) * rm.step);
+        }
+      }
       const int c_first = (strm ^ turn) * kGroupedChunk;
       if (c_first < i.valid) {
         if (p.r) {
@@ -654,7 +670,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmF, const __grid_constant__ 
           float v[16];
 #pragma unroll
           for (int x = 0; x < 16; ++x) v[x] = __uint_as_float(a[FROM + x]) * scale;
-          if constexpr (!kWeights) {
+          if constexpr (kFull) {
             if (p.row_scale) {
 #pragma unroll
               for (int x = 0; x < 16; ++x) v[x] *= __shfl_sync(0xFFFFFFFFu, factor, FROM + x);
@@ -670,8 +686,8 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmF, const __grid_constant__ 
             });
           }
           if (p.r) {
-            if (r16) epi_add<FROM / 2>(rm, left, pairs, odd, res, v);
-            else epi_add<FROM>(rm, left, pairs, odd, res, v);
+            if (r16) epi_add<FROM / 2>(rm, pairs, odd, res, v);
+            else epi_add<FROM>(rm, pairs, odd, res, v);
           }
           epi_store(dm, c + FROM, left, pairs, mine, odd, v);
         };

@@ -5,15 +5,18 @@
 
 namespace gb300 {
 
-const void* GB300_GROUPED_NAME(GB300_AB)(int cta_group, bool weights) {
+const void* GB300_GROUPED_NAME(GB300_AB)(int cta_group, int form) {
 #if GB300_AB == 2
-  if (weights)
-    return cta_group == 1 ? (const void*)&grouped_kernel<1, 2, true>
-                          : (const void*)&grouped_kernel<2, 2, true>;
+  if (form == kGroupedWeights)
+    return cta_group == 1 ? (const void*)&grouped_kernel<1, 2, kGroupedWeights>
+                          : (const void*)&grouped_kernel<2, 2, kGroupedWeights>;
+  if (form == kGroupedPlainRows)
+    return cta_group == 1 ? (const void*)&grouped_kernel<1, 2, kGroupedPlainRows>
+                          : (const void*)&grouped_kernel<2, 2, kGroupedPlainRows>;
 #endif
-  if (weights) return nullptr;
-  return cta_group == 1 ? (const void*)&grouped_kernel<1, GB300_AB, false>
-                        : (const void*)&grouped_kernel<2, GB300_AB, false>;
+  if (form != kGroupedRows) return nullptr;
+  return cta_group == 1 ? (const void*)&grouped_kernel<1, GB300_AB, kGroupedRows>
+                        : (const void*)&grouped_kernel<2, GB300_AB, kGroupedRows>;
 }
 
 }  // namespace gb300

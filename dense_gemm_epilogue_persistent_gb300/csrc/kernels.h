@@ -93,17 +93,18 @@ inline const void* linear_kernel_for(int ab_bytes, int cta_group, int ka, int ep
 const void* split_kernel_for(int ab_bytes);
 
 // kern_grouped.cu, compiled once per input width: products over groups of rows, by
-// CTA group, of the rows or (16 bits) of the weights.
+// CTA group and form (of the rows; at 16 bits also of the rows with a plain epilogue and of the
+// weights).
 #define GB300_GROUPED_NAME_(ab) kernel_grouped_ab##ab
 #define GB300_GROUPED_NAME(ab) GB300_GROUPED_NAME_(ab)
-const void* GB300_GROUPED_NAME(2)(int cta_group, bool weights);
-const void* GB300_GROUPED_NAME(1)(int cta_group, bool weights);
-const void* GB300_GROUPED_NAME(4)(int cta_group, bool weights);
-inline const void* grouped_kernel_for(int ab_bytes, int cta_group, bool weights) {
+const void* GB300_GROUPED_NAME(2)(int cta_group, int form);
+const void* GB300_GROUPED_NAME(1)(int cta_group, int form);
+const void* GB300_GROUPED_NAME(4)(int cta_group, int form);
+inline const void* grouped_kernel_for(int ab_bytes, int cta_group, int form) {
   switch (ab_bytes) {
-    case 2: return GB300_GROUPED_NAME(2)(cta_group, weights);
-    case 1: return GB300_GROUPED_NAME(1)(cta_group, weights);
-    case 4: return GB300_GROUPED_NAME(4)(cta_group, weights);
+    case 2: return GB300_GROUPED_NAME(2)(cta_group, form);
+    case 1: return GB300_GROUPED_NAME(1)(cta_group, form);
+    case 4: return GB300_GROUPED_NAME(4)(cta_group, form);
   }
   return nullptr;
 }

@@ -257,6 +257,11 @@ __device__ __forceinline__ void bulk_wait_group_read() {
   asm volatile("cp.async.bulk.wait_group.read %0;" :: "n"(N) : "memory");
 }
 
+// The line of a global address into L2.
+__device__ __forceinline__ void prefetch_l2(const void* p) {
+  asm volatile("prefetch.global.L2 [%0];" :: "l"(p) : "memory");
+}
+
 // Programmatic dependent launch.  launch_dependents lets the next kernel of
 // the stream (if launched with programmatic stream serialization) be
 // scheduled once every CTA of this grid has issued it or exited;
