@@ -28,13 +28,16 @@ struct Product {
   gb300::GroupedParams k_params{};     // the epilogue's part, offsets and index
 };
 
-// The kernel's form.
-int form_of(const Product& p) {
+// The type of the lean epilogue, or -1 for the whole one: nothing but alpha, a set's scale and a
+// residual of d's type; the 16-bit forms move features by twos.  (8191 x 8192 of inner size 64 with
+// a residual, bf16: 77 us, 125 by the whole one.)
+int lean_of(const Product& p) {
   const gb300::GroupedParams& k = p.k_params;
-  if (p.weights) return gb300::kGroupedWeights;
-  const bool plain = dtype_bytes(p.f_type) == 2 && !k.row_scale && !k.col_scale && !k.bias && !k.z &&
-                     k.act == gb300::ACT_NONE;
-  return plain ? gb300::kGroupedPlainRows : gb300::kGroupedRows;
+  const int dt = device_dt(k.d_dt);
+  const bool lean = dtype_bytes(p.f_type) == 2 && !k.row_scale && !k.col_scale && !k.bias && !k.z &&
+                    k.act == gb300::ACT_NONE && (!k.r || k.r_dt == k.d_dt) &&
+                    (dt == gb300::DT_F32 || p.feats % 2 == 0);
+  return lean ? dt : -1;
 }
 
 struct GroupedPlan {
@@ -93,12 +96,13 @@ gemm_status_t plan_grouped(gemm_handle* h, const Product& p, GroupedPlan& out) {
   c.tiles = p.weights ? p.groups * tiles_f * cdiv(p.cols, c.tile_n)
                       : (p.rows / c.tile_n + std::min(p.groups, p.rows)) * tiles_f;
   if (c.tiles > INT32_MAX / 2) return GEMM_ERR_INVALID_ARG;
-  const int form = form_of(p);
-  out.kern = gb300::grouped_kernel_for(es, c.cta_group, form);
+  const int lean = lean_of(p);
+  out.kern = gb300::grouped_kernel_for(es, c.cta_group, p.weights, lean);
   if (!out.kern) return GEMM_ERR_UNSUPPORTED_CONFIG;
   int resident = 0;
   GB300_CHECK(resident_kernel_clusters(
-      h, h->grouped_variants[es == 2 ? 0 : es == 1 ? 1 : 2][c.cta_group - 1][form], out.kern, c,
+      h, h->grouped_variants[es == 2 ? 0 : es == 1 ? 1 : 2][c.cta_group - 1][p.weights][lean + 1],
+      out.kern, c,
       c.cta_group, &resident));
   c.grid_ctas = (int)std::max<int64_t>(1, std::min<int64_t>(c.tiles, resident)) * c.cta_group;
   return GEMM_OK;

@@ -24,7 +24,7 @@
 // group's infinities).  The two CTAs of a pair do so each for its own half: such a
 // stage's copies report to a barrier of the CTA, the other CTA's zeroing warp to the
 // leader's, which then completes the stage.  (A remote arrival for every stage instead, to
-// have the stages count both CTAs, cost a quarter: 8192^3 bf16 880 us, XXX so.)
+// have the stages count both CTAs, cost a quarter: 8192^3 bf16 880 us, 648 so.)
 //
 // Block: warp 0 TMA producer, warp 1 tensor memory and MMA issue, warps 2-9
 // epilogue (two per lane quarter, taking 16-column chunks alternately), warp 10 (weights
@@ -90,7 +90,6 @@ struct GroupedParams {
   int bias_dt, r_dt, z_dt, d_dt, act;
 };
 
-enum : int { kGroupedRows = 0, kGroupedPlainRows = 1, kGroupedWeights = 2 };
 constexpr int kGroupedKA = 2;                  // 128-byte K atoms a ring stage
 constexpr int kGroupedEpiWarps = 8;
 constexpr int kGroupedChunk = 32;              // columns of an epilogue chunk
@@ -116,6 +115,7 @@ constexpr int grouped_smem(int cta_group, int bn, int stages, int groups) {
 // features, 4 bytes, of one of them: even lanes of x, odd lanes of x + 1.  (A quarter fewer
 // instructions than 2 bytes of each.)  That is the way of whole chunks (`pairs`); where columns or
 // the last of an odd number of features are missing every lane moves its own elements.
+__host__ __device__ constexpr int elem_size(int dt) { return dt == DT_F32 ? 4 : 2; }
 struct EpiMatrix {
   uint8_t* own;              // this lane's element of column 0
   uint8_t* pair;             // the two elements that it moves of columns 0, 1
@@ -220,13 +220,14 @@ __device__ __forceinline__ void epi_add(const EpiMatrix& m, bool pairs, uint32_t
   }
 }
 
-// FORM 0: rows; 1: rows with nothing but alpha, a set's scale and a residual behind the product;
-// 2: weights.
-template <int CG, int AB_BYTES, int FORM>
-__global__ void __launch_bounds__(grouped_threads(FORM == kGroupedWeights), 1)
+// LEAN < 0: the whole epilogue, every type.  Else nothing but alpha, a set's scale and a residual
+// follow the product, d and the residual are of type LEAN, and a 16-bit one has an even number
+// of features.
+template <int CG, int AB_BYTES, bool kWeights, int LEAN>
+__global__ void __launch_bounds__(grouped_threads(kWeights), 1)
 grouped_kernel(const __grid_constant__ CUtensorMap tmF, const __grid_constant__ CUtensorMap tmT,
                const __grid_constant__ GroupedParams p) {
-  constexpr bool kWeights = FORM == kGroupedWeights, kFull = FORM == kGroupedRows;
+  constexpr bool kFull = !kWeights && LEAN < 0;
   constexpr int KIND = (AB_BYTES == 1) ? 1 : (AB_BYTES == 4 ? 2 : 0);
   constexpr int KA = kGroupedKA;
   constexpr int ATOM_K = 128 / AB_BYTES;         // K of a 128-byte atom; features of an MN-major one
@@ -558,155 +559,277 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmF, const __grid_constant__ 
     const uint32_t odd = lane & 1;
     int acc = 0, turn = 0;
     uint32_t aph = 0;
-    const auto bytes = [](int dt) { return dt == DT_F32 ? 4 : 2; };
-    const bool r16 = p.r_dt != DT_F32;
-    for (int it = cluster_id; it < num_items; it += num_clusters, turn ^= 1) {
-      const Item i = item_at(it);
-      const int f = i.f0 + (int)rank * 128 + q * 32 + lane;
-      const bool mine = f < p.feats;
-      const bool pairs = !(p.feats & 1) || !__any_sync(0xFFFFFFFFu, f + 1 == p.feats);
-      // (debug build: what is stored lies inside d)
-      if (!dbg_check(i.f0 >= 0 && i.t0 >= 0 && i.valid <= i.width &&
-                         i.t0 + i.valid <= (kWeights ? p.cols : p.rows),
-                     kChkEpiStore, w))
-        break;
-      const auto place = [&](const void* base, long long ld, int dt) {
-        uint8_t* const row = static_cast<uint8_t*>(const_cast<void*>(base)) +
-                             ((kWeights ? (long long)i.g * p.sd : 0ll) + (long long)i.t0 * ld) * bytes(dt);
-        return EpiMatrix{row + (long long)f * bytes(dt),
-                         row + (long long)(f & ~1) * bytes(dt) + (odd ? ld * bytes(dt) : 0ll),
-                         ld * bytes(dt), dt};
-      };
-      const EpiMatrix rm = place(p.r, p.ldr, p.r_dt), zm = place(p.z, p.ldz, p.z_dt),
-                      dm = place(p.d, p.ldd, p.d_dt);
-      float scale = i.blocks ? p.alpha : 0.f, bias = 0.f;
-      if constexpr (!kWeights) {
-        if (p.set_scale && i.blocks) scale *= __ldg(p.set_scale + i.e);
+    constexpr int kNext = 2 * kGroupedChunk;     // from one of this warp's chunks to the next
+    // The accumulator's columns have been read.  (The arrival hands over nothing but these, whose
+    // loads have completed; the pair's leader may be the other CTA.)
+    const auto release = [&]() {
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) {
+        if constexpr (CG == 1) mbar_arrive(tempty0 + 8u * acc);
+        else mbar_arrive_cluster_relaxed(map_to_rank(tempty0 + 8u * acc, 0));
       }
-      if constexpr (kFull) {
-        if (mine && i.e >= 0) {
-          const long long at = (long long)i.e * p.feats + f;
-          if (p.col_scale && i.blocks) scale *= __ldg(p.col_scale + at);
-          if (p.bias) bias = p.bias_dt == DT_F32 ? __ldg(static_cast<const float*>(p.bias) + at)
-                             : p.bias_dt == DT_F16
-                                 ? __half2float(__ushort_as_half(__ldg(static_cast<const uint16_t*>(p.bias) + at)))
-                                 : __uint_as_float((uint32_t)__ldg(static_cast<const uint16_t*>(p.bias) + at) << 16);
+    };
+    if constexpr (LEAN >= 0) {
+      constexpr int ES = elem_size(LEAN), W = ES == 4 ? 16 : 8;    // words of 16 columns
+      constexpr int PER = 16 / W;                // columns from one of a lane's words to the next
+      const uint32_t second = PER == 2 ? odd : 0u;
+      // An item and this lane's place in it.
+      struct At {
+        Item i;
+        bool mine;
+        float scale;
+        const uint8_t* r;
+        uint8_t* d;
+      };
+      const long long d_step = p.ldd * ES, r_step = p.ldr * ES;
+      const auto at_item = [&](int it) {
+        At t;
+        t.i = item_at(it);
+        const int f = t.i.f0 + (int)rank * 128 + q * 32 + lane;
+        t.mine = f < p.feats;
+        const long long group = kWeights ? (long long)t.i.g * p.sd : 0ll;
+        const long long row = t.i.t0 + second, col = PER == 2 ? f & ~1 : f;
+        t.r = static_cast<const uint8_t*>(p.r) + (group + row * p.ldr + col) * ES;
+        t.d = static_cast<uint8_t*>(p.d) + (group + row * p.ldd + col) * ES;
+        t.scale = t.i.blocks ? p.alpha : 0.f;
+        if constexpr (!kWeights) {
+          if (p.set_scale && t.i.blocks) t.scale *= __ldg(p.set_scale + t.i.e);
         }
-      }
-      // Chunks of 32 columns, every other one this warp's; which warp of the two starts
-      // alternates, so that items of one chunk are shared out.  The residual of the first
-      // two chunks (the first, of 32 bits) and the first's row factors (one a lane) are on their
-      // way before the accumulator is waited for, the others two chunks (one) ahead.
-      constexpr int kNext = 2 * kGroupedChunk;
-      uint32_t res[32];
-      float factor = 1.f;
-      const auto fetch_32 = [&](int c) {
-        epi_load<0>(rm, c, i.valid - c, pairs, mine, odd, res);
-        if (c + 16 < i.valid) epi_load<16>(rm, c + 16, i.valid - c - 16, pairs, mine, odd, res);
+        return t;
       };
-      const auto fetch_16 = [&](auto from, int c) {
+      // The residual's words of 16 columns, `left` of them there, from `at` on.
+      uint32_t res[2 * W];
+      const auto fetch = [&](auto from, const uint8_t* at, int left) {
         constexpr int FROM = decltype(from)::value;
-        epi_load<FROM>(rm, c, i.valid - c, pairs, mine, odd, res);
-        if (c + 16 < i.valid) epi_load<FROM + 8>(rm, c + 16, i.valid - c - 16, pairs, mine, odd, res);
-      };
-      const auto fetch_factor = [&](int c) {
-        if constexpr (kFull) {
-          if (p.row_scale && i.blocks > 0)
-            factor = c + lane < i.valid ? __ldg(p.row_scale + i.t0 + c + lane) : 1.f;
+#pragma unroll
+        for (int x = 0; x < W; ++x, at += PER * r_step) {
+          res[FROM + x] = 0u;
+          if (PER * x + (int)second < left) res[FROM + x] = *reinterpret_cast<const uint32_t*>(at);
         }
       };
-      // The next item's residual into L2, a token a lane (a warp's 32 features of one are 64 or
-      // 128 bytes): 8191 x 8192 of inner size 64 XXX us, XXX without.
-      if (p.r && it + num_clusters < num_items) {
-        const Item next = peek(it + num_clusters);
-        const long long f_next = next.f0 + (int)rank * 128 + q * 32;
-        if (f_next < p.feats) {
-          const uint8_t* const at = static_cast<const uint8_t*>(p.r) +
-              ((kWeights ? (long long)next.g * p.sd : 0ll) + f_next) * bytes(p.r_dt);
-          for (int c = strm * 32 + lane; c < next.valid; c += 64)
-            prefetch_l2(at + (next.t0 + c) * rm.step);
-        }
-      }
-      const int c_first = (strm ^ turn) * kGroupedChunk;
-      if (c_first < i.valid) {
+      At t{};
+      if (cluster_id < num_items) {
+        t = at_item(cluster_id);
+        const int c = strm * kGroupedChunk;
         if (p.r) {
-          if (r16) {
-            fetch_16(IntC<0>{}, c_first);
-            if (c_first + kNext < i.valid) fetch_16(IntC<16>{}, c_first + kNext);
-          } else {
-            fetch_32(c_first);
-          }
+          fetch(IntC<0>{}, t.r + c * r_step, t.mine ? t.i.valid - c : 0);
+          fetch(IntC<W>{}, t.r + (c + 16) * r_step, t.mine ? t.i.valid - c - 16 : 0);
         }
-        fetch_factor(c_first);
       }
-      if (!__all_sync(0xFFFFFFFFu, wait_phase(tfull0 + 8u * acc, aph, w, kWaitEpilogue))) break;
-      tc_fence_after_sync();
-      // (What the arrival hands over is the accumulator, whose loads have completed; the
-      // pair's leader may be the other CTA.)
-      const auto release = [&]() {
-        tc_fence_before_sync();
-        __syncwarp();
-        if (lane == 0) {
-          if constexpr (CG == 1) mbar_arrive(tempty0 + 8u * acc);
-          else mbar_arrive_cluster_relaxed(map_to_rank(tempty0 + 8u * acc, 0));
-        }
-      };
-      if (c_first >= i.valid) release();
-      const uint32_t tbase = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)acc * kAccStride;
-#pragma unroll 1
-      for (int c = c_first; c < i.valid; c += kNext) {
-        uint32_t a[kGroupedChunk];
-        __syncwarp();
-        tmem_load_32cols(tbase + c, a);
-        tmem_wait_ld(a);
-        if (c + kNext >= i.valid) release();
-        if (i.blocks == 0) {                     // (nothing was accumulated)
-#pragma unroll
-          for (int x = 0; x < kGroupedChunk; ++x) a[x] = 0u;
-        }
-        const auto half = [&](auto from) {
-          constexpr int FROM = decltype(from)::value;      // 0, 16
-          const int left = i.valid - c - FROM;
-          float v[16];
-#pragma unroll
-          for (int x = 0; x < 16; ++x) v[x] = __uint_as_float(a[FROM + x]) * scale;
-          if constexpr (kFull) {
-            if (p.row_scale) {
-#pragma unroll
-              for (int x = 0; x < 16; ++x) v[x] *= __shfl_sync(0xFFFFFFFFu, factor, FROM + x);
-            }
-            if (p.bias) {
-#pragma unroll
-              for (int x = 0; x < 16; ++x) v[x] += bias;
-            }
-            if (p.z) epi_store(zm, c + FROM, left, pairs, mine, odd, v);
-            with_activation(p.act, [&](auto act) {
-#pragma unroll
-              for (int x = 0; x < 16; x += 2) activate2<decltype(act)::value>(v[x], v[x + 1]);
-            });
+      for (int it = cluster_id; it < num_items; it += num_clusters, turn ^= 1) {
+        // The next item, its residual on its way into L2 (a token a lane: a warp's 32 features of one
+        // are 64 or 128 bytes).  A chunk's residual is requested into registers when
+        // those of the one before it have been used, across items.
+        At next{};
+        if (it + num_clusters < num_items) {
+          next = at_item(it + num_clusters);
+          const int f_first = next.i.f0 + (int)rank * 128 + q * 32;
+          if (p.r && f_first < p.feats) {
+            const uint8_t* const first =
+                static_cast<const uint8_t*>(p.r) + ((kWeights ? (long long)next.i.g * p.sd : 0ll) +
+                                                    (long long)next.i.t0 * p.ldr + f_first) * ES;
+            for (int c = strm * 32 + lane; c < next.i.valid; c += 64) prefetch_l2(first + c * r_step);
           }
+        }
+        const Item& i = t.i;
+        // (debug build: what is stored lies inside d)
+        if (!dbg_check(i.f0 >= 0 && i.t0 >= 0 && i.valid <= i.width &&
+                           i.t0 + i.valid <= (kWeights ? p.cols : p.rows),
+                       kChkEpiStore, w))
+          break;
+        const int next_c = (strm ^ turn ^ 1) * kGroupedChunk;
+        int c = (strm ^ turn) * kGroupedChunk;
+        if (!__all_sync(0xFFFFFFFFu, wait_phase(tfull0 + 8u * acc, aph, w, kWaitEpilogue))) break;
+        tc_fence_after_sync();
+        if (c >= i.valid) {                      // no chunk of this item is this warp's
+          release();
           if (p.r) {
-            if (r16) epi_add<FROM / 2>(rm, pairs, odd, res, v);
-            else epi_add<FROM>(rm, pairs, odd, res, v);
+            fetch(IntC<0>{}, next.r + next_c * r_step, next.mine ? next.i.valid - next_c : 0);
+            fetch(IntC<W>{}, next.r + (next_c + 16) * r_step, next.mine ? next.i.valid - next_c - 16 : 0);
           }
-          epi_store(dm, c + FROM, left, pairs, mine, odd, v);
+        }
+        const uint32_t tbase = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)acc * kAccStride;
+#pragma unroll 1
+        for (; c < i.valid; c += kNext) {
+          uint32_t a[kGroupedChunk];
+          __syncwarp();
+          tmem_load_32cols(tbase + c, a);
+          tmem_wait_ld(a);
+          const bool last = c + kNext >= i.valid;
+          if (last) release();
+          if (i.blocks == 0) {                   // (nothing was accumulated)
+#pragma unroll
+            for (int x = 0; x < kGroupedChunk; ++x) a[x] = 0u;
+          }
+          // where the next chunk's residual lies
+          const uint8_t* const follow = last ? next.r + next_c * r_step : t.r + (c + kNext) * r_step;
+          const int follow_left = last ? (next.mine ? next.i.valid - next_c : 0)
+                                       : (t.mine ? i.valid - c - kNext : 0);
+          const auto half = [&](auto number) {
+            constexpr int H = decltype(number)::value;
+            float v[16];
+#pragma unroll
+            for (int x = 0; x < 16; ++x) v[x] = __uint_as_float(a[16 * H + x]) * t.scale;
+            if (p.r) {
+#pragma unroll
+              for (int x = 0; x < W; ++x) {
+                if constexpr (LEAN == DT_F32) {
+                  v[x] += __uint_as_float(res[W * H + x]);
+                } else {
+                  const uint32_t u = swap_halves(res[W * H + x], odd);
+                  const float2 e = LEAN == DT_F16 ? unpack_f16x2(u) : unpack_bf16x2(u);
+                  v[2 * x] += e.x;
+                  v[2 * x + 1] += e.y;
+                }
+              }
+              fetch(IntC<W * H>{}, follow + 16 * H * r_step, follow_left - 16 * H);
+            }
+            const int left = t.mine ? i.valid - c - 16 * H - (int)second : 0;
+            uint8_t* p_d = t.d + (c + 16 * H) * d_step;
+#pragma unroll
+            for (int x = 0; x < W; ++x, p_d += PER * d_step) {
+              uint32_t o;
+              if constexpr (LEAN == DT_F32) o = __float_as_uint(v[x]);
+              else o = swap_halves(LEAN == DT_F16 ? pack_f16x2(v[2 * x], v[2 * x + 1])
+                                                  : pack_bf16x2(v[2 * x], v[2 * x + 1]), odd);
+              if (PER * x < left) *reinterpret_cast<uint32_t*>(p_d) = o;
+            }
+          };
+          half(IntC<0>{});
+          half(IntC<1>{});
+        }
+        t = next;
+        if (++acc == kAccStages) { acc = 0; aph ^= 1u; }
+      }
+    } else {
+      const auto bytes = [](int dt) { return dt == DT_F32 ? 4 : 2; };
+      const bool r16 = p.r_dt != DT_F32;
+      for (int it = cluster_id; it < num_items; it += num_clusters, turn ^= 1) {
+        const Item i = item_at(it);
+        const int f = i.f0 + (int)rank * 128 + q * 32 + lane;
+        const bool mine = f < p.feats;
+        const bool pairs = !(p.feats & 1) || !__any_sync(0xFFFFFFFFu, f + 1 == p.feats);
+        // (debug build: what is stored lies inside d)
+        if (!dbg_check(i.f0 >= 0 && i.t0 >= 0 && i.valid <= i.width &&
+                           i.t0 + i.valid <= (kWeights ? p.cols : p.rows),
+                       kChkEpiStore, w))
+          break;
+        const auto place = [&](const void* base, long long ld, int dt) {
+          uint8_t* const row = static_cast<uint8_t*>(const_cast<void*>(base)) +
+                               ((kWeights ? (long long)i.g * p.sd : 0ll) + (long long)i.t0 * ld) * bytes(dt);
+          return EpiMatrix{row + (long long)f * bytes(dt),
+                           row + (long long)(f & ~1) * bytes(dt) + (odd ? ld * bytes(dt) : 0ll),
+                           ld * bytes(dt), dt};
         };
-        half(IntC<0>{});
-        if (c + 16 < i.valid) half(IntC<16>{});
-        if (c + kNext < i.valid) {
+        const EpiMatrix rm = place(p.r, p.ldr, p.r_dt), zm = place(p.z, p.ldz, p.z_dt),
+                        dm = place(p.d, p.ldd, p.d_dt);
+        float scale = i.blocks ? p.alpha : 0.f, bias = 0.f;
+        if constexpr (!kWeights) {
+          if (p.set_scale && i.blocks) scale *= __ldg(p.set_scale + i.e);
+        }
+        if constexpr (kFull) {
+          if (mine && i.e >= 0) {
+            const long long at = (long long)i.e * p.feats + f;
+            if (p.col_scale && i.blocks) scale *= __ldg(p.col_scale + at);
+            if (p.bias) bias = p.bias_dt == DT_F32 ? __ldg(static_cast<const float*>(p.bias) + at)
+                               : p.bias_dt == DT_F16
+                                   ? __half2float(__ushort_as_half(__ldg(static_cast<const uint16_t*>(p.bias) + at)))
+                                   : __uint_as_float((uint32_t)__ldg(static_cast<const uint16_t*>(p.bias) + at) << 16);
+          }
+        }
+        // Chunks of 32 columns, every other one this warp's; which warp of the two starts
+        // alternates, so that items of one chunk are shared out.  The residual of the first
+        // two chunks (the first, of 32 bits) and the first's row factors (one a lane) are on their
+        // way before the accumulator is waited for, the others two chunks (one) ahead.
+        uint32_t res[32];
+        float factor = 1.f;
+        const auto fetch_32 = [&](int c) {
+          epi_load<0>(rm, c, i.valid - c, pairs, mine, odd, res);
+          if (c + 16 < i.valid) epi_load<16>(rm, c + 16, i.valid - c - 16, pairs, mine, odd, res);
+        };
+        const auto fetch_16 = [&](auto from, int c) {
+          constexpr int FROM = decltype(from)::value;
+          epi_load<FROM>(rm, c, i.valid - c, pairs, mine, odd, res);
+          if (c + 16 < i.valid) epi_load<FROM + 8>(rm, c + 16, i.valid - c - 16, pairs, mine, odd, res);
+        };
+        const auto fetch_factor = [&](int c) {
+          if constexpr (kFull) {
+            if (p.row_scale && i.blocks > 0)
+              factor = c + lane < i.valid ? __ldg(p.row_scale + i.t0 + c + lane) : 1.f;
+          }
+        };
+        const int c_first = (strm ^ turn) * kGroupedChunk;
+        if (c_first < i.valid) {
           if (p.r) {
             if (r16) {
-#pragma unroll
-              for (int x = 0; x < 16; ++x) res[x] = res[16 + x];
-              if (c + 2 * kNext < i.valid) fetch_16(IntC<16>{}, c + 2 * kNext);
+              fetch_16(IntC<0>{}, c_first);
+              if (c_first + kNext < i.valid) fetch_16(IntC<16>{}, c_first + kNext);
             } else {
-              fetch_32(c + kNext);
+              fetch_32(c_first);
             }
           }
-          fetch_factor(c + kNext);
+          fetch_factor(c_first);
         }
+        if (!__all_sync(0xFFFFFFFFu, wait_phase(tfull0 + 8u * acc, aph, w, kWaitEpilogue))) break;
+        tc_fence_after_sync();
+        if (c_first >= i.valid) release();
+        const uint32_t tbase = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)acc * kAccStride;
+#pragma unroll 1
+        for (int c = c_first; c < i.valid; c += kNext) {
+          uint32_t a[kGroupedChunk];
+          __syncwarp();
+          tmem_load_32cols(tbase + c, a);
+          tmem_wait_ld(a);
+          if (c + kNext >= i.valid) release();
+          if (i.blocks == 0) {                     // (nothing was accumulated)
+#pragma unroll
+            for (int x = 0; x < kGroupedChunk; ++x) a[x] = 0u;
+          }
+          const auto half = [&](auto from) {
+            constexpr int FROM = decltype(from)::value;      // 0, 16
+            const int left = i.valid - c - FROM;
+            float v[16];
+#pragma unroll
+            for (int x = 0; x < 16; ++x) v[x] = __uint_as_float(a[FROM + x]) * scale;
+            if constexpr (kFull) {
+              if (p.row_scale) {
+#pragma unroll
+                for (int x = 0; x < 16; ++x) v[x] *= __shfl_sync(0xFFFFFFFFu, factor, FROM + x);
+              }
+              if (p.bias) {
+#pragma unroll
+                for (int x = 0; x < 16; ++x) v[x] += bias;
+              }
+              if (p.z) epi_store(zm, c + FROM, left, pairs, mine, odd, v);
+              with_activation(p.act, [&](auto act) {
+#pragma unroll
+                for (int x = 0; x < 16; x += 2) activate2<decltype(act)::value>(v[x], v[x + 1]);
+              });
+            }
+            if (p.r) {
+              if (r16) epi_add<FROM / 2>(rm, pairs, odd, res, v);
+              else epi_add<FROM>(rm, pairs, odd, res, v);
+            }
+            epi_store(dm, c + FROM, left, pairs, mine, odd, v);
+          };
+          half(IntC<0>{});
+          if (c + 16 < i.valid) half(IntC<16>{});
+          if (c + kNext < i.valid) {
+            if (p.r) {
+              if (r16) {
+#pragma unroll
+                for (int x = 0; x < 16; ++x) res[x] = res[16 + x];
+                if (c + 2 * kNext < i.valid) fetch_16(IntC<16>{}, c + 2 * kNext);
+              } else {
+                fetch_32(c + kNext);
+              }
+            }
+            fetch_factor(c + kNext);
+          }
+        }
+        if (++acc == kAccStages) { acc = 0; aph ^= 1u; }
       }
-      if (++acc == kAccStages) { acc = 0; aph ^= 1u; }
     }
   } else {
     // ---------------------------------------------------------- zeroing (weights form)

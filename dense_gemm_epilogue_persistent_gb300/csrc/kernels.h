@@ -92,19 +92,21 @@ inline const void* linear_kernel_for(int ab_bytes, int cta_group, int ka, int ep
 // kern_split.cu: the linear layer's split-K kernel, by input width.
 const void* split_kernel_for(int ab_bytes);
 
-// kern_grouped.cu, compiled once per input width: products over groups of rows, by
-// CTA group and form (of the rows; at 16 bits also of the rows with a plain epilogue and of the
-// weights).
-#define GB300_GROUPED_NAME_(ab) kernel_grouped_ab##ab
-#define GB300_GROUPED_NAME(ab) GB300_GROUPED_NAME_(ab)
-const void* GB300_GROUPED_NAME(2)(int cta_group, int form);
-const void* GB300_GROUPED_NAME(1)(int cta_group, int form);
-const void* GB300_GROUPED_NAME(4)(int cta_group, int form);
-inline const void* grouped_kernel_for(int ab_bytes, int cta_group, int form) {
+// kern_grouped.cu, compiled once per input width and form: products over groups of rows, of
+// the rows (weights = 0) or of the weights (1; 16 bits), by CTA group and the type of the lean
+// epilogue (16 bits; -1: the whole one).
+#define GB300_GROUPED_NAME_(ab, weights) kernel_grouped_ab##ab##_w##weights
+#define GB300_GROUPED_NAME(ab, weights) GB300_GROUPED_NAME_(ab, weights)
+const void* GB300_GROUPED_NAME(2, 0)(int cta_group, int lean);
+const void* GB300_GROUPED_NAME(2, 1)(int cta_group, int lean);
+const void* GB300_GROUPED_NAME(1, 0)(int cta_group, int lean);
+const void* GB300_GROUPED_NAME(4, 0)(int cta_group, int lean);
+inline const void* grouped_kernel_for(int ab_bytes, int cta_group, bool weights, int lean) {
+  if (weights) return ab_bytes == 2 ? GB300_GROUPED_NAME(2, 1)(cta_group, lean) : nullptr;
   switch (ab_bytes) {
-    case 2: return GB300_GROUPED_NAME(2)(cta_group, form);
-    case 1: return GB300_GROUPED_NAME(1)(cta_group, form);
-    case 4: return GB300_GROUPED_NAME(4)(cta_group, form);
+    case 2: return GB300_GROUPED_NAME(2, 0)(cta_group, lean);
+    case 1: return GB300_GROUPED_NAME(1, 0)(cta_group, lean);
+    case 4: return GB300_GROUPED_NAME(4, 0)(cta_group, lean);
   }
   return nullptr;
 }
