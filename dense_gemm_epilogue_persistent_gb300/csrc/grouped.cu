@@ -5,6 +5,7 @@
 #include <cstdint>
 #include <cstring>
 
+#include "adapters_few.cuh"
 #include "gemm_gb300.h"
 #include "grouped_kernel.cuh"
 #include "handle.h"
@@ -339,6 +340,62 @@ gemm_status_t check_grouped_bwd(const gemm_grouped_linear_bwd_t& p) {
   return GEMM_OK;
 }
 
+// Blocks that share a request's rows in the kernels for few of them.
+int few_splits(const gemm_adapters_t& p) {
+  return (int)std::min<int64_t>(4, std::max<int64_t>(1, p.M - p.requests + 1));
+}
+
+// Whether a call takes these (adapters_few.cuh) rather than products over groups: by estimates of
+// both, microseconds, fitted on GB300 to 1 to 256 requests of 1 to 16 rows, ranks 16 to 128, 1024^2
+// to 8192^2.  The first grow with the rows' weights and, since the host does not know whose the
+// rows are, with those that one request may have alone; the second with the inner size and
+// the tiles, of which every request has its own.  (Few, products: 64 requests of a row, 4096 x
+// 4096, rank 16 10.3, 36.2; rank 128 30.6, 37.9; of 2 rows, rank 64 30.2, 37.2; 256 requests of a row,
+// rank 16 18.8, 99.8; one request of 16 rows 13.4, 20.5.  255 requests of a row and one of 769, which
+// the choice has to keep from them: 672, 112.)
+bool few_rows(const gemm_adapters_t& p) {
+  const double row = (double)p.rank * (double)(p.K + p.N);
+  const double few = 7.0 + 0.36e-6 * (double)p.M * row +
+                     0.9 * (double)std::max<int64_t>(0, p.M - p.requests) / few_splits(p);
+  const double tiles = (double)std::min(p.requests, p.M) * (double)cdiv(p.N, 128);
+  const double products = 11.0 + 0.0021 * (double)p.K + 1.35 / 152.0 * tiles;
+  return few < products;
+}
+
+// The second kernel by the lanes that a row of `rank` elements feeds.
+template <int DT>
+void (*up_kernel(int64_t rank))(gb300::FewParams) {
+  return rank <= 8 ? gb300::adapters_up_kernel<DT, 1> : rank <= 16 ? gb300::adapters_up_kernel<DT, 2>
+         : rank <= 32 ? gb300::adapters_up_kernel<DT, 4> : gb300::adapters_up_kernel<DT, 8>;
+}
+
+gemm_status_t run_few(const gemm_adapters_t& p, struct CUstream_st* stream) {
+  gb300::FewParams k{};
+  k.M = (int)p.M; k.N = (int)p.N; k.K = (int)p.K; k.rank = (int)p.rank;
+  k.requests = (int)p.requests; k.adapters = (int)p.adapters;
+  k.offsets = p.offsets; k.index = p.index;
+  k.x = p.x; k.ldx = p.ldx;
+  k.a = p.A; k.lda = p.lda; k.stride_a = p.strideA;
+  k.b = p.B; k.ldb = p.ldb; k.stride_b = p.strideB;
+  k.scale = p.scale;
+  k.u = p.u; k.ldu = p.ldu;
+  k.r = p.r; k.ldr = p.ldr; k.r_dt = device_dt(p.r_type);
+  k.d = p.d; k.ldd = p.ldd; k.d_dt = device_dt(p.d_type);
+  k.in_place = p.r == p.d;
+  k.splits = few_splits(p);
+  const int64_t ranks = cdiv(p.rank, gb300::kFewRanks), feats = cdiv(p.N, gb300::kFewThreads);
+  const int64_t blocks = p.requests * k.splits;
+  if (std::max(ranks, feats) * blocks > INT32_MAX) return GEMM_ERR_INVALID_ARG;
+  const bool f16 = p.type == GEMM_F16;
+  k.chunks = (int)ranks;
+  GB300_CHECK(launch(f16 ? gb300::adapters_down_kernel<gb300::DT_F16>
+                         : gb300::adapters_down_kernel<gb300::DT_BF16>,
+                     k, blocks * ranks, gb300::kFewThreads, 0, stream));
+  k.chunks = (int)feats;
+  return launch(f16 ? up_kernel<gb300::DT_F16>(p.rank) : up_kernel<gb300::DT_BF16>(p.rank), k,
+                blocks * feats, gb300::kFewThreads, 0, stream);
+}
+
 gemm_status_t check_adapters(const gemm_adapters_t& p) {
   if (!is_extent(p.M) || !is_extent(p.N) || !is_extent(p.K) || !is_extent(p.rank) ||
       !is_count(p.requests) || !is_count(p.adapters))
@@ -443,6 +500,8 @@ GEMM_API gemm_status_t gemm_adapters(gemm_handle_t h, const gemm_adapters_t* pp,
   if (!on_device(h)) return GEMM_ERR_INVALID_ARG;
   if (p.M == 0 || p.N == 0 || p.requests == 0) return GEMM_OK;
   const bool any = p.rank > 0 && p.adapters > 0;
+  std::lock_guard<std::mutex> guard(h->mu);
+  if (any && p.K > 0 && few_rows(p) && !h->forced) return run_few(p, stream);
   Product down, up;
   down.rows = p.M; down.feats = p.rank; down.k = p.K; down.groups = p.requests;
   down.sets = p.adapters;
@@ -464,7 +523,6 @@ GEMM_API gemm_status_t gemm_adapters(gemm_handle_t h, const gemm_adapters_t* pp,
   up.k_params.r = p.r; up.k_params.ldr = p.ldr; up.k_params.r_dt = p.r_type;
   up.k_params.d = p.d; up.k_params.ldd = p.ldd; up.k_params.d_dt = p.d_type;
   up.k_params.skip_none = p.r == p.d;
-  std::lock_guard<std::mutex> guard(h->mu);
   GroupedPlan plan_down, plan_up;
   if (any) GB300_CHECK(plan_grouped(h, down, plan_down));
   GB300_CHECK(plan_grouped(h, up, plan_up));

@@ -29,6 +29,18 @@ __device__ __forceinline__ void store_elem(void* p, long long i, int dt, float v
   else static_cast<uint16_t*>(p)[i] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
 }
 
+// Element i of p, of a type known when compiled or at run time.
+template <int DT>
+__device__ __forceinline__ float load_elem(const void* p, long long i) {
+  if constexpr (DT == DT_F32) return static_cast<const float*>(p)[i];
+  const uint16_t b = static_cast<const uint16_t*>(p)[i];
+  return DT == DT_F16 ? __half2float(__ushort_as_half(b)) : __uint_as_float((uint32_t)b << 16);
+}
+__device__ __forceinline__ float load_elem_dt(const void* p, long long i, int dt) {
+  return dt == DT_F32 ? load_elem<DT_F32>(p, i)
+                      : dt == DT_F16 ? load_elem<DT_F16>(p, i) : load_elem<DT_BF16>(p, i);
+}
+
 // The raw bits of one vector of type DT, so that loads can be issued well
 // before their values are converted.
 template <int DT>

@@ -132,6 +132,56 @@ def test_adapters(gemm, sizes, n, N, K, rank, t):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("cfg", [dict(cta_group=1), dict(cta_group=2), dict(cta_group=1, tile_n=128)])
+@pytest.mark.parametrize("sizes,n,N,K,rank", [([1] * 40, 5, 520, 264, 16), ([1, 0, 3, 9], 2, 73, 77, 9),
+                                              ([5, 1, 200, 0, 31], 4, 264, 130, 12)])
+def test_adapters_on_the_matrix_units(gemm, cfg, sizes, n, N, K, rank):
+    """Whatever the number of rows: a forced configuration takes the products over groups."""
+    gemm.set_config(**cfg)
+    try:
+        index = [(3 * i) % (n + 1) - 1 for i in range(len(sizes))]
+        for t, r_t, d_t in (("f16", "f16", "f16"), ("bf16", "f32", "bf16"), ("f16", None, "f32")):
+            _check(gemm, sizes, index, n, N, K, rank, t, r_t=r_t, d_t=d_t, behind=2)
+    finally:
+        gemm.set_config(None)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("sizes", [[1] * 5, [0, 0, 4, 0], [2, 1, 0, 4], [5, 3, 4], [0] * 9 + [19], [13, 0, 0, 1]])
+@pytest.mark.parametrize("N,K,rank", [(8, 8, 1), (300, 129, 7), (513, 4200, 16), (264, 520, 40),
+                                      (100, 1000, 300), (257, 9000, 33)])
+def test_adapters_of_few_rows(gemm, sizes, N, K, rank):
+    """Few rows, of uneven shares: kernels of their own."""
+    index = [(2 * i) % 4 - 1 for i in range(len(sizes))]
+    _check(gemm, sizes, index, 3, N, K, rank, "f16", r_t="bf16", d_t="f32", before=1)
+    _check(gemm, sizes, index, 3, N, K, rank, "bf16", r_t="bf16", d_t="bf16", in_place=True, behind=2)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("offsets", [[-5, 3, 7], [0, 9, 4], [10, 4, 4], [6, 2, 8],
+                                     [1 << 30, -(1 << 31), (1 << 31) - 1]])
+def test_adapters_offsets_out_of_range(gemm, offsets):
+    M, N, K, rank = 8, 72, 64, 8
+    gen = torch.Generator().manual_seed(5)
+    x, X = _operand(gen, M, K, "f16")
+    a, A = _weights(gen, 2, rank, K, "f16", scale=K ** -0.5)
+    b, Bd = _weights(gen, 2, N, rank, "f16")
+    for cfg in (None, dict(cta_group=1)):
+        d, u = O.strided(torch.full((M, N), NAN), "f32"), O.strided(torch.zeros(M, rank), "f16")
+        gemm.set_config(**cfg) if cfg else gemm.set_config(None)
+        try:
+            gemm.adapters(X, A, Bd, _i32(offsets), _i32([0, 1]), u[0], d[0])
+            assert gemm.sync_status()[0] == G.GEMM_OK
+        finally:
+            gemm.set_config(None)
+        clamped = [min(max(o, 0), M) for o in offsets]
+        rest = torch.ones(M, dtype=torch.bool)
+        for g in range(2):
+            rest[clamped[g]:max(clamped[g], clamped[g + 1])] = False
+        assert torch.equal(torch.isnan(O.f64(d[0])).all(dim=1), rest) and O.padding_untouched(*d)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("index", [[-1, -1], [7, 1 << 30], [-(1 << 31), 0]])
 def test_requests_without_an_adapter(gemm, index):
     for r_t, in_place in (("bf16", False), ("bf16", True), (None, False)):
