@@ -17,6 +17,7 @@ struct RouteParams {
   long long ldi;
   int n, k, E;               // choices, choices of a token, experts
   int share;                 // choices of a warp: a multiple of 32
+  int bits;                  // of an expert's number
   int* offsets;
   int* slot;
   int* source;
@@ -28,7 +29,8 @@ constexpr int kRouteAhead = 8;         // loads of 32 choices a warp has in flig
 
 // A stable counting sort in one launch of one cluster (or one block).  Every warp
 // owns a run of choices.  It counts them by expert, 32 at a time: lanes of one expert
-// find one another (match), and one of them adds their number to the warp's counter,
+// find one another by a vote on each bit of its number (65536 choices of 64 experts: XXX us, 19.7 with
+// match instructions), and one of them adds their number to the warp's counter,
 // so that no two lanes ever add to one counter and no atomic decides an order.  The
 // counters, summed over warps, blocks (through distributed shared memory) and
 // experts in that order, are the place of each warp's first choice of each expert; a
@@ -71,8 +73,18 @@ route_kernel(const __grid_constant__ RouteParams p) {
         if (i0 + 32 * u < count) f(i0 + 32 * u + lane, e[u]);
     }
   };
+  // The lanes whose choice is this lane's (those without one among themselves).
+  const auto alike = [&](int e) {
+    uint32_t same = __ballot_sync(0xFFFFFFFFu, e >= 0);
+    if (e < 0) same = ~same;
+    for (int b = 0; b < p.bits; ++b) {
+      const uint32_t ones = __ballot_sync(0xFFFFFFFFu, e >> b & 1);
+      same &= e >> b & 1 ? ones : ~ones;
+    }
+    return same;
+  };
   walk([&](int, int e) {
-    const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
+    const uint32_t same = alike(e);
     if (e >= 0 && lane == __ffs(same) - 1) counts[e] += __popc(same);
     __syncwarp();
   });
@@ -131,7 +143,7 @@ route_kernel(const __grid_constant__ RouteParams p) {
   }
   __syncthreads();
   walk([&](int i, int e) {
-    const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
+    const uint32_t same = alike(e);
     int place = -1;
     if (e >= 0) place = before[e] + counts[e] + __popc(same & ((1u << lane) - 1u));
     __syncwarp();
@@ -212,15 +224,18 @@ struct CombineParams {
   long long ldys, ldr, ldy;
   long long T, R;
   int k, H, lanes, pieces;
+  int piece;                 // elements of a piece (the ring's)
   int r_dt, y_dt;
+  uint32_t* status;          // (the ring's waits)
+  unsigned long long timeout_ns;
 };
 
 constexpr int kSumThreads = 128;
-constexpr int kSumRows = 4;            // rows whose loads a thread has in flight
 
-// y = r + sum over the choices, fp32, in order: a thread keeps VECS vectors of 8 columns
-// and has 4 rows' loads in flight; rows are shared out as above.
-template <int DT, int VECS>
+// y = r + sum over the choices, fp32, in order.  `lanes` threads (32 to 128) a row, VECS vectors of 8
+// columns each, ROWS rows' loads in flight; longer rows are cut into `pieces`, a block each.  For
+// batches whose time is latency.
+template <int DT, int VECS, int ROWS>
 __global__ void __launch_bounds__(kSumThreads)
 combine_kernel(const __grid_constant__ CombineParams p) {
   grid_launch_dependents();
@@ -242,25 +257,25 @@ combine_kernel(const __grid_constant__ CombineParams p) {
   }
   const int* const slot = p.slot + t * p.k;
   const float* const weight = p.weight ? p.weight + t * p.k : nullptr;
-  for (int j0 = 0; j0 < p.k; j0 += kSumRows) {
-    int s[kSumRows];
-    float w[kSumRows];
+  for (int j0 = 0; j0 < p.k; j0 += ROWS) {
+    int s[ROWS];
+    float w[ROWS];
 #pragma unroll
-    for (int u = 0; u < kSumRows; ++u) {
+    for (int u = 0; u < ROWS; ++u) {
       s[u] = j0 + u < p.k ? __ldg(slot + j0 + u) : -1;
       w[u] = weight && j0 + u < p.k ? __ldg(weight + j0 + u) : 1.f;
       if (s[u] >= p.R) s[u] = -1;
     }
-    RawVec<DT> v[kSumRows][VECS];
+    RawVec<DT> v[ROWS][VECS];
 #pragma unroll
-    for (int u = 0; u < kSumRows; ++u) {
+    for (int u = 0; u < ROWS; ++u) {
       const uint8_t* const row = static_cast<const uint8_t*>(p.ys) + (long long)s[u] * p.ldys * es;
 #pragma unroll
       for (int i = 0; i < VECS; ++i)
         if (s[u] >= 0 && c0 + i * step < p.H) v[u][i] = load_raw<DT>(row, c0 + i * step, p.H);
     }
 #pragma unroll
-    for (int u = 0; u < kSumRows; ++u) {
+    for (int u = 0; u < ROWS; ++u) {
       if (s[u] < 0) continue;
 #pragma unroll
       for (int i = 0; i < VECS; ++i) {
@@ -277,6 +292,180 @@ combine_kernel(const __grid_constant__ CombineParams p) {
     if (c0 + i * step < p.H)
       store_vec(static_cast<uint8_t*>(p.y) + t * p.ldy * elem_bytes(p.y_dt), p.y_dt, c0 + i * step,
                 p.H, acc[i]);
+}
+
+// The same for batches whose time is bandwidth.  A warp copies the choices' rows, pieces of up to 4 KB
+// (bulk copies), into a ring of kRingSlots; kRingWarps warps add them up, VECS vectors of 8 columns
+// a thread.  The copies run ahead of the sums by the whole ring, across tokens, and the
+// places and weights by a token more, so that no wait for an address leaves memory idle.  A block takes
+// about 700 cycles an entry, whatever its size, so that many small blocks an SM are wanted: 8192
+// tokens of 8 x 4096 bf16 with a residual 104 us (6.5 TB/s; 116 with loads into registers), 112 with
+// two blocks of twelve 8 KB slots; 4096 of 2 x 8192 42.5 (67.8), 61.8.
+struct RingEntry {           // what a slot holds
+  int row;                   // of ys; kResidual: the token's of r; -1: nothing (a token without choices)
+  float weight;
+  int flags;
+};
+constexpr int kResidual = -2;
+enum : int { kLastEntry = 1, kWholeEntry = 2 };  // the token's last; its last 16 bytes are all there
+constexpr int kRingSlots = 4, kRingWarps = 4, kRingBytes = 4096, kRingBlocks = 8;
+constexpr int kRingThreads = 32 * (kRingWarps + 1);
+constexpr int kRingSmem = kRingSlots * (kRingBytes + 16 + (int)sizeof(RingEntry)) + 16;
+
+template <int DT, int VECS>
+__global__ void __launch_bounds__(kRingThreads, kRingBlocks)
+combine_ring_kernel(const __grid_constant__ CombineParams p) {
+  constexpr int es = elem_bytes(DT);
+  static_assert(32 * kRingWarps * VECS * kVec * es == kRingBytes, "a piece fills a slot");
+  extern __shared__ __align__(16) uint8_t ring[];
+  const uint32_t bars = smem_u32(ring) + kRingSlots * kRingBytes;
+  RingEntry* const entries = reinterpret_cast<RingEntry*>(ring + kRingSlots * (kRingBytes + 16));
+  volatile uint32_t* const abort_ptr = reinterpret_cast<volatile uint32_t*>(entries + kRingSlots);
+  const auto full = [&](int s) { return bars + 16u * s; };
+  const auto empty = [&](int s) { return bars + 16u * s + 8u; };
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  grid_launch_dependents();
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kRingSlots; ++s) {
+      mbar_init(full(s), 1);
+      mbar_init(empty(s), kRingWarps);
+    }
+    *abort_ptr = 0u;
+    fence_barrier_init();
+  }
+  __syncthreads();
+  grid_dependency_wait();
+  const Watch w{abort_ptr, p.status, p.timeout_ns};
+  // This block's piece of the rows (of p.piece elements, the last one shorter), and its tokens.
+  const int piece = blockIdx.x % p.pieces;
+  const int c_first = piece * p.piece, c_end = min(p.H, c_first + p.piece);
+  // A residual of the rows' type comes through the ring too.
+  const bool r_ring = p.r && p.r_dt == DT;
+  const long long t_first = blockIdx.x / p.pieces, t_step = gridDim.x / p.pieces;
+  int s = 0;
+  uint32_t ph = 0;
+  const auto advance = [&]() {
+    if (++s == kRingSlots) { s = 0; ph ^= 1u; }
+  };
+  if (warp == kRingWarps) {
+    // choices [j0, j0 + 32) of an item's token, one a lane; -1: none
+    int row_next = -1;
+    float w_next = 1.f;
+    const auto look = [&](long long t, int j0) {
+      const int j = j0 + lane;
+      row_next = -1;
+      w_next = 1.f;
+      if (t < p.T && j < p.k) {
+        const long long at = t * p.k + j;
+        row_next = __ldg(p.slot + at);
+        if (p.weight) w_next = __ldg(p.weight + at);
+        if (row_next >= p.R) row_next = -1;
+      }
+    };
+    bool ok = true;
+    // One entry: a piece of a row, or none.
+    const uint32_t bytes_here = (uint32_t)((c_end - c_first) * es);
+    const auto push = [&](int row, float weight, bool last, long long t) {
+      ok = __all_sync(0xFFFFFFFFu, wait_phase<true>(empty(s), ph ^ 1u, w, kWaitProducer));
+      if (!ok) return;
+      if (lane == 0) {
+        // (Behind a matrix's last row there may be no more memory; behind another there is the next.)
+        const bool whole = row == kResidual ? t + 1 < p.T : row + 1 < p.R;
+        entries[s] = RingEntry{row, weight, (last ? kLastEntry : 0) | (whole ? kWholeEntry : 0)};
+        const uint32_t bytes = row == -1 ? 0u : (whole ? bytes_here + 15u : bytes_here) & ~15u;
+        mbar_arrive_expect_tx(full(s), bytes);
+        if (bytes)
+          bulk_load(smem_u32(ring) + s * kRingBytes,
+                    (row == kResidual ? static_cast<const uint8_t*>(p.r) + t * p.ldr * es
+                                      : static_cast<const uint8_t*>(p.ys) + (long long)row * p.ldys * es) +
+                        (long long)c_first * es,
+                    bytes, full(s));
+      }
+      __syncwarp();
+      advance();
+    };
+    look(t_first, 0);
+    for (long long t = t_first; ok && t < p.T; t += t_step) {
+      // (an entry is pushed when the next is known, so that the last can be marked)
+      int row = r_ring ? kResidual : -1;
+      bool have = r_ring;
+      float weight = 1.f;
+      for (int j0 = 0; ok && j0 < p.k; j0 += 32) {
+        const int row_now = row_next;
+        const float w_now = w_next;
+        if (j0 + 32 < p.k) look(t, j0 + 32);
+        else look(t + t_step, 0);
+        const uint32_t there = __ballot_sync(0xFFFFFFFFu, row_now >= 0);
+        for (uint32_t left = there; ok && left; left &= left - 1) {
+          const int j = __ffs(left) - 1;
+          if (have) push(row, weight, false, t);
+          row = __shfl_sync(0xFFFFFFFFu, row_now, j);
+          weight = __shfl_sync(0xFFFFFFFFu, w_now, j);
+          have = true;
+        }
+      }
+      if (ok) push(row, weight, true, t);
+    }
+  } else {
+    const int c0 = c_first + (int)threadIdx.x * kVec;
+    constexpr int step = 32 * kRingWarps * kVec;
+    for (long long t = t_first; t < p.T; t += t_step) {
+      float acc[VECS][kVec];
+#pragma unroll
+      for (int i = 0; i < VECS; ++i) {
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) acc[i][e] = 0.f;
+        if (p.r && !r_ring && c0 + i * step < c_end)
+          load_vec_dt(static_cast<const uint8_t*>(p.r) + t * p.ldr * elem_bytes(p.r_dt), p.r_dt,
+                      c0 + i * step, p.H, acc[i]);
+      }
+      bool last = false;
+      while (!last) {
+        if (!__all_sync(0xFFFFFFFFu, wait_phase<true>(full(s), ph, w, kWaitEpilogue))) break;
+        const RingEntry entry = entries[s];
+        last = entry.flags & kLastEntry;
+        if (entry.row != -1) {
+          const uint8_t* const slot = ring + s * kRingBytes;
+          const uint8_t* const row =
+              entry.row == kResidual ? static_cast<const uint8_t*>(p.r) + t * p.ldr * es
+                                     : static_cast<const uint8_t*>(p.ys) + (long long)entry.row * p.ldys * es;
+#pragma unroll
+          for (int i = 0; i < VECS; ++i) {
+            const int c = c0 + i * step;
+            if (c >= c_end) continue;
+            RawVec<DT> v;
+            if (c + kVec <= p.H || (entry.flags & kWholeEntry)) {
+              const uint4* const at = reinterpret_cast<const uint4*>(slot + (threadIdx.x * kVec + i * step) * es);
+              v.q[0] = at[0];
+              if constexpr (DT == DT_F32) v.q[1] = at[1];
+            } else {
+              v = load_raw<DT>(row, c, p.H);
+            }
+            float f[kVec];
+            unpack<DT>(v, f);
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) acc[i][e] = fmaf(entry.weight, f[e], acc[i][e]);
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(empty(s));
+        advance();
+      }
+      if (!last) break;                          // (a wait ran out)
+#pragma unroll
+      for (int i = 0; i < VECS; ++i)
+        if (c0 + i * step < c_end)
+          store_vec(static_cast<uint8_t*>(p.y) + t * p.ldy * elem_bytes(p.y_dt), p.y_dt,
+                    c0 + i * step, p.H, acc[i]);
+    }
+  }
+  __syncthreads();
+  if (*abort_ptr) {
+    // A wait gave up: let copies already issued drain first.
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 2000000ull) {
+    }
+  }
 }
 
 // ------------------------------------------------------------------ its gradients
@@ -486,6 +675,7 @@ GEMM_API gemm_status_t gemm_route(gemm_handle_t h, const gemm_route_t* pp,
                           : gb300::kRouteWarps;
   const int blocks = k.n > 2048 ? gb300::kRouteCluster : 1;
   const int warps = blocks > 1 ? fit : std::min(fit, std::max(4, (int)cdiv(k.n, 32)));
+  while ((1ll << k.bits) < p.E) ++k.bits;
   k.share = (int)cdiv(cdiv(k.n, (int64_t)blocks * warps), 32) * 32;
   const size_t smem = (size_t)(3 + warps) * p.E * 4;
   typedef void (*Kern)(gb300::RouteParams);
@@ -546,15 +736,34 @@ GEMM_API gemm_status_t gemm_combine(gemm_handle_t h, const gemm_combine_t* pp,
   k.slot = p.slot; k.weight = p.weight;
   k.T = p.T; k.R = p.R;
   k.k = (int)p.k; k.H = (int)p.H;
+  typedef void (*Kern)(gb300::CombineParams);
+  const int es = dtype_bytes(p.type);
+  // The ring from 4 KB a row and 32 MB on (8192 tokens of 8 x 512 bf16 36.6 us by the ring, 18.0
+  // without; 1024 of 8 x 4096 17.3, 17.7; 512 of 8 x 4096 9.5, 10.5).
+  if (p.H * es >= 4096 && (double)p.T * (double)p.k * (double)p.H * es >= 32e6) {
+    k.pieces = (int)cdiv(p.H, gb300::kRingBytes / es);
+    k.piece = (int)cdiv(cdiv(p.H, k.pieces), gb300::kVec) * gb300::kVec;
+    k.status = h->d_status;
+    k.timeout_ns = h->timeout_ns;
+    const Kern kern = p.type == GEMM_F32   ? (Kern)gb300::combine_ring_kernel<gb300::DT_F32, 1>
+                      : p.type == GEMM_F16 ? (Kern)gb300::combine_ring_kernel<gb300::DT_F16, 2>
+                                           : (Kern)gb300::combine_ring_kernel<gb300::DT_BF16, 2>;
+    {
+      std::lock_guard<std::mutex> guard(h->mu);
+      GB300_CHECK(raise_smem(h, reinterpret_cast<const void*>(kern)));
+    }
+    const int64_t blocks = std::max<int64_t>(1, gb300::kRingBlocks * h->sm_count / k.pieces);    // of a piece
+    return launch(kern, k, std::min(p.T, blocks) * k.pieces, gb300::kRingThreads, gb300::kRingSmem,
+                  stream);
+  }
   const int64_t vecs = cdiv(p.H, gb300::kVec);
   k.lanes = row_lanes(vecs, 2);
   k.pieces = (int)cdiv(vecs, (int64_t)k.lanes * 2);
   const int64_t grid = cdiv(p.T, gb300::kSumThreads / k.lanes) * k.pieces;
   if (grid > INT32_MAX) return GEMM_ERR_INVALID_ARG;
-  typedef void (*Kern)(gb300::CombineParams);
-  const Kern kern = p.type == GEMM_F32   ? (Kern)gb300::combine_kernel<gb300::DT_F32, 2>
-                    : p.type == GEMM_F16 ? (Kern)gb300::combine_kernel<gb300::DT_F16, 2>
-                                         : (Kern)gb300::combine_kernel<gb300::DT_BF16, 2>;
+  const Kern kern = p.type == GEMM_F32   ? (Kern)gb300::combine_kernel<gb300::DT_F32, 2, 2>
+                    : p.type == GEMM_F16 ? (Kern)gb300::combine_kernel<gb300::DT_F16, 2, 4>
+                                         : (Kern)gb300::combine_kernel<gb300::DT_BF16, 2, 4>;
   return launch(kern, k, grid, gb300::kSumThreads, 0, stream);
 }
 
@@ -588,8 +797,9 @@ GEMM_API gemm_status_t gemm_combine_bwd(gemm_handle_t h, const gemm_combine_bwd_
     return GEMM_OK;
   }
   const int64_t vecs = cdiv(p.H, gb300::kVec);
-  const int threads =
-      (int)std::min<int64_t>(gb300::kBwdThreads, cdiv(cdiv(vecs, gb300::kBwdVecs), 32) * 32);
+  // as few passes over the row as there can be, of one length
+  const int64_t passes = cdiv(vecs, (int64_t)gb300::kBwdThreads * gb300::kBwdVecs);
+  const int threads = (int)(cdiv(cdiv(vecs, gb300::kBwdVecs * passes), 32) * 32);
   typedef void (*Kern)(gb300::CombineBwdParams);
   const Kern kern = p.type == GEMM_F32   ? (Kern)gb300::combine_bwd_kernel<gb300::DT_F32>
                     : p.type == GEMM_F16 ? (Kern)gb300::combine_bwd_kernel<gb300::DT_F16>

@@ -317,6 +317,46 @@ def test_combine(gemm, T, k, H, t, r_t, y_t, weighted):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T,k,H,t,r_t,y_t,weighted", [
+    (1500, 3, 5003, "f16", "f16", "f16", True), (2100, 4, 2048, "bf16", "bf16", "f32", True),
+    (2000, 1, 9001, "bf16", None, "bf16", False), (600, 40, 1025, "f32", "f32", "f32", True),
+    (700, 6, 4100, "f16", "f32", "bf16", True), (410, 2, 20011, "bf16", "f16", "f16", False),
+    (301, 33, 2051, "f16", "f16", "f16", True)])
+def test_combine_of_large_batches(gemm, T, k, H, t, r_t, y_t, weighted):
+    """Those whose rows come through a ring: rows ending inside 16 bytes, the last row of each matrix
+    among the choices, tokens without any, more choices than lanes."""
+    gen = torch.Generator().manual_seed(T + k + H)
+    R = T * k + 1 - T // 3
+    slot = _places(gen, T, k, T * k).clamp(max=T * k)
+    slot[slot >= R] = R + 3
+    slot[1] = -1
+    slot[0, 0] = R - 1
+    ys = torch.randn(R, H, generator=gen).to(O.TYPES[t])
+    r = torch.randn(T, H, generator=gen).to(O.TYPES[r_t]) if r_t else None
+    weight = torch.randn(T, k, generator=gen) if weighted else None
+    there = (slot >= 0) & (slot < R)
+    if weighted:
+        weight[~there] = NAN
+    # no padding behind the last row: the buffer ends with it
+    tight = lambda v, n: torch.empty((n - 1) * ((H + 15) // 16 * 16) + H, dtype=v.dtype, device="cuda") \
+        .as_strided((n, H), ((H + 15) // 16 * 16, 1)).copy_(v)
+    Y = O.strided(torch.full((T, H), NAN), y_t)
+    gemm.combine(tight(ys, R), slot.int().cuda(), Y[0], weight=weight.cuda() if weighted else None,
+                 residual=tight(r, T) if r_t else None)
+    assert gemm.sync_status()[0] == G.GEMM_OK
+    want = r.double() if r_t else torch.zeros(T, H, dtype=torch.float64)
+    mag = want.abs()
+    for j in range(k):
+        w = (weight[:, j].double() if weighted else torch.ones(T, dtype=torch.float64))
+        w = torch.where(there[:, j], w, torch.zeros_like(w))[:, None]
+        rows = ys[slot[:, j].clamp(0, R - 1)].double()
+        want, mag = want + w * rows, mag + w.abs() * rows.abs()
+    e = mag * (k + 1) * O.U32
+    O.within(Y[0], want, e + O.rounding(want.abs() + e, y_t), "y")
+    assert O.padding_untouched(*Y)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("T,k,H", [(1, 8, 4096), (30, 3, 1001)])
 def test_combine_in_place_residual(gemm, T, k, H):
     gen = torch.Generator().manual_seed(1)
@@ -417,6 +457,26 @@ def test_infinities_and_nan_stay_in_their_rows(gemm):
     assert (dw[0] == 72).all() and dw[1, 0] == INF and dw[1, 1] == 72 and torch.isnan(dw[2, 0])
     assert dw[2, 1] == 72 and (dw[3] == INF).all()
     assert (dys[:6] == 1).all() and (dys[6:, 1] == INF).all() and (dys[6:, 2:] == 1).all()
+
+
+@pytest.mark.gpu
+def test_large_batches_repeat_bit_for_bit(gemm):
+    """The same sums by the ring and without it (a smaller batch of the same rows), and in place."""
+    T, k, H = 2000, 4, 2200
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    ys = torch.randn(T * k, H, generator=gen, device="cuda").bfloat16()
+    r = torch.randn(T, H, generator=gen, device="cuda").bfloat16()
+    w = torch.randn(T, k, generator=gen, device="cuda")
+    slot = torch.randperm(T * k, generator=gen, device="cuda").int().view(T, k)
+    outs = [torch.zeros_like(r) for _ in range(3)]
+    gemm.combine(ys, slot, outs[0], weight=w, residual=r)
+    for t in range(0, T, 500):
+        gemm.combine(ys, slot[t:t + 500], outs[1][t:t + 500], weight=w[t:t + 500],
+                     residual=r[t:t + 500])
+    outs[2].copy_(r)
+    gemm.combine(ys, slot, outs[2], weight=w, residual=outs[2])
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
 
 
 @pytest.mark.gpu
