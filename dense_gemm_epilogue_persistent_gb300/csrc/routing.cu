@@ -17,26 +17,27 @@ struct RouteParams {
   long long ldi;
   int n, k, E;               // choices, choices of a token, experts
   int share;                 // choices of a warp: a multiple of 32
-  int bits;                  // of an expert's number
   int* offsets;
   int* slot;
   int* source;
 };
 
 constexpr int kRouteWarps = 32;
-constexpr int kRouteCluster = 8;
+constexpr int kRouteCluster = 16;      // blocks, where the device takes so large a cluster; else 8
 constexpr int kRouteAhead = 8;         // loads of 32 choices a warp has in flight
 
 // A stable counting sort in one launch of one cluster (or one block).  Every warp
 // owns a run of choices.  It counts them by expert, 32 at a time: lanes of one expert
-// find one another by a vote on each bit of its number (65536 choices of 64 experts: XXX us, 19.7 with
-// match instructions), and one of them adds their number to the warp's counter,
-// so that no two lanes ever add to one counter and no atomic decides an order.  The
+// find one another by a vote on each of the BITS of its number, and one of them adds their
+// number to the warp's counter, so that no two lanes ever add to one counter and no
+// atomic decides an order; each choice's rank within the run is left in `slot`.  The
 // counters, summed over warps, blocks (through distributed shared memory) and
-// experts in that order, are the place of each warp's first choice of each expert; a
-// second walk over the choices hands the places out.  8 bytes a choice written, 8 to 16
-// read: latency of the two walks, not bandwidth, bounds it.
-template <typename T>
+// experts in that order, are the place of each warp's first choice of each expert, to
+// which a second walk adds the ranks.  8 bytes a choice written, 8 to 16 read: the latency of
+// the walks and sums, then the scattered stores of few SMs bound it.  (65536 choices of 64
+// experts: 10.0 us; 13.5 by eight blocks, 14.1 so with the votes in both walks, 19.7 with match
+// instructions there.)
+template <typename T, int BITS>
 __global__ void __launch_bounds__(32 * kRouteWarps)
 route_kernel(const __grid_constant__ RouteParams p) {
   extern __shared__ int route_smem[];
@@ -73,20 +74,22 @@ route_kernel(const __grid_constant__ RouteParams p) {
         if (i0 + 32 * u < count) f(i0 + 32 * u + lane, e[u]);
     }
   };
-  // The lanes whose choice is this lane's (those without one among themselves).
-  const auto alike = [&](int e) {
+  walk([&](int i, int e) {
+    // the lanes whose choice is this lane's (those without one among themselves)
     uint32_t same = __ballot_sync(0xFFFFFFFFu, e >= 0);
     if (e < 0) same = ~same;
-    for (int b = 0; b < p.bits; ++b) {
-      const uint32_t ones = __ballot_sync(0xFFFFFFFFu, e >> b & 1);
-      same &= e >> b & 1 ? ones : ~ones;
+#pragma unroll
+    for (int b = 0; b < BITS; ++b) {
+      const bool one = e >> b & 1;
+      const uint32_t ones = __ballot_sync(0xFFFFFFFFu, one);
+      same &= one ? ones : ~ones;
     }
-    return same;
-  };
-  walk([&](int, int e) {
-    const uint32_t same = alike(e);
-    if (e >= 0 && lane == __ffs(same) - 1) counts[e] += __popc(same);
+    const uint32_t ahead = same & ((1u << lane) - 1u);
+    const int so_far = e >= 0 ? counts[e] : 0;
     __syncwarp();
+    if (e >= 0 && ahead == 0) counts[e] = so_far + __popc(same);
+    __syncwarp();
+    if (i < count) p.slot[first + i] = so_far + __popc(ahead);
   });
   __syncthreads();
   for (int e = threadIdx.x; e < E; e += blockDim.x) {
@@ -142,18 +145,22 @@ route_kernel(const __grid_constant__ RouteParams p) {
     if (rank == 0 && threadIdx.x == 0) p.offsets[E] = total;
   }
   __syncthreads();
-  walk([&](int i, int e) {
-    const uint32_t same = alike(e);
-    int place = -1;
-    if (e >= 0) place = before[e] + counts[e] + __popc(same & ((1u << lane) - 1u));
-    __syncwarp();
-    if (e >= 0 && lane == __ffs(same) - 1) counts[e] += __popc(same);
-    __syncwarp();
-    if (i < count) {
-      p.slot[first + i] = place;
+  for (int i0 = 0; i0 < count; i0 += 32 * kRouteAhead) {
+    int e[kRouteAhead], rank[kRouteAhead];
+#pragma unroll
+    for (int u = 0; u < kRouteAhead; ++u) {
+      const int i = i0 + 32 * u + lane;
+      e[u] = expert(i);
+      rank[u] = i < count ? p.slot[first + i] : 0;
+    }
+#pragma unroll
+    for (int u = 0; u < kRouteAhead; ++u) {
+      const int i = i0 + 32 * u + lane;
+      const int place = e[u] >= 0 ? before[e[u]] + counts[e[u]] + rank[u] : -1;
+      if (i < count) p.slot[first + i] = place;
       if (p.source && place >= 0) p.source[place] = (int)(first + i);
     }
-  });
+  }
   if (blocks > 1) cluster_sync_all();            // the others have read this block's totals
 }
 
@@ -644,6 +651,44 @@ gemm_status_t check_combine_bwd(const gemm_combine_bwd_t& p) {
   return GEMM_OK;
 }
 
+template <typename T>
+void (*route_kernel(int bits))(gb300::RouteParams) {
+  return bits <= 3   ? gb300::route_kernel<T, 3>
+         : bits <= 6 ? gb300::route_kernel<T, 6>
+         : bits <= 8 ? gb300::route_kernel<T, 8>
+                     : gb300::route_kernel<T, 12>;
+}
+
+// Blocks of the sort's cluster (h->mu held): 16, which a kernel has to be allowed first, if one with as much
+// shared memory as any call asks for fits the device; else 8.
+gemm_status_t route_cluster(gemm_handle* h, void (*kern)(gb300::RouteParams), size_t smem, int* blocks) {
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) {
+    cudaGetLastError();
+    return GEMM_ERR_CUDA;
+  }
+  if (h->route_cluster == 0) {
+    int n = 0;
+    cudaLaunchConfig_t lc{};
+    cudaLaunchAttribute attr[1];
+    lc.gridDim = dim3((unsigned)gb300::kRouteCluster);
+    lc.blockDim = dim3(32 * gb300::kRouteWarps);
+    lc.dynamicSmemBytes = smem;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)gb300::kRouteCluster;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    lc.attrs = attr;
+    lc.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, kern, &lc) != cudaSuccess) {
+      cudaGetLastError();
+      n = 0;
+    }
+    h->route_cluster = n > 0 ? gb300::kRouteCluster : 8;
+  }
+  *blocks = h->route_cluster;
+  return GEMM_OK;
+}
+
 // Threads of a row (32, 64 or 128) that take `vecs` of its `total` vectors each.
 int row_lanes(int64_t total, int vecs) {
   int lanes = 32;
@@ -673,18 +718,19 @@ GEMM_API gemm_status_t gemm_route(gemm_handle_t h, const gemm_route_t* pp,
   const int room = (h->smem_optin - 2048) / 4;
   const int fit = p.E > 0 ? (int)std::min<int64_t>(gb300::kRouteWarps, (room - 3 * p.E) / p.E)
                           : gb300::kRouteWarps;
-  const int blocks = k.n > 2048 ? gb300::kRouteCluster : 1;
-  const int warps = blocks > 1 ? fit : std::min(fit, std::max(4, (int)cdiv(k.n, 32)));
-  while ((1ll << k.bits) < p.E) ++k.bits;
-  k.share = (int)cdiv(cdiv(k.n, (int64_t)blocks * warps), 32) * 32;
-  const size_t smem = (size_t)(3 + warps) * p.E * 4;
+  int bits = 0;
+  while ((1ll << bits) < p.E) ++bits;
   typedef void (*Kern)(gb300::RouteParams);
-  const Kern kern = p.index_bytes == 8 ? (Kern)gb300::route_kernel<long long>
-                                       : (Kern)gb300::route_kernel<int>;
+  const Kern kern = p.index_bytes == 8 ? route_kernel<long long>(bits) : route_kernel<int>(bits);
+  int blocks = 1;
   {
     std::lock_guard<std::mutex> guard(h->mu);
     GB300_CHECK(raise_smem(h, reinterpret_cast<const void*>(kern)));
+    if (k.n > 2048) GB300_CHECK(route_cluster(h, kern, (size_t)room * 4, &blocks));
   }
+  const int warps = blocks > 1 ? fit : std::min(fit, std::max(4, (int)cdiv(k.n, 32)));
+  k.share = (int)cdiv(cdiv(k.n, (int64_t)blocks * warps), 32) * 32;
+  const size_t smem = (size_t)(3 + warps) * p.E * 4;
   return launch(kern, k, blocks, 32 * warps, smem, stream, blocks);
 }
 
