@@ -683,16 +683,35 @@ def _integers(t, shape, what, device):
             raise _elsewhere(t, what, device)
     except AttributeError:
         pass
-    if str(t.dtype) != "torch.int32":
+    if _integer_bytes(t, what) != 4:
         raise GemmError(GEMM_ERR_UNSUPPORTED_DTYPE, f"{what}: {t.dtype}")
     _packed(t, shape, what)
     return t.data_ptr()
+
+
+_BYTES_OF = {}          # bytes of the integer dtypes, filled as they are met
+
+
+def _integer_bytes(t, what):
+    dtype = t.dtype
+    n = _BYTES_OF.get(dtype)
+    if n is None:
+        n = {"torch.int32": 4, "torch.int64": 8}.get(str(dtype))
+        if n is None:
+            raise GemmError(GEMM_ERR_UNSUPPORTED_DTYPE, f"{what}: {dtype}")
+        _BYTES_OF[dtype] = n
+    return n
 
 
 def _packed(t, shape, what):
     """Refuses a tensor that is not contiguous of that shape."""
     if t.shape != shape:
         raise GemmError(GEMM_ERR_INVALID_ARG, f"{what}: shape {tuple(t.shape)}, not {tuple(shape)}")
+    try:
+        if t.is_contiguous():
+            return
+    except AttributeError:
+        pass
     want = 1
     for n, stride in zip(reversed(shape), reversed(t.stride())):
         if n > 1 and stride != want and 0 not in shape:
@@ -711,7 +730,7 @@ def _table(t, shape, what, device, code=None):
     except AttributeError:
         pass
     _packed(t, shape, what)
-    if code is not None and _code(t, what) != code:
+    if code is not None and _CODE_OF.get(t.dtype) != code and _code(t, what) != code:
         raise GemmError(GEMM_ERR_UNSUPPORTED_DTYPE, f"{what}: {t.dtype}")
     return t.data_ptr()
 
@@ -930,9 +949,7 @@ class Gemm:
         shape = _shape(index, "index")
         T, k = shape
         dev = self.device
-        width = {"torch.int32": 4, "torch.int64": 8}.get(str(index.dtype))
-        if width is None:
-            raise GemmError(GEMM_ERR_UNSUPPORTED_DTYPE, f"index: {index.dtype}")
+        width = _integer_bytes(index, "index")
         p_index, ldi = _rows(index, shape, "index", dev)
         E = _groups(offsets)
         st = self._lib.gemm_route(self.handle, _ROUTE.pack(

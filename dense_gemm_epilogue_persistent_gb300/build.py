@@ -68,9 +68,9 @@ SHARED_UNITS = [(f"kern_shared_ab{ab}_m{mc}_n{nc}", "kern_shared.cu",
 ROW_UNITS = [("norm", "norm.cu", []), ("linear", "linear.cu", []),
              ("kern_split", "kern_split.cu", []), ("routing", "routing.cu", []),
              ("grouped", "grouped.cu", [])]
-GROUPED_UNITS = [(f"kern_grouped_ab{ab}_w{w}", "kern_grouped.cu",
-                  [f"-DGB300_AB={ab}", f"-DGB300_WEIGHTS={w}"])
-                 for ab, w in ((2, 0), (2, 1), (1, 0), (4, 0))]
+GROUPED_UNITS = [(f"kern_grouped_ab{ab}_f{form}", "kern_grouped.cu",
+                  [f"-DGB300_AB={ab}", f"-DGB300_FORM={form}"])
+                 for ab, form in ((2, 0), (2, 1), (2, 2), (1, 0), (4, 0))]
 LINEAR_UNITS = [(f"kern_linear_ab{ab}_e{epw}_p{epi}", "kern_linear.cu",
                  [f"-DGB300_AB={ab}", f"-DGB300_EPW={epw}", f"-DGB300_EPI={epi}"])
                 for ab, epi in ((2, 1), (1, 1), (4, 1), (2, 2)) for epw in (1, 2)]

@@ -30,131 +30,174 @@ struct Product {
 };
 
 // The type of the lean epilogue, or -1 for the whole one: nothing but alpha, a set's scale and a
-// residual of d's type; the 16-bit forms move features by twos.  (8191 x 8192 of inner size 64 with
-// a residual, bf16: 77 us, 125 by the whole one.)
+// residual of d's type; the 16-bit forms move features, and read a residual's, by twos.  (8191 x 8192 of inner size 64 with
+// a residual, bf16: 66 us, 125 by the whole one.)
 int lean_of(const Product& p) {
   const gb300::GroupedParams& k = p.k_params;
   const int dt = device_dt(k.d_dt);
   const bool lean = dtype_bytes(p.f_type) == 2 && !k.row_scale && !k.col_scale && !k.bias && !k.z &&
                     k.act == gb300::ACT_NONE && (!k.r || k.r_dt == k.d_dt) &&
-                    (dt == gb300::DT_F32 || p.feats % 2 == 0);
+                    (dt == gb300::DT_F32 || p.feats % 2 == 0 || !k.r);
   return lean ? dt : -1;
 }
 
 struct GroupedPlan {
   gemm_config_t cfg{};
+  int form = gb300::kGroupedRows, lean = -1;
   const void* kern = nullptr;
 };
 
-// Widths of the token operand's boxes: a tile's width is a multiple of this x cta_group.
+// Columns of the token operand's boxes: a tile's width is a multiple of this x cta_group.
 int box_unit(bool weights, int cta_group, int bn) {
   return weights ? 64 : cta_group == 2 ? 32 : bn % 32 == 0 && bn > 64 ? 32 : 16;
 }
 
-// The launch's tile, ring and grid (h->mu held).
-gemm_status_t plan_grouped(gemm_handle* h, const Product& p, GroupedPlan& out) {
+// Features of a ring stage: a single narrow tile's own leave room for more stages.  (Adapters' first
+// product, 8191 rows of 4096 by 7 x 64 bf16: 24.1 us with 128, 21.5 so.)
+int f_rows_of(const Product& p) {
+  return !p.weights && !p.f_mn && p.feats < 128 ? (int)cdiv(p.feats, 8) * 8 : 128;
+}
+
+// Feature tiles x column tiles: the items of a launch, at most (the device finds out how
+// many there are).
+int64_t items_of(const Product& p, const gemm_config_t& c) {
+  const int64_t tiles_f = cdiv(p.feats, c.tile_m);
+  return p.weights ? p.groups * tiles_f * cdiv(p.cols, c.tile_n)
+                   : (p.rows / c.tile_n + std::min(p.groups, p.rows)) * tiles_f;
+}
+
+// A launch's tile.
+gemm_status_t choose_tile(const gemm_handle* h, const Product& p, gemm_config_t& c) {
   const gemm_config_t f = h->forced ? h->forced_cfg : gemm_config_t{};
   if (f.cluster_m > 1 || f.cluster_n > 1 || f.split_k > 0 || f.stream_k > 1)
     return GEMM_ERR_UNSUPPORTED_CONFIG;
-  const int es = dtype_bytes(p.f_type);
   const int64_t mean = cdiv(p.rows, std::max<int64_t>(1, std::min(p.groups, p.rows)));
-  gemm_config_t& c = out.cfg;
   if (p.weights)
     c.cta_group = p.groups * cdiv(p.feats, 256) * cdiv(p.cols, 256) * 2 > h->sm_count / 2 ? 2 : 1;
   else
     c.cta_group = p.feats > 128 && mean > 64 ? 2 : 1;
   if (f.cta_group) c.cta_group = f.cta_group;
-  if (c.cta_group != 1 && c.cta_group != 2) return GEMM_ERR_UNSUPPORTED_CONFIG;
   c.tile_n = c.cta_group == 2 ? 256 : p.weights ? 128 : 64;
   if (f.tile_n) c.tile_n = f.tile_n;
-  if (c.tile_n < 16 || c.tile_n > 256) return GEMM_ERR_UNSUPPORTED_CONFIG;
-  const int unit = box_unit(p.weights, c.cta_group, c.tile_n);
-  if (c.tile_n % (unit * c.cta_group) != 0) return GEMM_ERR_UNSUPPORTED_CONFIG;
-  const int table = (int)p.groups;
+  c.tile_m = 128 * c.cta_group;
+  return c.tile_n % (box_unit(p.weights, c.cta_group, c.tile_n) * c.cta_group) == 0
+             ? GEMM_OK : GEMM_ERR_UNSUPPORTED_CONFIG;
+}
+
+// The rest of a plan whose tile, form and epilogue are chosen (h->mu held).  `items`: at most so many.
+gemm_status_t finish_plan(gemm_handle* h, const Product& p, int64_t items, GroupedPlan& out) {
+  const int es = dtype_bytes(p.f_type), f_rows = f_rows_of(p);
+  const gemm_config_t f = h->forced ? h->forced_cfg : gemm_config_t{};
+  gemm_config_t& c = out.cfg;
   const auto smem = [&](int stages) {
-    return gb300::grouped_smem(c.cta_group, c.tile_n, stages, table);
+    return gb300::grouped_smem(c.cta_group, c.tile_n, f_rows, stages, (int)p.groups);
   };
+  c.stages = 0;
   while (c.stages < gb300::kGroupedMaxStages && smem(c.stages + 1) <= h->smem_optin) ++c.stages;
   if (f.stages) {
-    if (f.stages < 0 || f.stages > c.stages) return GEMM_ERR_UNSUPPORTED_CONFIG;
+    if (f.stages > c.stages) return GEMM_ERR_UNSUPPORTED_CONFIG;
     c.stages = f.stages;
   }
   if (c.stages < 1) return GEMM_ERR_UNSUPPORTED_CONFIG;
   // (more than half an SM's shared memory: one CTA an SM, which owns its tensor memory)
   c.smem_bytes = std::max(smem(c.stages), h->smem_optin / 2 + 1024);
-  c.tile_m = 128 * c.cta_group;
   c.tile_k = 128 / es * gb300::kGroupedKA;
   c.acc_stages = gb300::kAccStages;
-  c.ring_bytes = c.stages * gb300::grouped_stage_bytes(c.cta_group, c.tile_n);
+  c.ring_bytes = c.stages * gb300::grouped_stage_bytes(c.cta_group, c.tile_n, f_rows);
   c.cluster_m = c.cluster_n = 1;
-  c.epi_warps = 2;
+  c.epi_warps = gb300::grouped_streams(out.lean);
   c.inject_stall = f.inject_stall;
-  c.group_m = f.group_m ? f.group_m : 8;
-  c.epi_wait_ns = f.epi_wait_ns;
-  c.l2_hints = f.l2_hints & 256 ? f.l2_hints & 255 : 6;
-  // At most this many items: the device finds out how many there are.
-  const int64_t tiles_f = cdiv(p.feats, c.tile_m);
-  c.tiles = p.weights ? p.groups * tiles_f * cdiv(p.cols, c.tile_n)
-                      : (p.rows / c.tile_n + std::min(p.groups, p.rows)) * tiles_f;
+  c.group_m = f.group_m ? std::min(f.group_m, gb300::kGroupedMaxStrip) : 8;
+  c.tiles = items;
   if (c.tiles > INT32_MAX / 2) return GEMM_ERR_INVALID_ARG;
-  const int lean = lean_of(p);
-  out.kern = gb300::grouped_kernel_for(es, c.cta_group, p.weights, lean);
+  out.kern = gb300::grouped_kernel_for(es, c.cta_group, out.form, out.lean);
   if (!out.kern) return GEMM_ERR_UNSUPPORTED_CONFIG;
   int resident = 0;
+  gemm_config_t asked = c;
+  asked.epi_warps = 2;                 // (the threads that resident_kernel_clusters counts: one CTA an SM anyway)
   GB300_CHECK(resident_kernel_clusters(
-      h, h->grouped_variants[es == 2 ? 0 : es == 1 ? 1 : 2][c.cta_group - 1][p.weights][lean + 1],
-      out.kern, c,
-      c.cta_group, &resident));
+      h, h->grouped_variants[es == 2 ? 0 : es == 1 ? 1 : 2][c.cta_group - 1][out.form][out.lean + 1],
+      out.kern, asked, c.cta_group, &resident));
   c.grid_ctas = (int)std::max<int64_t>(1, std::min<int64_t>(c.tiles, resident)) * c.cta_group;
   return GEMM_OK;
 }
 
-// Enqueue a planned launch (h->mu held).
-gemm_status_t run_grouped(gemm_handle* h, const Product& p, const GroupedPlan& plan,
-                          struct CUstream_st* stream) {
-  const gemm_config_t& c = plan.cfg;
-  const int es = dtype_bytes(p.f_type);
-  const int unit = box_unit(p.weights, c.cta_group, c.tile_n), bk = c.tile_k;
-  CUtensorMap f, t;
+// Plan one product (h->mu held).
+gemm_status_t plan_grouped(gemm_handle* h, const Product& p, GroupedPlan& out) {
+  GB300_CHECK(choose_tile(h, p, out.cfg));
+  out.form = p.weights ? gb300::kGroupedWeights : gb300::kGroupedRows;
+  out.lean = lean_of(p);
+  return finish_plan(h, p, items_of(p, out.cfg), out);
+}
+
+// Plan both gradients as one launch, where one tile and one lean epilogue suit both (h->mu held);
+// out.kern stays null where not.  (2002 rows of 6 groups, 2003 x 1501 fp16: 38.2 us, 42.3 as two; 8192 of 16
+// uneven ones, 4096 x 4096 bf16 452, 466.)
+gemm_status_t plan_both(gemm_handle* h, const Product& da, const Product& db, GroupedPlan& out) {
+  gemm_config_t cb{};
+  GB300_CHECK(choose_tile(h, da, out.cfg));
+  GB300_CHECK(choose_tile(h, db, cb));
+  out.lean = lean_of(da);
+  if (out.lean < 0 || lean_of(db) != out.lean || cb.cta_group != out.cfg.cta_group ||
+      cb.tile_n != out.cfg.tile_n)
+    return GEMM_OK;
+  out.form = gb300::kGroupedBoth;
+  return finish_plan(h, da, items_of(da, out.cfg) + items_of(db, cb), out);
+}
+
+// A product's tensor maps (`whole`: a whole tile's tokens, of the rows form) and parameters by its plan.
+gemm_status_t prepare(gemm_handle* h, const Product& p, const gemm_config_t& c, CUtensorMap& f,
+                      CUtensorMap& t, CUtensorMap* whole, gb300::GroupedParams& k) {
+  const int unit = box_unit(p.weights, c.cta_group, c.tile_n);
   std::memset(&f, 0, sizeof(f));
   std::memset(&t, 0, sizeof(t));
-  gb300::GroupedParams k = p.k_params;
+  if (whole) std::memset(whole, 0, sizeof(*whole));
+  k = p.k_params;
   k.has_operands = p.weights ? p.rows > 0 : p.k > 0;
   if (k.has_operands) {
+    const int box = gb300::kGroupedMBox;
     const bool ok =
         p.weights
-            ? encode_stack(h->encode, &f, p.f, p.f_type, p.feats, p.rows, 1, p.ldf, 0, bk) &&
-                  encode_stack(h->encode, &t, p.t, p.t_type, p.cols, p.rows, 1, p.ldt, 0, bk)
+            ? encode_stack(h->encode, &f, p.f, p.f_type, p.feats, p.rows, 1, p.ldf, 0, box) &&
+                  encode_stack(h->encode, &t, p.t, p.t_type, p.cols, p.rows, 1, p.ldt, 0, box)
             : (p.f_mn ? encode_stack(h->encode, &f, p.f, p.f_type, p.feats, p.k, p.sets, p.ldf,
-                                     p.stride_f, bk)
+                                     p.stride_f, c.tile_k)
                       : encode_stack(h->encode, &f, p.f, p.f_type, p.k, p.feats, p.sets, p.ldf,
-                                     p.stride_f, 128)) &&
-                  encode_stack(h->encode, &t, p.t, p.t_type, p.k, p.rows, 1, p.ldt, 0, unit);
+                                     p.stride_f, f_rows_of(p))) &&
+                  encode_stack(h->encode, &t, p.t, p.t_type, p.k, p.rows, 1, p.ldt, 0, unit) &&
+                  encode_stack(h->encode, whole, p.t, p.t_type, p.k, p.rows, 1, p.ldt, 0,
+                               c.tile_n / c.cta_group);
     if (!ok) return GEMM_ERR_CUDA;
   }
   k.rows = (int)p.rows; k.feats = (int)p.feats; k.cols = (int)p.cols; k.k = (int)p.k;
   k.groups = (int)p.groups; k.sets = (int)p.sets;
   k.bn = c.tile_n;
   k.unit = unit;
+  k.f_rows = f_rows_of(p);
   k.tiles_f = (int)cdiv(p.feats, c.tile_m);
   k.tiles_c = p.weights ? (int)cdiv(p.cols, c.tile_n) : 1;
   k.stages = c.stages;
-  k.strip = std::min(c.group_m, gb300::kGroupedMaxStrip);
+  k.strip = c.group_m;
   k.by_bn = gb300::fast_div(k.bn);
   k.by_strip = gb300::fast_div(k.strip * k.tiles_f);
   k.by_group = gb300::fast_div(k.tiles_f * k.tiles_c);
-  k.alternate = c.epi_wait_ns != 7;
-  k.l2_hints = (uint32_t)c.l2_hints;
+  k.alternate = 1;
   k.f_mn = p.f_mn;
   k.idesc = make_idesc(p.f_type, p.t_type, false, c.cta_group, 0, p.weights || p.f_mn, p.weights);
   k.status = h->d_status;
   k.timeout_ns = h->timeout_ns;
   k.inject_stall = c.inject_stall;
-  (void)es;
+  return GEMM_OK;
+}
+
+// Enqueue a planned launch (h->mu held); args: its tensor maps and parameters.
+gemm_status_t launch_planned(gemm_handle* h, const GroupedPlan& plan, void** args,
+                             struct CUstream_st* stream) {
+  const gemm_config_t& c = plan.cfg;
   cudaLaunchConfig_t lc{};
   cudaLaunchAttribute attr[2];
   lc.gridDim = dim3((unsigned)c.grid_ctas);
-  lc.blockDim = dim3((unsigned)gb300::grouped_threads(p.weights));
+  lc.blockDim = dim3((unsigned)gb300::grouped_threads(plan.form, plan.lean));
   lc.dynamicSmemBytes = (size_t)c.smem_bytes;
   lc.stream = reinterpret_cast<cudaStream_t>(stream);
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -167,12 +210,30 @@ gemm_status_t run_grouped(gemm_handle* h, const Product& p, const GroupedPlan& p
   lc.numAttrs = c.cta_group > 1 ? 2 : 1;
   h->last = c;
   h->counted = false;
-  void* args[3] = {&f, &t, &k};
   if (cudaLaunchKernelExC(&lc, plan.kern, args) != cudaSuccess) {
     cudaGetLastError();
     return GEMM_ERR_CUDA;
   }
   return GEMM_OK;
+}
+
+gemm_status_t run_grouped(gemm_handle* h, const Product& p, const GroupedPlan& plan,
+                          struct CUstream_st* stream) {
+  CUtensorMap f, t, whole;
+  gb300::GroupedParams k{};
+  GB300_CHECK(prepare(h, p, plan.cfg, f, t, &whole, k));
+  void* args[4] = {&f, &t, &whole, &k};
+  return launch_planned(h, plan, args, stream);
+}
+
+gemm_status_t run_both(gemm_handle* h, const Product& da, const Product& db, const GroupedPlan& plan,
+                       struct CUstream_st* stream) {
+  CUtensorMap f, t, whole;
+  gb300::GroupedBothParams k{};
+  GB300_CHECK(prepare(h, da, plan.cfg, f, t, &whole, k));
+  GB300_CHECK(prepare(h, db, plan.cfg, k.f2, k.t2, nullptr, k.weights));
+  void* args[4] = {&f, &t, &whole, &k};
+  return launch_planned(h, plan, args, stream);
 }
 
 bool is_count(int64_t v) { return v >= 0 && v <= gb300::kGroupedMaxGroups; }
@@ -463,11 +524,12 @@ GEMM_API gemm_status_t gemm_grouped_linear_bwd(gemm_handle_t h, const gemm_group
   const bool da = p.da && p.M > 0 && p.K > 0, db = p.db && p.K > 0;
   const Product q_da = product_da(p, dz, lddz), q_db = product_db(p, dz, lddz);
   // both planned before anything is enqueued: a refused configuration changes no tensor
-  GroupedPlan plan_da, plan_db;
+  GroupedPlan plan_da, plan_db, both;
   {
     std::lock_guard<std::mutex> guard(h->mu);
-    if (da) GB300_CHECK(plan_grouped(h, q_da, plan_da));
-    if (db) GB300_CHECK(plan_grouped(h, q_db, plan_db));
+    if (da && db) GB300_CHECK(plan_both(h, q_da, q_db, both));
+    if (!both.kern && da) GB300_CHECK(plan_grouped(h, q_da, plan_da));
+    if (!both.kern && db) GB300_CHECK(plan_grouped(h, q_db, plan_db));
   }
   if ((p.dz && p.M > 0) || p.dbias) {
     GroupedActGrad g{};
@@ -482,6 +544,7 @@ GEMM_API gemm_status_t gemm_grouped_linear_bwd(gemm_handle_t h, const gemm_group
     GB300_CHECK(grouped_act_grad(h, g, stream));
   }
   std::lock_guard<std::mutex> guard(h->mu);
+  if (both.kern) return run_both(h, q_da, q_db, both, stream);
   if (da) GB300_CHECK(run_grouped(h, q_da, plan_da, stream));
   if (db) GB300_CHECK(run_grouped(h, q_db, plan_db, stream));
   return GEMM_OK;

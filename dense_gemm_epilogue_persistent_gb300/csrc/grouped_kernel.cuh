@@ -26,11 +26,16 @@
 // leader's, which then completes the stage.  (A remote arrival for every stage instead, to
 // have the stages count both CTAs, cost a quarter: 8192^3 bf16 880 us, 648 so.)
 //
-// Block: warp 0 TMA producer, warp 1 tensor memory and MMA issue, warps 2-9
-// epilogue (two per lane quarter, taking 16-column chunks alternately), warp 10 (weights
-// form) the zeroing.  Persistent grid of CTAs or CTA pairs, one CTA an SM, two
-// accumulator stages.  Bound by the tensor pipe for large groups, by the
-// weights' DRAM traffic for small ones.  The waits are bounded as in gemm_kernel.cuh.
+// Both gradients of a layer run as one launch: the items of da (rows), then those of db
+// (weights), dealt to the CTAs in one sequence, so that a launch's start and end and the
+// first product's last, partial round are paid once.
+//
+// Block: warp 0 TMA producer, warp 1 tensor memory and MMA issue, then the epilogue's (two warps
+// per lane quarter, three where its code is lean, taking 32-column chunks in turn) and,
+// with a weights form, the zeroing.  Persistent grid of CTAs or CTA pairs, one CTA an
+// SM, two accumulator stages.  Bound by the operands' way out of L2 for large groups (a stage of a
+// 256 x 256 pair tile takes 1230 cycles for 64 KB, 1024 of MMA), by the weights' DRAM traffic for small
+// ones.  The waits are bounded as in gemm_kernel.cuh.
 #pragma once
 
 #include "activations.cuh"
@@ -61,12 +66,15 @@ struct GroupedParams {
   int groups, sets;          // groups of rows, sets of weights
   int bn;                    // widest tile
   int unit;                  // columns of one box of the token operand
+  int f_rows;                // features of a stage: 128, or of a single narrow tile of K-major weights its
+                             // own (the MMA reads 128 rows of shared memory all the same; what it
+                             // makes of the others is not stored)
   int tiles_f, tiles_c;      // feature tiles; weights form: column tiles
   FastDiv by_bn, by_strip, by_group;   // by bn, a whole strip's items, a group's (weights form)
   int stages;
-  int alternate;             // odd waves of items walk the k-blocks from the last one down
+  int alternate;             // odd waves of items walk the k-blocks from the last one down (8192^3 bf16
+                             // 659 us, 675 without)
   int strip;                 // token (or column) tiles walked together
-  uint32_t l2_hints;         // L2 eviction priority (0 normal, 1 last, 2 first): bits 0-1 features, 2-3 tokens
   int f_mn;                  // rows form: weights with contiguous features
   int has_operands;          // the tensor maps are encoded
   int skip_none;             // groups without weights are left out: their d is r already
@@ -90,24 +98,48 @@ struct GroupedParams {
   int bias_dt, r_dt, z_dt, d_dt, act;
 };
 
+// Both forms in one launch: the rows form's, whose tile, ring and groups are common, and the
+// weights form's with its tensor maps.
+struct GroupedBothParams : GroupedParams {
+  GroupedParams weights;
+  CUtensorMap f2, t2;
+};
+enum : int { kGroupedRows = 0, kGroupedWeights = 1, kGroupedBoth = 2 };
+template <int FORM> struct GroupedParamsOf { using type = GroupedParams; };
+template <> struct GroupedParamsOf<kGroupedBoth> { using type = GroupedBothParams; };
+__device__ __forceinline__ const GroupedParams& weights_of(const GroupedParams& p) { return p; }
+__device__ __forceinline__ const GroupedParams& weights_of(const GroupedBothParams& p) { return p.weights; }
+__device__ __forceinline__ const CUtensorMap* second_map(const GroupedParams&, const CUtensorMap& map, int) {
+  return &map;
+}
+__device__ __forceinline__ const CUtensorMap* second_map(const GroupedBothParams& p, const CUtensorMap&, int i) {
+  return i ? &p.t2 : &p.f2;
+}
+
 constexpr int kGroupedKA = 2;                  // 128-byte K atoms a ring stage
-constexpr int kGroupedEpiWarps = 8;
+constexpr int kGroupedMBox = 128;              // rows of one box of the weights form (with 64: 16 groups 245 -> 258 us)
 constexpr int kGroupedChunk = 32;              // columns of an epilogue chunk
 constexpr int kGroupedMaxStrip = 16;
 constexpr int kGroupedMaxGroups = 4096;        // what the tables in shared memory hold
-constexpr int kGroupedMaxStages = 8;
+constexpr int kGroupedMaxStages = 10;
 
-constexpr int grouped_threads(bool weights) { return 64 + 32 * kGroupedEpiWarps + (weights ? 32 : 0); }
+// Epilogue warps per tensor-memory lane quarter: three where the lean epilogue's registers allow it
+// (64 groups' weight gradients of 128 rows, 4096 x 4096 bf16: 457 us, 549 with two).
+__host__ __device__ constexpr int grouped_streams(int lean) { return lean >= 0 ? 3 : 2; }
+constexpr int grouped_threads(int form, int lean) {
+  return 64 + 128 * grouped_streams(lean) + (form == kGroupedRows ? 0 : 32);
+}
 
 // Bytes of a ring stage and of what follows the ring: barriers (full, empty, tail, peer; two
 // accumulators' full and empty; one that nothing arrives at), tensor-memory
 // address and abort flag, warps' sums, reciprocals, the two tables.
-constexpr int grouped_stage_bytes(int cta_group, int bn) {
-  return kGroupedKA * (128 + bn / cta_group) * 128;
+constexpr int grouped_stage_bytes(int cta_group, int bn, int f_rows) {
+  return kGroupedKA * (f_rows + bn / cta_group) * 128;
 }
 constexpr int grouped_bar_bytes() { return 8 * (4 * kGroupedMaxStages + 5) + 16 + 64 + 80; }
-constexpr int grouped_smem(int cta_group, int bn, int stages, int groups) {
-  return 1024 + stages * grouped_stage_bytes(cta_group, bn) + grouped_bar_bytes() + 8 * (groups + 1);
+constexpr int grouped_smem(int cta_group, int bn, int f_rows, int stages, int groups) {
+  return 1024 + stages * grouped_stage_bytes(cta_group, bn, f_rows) + grouped_bar_bytes() +
+         8 * (groups + 1);
 }
 
 // Where a lane's values of the columns (tokens) of a matrix lie.  With 16 bits two neighbouring
@@ -221,13 +253,15 @@ __device__ __forceinline__ void epi_add(const EpiMatrix& m, bool pairs, uint32_t
 }
 
 // LEAN < 0: the whole epilogue, every type.  Else nothing but alpha, a set's scale and a residual
-// follow the product, d and the residual are of type LEAN, and a 16-bit one has an even number
-// of features.
-template <int CG, int AB_BYTES, bool kWeights, int LEAN>
-__global__ void __launch_bounds__(grouped_threads(kWeights), 1)
+// follow the product, d and the residual are of type LEAN, and with a 16-bit residual the number of
+// features is even.
+template <int CG, int AB_BYTES, int FORM, int LEAN>
+__global__ void __launch_bounds__(grouped_threads(FORM, LEAN), 1)
 grouped_kernel(const __grid_constant__ CUtensorMap tmF, const __grid_constant__ CUtensorMap tmT,
-               const __grid_constant__ GroupedParams p) {
-  constexpr bool kFull = !kWeights && LEAN < 0;
+               const __grid_constant__ CUtensorMap tmWhole,
+               const __grid_constant__ typename GroupedParamsOf<FORM>::type p) {
+  constexpr bool kRows = FORM != kGroupedWeights, kWeights = FORM != kGroupedRows;
+  constexpr bool kFull = FORM == kGroupedRows && LEAN < 0;
   constexpr int KIND = (AB_BYTES == 1) ? 1 : (AB_BYTES == 4 ? 2 : 0);
   constexpr int KA = kGroupedKA;
   constexpr int ATOM_K = 128 / AB_BYTES;         // K of a 128-byte atom; features of an MN-major one
@@ -236,11 +270,12 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmF, const __grid_constant__ 
   constexpr int K_STEPS = BK / UMMA_K;
   constexpr int STEPS_PER_ATOM = ATOM_K / UMMA_K;
   constexpr uint32_t MN_ATOM = BK * 128;         // bytes of an MN-major atom column
-  constexpr uint32_t F_ATOM = 128 * 128;         // bytes of a K-major atom of 128 features
-  constexpr uint32_t F_STAGE = F_ATOM * KA;
   constexpr int F_BOXES = 128 / ATOM_K;          // MN-major boxes of the 128 features
   constexpr bool PAIR = CG == 2;
+  constexpr int kStreams = grouped_streams(LEAN), kEpiWarps = 4 * kStreams;
   static_assert(!kWeights || AB_BYTES == 2, "weight gradients are of 16-bit operands");
+  static_assert(FORM != kGroupedBoth || LEAN >= 0, "both forms: the lean epilogue");
+  static_assert(BK % kGroupedMBox == 0 || !kWeights, "whole boxes a stage");
 
   grid_launch_dependents();
   extern __shared__ uint8_t smem_raw[];
@@ -250,10 +285,13 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmF, const __grid_constant__ 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = PAIR ? cluster_ctarank() : 0u;
   const int cluster_id = blockIdx.x / CG, num_clusters = gridDim.x / CG;
+  const GroupedParams& pw = weights_of(p);       // the weights form's
   const int S = p.stages, bn = p.bn;
   const uint32_t t_atom = (uint32_t)(bn / CG) * 128u;    // K-major atom of the CTA's tokens
   const uint32_t t_stage = t_atom * KA;
-  const uint32_t f_ring = base, t_ring = f_ring + S * F_STAGE;
+  const uint32_t f_atom = (uint32_t)p.f_rows * 128u;     // ... of its features (MN-major: 128 of them)
+  const uint32_t f_stage = f_atom * KA;
+  const uint32_t f_ring = base, t_ring = f_ring + S * f_stage;
   const uint32_t bars = t_ring + S * t_stage;
   const uint32_t full0 = bars, empty0 = full0 + 8u * S, tail0 = empty0 + 8u * S;
   const uint32_t peer0 = tail0 + 8u * S;         // the other CTA's half of a last block is zeroed
@@ -275,7 +313,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmF, const __grid_constant__ 
     }
     for (int a = 0; a < kAccStages; ++a) {
       mbar_init(tfull0 + 8u * a, 1);
-      mbar_init(tempty0 + 8u * a, kGroupedEpiWarps * CG);
+      mbar_init(tempty0 + 8u * a, kEpiWarps * CG);
     }
     mbar_init(never_bar, 1);
     *abort_ptr = 0u;
@@ -283,6 +321,11 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmF, const __grid_constant__ 
     if (p.has_operands) {
       prefetch_tensormap(&tmF);
       prefetch_tensormap(&tmT);
+      if constexpr (kRows) prefetch_tensormap(&tmWhole);
+    }
+    if constexpr (FORM == kGroupedBoth) {
+      prefetch_tensormap(&p.f2);
+      prefetch_tensormap(&p.t2);
     }
   }
   if (warp == 1) {
@@ -311,8 +354,8 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmF, const __grid_constant__ 
   for (int g = threadIdx.x; g <= p.groups; g += blockDim.x)
     offs[g] = min(max(__ldg(p.offsets + g), 0), p.rows);
   __syncthreads();
-  int num_items = p.groups * p.tiles_f * p.tiles_c;
-  if constexpr (!kWeights) {
+  int rows_items = 0;
+  if constexpr (kRows) {
     const int share = (p.groups + (int)blockDim.x - 1) / (int)blockDim.x;
     const int g0 = min((int)threadIdx.x * share, p.groups), g1 = min(g0 + share, p.groups);
     int mine = 0;
@@ -334,10 +377,42 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmF, const __grid_constant__ 
       starts[g] = at * p.tiles_f;
       at += tiles_of(g, max(0, offs[g + 1] - offs[g]));
     }
-    num_items = total * p.tiles_f;
-    if (threadIdx.x == 0) starts[p.groups] = num_items;
+    rows_items = total * p.tiles_f;
+    if (threadIdx.x == 0) starts[p.groups] = rows_items;
     __syncthreads();
   }
+  const int weights_items = kWeights ? pw.groups * pw.tiles_f * pw.tiles_c : 0;
+  const int num_items = rows_items + weights_items;
+
+  // The CTA's (pair's) sequence of items.  They are dealt in turn; with both forms, the CTAs that got
+  // one of the rows form's less have first of the others as many as take about as long (a
+  // stage takes 1230 cycles, an epilogue that no main loop hides 3000).
+  int lead = 0, lead_from = 0;                   // so many items ahead, to the CTAs from lead_from on
+  if constexpr (FORM == kGroupedBoth) {
+    lead_from = rows_items % num_clusters;
+    if (lead_from > 0) {
+      const int behind = num_clusters - lead_from;
+      const int mean = (offs[p.groups] - offs[0]) / p.groups;
+      const int one = max(1230 * ((mean + BK - 1) / BK), 3000);
+      const int rounds = (1230 * ((p.k + BK - 1) / BK) + 3000) / one;
+      lead = min(rounds, weights_items / behind) * behind;
+    }
+  }
+  const auto second_item = [&]() {
+    return lead > 0 && cluster_id >= lead_from ? rows_items + cluster_id - lead_from
+                                               : rows_items + lead + cluster_id;
+  };
+  const auto next_item = [&](int it) {
+    if constexpr (FORM == kGroupedBoth) {
+      if (it < rows_items) return it + num_clusters < rows_items ? it + num_clusters : second_item();
+      if (it < rows_items + lead) {
+        const int next = it + num_clusters - lead_from;
+        return next < rows_items + lead ? next : rows_items + lead + cluster_id;
+      }
+    }
+    return it + num_clusters;
+  };
+  const int first_item = FORM == kGroupedBoth && cluster_id >= rows_items ? second_item() : cluster_id;
 
   const Watch w{abort_ptr, p.status, p.timeout_ns};
 
@@ -346,6 +421,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmF, const __grid_constant__ 
   // go through its strips of `strip` token (or column) tiles, tile by tile, then feature by
   // feature, so that CTAs at work together share operands in L2.
   struct Item {
+    bool wt;                 // of the weights form
     int g, e;                // group; set of weights, -1 for none
     int f0;                  // first feature
     int t0;                  // first token (rows form) or output row (weights form)
@@ -354,17 +430,18 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmF, const __grid_constant__ 
     int blocks;              // k-blocks
     bool down;               // walked from the last one
   };
-  const int min_width = p.unit * CG;             // (a power of two)
   const int k_blocks = (p.k + BK - 1) / BK;
   int cursor = 0, wave = 0;                      // the last item's group; items so far
-  const auto peek = [&](int it) {
+  const auto item_at = [&](int it) {
     Item i;
-    i.down = p.alternate && (wave & 1);
+    i.wt = FORM == kGroupedBoth ? it >= rows_items : kWeights;
+    i.down = p.alternate && (wave++ & 1);
+    const GroupedParams& q = i.wt ? pw : p;
     int r, tiles;
-    if constexpr (kWeights) {
-      i.g = fast_quot(it, p.by_group);
-      r = it - i.g * p.by_group.d;
-      tiles = p.tiles_c;
+    if (kWeights && i.wt) {
+      i.g = fast_quot(it - rows_items, q.by_group);
+      r = it - rows_items - i.g * q.by_group.d;
+      tiles = q.tiles_c;
     } else {
       // starts[lo] <= it < starts[hi]; items come in increasing order
       int lo = cursor, hi = p.groups;
@@ -378,15 +455,15 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmF, const __grid_constant__ 
       r = it - starts[lo];
       tiles = fast_quot(offs[lo + 1] - offs[lo] + bn - 1, p.by_bn);
     }
-    const int strip = fast_quot(r, p.by_strip), rr = r - strip * p.by_strip.d;
-    const int high = min(p.strip, tiles - strip * p.strip);
+    const int strip = fast_quot(r, q.by_strip), rr = r - strip * q.by_strip.d;
+    const int high = min(q.strip, tiles - strip * q.strip);
     const int ft = high == 1 ? rr : (int)__umulhi((uint32_t)rr, magic[high]);
-    const int tile = strip * p.strip + rr - ft * high;
+    const int tile = strip * q.strip + rr - ft * high;
     i.f0 = ft * (128 * CG);
-    if constexpr (kWeights) {
+    if (kWeights && i.wt) {
       i.e = i.g;
       i.t0 = tile * bn;
-      i.valid = min(bn, p.cols - i.t0);
+      i.valid = min(bn, q.cols - i.t0);
       i.m0 = offs[i.g];
       i.mn = max(0, offs[i.g + 1] - i.m0);
       i.blocks = (i.mn + BK - 1) / BK;
@@ -398,22 +475,18 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmF, const __grid_constant__ 
       i.m0 = i.mn = 0;
       i.blocks = i.e < 0 ? 0 : k_blocks;
     }
+    const int min_width = q.unit * CG;           // (a power of two)
     i.width = (i.valid + min_width - 1) & -min_width;
-    return i;
-  };
-  const auto item_at = [&](int it) {
-    const Item i = peek(it);
-    ++wave;
     return i;
   };
 
   if (warp == 0) {
     // ---------------------------------------------------------- TMA producer
-    const uint64_t pol_f = make_l2_policy(p.l2_hints & 3u), pol_t = make_l2_policy(p.l2_hints >> 2 & 3u);
+    const uint64_t pol = make_l2_policy(0);
     int s = 0;
     uint32_t ph = 0;
     bool ok = true;
-    for (int it = cluster_id; ok && it < num_items; it += num_clusters) {
+    for (int it = first_item; ok && it < num_items; it = next_item(it)) {
       const Item i = item_at(it);
       const int f0 = i.f0 + (int)rank * 128;
       const int width = i.width / CG;                    // this CTA's columns
@@ -424,58 +497,73 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmF, const __grid_constant__ 
           ok = false;
           break;
         }
-        const uint32_t sf = f_ring + s * F_STAGE, st = t_ring + s * t_stage;
+        const uint32_t sf = f_ring + s * f_stage, st = t_ring + s * t_stage;
         // (debug build, by every lane alike: the boxes inside this stage, coordinates whole 16
         // bytes and from 0 on)
-        if (!dbg_check(in_range(sf, F_STAGE, f_ring, t_ring) && f0 >= 0, kChkLoadA, w) ||
+        if (!dbg_check(in_range(sf, f_stage, f_ring, t_ring) && f0 >= 0, kChkLoadA, w) ||
             !dbg_check(in_range(st, (uint32_t)width * KA * 128u, t_ring, bars) && t0 >= 0 &&
-                           i.m0 >= 0 && (!kWeights || t0 % 8 == 0),
+                           i.m0 >= 0 && (!i.wt || t0 % 8 == 0),
                        kChkLoadB, w)) {
           ok = false;
           break;
         }
         if (elect_one()) {
-          if constexpr (kWeights) {
-            const int m = i.m0 + kb * BK;
-            // both operands MN-major: boxes of 64 features or output rows x BK rows
-            const uint32_t bytes = (uint32_t)(F_BOXES + width / ATOM_K) * MN_ATOM;
-            const bool tail = kb == i.blocks - 1 && i.mn % UMMA_K != 0;
-            if (tail) {
-              // (completed on this CTA's own barrier: the zeroing warp goes on from there)
-              const uint32_t bar = tail0 + 8u * s;
-              mbar_arrive_expect_tx(bar, bytes);
-              for (int j = 0; j < F_BOXES; ++j)
-                tma_load_3d(sf + j * MN_ATOM, &tmF, bar, f0 + j * ATOM_K, m, 0, pol_f);
-              for (int j = 0; j < width / ATOM_K; ++j)
-                tma_load_3d(st + j * MN_ATOM, &tmT, bar, t0 + j * ATOM_K, m, 0, pol_t);
-            } else {
-              const uint32_t fb = full0 + 8u * s;
-              const uint32_t bar = PAIR ? map_to_rank(fb, 0) : fb;
-              if (rank == 0) mbar_arrive_expect_tx(fb, CG * bytes);
-              for (int j = 0; j < F_BOXES; ++j)
-                OperandLoad<CG, false>::load(sf + j * MN_ATOM, &tmF, bar, f0 + j * ATOM_K, m, 0, 0, pol_f);
-              for (int j = 0; j < width / ATOM_K; ++j)
-                OperandLoad<CG, false>::load(st + j * MN_ATOM, &tmT, bar, t0 + j * ATOM_K, m, 0, 0, pol_t);
+          if (kWeights && i.wt) {
+            // both operands MN-major: boxes of 64 features or output rows x 64 rows, those that
+            // hold rows of the group
+            const CUtensorMap* const map_f = second_map(p, tmF, 0);
+            const CUtensorMap* const map_t = second_map(p, tmT, 1);
+            const int m = i.m0 + kb * BK, left = i.mn - kb * BK;
+            const int halves = min(BK / kGroupedMBox, (left + kGroupedMBox - 1) / kGroupedMBox);
+            const uint32_t bytes =
+                (uint32_t)(halves * (F_BOXES + width / ATOM_K)) * (kGroupedMBox * 128u);
+            const bool tail = left <= BK && i.mn % UMMA_K != 0;
+            // (a last block that needs zeros is completed on this CTA's own barrier: the zeroing
+            // warp goes on from there)
+            const uint32_t fb = full0 + 8u * s;
+            const uint32_t bar = tail ? tail0 + 8u * s : PAIR ? map_to_rank(fb, 0) : fb;
+            if (tail) mbar_arrive_expect_tx(bar, bytes);
+            else if (rank == 0) mbar_arrive_expect_tx(fb, CG * bytes);
+            for (int h = 0; h < halves; ++h) {
+              const uint32_t at = (uint32_t)h * (kGroupedMBox * 128u);
+              const int row = m + h * kGroupedMBox;
+              for (int j = 0; j < F_BOXES; ++j) {
+                if (tail) tma_load_3d(sf + j * MN_ATOM + at, map_f, bar, f0 + j * ATOM_K, row, 0, pol);
+                else OperandLoad<CG, false>::load(sf + j * MN_ATOM + at, map_f, bar, f0 + j * ATOM_K,
+                                                  row, 0, 0, pol);
+              }
+              for (int j = 0; j < width / ATOM_K; ++j) {
+                if (tail) tma_load_3d(st + j * MN_ATOM + at, map_t, bar, t0 + j * ATOM_K, row, 0, pol);
+                else OperandLoad<CG, false>::load(st + j * MN_ATOM + at, map_t, bar, t0 + j * ATOM_K,
+                                                  row, 0, 0, pol);
+              }
             }
-          } else {
+          } else if (kRows) {
             const int k0 = kb * BK;
             const int atoms = min(KA, (p.k - k0 + ATOM_K - 1) / ATOM_K);   // those with elements
             const uint32_t fb = full0 + 8u * s;
             const uint32_t bar = PAIR ? map_to_rank(fb, 0) : fb;
             if (rank == 0)
-              mbar_arrive_expect_tx(fb, CG * ((p.f_mn ? F_STAGE : atoms * F_ATOM) +
+              mbar_arrive_expect_tx(fb, CG * ((p.f_mn ? f_stage : (uint32_t)atoms * f_atom) +
                                               (uint32_t)(atoms * width) * 128u));
             if (p.f_mn) {
               for (int j = 0; j < F_BOXES; ++j)
-                OperandLoad<CG, false>::load(sf + j * MN_ATOM, &tmF, bar, f0 + j * ATOM_K, k0, i.e, 0, pol_f);
+                OperandLoad<CG, false>::load(sf + j * MN_ATOM, &tmF, bar, f0 + j * ATOM_K, k0, i.e, 0, pol);
             } else {
               for (int a = 0; a < atoms; ++a)
-                OperandLoad<CG, false>::load(sf + a * F_ATOM, &tmF, bar, k0 + a * ATOM_K, f0, i.e, 0, pol_f);
+                OperandLoad<CG, false>::load(sf + a * f_atom, &tmF, bar, k0 + a * ATOM_K, f0, i.e, 0, pol);
             }
-            for (int a = 0; a < atoms; ++a)
-              for (int u = 0; u < width; u += p.unit)
-                OperandLoad<CG, false>::load(st + a * t_atom + u * 128, &tmT, bar, k0 + a * ATOM_K,
-                                             t0 + u, 0, 0, pol_t);
+            // a whole tile's tokens in one box an atom, else in units (adapters' first product, 8191
+            // rows of 4096 by 7 x 64 bf16: 21.5 us, 22.5 in units alone; 8192^3 659, 673)
+            if (i.width == bn) {
+              for (int a = 0; a < atoms; ++a)
+                OperandLoad<CG, false>::load(st + a * t_atom, &tmWhole, bar, k0 + a * ATOM_K, t0, 0, 0, pol);
+            } else {
+              for (int a = 0; a < atoms; ++a)
+                for (int u = 0; u < width; u += p.unit)
+                  OperandLoad<CG, false>::load(st + a * t_atom + u * 128, &tmT, bar, k0 + a * ATOM_K,
+                                               t0 + u, 0, 0, pol);
+            }
           }
         }
         __syncwarp();
@@ -485,43 +573,43 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmF, const __grid_constant__ 
   } else if (warp == 1) {
     // ---------------------------------------------------------- MMA issuer
     if (rank == 0) {
-      const bool f_mn = kWeights || p.f_mn;
-      const uint64_t fd0 = f_mn ? smem_desc_sw128(f_ring, MN_ATOM, 1024)
-                                : smem_desc_sw128(f_ring, 16, 1024);
-      const uint64_t td0 = kWeights ? smem_desc_sw128(t_ring, MN_ATOM, 1024)
-                                    : smem_desc_sw128(t_ring, 16, 1024);
-      // 16-byte units from one K step to the next, and from one atom of steps to the next
-      const uint32_t f_step = (f_mn ? UMMA_K * 128 : 32) / 16;
-      const uint32_t t_step = (kWeights ? UMMA_K * 128 : 32) / 16;
-      const uint32_t f_next = f_mn ? STEPS_PER_ATOM * f_step : F_ATOM / 16;
-      const uint32_t t_next = kWeights ? STEPS_PER_ATOM * t_step : t_atom / 16;
       int s = 0, acc = 0;
       uint32_t ph = 0, aph = 0;
       bool ok = !p.inject_stall ||
                 __all_sync(0xFFFFFFFFu, wait_phase(never_bar, 0u, w, kWaitInjected));
-      for (int it = cluster_id; ok && it < num_items; it += num_clusters) {
+      for (int it = first_item; ok && it < num_items; it = next_item(it)) {
         const Item i = item_at(it);
+        const bool wt = kWeights && i.wt, f_mn = wt || p.f_mn;
+        const uint64_t fd0 = f_mn ? smem_desc_sw128(f_ring, MN_ATOM, 1024)
+                                  : smem_desc_sw128(f_ring, 16, 1024);
+        const uint64_t td0 = wt ? smem_desc_sw128(t_ring, MN_ATOM, 1024)
+                                : smem_desc_sw128(t_ring, 16, 1024);
+        // 16-byte units from one K step to the next, and from one atom of steps to the next
+        const uint32_t f_step = (f_mn ? UMMA_K * 128 : 32) / 16;
+        const uint32_t t_step = (wt ? UMMA_K * 128 : 32) / 16;
+        const uint32_t f_next = f_mn ? STEPS_PER_ATOM * f_step : f_atom / 16;
+        const uint32_t t_next = wt ? STEPS_PER_ATOM * t_step : t_atom / 16;
         if (!__all_sync(0xFFFFFFFFu, wait_phase(tempty0 + 8u * acc, aph ^ 1u, w, kWaitMmaAcc)))
           break;
         tc_fence_after_sync();
         const uint32_t d_tmem = tmem_base + (uint32_t)acc * kAccStride;
-        const uint32_t idesc = p.idesc | (uint32_t)(i.width >> 3) << 17;
+        const uint32_t idesc = (wt ? pw.idesc : p.idesc) | (uint32_t)(i.width >> 3) << 17;
         if (!dbg_check((uint32_t)i.width <= kAccStride, kChkMmaTmem, w)) break;
         for (int n = 0; n < i.blocks; ++n) {
           const int kb = i.down ? i.blocks - 1 - n : n;
           ok = __all_sync(0xFFFFFFFFu, wait_phase(full0 + 8u * s, ph, w, kWaitMmaFull));
           if (!ok) break;
           tc_fence_after_sync();
-          const uint64_t fd = fd0 + (uint32_t)(s * F_STAGE) / 16;
+          const uint64_t fd = fd0 + (uint32_t)(s * f_stage) / 16;
           const uint64_t td = td0 + (uint32_t)(s * t_stage) / 16;
           // the steps that hold elements (past them shared memory may hold anything)
-          const int left = (kWeights ? i.mn : p.k) - kb * BK;
+          const int left = (wt ? i.mn : p.k) - kb * BK;
           const int steps = min(K_STEPS, (left + UMMA_K - 1) / UMMA_K);
           if constexpr (kDebug) {
             for (int k = 0; k < steps; ++k)
               ok = ok && dbg_check(desc_in_range(fd + (k / STEPS_PER_ATOM * f_next +
                                                        k % STEPS_PER_ATOM * f_step),
-                                                 f_ring + s * F_STAGE, F_STAGE) &&
+                                                 f_ring + s * f_stage, f_stage) &&
                                        desc_in_range(td + (k / STEPS_PER_ATOM * t_next +
                                                            k % STEPS_PER_ATOM * t_step),
                                                      t_ring + s * t_stage, t_stage),
@@ -552,14 +640,18 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmF, const __grid_constant__ 
         if (++acc == kAccStages) { acc = 0; aph ^= 1u; }
       }
     }
-  } else if (!kWeights || warp < 2 + kGroupedEpiWarps) {
+  } else if (warp < 2 + kEpiWarps) {
     // ---------------------------------------------------------- epilogue
     const int q = warp & 3;                      // TMEM lane quarter of this warp
     const int strm = (warp - 2) >> 2;
     const uint32_t odd = lane & 1;
-    int acc = 0, turn = 0;
+    int acc = 0, turn = 0;                       // turn: the stream that takes the item's first chunk
     uint32_t aph = 0;
-    constexpr int kNext = 2 * kGroupedChunk;     // from one of this warp's chunks to the next
+    constexpr int kNext = kStreams * kGroupedChunk;      // from one of this warp's chunks to the next
+    const auto first_chunk = [&](int t) {
+      return (strm >= t ? strm - t : strm - t + kStreams) * kGroupedChunk;
+    };
+    const auto next_turn = [&](int t) { return t + 1 == kStreams ? 0 : t + 1; };
     // The accumulator's columns have been read.  (The arrival hands over nothing but these, whose
     // loads have completed; the pair's leader may be the other CTA.)
     const auto release = [&]() {
@@ -577,77 +669,85 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmF, const __grid_constant__ 
       // An item and this lane's place in it.
       struct At {
         Item i;
-        bool mine;
+        bool mine, has_r;
+        bool odd_feats;        // 16 bits: an odd number of features, moved one by one
         float scale;
         const uint8_t* r;
         uint8_t* d;
+        long long r_step, d_step;
       };
-      const long long d_step = p.ldd * ES, r_step = p.ldr * ES;
       const auto at_item = [&](int it) {
         At t;
         t.i = item_at(it);
         const int f = t.i.f0 + (int)rank * 128 + q * 32 + lane;
-        t.mine = f < p.feats;
-        const long long group = kWeights ? (long long)t.i.g * p.sd : 0ll;
-        const long long row = t.i.t0 + second, col = PER == 2 ? f & ~1 : f;
-        t.r = static_cast<const uint8_t*>(p.r) + (group + row * p.ldr + col) * ES;
-        t.d = static_cast<uint8_t*>(p.d) + (group + row * p.ldd + col) * ES;
-        t.scale = t.i.blocks ? p.alpha : 0.f;
-        if constexpr (!kWeights) {
-          if (p.set_scale && t.i.blocks) t.scale *= __ldg(p.set_scale + t.i.e);
+        const GroupedParams& o = t.i.wt ? pw : p;
+        const long long group = t.i.wt ? (long long)t.i.g * o.sd : 0ll;
+        t.odd_feats = PER == 2 && (o.feats & 1);
+        const bool pairs = PER == 2 && !t.odd_feats;
+        const long long row = t.i.t0 + (pairs ? second : 0u), col = pairs ? f & ~1 : f;
+        t.has_r = o.r != nullptr;
+        t.r_step = o.ldr * ES;
+        t.d_step = o.ldd * ES;
+        t.r = static_cast<const uint8_t*>(o.r) + (group + row * o.ldr + col) * ES;
+        t.d = static_cast<uint8_t*>(o.d) + (group + row * o.ldd + col) * ES;
+        t.mine = f < o.feats;
+        t.scale = t.i.blocks ? o.alpha : 0.f;
+        if constexpr (kRows) {
+          if (!t.i.wt && p.set_scale && t.i.blocks) t.scale *= __ldg(p.set_scale + t.i.e);
         }
         return t;
       };
       // The residual's words of 16 columns, `left` of them there, from `at` on.
       uint32_t res[2 * W];
-      const auto fetch = [&](auto from, const uint8_t* at, int left) {
+      const auto fetch = [&](auto from, const uint8_t* at, long long step, int left) {
         constexpr int FROM = decltype(from)::value;
 #pragma unroll
-        for (int x = 0; x < W; ++x, at += PER * r_step) {
+        for (int x = 0; x < W; ++x, at += PER * step) {
           res[FROM + x] = 0u;
           if (PER * x + (int)second < left) res[FROM + x] = *reinterpret_cast<const uint32_t*>(at);
         }
       };
       At t{};
-      if (cluster_id < num_items) {
-        t = at_item(cluster_id);
-        const int c = strm * kGroupedChunk;
-        if (p.r) {
-          fetch(IntC<0>{}, t.r + c * r_step, t.mine ? t.i.valid - c : 0);
-          fetch(IntC<W>{}, t.r + (c + 16) * r_step, t.mine ? t.i.valid - c - 16 : 0);
-        }
+      const auto fetch_first = [&](const At& a, int c) {
+        if (!a.has_r) return;
+        fetch(IntC<0>{}, a.r + c * a.r_step, a.r_step, a.mine ? a.i.valid - c : 0);
+        fetch(IntC<W>{}, a.r + (c + 16) * a.r_step, a.r_step, a.mine ? a.i.valid - c - 16 : 0);
+      };
+      if (first_item < num_items) {
+        t = at_item(first_item);
+        fetch_first(t, first_chunk(turn));
       }
-      for (int it = cluster_id; it < num_items; it += num_clusters, turn ^= 1) {
+      for (int it = first_item, it_next; it < num_items; it = it_next, turn = next_turn(turn)) {
         // The next item, its residual on its way into L2 (a token a lane: a warp's 32 features of one
         // are 64 or 128 bytes).  A chunk's residual is requested into registers when
         // those of the one before it have been used, across items.
         At next{};
-        if (it + num_clusters < num_items) {
-          next = at_item(it + num_clusters);
+        it_next = next_item(it);
+        if (it_next < num_items) {
+          next = at_item(it_next);
+          const GroupedParams& o = next.i.wt ? pw : p;
           const int f_first = next.i.f0 + (int)rank * 128 + q * 32;
-          if (p.r && f_first < p.feats) {
+          if (next.has_r && f_first < o.feats) {
             const uint8_t* const first =
-                static_cast<const uint8_t*>(p.r) + ((kWeights ? (long long)next.i.g * p.sd : 0ll) +
-                                                    (long long)next.i.t0 * p.ldr + f_first) * ES;
-            for (int c = strm * 32 + lane; c < next.i.valid; c += 64) prefetch_l2(first + c * r_step);
+                static_cast<const uint8_t*>(o.r) + ((next.i.wt ? (long long)next.i.g * o.sd : 0ll) +
+                                                    (long long)next.i.t0 * o.ldr + f_first) * ES;
+            for (int c = strm * 32 + lane; c < next.i.valid; c += 32 * kStreams)
+              prefetch_l2(first + c * next.r_step);
           }
         }
         const Item& i = t.i;
         // (debug build: what is stored lies inside d)
         if (!dbg_check(i.f0 >= 0 && i.t0 >= 0 && i.valid <= i.width &&
-                           i.t0 + i.valid <= (kWeights ? p.cols : p.rows),
+                           i.t0 + i.valid <= (i.wt ? pw.cols : p.rows),
                        kChkEpiStore, w))
           break;
-        const int next_c = (strm ^ turn ^ 1) * kGroupedChunk;
-        int c = (strm ^ turn) * kGroupedChunk;
+        const int next_c = first_chunk(next_turn(turn));
+        int c = first_chunk(turn);
         if (!__all_sync(0xFFFFFFFFu, wait_phase(tfull0 + 8u * acc, aph, w, kWaitEpilogue))) break;
         tc_fence_after_sync();
         if (c >= i.valid) {                      // no chunk of this item is this warp's
           release();
-          if (p.r) {
-            fetch(IntC<0>{}, next.r + next_c * r_step, next.mine ? next.i.valid - next_c : 0);
-            fetch(IntC<W>{}, next.r + (next_c + 16) * r_step, next.mine ? next.i.valid - next_c - 16 : 0);
-          }
+          fetch_first(next, next_c);
         }
         const uint32_t tbase = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)acc * kAccStride;
 #pragma unroll 1
@@ -663,7 +763,10 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmF, const __grid_constant__ 
             for (int x = 0; x < kGroupedChunk; ++x) a[x] = 0u;
           }
           // where the next chunk's residual lies
-          const uint8_t* const follow = last ? next.r + next_c * r_step : t.r + (c + kNext) * r_step;
+          const long long follow_step = last ? next.r_step : t.r_step;
+          const uint8_t* const follow =
+              last ? next.r + next_c * follow_step : t.r + (c + kNext) * follow_step;
+          const bool follow_r = last ? next.has_r : t.has_r;
           const int follow_left = last ? (next.mine ? next.i.valid - next_c : 0)
                                        : (t.mine ? i.valid - c - kNext : 0);
           const auto half = [&](auto number) {
@@ -671,7 +774,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmF, const __grid_constant__ 
             float v[16];
 #pragma unroll
             for (int x = 0; x < 16; ++x) v[x] = __uint_as_float(a[16 * H + x]) * t.scale;
-            if (p.r) {
+            if (t.has_r) {
 #pragma unroll
               for (int x = 0; x < W; ++x) {
                 if constexpr (LEAN == DT_F32) {
@@ -683,17 +786,27 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmF, const __grid_constant__ 
                   v[2 * x + 1] += e.y;
                 }
               }
-              fetch(IntC<W * H>{}, follow + 16 * H * r_step, follow_left - 16 * H);
             }
-            const int left = t.mine ? i.valid - c - 16 * H - (int)second : 0;
-            uint8_t* p_d = t.d + (c + 16 * H) * d_step;
+            if (follow_r) fetch(IntC<W * H>{}, follow + 16 * H * follow_step, follow_step, follow_left - 16 * H);
+            uint8_t* p_d = t.d + (c + 16 * H) * t.d_step;
+            if (PER == 2 && t.odd_feats) {       // every lane its own feature
+              const int left = t.mine ? i.valid - c - 16 * H : 0;
 #pragma unroll
-            for (int x = 0; x < W; ++x, p_d += PER * d_step) {
-              uint32_t o;
-              if constexpr (LEAN == DT_F32) o = __float_as_uint(v[x]);
-              else o = swap_halves(LEAN == DT_F16 ? pack_f16x2(v[2 * x], v[2 * x + 1])
-                                                  : pack_bf16x2(v[2 * x], v[2 * x + 1]), odd);
-              if (PER * x < left) *reinterpret_cast<uint32_t*>(p_d) = o;
+              for (int x = 0; x < 16; x += 2, p_d += 2 * t.d_step) {
+                const uint32_t u = LEAN == DT_F16 ? pack_f16x2(v[x], v[x + 1]) : pack_bf16x2(v[x], v[x + 1]);
+                if (x < left) *reinterpret_cast<uint16_t*>(p_d) = (uint16_t)u;
+                if (x + 1 < left) *reinterpret_cast<uint16_t*>(p_d + t.d_step) = (uint16_t)(u >> 16);
+              }
+            } else {
+              const int left = t.mine ? i.valid - c - 16 * H - (int)second : 0;
+#pragma unroll
+              for (int x = 0; x < W; ++x, p_d += PER * t.d_step) {
+                uint32_t o;
+                if constexpr (LEAN == DT_F32) o = __float_as_uint(v[x]);
+                else o = swap_halves(LEAN == DT_F16 ? pack_f16x2(v[2 * x], v[2 * x + 1])
+                                                    : pack_bf16x2(v[2 * x], v[2 * x + 1]), odd);
+                if (PER * x < left) *reinterpret_cast<uint32_t*>(p_d) = o;
+              }
             }
           };
           half(IntC<0>{});
@@ -705,7 +818,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmF, const __grid_constant__ 
     } else {
       const auto bytes = [](int dt) { return dt == DT_F32 ? 4 : 2; };
       const bool r16 = p.r_dt != DT_F32;
-      for (int it = cluster_id; it < num_items; it += num_clusters, turn ^= 1) {
+      for (int it = first_item; it < num_items; it = next_item(it), turn = next_turn(turn)) {
         const Item i = item_at(it);
         const int f = i.f0 + (int)rank * 128 + q * 32 + lane;
         const bool mine = f < p.feats;
@@ -725,7 +838,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmF, const __grid_constant__ 
         const EpiMatrix rm = place(p.r, p.ldr, p.r_dt), zm = place(p.z, p.ldz, p.z_dt),
                         dm = place(p.d, p.ldd, p.d_dt);
         float scale = i.blocks ? p.alpha : 0.f, bias = 0.f;
-        if constexpr (!kWeights) {
+        if constexpr (kRows) {
           if (p.set_scale && i.blocks) scale *= __ldg(p.set_scale + i.e);
         }
         if constexpr (kFull) {
@@ -759,7 +872,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmF, const __grid_constant__ 
               factor = c + lane < i.valid ? __ldg(p.row_scale + i.t0 + c + lane) : 1.f;
           }
         };
-        const int c_first = (strm ^ turn) * kGroupedChunk;
+        const int c_first = first_chunk(turn);
         if (c_first < i.valid) {
           if (p.r) {
             if (r16) {
@@ -831,20 +944,20 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmF, const __grid_constant__ 
         if (++acc == kAccStages) { acc = 0; aph ^= 1u; }
       }
     }
-  } else {
+  } else if constexpr (kWeights) {
     // ---------------------------------------------------------- zeroing (weights form)
     int s = 0;
     uint32_t phases = 0;                         // a bit per stage: its tail barrier's phase
-    for (int it = cluster_id; it < num_items; it += num_clusters) {
+    for (int it = first_item; it < num_items; it = next_item(it)) {
       const Item i = item_at(it);
-      if (i.blocks > 0 && i.mn % UMMA_K != 0) {
+      if (i.wt && i.blocks > 0 && i.mn % UMMA_K != 0) {
         const int at = i.down ? s : (s + i.blocks - 1) % S;
         if (!__all_sync(0xFFFFFFFFu, wait_phase<true>(tail0 + 8u * at, phases >> at & 1u, w,
                                                       kWaitProducer)))
           break;
         // rows [from, to) of every 128-byte wide atom column
         const int from = i.mn - (i.blocks - 1) * BK, to = (from + UMMA_K - 1) / UMMA_K * UMMA_K;
-        uint8_t* const sf = gbase + (f_ring + at * F_STAGE - base);
+        uint8_t* const sf = gbase + (f_ring + at * f_stage - base);
         uint8_t* const st = gbase + (t_ring + at * t_stage - base);
         const int boxes = i.width / CG / ATOM_K;
         for (int j = 0; j < F_BOXES + boxes; ++j) {

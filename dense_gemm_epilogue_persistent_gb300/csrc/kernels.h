@@ -93,22 +93,23 @@ inline const void* linear_kernel_for(int ab_bytes, int cta_group, int ka, int ep
 const void* split_kernel_for(int ab_bytes);
 
 // kern_grouped.cu, compiled once per input width and form: products over groups of rows, of
-// the rows (weights = 0) or of the weights (1; 16 bits), by CTA group and the type of the lean
-// epilogue (16 bits; -1: the whole one).
-#define GB300_GROUPED_NAME_(ab, weights) kernel_grouped_ab##ab##_w##weights
-#define GB300_GROUPED_NAME(ab, weights) GB300_GROUPED_NAME_(ab, weights)
+// the rows (form 0), of the weights (1; 16 bits), of both in one launch (2; 16 bits), by CTA
+// group and the type of the lean epilogue (16 bits; -1: the whole one).
+#define GB300_GROUPED_NAME_(ab, form) kernel_grouped_ab##ab##_f##form
+#define GB300_GROUPED_NAME(ab, form) GB300_GROUPED_NAME_(ab, form)
 const void* GB300_GROUPED_NAME(2, 0)(int cta_group, int lean);
 const void* GB300_GROUPED_NAME(2, 1)(int cta_group, int lean);
+const void* GB300_GROUPED_NAME(2, 2)(int cta_group, int lean);
 const void* GB300_GROUPED_NAME(1, 0)(int cta_group, int lean);
 const void* GB300_GROUPED_NAME(4, 0)(int cta_group, int lean);
-inline const void* grouped_kernel_for(int ab_bytes, int cta_group, bool weights, int lean) {
-  if (weights) return ab_bytes == 2 ? GB300_GROUPED_NAME(2, 1)(cta_group, lean) : nullptr;
-  switch (ab_bytes) {
-    case 2: return GB300_GROUPED_NAME(2, 0)(cta_group, lean);
-    case 1: return GB300_GROUPED_NAME(1, 0)(cta_group, lean);
-    case 4: return GB300_GROUPED_NAME(4, 0)(cta_group, lean);
-  }
-  return nullptr;
+inline const void* grouped_kernel_for(int ab_bytes, int cta_group, int form, int lean) {
+  if (ab_bytes == 2)
+    return form == 0   ? GB300_GROUPED_NAME(2, 0)(cta_group, lean)
+           : form == 1 ? GB300_GROUPED_NAME(2, 1)(cta_group, lean)
+                       : GB300_GROUPED_NAME(2, 2)(cta_group, lean);
+  if (form != 0) return nullptr;
+  return ab_bytes == 1   ? GB300_GROUPED_NAME(1, 0)(cta_group, lean)
+         : ab_bytes == 4 ? GB300_GROUPED_NAME(4, 0)(cta_group, lean) : nullptr;
 }
 
 }  // namespace gb300

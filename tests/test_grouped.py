@@ -317,7 +317,7 @@ def test_forward_forced_configurations(gemm, cfg, ab):
 @pytest.mark.gpu
 @pytest.mark.parametrize("cfg", [dict(cluster_m=2), dict(split_k=2), dict(stream_k=2),
                                  dict(cta_group=2, tile_n=96),
-                                 dict(cta_group=2, tile_n=256, stages=4)])
+                                 dict(cta_group=2, tile_n=256, stages=12)])
 def test_forced_configurations_it_cannot_take(gemm, cfg):
     d, a, b, offsets = (torch.zeros(8, 64, device="cuda").half() for _ in range(4))
     gemm.set_config(**cfg)
