@@ -156,13 +156,14 @@ gemm_status_t prepare(gemm_handle* h, const Product& p, const gemm_config_t& c, 
   k.has_operands = p.weights ? p.rows > 0 : p.k > 0;
   if (k.has_operands) {
     const int box = gb300::kGroupedMBox;
+    const int64_t sets = p.stride_f ? p.sets : 1;      // (a map's stride may not be 0)
     const bool ok =
         p.weights
             ? encode_stack(h->encode, &f, p.f, p.f_type, p.feats, p.rows, 1, p.ldf, 0, box) &&
                   encode_stack(h->encode, &t, p.t, p.t_type, p.cols, p.rows, 1, p.ldt, 0, box)
-            : (p.f_mn ? encode_stack(h->encode, &f, p.f, p.f_type, p.feats, p.k, p.sets, p.ldf,
+            : (p.f_mn ? encode_stack(h->encode, &f, p.f, p.f_type, p.feats, p.k, sets, p.ldf,
                                      p.stride_f, c.tile_k)
-                      : encode_stack(h->encode, &f, p.f, p.f_type, p.k, p.feats, p.sets, p.ldf,
+                      : encode_stack(h->encode, &f, p.f, p.f_type, p.k, p.feats, sets, p.ldf,
                                      p.stride_f, f_rows_of(p))) &&
                   encode_stack(h->encode, &t, p.t, p.t_type, p.k, p.rows, 1, p.ldt, 0, unit) &&
                   encode_stack(h->encode, whole, p.t, p.t_type, p.k, p.rows, 1, p.ldt, 0,
@@ -178,6 +179,7 @@ gemm_status_t prepare(gemm_handle* h, const Product& p, const gemm_config_t& c, 
   k.tiles_c = p.weights ? (int)cdiv(p.cols, c.tile_n) : 1;
   k.stages = c.stages;
   k.strip = c.group_m;
+  k.set_step = p.stride_f != 0;
   k.by_bn = gb300::fast_div(k.bn);
   k.by_strip = gb300::fast_div(k.strip * k.tiles_f);
   k.by_group = gb300::fast_div(k.tiles_f * k.tiles_c);

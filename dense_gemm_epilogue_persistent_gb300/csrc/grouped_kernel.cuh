@@ -75,6 +75,7 @@ struct GroupedParams {
   int alternate;             // odd waves of items walk the k-blocks from the last one down (8192^3 bf16
                              // 659 us, 675 without)
   int strip;                 // token (or column) tiles walked together
+  int set_step;              // 0: all sets are one matrix
   int f_mn;                  // rows form: weights with contiguous features
   int has_operands;          // the tensor maps are encoded
   int skip_none;             // groups without weights are left out: their d is r already
@@ -136,7 +137,7 @@ constexpr int grouped_threads(int form, int lean) {
 constexpr int grouped_stage_bytes(int cta_group, int bn, int f_rows) {
   return kGroupedKA * (f_rows + bn / cta_group) * 128;
 }
-constexpr int grouped_bar_bytes() { return 8 * (4 * kGroupedMaxStages + 5) + 16 + 64 + 80; }
+constexpr int grouped_bar_bytes() { return 8 * (4 * kGroupedMaxStages + 5) + 16 + 128 + 80; }
 constexpr int grouped_smem(int cta_group, int bn, int f_rows, int stages, int groups) {
   return 1024 + stages * grouped_stage_bytes(cta_group, bn, f_rows) + grouped_bar_bytes() +
          8 * (groups + 1);
@@ -299,9 +300,9 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmF, const __grid_constant__ 
   const uint32_t never_bar = tempty0 + 16u, holder = never_bar + 8u;
   volatile uint32_t* const holder_ptr = reinterpret_cast<volatile uint32_t*>(gbase + (holder - base));
   volatile uint32_t* const abort_ptr = holder_ptr + 1;
-  int* const sums = reinterpret_cast<int*>(gbase + (holder + 16u - base));    // one per warp
+  long long* const sums = reinterpret_cast<long long*>(gbase + (holder + 16u - base));    // one per warp
   uint32_t* const magic = reinterpret_cast<uint32_t*>(sums + 16);     // ceil(2^32 / n), [17]
-  int* const offs = sums + 16 + 20;              // clamped offsets, [groups + 1]
+  int* const offs = reinterpret_cast<int*>(magic) + 20;        // clamped offsets, [groups + 1]
   int* const starts = offs + p.groups + 1;       // a group's first item, [groups + 1] (rows form)
 
   if (threadIdx.x == 0) {
@@ -358,26 +359,29 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmF, const __grid_constant__ 
   if constexpr (kRows) {
     const int share = (p.groups + (int)blockDim.x - 1) / (int)blockDim.x;
     const int g0 = min((int)threadIdx.x * share, p.groups), g1 = min(g0 + share, p.groups);
-    int mine = 0;
+    // (64 bits: groups that lie on one another may together hold any number of tiles; those past
+    // 2^30 items are left out)
+    const auto items_to = [&](long long tiles) { return (int)min(tiles * p.tiles_f, 1ll << 30); };
+    long long mine = 0;
     for (int g = g0; g < g1; ++g) mine += tiles_of(g, max(0, offs[g + 1] - offs[g]));
-    int upto = mine;                             // inclusive over the warp, then the block
+    long long upto = mine;                       // inclusive over the warp, then the block
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+      const long long v = __shfl_up_sync(0xFFFFFFFFu, upto, o);
       if (lane >= o) upto += v;
     }
     if (lane == 31) sums[warp] = upto;
     __syncthreads();
-    int at = upto - mine, total = 0;
+    long long at = upto - mine, total = 0;
     for (int i = 0; i < (int)blockDim.x / 32; ++i) {
       if (i < warp) at += sums[i];
       total += sums[i];
     }
     for (int g = g0; g < g1; ++g) {
-      starts[g] = at * p.tiles_f;
+      starts[g] = items_to(at);
       at += tiles_of(g, max(0, offs[g + 1] - offs[g]));
     }
-    rows_items = total * p.tiles_f;
+    rows_items = items_to(total);
     if (threadIdx.x == 0) starts[p.groups] = rows_items;
     __syncthreads();
   }
@@ -539,7 +543,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmF, const __grid_constant__ 
               }
             }
           } else if (kRows) {
-            const int k0 = kb * BK;
+            const int k0 = kb * BK, set = i.e * p.set_step;
             const int atoms = min(KA, (p.k - k0 + ATOM_K - 1) / ATOM_K);   // those with elements
             const uint32_t fb = full0 + 8u * s;
             const uint32_t bar = PAIR ? map_to_rank(fb, 0) : fb;
@@ -548,10 +552,10 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmF, const __grid_constant__ 
                                               (uint32_t)(atoms * width) * 128u));
             if (p.f_mn) {
               for (int j = 0; j < F_BOXES; ++j)
-                OperandLoad<CG, false>::load(sf + j * MN_ATOM, &tmF, bar, f0 + j * ATOM_K, k0, i.e, 0, pol);
+                OperandLoad<CG, false>::load(sf + j * MN_ATOM, &tmF, bar, f0 + j * ATOM_K, k0, set, 0, pol);
             } else {
               for (int a = 0; a < atoms; ++a)
-                OperandLoad<CG, false>::load(sf + a * f_atom, &tmF, bar, k0 + a * ATOM_K, f0, i.e, 0, pol);
+                OperandLoad<CG, false>::load(sf + a * f_atom, &tmF, bar, k0 + a * ATOM_K, f0, set, 0, pol);
             }
             // a whole tile's tokens in one box an atom, else in units (adapters' first product, 8191
             // rows of 4096 by 7 x 64 bf16: 21.5 us, 22.5 in units alone; 8192^3 659, 673)

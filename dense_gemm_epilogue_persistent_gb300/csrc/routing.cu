@@ -594,8 +594,9 @@ gemm_status_t check_route(const gemm_route_t& p) {
       !aligned_to(p.index, p.index_bytes))
     return GEMM_ERR_MISALIGNED;
   if (p.T * p.k > 0 && (!p.index || !p.slot || p.ldi < p.k)) return GEMM_ERR_INVALID_ARG;
-  if (p.T * p.k > 0 && (p.slot == p.offsets || p.slot == p.source || p.source == p.offsets))
-    return GEMM_ERR_INVALID_ARG;
+  if (p.T * p.k > 0 && (p.slot == p.offsets || p.slot == p.source || p.source == p.offsets ||
+                        p.index == p.slot || p.index == p.source || p.index == p.offsets))
+    return GEMM_ERR_INVALID_ARG;       // (index is read again once slot has been written)
   return GEMM_OK;
 }
 

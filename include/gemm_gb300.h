@@ -572,7 +572,7 @@ gemm_status_t gemm_linear_bwd(gemm_handle_t h, const gemm_linear_bwd_t* p,
  *   index [T, k]: 4- or 8-byte signed integers (index_bytes), rows ldi apart, each
  *   aligned to its size.  k at most 128, T k at most 2^31 - 8193, E at most 4096.
  *   offsets [E + 1], slot [T k], source [T k] (optional): int32.
- * T = 0: offsets are 0. */
+ * T = 0: offsets are 0.  (slot serves as a workspace before it holds the places.) */
 typedef struct {
   int64_t T, k, E;
   int index_bytes;
@@ -588,7 +588,8 @@ gemm_status_t gemm_route(gemm_handle_t h, const gemm_route_t* p, struct CUstream
 /* Each token's row to the places of its choices:
  *     y(slot(t k + j), c) = x(t, c),   y_scale(slot(t k + j)) = scale(t)
  * A choice whose slot is outside 0..R-1 is left out; rows of y that no choice
- * has stay as they were.  (Two choices of one slot: either's row.)
+ * has stay as they were.  (Two choices of one slot: each element of that row is
+ * either's.)
  *   x [T, H], y [R, H] of one type (any but TF32); slot [T k]: int32; scale [T],
  *   y_scale [R]: fp32, both or neither (the row scales of an 8-bit x).
  * The gradient of x is gemm_combine's y of y's gradient, without weights. */
@@ -610,7 +611,8 @@ gemm_status_t gemm_dispatch(gemm_handle_t h, const gemm_dispatch_t* p, struct CU
  * in fp32, in order of j, rounded once.  A choice whose slot is outside 0..R-1
  * adds nothing, whatever its weight.
  *   ys [R, H], r [T, H] (optional: 0), y [T, H]: F32, F16 or BF16 each.  weight
- *   [T k]: fp32, optional (1).  y may be r (same type and leading dimension). */
+ *   [T k]: fp32, optional (1).  y may be r (same type and leading dimension).
+ * A launch is under the watchdog of gemm_sync_status. */
 typedef struct {
   int64_t T, k, H, R;
   gemm_dtype_t type, r_type, y_type;
@@ -631,7 +633,8 @@ gemm_status_t gemm_combine(gemm_handle_t h, const gemm_combine_t* p, struct CUst
  * of dys that no choice has stay as they were.
  *   dy [T, H], ys [R, H], dys [R, H]: one type, F32, F16 or BF16.  weight [T k]:
  *   fp32, optional (1).  dys, dweight [T k] fp32: each optional; ys is read
- *   for dweight only.  dys may be ys (same leading dimension). */
+ *   for dweight only.  dys may be ys (same leading dimension; no two choices of one
+ *   slot then). */
 typedef struct {
   int64_t T, k, H, R;
   gemm_dtype_t type;
@@ -656,9 +659,10 @@ gemm_status_t gemm_combine_bwd(gemm_handle_t h, const gemm_combine_bwd_t* p,
  * unrounded z.  A group whose index is outside 0..sets-1 has no weights: z = 0,
  * D = R there.  Rows of no group (before offsets(0), behind offsets(groups), of
  * groups of no or negative size) stay as they were in Z and D; offsets are clamped to
- * 0..M.  (Groups that overlap: the rows that they share hold either's values.)
+ * 0..M.  (Groups that overlap: each element of the rows that they share is either's,
+ * and undefined where D is R.)
  *   A [M, K]: K contiguous.  B: `sets` matrices [N, K], strideB elements
- *   apart (a multiple of 16 bytes), each K-major or (8 and 16 bits) with N
+ *   apart (a multiple of 16 bytes; 0: one matrix for all), each K-major or (8 and 16 bits) with N
  *   contiguous (layoutB, ldb).  Types as for gemm_linear.  K = 0: the sum is 0.
  *   offsets [groups + 1], index [groups] (optional): int32.  groups and sets at
  *   most 4096; without an index sets >= groups.
@@ -666,8 +670,8 @@ gemm_status_t gemm_combine_bwd(gemm_handle_t h, const gemm_combine_bwd_t* p,
  *   F16 or BF16, optional.  R, Z: optional.  R, Z and D: F32, F16 or BF16 each.
  * D may be R (same type and leading dimension).  Of a configuration forced with
  * gemm_set_config cta_group, tile_n (the widest tile, in tokens; a multiple of 64 in
- * pairs), stages and inject_stall apply; multicast clusters, split_k and stream_k are
- * refused.  A launch is under the watchdog of gemm_sync_status. */
+ * pairs), stages, group_m and inject_stall apply; multicast clusters, split_k and stream_k
+ * are refused.  A launch is under the watchdog of gemm_sync_status. */
 typedef struct {
   int64_t M, N, K, groups, sets;
   gemm_dtype_t a_type, b_type, bias_type, r_type, z_type, d_type;
@@ -735,7 +739,7 @@ gemm_status_t gemm_grouped_linear_bwd(gemm_handle_t h, const gemm_grouped_linear
  *     u = x A(e)^T                          rounded to `type`
  *     d = r + scale(e) * (u B(e)^T)
  * A request whose index is outside 0..adapters-1 has none: d = r there.  Rows of
- * no request stay as they were in d.
+ * no request stay as they were in d.  (Requests may not share rows.)
  *   x [M, K]; A: `adapters` matrices [rank, K], B: as many [N, rank], strideA
  *   and strideB elements apart (multiples of 16 bytes); u [M, rank]: a workspace that
  *   the call overwrites (calls that may overlap need one each); all of one type,

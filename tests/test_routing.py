@@ -48,7 +48,8 @@ OK, INVALID, DTYPE, ALIGN = (0, G.GEMM_ERR_INVALID_ARG, G.GEMM_ERR_UNSUPPORTED_D
     (dict(E=-1), INVALID), (dict(T=1 << 30, k=4), INVALID), (dict(ldi=2), INVALID),
     (dict(index=None), INVALID), (dict(slot=None), INVALID), (dict(offsets=None), INVALID),
     (dict(T=0, offsets=None), INVALID), (dict(slot=P[1]), INVALID), (dict(source=P[2]), INVALID),
-    (dict(source=P[1]), INVALID), (dict(index_bytes=2), DTYPE), (dict(index_bytes=0), DTYPE),
+    (dict(source=P[1]), INVALID), (dict(index=P[2]), INVALID), (dict(index=P[3]), INVALID),
+    (dict(index=P[1]), INVALID), (dict(index_bytes=2), DTYPE), (dict(index_bytes=0), DTYPE),
     (dict(index=P[0] + 2), ALIGN), (dict(index_bytes=8, index=P[0] + 4), ALIGN),
     (dict(offsets=P[1] + 2), ALIGN), (dict(slot=P[2] + 1), ALIGN), (dict(source=P[3] + 3), ALIGN),
 ])
