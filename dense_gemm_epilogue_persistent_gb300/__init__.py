@@ -610,9 +610,9 @@ def _shape(t, what):
     return shape
 
 
-def _rows(t, shape, what, device, code=None):
-    """(address, row stride) of a matrix of that shape whose rows are contiguous, on GPU
-    `device` and of type `code` if given; (0, 0) for None."""
+def _rows(t, shape, what, device, code=None, own=False):
+    """(address, row stride) of a matrix of that shape (`own`: which was read off it) whose rows
+    are contiguous, on GPU `device` and of type `code` if given; (0, 0) for None."""
     if t is None:
         return 0, 0
     try:
@@ -620,7 +620,7 @@ def _rows(t, shape, what, device, code=None):
             raise _elsewhere(t, what, device)
     except AttributeError:
         pass
-    if t.shape != shape:
+    if not own and t.shape != shape:
         raise GemmError(GEMM_ERR_INVALID_ARG, f"{what}: shape {tuple(t.shape)}, not {tuple(shape)}")
     if code is not None and _CODE_OF.get(t.dtype) != code and _code(t, what) != code:
         raise GemmError(GEMM_ERR_UNSUPPORTED_DTYPE, f"{what}: {t.dtype}")
@@ -674,8 +674,9 @@ def _vector(t, n, what, device, code=None):
     return t.data_ptr()
 
 
-def _integers(t, shape, what, device):
-    """Address of a contiguous tensor of int32 of that shape on GPU `device`; 0 for None."""
+def _integers(t, shape, what, device, own=False):
+    """Address of a contiguous tensor of int32 of that shape (`own`: which was read off it) on GPU
+    `device`; 0 for None."""
     if t is None:
         return 0
     try:
@@ -683,9 +684,9 @@ def _integers(t, shape, what, device):
             raise _elsewhere(t, what, device)
     except AttributeError:
         pass
-    if _integer_bytes(t, what) != 4:
+    if _BYTES_OF.get(t.dtype) != 4 and _integer_bytes(t, what) != 4:
         raise GemmError(GEMM_ERR_UNSUPPORTED_DTYPE, f"{what}: {t.dtype}")
-    _packed(t, shape, what)
+    _packed(t, shape, what, own)
     return t.data_ptr()
 
 
@@ -703,9 +704,9 @@ def _integer_bytes(t, what):
     return n
 
 
-def _packed(t, shape, what):
-    """Refuses a tensor that is not contiguous of that shape."""
-    if t.shape != shape:
+def _packed(t, shape, what, own=False):
+    """Refuses a tensor that is not contiguous of that shape (`own`: which was read off it)."""
+    if not own and t.shape != shape:
         raise GemmError(GEMM_ERR_INVALID_ARG, f"{what}: shape {tuple(t.shape)}, not {tuple(shape)}")
     try:
         if t.is_contiguous():
@@ -735,19 +736,20 @@ def _table(t, shape, what, device, code=None):
     return t.data_ptr()
 
 
-def _choices(slot, T, what="slot"):
-    """k of a [T, k] tensor of places."""
-    shape = _shape(slot, what)
+def _choices(slot, T, device):
+    """(address, k) of a [T, k] tensor of places on GPU `device`."""
+    shape = _shape(slot, "slot")
     if shape[0] != T:
-        raise GemmError(GEMM_ERR_INVALID_ARG, f"{what}: {shape[0]} tokens, not {T}")
-    return shape[1]
+        raise GemmError(GEMM_ERR_INVALID_ARG, f"slot: {shape[0]} tokens, not {T}")
+    return _integers(slot, shape, "slot", device, own=True), shape[1]
 
 
-def _groups(offsets, what="offsets"):
-    """Groups of a vector of their bounds."""
-    if len(offsets.shape) != 1 or offsets.shape[0] < 1:
-        raise GemmError(GEMM_ERR_INVALID_ARG, f"{what}: shape {tuple(offsets.shape)}")
-    return offsets.shape[0] - 1
+def _bounds(offsets, device):
+    """(address, groups) of a vector of the groups' bounds on GPU `device`."""
+    shape = offsets.shape
+    if len(shape) != 1 or shape[0] < 1:
+        raise GemmError(GEMM_ERR_INVALID_ARG, f"offsets: shape {tuple(shape)}")
+    return _integers(offsets, shape, "offsets", device, own=True), shape[0] - 1
 
 
 def _stack(t, shape, what, device, code=None, k_major=False):
@@ -950,10 +952,10 @@ class Gemm:
         T, k = shape
         dev = self.device
         width = _integer_bytes(index, "index")
-        p_index, ldi = _rows(index, shape, "index", dev)
-        E = _groups(offsets)
+        p_index, ldi = _rows(index, shape, "index", dev, own=True)
+        p_offsets, E = _bounds(offsets, dev)
         st = self._lib.gemm_route(self.handle, _ROUTE.pack(
-            T, k, E, width, p_index, ldi, _integers(offsets, (E + 1,), "offsets", dev),
+            T, k, E, width, p_index, ldi, p_offsets,
             _integers(slot, shape, "slot", dev), _integers(source, (T * k,), "source", dev)),
             stream and _stream(stream))
         if st:
@@ -964,10 +966,10 @@ class Gemm:
         gemm_dispatch in the C header."""
         shape = _shape(x, "x")
         T, H = shape
-        k, R = _choices(slot, T), _shape(y, "y")[0]
-        t, dev = _code(x, "x"), self.device
+        t, dev, R = _code(x, "x"), self.device, _shape(y, "y")[0]
+        p_slot, k = _choices(slot, T, dev)
         st = self._lib.gemm_dispatch(self.handle, _DISPATCH.pack(
-            T, k, H, R, t, *_rows(x, shape, "x", dev), _integers(slot, (T, k), "slot", dev),
+            T, k, H, R, t, *_rows(x, shape, "x", dev, own=True), p_slot,
             _vector(scale, T, "scale", dev, GEMM_F32), *_rows(y, (R, H), "y", dev, t),
             _vector(y_scale, R, "y_scale", dev, GEMM_F32)), stream and _stream(stream))
         if st:
@@ -978,13 +980,13 @@ class Gemm:
         weight [T, k]; see gemm_combine in the C header."""
         shape = _shape(y, "y")
         T, H = shape
-        k, R = _choices(slot, T), _shape(ys, "ys")[0]
-        dev = self.device
+        dev, R = self.device, _shape(ys, "ys")[0]
+        p_slot, k = _choices(slot, T, dev)
         st = self._lib.gemm_combine(self.handle, _COMBINE.pack(
             T, k, H, R, _code(ys, "ys"), 0 if residual is None else _code(residual, "residual"),
-            _code(y, "y"), *_rows(ys, (R, H), "ys", dev), _integers(slot, (T, k), "slot", dev),
+            _code(y, "y"), *_rows(ys, (R, H), "ys", dev), p_slot,
             _table(weight, (T, k), "weight", dev, GEMM_F32),
-            *_rows(residual, shape, "residual", dev), *_rows(y, shape, "y", dev)),
+            *_rows(residual, shape, "residual", dev), *_rows(y, shape, "y", dev, own=True)),
             stream and _stream(stream))
         if st:
             raise GemmError(st, "gemm_combine")
@@ -995,10 +997,11 @@ class Gemm:
         shape = _shape(dy, "dy")
         T, H = shape
         rows = dys if dys is not None else ys
-        k, R = _choices(slot, T), 0 if rows is None else _shape(rows, "dys or ys")[0]
+        R = 0 if rows is None else _shape(rows, "dys or ys")[0]
         t, dev = _code(dy, "dy"), self.device
+        p_slot, k = _choices(slot, T, dev)
         st = self._lib.gemm_combine_bwd(self.handle, _COMBINE_BWD.pack(
-            T, k, H, R, t, *_rows(dy, shape, "dy", dev), _integers(slot, (T, k), "slot", dev),
+            T, k, H, R, t, *_rows(dy, shape, "dy", dev, own=True), p_slot,
             _table(weight, (T, k), "weight", dev, GEMM_F32), *_rows(ys, (R, H), "ys", dev, t),
             *_rows(dys, (R, H), "dys", dev, t),
             _table(dweight, (T, k), "dweight", dev, GEMM_F32)), stream and _stream(stream))
@@ -1016,7 +1019,8 @@ class Gemm:
         sets, N, inner = _stack_shape(b, "b")
         if inner != K:
             raise GemmError(GEMM_ERR_INVALID_ARG, f"b: shape {(sets, N, inner)}, not {(sets, N, K)}")
-        dev, groups = self.device, _groups(offsets)
+        dev = self.device
+        p_offsets, groups = _bounds(offsets, dev)
         pb, ldb, lb, stride = _stack(b, (sets, N, K), "b", dev)
         out, cols = (M, N), (sets, N)
         st = self._lib.gemm_grouped_linear(self.handle, _GROUPED.pack(
@@ -1024,8 +1028,8 @@ class Gemm:
             0 if bias is None else _code(bias, "bias"),
             0 if residual is None else _code(residual, "residual"),
             0 if z is None else _code(z, "z"), _code(d, "d"), lb, _activation(activation), alpha,
-            _integers(offsets, (groups + 1,), "offsets", dev),
-            _integers(index, (groups,), "index", dev), *_rows(a, (M, K), "a", dev), pb, ldb, stride,
+            p_offsets, _integers(index, (groups,), "index", dev),
+            *_rows(a, (M, K), "a", dev, own=True), pb, ldb, stride,
             _vector(row_scale, M, "row_scale", dev, GEMM_F32),
             _table(col_scale, cols, "col_scale", dev, GEMM_F32), _table(bias, cols, "bias", dev),
             *_rows(residual, out, "residual", dev), *_rows(z, out, "z", dev),
@@ -1043,7 +1047,8 @@ class Gemm:
         M, N = out
         inner = a if a is not None else da if da is not None else b if b is not None else db
         K = 0 if inner is None else inner.shape[-1]
-        t, dev, groups = _code(dd, "dd"), self.device, _groups(offsets)
+        t, dev = _code(dd, "dd"), self.device
+        p_offsets, groups = _bounds(offsets, dev)
         rows_a, stack_b = (M, K), (groups, N, K)
         pb, ldb, _, strideb = _stack(b, stack_b, "b", dev, t, k_major=True)
         pdb, lddb, _, stridedb = _stack(db, stack_b, "db", dev, k_major=True)
@@ -1051,7 +1056,7 @@ class Gemm:
             M, N, K, groups, t, 0 if da is None else _code(da, "da"),
             0 if db is None else _code(db, "db"), 0 if dbias is None else _code(dbias, "dbias"),
             _activation(activation), int(accumulate), alpha,
-            _integers(offsets, (groups + 1,), "offsets", dev), *_rows(dd, out, "dd", dev),
+            p_offsets, *_rows(dd, out, "dd", dev, own=True),
             *_rows(z, out, "z", dev, t), *_rows(a, rows_a, "a", dev, t), pb, ldb, strideb,
             *_rows(dz, out, "dz", dev, t), *_rows(da, rows_a, "da", dev), pdb, lddb, stridedb,
             _table(dbias, (groups, N), "dbias", dev)), stream and _stream(stream))
@@ -1069,13 +1074,14 @@ class Gemm:
             raise GemmError(GEMM_ERR_INVALID_ARG, f"a: shape {(n, rank, inner)}, not {(n, rank, K)}")
         out = _shape(d, "d")
         N = out[1]
-        t, dev, requests = _code(x, "x"), self.device, _groups(offsets)
+        t, dev = _code(x, "x"), self.device
+        p_offsets, requests = _bounds(offsets, dev)
         pa, lda, _, stride_a = _stack(a, (n, rank, K), "a", dev, t, k_major=True)
         pb, ldb, _, stride_b = _stack(b, (n, N, rank), "b", dev, t, k_major=True)
         st = self._lib.gemm_adapters(self.handle, _ADAPTERS.pack(
             M, N, K, rank, requests, n, t, 0 if residual is None else _code(residual, "residual"),
-            _code(d, "d"), _integers(offsets, (requests + 1,), "offsets", dev),
-            _integers(index, (requests,), "index", dev), *_rows(x, (M, K), "x", dev),
+            _code(d, "d"), p_offsets, _integers(index, (requests,), "index", dev),
+            *_rows(x, (M, K), "x", dev, own=True),
             pa, lda, stride_a, pb, ldb, stride_b, _vector(scale, n, "scale", dev, GEMM_F32),
             *_rows(u, (M, rank), "u", dev, t), *_rows(residual, (M, N), "residual", dev),
             *_rows(d, (M, N), "d", dev)), stream and _stream(stream))

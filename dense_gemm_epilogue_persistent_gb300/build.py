@@ -78,7 +78,7 @@ LINEAR_UNITS = [(f"kern_linear_ab{ab}_e{epw}_p{epi}", "kern_linear.cu",
 # header they include): none of them names a multicast TMA load.
 NOMC_FILES = ["gemm_api.cu", "norm.cu", "linear.cu", "kern_plain.cu", "kern_linear.cu",
               "kern_split.cu", "routing.cu", "grouped.cu", "kern_grouped.cu", "gemm_kernel.cuh",
-              "split_kernel.cuh", "grouped_kernel.cuh", "activations.cuh", "rows.cuh",
+              "split_kernel.cuh", "grouped_kernel.cuh", "adapters_few.cuh", "activations.cuh", "rows.cuh",
               "ptx.cuh", "kernels.h", "handle.h", "rows_host.h"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -403,33 +403,35 @@ gemm_status_t check_grouped_bwd(const gemm_grouped_linear_bwd_t& p) {
   return GEMM_OK;
 }
 
-// Blocks that share a request's rows in the kernels for few of them.
+// Clusters that share a request's rows in the kernel for few of them.
 int few_splits(const gemm_adapters_t& p) {
   return (int)std::min<int64_t>(4, std::max<int64_t>(1, p.M - p.requests + 1));
 }
 
-// Whether a call takes these (adapters_few.cuh) rather than products over groups: by estimates of
-// both, microseconds, fitted on GB300 to 1 to 256 requests of 1 to 16 rows, ranks 16 to 128, 1024^2
-// to 8192^2.  The first grow with the rows' weights and, since the host does not know whose the
-// rows are, with those that one request may have alone; the second with the inner size and
-// the tiles, of which every request has its own.  (Few, products: 64 requests of a row, 4096 x
-// 4096, rank 16 10.3, 36.2; rank 128 30.6, 37.9; of 2 rows, rank 64 30.2, 37.2; 256 requests of a row,
-// rank 16 18.8, 99.8; one request of 16 rows 13.4, 20.5.  255 requests of a row and one of 769, which
-// the choice has to keep from them: 672, 112.)
+// Whether a call takes it (adapters_few.cuh) rather than products over groups: by estimates of
+// both, microseconds, fitted on GB300 to 1 to 256 requests of 1 to 16 rows, ranks 8 to 128, 1024^2
+// to 8192^2.  The first grows with the clusters and the rows' weights, or with the rows that one cluster
+// goes through: the host does not know whose the rows are, so as many as one request may
+// have; the second with the inner size and the tiles, of which every request has its own.  (Few, products:
+// 64 requests of a row, 4096 x 4096, rank 16 8.3, 42.6; rank 64 24.8, 40.7; 8192 x 8192, rank 128 69.3,
+// 72.1; 256 requests, rank 16 21.2, 113.2; one request of 16 rows, rank 16 13.2, 22.4, rank 64 25.8, 22.2.  64
+// requests, one of 65 rows, which the choice has to keep from the first: rank 64 121, 41.)
 bool few_rows(const gemm_adapters_t& p) {
+  const int splits = few_splits(p);
   const double row = (double)p.rank * (double)(p.K + p.N);
-  const double few = 7.0 + 0.36e-6 * (double)p.M * row +
-                     0.9 * (double)std::max<int64_t>(0, p.M - p.requests) / few_splits(p);
+  const double longest = (double)cdiv(p.M - std::min(p.requests, p.M) + 1, splits);
+  const double few = std::max(6.0 + 0.02 * (double)(p.requests * splits) + 0.40e-6 * (double)p.M * row,
+                              3.0 + longest * (1.8 + 9e-6 * row));
   const double tiles = (double)std::min(p.requests, p.M) * (double)cdiv(p.N, 128);
-  const double products = 11.0 + 0.0021 * (double)p.K + 1.35 / 152.0 * tiles;
-  return few < products;
+  const double products = 10.0 + 0.003 * (double)p.K + 1.5 / 152.0 * tiles;
+  return p.rank <= gb300::kFewRank && few < products;
 }
 
-// The second kernel by the lanes that a row of `rank` elements feeds.
+// The kernel by the lanes that a row of `rank` elements feeds.
 template <int DT>
-void (*up_kernel(int64_t rank))(gb300::FewParams) {
-  return rank <= 8 ? gb300::adapters_up_kernel<DT, 1> : rank <= 16 ? gb300::adapters_up_kernel<DT, 2>
-         : rank <= 32 ? gb300::adapters_up_kernel<DT, 4> : gb300::adapters_up_kernel<DT, 8>;
+void (*few_kernel(int64_t rank))(gb300::FewParams) {
+  return rank <= 8 ? gb300::adapters_few_kernel<DT, 1> : rank <= 16 ? gb300::adapters_few_kernel<DT, 2>
+         : rank <= 32 ? gb300::adapters_few_kernel<DT, 4> : gb300::adapters_few_kernel<DT, 8>;
 }
 
 gemm_status_t run_few(const gemm_adapters_t& p, struct CUstream_st* stream) {
@@ -441,22 +443,13 @@ gemm_status_t run_few(const gemm_adapters_t& p, struct CUstream_st* stream) {
   k.a = p.A; k.lda = p.lda; k.stride_a = p.strideA;
   k.b = p.B; k.ldb = p.ldb; k.stride_b = p.strideB;
   k.scale = p.scale;
-  k.u = p.u; k.ldu = p.ldu;
   k.r = p.r; k.ldr = p.ldr; k.r_dt = device_dt(p.r_type);
   k.d = p.d; k.ldd = p.ldd; k.d_dt = device_dt(p.d_type);
   k.in_place = p.r == p.d;
   k.splits = few_splits(p);
-  const int64_t ranks = cdiv(p.rank, gb300::kFewRanks), feats = cdiv(p.N, gb300::kFewThreads);
-  const int64_t blocks = p.requests * k.splits;
-  if (std::max(ranks, feats) * blocks > INT32_MAX) return GEMM_ERR_INVALID_ARG;
-  const bool f16 = p.type == GEMM_F16;
-  k.chunks = (int)ranks;
-  GB300_CHECK(launch(f16 ? gb300::adapters_down_kernel<gb300::DT_F16>
-                         : gb300::adapters_down_kernel<gb300::DT_BF16>,
-                     k, blocks * ranks, gb300::kFewThreads, 0, stream));
-  k.chunks = (int)feats;
-  return launch(f16 ? up_kernel<gb300::DT_F16>(p.rank) : up_kernel<gb300::DT_BF16>(p.rank), k,
-                blocks * feats, gb300::kFewThreads, 0, stream);
+  return launch(p.type == GEMM_F16 ? few_kernel<gb300::DT_F16>(p.rank) : few_kernel<gb300::DT_BF16>(p.rank), k,
+                p.requests * k.splits * gb300::kFewCluster, gb300::kFewThreads, 0, stream,
+                gb300::kFewCluster);
 }
 
 gemm_status_t check_adapters(const gemm_adapters_t& p) {

@@ -741,8 +741,8 @@ gemm_status_t gemm_grouped_linear_bwd(gemm_handle_t h, const gemm_grouped_linear
  * A request whose index is outside 0..adapters-1 has none: d = r there.  Rows of
  * no request stay as they were in d.  (Requests may not share rows.)
  *   x [M, K]; A: `adapters` matrices [rank, K], B: as many [N, rank], strideA
- *   and strideB elements apart (multiples of 16 bytes); u [M, rank]: a workspace that
- *   the call overwrites (calls that may overlap need one each); all of one type,
+ *   and strideB elements apart (multiples of 16 bytes; 0: one matrix); u [M, rank]: a workspace that
+ *   the call may overwrite (calls that may overlap need one each); all of one type,
  *   F16 or BF16.  r [M, N] (optional: 0; typically the shared layer's output),
  *   d [M, N]: F32, F16 or BF16 each.  scale [adapters]: fp32, optional (1).
  *   offsets [requests + 1], index [requests]: int32.  requests and adapters at

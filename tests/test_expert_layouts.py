@@ -129,7 +129,7 @@ def test_adapters(gemm, sizes):
     bounds = torch.tensor([0, *sizes], device="cuda").cumsum(0).int()
     index = torch.tensor([2, 1, 0], dtype=torch.int32, device="cuda")
     _both(gemm, lambda x, a, b, r, u, d: gemm.adapters(x, a, b, bounds, index, u, d, residual=r),
-          dict(x=x, a=a, b=b, r=r), dict(u=_zeros(rows, 16), d=_zeros(rows, N)))
+          dict(x=x, a=a, b=b, r=r, u=_zeros(rows, 16)), dict(d=_zeros(rows, N)))
 
 
 @pytest.mark.parametrize("sizes", [[1, 2, 1], [100, 0, 200]])
