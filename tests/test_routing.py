@@ -523,3 +523,63 @@ def test_repeats_bit_for_bit_on_any_stream_and_in_a_graph(gemm):
     graph.replay()
     torch.cuda.synchronize()
     assert o["slot"].view(-1).tolist() == sort(index.cpu(), E)[1]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,k,H,t,weighted,parts", [
+    (5001, 3, 5003, "f16", True, "both"), (2100, 4, 2048, "bf16", True, "both"),
+    (2000, 1, 9001, "bf16", False, "both"), (300, 32, 2051, "f32", True, "both"),
+    (410, 9, 4999, "f16", True, "dweight"), (301, 31, 2064, "bf16", True, "both"),
+    (300, 33, 2051, "f16", True, "both")])
+def test_combine_bwd_of_large_batches(gemm, T, k, H, t, weighted, parts):
+    """Rows of several passes ending inside 16 bytes, the last row of each matrix among the choices,
+    tokens without any, infinities and NaN in rows of no choice and behind rows."""
+    gen = torch.Generator().manual_seed(T + k + H)
+    R = T * k + 1 - T // 3
+    slot = torch.randperm(T * k, generator=gen).view(T, k)
+    slot[T // 2] = -1
+    slot[-1, -1], slot[slot == R - 1] = R - 1, -1
+    dy = torch.randn(T, H, generator=gen).to(O.TYPES[t])
+    ys = torch.randn(R, H, generator=gen).to(O.TYPES[t])
+    chosen = torch.zeros(R, dtype=torch.bool)
+    chosen[slot[(slot >= 0) & (slot < R)]] = True
+    ys[~chosen] = torch.tensor([NAN, float("inf")])[torch.arange(int((~chosen).sum())) % 2][:, None].to(ys.dtype)
+    weight = torch.randn(T, k, generator=gen) if weighted else None
+    DY, YS, DYS = O.strided(dy.float(), t), O.strided(ys.float(), t), O.strided(torch.full((R, H), NAN), t)
+    dweight = torch.full((T, k), NAN, device="cuda")
+    gemm.combine_bwd(DY[0], slot.int().cuda(), DYS[0] if parts == "both" else None,
+                     weight=weight.cuda() if weighted else None, ys=YS[0], dweight=dweight)
+    assert gemm.sync_status()[0] == G.GEMM_OK
+    safe = ys.double().masked_fill(~chosen[:, None], 0.0)
+    there = (slot >= 0) & (slot < R)
+    at = slot.clamp(0, R - 1)
+    for j in range(k):
+        terms = dy.double() * safe[at[:, j]] * there[:, j, None]
+        # a sum of H terms in fp32, in threads' and lanes' parts: each partial sum rounds once
+        O.within(dweight[:, j], terms.sum(1), terms.abs().sum(1) * 200 * O.U32 + 1e-30, "dweight")
+    if parts == "both":
+        want = torch.full((R, H), NAN, dtype=torch.float64)
+        w = weight.double() if weighted else torch.ones(T, k, dtype=torch.float64)
+        for j in range(k):
+            want[at[there[:, j], j]] = (w[:, j, None] * dy.double())[there[:, j]]
+        got = O.f64(DYS[0])
+        assert torch.isnan(got[~chosen]).all() and O.padding_untouched(*DYS)
+        O.within(got[chosen], want[chosen], O.rounding(want[chosen].abs() * (1 + O.U32), t) +
+                 want[chosen].abs() * O.U32, "dys")
+
+
+@pytest.mark.gpu
+def test_combine_bwd_of_large_batches_in_place_and_again(gemm):
+    T, k, H = 4000, 2, 2056
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    rnd = lambda *s: torch.randn(*s, generator=gen, device="cuda").bfloat16()
+    dy, ys, weight = rnd(T, H), rnd(T * k, H), torch.rand(T, k, generator=gen, device="cuda")
+    slot = torch.randperm(T * k, generator=gen, device="cuda").int().view(T, k)
+    first = None
+    for in_place in (False, True, False):
+        rows = ys.clone()
+        dys, dweight = rows if in_place else torch.empty_like(ys), torch.empty(T, k, device="cuda")
+        gemm.combine_bwd(dy, slot, dys, weight=weight, ys=rows, dweight=dweight)
+        assert gemm.sync_status()[0] == G.GEMM_OK
+        first = first or (dys.clone(), dweight.clone())
+        assert torch.equal(first[0], dys) and torch.equal(first[1], dweight)
