@@ -3,7 +3,7 @@
 // the inner size, which the cluster adds up through distributed shared memory, then its share of
 // the features.  The bytes of a row's adapter are asked for at once, those of the second matrix
 // before the first sums, so that what bounds a call are a memory latency or two a wave of blocks
-// and the launch.  (64 requests of a row, rank 16, 4096 x 4096 bf16: 8.3 us, the host's call included; 36.2 by
+// and the launch.  (64 requests of a row, rank 16, 4096 x 4096 bf16: 8.0 us, the host's call included; 36.2 by
 // products over groups of rows, each tile of which moves and multiplies 128 features for
 // its one row; 10.3 by two kernels, one a matrix.)
 #pragma once

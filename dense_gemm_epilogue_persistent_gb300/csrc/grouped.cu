@@ -413,7 +413,7 @@ int few_splits(const gemm_adapters_t& p) {
 // to 8192^2.  The first grows with the clusters and the rows' weights, or with the rows that one cluster
 // goes through: the host does not know whose the rows are, so as many as one request may
 // have; the second with the inner size and the tiles, of which every request has its own.  (Few, products:
-// 64 requests of a row, 4096 x 4096, rank 16 8.3, 42.6; rank 64 24.8, 40.7; 8192 x 8192, rank 128 69.3,
+// 64 requests of a row, 4096 x 4096, rank 16 8.0, 42.6; rank 64 24.7, 40.7; 8192 x 8192, rank 128 69.3,
 // 72.1; 256 requests, rank 16 21.2, 113.2; one request of 16 rows, rank 16 13.2, 22.4, rank 64 25.8, 22.2.  64
 // requests, one of 65 rows, which the choice has to keep from the first: rank 64 121, 41.)
 bool few_rows(const gemm_adapters_t& p) {
