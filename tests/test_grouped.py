@@ -751,3 +751,32 @@ def test_backward_repeats_bit_for_bit(gemm):
     torch.cuda.synchronize()
     for o in outs[1:]:
         assert all(torch.equal(outs[0][k], o[k]) for k in o)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("cg", [1, 2])
+@pytest.mark.parametrize("give", [("db",), ("da", "db")])
+def test_watchdog_of_the_gradients(gemm, cg, give):
+    """A stalled launch whose last blocks are zeroed by the warps of both CTAs ends with the error, and
+    the next one is right."""
+    gen = torch.Generator(device="cuda").manual_seed(0)
+    rnd = lambda *s: torch.randn(*s, generator=gen, device="cuda").half()
+    dd, a, b = rnd(323, 264), rnd(323, 520), rnd(2, 264, 520)
+    out = dict(da=torch.zeros(323, 520, device="cuda").half(), db=torch.zeros(2, 264, 520, device="cuda").half())
+    out = {k: out[k] for k in give}
+    gemm.set_config(cta_group=cg, tile_n=128 * cg, inject_stall=1)
+    G.gemm_set_timeout_ns(gemm.handle, 50_000_000)
+    try:
+        gemm.grouped_linear_bwd(dd, a, b, _i32([0, 5, 323]), **out)
+        assert gemm.sync_status()[0] == G.GEMM_ERR_DEVICE_TIMEOUT
+    finally:
+        G.gemm_set_timeout_ns(gemm.handle, 0)
+        gemm.set_config(cta_group=cg, tile_n=128 * cg)
+    gemm.grouped_linear_bwd(dd, a, b, _i32([0, 5, 323]), **out)
+    assert gemm.sync_status()[0] == G.GEMM_OK
+    gemm.set_config(None)
+    for g in range(2):
+        rows = slice(0, 5) if g == 0 else slice(5, 323)
+        want = O.f64(dd[rows]).T @ O.f64(a[rows])
+        mag = O.f64(dd[rows]).abs().T @ O.f64(a[rows]).abs()
+        O.within(out["db"][g], want, mag * ACCUM + O.rounding(want.abs() + mag * ACCUM, "f16"), "db")
