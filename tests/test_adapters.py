@@ -250,3 +250,35 @@ def test_beside_a_shared_layer_in_a_graph(gemm):
                 want[rows] += u64 @ b[e].T
                 err[rows] += eu @ b[e].abs().T + (u64.abs() + eu) @ b[e].abs().T * (ACCUM + 4 * O.U32)
         O.within(d, want, err + O.rounding(want.abs() + err, "f32"), "d")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rank", [255, 256, 257, 1000, 1024, 1025])
+@pytest.mark.parametrize("sizes,N,K", [([1, 1], 264, 136), ([0, 3, 1], 77, 40), ([1], 2310, 8)])
+def test_adapters_of_few_rows_and_large_ranks(gemm, sizes, N, K, rank):
+    index = [(i + 1) % 2 for i in range(len(sizes))]
+    _check(gemm, sizes, index, 2, N, K, rank, t="f16", r_t="f32", d_t="bf16", before=1, behind=2)
+
+
+@pytest.mark.gpu
+def test_adapters_in_place_by_either_way_agree(gemm):
+    """d on r, requests without an adapter among them: by the kernel of few rows and by products the
+    results are the same but for the order of the sums (each within 2^-10 of its terms)."""
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    rnd = lambda *s: torch.randn(*s, generator=gen, device="cuda").bfloat16()
+    x, a, b, r = rnd(40, 520), rnd(5, 24, 520), rnd(5, 1032, 24), rnd(40, 1032).float()
+    index = torch.randint(-1, 5, (40,), generator=gen, device="cuda", dtype=torch.int32)
+    bounds, u, got = _i32(list(range(41))), torch.empty(40, 24, device="cuda").bfloat16(), []
+    for cfg in (None, dict(cta_group=1)):
+        gemm.set_config(**cfg) if cfg else gemm.set_config(None)
+        d = r.clone()
+        gemm.adapters(x, a, b, bounds, index, u, d, residual=d)
+        assert gemm.sync_status()[0] == G.GEMM_OK
+        got.append(d)
+    gemm.set_config(None)
+    none = index < 0
+    assert torch.equal(got[0][none], r[none]) and torch.equal(got[1][none], r[none])
+    # |u| terms: 24 of |x a| sums, each off by 2^-10 of 520 terms of about 0.64 and a rounding
+    size = torch.einsum("mk,mrk->mr", x.double().abs(), a[index.clamp(min=0).long()].double().abs())
+    mag = torch.einsum("mr,mnr->mn", size, b[index.clamp(min=0).long()].double().abs())
+    assert ((got[0] - got[1]).double().abs() <= mag * (2 * 2.0 ** -10 + 2 * 2.0 ** -8) + 1e-6).all()
