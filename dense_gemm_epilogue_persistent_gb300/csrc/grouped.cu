@@ -2,6 +2,7 @@
 // low-rank adapters (include/gemm_gb300.h): argument checks, planning and launches of
 // the kernel in grouped_kernel.cuh.
 #include <algorithm>
+#include <cmath>
 #include <cstdint>
 #include <cstring>
 
@@ -66,6 +67,27 @@ int64_t items_of(const Product& p, const gemm_config_t& c) {
                    : (p.rows / c.tile_n + std::min(p.groups, p.rows)) * tiles_f;
 }
 
+// An estimate, microseconds, of the rows form with tiles of `bn` tokens: the launch and a first item's
+// k-blocks and epilogue, then rounds of items at the pace of their loads or their epilogues.  Fitted on
+// GB300 to 40 to 9600 rows in 1 to 32 uneven groups, 512 to 4096 features of inner sizes 512 and 2048 bf16,
+// with gelu and without: over those the choice is 1 % slower than the best of the three tiles, 10 % (gelu) and 5 %
+// faster than the widest wherever groups have more than 64 rows.  (600 rows of 8 groups, 1024 x 512: 7.4 us with
+// single tiles, 9.0 with the widest; 300 of one, 2048 x 512 6.8, 12.3; 2400 of 8, 512 x 2048 13.5 with pairs of 128, 18.9.)
+double rows_us(const gemm_handle* h, const Product& p, int cg, int bn, bool lean) {
+  const double groups = (double)std::max<int64_t>(1, std::min(p.groups, p.rows));
+  const double mean = (double)p.rows / groups, width = std::min((double)bn, mean);
+  const double tiles = groups > 1 ? groups * (mean > 0.5 * bn ? std::max(1.0, mean / bn + 0.5) : 1.0)
+                                  : (double)cdiv(p.rows, bn);
+  const double items = tiles * (double)cdiv(p.feats, 128 * cg);
+  const double rounds = std::max(1.0, std::ceil(items / (h->sm_count / cg)));
+  const double blocks = (double)cdiv(p.k * dtype_bytes(p.f_type), 128 * gb300::kGroupedKA);
+  const double first = cg == 1 ? 0.35 : bn == 128 ? 0.30 : 0.45;
+  const double block = cg == 1 ? 0.41 : 0.22 + 0.0018 * width;
+  const double whole = lean ? (cg == 1 ? 1.8 : bn == 128 ? 2.6 : 4.0) : (cg == 1 ? 2.4 : bn == 128 ? 3.9 : 7.3);
+  const double epilogue = whole * std::max(0.25, width / bn);
+  return 4.2 + first * blocks + epilogue + (rounds - 1) * std::max(block * blocks, epilogue);
+}
+
 // A launch's tile.
 gemm_status_t choose_tile(const gemm_handle* h, const Product& p, gemm_config_t& c) {
   const gemm_config_t f = h->forced ? h->forced_cfg : gemm_config_t{};
@@ -78,6 +100,13 @@ gemm_status_t choose_tile(const gemm_handle* h, const Product& p, gemm_config_t&
     c.cta_group = p.feats > 128 && mean > 64 ? 2 : 1;
   if (f.cta_group) c.cta_group = f.cta_group;
   c.tile_n = c.cta_group == 2 ? 256 : p.weights ? 128 : 64;
+  if (!p.weights && c.cta_group == 2 && !f.cta_group && !f.tile_n) {
+    const bool lean = lean_of(p) >= 0;
+    const double widest = rows_us(h, p, 2, 256, lean), pairs = rows_us(h, p, 2, 128, lean),
+                 single = rows_us(h, p, 1, 64, lean);
+    if (single < widest && single < pairs) { c.cta_group = 1; c.tile_n = 64; }
+    else if (pairs < widest) c.tile_n = 128;
+  }
   if (f.tile_n) c.tile_n = f.tile_n;
   c.tile_m = 128 * c.cta_group;
   return c.tile_n % (box_unit(p.weights, c.cta_group, c.tile_n) * c.cta_group) == 0
@@ -130,19 +159,27 @@ gemm_status_t plan_grouped(gemm_handle* h, const Product& p, GroupedPlan& out) {
   return finish_plan(h, p, items_of(p, out.cfg), out);
 }
 
-// Plan both gradients as one launch, where one tile and one lean epilogue suit both (h->mu held);
-// out.kern stays null where not.  (2002 rows of 6 groups, 2003 x 1501 fp16: 38.2 us, 42.3 as two; 8192 of 16
-// uneven ones, 4096 x 4096 bf16 452, 466.)
+// Plan both gradients as one launch, where one lean epilogue suits both (h->mu held); out.kern stays null
+// where not.  The tile is the weight gradient's, or pairs of 128 where that alone would take single
+// ones: what a launch of their own would gain by other tiles is less than it costs.  (One launch, two with
+// tiles of their own: 100 rows of one group, 512 x 512 7.4 us, 11.0; of 6, 1024 x 1024 12.3, 16.4; 2400 of one, 1024 x
+// 1024 17.1, 21.5; 2002 of 6, 2003 x 1501 38.2, 42.3; 8192 of 16, 4096 x 4096 452, 466; the other way round where many
+// groups have few rows of large weights: 100 of 64, 2048 x 2048 197, 189.)
 gemm_status_t plan_both(gemm_handle* h, const Product& da, const Product& db, GroupedPlan& out) {
-  gemm_config_t cb{};
-  GB300_CHECK(choose_tile(h, da, out.cfg));
-  GB300_CHECK(choose_tile(h, db, cb));
+  gemm_config_t ca{};
+  GB300_CHECK(choose_tile(h, da, ca));
+  GB300_CHECK(choose_tile(h, db, out.cfg));
   out.lean = lean_of(da);
-  if (out.lean < 0 || lean_of(db) != out.lean || cb.cta_group != out.cfg.cta_group ||
-      cb.tile_n != out.cfg.tile_n)
-    return GEMM_OK;
+  if (out.lean < 0 || lean_of(db) != out.lean) return GEMM_OK;
+  if (h->forced || da.feats <= 128) {
+    if (ca.cta_group != out.cfg.cta_group || ca.tile_n != out.cfg.tile_n) return GEMM_OK;
+  } else if (out.cfg.cta_group == 1) {
+    out.cfg.cta_group = 2;
+    out.cfg.tile_n = 128;
+    out.cfg.tile_m = 256;
+  }
   out.form = gb300::kGroupedBoth;
-  return finish_plan(h, da, items_of(da, out.cfg) + items_of(db, cb), out);
+  return finish_plan(h, da, items_of(da, out.cfg) + items_of(db, out.cfg), out);
 }
 
 // A product's tensor maps (`whole`: a whole tile's tokens, of the rows form) and parameters by its plan.
