@@ -440,9 +440,11 @@ gemm_status_t check_grouped_bwd(const gemm_grouped_linear_bwd_t& p) {
   return GEMM_OK;
 }
 
-// Clusters that share a request's rows in the kernel for few of them.
+// Clusters that share a request's rows in the kernel for few of them: as many as one request may have
+// rows, up to 16 and about a thousand in all (one without a row costs 6 ns).
 int few_splits(const gemm_adapters_t& p) {
-  return (int)std::min<int64_t>(4, std::max<int64_t>(1, p.M - p.requests + 1));
+  const int64_t longest = std::max<int64_t>(1, p.M - p.requests + 1);
+  return (int)std::min({(int64_t)16, std::max<int64_t>(1, 1024 / p.requests), longest});
 }
 
 // Whether a call takes it (adapters_few.cuh) rather than products over groups: by estimates of
@@ -451,13 +453,14 @@ int few_splits(const gemm_adapters_t& p) {
 // goes through: the host does not know whose the rows are, so as many as one request may
 // have; the second with the inner size and the tiles, of which every request has its own.  (Few, products:
 // 64 requests of a row, 4096 x 4096, rank 16 8.0, 42.6; rank 64 24.7, 40.7; 8192 x 8192, rank 128 69.3,
-// 72.1; 256 requests, rank 16 21.2, 113.2; one request of 16 rows, rank 16 13.2, 22.4, rank 64 25.8, 22.2.  64
-// requests, one of 65 rows, which the choice has to keep from the first: rank 64 121, 41.)
+// 72.1; 256 requests, rank 16 21.2, 113.2; one request of 16 rows, rank 64 10.8, 22.2; 64 of two rows, rank 16 17.1,
+// 41.1, of 65 and 63 of one 19.0, 43.2; what the choice has to keep from the first: 4 requests, one of 61 rows,
+// rank 64 29.1, 22.5.)
 bool few_rows(const gemm_adapters_t& p) {
   const int splits = few_splits(p);
   const double row = (double)p.rank * (double)(p.K + p.N);
   const double longest = (double)cdiv(p.M - std::min(p.requests, p.M) + 1, splits);
-  const double few = std::max(6.0 + 0.02 * (double)(p.requests * splits) + 0.40e-6 * (double)p.M * row,
+  const double few = std::max(6.0 + 0.006 * (double)(p.requests * splits) + 0.40e-6 * (double)p.M * row,
                               3.0 + longest * (1.8 + 9e-6 * row));
   const double tiles = (double)std::min(p.requests, p.M) * (double)cdiv(p.N, 128);
   const double products = 10.0 + 0.003 * (double)p.K + 1.5 / 152.0 * tiles;
