@@ -780,3 +780,29 @@ def test_watchdog_of_the_gradients(gemm, cg, give):
         want = O.f64(dd[rows]).T @ O.f64(a[rows])
         mag = O.f64(dd[rows]).abs().T @ O.f64(a[rows]).abs()
         O.within(out["db"][g], want, mag * ACCUM + O.rounding(want.abs() + mag * ACCUM, "f16"), "db")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("sizes", [[37] + [0] * 14 + [3], [0] * 20 + [16, 17, 0, 1], [100] + [1] * 10, [0, 65, 0, 0, 0, 32, 33]])
+@pytest.mark.parametrize("ab", ["bf16", "e4m3", "tf32"])
+def test_forward_long_groups_among_short_ones(gemm, sizes, ab):
+    """Tiles as narrow as the mean group suggests, and groups of several of them."""
+    _check_forward(gemm, sizes, 263, 200, ab, d_t="bf16", act="silu", r_t="f32", z_t="f16", scales=ab == "e4m3",
+                   before=2, behind=3)
+    _check_forward(gemm, sizes, 264, 300, ab, d_t="f16", r_t="f16")
+    if ab != "tf32":
+        _check_forward(gemm, sizes, 136, 264, ab, d_t="f32", b_mn=True)
+    else:
+        _check_forward(gemm, sizes, 136, 264, ab, d_t="f32")
+    mean = -(-sum(sizes) // len(sizes))
+    assert gemm.last_config().tile_n == (16 if mean <= 4 else 32 if mean <= 16 else 64)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("sizes,N,K", [([100], 512, 520), ([70, 30], 136, 1032), ([300, 0, 1], 200, 264), ([90], 40, 130),
+                                       ([1200], 1000, 512), ([2400], 264, 2056)])
+def test_backward_in_one_launch_of_few_items(gemm, sizes, N, K):
+    """Both gradients by one launch with the tiles that few items get, and each by itself."""
+    for give in (("da", "db"), ("da",), ("db",)):
+        _check_backward(gemm, sizes, N, K, "f16", da_t="f16", db_t="f16", give=give, before=3, behind=2)
+    _check_backward(gemm, sizes, N, K, "bf16", act="gelu", da_t="bf16", db_t="bf16", accumulate=True)
