@@ -712,7 +712,8 @@ gemm_status_t gemm_grouped_linear(gemm_handle_t h, const gemm_grouped_linear_t* 
  *   z: required unless activation is NONE.  da, db, dbias: each optional; a is
  *   read for db only, b for da only.  dz: required for da or db with an activation;
  *   without one it is optional (where given it receives dd).
- * dz may be dd or z (same leading dimension). */
+ * dz may be dd or z (same leading dimension).  Forced configurations apply as above
+ * (the width of db's tiles: a multiple of 64 a CTA). */
 typedef struct {
   int64_t M, N, K, groups;
   gemm_dtype_t type, da_type, db_type, dbias_type;
