@@ -748,7 +748,9 @@ gemm_status_t gemm_grouped_linear_bwd(gemm_handle_t h, const gemm_grouped_linear
  *   d [M, N]: F32, F16 or BF16 each.  scale [adapters]: fp32, optional (1).
  *   offsets [requests + 1], index [requests]: int32.  requests and adapters at
  *   most 4096.
- * d may be r (same type and leading dimension). */
+ * d may be r (same type and leading dimension).  Few rows are computed without matrix
+ * units and u; otherwise, and wherever a configuration is forced, by two products to which it
+ * applies as above. */
 typedef struct {
   int64_t M, N, K, rank, requests, adapters;
   gemm_dtype_t type, r_type, d_type;
