@@ -147,7 +147,7 @@ struct gemm_handle {
   gb300host::VariantState grouped_variants[3][2][3][4];  // [ab][cta_group][form][lean epilogue's type + 1]
   int route_cluster = 0;      // blocks of the sort's cluster (0: not asked)
   int split_clusters[9] = {0, 0, 0, 0, 0, 0, 0, 0, 0};   // resident, by cluster size (0: not asked)
-  int act_clusters[2][2][3][9] = {};   // activation gradient's, by form, type, block size and cluster
+  int act_clusters[3][2][3][9] = {};   // activation gradient's, by form, type, block size and cluster
   std::mutex mu;
   void* ws = nullptr;          // gemm_run_host's device copies of its host buffers
   size_t ws_bytes = 0;

@@ -26,16 +26,17 @@ struct ActGradParams {
   int M, N;
   int act, dbias_dt;
   int row_split;                    // blocks of a cluster, sharing the rows
-  // Groups of rows (else null): group g's are those between offsets[g * span] and
-  // offsets[(g + 1) * span], clamped to 0..M, and it has its own dbias.
+  // Groups of rows: group g's are those between offsets[g] and offsets[g + 1], clamped to 0..M.
   const int* offsets;
-  int span;
+  int groups;
 };
+// What a cluster goes through: its strip of all rows; of one group's, which has its own dbias; of all
+// groups', without dbias.
+enum : int { kActRows = 0, kActGroup = 1, kActGroups = 2 };
 
 // dz = dd act'(z) and dbias = its column sums (of the values before dz is
 // rounded), 6 bytes and about 25 instructions an element.  A block owns 64
-// columns (8 lanes of one vector each) and 1/R of the rows (GROUPED: of one group's, a
-// cluster for each strip and group), R the cluster size:
+// columns (8 lanes of one vector each) and 1/R of the rows, R the cluster size:
 // thread group g of G = THREADS / 8 walks rows first + g, + G, ..., each thread
 // copying its own pieces of the next kActDepth rows into its own slots of shared
 // memory (16 bytes and the row's end as they lie in memory; before the launch shapes
@@ -45,9 +46,13 @@ struct ActGradParams {
 // through shared memory, the cluster's blocks by its first one.
 // (4096 x 8192 gelu: 34.1 us with three rows, 35.1 with two, 34.2 with four; 16384 x
 // 4096: 65.5, 67.4, 65.1; 8192 x 700: 13.4, 12.9, 13.4)
+// The rows of groups lie one behind the other and are one run of rows (kActGroups), unless an offset
+// is less than the one before it: what lies between two such offsets need not be a group's, and
+// the groups are gone through one by one.  The offsets are looked through while the first
+// rows, which are read only in the other case, are on their way.
 constexpr int kActDepth = 3;
 
-template <int DT, int THREADS, bool GROUPED = false>
+template <int DT, int THREADS, int FORM = kActRows>
 __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
 act_grad_kernel(const __grid_constant__ ActGradParams p) {
   constexpr int G = THREADS / 8;
@@ -59,8 +64,8 @@ act_grad_kernel(const __grid_constant__ ActGradParams p) {
   const int lane = threadIdx.x & 7, group = threadIdx.x >> 3;
   const int R = p.row_split, rank = blockIdx.x % R;
   const int strips = (p.N + 63) / 64;
-  const int strip = GROUPED ? (int)(blockIdx.x / R) % strips : blockIdx.x / R;
-  const int grp = GROUPED ? (int)(blockIdx.x / R) / strips : 0;
+  const int strip = FORM == kActGroup ? (int)(blockIdx.x / R) % strips : blockIdx.x / R;
+  const int grp = FORM == kActGroup ? (int)(blockIdx.x / R) / strips : 0;
   const int c = strip * 64 + lane * kVec;
   const int share = (p.M + R - 1) / R;
   long long first = (long long)rank * share;
@@ -69,14 +74,17 @@ act_grad_kernel(const __grid_constant__ ActGradParams p) {
 #pragma unroll
   for (int i = 0; i < kVec; ++i) acc[i] = 0.f;
   grid_dependency_wait();
-  if constexpr (GROUPED) {
-    const int lo = min(max(__ldg(p.offsets + (long long)grp * p.span), 0), p.M);
-    const int hi = min(max(__ldg(p.offsets + (long long)(grp + 1) * p.span), lo), p.M);
+  // (this block's share of the rows between two offsets)
+  const auto between = [&](int from, int to) {
+    const int lo = min(max(__ldg(p.offsets + from), 0), p.M);
+    const int hi = min(max(__ldg(p.offsets + to), lo), p.M);
     const int part = (hi - lo + R - 1) / R;
     first = min((long long)hi, lo + (long long)rank * part);
     last = min((long long)hi, first + part);
-  }
-  if (c < p.N) {
+    if (FORM == kActGroups && c >= p.N) last = first;      // (no column, no rows)
+  };
+  if constexpr (FORM != kActRows) between(grp, FORM == kActGroup ? grp + 1 : p.groups);
+  if (c < p.N || FORM == kActGroups) {             // (all threads meet below)
     const uint8_t* const dd = static_cast<const uint8_t*>(p.dd);
     const uint8_t* const zz = static_cast<const uint8_t*>(p.z);
     with_activation(p.act, [&](auto a) {
@@ -92,30 +100,53 @@ act_grad_kernel(const __grid_constant__ ActGradParams p) {
         }
         copy_commit();
       };
+      const auto start = [&]() {
 #pragma unroll
-      for (int s = 0; s < kActDepth; ++s) request(first + group + s * G, s);
-      int slot = 0;
-      for (long long row = first + group; row < last; row += G) {
-        copy_wait(kActDepth - 1);
-        const uint4* const at = act_ring + slot * (2 * THREADS) + threadIdx.x;
-        float g[kVec];
-        unpack<DT>(RawVec<DT>{{at[0]}}, g);
-        if constexpr (ACT != ACT_NONE) {
-          float z[kVec];
-          unpack<DT>(RawVec<DT>{{at[THREADS]}}, z);
+        for (int s = 0; s < kActDepth; ++s) request(first + group + s * G, s);
+      };
+      const auto walk = [&]() {
+        int slot = 0;
+        for (long long row = first + group; row < last; row += G) {
+          copy_wait(kActDepth - 1);
+          const uint4* const at = act_ring + slot * (2 * THREADS) + threadIdx.x;
+          float g[kVec];
+          unpack<DT>(RawVec<DT>{{at[0]}}, g);
+          if constexpr (ACT != ACT_NONE) {
+            float z[kVec];
+            unpack<DT>(RawVec<DT>{{at[THREADS]}}, z);
 #pragma unroll
-          for (int i = 0; i < kVec; i += 2)
-            unpair(mul2(pair(g[i], g[i + 1]), activate_grad2<ACT>(z[i], z[i + 1])), g[i], g[i + 1]);
+            for (int i = 0; i < kVec; i += 2)
+              unpair(mul2(pair(g[i], g[i + 1]), activate_grad2<ACT>(z[i], z[i + 1])), g[i], g[i + 1]);
+          }
+          if (p.dz) store_vec(static_cast<uint8_t*>(p.dz) + row * p.lddz * es, DT, c, p.N, g);
+          if constexpr (FORM != kActGroups) {
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) acc[i] += g[i];
+          }
+          request(row + kActDepth * G, slot);       // (into the slot just read)
+          if (++slot == kActDepth) slot = 0;
         }
-        if (p.dz) store_vec(static_cast<uint8_t*>(p.dz) + row * p.lddz * es, DT, c, p.N, g);
-#pragma unroll
-        for (int i = 0; i < kVec; ++i) acc[i] += g[i];
-        request(row + kActDepth * G, slot);       // (into the slot just read)
-        if (++slot == kActDepth) slot = 0;
+      };
+      start();
+      if constexpr (FORM == kActGroups) {
+        int down = 0;
+        for (int g = threadIdx.x; g < p.groups; g += THREADS)
+          down |= __ldg(p.offsets + g + 1) < __ldg(p.offsets + g);
+        if (__syncthreads_or(down)) {
+#pragma unroll 1
+          for (int g = 0; g < p.groups; ++g) {
+            copy_wait(0);                          // (what was requested for all of them)
+            between(g, g + 1);
+            start();
+            walk();
+          }
+          return;
+        }
       }
+      walk();
     });
   }
-  if (!p.dbias) return;                  // (the whole grid)
+  if (FORM == kActGroups || !p.dbias) return;      // (the whole grid)
 #pragma unroll
   for (int i = 0; i < kVec; ++i) part[group][lane * kVec + i] = acc[i];
   __syncthreads();
@@ -859,13 +890,13 @@ int act_clusters(int& n, const gemm_handle* h, Kern kern, int threads, size_t sm
 // clusters of 6 blocks of 1024, 22.2 with clusters of 8, of which the device holds 15;
 // 3000 x 5000 17.8 with clusters of 7 of 256, 19.4 with 8.
 // With groups the same estimate for their mean number of rows.
-template <int DT, bool GROUPED = false>
+template <int DT, int FORM = gb300::kActRows>
 gemm_status_t launch_act_grad(gemm_handle* h, gb300::ActGradParams& k, struct CUstream_st* stream,
                               int64_t groups = 1) {
   typedef void (*Kern)(gb300::ActGradParams);
-  const Kern kerns[3] = {gb300::act_grad_kernel<DT, 1024, GROUPED>,
-                         gb300::act_grad_kernel<DT, 512, GROUPED>,
-                         gb300::act_grad_kernel<DT, 256, GROUPED>};
+  const Kern kerns[3] = {gb300::act_grad_kernel<DT, 1024, FORM>,
+                         gb300::act_grad_kernel<DT, 512, FORM>,
+                         gb300::act_grad_kernel<DT, 256, FORM>};
   const int64_t strips = cdiv(k.N, 64) * groups;
   const int64_t rows = cdiv(k.M, groups);
   Kern kern = nullptr;
@@ -878,7 +909,7 @@ gemm_status_t launch_act_grad(gemm_handle* h, gb300::ActGradParams& k, struct CU
       const int t = 1024 >> size;
       GB300_CHECK(raise_smem(h, reinterpret_cast<const void*>(kerns[size])));
       for (int split = 1; split <= 8; ++split) {
-        const int held = act_clusters(h->act_clusters[GROUPED][DT == gb300::DT_F16][size][split], h, kerns[size],
+        const int held = act_clusters(h->act_clusters[FORM][DT == gb300::DT_F16][size][split], h, kerns[size],
                                       t, smem(t), split);
         const double full = (double)strips / held;
         const double waves = full <= 1.0 ? 1.0 : full + 0.156 * (std::ceil(full) - full);
@@ -911,12 +942,13 @@ gemm_status_t gb300host::grouped_act_grad(gemm_handle* h, const GroupedActGrad& 
   k.M = (int)g.M; k.N = (int)g.N;
   k.act = g.activation;
   k.offsets = g.offsets;
-  // (without a bias's gradient all groups' rows are one run of rows)
-  const int64_t groups = g.dbias ? g.groups : 1;
-  k.span = g.dbias ? 1 : (int)g.groups;
-  if (cdiv(g.N, 64) * groups > INT32_MAX / 8) return GEMM_ERR_INVALID_ARG;
-  return g.type == GEMM_F16 ? launch_act_grad<gb300::DT_F16, true>(h, k, stream, groups)
-                            : launch_act_grad<gb300::DT_BF16, true>(h, k, stream, groups);
+  k.groups = (int)g.groups;
+  if (!g.dbias)
+    return g.type == GEMM_F16 ? launch_act_grad<gb300::DT_F16, gb300::kActGroups>(h, k, stream)
+                              : launch_act_grad<gb300::DT_BF16, gb300::kActGroups>(h, k, stream);
+  if (cdiv(g.N, 64) * g.groups > INT32_MAX / 8) return GEMM_ERR_INVALID_ARG;
+  return g.type == GEMM_F16 ? launch_act_grad<gb300::DT_F16, gb300::kActGroup>(h, k, stream, g.groups)
+                            : launch_act_grad<gb300::DT_BF16, gb300::kActGroup>(h, k, stream, g.groups);
 }
 
 namespace {

@@ -704,7 +704,9 @@ gemm_status_t gemm_grouped_linear(gemm_handle_t h, const gemm_grouped_linear_t* 
  * The gradient of the residual is dd itself.  Rows of no group stay as they were in
  * dz and da; an empty group's dbias and db are 0 (db unchanged where accumulated).
  * What dd, z and a hold in rows of no group reaches nothing, infinities and NaN
- * included.
+ * included.  Groups are what they are forward, offsets out of range or out of order included.  (Of
+ * groups that overlap each counts all its rows in its dbias and db; each element of da in the rows
+ * that they share is either's, and with dz on dd or z all that is made of these is undefined.)
  *   dd, z, dz [M, N], a, da [M, K]; b, db: `groups` K-major matrices [N, K],
  *   strideb and stridedb elements apart; dbias [groups, N].
  *   type: F16 or BF16, the type of dd, z, a, b and dz.  da_type, db_type,
