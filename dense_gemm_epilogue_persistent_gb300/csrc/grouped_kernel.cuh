@@ -396,10 +396,11 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmF, const __grid_constant__ 
     lead_from = rows_items % num_clusters;
     if (lead_from > 0) {
       const int behind = num_clusters - lead_from;
+      // (cycles in 64 bits: 224 million features are 2^31 of them)
       const int mean = (offs[p.groups] - offs[0]) / p.groups;
-      const int one = max(1230 * ((mean + BK - 1) / BK), 3000);
-      const int rounds = (1230 * ((p.k + BK - 1) / BK) + 3000) / one;
-      lead = min(rounds, weights_items / behind) * behind;
+      const long long one = max(1230ll * ((mean + BK - 1) / BK), 3000ll);
+      const long long rounds = (1230ll * ((p.k + BK - 1) / BK) + 3000) / one;
+      lead = (int)min(rounds, (long long)(weights_items / behind)) * behind;
     }
   }
   const auto second_item = [&]() {
