@@ -395,6 +395,11 @@ Product product_db(const gemm_grouped_linear_bwd_t& p, const void* dz, int64_t l
   return q;
 }
 
+// Without features there is nothing to compute but da, the sum of nothing, in the groups' rows.
+bool no_gradient(const gemm_grouped_linear_bwd_t& p) {
+  return p.groups == 0 || (p.N == 0 && (!p.da || p.M == 0 || p.K == 0 || !p.offsets));
+}
+
 gemm_status_t check_grouped_bwd(const gemm_grouped_linear_bwd_t& p) {
   if (!is_extent(p.M) || !is_extent(p.N) || !is_extent(p.K) || !is_count(p.groups) ||
       !is_activation(p.activation))
@@ -403,11 +408,12 @@ gemm_status_t check_grouped_bwd(const gemm_grouped_linear_bwd_t& p) {
   if ((p.da && !is_epi_type(p.da_type)) || (p.db && !is_epi_type(p.db_type)) ||
       (p.dbias && !is_epi_type(p.dbias_type)))
     return GEMM_ERR_UNSUPPORTED_DTYPE;
-  if (p.N == 0 || p.groups == 0) return GEMM_OK;
+  if (no_gradient(p)) return GEMM_OK;
   GB300_CHECK(check_groups(p.offsets, nullptr));
   if (cdiv(p.N, 64) * p.groups > INT32_MAX / 8 || !items_ok(p.M, p.groups, p.K) ||
       p.groups * cdiv(p.K, 128) * cdiv(p.N, 64) > INT32_MAX / 2)
     return GEMM_ERR_INVALID_ARG;
+  if (p.N == 0) return check_operand(p.da, p.ldda, p.K, p.M, p.da_type);
   if (p.M > 0) {
     GB300_CHECK(check_operand(p.dd, p.lddd, p.N, p.M, p.type));
     if (p.activation != GEMM_ACT_NONE) {
@@ -555,10 +561,10 @@ GEMM_API gemm_status_t gemm_grouped_linear_bwd(gemm_handle_t h, const gemm_group
   const gemm_grouped_linear_bwd_t& p = *pp;
   GB300_CHECK(check_grouped_bwd(p));
   if (!on_device(h)) return GEMM_ERR_INVALID_ARG;
-  if (p.N == 0 || p.groups == 0) return GEMM_OK;
+  if (no_gradient(p)) return GEMM_OK;
   int64_t lddz = 0;
   const void* dz = dz_of(p, lddz);
-  const bool da = p.da && p.M > 0 && p.K > 0, db = p.db && p.K > 0;
+  const bool da = p.da && p.M > 0 && p.K > 0, db = p.db && p.K > 0 && p.N > 0;
   const Product q_da = product_da(p, dz, lddz), q_db = product_db(p, dz, lddz);
   // both planned before anything is enqueued: a refused configuration changes no tensor
   GroupedPlan plan_da, plan_db, both;
@@ -568,7 +574,7 @@ GEMM_API gemm_status_t gemm_grouped_linear_bwd(gemm_handle_t h, const gemm_group
     if (!both.kern && da) GB300_CHECK(plan_grouped(h, q_da, plan_da));
     if (!both.kern && db) GB300_CHECK(plan_grouped(h, q_db, plan_db));
   }
-  if ((p.dz && p.M > 0) || p.dbias) {
+  if (p.N > 0 && ((p.dz && p.M > 0) || p.dbias)) {
     GroupedActGrad g{};
     g.M = p.M; g.N = p.N; g.groups = p.groups;
     g.type = p.type; g.dbias_type = p.dbias_type;

@@ -702,7 +702,8 @@ gemm_status_t gemm_grouped_linear(gemm_handle_t h, const gemm_grouped_linear_t* 
  *     db(g) = alpha * dz^T a  (+ db(g))   over the group's rows; added to where
  *                                         accumulate is non-zero
  * The gradient of the residual is dd itself.  Rows of no group stay as they were in
- * dz and da; an empty group's dbias and db are 0 (db unchanged where accumulated).
+ * dz and da; an empty group's dbias and db are 0 (db unchanged where accumulated).  N = 0: da is
+ * 0 in the groups' rows (without offsets, which may be left out then, nothing is written).
  * What dd, z and a hold in rows of no group reaches nothing, infinities and NaN
  * included.  Groups are what they are forward, offsets out of range or out of order included.  (Of
  * groups that overlap each counts all its rows in its dbias and db; each element of da in the rows
