@@ -332,9 +332,11 @@ gemm_status_t check_grouped(const gemm_grouped_linear_t& p) {
     return GEMM_ERR_MISALIGNED;
   // in place: element for element only; nothing else may share an output
   if (p.R == p.D && (p.r_type != p.d_type || p.ldr != p.ldd)) return GEMM_ERR_INVALID_ARG;
-  if (p.Z && (p.Z == p.D || p.Z == p.R)) return GEMM_ERR_INVALID_ARG;
-  if (p.K > 0 && (p.D == p.A || p.D == p.B || (p.Z && (p.Z == p.A || p.Z == p.B))))
-    return GEMM_ERR_INVALID_ARG;
+  for (const void* out : {(const void*)p.D, (const void*)p.Z})
+    if (same_place(out, {p.offsets, p.index, p.row_scale, p.col_scale, p.bias}) ||
+        (p.K > 0 && same_place(out, {p.A, p.B})))
+      return GEMM_ERR_INVALID_ARG;
+  if (same_place(p.Z, {p.D, p.R})) return GEMM_ERR_INVALID_ARG;
   return GEMM_OK;
 }
 
@@ -428,6 +430,17 @@ gemm_status_t check_grouped_bwd(const gemm_grouped_linear_bwd_t& p) {
     }
   }
   if (p.dbias && !aligned_to(p.dbias, dtype_bytes(p.dbias_type))) return GEMM_ERR_MISALIGNED;
+  // no output where another tensor of the call lies that is read or written: dz is complete before a and b
+  // are read, dbias before dz is
+  const void* const da = p.M > 0 && p.K > 0 ? p.da : nullptr;
+  const void* const db = p.K > 0 ? p.db : nullptr;
+  const void* const a = db && p.M > 0 ? p.a : nullptr;
+  const void* const b = da ? p.b : nullptr;
+  if (same_place(p.dbias, {p.offsets, a, b, da, db}) || same_place(da, {p.offsets}) ||
+      same_place(db, {p.offsets}))
+    return GEMM_ERR_INVALID_ARG;
+  if (p.M > 0 && (same_place(p.dz, {p.offsets, a, b, p.dbias, da, db}) || same_place(p.dbias, {p.dd, p.z})))
+    return GEMM_ERR_INVALID_ARG;
   if (p.K == 0) return GEMM_OK;
   int64_t lddz = 0;
   const void* dz = dz_of(p, lddz);
@@ -521,10 +534,11 @@ gemm_status_t check_adapters(const gemm_adapters_t& p) {
       GB300_CHECK(check_stack(p.A, p.lda, p.K, p.rank, p.adapters, p.strideA, p.type));
     }
     GB300_CHECK(check_stack(p.B, p.ldb, p.rank, p.N, p.adapters, p.strideB, p.type));
-    if (p.u == p.x || p.u == p.A || p.u == p.B || p.u == p.r || p.u == p.d || p.d == p.x ||
-        p.d == p.A || p.d == p.B)
+    if (same_place(p.u, {p.x, p.A, p.B, p.r, p.d, p.offsets, p.index, p.scale}) ||
+        same_place(p.d, {p.x, p.A, p.B, p.scale}))
       return GEMM_ERR_INVALID_ARG;
   }
+  if (same_place(p.d, {p.offsets, p.index})) return GEMM_ERR_INVALID_ARG;
   if (!aligned_to(p.scale, 4)) return GEMM_ERR_MISALIGNED;
   if (p.r == p.d && (p.r_type != p.d_type || p.ldr != p.ldd)) return GEMM_ERR_INVALID_ARG;
   return GEMM_OK;

@@ -594,8 +594,8 @@ gemm_status_t check_route(const gemm_route_t& p) {
       !aligned_to(p.index, p.index_bytes))
     return GEMM_ERR_MISALIGNED;
   if (p.T * p.k > 0 && (!p.index || !p.slot || p.ldi < p.k)) return GEMM_ERR_INVALID_ARG;
-  if (p.T * p.k > 0 && (p.slot == p.offsets || p.slot == p.source || p.source == p.offsets ||
-                        p.index == p.slot || p.index == p.source || p.index == p.offsets))
+  if (p.T * p.k > 0 && (same_place(p.offsets, {p.index, p.slot, p.source}) ||
+                        same_place(p.slot, {p.index, p.source}) || same_place(p.source, {p.index})))
     return GEMM_ERR_INVALID_ARG;       // (index is read again once slot has been written)
   return GEMM_OK;
 }
@@ -613,10 +613,13 @@ gemm_status_t check_dispatch(const gemm_dispatch_t& p) {
   if ((p.scale != nullptr) != (p.y_scale != nullptr) || (p.scale && p.scale == p.y_scale))
     return GEMM_ERR_INVALID_ARG;
   if (!aligned_to(p.scale, 4) || !aligned_to(p.y_scale, 4)) return GEMM_ERR_MISALIGNED;
-  if (p.T * p.k == 0 || p.H == 0 || p.R == 0) return GEMM_OK;
+  if (p.T * p.k == 0 || p.R == 0) return GEMM_OK;
+  if (same_place(p.y_scale, {p.slot})) return GEMM_ERR_INVALID_ARG;
+  if (p.H == 0) return GEMM_OK;
   GB300_CHECK(check_matrix(p.x, p.ldx, p.H, p.type));
   GB300_CHECK(check_matrix(p.y, p.ldy, p.H, p.type));
-  return p.x == p.y ? GEMM_ERR_INVALID_ARG : GEMM_OK;
+  return same_place(p.y, {p.x, p.slot, p.scale, p.y_scale}) || same_place(p.y_scale, {p.x})
+             ? GEMM_ERR_INVALID_ARG : GEMM_OK;
 }
 
 gemm_status_t check_combine(const gemm_combine_t& p) {
@@ -629,7 +632,7 @@ gemm_status_t check_combine(const gemm_combine_t& p) {
   if (p.r) GB300_CHECK(check_matrix(p.r, p.ldr, p.H, p.r_type));
   if (p.k > 0 && p.R > 0) {
     GB300_CHECK(check_matrix(p.ys, p.ldys, p.H, p.type));
-    if (p.ys == p.y) return GEMM_ERR_INVALID_ARG;
+    if (same_place(p.y, {p.ys, p.slot, p.weight})) return GEMM_ERR_INVALID_ARG;
   }
   if (p.r == p.y && (p.r_type != p.y_type || p.ldr != p.ldy)) return GEMM_ERR_INVALID_ARG;
   return GEMM_OK;
@@ -640,13 +643,14 @@ gemm_status_t check_combine_bwd(const gemm_combine_bwd_t& p) {
   if (!is_epi_type(p.type)) return GEMM_ERR_UNSUPPORTED_DTYPE;
   if (!aligned_to(p.weight, 4) || !aligned_to(p.dweight, 4)) return GEMM_ERR_MISALIGNED;
   if (p.T * p.k == 0) return GEMM_OK;
-  if (p.dweight && p.dweight == p.weight) return GEMM_ERR_INVALID_ARG;
+  if (same_place(p.dweight, {p.weight, p.slot})) return GEMM_ERR_INVALID_ARG;
   if (p.H == 0 || p.R == 0) return GEMM_OK;
   GB300_CHECK(check_matrix(p.dy, p.lddy, p.H, p.type));
   if (p.dweight) GB300_CHECK(check_matrix(p.ys, p.ldys, p.H, p.type));
+  if (same_place(p.dweight, {p.dy, p.ys})) return GEMM_ERR_INVALID_ARG;
   if (p.dys) {
     GB300_CHECK(check_matrix(p.dys, p.lddys, p.H, p.type));
-    if (p.dys == p.dy || (p.dweight && p.dys == p.ys && p.lddys != p.ldys))
+    if (same_place(p.dys, {p.dy, p.slot, p.weight, p.dweight}) || (p.dweight && p.dys == p.ys && p.lddys != p.ldys))
       return GEMM_ERR_INVALID_ARG;
   }
   return GEMM_OK;

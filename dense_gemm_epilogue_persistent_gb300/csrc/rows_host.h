@@ -2,6 +2,7 @@
 #pragma once
 
 #include <cstdint>
+#include <initializer_list>
 
 #include "gemm_gb300.h"
 #include "handle.h"
@@ -30,6 +31,13 @@ inline gemm_status_t check_matrix(const void* p, int64_t ld, int64_t cols, int d
   if (!p || ld < cols) return GEMM_ERR_INVALID_ARG;
   if (!aligned16(p) || (ld * dtype_bytes(dt)) % 16 != 0) return GEMM_ERR_MISALIGNED;
   return GEMM_OK;
+}
+
+// Whether an output, where there is one, lies where another of the call's tensors does.
+inline bool same_place(const void* out, std::initializer_list<const void*> others) {
+  for (const void* p : others)
+    if (out && p == out) return true;
+  return false;
 }
 
 #define GB300_CHECK(expr)                                     \

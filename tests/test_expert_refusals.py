@@ -56,3 +56,56 @@ def test_gradients_of_no_features(gemm, offsets, K, da_t):
     gemm.linear_bwd(e(M, 0), None, e(0, K), da=one)
     assert gemm.sync_status()[0] == G.GEMM_OK
     assert not one.any()
+
+
+# ---------------------------------------------------------------- outputs that another argument is
+
+_DISPATCH = dict(T=5, k=3, H=32, R=9, type=G.GEMM_E4M3, x=P[0], ldx=32, slot=P[1], scale=P[2], y=P[3], ldy=32,
+                 y_scale=P[4])
+_COMBINE = dict(T=5, k=3, H=30, R=9, type=G.GEMM_F16, r_type=G.GEMM_F16, y_type=G.GEMM_F16, ys=P[0],
+                ldys=32, slot=P[1], weight=P[2], r=P[3], ldr=32, y=P[4], ldy=32)
+_COMBINE_BWD = dict(T=5, k=3, H=30, R=9, type=G.GEMM_F16, dy=P[0], lddy=32, slot=P[1], weight=P[2],
+                    ys=P[3], ldys=32, dys=P[4], lddys=32, dweight=P[5])
+_ROUTE = dict(T=5, k=2, E=4, index_bytes=4, index=P[0], ldi=2, offsets=P[1], slot=P[2], source=P[3])
+_ADAPTERS = dict(M=5, N=96, K=96, rank=96, requests=3, adapters=4, type=G.GEMM_F16, r_type=G.GEMM_F16,
+                 d_type=G.GEMM_F16, offsets=P[0], index=P[1], x=P[2], ldx=96, A=P[3], lda=96, strideA=96 * 96,
+                 B=P[4], ldb=96, strideB=96 * 96, scale=P[5], u=P[6], ldu=96, r=P[7], ldr=96, d=P[8], ldd=96)
+_GROUPED = dict(M=5, N=96, K=96, groups=3, sets=4, a_type=G.GEMM_F16, b_type=G.GEMM_F16, bias_type=G.GEMM_F16,
+                r_type=G.GEMM_F16, z_type=G.GEMM_F16, d_type=G.GEMM_F16, alpha=1.0, offsets=P[0], index=P[1],
+                A=P[2], lda=96, B=P[3], ldb=96, strideB=96 * 96, row_scale=P[4], col_scale=P[5], bias=P[6],
+                R=P[7], ldr=96, Z=P[8], ldz=96, D=P[9], ldd=96)
+_GROUPED_BWD = dict(M=5, N=96, K=96, groups=3, type=G.GEMM_F16, da_type=G.GEMM_F16, db_type=G.GEMM_F16,
+                    dbias_type=G.GEMM_F16, activation=G.GEMM_ACT_SILU, alpha=1.0, offsets=P[0], dd=P[1], lddd=96,
+                    z=P[2], ldz=96, a=P[3], lda=96, b=P[4], ldb=96, strideb=96 * 96, dz=P[5], lddz=96, da=P[6],
+                    ldda=96, db=P[7], lddb=96, stridedb=96 * 96, dbias=P[8])
+# operator: its structure, a call of it with every tensor (all of one width, so that no size or stride
+# refuses any of them in another's place), outputs, and what may be one tensor
+CALLS = {
+    "route": (G.gemm_route_t, _ROUTE, ("offsets", "slot", "source"), ()),
+    "dispatch": (G.gemm_dispatch_t, _DISPATCH, ("y", "y_scale"), ()),
+    "combine": (G.gemm_combine_t, _COMBINE, ("y",), ({"y", "r"},)),
+    "combine_bwd": (G.gemm_combine_bwd_t, _COMBINE_BWD, ("dys", "dweight"), ({"dys", "ys"},)),
+    "grouped_linear": (G.gemm_grouped_linear_t, _GROUPED, ("Z", "D"), ({"D", "R"},)),
+    "grouped_linear_bwd": (G.gemm_grouped_linear_bwd_t, _GROUPED_BWD, ("dz", "da", "db", "dbias"),
+                           ({"dz", "dd"}, {"dz", "z"})),
+    "adapters": (G.gemm_adapters_t, _ADAPTERS, ("u", "d"), ({"d", "r"},)),
+}
+PAIRS = [(name, out, other) for name, (_, call, outs, _) in CALLS.items() for out in outs
+         for other in call if call[other] in P and other != out]
+
+
+@pytest.mark.parametrize("name,out,other", PAIRS)
+def test_check_an_output_that_is_another_argument(lib, name, out, other):
+    """Each output at every other tensor's address: only what may be in place passes."""
+    struct, call, _, in_place = CALLS[name]
+    check = getattr(G, f"gemm_{name}_check")
+    assert check(struct(**call)) == 0
+    want = 0 if {out, other} in in_place else INVALID
+    assert check(struct(**{**call, out: call[other]})) == want
+
+
+@pytest.mark.parametrize("kw", [dict(dz=P[3], db=None), dict(dz=P[4], da=None), dict(dbias=P[4], da=None),
+                                dict(dbias=P[3], db=None)])
+def test_check_what_is_not_read_may_be_an_output(lib, kw):
+    """a is read for db only, b for da only."""
+    assert G.gemm_grouped_linear_bwd_check(G.gemm_grouped_linear_bwd_t(**{**_GROUPED_BWD, **kw})) == 0
