@@ -1017,6 +1017,15 @@ gemm_status_t check_linear_bwd(const gemm_linear_bwd_t& p) {
     GB300_CHECK(check_linear(q));
     if (p.N > 0 && p.K > 0 && (p.db == p.dd || (p.b && p.db == p.b))) return GEMM_ERR_INVALID_ARG;
   }
+  // dz is complete before a and b are read, dbias before dz is
+  if (p.M > 0 && p.N > 0) {
+    const void* const da = p.K > 0 ? p.da : nullptr;
+    const void* const db = p.K > 0 ? p.db : nullptr;
+    const void* const a = db ? p.a : nullptr;
+    const void* const b = da ? p.b : nullptr;
+    if (same_place(p.dz, {a, b, p.dbias}) || same_place(p.dbias, {p.dd, p.z, a, b, da, db}))
+      return GEMM_ERR_INVALID_ARG;
+  }
   return GEMM_OK;
 }
 

@@ -104,6 +104,18 @@ def test_check_an_output_that_is_another_argument(lib, name, out, other):
     assert check(struct(**{**call, out: call[other]})) == want
 
 
+_LINEAR_BWD = {k: v for k, v in _GROUPED_BWD.items() if k not in ("groups", "offsets", "strideb", "stridedb")}
+
+
+@pytest.mark.parametrize("kw,code", [
+    ({}, 0), (dict(dz=P[1]), 0), (dict(dz=P[2]), 0), (dict(dz=P[3], db=None), 0), (dict(dz=P[4], da=None), 0),
+    (dict(dz=P[3]), INVALID), (dict(dz=P[4]), INVALID), (dict(dz=P[8]), INVALID), (dict(dbias=P[1]), INVALID),
+    (dict(dbias=P[2]), INVALID), (dict(dbias=P[3]), INVALID), (dict(dbias=P[4]), INVALID),
+    (dict(dbias=P[6]), INVALID), (dict(dbias=P[7]), INVALID)])
+def test_check_the_same_without_groups(lib, kw, code):
+    assert G.gemm_linear_bwd_check(G.gemm_linear_bwd_t(**{**_LINEAR_BWD, **kw})) == code
+
+
 @pytest.mark.parametrize("kw", [dict(dz=P[3], db=None), dict(dz=P[4], da=None), dict(dbias=P[4], da=None),
                                 dict(dbias=P[3], db=None)])
 def test_check_what_is_not_read_may_be_an_output(lib, kw):
