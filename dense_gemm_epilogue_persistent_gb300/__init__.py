@@ -996,6 +996,8 @@ class Gemm:
         [T, k] (which reads ys), each where given; see gemm_combine_bwd in the C header."""
         shape = _shape(dy, "dy")
         T, H = shape
+        if dweight is not None and ys is None:
+            raise GemmError(GEMM_ERR_INVALID_ARG, "dweight: without ys")
         rows = dys if dys is not None else ys
         R = 0 if rows is None else _shape(rows, "dys or ys")[0]
         t, dev = _code(dy, "dy"), self.device

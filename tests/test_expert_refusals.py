@@ -6,6 +6,7 @@ import torch
 import dense_gemm_epilogue_persistent_gb300 as G
 from dense_gemm_epilogue_persistent_gb300 import build as B
 from test_grouped import _bwd, P
+from test_layer_arguments import Library, Placed, _handle
 
 INVALID, ALIGN = G.GEMM_ERR_INVALID_ARG, G.GEMM_ERR_MISALIGNED
 
@@ -121,3 +122,21 @@ def test_check_the_same_without_groups(lib, kw, code):
 def test_check_what_is_not_read_may_be_an_output(lib, kw):
     """a is read for db only, b for da only."""
     assert G.gemm_grouped_linear_bwd_check(G.gemm_grouped_linear_bwd_t(**{**_GROUPED_BWD, **kw})) == 0
+
+
+# ---------------------------------------------------------------- a gradient without what it is made from
+
+def test_the_weights_gradient_without_the_rows_is_refused():
+    """combine's dweight is made from ys: without, there is no number of rows to read off it, and no places in
+    0 rows would give 0."""
+    e = lambda *s: Placed(torch.zeros(*s), 0)
+    slot = Placed(torch.zeros(4, 2, dtype=torch.int32), 0)
+    lib = Library()
+    for kw in (dict(), dict(dys=e(8, 64)), dict(weight=e(4, 2))):
+        with pytest.raises(G.GemmError) as err:
+            _handle(lib).combine_bwd(e(4, 64), slot, dweight=e(4, 2), **kw)
+        assert err.value.status == INVALID and "ys" in str(err.value)
+    assert lib.calls == 0
+    _handle(lib).combine_bwd(e(4, 64), slot, dweight=e(4, 2), ys=e(0, 64))
+    _handle(lib).combine_bwd(e(4, 64), slot, dys=e(8, 64))
+    assert lib.calls == 2
