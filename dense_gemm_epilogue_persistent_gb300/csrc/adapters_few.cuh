@@ -40,13 +40,9 @@ __device__ __forceinline__ int few_request(const FewParams& p, int s, int& first
   return e >= 0 && e < p.adapters ? e : -1;
 }
 
-template <int DT>
-__device__ __forceinline__ float round_to(float v) {
-  return DT == DT_F16 ? __half2float(__float2half_rn(v)) : __bfloat162float(__float2bfloat16_rn(v));
-}
-
 // u(m, j) = sum_k x(m, k) A(e, j, k): a warp has ranks, its lanes every 32nd vector of the block's
-// share; partial sums are added in the order lanes, blocks, and u is rounded to DT.
+// share; partial sums are added in the order lanes, blocks, and stay fp32: u never leaves shared
+// memory, so nothing is saved by rounding it to DT as the products' workspace has it.
 // d(m, n) = r(m, n) + scale(e) sum_j u(m, j) B(e, n, j): LANES lanes read a row of B together (8 ranks
 // each: up to 128 contiguous bytes), in LANES passes over a warp's 32 features; then every
 // lane takes over the sums of one of the features of its LANES (a lane that keeps a half of its
@@ -143,7 +139,7 @@ adapters_few_kernel(const __grid_constant__ FewParams p) {
           for (uint32_t c = 0; c < kFewCluster; ++c)
             sum += __uint_as_float(load_cluster_u32(map_to_rank(smem_u32(&parts[turn][j]), c)));
         }
-        us[j] = round_to<DT>(sum);
+        us[j] = sum;
       }
       __syncthreads();
     }

@@ -740,7 +740,7 @@ gemm_status_t gemm_grouped_linear_bwd(gemm_handle_t h, const gemm_grouped_linear
 
 /* Low-rank adapters of many requests beside a shared layer: request s has the
  * rows offsets(s) .. offsets(s + 1) - 1 and the adapter e = index(s):
- *     u = x A(e)^T                          rounded to `type`
+ *     u = x A(e)^T                          rounded to `type` where it passes through the workspace
  *     d = r + scale(e) * (u B(e)^T)
  * A request whose index is outside 0..adapters-1 has none: d = r there.  Rows of
  * no request stay as they were in d.  (Requests may not share rows.)
@@ -752,7 +752,7 @@ gemm_status_t gemm_grouped_linear_bwd(gemm_handle_t h, const gemm_grouped_linear
  *   offsets [requests + 1], index [requests]: int32.  requests and adapters at
  *   most 4096.
  * d may be r (same type and leading dimension).  Few rows are computed without matrix
- * units and u; otherwise, and wherever a configuration is forced, by two products to which it
+ * units and the workspace, u staying in fp32; otherwise, and wherever a configuration is forced, by two products to which it
  * applies as above. */
 typedef struct {
   int64_t M, N, K, rank, requests, adapters;
