@@ -495,7 +495,8 @@ void (*few_kernel(int64_t rank))(gb300::FewParams) {
          : rank <= 32 ? gb300::adapters_few_kernel<DT, 4> : gb300::adapters_few_kernel<DT, 8>;
 }
 
-gemm_status_t run_few(const gemm_adapters_t& p, struct CUstream_st* stream) {
+// Enqueue it (h->mu held).
+gemm_status_t run_few(gemm_handle* h, const gemm_adapters_t& p, struct CUstream_st* stream) {
   gb300::FewParams k{};
   k.M = (int)p.M; k.N = (int)p.N; k.K = (int)p.K; k.rank = (int)p.rank;
   k.requests = (int)p.requests; k.adapters = (int)p.adapters;
@@ -508,6 +509,8 @@ gemm_status_t run_few(const gemm_adapters_t& p, struct CUstream_st* stream) {
   k.d = p.d; k.ldd = p.ldd; k.d_dt = device_dt(p.d_type);
   k.in_place = p.r == p.d;
   k.splits = few_splits(p);
+  h->last = gemm_config_t{};           // (no tile, no counters)
+  h->counted = false;
   return launch(p.type == GEMM_F16 ? few_kernel<gb300::DT_F16>(p.rank) : few_kernel<gb300::DT_BF16>(p.rank), k,
                 p.requests * k.splits * gb300::kFewCluster, gb300::kFewThreads, 0, stream,
                 gb300::kFewCluster);
@@ -621,7 +624,7 @@ GEMM_API gemm_status_t gemm_adapters(gemm_handle_t h, const gemm_adapters_t* pp,
   if (p.M == 0 || p.N == 0 || p.requests == 0) return GEMM_OK;
   const bool any = p.rank > 0 && p.adapters > 0;
   std::lock_guard<std::mutex> guard(h->mu);
-  if (any && p.K > 0 && few_rows(p) && !h->forced) return run_few(p, stream);
+  if (any && p.K > 0 && few_rows(p) && !h->forced) return run_few(h, p, stream);
   Product down, up;
   down.rows = p.M; down.feats = p.rank; down.k = p.K; down.groups = p.requests;
   down.sets = p.adapters;

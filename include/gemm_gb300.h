@@ -294,7 +294,8 @@ gemm_status_t gemm_run_host(gemm_handle_t h, int64_t M, int64_t N, int64_t K, in
  * into shared memory, issuing the stores and next loads (with their wait);
  * the chunks the store thread's warp processed (the CTA's chunks with one
  * epilogue warp per lane quarter, about half of them with two); two spare
- * words.  After a split-K launch *n_ctas is 0: that kernel keeps no counters. */
+ * words.  After a split-K launch, products over groups of rows or adapters *n_ctas is 0: those kernels
+ * keep no counters. */
 #define GEMM_RING_STAT_WORDS 16
 gemm_status_t gemm_ring_stats(gemm_handle_t h, struct CUstream_st* stream, uint64_t* out,
                               int max_ctas, int* n_ctas);
@@ -337,7 +338,8 @@ gemm_status_t gemm_plan(const gemm_problem_t* p, int sm_count, int smem_optin,
  * (NULL restores automatic selection).  Used by tests and tuning sweeps. */
 gemm_status_t gemm_set_config(gemm_handle_t h, const gemm_config_t* cfg);
 
-/* The configuration chosen by the most recent successful gemm_run. */
+/* The configuration chosen by the most recent successful gemm_run, or by the most recent launch of a
+ * product of the operators below; all zero where that was adapters of few rows, which have no tile. */
 gemm_status_t gemm_last_config(gemm_handle_t h, gemm_config_t* out);
 
 /* Tensor-memory columns one fp32 accumulator of tile_m x tile_n occupies:
