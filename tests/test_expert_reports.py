@@ -43,3 +43,40 @@ def test_reports_after_adapters():
     r = subprocess.run([sys.executable, "-c", STATS], cwd=ROOT, capture_output=True, text=True,
                        timeout=1200)
     assert r.returncode == 0 and "STATS_OK" in r.stdout, r.stdout[-3000:] + r.stderr[-3000:]
+
+
+DEBUG = r'''
+import sys
+sys.path.insert(0, "tests")
+import torch
+import dense_gemm_epilogue_persistent_gb300 as G
+from dense_gemm_epilogue_persistent_gb300 import build as B
+G.select_library(B.build(kind=sys.argv[1]))
+import test_expert_bounds as L
+import test_grouped as F
+g = G.Gemm(0)
+for sizes, N, K in (([1], 8, 1), ([3, 0, 40], 129, 77), ([300, 0, 65, 513], 520, 701)):
+    for cfg in (None, dict(cta_group=1, tile_n=64), dict(cta_group=2, tile_n=256)):
+        g.set_config(**cfg) if cfg else g.set_config(None)
+        F._check_backward(g, sizes, N, K, "bf16", "gelu", db_t="bf16", accumulate=True)
+g.set_config(None)
+for offsets in ([60, 20, 65], [0, 200, 90], [40, 65, 3, 9, 9, 20, 0, 2]):
+    for give in (("dz", "da", "db"), ("dz", "da", "db", "dbias")):
+        L._check_backward(g, offsets, 65, 136, 72, "silu", give)
+st, detail = g.sync_status()
+assert st == G.GEMM_OK, (G.gemm_status_string(st), hex(detail))
+g.close()
+maps = open("/proc/self/maps").read()
+assert f"libgemm_gb300_{sys.argv[1]}.so" in maps and "libgemm_gb300.so" not in maps
+print("BUILD_OK")
+'''
+
+
+@pytest.mark.parametrize("kind", ["debug", "nomc"])
+def test_gradients_in_another_build(kind):
+    """Odd gradients added to in 16 bits, and offsets out of order, with every access checked."""
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    r = subprocess.run([sys.executable, "-c", DEBUG, kind], cwd=ROOT, capture_output=True, text=True,
+                       timeout=1200)
+    assert r.returncode == 0 and "BUILD_OK" in r.stdout, r.stdout[-3000:] + r.stderr[-3000:]
