@@ -10,8 +10,9 @@
 // and walks it with the others, item by item in turn.
 //
 // The features lie on the MMA's rows (tensor-memory lanes), the tokens on its
-// columns.  A tile's width then follows its group in steps of 16 or 64 columns, so
-// that a ragged group costs no more than its own rows; an accumulator column is
+// columns.  A tile's width then follows its group in steps of 16 columns (32 of single CTAs'
+// tiles wider than 64, 64 of pairs' and in the weights form of each CTA's), so
+// that a ragged group costs little more than its own rows; an accumulator column is
 // one token, whose 32 features a warp stores as one contiguous piece; nothing is
 // ever written between the groups, whatever lies next to them, and neither row
 // ends nor tile ends need padding.  (Rows of other groups inside a token box give
@@ -118,7 +119,8 @@ __device__ __forceinline__ const CUtensorMap* second_map(const GroupedBothParams
 }
 
 constexpr int kGroupedKA = 2;                  // 128-byte K atoms a ring stage
-constexpr int kGroupedMBox = 128;              // rows of one box of the weights form (with 64: 16 groups 245 -> 258 us)
+constexpr int kGroupedMBox = 128;              // rows of one box of the weights form, a stage's (boxes of 64: 16
+                                               // groups 245 -> 258 us)
 constexpr int kGroupedChunk = 32;              // columns of an epilogue chunk
 constexpr int kGroupedMaxStrip = 16;
 constexpr int kGroupedMaxGroups = 4096;        // what the tables in shared memory hold
@@ -276,7 +278,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmF, const __grid_constant__ 
   constexpr int kStreams = grouped_streams(LEAN), kEpiWarps = 4 * kStreams;
   static_assert(!kWeights || AB_BYTES == 2, "weight gradients are of 16-bit operands");
   static_assert(FORM != kGroupedBoth || LEAN >= 0, "both forms: the lean epilogue");
-  static_assert(BK % kGroupedMBox == 0 || !kWeights, "whole boxes a stage");
+  static_assert(BK == kGroupedMBox || !kWeights, "a stage's rows in one box");
 
   grid_launch_dependents();
   extern __shared__ uint8_t smem_raw[];
@@ -514,14 +516,11 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmF, const __grid_constant__ 
         }
         if (elect_one()) {
           if (kWeights && i.wt) {
-            // both operands MN-major: boxes of 64 features or output rows x 64 rows, those that
-            // hold rows of the group
+            // both operands MN-major: boxes of 64 features or output rows x the stage's rows
             const CUtensorMap* const map_f = second_map(p, tmF, 0);
             const CUtensorMap* const map_t = second_map(p, tmT, 1);
             const int m = i.m0 + kb * BK, left = i.mn - kb * BK;
-            const int halves = min(BK / kGroupedMBox, (left + kGroupedMBox - 1) / kGroupedMBox);
-            const uint32_t bytes =
-                (uint32_t)(halves * (F_BOXES + width / ATOM_K)) * (kGroupedMBox * 128u);
+            const uint32_t bytes = (uint32_t)(F_BOXES + width / ATOM_K) * MN_ATOM;
             const bool tail = left <= BK && i.mn % UMMA_K != 0;
             // (a last block that needs zeros is completed on this CTA's own barrier: the zeroing
             // warp goes on from there)
@@ -529,19 +528,13 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmF, const __grid_constant__ 
             const uint32_t bar = tail ? tail0 + 8u * s : PAIR ? map_to_rank(fb, 0) : fb;
             if (tail) mbar_arrive_expect_tx(bar, bytes);
             else if (rank == 0) mbar_arrive_expect_tx(fb, CG * bytes);
-            for (int h = 0; h < halves; ++h) {
-              const uint32_t at = (uint32_t)h * (kGroupedMBox * 128u);
-              const int row = m + h * kGroupedMBox;
-              for (int j = 0; j < F_BOXES; ++j) {
-                if (tail) tma_load_3d(sf + j * MN_ATOM + at, map_f, bar, f0 + j * ATOM_K, row, 0, pol);
-                else OperandLoad<CG, false>::load(sf + j * MN_ATOM + at, map_f, bar, f0 + j * ATOM_K,
-                                                  row, 0, 0, pol);
-              }
-              for (int j = 0; j < width / ATOM_K; ++j) {
-                if (tail) tma_load_3d(st + j * MN_ATOM + at, map_t, bar, t0 + j * ATOM_K, row, 0, pol);
-                else OperandLoad<CG, false>::load(st + j * MN_ATOM + at, map_t, bar, t0 + j * ATOM_K,
-                                                  row, 0, 0, pol);
-              }
+            for (int j = 0; j < F_BOXES; ++j) {
+              if (tail) tma_load_3d(sf + j * MN_ATOM, map_f, bar, f0 + j * ATOM_K, m, 0, pol);
+              else OperandLoad<CG, false>::load(sf + j * MN_ATOM, map_f, bar, f0 + j * ATOM_K, m, 0, 0, pol);
+            }
+            for (int j = 0; j < width / ATOM_K; ++j) {
+              if (tail) tma_load_3d(st + j * MN_ATOM, map_t, bar, t0 + j * ATOM_K, m, 0, pol);
+              else OperandLoad<CG, false>::load(st + j * MN_ATOM, map_t, bar, t0 + j * ATOM_K, m, 0, 0, pol);
             }
           } else if (kRows) {
             const int k0 = kb * BK, set = i.e * p.set_step;
