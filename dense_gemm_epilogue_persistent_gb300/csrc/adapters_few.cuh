@@ -1,11 +1,12 @@
-// Low-rank adapters of requests with a row or two each (a decode batch): one kernel without matrix
-// units.  A cluster of blocks has the rows of a request: each block the sums over its share of
+// Low-rank adapters of few rows (a decode batch, short prompts among it): one kernel without matrix
+// units.  A cluster of blocks has the rows of a request, or up to 16 clusters have every 16th of them: each block the sums over its share of
 // the inner size, which the cluster adds up through distributed shared memory, then its share of
 // the features.  The bytes of a row's adapter are asked for at once, those of the second matrix
 // before the first sums, so that what bounds a call are a memory latency or two a wave of blocks
-// and the launch.  (64 requests of a row, rank 16, 4096 x 4096 bf16: 8.0 us, the host's call included; 36.2 by
-// products over groups of rows, each tile of which moves and multiplies 128 features for
-// its one row; 10.3 by two kernels, one a matrix.)
+// and the launch; of a request with many rows one row after the other, which is where products over groups of rows take
+// over.  (64 requests of a row, rank 16, 4096 x 4096 bf16: 8.0 us, the host's call included, 7.0 in a graph; 41.8 by
+// products, each tile of which moves and multiplies 128 features for its one row; 10.3 by two kernels, one
+// a matrix.)
 #pragma once
 
 #include "rows.cuh"

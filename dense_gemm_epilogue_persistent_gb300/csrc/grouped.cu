@@ -70,7 +70,8 @@ int64_t items_of(const Product& p, const gemm_config_t& c) {
 // An estimate, microseconds, of the rows form with tiles of `bn` tokens: the launch and a first item's
 // k-blocks and epilogue, then rounds of items at the pace of their loads or their epilogues.  Fitted on
 // GB300 to 40 to 9600 rows in 1 to 32 uneven groups, 512 to 4096 features of inner sizes 512 and 2048 bf16,
-// with gelu and without: over those the choice is 1 % slower than the best of the three tiles, 10 % (gelu) and 5 %
+// with gelu and without: over those the choice is 1 % slower than the best of its three tiles (1.5 % than the best of
+// five, single CTAs with 128 and 256 among them), 10 % (gelu) and 5 %
 // faster than the widest wherever groups have more than 64 rows.  (600 rows of 8 groups, 1024 x 512: 7.4 us with
 // single tiles, 9.0 with the widest; 300 of one, 2048 x 512 6.8, 12.3; 2400 of 8, 512 x 2048 13.5 with pairs of 128, 18.9.)
 double rows_us(const gemm_handle* h, const Product& p, int cg, int bn, bool lean) {
@@ -472,19 +473,19 @@ int few_splits(const gemm_adapters_t& p) {
 // both, microseconds, fitted on GB300 to 1 to 256 requests of 1 to 16 rows, ranks 8 to 128, 1024^2
 // to 8192^2.  The first grows with the clusters and the rows' weights, or with the rows that one cluster
 // goes through: the host does not know whose the rows are, so as many as one request may
-// have; the second with the inner size and the tiles, of which every request has its own.  (Few, products:
-// 64 requests of a row, 4096 x 4096, rank 16 8.0, 42.6; rank 64 24.7, 40.7; 8192 x 8192, rank 128 69.3,
-// 72.1; 256 requests, rank 16 21.2, 113.2; one request of 16 rows, rank 64 10.8, 22.2; 64 of two rows, rank 16 17.1,
-// 41.1, of 65 and 63 of one 19.0, 43.2; what the choice has to keep from the first: 4 requests, one of 61 rows,
-// rank 64 29.1, 22.5.)
-bool few_rows(const gemm_adapters_t& p) {
+// have; the second with the inner size and the tiles, of which every request has its own.  (Microseconds a call
+// through the Python binding, calls back to back, few and products, bf16, each request with an adapter of its own: 64 requests of a row, 4096 x 4096, rank 16
+// 8.0, 41.8; rank 64 20.4, 40.0; 8192 x 8192, rank 128 74.6, 75.3; 256 requests, rank 16 20.7, 112.1; one request of 16 rows,
+// rank 64 10.7, 22.5; 64 of two rows, rank 16 17.4, 42.2, of 65 and 63 of one 19.4, 41.6; what the choice has to
+// keep from the first: 4 requests, one of 61 rows, rank 64 29.1, 22.5.)
+bool few_rows(const gemm_handle* h, const gemm_adapters_t& p) {
   const int splits = few_splits(p);
   const double row = (double)p.rank * (double)(p.K + p.N);
   const double longest = (double)cdiv(p.M - std::min(p.requests, p.M) + 1, splits);
   const double few = std::max(6.0 + 0.006 * (double)(p.requests * splits) + 0.40e-6 * (double)p.M * row,
                               3.0 + longest * (1.8 + 9e-6 * row));
   const double tiles = (double)std::min(p.requests, p.M) * (double)cdiv(p.N, 128);
-  const double products = 10.0 + 0.003 * (double)p.K + 1.5 / 152.0 * tiles;
+  const double products = 10.0 + 0.003 * (double)p.K + 1.5 / h->sm_count * tiles;
   return p.rank <= gb300::kFewRank && few < products;
 }
 
@@ -624,7 +625,7 @@ GEMM_API gemm_status_t gemm_adapters(gemm_handle_t h, const gemm_adapters_t* pp,
   if (p.M == 0 || p.N == 0 || p.requests == 0) return GEMM_OK;
   const bool any = p.rank > 0 && p.adapters > 0;
   std::lock_guard<std::mutex> guard(h->mu);
-  if (any && p.K > 0 && few_rows(p) && !h->forced) return run_few(h, p, stream);
+  if (any && p.K > 0 && few_rows(h, p) && !h->forced) return run_few(h, p, stream);
   Product down, up;
   down.rows = p.M; down.feats = p.rank; down.k = p.K; down.groups = p.requests;
   down.sets = p.adapters;
