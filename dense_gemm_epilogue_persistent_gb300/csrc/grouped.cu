@@ -626,6 +626,7 @@ GEMM_API gemm_status_t gemm_adapters(gemm_handle_t h, const gemm_adapters_t* pp,
   const bool any = p.rank > 0 && p.adapters > 0;
   std::lock_guard<std::mutex> guard(h->mu);
   if (any && p.K > 0 && few_rows(h, p) && !h->forced) return run_few(h, p, stream);
+  // (u is rounded to the operands' 16 bits: the second product's matrix units take no more)
   Product down, up;
   down.rows = p.M; down.feats = p.rank; down.k = p.K; down.groups = p.requests;
   down.sets = p.adapters;
