@@ -535,7 +535,8 @@ gemm_status_t gemm_linear(gemm_handle_t h, const gemm_linear_t* p, struct CUstre
  *   (NULL: not computed; a is read for db only, b for da only).  dz: required
  *   for da or db with an activation; without one it is optional (where given
  *   it receives dd).  M = 0: dbias and db are 0 (db unchanged where accumulated).
- * dz may be dd or z (same leading dimension). */
+ * dz may be dd or z (same leading dimension); dz at an a or b that is read, or dbias at another
+ * argument's address, is refused. */
 typedef struct {
   int64_t M, N, K;
   gemm_dtype_t type, da_type, db_type, dbias_type;
@@ -563,7 +564,8 @@ gemm_status_t gemm_linear_bwd(gemm_handle_t h, const gemm_linear_bwd_t* p,
  * numbers, places, offsets) lies in device memory and is never read by the host:
  * one captured graph serves whatever a router decides.  Such numbers out of
  * range never make a call read or write outside the tensors given: each
- * operator says below what it makes of them. */
+ * operator says below what it makes of them.  An output may share memory with another argument
+ * of its call only where that is said; one at another's address is refused. */
 
 /* Sorting by expert.  The T tokens' k choices, numbered i = t k + j, in order
  * of (expert, i):
